@@ -50,6 +50,8 @@ extern "C" {
 
 #define HC_F32 0
 #define HC_BF16 1
+#define HC_E4M3 2 /* 8-bit float, 4 exponent and 3 mantissa bits, largest 448, no infinity (norm outputs only) */
+#define HC_I8 3   /* 8-bit integer codes -127 .. 127 (norm outputs only) */
 
 #define HC_OK 0
 #define HC_ERR_NULL (-1)      /* a required pointer is NULL */
@@ -71,6 +73,8 @@ extern "C" {
 #define HC_MAX_ITERS 10000    /* Sinkhorn iterations */
 #define HC_MAX_BWD_ITERS 64   /* Sinkhorn iterations of hc_backward (iterates kept on chip) */
 #define HC_MAX_FLASH_SUBLAYERS 4 /* L, sublayers of an xHC-Flash block */
+#define HC_MAX_NORM_CHANNELS 16384 /* C of the norm calls */
+#define HC_MAX_ROUTER_STREAMS 16   /* N of xhc_router_backward */
 
 /* Human-readable text of a status code (static string, never NULL). */
 const char* hc_status_string(int status);
@@ -586,6 +590,144 @@ int hc_static_pre(const void* X, int dtype, int64_t T, int n, int64_t C, const f
                   void* stream);
 int hc_static_post(const void* X, int dtype, int64_t T, int n, int64_t C, const float* h_res, const float* h_post,
                    const void* F_out, void* X_next, void* stream);
+
+/* ------------------------------------------- norm in front of the sublayer -- */
+
+/*
+ * hc_rms_norm - root-mean-square norm of a sublayer's input, with the residual's
+ * addition of a one-stream model, in the stream dtype or in 8 bits with scales:
+ *   v = x + residual (x alone when residual is NULL),
+ *   y = v / sqrt(mean_c v^2 + eps) * weight.
+ *   x, residual, s [T, C] stream dtype; weight [C] float32 (NULL: ones); eps >= 0
+ *   (a row whose mean square + eps is 0 gives y = 0).
+ *   s: v rounded to the stream dtype, the residual stream for the next addition
+ *   (NULL: not stored; without a residual it must be NULL). s may be residual
+ *   itself (in place). y is formed from v before that rounding.
+ *   y [T, C]: y_dtype the stream dtype (rounded once; group must be 0), or HC_E4M3
+ *   or HC_I8 with scale float32: group 0: one scale a row, scale [T]; group 32, 64
+ *   or 128: one for each `group` channels (the last may be shorter), scale
+ *   [T, ceil(C / group)]. scale = max |y| / qmax over the row or group (qmax 448 or
+ *   127; 1 where that is below the smallest normal float32), code = y * (1 / scale)
+ *   rounded to nearest even; the value it stands for is code * scale. A NaN in a
+ *   group makes its scale NaN.
+ *   1 <= C <= HC_MAX_NORM_CHANNELS. No workspace. Statistics are float32.
+ *
+ * hc_pre_norm - hc_pre followed by the norm in one pass over the state: v = F_in =
+ *   sum_i h_pre[t, i] X[t, i] ([mHC] 4.3.1), y as above.
+ *   X [T, n, C] stream dtype, h_pre [T, n] float32, 1 <= n <= HC_MAX_STREAMS (xhc_pre's
+ *   h_pre as well); F_in [T, C] stream dtype (NULL: not stored; the backward reads it).
+ *
+ * hc_rms_norm_backward - gradients of both for the upstream gradient dy [T, C] of y
+ *   (with an 8-bit y: of the value it stands for, rounding passed through):
+ *   with v = s as stored, rstd = 1 / sqrt(mean v^2 + eps),
+ *   dx = rstd (weight dy - v rstd^2 mean_c(weight dy v)) + ds  (= dx and dresidual,
+ *     or dF_in), stored in the stream dtype, rounded once;
+ *   dweight[c] = sum_t dy v rstd, float32 (NULL: not formed; T = 0 gives zeros).
+ *   s (x where there was no residual), dy, ds, dx [T, C] stream dtype; ds: the
+ *   gradient that reaches the residual stream from behind (NULL: zero); dx may be ds.
+ *   Workspace: hc_rms_norm_backward_workspace_bytes(T, C) (0 for T = 0; may be NULL
+ *   when dweight is). Deterministic: every sum runs in a fixed order.
+ * All: dtype HC_F32 or HC_BF16, arrays aligned to their element size; outputs overlap
+ * no input (but as stated), other output or workspace (HC_ERR_ALIAS).
+ */
+int hc_rms_norm(const void* x, int dtype, int64_t T, int64_t C, const void* residual, const float* weight, float eps,
+                void* s, int y_dtype, int group, void* y, float* scale, void* stream);
+int hc_pre_norm(const void* X, int dtype, int64_t T, int n, int64_t C, const float* h_pre, const float* weight,
+                float eps, void* F_in, int y_dtype, int group, void* y, float* scale, void* stream);
+int64_t hc_rms_norm_backward_workspace_bytes(int64_t T, int64_t C);
+int hc_rms_norm_backward(const void* s, int dtype, int64_t T, int64_t C, const float* weight, float eps,
+                         const void* dy, const void* ds, void* dx, float* dweight, void* workspace,
+                         int64_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------ gated linear recurrence -- */
+
+/*
+ * hc_gated_scan - the diagonal gated linear recurrence of a state space block, the
+ * sublayer function that static mHC wraps, over B sequences of S tokens ([B, S]
+ * row-major, as in xhc_augment):
+ *   a_t = sigmoid(gate_t), u_t = 1 - a_t (tied != 0) or 1 (tied == 0),
+ *   h_t = a_t h_{t-1} + u_t x_t,  y_t = h_t, per channel; h_{-1} = h0.
+ *   x, gate, y [B, S, C] stream dtype; h0 (NULL: zeros) and h_last (NULL: not
+ *   stored) [B, C] float32: the state before the first and after the last token, so
+ *   that a sequence can go on in a later call (S = 1: one new token each). h_last
+ *   may be h0.
+ *   lengths (NULL: S each) [B] int32 device array: sequence b has lengths[b] tokens
+ *   (taken as 0 below 0 and as S above S); behind them x and gate are not used, y is
+ *   left as it was, and h_last is the state after the last token (h0 for length 0).
+ *   The state is float32 throughout; y is rounded once.
+ *
+ * hc_gated_scan_backward - gradients for the upstream gradients dy [B, S, C] of y
+ *   and dh_last [B, C] float32 (NULL: zeros) of h_last. With y the forward's output
+ *   as stored (h_{t-1} is read from it) and R_t the gradient from later tokens:
+ *   dh_t = dy_t + R_t, R_{t-1} = a_t dh_t, dx_t = u_t dh_t,
+ *   dgate_t = dh_t (h_{t-1} - x_t) a_t (1 - a_t) (tied) or dh_t h_{t-1} a_t (1 - a_t).
+ *   dx, dgate [B, S, C] stream dtype (rounded once; zero behind a sequence's
+ *   length); dh0 [B, C] float32 (NULL: not stored).
+ * Both: dtype HC_F32 or HC_BF16, C >= 1; S = 0 passes the state on (B = 0 does
+ * nothing); arrays aligned to their element size; workspace
+ * hc_gated_scan_workspace_bytes(B, S, C) bytes (may be NULL when that is 0), 256-byte
+ * aligned. Outputs overlap no input (but as stated), other output or workspace
+ * (HC_ERR_ALIAS). B * max(S, 64) * C at most 2^39 (else HC_ERR_SHAPE).
+ */
+int64_t hc_gated_scan_workspace_bytes(int64_t B, int64_t S, int64_t C);
+int hc_gated_scan(const void* x, const void* gate, int dtype, int64_t B, int64_t S, int64_t C, const float* h0,
+                  const int32_t* lengths, int tied, void* y, float* h_last, void* workspace, int64_t workspace_bytes,
+                  void* stream);
+int hc_gated_scan_backward(const void* x, const void* gate, const void* y, const void* dy, int dtype, int64_t B,
+                           int64_t S, int64_t C, const float* h0, const float* dh_last, const int32_t* lengths,
+                           int tied, void* dx, void* dgate, float* dh0, void* workspace, int64_t workspace_bytes,
+                           void* stream);
+
+/* --------------------------------------------- training the stream router -- */
+
+/*
+ * xhc_balance_loss - keeps the xHC router from choosing the same streams for every
+ * token: over B sequences of S tokens, for sequence b with n_b unmasked tokens,
+ *   count[b, i] = its tokens whose active set idx holds stream i (entries outside
+ *     [0, N) count nowhere), p_tj = score[t, j] / sum_j score[t, j] (0 where the sum is 0),
+ *   P[b, j] = mean_t p_tj, f_bj = E / ((k - m) n_b) * count[b, m + j], E = N - m,
+ *   loss = coef / B * sum_b sum_j f_bj P_bj  (coef when the choice is even).
+ *   score [T, E] float32 and idx [T, k] int32 as xhc_pre or xhc_route wrote them
+ *   (T = B*S); mask [T] bytes, 0 for tokens that take no part (NULL: all do), whose
+ *   scores may hold anything. A sequence without tokens adds 0.
+ *   Outputs: loss [1] float32, count [B, N] int32, tokens [B] int32 (n_b), mean_p
+ *   [B, E] float32 (P).
+ *   Workspace: xhc_balance_loss_workspace_bytes.
+ * xhc_balance_loss_backward - dscore [T, E] = dloss * dloss/dscore (f is constant:
+ *   the counts are a discrete choice), 0 for masked tokens:
+ *   dscore_tj = dloss coef / (B n_b) (f_bj - sum_i f_bi p_ti) / sum_i score_ti.
+ *   dloss [1] float32 device value (NULL: 1); count, tokens as the forward wrote them.
+ *   Both: 1 <= m < k <= N <= 64, k <= 16, T * 64 < 2^32 (HC_ERR_SHAPE); 4-byte aligned
+ *   arrays; outputs overlap no input, other output or workspace (HC_ERR_ALIAS).
+ *   Deterministic: every sum runs in a fixed order.
+ *
+ * xhc_router_backward - gradients of the router's projection score = sigmoid((vec X @
+ *   w_router) / r), r = ||vec X|| / sqrt(NC) (xhc_pre), for dscore [T, E] float32
+ *   (xhc_balance_loss_backward's, or any): with dz = dscore score (1 - score) and z
+ *   the logit of score,
+ *   dX_out = dX + (dz @ w_router^T) / r - X sum_j(dz_j z_j) / (r^2 NC)  (bfloat16,
+ *     rounded once), dw_router [NC, E] = sum_t vec X_t^T dz_t / r_t (float32; T = 0
+ *     gives zeros).
+ *   X [T, N, C]: the state the router read; dX, dX_out [T, N, C]: the gradient that
+ *   xhc_route_backward and xhc_pre_backward formed and the one with the router's
+ *   part; dX_out may be dX (in place). A token whose dscore is all zero takes no
+ *   part (its X and score may hold anything); the all-zero state passes nothing.
+ *   Covered: dtype HC_BF16 (HC_F32 -> HC_ERR_DTYPE), 1 <= m < N <=
+ *   HC_MAX_ROUTER_STREAMS, C a multiple of 32, T < 2^24 (else HC_ERR_SHAPE). X, dX,
+ *   dX_out 16-byte aligned, float arrays 4; workspace 256 bytes,
+ *   xhc_router_backward_workspace_bytes (-1 for what is not covered). Deterministic.
+ */
+int64_t xhc_balance_loss_workspace_bytes(int64_t B, int64_t S, int N, int m);
+int xhc_balance_loss(const float* score, const int32_t* idx, const uint8_t* mask, int64_t B, int64_t S, int N, int k,
+                     int m, float coef, float* loss, int32_t* count, int32_t* tokens, float* mean_p, void* workspace,
+                     int64_t workspace_bytes, void* stream);
+int xhc_balance_loss_backward(const float* score, const int32_t* count, const int32_t* tokens, const uint8_t* mask,
+                              int64_t B, int64_t S, int N, int k, int m, float coef, const float* dloss,
+                              float* dscore, void* stream);
+int64_t xhc_router_backward_workspace_bytes(int64_t T, int N, int64_t C, int m, int dtype);
+int xhc_router_backward(const void* X, int dtype, int64_t T, int N, int64_t C, int m, const float* w_router,
+                        const float* score, const float* dscore, const void* dX, void* dX_out, float* dw_router,
+                        void* workspace, int64_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------ measurement -- */
 

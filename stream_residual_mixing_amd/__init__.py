@@ -82,6 +82,25 @@ _SIGS = {
     "xhc_augment_backward_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64, _vp, _c_int, _c_int]),
     "xhc_augment_backward": (_c_int, [_vp, _c_int, _c_i64, _c_i64, _c_i64, _vp, _vp, _c_int, _vp, _vp, _vp, _vp,
                                       _c_i64, _vp]),
+    "hc_rms_norm": (_c_int, [_vp, _c_int, _c_i64, _c_i64, _vp, _vp, _c_float, _vp, _c_int, _c_int, _vp, _vp, _vp]),
+    "hc_pre_norm": (_c_int, [_vp, _c_int, _c_i64, _c_int, _c_i64, _vp, _vp, _c_float, _vp, _c_int, _c_int, _vp, _vp,
+                             _vp]),
+    "hc_rms_norm_backward_workspace_bytes": (_c_i64, [_c_i64, _c_i64]),
+    "hc_rms_norm_backward": (_c_int, [_vp, _c_int, _c_i64, _c_i64, _vp, _c_float, _vp, _vp, _vp, _vp, _vp, _c_i64,
+                                      _vp]),
+    "hc_gated_scan_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64]),
+    "hc_gated_scan": (_c_int, [_vp, _vp, _c_int, _c_i64, _c_i64, _c_i64, _vp, _vp, _c_int, _vp, _vp, _vp, _c_i64,
+                               _vp]),
+    "hc_gated_scan_backward": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp, _c_int,
+                                        _vp, _vp, _vp, _vp, _c_i64, _vp]),
+    "xhc_balance_loss_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_int, _c_int]),
+    "xhc_balance_loss": (_c_int, [_vp, _vp, _vp, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_float, _vp, _vp, _vp, _vp,
+                                  _vp, _c_i64, _vp]),
+    "xhc_balance_loss_backward": (_c_int, [_vp, _vp, _vp, _vp, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_float, _vp,
+                                           _vp, _vp]),
+    "xhc_router_backward_workspace_bytes": (_c_i64, [_c_i64, _c_int, _c_i64, _c_int, _c_int]),
+    "xhc_router_backward": (_c_int, [_vp, _c_int, _c_i64, _c_int, _c_i64, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                     _c_i64, _vp]),
     "hc_copy_probe": (_c_int, [_vp, _vp, _c_i64, _vp]),
     "hc_tanh_coeffs": (_c_int, [_vp, _c_int, _c_i64, _c_int, _c_i64, _vp, _vp, _c_float, _c_float, _c_float,
                                 _vp, _vp, _vp, _vp]),
@@ -789,6 +808,347 @@ def xhc_augment(F_out, conv_w, kappas, batch, seq, *, v_dtype=None, out=None, wo
                                             _ptr(V), _DT[vdt], _ptr(ws), 0 if ws is None else _nbytes(ws),
                                             _stream(dev, stream)))
     return V
+
+
+# ---------------------------------------------- norm in front of the sublayer
+
+HC_E4M3, HC_I8 = 2, 3
+_QUANT = {torch.float8_e4m3fn: HC_E4M3, torch.int8: HC_I8}
+
+
+class _Here:
+    """Nothing to switch: the arrays' device is current and the call goes to its current stream."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+class _There:
+    """The arrays' device, and the caller's stream if one is given, are current inside: a kernel is
+    launched on the device its stream belongs to, and what is allocated belongs to that stream, so
+    that no other stream is handed a workspace that is still in use."""
+
+    def __init__(self, device, stream):
+        self._device = torch.cuda.device(device)
+        self._stream = None
+        if stream is not None:
+            self._stream = torch.cuda.stream(
+                torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else
+                torch.cuda.default_stream(device))
+
+    def __enter__(self):
+        self._device.__enter__()
+        if self._stream is not None:
+            self._stream.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self._stream is not None:
+            self._stream.__exit__(*exc)
+        return self._device.__exit__(*exc)
+
+
+def _on(device, stream):
+    if stream is None and device.index == torch.cuda.current_device():
+        return _HERE
+    return _There(device, stream)
+
+
+def _norm_args(x, weight, C, quant, group):
+    """(weight, C dtype code of y, number of scale groups or 0)."""
+    if weight is not None:
+        weight = _f32(weight, "weight", (C,), x.device)
+    if quant is None:
+        if group:
+            raise ValueError("group needs an 8-bit output (quant)")
+        return weight, _DT[x.dtype], 0
+    if quant not in _QUANT:
+        raise TypeError(f"quant must be one of {tuple(_QUANT)}, got {quant}")
+    if group not in (0, 32, 64, 128):
+        raise ValueError(f"group must be 0, 32, 64 or 128, got {group}")
+    return weight, _QUANT[quant], -(-C // group) if group else 1
+
+
+def _norm_outs(out, x, T, C, quant, ngroups):
+    """(y, scale or None), of `out` or new."""
+    dt = x.dtype if quant is None else quant
+    y, scale = (None, None) if out is None else out
+    y = torch.empty(T, C, dtype=dt, device=x.device) if y is None else _dev_tensor(y, "y out", (dt,), (T, C), x.device)
+    if quant is None:
+        return y, None
+    if scale is None:
+        return y, torch.empty(T, ngroups, device=x.device)
+    return y, _f32(scale, "scale out", (T, ngroups), x.device)
+
+
+def _matrix(t, name, dtypes=None):
+    t = _dev_tensor(t, name, _DT if dtypes is None else dtypes)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [T, C], got shape {tuple(t.shape)}")
+    return t
+
+
+def hc_rms_norm(x, weight=None, eps=1e-6, *, residual=None, quant=None, group=0, s_out=None, out=None, stream=None):
+    """y = v / sqrt(mean v^2 + eps) * weight of v = x [T, C] (+ residual). quant: None (y in x's
+    dtype), torch.float8_e4m3fn or torch.int8, with a scale per row (group 0) or per 32, 64 or 128
+    channels. Returns dict(y[, s][, scale]): s = v rounded to x's dtype, with a residual (s_out may be
+    the residual itself); scale [T, groups] float32. out = (y, scale)."""
+    x = _matrix(x, "x")
+    T, C = x.shape
+    dev = x.device
+    weight, code, ngroups = _norm_args(x, weight, C, quant, group)
+    with _on(dev, stream):
+        s = None
+        if residual is not None:
+            residual = _dev_tensor(residual, "residual", (x.dtype,), (T, C), dev)
+            s = _stream_out(s_out, "s out", (T, C), x.dtype, dev)
+        elif s_out is not None:
+            raise ValueError("s_out needs a residual")
+        y, scale = _norm_outs(out, x, T, C, quant, ngroups)
+        _check("hc_rms_norm", lib().hc_rms_norm(_ptr(x), _DT[x.dtype], T, C, _ptr(residual), _ptr(weight), float(eps),
+                                                _ptr(s), code, int(group), _ptr(y), _ptr(scale), _stream(dev, stream)))
+    res = dict(y=y)
+    if s is not None:
+        res["s"] = s
+    if scale is not None:
+        res["scale"] = scale
+    return res
+
+
+def hc_pre_norm(X, h_pre, weight=None, eps=1e-6, *, quant=None, group=0, want_F_in=True, F_in_out=None, out=None,
+                stream=None):
+    """hc_pre and the norm of its result in one pass: v = sum_i h_pre[:, i] X[:, i, :]; quant and group
+    as hc_rms_norm. Returns dict(y[, F_in][, scale]); F_in = v rounded to X's dtype. out = (y, scale)."""
+    X = _state(X)
+    T, n, C = X.shape
+    dev = X.device
+    h_pre = _f32(h_pre, "h_pre", (T, n), dev)
+    weight, code, ngroups = _norm_args(X, weight, C, quant, group)
+    with _on(dev, stream):
+        F_in = None
+        if want_F_in or F_in_out is not None:
+            F_in = _stream_out(F_in_out, "F_in out", (T, C), X.dtype, dev)
+        y, scale = _norm_outs(out, X, T, C, quant, ngroups)
+        _check("hc_pre_norm", lib().hc_pre_norm(_ptr(X), _DT[X.dtype], T, n, C, _ptr(h_pre), _ptr(weight), float(eps),
+                                                _ptr(F_in), code, int(group), _ptr(y), _ptr(scale),
+                                                _stream(dev, stream)))
+    res = dict(y=y)
+    if F_in is not None:
+        res["F_in"] = F_in
+    if scale is not None:
+        res["scale"] = scale
+    return res
+
+
+def hc_rms_norm_backward_workspace_bytes(T: int, C: int) -> int:
+    return int(lib().hc_rms_norm_backward_workspace_bytes(T, C))
+
+
+def hc_rms_norm_backward(s, weight, dy, eps=1e-6, *, ds=None, want_dweight=True, out=None, workspace=None,
+                         stream=None):
+    """Backward of hc_rms_norm (s: its s, or x without a residual) and of hc_pre_norm's norm (s: F_in):
+    (dx, dweight or None) for the gradient dy of y and ds of s (dx may be ds). out = (dx, dweight)."""
+    s = _matrix(s, "s")
+    T, C = s.shape
+    dev = s.device
+    if weight is not None:
+        weight = _f32(weight, "weight", (C,), dev)
+    dy = _dev_tensor(dy, "dy", (s.dtype,), (T, C), dev)
+    if ds is not None:
+        ds = _dev_tensor(ds, "ds", (s.dtype,), (T, C), dev)
+    dx, dw = (None, None) if out is None else out
+    with _on(dev, stream):
+        dx = _stream_out(dx, "dx out", (T, C), s.dtype, dev)
+        if dw is not None:
+            dw = _f32(dw, "dweight out", (C,), dev)
+        elif want_dweight:
+            dw = torch.empty(C, device=dev)
+        ws = None
+        if dw is not None:
+            ws = _workspace(hc_rms_norm_backward_workspace_bytes(T, C), dev, workspace)
+        _check("hc_rms_norm_backward", lib().hc_rms_norm_backward(
+            _ptr(s), _DT[s.dtype], T, C, _ptr(weight), float(eps), _ptr(dy), _ptr(ds), _ptr(dx), _ptr(dw), _ptr(ws),
+            0 if ws is None else _nbytes(ws), _stream(dev, stream)))
+    return dx, dw
+
+
+# ---------------------------------------------------- gated linear recurrence
+
+
+def hc_gated_scan_workspace_bytes(B: int, S: int, C: int) -> int:
+    return int(lib().hc_gated_scan_workspace_bytes(B, S, C))
+
+
+def _sequences(t, name):
+    t = _dev_tensor(t, name, _DT)
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [B, S, C], got shape {tuple(t.shape)}")
+    return t
+
+
+def _per_channel(t, name, B, C, dev):
+    return None if t is None else _f32(t, name, (B, C), dev)
+
+
+def hc_gated_scan(x, gate, h0=None, *, lengths=None, tied=True, want_state=True, out=None, workspace=None,
+                  stream=None):
+    """h_t = a_t h_{t-1} + u_t x_t with a = sigmoid(gate) and u = 1 - a (tied) or 1, over x, gate
+    [B, S, C]; h0 [B, C] float32, lengths [B] int32. Returns (y [B, S, C], h_last [B, C] or None);
+    out = (y, h_last), h_last may be h0. Rows of y behind a sequence's length are left as they are."""
+    x = _sequences(x, "x")
+    B, S, C = x.shape
+    dev = x.device
+    gate = _dev_tensor(gate, "gate", (x.dtype,), (B, S, C), dev)
+    h0 = _per_channel(h0, "h0", B, C, dev)
+    if lengths is not None:
+        lengths = _i32(lengths, "lengths", (B,), dev)
+    y, h_last = (None, None) if out is None else out
+    h_last = _per_channel(h_last, "h_last out", B, C, dev)
+    with _on(dev, stream):
+        y = _stream_out(y, "y out", (B, S, C), x.dtype, dev)
+        if h_last is None and want_state:
+            h_last = torch.empty(B, C, device=dev)
+        nbytes = hc_gated_scan_workspace_bytes(B, S, C)
+        ws = None if nbytes == 0 else _workspace(nbytes, dev, workspace)
+        _check("hc_gated_scan", lib().hc_gated_scan(
+            _ptr(x), _ptr(gate), _DT[x.dtype], B, S, C, _ptr(h0), _ptr(lengths), int(bool(tied)), _ptr(y),
+            _ptr(h_last), _ptr(ws), 0 if ws is None else _nbytes(ws), _stream(dev, stream)))
+    return y, h_last
+
+
+def hc_gated_scan_backward(x, gate, y, dy, h0=None, dh_last=None, *, lengths=None, tied=True, out=None,
+                           workspace=None, stream=None):
+    """Backward of hc_gated_scan (y: its output): (dx, dgate [B, S, C], dh0 [B, C]) for the gradients dy
+    of y and dh_last of h_last. out = (dx, dgate, dh0)."""
+    x = _sequences(x, "x")
+    B, S, C = x.shape
+    dev = x.device
+    gate, y, dy = (_dev_tensor(t, name, (x.dtype,), (B, S, C), dev)
+                   for t, name in ((gate, "gate"), (y, "y"), (dy, "dy")))
+    h0 = _per_channel(h0, "h0", B, C, dev)
+    dh_last = _per_channel(dh_last, "dh_last", B, C, dev)
+    if lengths is not None:
+        lengths = _i32(lengths, "lengths", (B,), dev)
+    dx, dgate, dh0 = (None, None, None) if out is None else out
+    dh0 = _per_channel(dh0, "dh0 out", B, C, dev)
+    with _on(dev, stream):
+        dx = _stream_out(dx, "dx out", (B, S, C), x.dtype, dev)
+        dgate = _stream_out(dgate, "dgate out", (B, S, C), x.dtype, dev)
+        if dh0 is None:
+            dh0 = torch.empty(B, C, device=dev)
+        nbytes = hc_gated_scan_workspace_bytes(B, S, C)
+        ws = None if nbytes == 0 else _workspace(nbytes, dev, workspace)
+        _check("hc_gated_scan_backward", lib().hc_gated_scan_backward(
+            _ptr(x), _ptr(gate), _ptr(y), _ptr(dy), _DT[x.dtype], B, S, C, _ptr(h0), _ptr(dh_last), _ptr(lengths),
+            int(bool(tied)), _ptr(dx), _ptr(dgate), _ptr(dh0), _ptr(ws), 0 if ws is None else _nbytes(ws),
+            _stream(dev, stream)))
+    return dx, dgate, dh0
+
+
+# ------------------------------------------------- training the stream router
+
+
+def xhc_balance_loss_workspace_bytes(B: int, S: int, N: int, m: int) -> int:
+    return int(lib().xhc_balance_loss_workspace_bytes(B, S, N, m))
+
+
+def _scores(score, T, m):
+    """(score [T, E] checked, E, N = E + m)."""
+    score = _f32(score, "score")
+    if score.dim() != 2 or score.shape[0] != T or score.shape[1] < 1:
+        raise ValueError(f"score has shape {tuple(score.shape)}, expected ({T}, N - m)")
+    return score, score.shape[1], score.shape[1] + int(m)
+
+
+def _token_mask(mask, T, dev):
+    return None if mask is None else _dev_tensor(mask, "mask", (torch.bool, torch.uint8), (T,), dev)
+
+
+def xhc_balance_loss(score, idx, B, S, *, m=2, coef=1.0, mask=None, out=None, workspace=None, stream=None):
+    """Balance loss of the router over B sequences of S tokens: score [B*S, N-m] and idx [B*S, k] as
+    xhc_pre wrote them; mask [B*S] (bool): the tokens that take part. Returns dict(loss [], count
+    [B, N] int32, tokens [B] int32, mean_p [B, N-m]); out = these four, in this order."""
+    T = int(B) * int(S)
+    score, E, N = _scores(score, T, m)
+    dev = score.device
+    idx = _i32(idx, "idx", device=dev)
+    if idx.dim() != 2 or idx.shape[0] != T:
+        raise ValueError(f"idx has shape {tuple(idx.shape)}, expected ({T}, k)")
+    k = idx.shape[1]
+    mask = _token_mask(mask, T, dev)
+    with _on(dev, stream):
+        if out is None:
+            loss, count = torch.empty((), device=dev), torch.empty(B, N, dtype=torch.int32, device=dev)
+            tokens, mean_p = torch.empty(B, dtype=torch.int32, device=dev), torch.empty(B, E, device=dev)
+        else:
+            loss, count = _f32(out[0], "loss out", (), dev), _i32(out[1], "count out", (B, N), dev)
+            tokens, mean_p = _i32(out[2], "tokens out", (B,), dev), _f32(out[3], "mean_p out", (B, E), dev)
+        ws = _workspace(xhc_balance_loss_workspace_bytes(B, S, N, m), dev, workspace)
+        _check("xhc_balance_loss", lib().xhc_balance_loss(
+            _ptr(score), _ptr(idx), _ptr(mask), B, S, N, k, m, float(coef), _ptr(loss), _ptr(count), _ptr(tokens),
+            _ptr(mean_p), _ptr(ws), _nbytes(ws), _stream(dev, stream)))
+    return dict(loss=loss, count=count, tokens=tokens, mean_p=mean_p)
+
+
+def xhc_balance_loss_backward(score, count, tokens, k, B, S, *, coef=1.0, dloss=None, mask=None, out=None,
+                              stream=None):
+    """dscore [B*S, N-m] of xhc_balance_loss (count, tokens: its outputs; k: streams per token); dloss: the
+    loss's gradient, one float32 on the device (None: 1)."""
+    T = int(B) * int(S)
+    score, E, _ = _scores(score, T, 0)
+    dev = score.device
+    count = _i32(count, "count", device=dev)
+    if count.dim() != 2 or count.shape[0] != B:
+        raise ValueError(f"count has shape {tuple(count.shape)}, expected ({B}, N)")
+    N = count.shape[1]
+    tokens = _i32(tokens, "tokens", (B,), dev)
+    mask = _token_mask(mask, T, dev)
+    if dloss is not None:
+        dloss = _f32(dloss, "dloss", device=dev)
+        if dloss.numel() != 1:
+            raise ValueError(f"dloss must hold one value, got shape {tuple(dloss.shape)}")
+    with _on(dev, stream):
+        dscore = torch.empty(T, E, device=dev) if out is None else _f32(out, "dscore out", (T, E), dev)
+        _check("xhc_balance_loss_backward", lib().xhc_balance_loss_backward(
+            _ptr(score), _ptr(count), _ptr(tokens), _ptr(mask), B, S, N, int(k), N - E, float(coef), _ptr(dloss),
+            _ptr(dscore), _stream(dev, stream)))
+    return dscore
+
+
+def xhc_router_backward_workspace_bytes(T: int, N: int, C: int, m: int, dtype) -> int:
+    return int(lib().xhc_router_backward_workspace_bytes(T, N, C, m, _DT[dtype]))
+
+
+def xhc_router_backward(X, w_router, score, dscore, dX, *, out=None, workspace=None, stream=None):
+    """Backward of the router's projection (bfloat16, N <= 16): the gradient dscore [T, N-m] of the scores
+    goes to the state and the weights. Returns (dX + its part, dw_router); the sum is written in place on
+    dX, or to out."""
+    X = _state(X, dtypes=(torch.bfloat16,))
+    T, N, C = X.shape
+    dev = X.device
+    score, E, _ = _scores(score, T, 0)
+    if score.device != dev:
+        raise ValueError(f"score is on {score.device}, expected {dev}")
+    dscore = _f32(dscore, "dscore", (T, E), dev)
+    w_router = _f32(w_router, "w_router", (N * C, E), dev)
+    dX = _dev_tensor(dX, "dX", (X.dtype,), (T, N, C), dev)
+    dX_out = dX if out is None else _dev_tensor(out, "dX out", (X.dtype,), (T, N, C), dev)
+    with _on(dev, stream):
+        dw = torch.empty(N * C, E, device=dev)
+        ws = _workspace(xhc_router_backward_workspace_bytes(T, N, C, N - E, X.dtype), dev, workspace)
+        _check("xhc_router_backward", lib().xhc_router_backward(
+            _ptr(X), _DT[X.dtype], T, N, C, N - E, _ptr(w_router), _ptr(score), _ptr(dscore), _ptr(dX), _ptr(dX_out),
+            _ptr(dw), _ptr(ws), _nbytes(ws), _stream(dev, stream)))
+    return dX_out, dw
+
+
+# ------------------------------------------- HC baseline and gain diagnostic
 
 
 def hc_tanh_coeffs(X, theta, bias, alpha, *, out=None, stream=None):

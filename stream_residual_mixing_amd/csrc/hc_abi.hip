@@ -152,7 +152,7 @@ const char* hc_status_string(int status) {
   }
 }
 
-int hc_version(void) { return 102; }
+int hc_version(void) { return 103; }
 
 int64_t hc_coeffs_workspace_bytes(int64_t T, int n, int64_t C, int dtype) {
   if (T < 0 || n < 1 || n > HC_MAX_MHC_STREAMS || C < 1 || !dtype_ok(dtype)) return -1;
@@ -1380,6 +1380,273 @@ int hc_static_post(const void* X, int dtype, int64_t T, int n, int64_t C, const 
   if ((s = device_status()) != HC_OK) return s;
   return launch_status(hc::launch_static_apply(dtype, true, vec_ok(C, {X, F_out, X_next}), X, T, n, C, h_res, h_post,
                                                F_out, X_next, (hipStream_t)stream));
+}
+
+// ------------------------------------------- norm in front of the sublayer
+
+// One array of a call: where, how many bytes, its alignment, and whether it is required.
+struct Buf {
+  const void* p;
+  int64_t bytes;
+  uintptr_t align;
+  bool need;
+};
+
+static int check_bufs(std::initializer_list<Buf> bs) {
+  for (const Buf& b : bs)
+    if (b.need && !b.p) return HC_ERR_NULL;
+  for (const Buf& b : bs)
+    if (b.p && !aligned_to(b.p, b.align)) return HC_ERR_ALIGN;
+  return HC_OK;
+}
+
+// outs against ins and against each other
+static bool bufs_overlap(std::initializer_list<Buf> outs, std::initializer_list<Buf> ins) {
+  for (const Buf* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Buf& i : ins)
+      if (overlaps(o->p, o->bytes, i.p, i.bytes)) return true;
+    for (const Buf* q = outs.begin(); q != o; ++q)
+      if (overlaps(o->p, o->bytes, q->p, q->bytes)) return true;
+  }
+  return false;
+}
+
+static int check_ws(const void* ws, int64_t bytes, int64_t need) {
+  return need > 0 && (!ws || !aligned_to(ws, 256) || bytes < need) ? HC_ERR_WORKSPACE : HC_OK;
+}
+
+static int check_norm(int dtype, int64_t T, int64_t C, float eps, int y_dtype, int group) {
+  if (!dtype_ok(dtype)) return HC_ERR_DTYPE;
+  const bool q8 = y_dtype == HC_E4M3 || y_dtype == HC_I8;
+  if (!q8 && y_dtype != dtype) return HC_ERR_DTYPE;
+  if (T < 0 || T > (1ll << 40) || C < 1 || C > HC_MAX_NORM_CHANNELS) return HC_ERR_SHAPE;
+  if (!(eps >= 0.f) || eps > 3.4e38f) return HC_ERR_SHAPE;
+  if (group != 0 && !(q8 && (group == 32 || group == 64 || group == 128))) return HC_ERR_SHAPE;
+  return HC_OK;
+}
+
+// the y and scale arrays of a norm call
+static void norm_outs(int dtype, int64_t T, int64_t C, int y_dtype, int group, void* y, float* scale, Buf& by, Buf& bs,
+                      int64_t& ngroups) {
+  const bool q8 = y_dtype != dtype;
+  ngroups = group ? (C + group - 1) / group : 1;
+  by = Buf{y, T * C * (q8 ? 1 : (int64_t)esize(dtype)), q8 ? 1 : esize(dtype), true};
+  bs = Buf{q8 ? scale : nullptr, T * ngroups * 4, 4, q8};
+}
+
+int hc_rms_norm(const void* x, int dtype, int64_t T, int64_t C, const void* residual, const float* weight, float eps,
+                void* s, int y_dtype, int group, void* y, float* scale, void* stream) {
+  int r = check_norm(dtype, T, C, eps, y_dtype, group);
+  if (r != HC_OK || T == 0) return r;
+  if (s && !residual) return HC_ERR_NULL;
+  const int64_t e = (int64_t)esize(dtype), xb = T * C * e;
+  Buf by, bs;
+  int64_t ngroups;
+  norm_outs(dtype, T, C, y_dtype, group, y, scale, by, bs, ngroups);
+  const Buf bx{x, xb, (uintptr_t)e, true}, br{residual, xb, (uintptr_t)e, false}, bw{weight, C * 4, 4, false},
+      bo{s, xb, (uintptr_t)e, false};
+  if ((r = check_bufs({bx, br, bw, bo, by, bs})) != HC_OK) return r;
+  if (bufs_overlap({by, bs}, {bx, br, bw, bo}) || bufs_overlap({bo}, {bx, bw}) ||
+      (s != residual && overlaps(s, xb, residual, xb)))
+    return HC_ERR_ALIAS;
+  if ((r = device_status()) != HC_OK) return r;
+  const bool q8 = y_dtype != dtype;
+  const bool vec = vec_ok(C, {x, residual, weight, s}) && aligned_to(y, q8 ? 8 : 16);
+  const hc::NormArgs a{x, residual, nullptr, weight, s, y, scale, T, C, ngroups, 1, q8 ? y_dtype : 0, group, eps};
+  return launch_status(hc::launch_rms_norm(dtype, residual ? 1 : 0, vec, a, (hipStream_t)stream));
+}
+
+int hc_pre_norm(const void* X, int dtype, int64_t T, int n, int64_t C, const float* h_pre, const float* weight,
+                float eps, void* F_in, int y_dtype, int group, void* y, float* scale, void* stream) {
+  int r = check_norm(dtype, T, C, eps, y_dtype, group);
+  if (r != HC_OK) return r;
+  if (n < 1 || n > HC_MAX_STREAMS) return HC_ERR_SHAPE;
+  if (T == 0) return HC_OK;
+  const int64_t e = (int64_t)esize(dtype), fb = T * C * e;
+  Buf by, bs;
+  int64_t ngroups;
+  norm_outs(dtype, T, C, y_dtype, group, y, scale, by, bs, ngroups);
+  const Buf bx{X, fb * n, (uintptr_t)e, true}, bh{h_pre, T * n * 4, 4, true}, bw{weight, C * 4, 4, false},
+      bo{F_in, fb, (uintptr_t)e, false};
+  if ((r = check_bufs({bx, bh, bw, bo, by, bs})) != HC_OK) return r;
+  if (bufs_overlap({by, bs, bo}, {bx, bh, bw})) return HC_ERR_ALIAS;
+  if ((r = device_status()) != HC_OK) return r;
+  const bool q8 = y_dtype != dtype;
+  const bool vec = vec_ok(C, {X, weight, F_in}) && aligned_to(y, q8 ? 8 : 16);
+  const hc::NormArgs a{X, nullptr, h_pre, weight, F_in, y, scale, T, C, ngroups, n, q8 ? y_dtype : 0, group, eps};
+  return launch_status(hc::launch_rms_norm(dtype, 2, vec, a, (hipStream_t)stream));
+}
+
+int64_t hc_rms_norm_backward_workspace_bytes(int64_t T, int64_t C) {
+  if (T < 0 || T > (1ll << 40) || C < 1 || C > HC_MAX_NORM_CHANNELS) return -1;
+  return T == 0 ? 0 : hc::norm_backward_parts(T, C) * C * 4;
+}
+
+int hc_rms_norm_backward(const void* s, int dtype, int64_t T, int64_t C, const float* weight, float eps,
+                         const void* dy, const void* ds, void* dx, float* dweight, void* workspace,
+                         int64_t workspace_bytes, void* stream) {
+  int r = check_norm(dtype, T, C, eps, dtype, 0);
+  if (r != HC_OK || (T == 0 && !dweight)) return r;
+  const int64_t e = (int64_t)esize(dtype), xb = T * C * e;
+  const int64_t wsb = dweight ? hc_rms_norm_backward_workspace_bytes(T, C) : 0;
+  const Buf bv{s, xb, (uintptr_t)e, T > 0}, bw{weight, C * 4, 4, false}, bd{dy, xb, (uintptr_t)e, T > 0},
+      bs{ds, xb, (uintptr_t)e, false}, bx{dx, xb, (uintptr_t)e, T > 0}, bg{dweight, C * 4, 4, false},
+      bk{wsb ? workspace : nullptr, wsb, 1, false};
+  if ((r = check_bufs({bv, bw, bd, bs, bx, bg})) != HC_OK) return r;
+  if ((r = check_ws(workspace, workspace_bytes, wsb)) != HC_OK) return r;
+  if (bufs_overlap({bx, bg, bk}, {bv, bw, bd}) || bufs_overlap({bg, bk}, {bs}) ||
+      (dx != ds && overlaps(dx, xb, ds, xb)))
+    return HC_ERR_ALIAS;
+  if ((r = device_status()) != HC_OK) return r;
+  const bool vec = vec_ok(C, {s, weight, dy, ds, dx});
+  const hc::NormBwdArgs a{s, weight, dy, ds, dx, dweight ? (float*)workspace : nullptr, T, C, eps};
+  return launch_status(hc::launch_rms_norm_backward(dtype, vec, a, dweight, (hipStream_t)stream));
+}
+
+// ------------------------------------------------- gated linear recurrence
+
+static int check_scan_shape(int dtype, int64_t B, int64_t S, int64_t C) {
+  if (!dtype_ok(dtype)) return HC_ERR_DTYPE;
+  if (B < 0 || S < 0 || C < 1 || C > (1ll << 26) || B > (1ll << 31) || S > (1ll << 40)) return HC_ERR_SHAPE;
+  if ((double)B * (double)(S > 64 ? S : 64) * (double)C > 549755813888.0) return HC_ERR_SHAPE;  // grid size
+  return HC_OK;
+}
+
+int64_t hc_gated_scan_workspace_bytes(int64_t B, int64_t S, int64_t C) {
+  if (check_scan_shape(HC_F32, B, S, C) != HC_OK) return -1;
+  return B == 0 ? 0 : hc::scan_ws_bytes(B, S, C);
+}
+
+// four channels of a row in one aligned access, and the states' rows too
+static bool scan_vec(int64_t C, int dtype, std::initializer_list<const void*> streams,
+                     std::initializer_list<const void*> states) {
+  if (C % 4 != 0) return false;
+  for (const void* p : streams)
+    if (p && !aligned_to(p, 4 * esize(dtype))) return false;
+  for (const void* p : states)
+    if (p && !aligned_to(p, 16)) return false;
+  return true;
+}
+
+int hc_gated_scan(const void* x, const void* gate, int dtype, int64_t B, int64_t S, int64_t C, const float* h0,
+                  const int32_t* lengths, int tied, void* y, float* h_last, void* workspace, int64_t workspace_bytes,
+                  void* stream) {
+  int r = check_scan_shape(dtype, B, S, C);
+  if (r != HC_OK || B == 0 || (S == 0 && !h_last)) return r;
+  const int64_t e = (int64_t)esize(dtype), xb = B * S * C * e, hb = B * C * 4;
+  const int64_t wsb = hc::scan_ws_bytes(B, S, C);
+  const Buf bx{x, xb, (uintptr_t)e, S > 0}, bg{gate, xb, (uintptr_t)e, S > 0}, b0{h0, hb, 4, false},
+      bl{lengths, B * 4, 4, false}, by{y, xb, (uintptr_t)e, S > 0}, b1{h_last, hb, 4, false},
+      bk{wsb ? workspace : nullptr, wsb, 1, false};
+  if ((r = check_bufs({bx, bg, b0, bl, by, b1})) != HC_OK) return r;
+  if ((r = check_ws(workspace, workspace_bytes, wsb)) != HC_OK) return r;
+  if (bufs_overlap({by, b1, bk}, {bx, bg, bl}) || bufs_overlap({by, bk}, {b0}) ||
+      (h_last != h0 && overlaps(h_last, hb, h0, hb)))
+    return HC_ERR_ALIAS;
+  if ((r = device_status()) != HC_OK) return r;
+  const hc::ScanArgs a{x, gate, nullptr, nullptr, h0, nullptr, lengths, y, nullptr, h_last, workspace, B, S, C, tied};
+  return launch_status(hc::launch_scan(dtype, false, scan_vec(C, dtype, {x, gate, y}, {h0, h_last}), a,
+                                       (hipStream_t)stream));
+}
+
+int hc_gated_scan_backward(const void* x, const void* gate, const void* y, const void* dy, int dtype, int64_t B,
+                           int64_t S, int64_t C, const float* h0, const float* dh_last, const int32_t* lengths,
+                           int tied, void* dx, void* dgate, float* dh0, void* workspace, int64_t workspace_bytes,
+                           void* stream) {
+  int r = check_scan_shape(dtype, B, S, C);
+  if (r != HC_OK || B == 0 || (S == 0 && !dh0)) return r;
+  const int64_t e = (int64_t)esize(dtype), xb = B * S * C * e, hb = B * C * 4;
+  const uintptr_t ea = (uintptr_t)e;
+  const int64_t wsb = hc::scan_ws_bytes(B, S, C);
+  const Buf bx{x, xb, ea, S > 0}, bg{gate, xb, ea, S > 0}, by{y, xb, ea, S > 0}, bd{dy, xb, ea, S > 0},
+      b0{h0, hb, 4, false}, bh{dh_last, hb, 4, false}, bl{lengths, B * 4, 4, false}, ox{dx, xb, ea, S > 0},
+      og{dgate, xb, ea, S > 0}, o0{dh0, hb, 4, false}, bk{wsb ? workspace : nullptr, wsb, 1, false};
+  if ((r = check_bufs({bx, bg, by, bd, b0, bh, bl, ox, og, o0})) != HC_OK) return r;
+  if ((r = check_ws(workspace, workspace_bytes, wsb)) != HC_OK) return r;
+  if (bufs_overlap({ox, og, o0, bk}, {bx, bg, by, bd, b0, bh, bl})) return HC_ERR_ALIAS;
+  if ((r = device_status()) != HC_OK) return r;
+  const hc::ScanArgs a{x, gate, y, dy, h0, dh_last, lengths, dx, dgate, dh0, workspace, B, S, C, tied};
+  return launch_status(hc::launch_scan(
+      dtype, true, scan_vec(C, dtype, {x, gate, y, dy, dx, dgate}, {h0, dh_last, dh0}), a, (hipStream_t)stream));
+}
+
+// ----------------------------------------------- training the stream router
+
+static int check_balance_shape(int64_t B, int64_t S, int N, int k, int m) {
+  if (N < 2 || N > HC_MAX_STREAMS || m < 1 || k <= m || k > N || k > HC_MAX_ACTIVE) return HC_ERR_SHAPE;
+  if (B < 0 || S < 0 || B >= (1ll << 26) || S >= (1ll << 26) || B * S >= (1ll << 26)) return HC_ERR_SHAPE;
+  return HC_OK;
+}
+
+int64_t xhc_balance_loss_workspace_bytes(int64_t B, int64_t S, int N, int m) {
+  if (check_balance_shape(B, S, N, m + 1, m) != HC_OK) return -1;
+  return hc::balance_ws_bytes(B, S, N, m);
+}
+
+int xhc_balance_loss(const float* score, const int32_t* idx, const uint8_t* mask, int64_t B, int64_t S, int N, int k,
+                     int m, float coef, float* loss, int32_t* count, int32_t* tokens, float* mean_p, void* workspace,
+                     int64_t workspace_bytes, void* stream) {
+  int r = check_balance_shape(B, S, N, k, m);
+  if (r != HC_OK) return r;
+  const int64_t T = B * S, E = N - m, wsb = hc::balance_ws_bytes(B, S, N, m);
+  const Buf bs{score, T * E * 4, 4, T > 0}, bi{idx, T * k * 4, 4, T > 0}, bm{mask, T, 1, false}, ol{loss, 4, 4, true},
+      oc{count, B * N * 4, 4, B > 0}, ot{tokens, B * 4, 4, B > 0}, op{mean_p, B * E * 4, 4, B > 0},
+      bk{wsb ? workspace : nullptr, wsb, 1, false};
+  if ((r = check_bufs({bs, bi, bm, ol, oc, ot, op})) != HC_OK) return r;
+  if ((r = check_ws(workspace, workspace_bytes, wsb)) != HC_OK) return r;
+  if (bufs_overlap({ol, oc, ot, op, bk}, {bs, bi, bm})) return HC_ERR_ALIAS;
+  if ((r = device_status()) != HC_OK) return r;
+  return launch_status(hc::launch_balance(score, idx, mask, B, S, N, k, m, coef, loss, count, tokens, mean_p,
+                                          workspace, (hipStream_t)stream));
+}
+
+int xhc_balance_loss_backward(const float* score, const int32_t* count, const int32_t* tokens, const uint8_t* mask,
+                              int64_t B, int64_t S, int N, int k, int m, float coef, const float* dloss,
+                              float* dscore, void* stream) {
+  int r = check_balance_shape(B, S, N, k, m);
+  if (r != HC_OK || B * S == 0) return r;
+  const int64_t T = B * S, E = N - m;
+  const Buf bs{score, T * E * 4, 4, true}, bc{count, B * N * 4, 4, true}, bt{tokens, B * 4, 4, true},
+      bm{mask, T, 1, false}, bl{dloss, 4, 4, false}, od{dscore, T * E * 4, 4, true};
+  if ((r = check_bufs({bs, bc, bt, bm, bl, od})) != HC_OK) return r;
+  if (bufs_overlap({od}, {bs, bc, bt, bm, bl})) return HC_ERR_ALIAS;
+  if ((r = device_status()) != HC_OK) return r;
+  return launch_status(hc::launch_balance_backward(score, count, tokens, mask, B, S, N, k, m, coef, dloss, dscore,
+                                                   (hipStream_t)stream));
+}
+
+static int check_router_shape(int dtype, int64_t T, int N, int64_t C, int m) {
+  if (dtype != HC_BF16) return HC_ERR_DTYPE;
+  if (T < 0 || T >= (1ll << 24) || m < 1 || N <= m || N > HC_MAX_ROUTER_STREAMS || C < 32 || C % 32 != 0 ||
+      C > (1ll << 26))
+    return HC_ERR_SHAPE;
+  return HC_OK;
+}
+
+int64_t xhc_router_backward_workspace_bytes(int64_t T, int N, int64_t C, int m, int dtype) {
+  if (check_router_shape(dtype, T, N, C, m) != HC_OK) return -1;
+  return hc::router_backward_ws_bytes(T, N, C, m);
+}
+
+int xhc_router_backward(const void* X, int dtype, int64_t T, int N, int64_t C, int m, const float* w_router,
+                        const float* score, const float* dscore, const void* dX, void* dX_out, float* dw_router,
+                        void* workspace, int64_t workspace_bytes, void* stream) {
+  int r = check_router_shape(dtype, T, N, C, m);
+  if (r != HC_OK) return r;
+  const int64_t E = N - m, xb = T * N * C * 2, wb = (int64_t)N * C * E * 4;
+  const int64_t wsb = hc::router_backward_ws_bytes(T, N, C, m);
+  const bool some = T > 0;
+  const Buf bx{X, xb, 16, some}, bw{w_router, wb, 4, some}, bs{score, T * E * 4, 4, some},
+      bd{dscore, T * E * 4, 4, some}, bi{dX, xb, 16, some}, ox{dX_out, xb, 16, some}, ow{dw_router, wb, 4, true},
+      bk{wsb ? workspace : nullptr, wsb, 1, false};
+  if ((r = check_bufs({bx, bw, bs, bd, bi, ox, ow})) != HC_OK) return r;
+  if ((r = check_ws(workspace, workspace_bytes, wsb)) != HC_OK) return r;
+  if (bufs_overlap({ox, ow, bk}, {bx, bw, bs, bd}) || bufs_overlap({ow, bk}, {bi}) ||
+      (dX_out != dX && overlaps(dX_out, xb, dX, xb)))
+    return HC_ERR_ALIAS;
+  if ((r = device_status()) != HC_OK) return r;
+  return launch_status(hc::launch_router_backward(X, T, N, C, m, w_router, score, dscore, dX, dX_out, dw_router,
+                                                  workspace, (hipStream_t)stream));
 }
 
 int hc_copy_probe(const void* src, void* dst, int64_t bytes, void* stream) {

@@ -1,0 +1,431 @@
+// Root-mean-square norm in front of a sublayer function, forward and backward.
+//   v = x, x + residual, or the pre-read sum_i h_pre[i] X[i];
+//   y = v * w / sqrt(mean_c v^2 + eps), stored in the stream dtype or as 8-bit
+//   codes with a scale per row or per group of 32, 64 or 128 channels.
+// Each row is read once and stays in float32 registers between the sum of squares
+// and the outputs, so the passes are bound by HBM traffic.
+#include "hc_device.h"
+#include "hc_launch.h"
+
+namespace hc {
+
+namespace {
+
+constexpr int OUT_STREAM = 0, OUT_E4M3 = 2, OUT_I8 = 3;  // the dtype codes of hc.h for the 8-bit forms
+
+// One row's threads: NT threads with ITEMS pieces of 8 channels each, piece
+// (it * NT + tid). 64 threads (a wave, four rows per workgroup, no barrier) up to
+// 2,048 channels, a workgroup of 256 up to 8,192, of 1,024 up to 16,384.
+template <int NT>
+struct RowThreads {
+  static constexpr int RPB = NT < 256 ? 256 / NT : 1;  // rows in flight per workgroup
+  static constexpr int BLOCK = NT * RPB;
+  static constexpr int NW = NT / 64;
+};
+
+// VEC: rows of whole pieces at 16-byte aligned addresses. Otherwise whole pieces are
+// still one access each (global memory takes any element-aligned address), and only
+// a row's ragged last piece goes element by element.
+__device__ __forceinline__ int piece_count(int64_t c0, int64_t C) {
+  return (int)max((int64_t)0, min((int64_t)8, C - c0));
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void row_load(const T* row, int64_t c0, int64_t C, float v[8]) {
+  const int cnt = piece_count(c0, C);
+  if (VEC) {
+    if (cnt > 0) load8_nt(row + c0, v);
+    else
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+  } else if (cnt == 8) {
+    load8_any(row + c0, v);
+  } else {
+    load8_tail(row + c0, cnt, v);
+  }
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void row_store(T* row, int64_t c0, int64_t C, const float v[8]) {
+  const int cnt = piece_count(c0, C);
+  if (VEC) {
+    if (cnt > 0) store8_nt(row + c0, v);
+  } else if (cnt == 8) {
+    store8_any(row + c0, v);
+  } else {
+    store8_tail(row + c0, cnt, v);
+  }
+}
+
+// The weight is used by every row: ordinary loads, kept in registers over the rows.
+template <bool VEC, int NT, int ITEMS>
+__device__ __forceinline__ void load_weight(const float* w, int64_t C, int tid, float out[ITEMS][8]) {
+#pragma unroll
+  for (int it = 0; it < ITEMS; ++it) {
+    const int64_t c0 = ((int64_t)it * NT + tid) * 8;
+    if (w == nullptr) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out[it][e] = 1.f;
+    } else if (piece_count(c0, C) == 8) {
+      if (VEC) load8(w + c0, out[it]);
+      else load8_any(w + c0, out[it]);
+    } else {
+      load8_tail(w + c0, piece_count(c0, C), out[it]);
+    }
+  }
+}
+
+// Sums over one row's threads, the same value in each; `red` is this row parity's
+// slice of LDS (the next row uses the other one, so one barrier per sum is enough).
+template <int NT>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = wave_sum(v);
+  if (NT == 64) return v;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < RowThreads<NT>::NW; ++i) s += red[i];
+  return s;
+}
+
+// The largest magnitude as float bits: ordering the bits as unsigned numbers puts
+// infinity above every number and NaN above infinity, so a NaN is never lost.
+__device__ __forceinline__ uint32_t umax_xor(uint32_t v, int mask) {
+  return max(v, (uint32_t)__shfl_xor((int)v, mask, 64));
+}
+
+template <int NT>
+__device__ __forceinline__ uint32_t row_umax(uint32_t v, uint32_t* red) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) v = umax_xor(v, o);
+  if (NT == 64) return v;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  uint32_t s = 0;
+#pragma unroll
+  for (int i = 0; i < RowThreads<NT>::NW; ++i) s = max(s, red[i]);
+  return s;
+}
+
+__device__ __forceinline__ float rms_factor(float sumsq, float inv_c, float eps) {
+  const float ms = sumsq * inv_c + eps;
+  return ms == 0.f ? 0.f : 1.0f / sqrtf(ms);  // the all-zero row without eps normalises to zero
+}
+
+// 8 codes of 8 bits. Clamped first: rounding up at the largest code would overflow.
+__device__ __forceinline__ uint2 pack_e4m3(const float v[8], float inv) {
+  float c[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float q = v[e] * inv;
+    c[e] = q != q ? q : fminf(fmaxf(q, -448.f), 448.f);
+  }
+  uint2 r;
+  int lo = 0, hi = 0;
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[0], c[1], lo, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(c[2], c[3], lo, true);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(c[4], c[5], hi, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(c[6], c[7], hi, true);
+  r.x = (uint32_t)lo;
+  r.y = (uint32_t)hi;
+  return r;
+}
+
+__device__ __forceinline__ uint2 pack_i8(const float v[8], float inv) {
+  uint32_t b[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float q = v[e] * inv;
+    b[e] = (uint32_t)(q != q ? 0 : (int)rintf(fminf(fmaxf(q, -127.f), 127.f))) & 0xffu;
+  }
+  uint2 r;
+  r.x = b[0] | (b[1] << 8) | (b[2] << 16) | (b[3] << 24);
+  r.y = b[4] | (b[5] << 8) | (b[6] << 16) | (b[7] << 24);
+  return r;
+}
+
+// MODE 0: v = x; 1: v = x + residual; 2: v = sum_i h[i] x[i] (n streams).
+template <typename T, int MODE, int NT, int ITEMS, bool VEC>
+__global__ __launch_bounds__(RowThreads<NT>::BLOCK) void rms_norm_kernel(NormArgs a) {
+  using R = RowThreads<NT>;
+  __shared__ float red[2][16];
+  __shared__ uint32_t redm[2][16];
+  const int tid = threadIdx.x % NT, sub = threadIdx.x / NT;
+  const int64_t C = a.C;
+  const float inv_c = 1.0f / (float)C;
+  float w[ITEMS][8];
+  load_weight<VEC, NT, ITEMS>(a.w, C, tid, w);
+  int parity = 0;
+  for (int64_t t = (int64_t)blockIdx.x * R::RPB + sub; t < a.T; t += (int64_t)gridDim.x * R::RPB, parity ^= 1) {
+    float v[ITEMS][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const int64_t c0 = ((int64_t)it * NT + tid) * 8;
+      if (MODE == 2) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[it][e] = 0.f;
+        for (int i = 0; i < a.n; ++i) {
+          float xi[8];
+          row_load<VEC>((const T*)a.x + (t * a.n + i) * C, c0, C, xi);
+          const float hi = a.h[t * a.n + i];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[it][e] += hi * xi[e];
+        }
+      } else {
+        row_load<VEC>((const T*)a.x + t * C, c0, C, v[it]);
+        if (MODE == 1) {
+          float r[8];
+          row_load<VEC>((const T*)a.res + t * C, c0, C, r);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[it][e] += r[e];
+        }
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const int64_t c0 = ((int64_t)it * NT + tid) * 8;
+      if (MODE != 0 && a.s) row_store<VEC>((T*)a.s + t * C, c0, C, v[it]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (MODE != 2 || (VEC ? c0 : c0 + e) < C) ss += v[it][e] * v[it][e];  // 0 * an infinite h is no channel's
+    }
+    const float rstd = rms_factor(row_sum<NT>(ss, red[parity]), inv_c, a.eps);
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[it][e] *= rstd * w[it][e];
+    if (a.out == OUT_STREAM) {
+#pragma unroll
+      for (int it = 0; it < ITEMS; ++it)
+        row_store<VEC>((T*)a.y + t * C, ((int64_t)it * NT + tid) * 8, C, v[it]);
+      continue;
+    }
+    uint32_t m[ITEMS];
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      m[it] = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const bool in = VEC ? ((int64_t)it * NT + tid) * 8 < C : ((int64_t)it * NT + tid) * 8 + e < C;
+        if (in) m[it] = max(m[it], __float_as_uint(v[it][e]) & 0x7fffffffu);
+      }
+    }
+    const float qmax = a.out == OUT_E4M3 ? 448.f : 127.f;
+    if (a.group == 0) {
+      uint32_t all = 0;
+#pragma unroll
+      for (int it = 0; it < ITEMS; ++it) all = max(all, m[it]);
+      all = row_umax<NT>(all, redm[parity]);
+#pragma unroll
+      for (int it = 0; it < ITEMS; ++it) m[it] = all;
+    } else {  // a group's 4, 8 or 16 threads are neighbours in a wave
+#pragma unroll
+      for (int it = 0; it < ITEMS; ++it) {
+        m[it] = umax_xor(umax_xor(m[it], 1), 2);
+        if (a.group > 32) m[it] = umax_xor(m[it], 4);
+        if (a.group > 64) m[it] = umax_xor(m[it], 8);
+      }
+    }
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const int64_t c0 = ((int64_t)it * NT + tid) * 8;
+      float scale = __uint_as_float(m[it]) / qmax;
+      if (scale < 0x1p-126f) scale = 1.f;
+      const float inv = 1.f / scale;
+      if (c0 < C) {
+        if (a.group == 0) {
+          if (c0 == 0) a.scale[t] = scale;
+        } else if (c0 % a.group == 0) {
+          a.scale[t * a.ngroups + c0 / a.group] = scale;
+        }
+        const uint2 q = a.out == OUT_E4M3 ? pack_e4m3(v[it], inv) : pack_i8(v[it], inv);
+        uint8_t* p = (uint8_t*)a.y + t * C + c0;
+        const int cnt = piece_count(c0, C);
+        if (VEC) {
+          *reinterpret_cast<uint2*>(p) = q;
+        } else if (cnt == 8) {
+          __builtin_memcpy(p, &q, 8);
+        } else {
+          for (int e = 0; e < cnt; ++e) p[e] = (uint8_t)((e < 4 ? q.x >> (8 * e) : q.y >> (8 * (e - 4))) & 0xffu);
+        }
+      }
+    }
+  }
+}
+
+// dx = rstd w dy - v rstd^3 mean(w dy v) + ds, and this workgroup's part of
+// dw = sum_t dy v rstd, kept in registers over its rows and written once to
+// part[workgroup row][C] (the parts are added in a fixed order afterwards).
+template <typename T, int NT, int ITEMS, bool VEC>
+__global__ __launch_bounds__(RowThreads<NT>::BLOCK) void rms_norm_backward_kernel(NormBwdArgs a) {
+  using R = RowThreads<NT>;
+  __shared__ float red[2][2][16];
+  const int tid = threadIdx.x % NT, sub = threadIdx.x / NT;
+  const int64_t C = a.C;
+  const float inv_c = 1.0f / (float)C;
+  float w[ITEMS][8], dw[ITEMS][8];
+  load_weight<VEC, NT, ITEMS>(a.w, C, tid, w);
+#pragma unroll
+  for (int it = 0; it < ITEMS; ++it)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[it][e] = 0.f;
+  int parity = 0;
+  for (int64_t t = (int64_t)blockIdx.x * R::RPB + sub; t < a.T; t += (int64_t)gridDim.x * R::RPB, parity ^= 1) {
+    float v[ITEMS][8], dy[ITEMS][8], ds[ITEMS][8];
+    float ss = 0.f, dot = 0.f;
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const int64_t c0 = ((int64_t)it * NT + tid) * 8;
+      row_load<VEC>((const T*)a.s + t * C, c0, C, v[it]);
+      row_load<VEC>((const T*)a.dy + t * C, c0, C, dy[it]);
+      if (a.ds) row_load<VEC>((const T*)a.ds + t * C, c0, C, ds[it]);
+    }
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        ss += v[it][e] * v[it][e];
+        dot += v[it][e] * (w[it][e] * dy[it][e]);
+      }
+    if (NT == 64) {
+      ss = wave_sum(ss);
+      dot = wave_sum(dot);
+    } else {
+      ss = wave_sum(ss);
+      dot = wave_sum(dot);
+      if ((threadIdx.x & 63) == 0) {
+        red[parity][0][threadIdx.x >> 6] = ss;
+        red[parity][1][threadIdx.x >> 6] = dot;
+      }
+      __syncthreads();
+      ss = dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < R::NW; ++i) {
+        ss += red[parity][0][i];
+        dot += red[parity][1][i];
+      }
+    }
+    const float rstd = rms_factor(ss, inv_c, a.eps);
+    const float k = (dot * rstd) * inv_c * rstd;
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      float o[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        dw[it][e] += dy[it][e] * (v[it][e] * rstd);
+        o[e] = rstd * (w[it][e] * dy[it][e] - v[it][e] * k) + (a.ds ? ds[it][e] : 0.f);
+      }
+      row_store<VEC>((T*)a.dx + t * C, ((int64_t)it * NT + tid) * 8, C, o);
+    }
+  }
+  if (a.part == nullptr) return;
+  float* p = a.part + ((int64_t)blockIdx.x * R::RPB + sub) * C;
+#pragma unroll
+  for (int it = 0; it < ITEMS; ++it) {
+    const int64_t c0 = ((int64_t)it * NT + tid) * 8;
+    if (VEC) {
+      if (c0 < C) store8(p + c0, dw[it]);
+    } else if (piece_count(c0, C) == 8) {
+      store8_any(p + c0, dw[it]);
+    } else {
+      store8_tail(p + c0, piece_count(c0, C), dw[it]);
+    }
+  }
+}
+
+// out[c] = sum_p part[p][c]: 32 columns by 8 interleaved walks per workgroup, the
+// walks added in order.
+__global__ __launch_bounds__(256) void column_sum_kernel(const float* __restrict__ part, int64_t P, int64_t C,
+                                                         float* __restrict__ out) {
+  __shared__ float s[8][32];
+  const int cl = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + cl;
+  float v = 0.f;
+  if (c < C)
+    for (int64_t p = g; p < P; p += 8) v += part[p * C + c];
+  s[g][cl] = v;
+  __syncthreads();
+  if (g == 0 && c < C) {
+    float r = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r += s[i][cl];
+    out[c] = r;
+  }
+}
+
+// The workgroups of a pass over T rows: enough to fill the device, few enough that
+// each keeps the weight in registers over several rows.
+template <int NT>
+int64_t row_blocks(int64_t T, int64_t most) {
+  const int64_t need = (T + RowThreads<NT>::RPB - 1) / RowThreads<NT>::RPB;
+  return need < most ? need : most;
+}
+
+constexpr int64_t FWD_BLOCKS = 2048, BWD_BLOCKS = 512;
+
+template <typename T, int MODE, int NT, int ITEMS>
+void norm_go(bool vec, const NormArgs& a, hipStream_t st) {
+  const dim3 g((unsigned)row_blocks<NT>(a.T, FWD_BLOCKS)), b(RowThreads<NT>::BLOCK);
+  if (vec) hipLaunchKernelGGL((rms_norm_kernel<T, MODE, NT, ITEMS, true>), g, b, 0, st, a);
+  else hipLaunchKernelGGL((rms_norm_kernel<T, MODE, NT, ITEMS, false>), g, b, 0, st, a);
+}
+
+template <typename T, int MODE>
+void norm_by_width(bool vec, const NormArgs& a, hipStream_t st) {
+  if (a.C <= 512) norm_go<T, MODE, 64, 1>(vec, a, st);
+  else if (a.C <= 1024) norm_go<T, MODE, 64, 2>(vec, a, st);
+  else if (a.C <= 2048) norm_go<T, MODE, 64, 4>(vec, a, st);
+  else if (a.C <= 4096) norm_go<T, MODE, 256, 2>(vec, a, st);
+  else if (a.C <= 8192) norm_go<T, MODE, 256, 4>(vec, a, st);
+  else norm_go<T, MODE, 1024, 2>(vec, a, st);
+}
+
+template <typename T, int NT, int ITEMS>
+void norm_bwd_go(bool vec, const NormBwdArgs& a, hipStream_t st) {
+  const dim3 g((unsigned)row_blocks<NT>(a.T, BWD_BLOCKS)), b(RowThreads<NT>::BLOCK);
+  if (vec) hipLaunchKernelGGL((rms_norm_backward_kernel<T, NT, ITEMS, true>), g, b, 0, st, a);
+  else hipLaunchKernelGGL((rms_norm_backward_kernel<T, NT, ITEMS, false>), g, b, 0, st, a);
+}
+
+template <typename T>
+void norm_bwd_by_width(bool vec, const NormBwdArgs& a, hipStream_t st) {
+  if (a.C <= 512) norm_bwd_go<T, 64, 1>(vec, a, st);
+  else if (a.C <= 1024) norm_bwd_go<T, 64, 2>(vec, a, st);
+  else if (a.C <= 2048) norm_bwd_go<T, 64, 4>(vec, a, st);
+  else if (a.C <= 4096) norm_bwd_go<T, 256, 2>(vec, a, st);
+  else if (a.C <= 8192) norm_bwd_go<T, 256, 4>(vec, a, st);
+  else norm_bwd_go<T, 1024, 2>(vec, a, st);
+}
+
+}  // namespace
+
+int64_t norm_backward_parts(int64_t T, int64_t C) {
+  return C <= 2048 ? row_blocks<64>(T, BWD_BLOCKS) * RowThreads<64>::RPB : row_blocks<256>(T, BWD_BLOCKS);
+}
+
+hipError_t launch_rms_norm(int dtype, int mode, bool vec, const NormArgs& a, hipStream_t st) {
+  if (dtype == 0) {
+    if (mode == 0) norm_by_width<float, 0>(vec, a, st);
+    else if (mode == 1) norm_by_width<float, 1>(vec, a, st);
+    else norm_by_width<float, 2>(vec, a, st);
+  } else {
+    if (mode == 0) norm_by_width<bf16_t, 0>(vec, a, st);
+    else if (mode == 1) norm_by_width<bf16_t, 1>(vec, a, st);
+    else norm_by_width<bf16_t, 2>(vec, a, st);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_rms_norm_backward(int dtype, bool vec, const NormBwdArgs& a, float* dw, hipStream_t st) {
+  if (a.T > 0 && dtype == 0) norm_bwd_by_width<float>(vec, a, st);
+  else if (a.T > 0) norm_bwd_by_width<bf16_t>(vec, a, st);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || dw == nullptr) return e;
+  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((a.C + 31) / 32)), dim3(256), 0, st, a.part,
+                     norm_backward_parts(a.T, a.C), a.C, dw);
+  return hipGetLastError();
+}
+
+}  // namespace hc

@@ -1,0 +1,343 @@
+// Training of the xHC stream router: the balance loss over the active sets, with
+// its gradient to the scores, and the backward of the router's projection.
+//   balance, per sequence b of n_b unmasked tokens: count_i = tokens whose active
+//   set holds stream i, p_tj = s_tj / sum_j s_tj, P_j = mean_t p_tj,
+//   f_j = E / ((k - m) n_b) count_{m+j};  loss = coef / B sum_b sum_j f_j P_j.
+//   router: z_t = (vec X_t @ W) / r_t, s = sigmoid(z), r = ||vec X|| / sqrt(NC).
+#include "hc_device.h"
+#include "hc_launch.h"
+
+namespace hc {
+
+namespace {
+
+// W lanes of a wave share a token (lane j: candidate j, or stream j for the
+// counts), so the scores are read once, in order, and the row's sum is a DPP sum.
+template <int W>
+__device__ __forceinline__ float lanes_sum(float v) {
+  return W == 16 ? row16_sum(v) : wave_sum(v);
+}
+
+constexpr int BAL_TOKENS = 256;  // tokens of one workgroup's part
+
+__device__ __forceinline__ float share(float s, float total) { return total == 0.f ? 0.f : s / total; }
+
+// Per (sequence, 256 tokens): counts [W], sums of p [W] and the unmasked tokens.
+template <int W>
+__global__ __launch_bounds__(256) void balance_part_kernel(const float* __restrict__ score,
+                                                           const int32_t* __restrict__ idx,
+                                                           const uint8_t* __restrict__ mask, int64_t S, int64_t nblk, int E,
+                                                           int k, float* __restrict__ psum, int32_t* __restrict__ cnt,
+                                                           int32_t* __restrict__ tok) {
+  constexpr int SLOTS = 256 / W;
+  __shared__ float sp[SLOTS][W];
+  __shared__ int32_t sc[SLOTS][W], sn[SLOTS];
+  const int j = threadIdx.x % W, slot = threadIdx.x / W;
+  const int64_t part = blockIdx.x, b = part / nblk, t0 = (part - b * nblk) * BAL_TOKENS;
+  const int64_t t1 = t0 + BAL_TOKENS < S ? t0 + BAL_TOKENS : S;
+  float p = 0.f;
+  int32_t c = 0, n = 0;
+  for (int64_t t = t0 + slot; t < t1; t += SLOTS) {
+    const int64_t at = b * S + t;
+    if (mask && !mask[at]) continue;
+    const float s = j < E ? score[at * E + j] : 0.f;
+    p += share(s, lanes_sum<W>(s));
+    for (int a = 0; a < k; ++a) c += idx[at * k + a] == j;
+    ++n;
+  }
+  sp[slot][j] = p;
+  sc[slot][j] = c;
+  if (j == 0) sn[slot] = n;
+  __syncthreads();
+  if (slot == 0) {
+    float ps = 0.f;
+    int32_t cs = 0, ns = 0;
+    for (int i = 0; i < SLOTS; ++i) {
+      ps += sp[i][j];
+      cs += sc[i][j];
+      ns += sn[i];
+    }
+    psum[part * W + j] = ps;
+    cnt[part * W + j] = cs;
+    if (j == 0) tok[part] = ns;
+  }
+}
+
+// One workgroup adds the parts, in order, and forms the loss.
+template <int W>
+__global__ __launch_bounds__(256) void balance_finish_kernel(const float* __restrict__ psum,
+                                                             const int32_t* __restrict__ cnt,
+                                                             const int32_t* __restrict__ tok, int64_t B, int64_t nblk,
+                                                             int N, int k, int m, float coef, float* __restrict__ loss,
+                                                             int32_t* __restrict__ count,
+                                                             int32_t* __restrict__ tokens,
+                                                             float* __restrict__ mean_p) {
+  constexpr int SLOTS = 256 / W;
+  __shared__ float red[4];
+  __shared__ int32_t sc[SLOTS][W];
+  const int j = threadIdx.x % W, slot = threadIdx.x / W;
+  const int E = N - m;
+  float sum = 0.f;
+  for (int64_t b0 = 0; b0 < B; b0 += SLOTS) {
+    const int64_t b = b0 + slot;
+    float ps = 0.f;
+    int32_t cs = 0, ns = 0;
+    if (b < B) {
+      for (int64_t i = 0; i < nblk; ++i) {
+        const int64_t part = b * nblk + i;
+        ps += psum[part * W + j];
+        cs += cnt[part * W + j];
+        ns += tok[part];
+      }
+    }
+    sc[slot][j] = cs;
+    __syncthreads();
+    if (b < B) {
+      if (j < N) count[b * N + j] = cs;
+      if (j == 0) tokens[b] = ns;
+      if (j < E) {
+        const float n = (float)(ns > 0 ? ns : 1);
+        const float mp = ps / n;
+        const float f = (float)sc[slot][m + j] * ((float)E / (float)(k - m)) / n;
+        mean_p[b * E + j] = mp;
+        sum += f * mp;
+      }
+    }
+    __syncthreads();
+  }
+  const float all = block_sum(sum, red);
+  if (threadIdx.x == 0) *loss = B > 0 ? coef * (all / (float)B) : 0.f;
+}
+
+// dscore_tj = dloss coef / (B n) (f_j - sum_i f_i p_ti) / sum_i s_ti; 0 for masked tokens.
+template <int W>
+__global__ __launch_bounds__(256) void balance_backward_kernel(const float* __restrict__ score,
+                                                               const int32_t* __restrict__ count,
+                                                               const int32_t* __restrict__ tokens,
+                                                               const uint8_t* __restrict__ mask, int64_t B, int64_t S,
+                                                               int N, int k, int m, float coef,
+                                                               const float* __restrict__ dloss,
+                                                               float* __restrict__ dscore) {
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) / W;
+  const int j = threadIdx.x % W;
+  const int E = N - m;
+  if (at >= B * S) return;
+  const int64_t b = at / S;
+  const bool live = !mask || mask[at];
+  float g = 0.f;
+  if (live) {  // uniform over the token's lanes
+    const int32_t ns = tokens[b];
+    const float n = (float)(ns > 0 ? ns : 1);
+    const float s = j < E ? score[at * E + j] : 0.f;
+    const float f = j < E ? (float)count[b * N + m + j] * ((float)E / (float)(k - m)) / n : 0.f;
+    const float total = lanes_sum<W>(s);
+    const float dot = lanes_sum<W>(f * share(s, total));
+    const float w = (dloss ? *dloss : 1.f) * coef / ((float)B * n);
+    g = total == 0.f ? 0.f : w * (f - dot) / total;
+  }
+  if (j < E) dscore[at * E + j] = g;
+}
+
+// ---------------------------------------------------- the router's projection
+
+constexpr int PW = 16;  // floats per token: dz_j / r for j < E <= 15, and the factor of x in slot 15
+
+// One workgroup per token: r from the whole row, then the token's factors. A token
+// whose dscore is all zero takes part in nothing: its row is not read.
+__global__ __launch_bounds__(256) void router_factors_kernel(const bf16_t* __restrict__ X, int64_t NC, int E,
+                                                             const float* __restrict__ score,
+                                                             const float* __restrict__ dscore, float* __restrict__ P) {
+  __shared__ float red[4];
+  const int64_t t = blockIdx.x;
+  const int j = threadIdx.x;
+  bool any = false;
+  for (int i = 0; i < E; ++i) any |= dscore[t * E + i] != 0.f;
+  float* out = P + t * PW;
+  if (!any) {
+    if (j < PW) out[j] = 0.f;
+    return;
+  }
+  const bf16_t* x = X + t * NC;
+  float ss = 0.f;
+  for (int64_t c = (int64_t)threadIdx.x * 8; c < NC; c += 2048) {
+    float v[8];
+    load8(x + c, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
+  }
+  ss = block_sum(ss, red);
+  if (j < 64) {
+    float dz = 0.f, along = 0.f;
+    if (j < E) {
+      const float s = score[t * E + j];
+      dz = dscore[t * E + j] * (s * (1.f - s));
+      along = dz == 0.f ? 0.f : dz * (logf(s) - logf(1.f - s));  // z from its sigmoid
+    }
+    along = row16_sum(along);  // E <= 15: one row of 16 lanes
+    const float ms = ss / (float)NC;
+    const float inv_r = ms == 0.f ? 0.f : 1.f / sqrtf(ms);
+    if (j < PW - 1) out[j] = dz * inv_r;
+    else if (j == PW - 1) out[j] = along * inv_r * inv_r / (float)NC;
+  }
+}
+
+// dX_out = dX_in + P w - c x and this split's part of dw = sum_t x P. Each thread
+// owns 4 of the N*C channels and keeps their rows of w and dw in registers; the
+// token's 16 factors are the same for the whole wave.
+template <int E>
+__global__ __launch_bounds__(256) void router_apply_kernel(const bf16_t* __restrict__ X, int64_t T, int64_t NC, int Er,
+                                                           int64_t per, const float* __restrict__ w,
+                                                           const float* __restrict__ P, const bf16_t* dX_in,
+                                                           bf16_t* dX_out, float* __restrict__ part) {
+  const int64_t c0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (c0 >= NC) return;
+  float wv[4][E], dw[4][E];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      wv[e][j] = j < Er ? w[(c0 + e) * Er + j] : 0.f;
+      dw[e][j] = 0.f;
+    }
+  const int64_t t0 = (int64_t)blockIdx.y * per, t1 = t0 + per < T ? t0 + per : T;
+#pragma unroll 4
+  for (int64_t t = t0; t < t1; ++t) {
+    const uint2 xq = *reinterpret_cast<const uint2*>(X + t * NC + c0);
+    const uint2 dq = *reinterpret_cast<const uint2*>(dX_in + t * NC + c0);
+    const float* f = P + t * PW;
+    bool any = f[PW - 1] != 0.f;
+#pragma unroll
+    for (int j = 0; j < E; ++j) any |= f[j] != 0.f;
+    float x[4] = {bf2f(xq.x & 0xffffu), __uint_as_float(xq.x & 0xffff0000u), bf2f(xq.y & 0xffffu),
+                  __uint_as_float(xq.y & 0xffff0000u)};
+    float o[4] = {bf2f(dq.x & 0xffffu), __uint_as_float(dq.x & 0xffff0000u), bf2f(dq.y & 0xffffu),
+                  __uint_as_float(dq.y & 0xffff0000u)};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[e] = any ? x[e] : 0.f;  // a token that takes no part may hold anything
+      float s = -f[PW - 1] * x[e];
+#pragma unroll
+      for (int j = 0; j < E; ++j) {
+        s += f[j] * wv[e][j];
+        dw[e][j] += f[j] * x[e];
+      }
+      o[e] += s;
+    }
+    *reinterpret_cast<uint2*>(dX_out + t * NC + c0) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
+  }
+  float* p = part + ((int64_t)blockIdx.y * NC + c0) * Er;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (j < Er) p[e * Er + j] = dw[e][j];
+}
+
+__global__ __launch_bounds__(256) void split_sum_kernel(const float* __restrict__ part, int64_t n, int splits,
+                                                        float* __restrict__ out) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  float s = 0.f;
+  for (int k = 0; k < splits; ++k) s += part[k * n + i];
+  out[i] = s;
+}
+
+// Token splits of the apply pass: enough workgroups for the device, 32 tokens at
+// least in each (a split writes its part of dw once).
+int64_t router_splits(int64_t T, int64_t NC) {
+  const int64_t blocks = (NC + 1023) / 1024;
+  int64_t s = (1024 + blocks - 1) / blocks;
+  const int64_t most = (T + 31) / 32;
+  if (s > most) s = most;
+  return s < 1 ? 1 : s;
+}
+
+inline int64_t al256(int64_t b) { return (b + 255) & ~(int64_t)255; }
+
+inline int64_t bal_blocks(int64_t S) { return (S + BAL_TOKENS - 1) / BAL_TOKENS; }
+
+template <int W>
+hipError_t balance_go(const float* score, const int32_t* idx, const uint8_t* mask, int64_t B, int64_t S, int N, int k,
+                      int m, float coef, float* loss, int32_t* count, int32_t* tokens, float* mean_p, void* ws,
+                      hipStream_t st) {
+  const int64_t nblk = bal_blocks(S), parts = B * nblk;
+  char* q = (char*)ws;
+  float* psum = (float*)q;
+  q += al256(parts * W * 4);
+  int32_t* cnt = (int32_t*)q;
+  q += al256(parts * W * 4);
+  int32_t* tok = (int32_t*)q;
+  if (parts > 0)
+    hipLaunchKernelGGL((balance_part_kernel<W>), dim3((unsigned)parts), dim3(256), 0, st, score, idx, mask, S, nblk,
+                       N - m, k, psum, cnt, tok);
+  hipLaunchKernelGGL((balance_finish_kernel<W>), dim3(1), dim3(256), 0, st, psum, cnt, tok, B, nblk, N, k, m, coef,
+                     loss, count, tokens, mean_p);
+  return hipGetLastError();
+}
+
+template <int E>
+void router_apply(const void* X, int64_t T, int64_t NC, int Er, int64_t splits, const float* w, const float* P,
+                  const void* dX_in, void* dX_out, float* part, hipStream_t st) {
+  const int64_t per = (T + splits - 1) / splits;
+  hipLaunchKernelGGL((router_apply_kernel<E>), dim3((unsigned)((NC + 1023) / 1024), (unsigned)splits), dim3(256), 0, st,
+                     (const bf16_t*)X, T, NC, Er, per, w, P, (const bf16_t*)dX_in, (bf16_t*)dX_out, part);
+}
+
+}  // namespace
+
+int64_t balance_ws_bytes(int64_t B, int64_t S, int N, int m) {
+  const int W = N <= 16 ? 16 : 64;
+  const int64_t parts = B * bal_blocks(S);
+  return 2 * al256(parts * W * 4) + al256(parts * 4);
+}
+
+hipError_t launch_balance(const float* score, const int32_t* idx, const uint8_t* mask, int64_t B, int64_t S, int N,
+                          int k, int m, float coef, float* loss, int32_t* count, int32_t* tokens, float* mean_p,
+                          void* ws, hipStream_t st) {
+  return N <= 16 ? balance_go<16>(score, idx, mask, B, S, N, k, m, coef, loss, count, tokens, mean_p, ws, st)
+                 : balance_go<64>(score, idx, mask, B, S, N, k, m, coef, loss, count, tokens, mean_p, ws, st);
+}
+
+hipError_t launch_balance_backward(const float* score, const int32_t* count, const int32_t* tokens,
+                                   const uint8_t* mask, int64_t B, int64_t S, int N, int k, int m, float coef,
+                                   const float* dloss, float* dscore, hipStream_t st) {
+  const int W = N <= 16 ? 16 : 64;
+  const dim3 g((unsigned)((B * S * W + 255) / 256)), b(256);
+  if (W == 16)
+    hipLaunchKernelGGL((balance_backward_kernel<16>), g, b, 0, st, score, count, tokens, mask, B, S, N, k, m, coef,
+                       dloss, dscore);
+  else
+    hipLaunchKernelGGL((balance_backward_kernel<64>), g, b, 0, st, score, count, tokens, mask, B, S, N, k, m, coef,
+                       dloss, dscore);
+  return hipGetLastError();
+}
+
+int64_t router_backward_ws_bytes(int64_t T, int N, int64_t C, int m) {
+  if (T == 0) return 0;
+  const int64_t NC = (int64_t)N * C;
+  return al256(T * PW * 4) + al256(router_splits(T, NC) * NC * (N - m) * 4);
+}
+
+hipError_t launch_router_backward(const void* X, int64_t T, int N, int64_t C, int m, const float* w,
+                                  const float* score, const float* dscore, const void* dX_in, void* dX_out, float* dw,
+                                  void* ws, hipStream_t st) {
+  const int64_t NC = (int64_t)N * C, splits = router_splits(T, NC);
+  const int E = N - m;
+  float* P = (float*)ws;
+  float* part = (float*)((char*)ws + al256(T * PW * 4));
+  const int64_t n = NC * E;
+  if (T == 0) {
+    hipLaunchKernelGGL(split_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, n, 0, dw);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(router_factors_kernel, dim3((unsigned)T), dim3(256), 0, st, (const bf16_t*)X, NC, E, score,
+                     dscore, P);
+  if (E <= 4) router_apply<4>(X, T, NC, E, splits, w, P, dX_in, dX_out, part, st);
+  else if (E <= 8) router_apply<8>(X, T, NC, E, splits, w, P, dX_in, dX_out, part, st);
+  else if (E <= 12) router_apply<12>(X, T, NC, E, splits, w, P, dX_in, dX_out, part, st);
+  else router_apply<15>(X, T, NC, E, splits, w, P, dX_in, dX_out, part, st);
+  hipLaunchKernelGGL(split_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, n, (int)splits, dw);
+  return hipGetLastError();
+}
+
+}  // namespace hc
