@@ -667,7 +667,8 @@ int hc_rms_norm_backward(const void* s, int dtype, int64_t T, int64_t C, const f
  * nothing); arrays aligned to their element size; workspace
  * hc_gated_scan_workspace_bytes(B, S, C) bytes (may be NULL when that is 0), 256-byte
  * aligned. Outputs overlap no input (but as stated), other output or workspace
- * (HC_ERR_ALIAS). B * max(S, 64) * C at most 2^39 (else HC_ERR_SHAPE).
+ * (HC_ERR_ALIAS). B * ceil(max(S, 64) / 64) * ceil(C / 128) < 2^23
+ * (else HC_ERR_SHAPE).
  */
 int64_t hc_gated_scan_workspace_bytes(int64_t B, int64_t S, int64_t C);
 int hc_gated_scan(const void* x, const void* gate, int dtype, int64_t B, int64_t S, int64_t C, const float* h0,

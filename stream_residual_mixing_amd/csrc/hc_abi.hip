@@ -1508,7 +1508,9 @@ int hc_rms_norm_backward(const void* s, int dtype, int64_t T, int64_t C, const f
 static int check_scan_shape(int dtype, int64_t B, int64_t S, int64_t C) {
   if (!dtype_ok(dtype)) return HC_ERR_DTYPE;
   if (B < 0 || S < 0 || C < 1 || C > (1ll << 26) || B > (1ll << 31) || S > (1ll << 40)) return HC_ERR_SHAPE;
-  if ((double)B * (double)(S > 64 ? S : 64) * (double)C > 549755813888.0) return HC_ERR_SHAPE;  // grid size
+  // the grid: tiles of at least 64 tokens and 128 channels
+  const int64_t per = ((S > 64 ? S + 63 : 64) / 64) * ((C + 127) / 128);
+  if (per >= (1ll << 23) || B * per >= (1ll << 23)) return HC_ERR_SHAPE;
   return HC_OK;
 }
 
@@ -1517,14 +1519,14 @@ int64_t hc_gated_scan_workspace_bytes(int64_t B, int64_t S, int64_t C) {
   return B == 0 ? 0 : hc::scan_ws_bytes(B, S, C);
 }
 
-// four channels of a row in one aligned access, and the states' rows too
+// two channels of a row in one aligned access, and of the states' rows too
 static bool scan_vec(int64_t C, int dtype, std::initializer_list<const void*> streams,
                      std::initializer_list<const void*> states) {
-  if (C % 4 != 0) return false;
+  if (C % 2 != 0) return false;
   for (const void* p : streams)
-    if (p && !aligned_to(p, 4 * esize(dtype))) return false;
+    if (p && !aligned_to(p, 2 * esize(dtype))) return false;
   for (const void* p : states)
-    if (p && !aligned_to(p, 16)) return false;
+    if (p && !aligned_to(p, 8)) return false;
   return true;
 }
 

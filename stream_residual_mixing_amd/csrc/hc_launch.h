@@ -91,8 +91,8 @@ hipError_t launch_rms_norm_backward(int dtype, bool vec, const NormBwdArgs& a, f
 
 // ---- gated linear recurrence (hc_scan.hip)
 // Forward: y, last from x, gate, h0. Backward (bwd): dx, dgate, dh0 from x, gate, y,
-// dy, h0, dh_last. vec: C % 4 == 0 with the stream arrays aligned to 4 elements and
-// the state arrays and workspace to 16 bytes.
+// dy, h0, dh_last. vec: C even, the stream arrays aligned to 2 elements and the state
+// arrays to 8 bytes.
 struct ScanArgs {
   const void* x;
   const void* gate;

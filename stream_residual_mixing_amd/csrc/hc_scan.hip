@@ -4,10 +4,17 @@
 // Backward, with R_t the gradient that reaches h_t from later tokens (R = dh_last
 // behind the last token): dh_t = dy_t + R_t, R_{t-1} = a_t dh_t, dx_t = u_t dh_t,
 // dgate_t = dh_t (h_{t-1} - x_t (tied) or h_{t-1}) a_t (1 - a_t), dh0 = R before token 0.
-// Both directions walk an affine map per token and channel, s -> a s + b; maps
-// compose, so the sequence is cut into chunks: each chunk's composed map, a walk
-// over the chunks for each chunk's first state, and a second walk inside the
-// chunks that writes the outputs.
+// Both directions walk an affine map per token and channel, s -> a s + b (the
+// backward with b = a dy, from the last token). Maps compose, so a long sequence is
+// cut along time and the pieces' composed maps (A, H): s -> A s + H are joined.
+//
+// Two forms. Up to SHORT tokens one thread walks the whole sequence of its channels.
+// Longer ones run in one pass over the data: a workgroup holds a tile of tokens in
+// registers, publishes the tile's composed map, composes the maps of the tiles
+// before it while they are published (or takes a finished state, published as a
+// constant map, where one is there), and walks its tokens again from registers.
+// Tiles are taken from a counter in walk order, so that every tile waited for
+// belongs to a workgroup that already runs and waits for earlier tiles only.
 #include "hc_device.h"
 #include "hc_launch.h"
 
@@ -15,74 +22,82 @@ namespace hc {
 
 namespace {
 
-constexpr int CHUNK = 64;  // tokens of one thread's walk
+constexpr int V = 2;          // channels of one thread: 128 of a wave, one full access a row
+constexpr int WAVES = 8;      // waves of a tile, one after another in time
+constexpr int TILE_C = 64 * V;
+constexpr int SHORT = 32;
 
-constexpr int V = 4;       // channels of one thread
+// Tokens of one wave's walk in registers: fewer where each takes more of them.
+template <typename T, bool BWD>
+struct Tile {
+  static constexpr int LW = BWD ? 8 : 16;
+  static constexpr int TOKENS = LW * WAVES;
+};
 
-// V consecutive channels of one row. VEC: C is a multiple of V and every row is
-// aligned to V elements. Otherwise four channels are still one access where the row
-// has them (global memory takes any element-aligned address); `cnt` of them at its end.
-template <bool VEC>
-__device__ __forceinline__ void ld4(const float* p, int cnt, float v[V]) {
+// V channels of a row as stored. VEC: C is even and every row is aligned to two
+// elements. Otherwise two channels are still one access where the row has them
+// (global memory takes any element-aligned address).
+template <typename T> struct Pair;
+template <> struct Pair<float> {
+  typedef float2 raw;
+  static __device__ __forceinline__ void open(raw q, float v[V]) { v[0] = q.x; v[1] = q.y; }
+  static __device__ __forceinline__ raw close(const float v[V]) { return make_float2(v[0], v[1]); }
+  static __device__ __forceinline__ raw one(float e) { return make_float2(e, 0.f); }
+};
+template <> struct Pair<bf16_t> {
+  typedef uint32_t raw;
+  static __device__ __forceinline__ void open(raw q, float v[V]) {
+    v[0] = __uint_as_float(q << 16);
+    v[1] = __uint_as_float(q & 0xffff0000u);
+  }
+  static __device__ __forceinline__ raw close(const float v[V]) { return pack_bf2_hw(v[0], v[1]); }
+  static __device__ __forceinline__ raw one(bf16_t e) { return e; }
+};
+
+template <bool VEC, typename T>
+__device__ __forceinline__ typename Pair<T>::raw ld2(const T* p, int cnt) {
+  typename Pair<T>::raw q;
   if (VEC) {
-    const float4 q = *reinterpret_cast<const float4*>(p);
-    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-  } else if (cnt == V) {
-    __builtin_memcpy(v, p, 16);
+    q = *reinterpret_cast<const typename Pair<T>::raw*>(p);
+  } else if (cnt >= V) {
+    __builtin_memcpy(&q, p, sizeof(q));
   } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = e < cnt ? p[e] : 0.f;
+    q = Pair<T>::one(p[0]);
+  }
+  return q;
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void st2(T* p, int cnt, const float v[V]) {
+  const typename Pair<T>::raw q = Pair<T>::close(v);
+  if (VEC) {
+    *reinterpret_cast<typename Pair<T>::raw*>(p) = q;
+  } else if (cnt >= V) {
+    __builtin_memcpy(p, &q, sizeof(q));
+  } else {
+    __builtin_memcpy(p, &q, sizeof(T));
   }
 }
 
 template <bool VEC>
-__device__ __forceinline__ void ld4(const bf16_t* p, int cnt, float v[V]) {
-  uint2 q;
-  if (VEC) {
-    q = *reinterpret_cast<const uint2*>(p);
-  } else if (cnt == V) {
-    __builtin_memcpy(&q, p, 8);
-  } else {
-    q.x = (uint32_t)p[0] | (cnt > 1 ? (uint32_t)p[1] << 16 : 0u);
-    q.y = cnt > 2 ? (uint32_t)p[2] : 0u;
-  }
-  v[0] = bf2f(q.x & 0xffffu); v[1] = __uint_as_float(q.x & 0xffff0000u);
-  v[2] = bf2f(q.y & 0xffffu); v[3] = __uint_as_float(q.y & 0xffff0000u);
+__device__ __forceinline__ void ld2f(const float* p, int cnt, float v[V]) {
+  Pair<float>::open(ld2<VEC>(p, cnt), v);
 }
 
-template <bool VEC>
-__device__ __forceinline__ void st4(float* p, int cnt, const float v[V]) {
-  if (VEC) {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  } else if (cnt == V) {
-    __builtin_memcpy(p, v, 16);
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (e < cnt) p[e] = v[e];
-  }
+// a = sigmoid(g), u = 1 - a. The smaller of the two is q = e / (1 + e) with e =
+// exp(-|g|), free of cancellation; the larger is 1 - q, which rounds once (from the
+// reciprocal itself a would carry its error through every token of a long memory).
+// q is kept with the sign of g: one register per token for both.
+__device__ __forceinline__ float gate_q(float g) {
+  const float e = __builtin_amdgcn_exp2f(-1.44269504f * fabsf(g));
+  return copysignf(e * __builtin_amdgcn_rcpf(1.f + e), g);
 }
 
-template <bool VEC>
-__device__ __forceinline__ void st4(bf16_t* p, int cnt, const float v[V]) {
-  const uint2 q = make_uint2(pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3]));
-  if (VEC) {
-    *reinterpret_cast<uint2*>(p) = q;
-  } else if (cnt == V) {
-    __builtin_memcpy(p, &q, 8);
-  } else {
-    p[0] = (bf16_t)q.x;
-    if (cnt > 1) p[1] = (bf16_t)(q.x >> 16);
-    if (cnt > 2) p[2] = (bf16_t)q.y;
-  }
-}
-
-// a = sigmoid(g) and u = 1 - a, each from exp(-|g|) so that neither cancels.
-__device__ __forceinline__ void gates(float g, float& a, float& u) {
-  const float e = __expf(-fabsf(g));
-  const float s = __builtin_amdgcn_rcpf(1.f + e);
-  a = g >= 0.f ? s : e * s;
-  u = g >= 0.f ? e * s : s;
+__device__ __forceinline__ void gate_au(float q, float& a, float& u) {
+  const float lo = fabsf(q), hi = 1.f - lo;
+  const bool neg = (int)__float_as_uint(q) < 0;
+  a = neg ? lo : hi;
+  u = neg ? hi : lo;
 }
 
 __device__ __forceinline__ int64_t seq_len(const int32_t* lengths, int64_t b, int64_t S) {
@@ -91,155 +106,301 @@ __device__ __forceinline__ int64_t seq_len(const int32_t* lengths, int64_t b, in
   return n < 0 ? 0 : (n > S ? S : n);
 }
 
-// Thread -> (sequence, chunk, V channels); tokens t0 .. t1 - 1.
-struct Place {
-  int64_t b, j, c, t0, t1;
-  int cnt;
-};
+// The backward's outputs of one token from the state s (R_t), which becomes R_{t-1}.
+__device__ __forceinline__ void back_step(bool tied, float a, float u, float dy, float x, float hp, float& s,
+                                          float& dx, float& dg) {
+  const float dh = dy + s;
+  dx = tied ? u * dh : dh;
+  dg = dh * (tied ? hp - x : hp) * (a * u);
+  s = a * dh;
+}
 
-__device__ __forceinline__ bool place(const ScanArgs& a, int64_t nchunk, Place& p) {
+// ------------------------------------------------ short sequences: one walk
+
+template <typename T, bool VEC, bool BWD>
+__global__ __launch_bounds__(256) void scan_short_kernel(ScanArgs a) {
   const int64_t ncg = (a.C + V - 1) / V;
   const int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (g >= a.B * nchunk * ncg) return false;
-  p.c = (g % ncg) * V;
-  p.cnt = (int)(a.C - p.c < V ? a.C - p.c : V);
-  const int64_t r = g / ncg;
-  p.j = r % nchunk;
-  p.b = r / nchunk;
-  const int64_t len = seq_len(a.lengths, p.b, a.S);
-  p.t0 = p.j * CHUNK < len ? p.j * CHUNK : len;
-  p.t1 = (p.j + 1) * CHUNK < len ? (p.j + 1) * CHUNK : len;
-  return true;
-}
-
-// The composed map of one chunk, (A, H): s -> A s + H, at ws[(b, j)][2][C].
-template <typename T, bool VEC, bool BWD>
-__global__ __launch_bounds__(256) void scan_chunk_kernel(ScanArgs a, int64_t nchunk) {
-  Place p;
-  if (!place(a, nchunk, p)) return;
-  float A[V], H[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) { A[e] = 1.f; H[e] = 0.f; }
-  const int64_t n = p.t1 - p.t0;
-#pragma unroll 8
-  for (int64_t i = 0; i < n; ++i) {
-    const int64_t t = BWD ? p.t1 - 1 - i : p.t0 + i;
-    const int64_t at = (p.b * a.S + t) * a.C + p.c;
-    float g[V], x[V];
-    ld4<VEC>((const T*)a.gate + at, p.cnt, g);
-    ld4<VEC>((const T*)(BWD ? a.dy : a.x) + at, p.cnt, x);
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      float d, u;
-      gates(g[e], d, u);
-      H[e] = BWD ? d * (H[e] + x[e]) : d * H[e] + (a.tied ? u * x[e] : x[e]);
-      A[e] *= d;
-    }
-  }
-  float* w = (float*)a.ws + (p.b * nchunk + p.j) * 2 * a.C + p.c;
-  st4<VEC>(w, p.cnt, A);
-  st4<VEC>(w + a.C, p.cnt, H);
-}
-
-// The state before each chunk, in place of the chunk's A.
-template <bool BWD>
-__global__ __launch_bounds__(64) void scan_carry_kernel(ScanArgs a, int64_t nchunk) {
-  const int64_t g = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (g >= a.B * a.C) return;
-  const int64_t b = g / a.C, c = g - b * a.C;
+  if (g >= a.B * ncg) return;
+  const int64_t b = g / ncg, c = (g - b * ncg) * V;
+  const int cnt = (int)(a.C - c < V ? a.C - c : V);
+  const int64_t len = seq_len(a.lengths, b, a.S);
   const float* first = BWD ? a.dlast : a.state0;
-  float s = first ? first[g] : 0.f;
-  float* w = (float*)a.ws + b * nchunk * 2 * a.C + c;
-#pragma unroll 8
-  for (int64_t i = 0; i < nchunk; ++i) {
-    float* q = w + (BWD ? nchunk - 1 - i : i) * 2 * a.C;
-    const float A = q[0], H = q[a.C];
-    q[0] = s;
-    s = A * s + H;
-  }
-}
-
-// The walk inside each chunk from its first state; with one chunk the state comes
-// from and goes to the caller's arrays.
-template <typename T, bool VEC, bool BWD>
-__global__ __launch_bounds__(256) void scan_apply_kernel(ScanArgs a, int64_t nchunk) {
-  Place p;
-  if (!place(a, nchunk, p)) return;
-  float s[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) s[e] = 0.f;
-  if (nchunk > 1) {
-    ld4<VEC>((const float*)a.ws + (p.b * nchunk + p.j) * 2 * a.C + p.c, p.cnt, s);
-  } else {
-    const float* first = BWD ? a.dlast : a.state0;
-    if (first) ld4<VEC>(first + p.b * a.C + p.c, p.cnt, s);
-  }
-  const int64_t n = p.t1 - p.t0;
+  float s[V] = {0.f, 0.f};
+  if (first) ld2f<VEC>(first + b * a.C + c, cnt, s);
+  const int64_t row0 = b * a.S * a.C + c;
 #pragma unroll 4
-  for (int64_t i = 0; i < n; ++i) {
-    const int64_t t = BWD ? p.t1 - 1 - i : p.t0 + i;
-    const int64_t at = (p.b * a.S + t) * a.C + p.c;
-    float g[V], x[V];
-    ld4<VEC>((const T*)a.gate + at, p.cnt, g);
-    ld4<VEC>((const T*)a.x + at, p.cnt, x);
+  for (int64_t i = 0; i < len; ++i) {
+    const int64_t t = BWD ? len - 1 - i : i;
+    const int64_t at = row0 + t * a.C;
+    float gv[V], x[V], d[V], u[V];
+    Pair<T>::open(ld2<VEC>((const T*)a.gate + at, cnt), gv);
+    Pair<T>::open(ld2<VEC>((const T*)a.x + at, cnt), x);
+#pragma unroll
+    for (int e = 0; e < V; ++e) gate_au(gate_q(gv[e]), d[e], u[e]);
     if (!BWD) {
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float d, u;
-        gates(g[e], d, u);
-        s[e] = d * s[e] + (a.tied ? u * x[e] : x[e]);
-      }
-      st4<VEC>((T*)a.y + at, p.cnt, s);
+      for (int e = 0; e < V; ++e) s[e] = d[e] * s[e] + (a.tied ? u[e] * x[e] : x[e]);
+      st2<VEC>((T*)a.y + at, cnt, s);
     } else {
-      float dy[V], hp[V], dx[V], dg[V];
-      ld4<VEC>((const T*)a.dy + at, p.cnt, dy);
-      if (t > 0) {
-        ld4<VEC>((const T*)a.y_in + at - a.C, p.cnt, hp);
-      } else if (a.state0) {
-        ld4<VEC>(a.state0 + p.b * a.C + p.c, p.cnt, hp);
-      } else {
+      float dy[V], hp[V] = {0.f, 0.f}, dx[V], dg[V];
+      Pair<T>::open(ld2<VEC>((const T*)a.dy + at, cnt), dy);
+      if (t > 0) Pair<T>::open(ld2<VEC>((const T*)a.y_in + at - a.C, cnt), hp);
+      else if (a.state0) ld2f<VEC>(a.state0 + b * a.C + c, cnt, hp);
 #pragma unroll
-        for (int e = 0; e < V; ++e) hp[e] = 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float d, u;
-        gates(g[e], d, u);
-        const float dh = dy[e] + s[e];
-        dx[e] = a.tied ? u * dh : dh;
-        dg[e] = dh * (a.tied ? hp[e] - x[e] : hp[e]) * (d * u);
-        s[e] = d * dh;
-      }
-      st4<VEC>((T*)a.y + at, p.cnt, dx);
-      st4<VEC>((T*)a.dgate + at, p.cnt, dg);
+      for (int e = 0; e < V; ++e) back_step(a.tied, d[e], u[e], dy[e], x[e], hp[e], s[e], dx[e], dg[e]);
+      st2<VEC>((T*)a.y + at, cnt, dx);
+      st2<VEC>((T*)a.dgate + at, cnt, dg);
     }
   }
   if (BWD) {  // padding receives no gradient
-    const int64_t end = (p.j + 1) * CHUNK < a.S ? (p.j + 1) * CHUNK : a.S;
-    const float zero[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t t = p.t1 > p.j * CHUNK ? p.t1 : p.j * CHUNK; t < end; ++t) {
-      const int64_t at = (p.b * a.S + t) * a.C + p.c;
-      st4<VEC>((T*)a.y + at, p.cnt, zero);
-      st4<VEC>((T*)a.dgate + at, p.cnt, zero);
+    const float zero[V] = {0.f, 0.f};
+    for (int64_t t = len; t < a.S; ++t) {
+      st2<VEC>((T*)a.y + row0 + t * a.C, cnt, zero);
+      st2<VEC>((T*)a.dgate + row0 + t * a.C, cnt, zero);
     }
   }
-  // the last chunk's walk ends in the state that goes on, the same value as its last y
-  if (p.j == (BWD ? 0 : nchunk - 1) && a.state1) st4<VEC>(a.state1 + p.b * a.C + p.c, p.cnt, s);
+  if (a.state1) st2<VEC>(a.state1 + b * a.C + c, cnt, s);
 }
 
-// at least one, whose walk also passes the state on when there is no token
-int64_t chunks_of(int64_t S) { return S > CHUNK ? (S + CHUNK - 1) / CHUNK : 1; }
+// ---------------------------------------------- long sequences: joined tiles
+
+// A published map is one 64-bit word per channel, so no word is ever seen half
+// written: A in the low half, H in the high half. All ones: not there yet (a value
+// of that pattern, a NaN, is published as another NaN). A = -0: a constant map, the
+// finished state behind the tile (a is never negative, so no composed map has it).
+constexpr uint32_t DONE = 0x80000000u;
+constexpr uint64_t ABSENT = ~0ull;
+
+__device__ __forceinline__ uint64_t word_of(uint32_t A, float H) {
+  uint32_t h = __float_as_uint(H);
+  if (h == 0xffffffffu) h = 0x7fc00000u;
+  if (A == 0xffffffffu) A = 0x7fc00000u;
+  return (uint64_t)h << 32 | A;
+}
+
+__device__ __forceinline__ void publish(uint64_t* p, uint64_t w) {
+  __hip_atomic_store(p, w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ uint64_t peek(const uint64_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// Waits for a word. The tile waited for is running (see the counter), so the wait
+// ends; the bound turns a broken workspace into NaN outputs instead of a hang.
+constexpr int MOST_POLLS = 1 << 22;
+
+__device__ __forceinline__ uint64_t await(const uint64_t* p) {
+  uint64_t w = peek(p);
+  for (int i = 0; w == ABSENT && i < MOST_POLLS; ++i) {
+    __builtin_amdgcn_s_sleep(1);
+    w = peek(p);
+  }
+  return w;
+}
+
+// The words of all tiles absent, the counter zero.
+__global__ __launch_bounds__(256) void scan_clear_kernel(uint4* ws, int64_t n16) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n16) return;
+  const uint32_t v = i < 16 ? 0u : 0xffffffffu;  // 256 bytes of counter, then the words
+  ws[i] = make_uint4(v, v, v, v);
+}
+
+template <typename T, bool VEC, bool BWD>
+__global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, int64_t ntile, int64_t nct) {
+  constexpr int LW = Tile<T, BWD>::LW, TOKENS = Tile<T, BWD>::TOKENS;
+  typedef typename Pair<T>::raw raw;
+  __shared__ float sA[WAVES][TILE_C], sH[WAVES][TILE_C];   // the waves' maps
+  __shared__ float lA[WAVES][TILE_C], lH[WAVES][TILE_C];   // earlier tiles' maps
+  __shared__ unsigned ticket;
+  // what the whole wave shares is kept in scalar registers: every row is then one scalar
+  // base and a 32-bit lane offset
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (threadIdx.x == 0) ticket = atomicAdd((unsigned*)a.ws, 1u);
+  __syncthreads();
+  // walk order: every sequence's and channel tile's j-th tile before any (j+1)-th
+  const uint32_t tk = __builtin_amdgcn_readfirstlane(ticket);
+  const uint32_t ct = tk % (uint32_t)nct, r = tk / (uint32_t)nct, b = r % (uint32_t)a.B, j = r / (uint32_t)a.B;
+  const int64_t c0 = (int64_t)ct * TILE_C;
+  const bool in = lane * V < a.C - c0;
+  const uint32_t lo = in ? lane * V : 0;  // lanes past the row read its tile's first channels and store nothing
+  const int cnt = (int)min((int64_t)V, a.C - c0 - lo);
+  const int64_t len = seq_len(a.lengths, b, a.S);
+  const int64_t seq0 = b * a.S * a.C + c0, st0 = b * a.C + c0;
+  const int64_t i0 = (int64_t)j * TOKENS + wv * LW;  // this wave's first step of the walk
+  const bool tied = a.tied;
+
+  // token of step k, and the row that is read for it (a real one for every step)
+#define HC_TOKEN(k) (BWD ? a.S - 1 - (i0 + (k)) : i0 + (k))
+  raw rg[LW], rx[LW], rd[BWD ? LW : 1], ry[BWD ? LW : 1];
+#pragma unroll
+  for (int k = 0; k < LW; ++k) {
+    int64_t t = HC_TOKEN(k);
+    t = t < 0 ? 0 : (t >= a.S ? a.S - 1 : t);
+    const int64_t at = seq0 + t * a.C;
+    rg[k] = ld2<VEC>((const T*)a.gate + at + lo, cnt);
+    rx[k] = ld2<VEC>((const T*)a.x + at + lo, cnt);
+    if (BWD) {
+      rd[k] = ld2<VEC>((const T*)a.dy + at + lo, cnt);
+      ry[k] = ld2<VEC>((const T*)a.y_in + (at - (t > 0 ? a.C : 0)) + lo, cnt);
+    }
+  }
+
+  // this wave's composed map; the forward keeps a and b, the backward the signed q
+  float ka[LW][V], kb[BWD ? 1 : LW][V];
+  float A[V] = {1.f, 1.f}, H[V] = {0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < LW; ++k) {
+    const int64_t t = HC_TOKEN(k);
+    const bool live = t >= 0 && t < len;
+    float g[V], x[V];
+    Pair<T>::open(rg[k], g);
+    Pair<T>::open(BWD ? rd[BWD ? k : 0] : rx[k], x);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float q = gate_q(g[e]);
+      float d, u;
+      gate_au(q, d, u);
+      float bb = BWD ? d * x[e] : (tied ? u * x[e] : x[e]);
+      d = live ? d : 1.f;
+      bb = live ? bb : 0.f;
+      H[e] = d * H[e] + bb;
+      A[e] *= d;
+      ka[k][e] = BWD ? q : d;
+      if (!BWD) kb[BWD ? 0 : k][e] = bb;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    sA[wv][lane * V + e] = A[e];
+    sH[wv][lane * V + e] = H[e];
+  }
+  __syncthreads();
+  // the waves before this one (pA, pH), and the whole tile's map
+  float pA[V] = {1.f, 1.f}, pH[V] = {0.f, 0.f}, tA[V] = {1.f, 1.f}, tH[V] = {0.f, 0.f};
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w)
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      if (w == wv) {
+        pA[e] = tA[e];
+        pH[e] = tH[e];
+      }
+      const float wa = sA[w][lane * V + e];
+      tH[e] = wa * tH[e] + sH[w][lane * V + e];
+      tA[e] *= wa;
+    }
+
+  uint64_t* words = (uint64_t*)((char*)a.ws + 256) + (b * nct + ct) * TILE_C + lane * V;  // one per lane channel, inside the row or not
+  const int64_t wstep = a.B * nct * TILE_C;  // from one tile of the walk to the next
+  if (wv == WAVES - 1 && j > 0 && j + 1 < ntile)
+#pragma unroll
+    for (int e = 0; e < V; ++e) publish(words + (int64_t)j * wstep + e, word_of(__float_as_uint(tA[e]), tH[e]));
+
+  // the state before the tile: compose backwards until a constant map is met
+  float init[V] = {0.f, 0.f};
+  const float* first = BWD ? a.dlast : a.state0;
+  if (first) ld2f<VEC>(first + st0 + lo, cnt, init);
+  float s[V];
+  if (j == 0) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) s[e] = init[e];
+  } else {
+    float bA[V] = {1.f, 1.f}, bH[V] = {0.f, 0.f};
+    bool done[V] = {false, false};
+    for (int64_t p0 = (int64_t)j - 1;; p0 -= WAVES) {
+      const int64_t p = p0 - wv;  // each wave fetches one of the next WAVES tiles
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        uint32_t wa = DONE;
+        float wh = init[e];
+        if (p >= 0) {
+          const uint64_t w = await(words + p * wstep + e);
+          wa = (uint32_t)w;
+          wh = __uint_as_float((uint32_t)(w >> 32));
+        }
+        lA[wv][lane * V + e] = __uint_as_float(wa);
+        lH[wv][lane * V + e] = wh;
+      }
+      __syncthreads();
+      bool more = false;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+          const float wa = lA[w][lane * V + e], wh = lH[w][lane * V + e];
+          if (!done[e]) {
+            bH[e] += bA[e] * wh;
+            bA[e] *= wa;
+            done[e] = __float_as_uint(wa) == DONE;
+          }
+        }
+        more |= !done[e];
+      }
+      if (!__syncthreads_or(more)) break;  // also: all have read lA, lH
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) s[e] = bH[e];
+  }
+  if (wv == WAVES - 1 && j + 1 < ntile)
+#pragma unroll
+    for (int e = 0; e < V; ++e) publish(words + (int64_t)j * wstep + e, word_of(DONE, tA[e] * s[e] + tH[e]));
+
+  // the walk itself
+#pragma unroll
+  for (int e = 0; e < V; ++e) s[e] = pA[e] * s[e] + pH[e];
+#pragma unroll
+  for (int k = 0; k < LW; ++k) {
+    const int64_t t = HC_TOKEN(k);
+    const bool live = t >= 0 && t < len;
+    const int64_t at = seq0 + t * a.C;
+    if (!BWD) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[e] = ka[k][e] * s[e] + kb[BWD ? 0 : k][e];
+      if (live && in) st2<VEC>((T*)a.y + at + lo, cnt, s);
+    } else if (t >= 0 && t < a.S) {
+      float x[V], dy[V], hp[V], dx[V] = {0.f, 0.f}, dg[V] = {0.f, 0.f};
+      if (live) {
+        Pair<T>::open(rx[k], x);
+        Pair<T>::open(rd[BWD ? k : 0], dy);
+        Pair<T>::open(ry[BWD ? k : 0], hp);
+        if (t == 0) {
+          hp[0] = hp[1] = 0.f;
+          if (a.state0) ld2f<VEC>(a.state0 + st0 + lo, cnt, hp);
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          float d, u;
+          gate_au(ka[k][e], d, u);
+          back_step(tied, d, u, dy[e], x[e], hp[e], s[e], dx[e], dg[e]);
+        }
+      }
+      if (in) {  // padding receives no gradient
+        st2<VEC>((T*)a.y + at + lo, cnt, dx);
+        st2<VEC>((T*)a.dgate + at + lo, cnt, dg);
+      }
+    }
+  }
+  // the wave of the walk's last step ends in the state that goes on
+  if (a.state1 && in && i0 <= a.S - 1 && a.S - 1 < i0 + LW) st2<VEC>(a.state1 + st0 + lo, cnt, s);
+#undef HC_TOKEN
+}
 
 template <typename T, bool VEC, bool BWD>
 hipError_t scan_go(const ScanArgs& a, hipStream_t st) {
-  const int64_t nchunk = chunks_of(a.S);
-  const int64_t threads = a.B * nchunk * ((a.C + V - 1) / V);
-  const dim3 g((unsigned)((threads + 255) / 256)), b(256);
-  if (nchunk > 1) {
-    hipLaunchKernelGGL((scan_chunk_kernel<T, VEC, BWD>), g, b, 0, st, a, nchunk);
-    hipLaunchKernelGGL((scan_carry_kernel<BWD>), dim3((unsigned)((a.B * a.C + 63) / 64)), dim3(64), 0, st, a, nchunk);
+  if (a.S <= SHORT) {
+    const int64_t threads = a.B * ((a.C + V - 1) / V);
+    hipLaunchKernelGGL((scan_short_kernel<T, VEC, BWD>), dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st, a);
+    return hipGetLastError();
   }
-  hipLaunchKernelGGL((scan_apply_kernel<T, VEC, BWD>), g, b, 0, st, a, nchunk);
+  constexpr int TOKENS = Tile<T, BWD>::TOKENS;
+  const int64_t ntile = (a.S + TOKENS - 1) / TOKENS, nct = (a.C + TILE_C - 1) / TILE_C;
+  const int64_t n16 = 16 + (ntile > 1 ? ntile * a.B * nct * TILE_C / 2 : 0);
+  hipLaunchKernelGGL(scan_clear_kernel, dim3((unsigned)((n16 + 255) / 256)), dim3(256), 0, st, (uint4*)a.ws, n16);
+  hipLaunchKernelGGL((scan_tile_kernel<T, VEC, BWD>), dim3((unsigned)(ntile * a.B * nct)), dim3(64 * WAVES), 0, st, a,
+                     ntile, nct);
   return hipGetLastError();
 }
 
@@ -251,9 +412,12 @@ hipError_t scan_by_type(int dtype, bool vec, const ScanArgs& a, hipStream_t st) 
 
 }  // namespace
 
+// The counter and the words of the finest tiling (both directions and types).
 int64_t scan_ws_bytes(int64_t B, int64_t S, int64_t C) {
-  const int64_t n = chunks_of(S);
-  return n > 1 ? B * n * 2 * C * 4 : 0;
+  if (S <= SHORT) return 0;
+  constexpr int TOKENS = Tile<float, true>::TOKENS;
+  const int64_t ntile = (S + TOKENS - 1) / TOKENS, nct = (C + TILE_C - 1) / TILE_C;
+  return 256 + ntile * B * nct * TILE_C * 8;
 }
 
 hipError_t launch_scan(int dtype, bool bwd, bool vec, const ScanArgs& a, hipStream_t st) {
