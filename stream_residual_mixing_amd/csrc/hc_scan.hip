@@ -27,7 +27,8 @@ constexpr int WAVES = 8;      // waves of a tile, one after another in time
 constexpr int TILE_C = 64 * V;
 constexpr int SHORT = 32;
 
-// Tokens of one wave's walk in registers: fewer where each takes more of them.
+// Tokens of one wave's walk in registers: 16 forward (8: 73 against 57 us at 8,192 x
+// 4,096, twice the tiles to join), 8 backward, which keeps four values of each.
 template <typename T, bool BWD>
 struct Tile {
   static constexpr int LW = BWD ? 8 : 16;
@@ -42,6 +43,11 @@ template <> struct Pair<float> {
   typedef float2 raw;
   static __device__ __forceinline__ void open(raw q, float v[V]) { v[0] = q.x; v[1] = q.y; }
   static __device__ __forceinline__ raw close(const float v[V]) { return make_float2(v[0], v[1]); }
+  static __device__ __forceinline__ raw stream(const float* p) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    const f2 q = __builtin_nontemporal_load(reinterpret_cast<const f2*>(p));
+    return make_float2(q.x, q.y);
+  }
   static __device__ __forceinline__ raw one(float e) { return make_float2(e, 0.f); }
 };
 template <> struct Pair<bf16_t> {
@@ -51,13 +57,21 @@ template <> struct Pair<bf16_t> {
     v[1] = __uint_as_float(q & 0xffff0000u);
   }
   static __device__ __forceinline__ raw close(const float v[V]) { return pack_bf2_hw(v[0], v[1]); }
+  static __device__ __forceinline__ raw stream(const bf16_t* p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
+  }
   static __device__ __forceinline__ raw one(bf16_t e) { return e; }
 };
 
-template <bool VEC, typename T>
+// OLD: the backward's arrays were written long before and are not kept in the caches
+// (98 -> 94 us at 2 x 4096 x 4096); the forward's were just produced, and keeping them
+// costs nothing where they are not (22 -> 19.5 us where they fit).
+template <bool VEC, bool OLD = false, typename T>
 __device__ __forceinline__ typename Pair<T>::raw ld2(const T* p, int cnt) {
   typename Pair<T>::raw q;
-  if (VEC) {
+  if (VEC && OLD) {
+    q = Pair<T>::stream(p);
+  } else if (VEC) {
     q = *reinterpret_cast<const typename Pair<T>::raw*>(p);
   } else if (cnt >= V) {
     __builtin_memcpy(&q, p, sizeof(q));
@@ -208,6 +222,20 @@ __global__ __launch_bounds__(256) void scan_clear_kernel(uint4* ws, int64_t n16)
   ws[i] = make_uint4(v, v, v, v);
 }
 
+// A barrier that orders LDS alone: the rows that are on their way stay on their way.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+__device__ __forceinline__ void forget(float& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void forget(uint32_t& v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void forget(float2& v) {
+  forget(v.x);
+  forget(v.y);
+}
+
 template <typename T, bool VEC, bool BWD>
 __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, int64_t ntile, int64_t nct) {
   constexpr int LW = Tile<T, BWD>::LW, TOKENS = Tile<T, BWD>::TOKENS;
@@ -219,7 +247,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
   // base and a 32-bit lane offset
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (threadIdx.x == 0) ticket = atomicAdd((unsigned*)a.ws, 1u);
-  __syncthreads();
+  lds_barrier();
   // walk order: every sequence's and channel tile's j-th tile before any (j+1)-th
   const uint32_t tk = __builtin_amdgcn_readfirstlane(ticket);
   const uint32_t ct = tk % (uint32_t)nct, r = tk / (uint32_t)nct, b = r % (uint32_t)a.B, j = r / (uint32_t)a.B;
@@ -240,11 +268,11 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
     int64_t t = HC_TOKEN(k);
     t = t < 0 ? 0 : (t >= a.S ? a.S - 1 : t);
     const int64_t at = seq0 + t * a.C;
-    rg[k] = ld2<VEC>((const T*)a.gate + at + lo, cnt);
-    rx[k] = ld2<VEC>((const T*)a.x + at + lo, cnt);
+    rg[k] = ld2<VEC, BWD>((const T*)a.gate + at + lo, cnt);
+    rx[k] = ld2<VEC, BWD>((const T*)a.x + at + lo, cnt);
     if (BWD) {
-      rd[k] = ld2<VEC>((const T*)a.dy + at + lo, cnt);
-      ry[k] = ld2<VEC>((const T*)a.y_in + (at - (t > 0 ? a.C : 0)) + lo, cnt);
+      rd[k] = ld2<VEC, BWD>((const T*)a.dy + at + lo, cnt);
+      ry[k] = ld2<VEC, BWD>((const T*)a.y_in + (at - (t > 0 ? a.C : 0)) + lo, cnt);
     }
   }
 
@@ -277,10 +305,10 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
     sA[wv][lane * V + e] = A[e];
     sH[wv][lane * V + e] = H[e];
   }
-  __syncthreads();
+  lds_barrier();
   // the waves before this one (pA, pH), and the whole tile's map
   float pA[V] = {1.f, 1.f}, pH[V] = {0.f, 0.f}, tA[V] = {1.f, 1.f}, tH[V] = {0.f, 0.f};
-#pragma unroll
+#pragma unroll BWD ? 2 : WAVES
   for (int w = 0; w < WAVES; ++w)
 #pragma unroll
     for (int e = 0; e < V; ++e) {
@@ -324,11 +352,11 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
         lA[wv][lane * V + e] = __uint_as_float(wa);
         lH[wv][lane * V + e] = wh;
       }
-      __syncthreads();
+      lds_barrier();
       bool more = false;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-#pragma unroll
+#pragma unroll BWD ? 2 : WAVES
         for (int w = 0; w < WAVES; ++w) {
           const float wa = lA[w][lane * V + e], wh = lH[w][lane * V + e];
           if (!done[e]) {
@@ -339,7 +367,8 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
         }
         more |= !done[e];
       }
-      if (!__syncthreads_or(more)) break;  // also: all have read lA, lH
+      if (!__any(more)) break;  // the same in every wave: all compose the same maps
+      lds_barrier();            // lA, lH are read
     }
 #pragma unroll
     for (int e = 0; e < V; ++e) s[e] = bH[e];
@@ -347,6 +376,17 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
   if (wv == WAVES - 1 && j + 1 < ntile)
 #pragma unroll
     for (int e = 0; e < V; ++e) publish(words + (int64_t)j * wstep + e, word_of(DONE, tA[e] * s[e] + tH[e]));
+
+  // The backward's walk opens q and the rows again: without this the compiler keeps what
+  // it made of them, four registers for one.
+  if (BWD)
+#pragma unroll
+    for (int k = 0; k < LW; ++k) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) forget(ka[k][e]);
+      forget(rx[k]);
+      forget(rd[BWD ? k : 0]);
+    }
 
   // the walk itself
 #pragma unroll
