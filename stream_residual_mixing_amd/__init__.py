@@ -147,9 +147,15 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# The current stream's handle without building a Stream object (2 us of every call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device, stream):
     if stream is not None:
         return ctypes.c_void_p(int(stream))
+    if _raw_stream is not None and device.index is not None:
+        return ctypes.c_void_p(_raw_stream(device.index))
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
@@ -157,7 +163,7 @@ def _dev_tensor(t, name, dtypes=None, shape=None, device=None):
     """t checked before any launch: a contiguous tensor on a HIP device (the given
     one if any), of one of `dtypes` and exactly `shape`. The C ABI takes raw
     pointers, so a wrong size would reach the kernels; here it raises instead."""
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a tensor on a HIP device")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
@@ -165,7 +171,7 @@ def _dev_tensor(t, name, dtypes=None, shape=None, device=None):
         raise ValueError(f"{name} must be contiguous")
     if dtypes is not None and t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {tuple(dtypes)}")
-    if shape is not None and tuple(t.shape) != tuple(int(v) for v in shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(int(v) for v in shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(int(v) for v in shape)}")
     return t
 
