@@ -1095,10 +1095,11 @@ def xhc_balance_loss(score, idx, B, S, *, m=2, coef=1.0, mask=None, out=None, wo
         else:
             loss, count = _f32(out[0], "loss out", (), dev), _i32(out[1], "count out", (B, N), dev)
             tokens, mean_p = _i32(out[2], "tokens out", (B,), dev), _f32(out[3], "mean_p out", (B, E), dev)
-        ws = _workspace(xhc_balance_loss_workspace_bytes(B, S, N, m), dev, workspace)
+        nbytes = xhc_balance_loss_workspace_bytes(B, S, N, m)
+        ws = None if nbytes == 0 else _workspace(nbytes, dev, workspace)
         _check("xhc_balance_loss", lib().xhc_balance_loss(
             _ptr(score), _ptr(idx), _ptr(mask), B, S, N, k, m, float(coef), _ptr(loss), _ptr(count), _ptr(tokens),
-            _ptr(mean_p), _ptr(ws), _nbytes(ws), _stream(dev, stream)))
+            _ptr(mean_p), _ptr(ws), 0 if ws is None else _nbytes(ws), _stream(dev, stream)))
     return dict(loss=loss, count=count, tokens=tokens, mean_p=mean_p)
 
 

@@ -18,87 +18,119 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return W == 16 ? row16_sum(v) : wave_sum(v);
 }
 
-constexpr int BAL_TOKENS = 256;  // tokens of one workgroup's part
+// Tokens of one workgroup's part, and the most that one workgroup takes alone: above,
+// the loads of more workgroups pay for a second launch.
+constexpr int BAL_TOKENS = 128, BAL_ALONE = 1024;
 
 __device__ __forceinline__ float share(float s, float total) { return total == 0.f ? 0.f : s / total; }
 
-// Per (sequence, 256 tokens): counts [W], sums of p [W] and the unmasked tokens.
+// Token `at` of a lane group: adds its share, its streams (LDS counts: integer sums do
+// not depend on their order) and itself.
+template <int W>
+__device__ __forceinline__ void balance_token(const float* __restrict__ score, const int32_t* __restrict__ idx,
+                                              const uint8_t* __restrict__ mask, int64_t at, int E, int k, int j,
+                                              int32_t* hist, float& p, int32_t& n) {
+  const bool live = !mask || mask[at];
+  float s = j < E ? score[at * E + j] : 0.f;
+  const int32_t i = j < k ? idx[at * k + j] : -1;
+  if (!live) s = 0.f;
+  p += share(s, lanes_sum<W>(s));
+  if (live) {
+    if (i >= 0 && i < W) atomicAdd(&hist[i], 1);
+    ++n;
+  }
+}
+
+// Per (sequence, BAL_TOKENS tokens): counts [W], sums of p [W] and the unmasked tokens.
 template <int W>
 __global__ __launch_bounds__(256) void balance_part_kernel(const float* __restrict__ score,
                                                            const int32_t* __restrict__ idx,
-                                                           const uint8_t* __restrict__ mask, int64_t S, int64_t nblk, int E,
-                                                           int k, float* __restrict__ psum, int32_t* __restrict__ cnt,
-                                                           int32_t* __restrict__ tok) {
+                                                           const uint8_t* __restrict__ mask, int64_t S, int64_t nblk,
+                                                           int E, int k, float* __restrict__ psum,
+                                                           int32_t* __restrict__ cnt, int32_t* __restrict__ tok) {
   constexpr int SLOTS = 256 / W;
   __shared__ float sp[SLOTS][W];
-  __shared__ int32_t sc[SLOTS][W], sn[SLOTS];
+  __shared__ int32_t sn[SLOTS], hist[W];
   const int j = threadIdx.x % W, slot = threadIdx.x / W;
   const int64_t part = blockIdx.x, b = part / nblk, t0 = (part - b * nblk) * BAL_TOKENS;
   const int64_t t1 = t0 + BAL_TOKENS < S ? t0 + BAL_TOKENS : S;
+  if (threadIdx.x < W) hist[threadIdx.x] = 0;
+  __syncthreads();
   float p = 0.f;
-  int32_t c = 0, n = 0;
-  for (int64_t t = t0 + slot; t < t1; t += SLOTS) {
-    const int64_t at = b * S + t;
-    if (mask && !mask[at]) continue;
-    const float s = j < E ? score[at * E + j] : 0.f;
-    p += share(s, lanes_sum<W>(s));
-    for (int a = 0; a < k; ++a) c += idx[at * k + a] == j;
-    ++n;
-  }
+  int32_t n = 0;
+#pragma unroll 4
+  for (int64_t t = t0 + slot; t < t1; t += SLOTS)
+    balance_token<W>(score, idx, mask, b * S + t, E, k, j, hist, p, n);
   sp[slot][j] = p;
-  sc[slot][j] = c;
   if (j == 0) sn[slot] = n;
   __syncthreads();
   if (slot == 0) {
     float ps = 0.f;
-    int32_t cs = 0, ns = 0;
+    int32_t ns = 0;
+#pragma unroll
     for (int i = 0; i < SLOTS; ++i) {
       ps += sp[i][j];
-      cs += sc[i][j];
       ns += sn[i];
     }
     psum[part * W + j] = ps;
-    cnt[part * W + j] = cs;
+    cnt[part * W + j] = hist[j];
     if (j == 0) tok[part] = ns;
   }
 }
 
-// One workgroup adds the parts, in order, and forms the loss.
-template <int W>
-__global__ __launch_bounds__(256) void balance_finish_kernel(const float* __restrict__ psum,
-                                                             const int32_t* __restrict__ cnt,
-                                                             const int32_t* __restrict__ tok, int64_t B, int64_t nblk,
-                                                             int N, int k, int m, float coef, float* __restrict__ loss,
-                                                             int32_t* __restrict__ count,
-                                                             int32_t* __restrict__ tokens,
-                                                             float* __restrict__ mean_p) {
-  constexpr int SLOTS = 256 / W;
-  __shared__ float red[4];
-  __shared__ int32_t sc[SLOTS][W];
-  const int j = threadIdx.x % W, slot = threadIdx.x / W;
-  const int E = N - m;
+// One workgroup adds up each sequence, in a fixed order, and forms the loss: from the
+// parts, or (ALONE) from the tokens themselves. `subs` lane groups share a sequence.
+template <int W, bool ALONE>
+__global__ __launch_bounds__(1024) void balance_finish_kernel(
+    const float* __restrict__ psum, const int32_t* __restrict__ cnt, const int32_t* __restrict__ tok,
+    const float* __restrict__ score, const int32_t* __restrict__ idx, const uint8_t* __restrict__ mask, int64_t B,
+    int64_t S, int64_t nblk, int subs, int N, int k, int m, float coef, float* __restrict__ loss,
+    int32_t* __restrict__ count, int32_t* __restrict__ tokens, float* __restrict__ mean_p) {
+  constexpr int SLOTS = 1024 / W;
+  __shared__ float red[16], sp[SLOTS][W];
+  __shared__ int32_t sn[SLOTS], hist[SLOTS][W];
+  const int j = threadIdx.x % W, slot = threadIdx.x / W, sub = slot % subs, own = slot - sub;
+  const int E = N - m, per = SLOTS / subs;  // sequences at once
   float sum = 0.f;
-  for (int64_t b0 = 0; b0 < B; b0 += SLOTS) {
-    const int64_t b = b0 + slot;
+  for (int64_t b0 = 0; b0 < B; b0 += per) {
+    const int64_t b = b0 + slot / subs;
+    hist[slot][j] = 0;
+    __syncthreads();
     float ps = 0.f;
-    int32_t cs = 0, ns = 0;
-    if (b < B) {
-      for (int64_t i = 0; i < nblk; ++i) {
-        const int64_t part = b * nblk + i;
-        ps += psum[part * W + j];
-        cs += cnt[part * W + j];
-        ns += tok[part];
+    int32_t ns = 0;
+    if (b < B && slot < per * subs) {
+      if (ALONE) {
+#pragma unroll 4
+        for (int64_t t = sub; t < S; t += subs)
+          balance_token<W>(score, idx, mask, b * S + t, E, k, j, hist[own], ps, ns);
+      } else {
+        int32_t cs = 0;
+#pragma unroll 4
+        for (int64_t i = sub; i < nblk; i += subs) {
+          const int64_t part = b * nblk + i;
+          ps += psum[part * W + j];
+          cs += cnt[part * W + j];
+          ns += tok[part];
+        }
+        if (cs) atomicAdd(&hist[own][j], cs);
       }
     }
-    sc[slot][j] = cs;
+    sp[slot][j] = ps;
+    if (j == 0) sn[slot] = ns;
     __syncthreads();
-    if (b < B) {
-      if (j < N) count[b * N + j] = cs;
+    if (b < B && sub == 0 && slot < per * subs) {
+      ps = 0.f;
+      ns = 0;
+      for (int i = 0; i < subs; ++i) {
+        ps += sp[slot + i][j];
+        ns += sn[slot + i];
+      }
+      if (j < N) count[b * N + j] = hist[slot][j];
       if (j == 0) tokens[b] = ns;
       if (j < E) {
         const float n = (float)(ns > 0 ? ns : 1);
         const float mp = ps / n;
-        const float f = (float)sc[slot][m + j] * ((float)E / (float)(k - m)) / n;
+        const float f = (float)hist[slot][m + j] * ((float)E / (float)(k - m)) / n;
         mean_p[b * E + j] = mp;
         sum += f * mp;
       }
@@ -140,7 +172,10 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(const float* __re
 
 // ---------------------------------------------------- the router's projection
 
-constexpr int PW = 16;  // floats per token: dz_j / r for j < E <= 15, and the factor of x in slot 15
+// Floats per token: dz_j / r for j < E <= 15, and the factor c of x in slot 15, -0 for a
+// token that takes no part (one that does has +0).
+constexpr int PW = 16;
+constexpr uint32_t NO_PART = 0x80000000u;
 
 // One workgroup per token: r from the whole row, then the token's factors. A token
 // whose dscore is all zero takes part in nothing: its row is not read.
@@ -154,7 +189,7 @@ __global__ __launch_bounds__(256) void router_factors_kernel(const bf16_t* __res
   for (int i = 0; i < E; ++i) any |= dscore[t * E + i] != 0.f;
   float* out = P + t * PW;
   if (!any) {
-    if (j < PW) out[j] = 0.f;
+    if (j < PW) out[j] = j == PW - 1 ? __uint_as_float(NO_PART) : 0.f;
     return;
   }
   const bf16_t* x = X + t * NC;
@@ -177,18 +212,19 @@ __global__ __launch_bounds__(256) void router_factors_kernel(const bf16_t* __res
     const float ms = ss / (float)NC;
     const float inv_r = ms == 0.f ? 0.f : 1.f / sqrtf(ms);
     if (j < PW - 1) out[j] = dz * inv_r;
-    else if (j == PW - 1) out[j] = along * inv_r * inv_r / (float)NC;
+    else if (j == PW - 1) out[j] = along * inv_r * inv_r / (float)NC + 0.f;  // -0 + 0 = +0
   }
 }
 
 // dX_out = dX_in + P w - c x and this split's part of dw = sum_t x P. Each thread
 // owns 4 of the N*C channels and keeps their rows of w and dw in registers; the
-// token's 16 factors are the same for the whole wave.
+// token's 16 factors are the same for the whole wave (scalar registers).
 template <int E>
-__global__ __launch_bounds__(256) void router_apply_kernel(const bf16_t* __restrict__ X, int64_t T, int64_t NC, int Er,
+__global__ __launch_bounds__(256) void router_apply_kernel(const bf16_t* __restrict__ X, int64_t T, int64_t NC,
                                                            int64_t per, const float* __restrict__ w,
                                                            const float* __restrict__ P, const bf16_t* dX_in,
                                                            bf16_t* dX_out, float* __restrict__ part) {
+  typedef uint32_t u2 __attribute__((ext_vector_type(2)));
   const int64_t c0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   if (c0 >= NC) return;
   float wv[4][E], dw[4][E];
@@ -196,25 +232,22 @@ __global__ __launch_bounds__(256) void router_apply_kernel(const bf16_t* __restr
   for (int e = 0; e < 4; ++e)
 #pragma unroll
     for (int j = 0; j < E; ++j) {
-      wv[e][j] = j < Er ? w[(c0 + e) * Er + j] : 0.f;
+      wv[e][j] = w[(c0 + e) * E + j];
       dw[e][j] = 0.f;
     }
   const int64_t t0 = (int64_t)blockIdx.y * per, t1 = t0 + per < T ? t0 + per : T;
 #pragma unroll 4
   for (int64_t t = t0; t < t1; ++t) {
-    const uint2 xq = *reinterpret_cast<const uint2*>(X + t * NC + c0);
-    const uint2 dq = *reinterpret_cast<const uint2*>(dX_in + t * NC + c0);
+    u2 xq = __builtin_nontemporal_load(reinterpret_cast<const u2*>(X + t * NC + c0));
+    const u2 dq = __builtin_nontemporal_load(reinterpret_cast<const u2*>(dX_in + t * NC + c0));
     const float* f = P + t * PW;
-    bool any = f[PW - 1] != 0.f;
-#pragma unroll
-    for (int j = 0; j < E; ++j) any |= f[j] != 0.f;
-    float x[4] = {bf2f(xq.x & 0xffffu), __uint_as_float(xq.x & 0xffff0000u), bf2f(xq.y & 0xffffu),
-                  __uint_as_float(xq.y & 0xffff0000u)};
-    float o[4] = {bf2f(dq.x & 0xffffu), __uint_as_float(dq.x & 0xffff0000u), bf2f(dq.y & 0xffffu),
+    if (__float_as_uint(f[PW - 1]) == NO_PART) xq = u2{0u, 0u};  // such a token may hold anything
+    const float x[4] = {__uint_as_float(xq.x << 16), __uint_as_float(xq.x & 0xffff0000u),
+                        __uint_as_float(xq.y << 16), __uint_as_float(xq.y & 0xffff0000u)};
+    float o[4] = {__uint_as_float(dq.x << 16), __uint_as_float(dq.x & 0xffff0000u), __uint_as_float(dq.y << 16),
                   __uint_as_float(dq.y & 0xffff0000u)};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      x[e] = any ? x[e] : 0.f;  // a token that takes no part may hold anything
       float s = -f[PW - 1] * x[e];
 #pragma unroll
       for (int j = 0; j < E; ++j) {
@@ -223,14 +256,14 @@ __global__ __launch_bounds__(256) void router_apply_kernel(const bf16_t* __restr
       }
       o[e] += s;
     }
-    *reinterpret_cast<uint2*>(dX_out + t * NC + c0) = make_uint2(pack_bf2(o[0], o[1]), pack_bf2(o[2], o[3]));
+    __builtin_nontemporal_store(u2{pack_bf2_hw(o[0], o[1]), pack_bf2_hw(o[2], o[3])},
+                                reinterpret_cast<u2*>(dX_out + t * NC + c0));
   }
-  float* p = part + ((int64_t)blockIdx.y * NC + c0) * Er;
+  float* p = part + ((int64_t)blockIdx.y * NC + c0) * E;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
 #pragma unroll
-    for (int j = 0; j < E; ++j)
-      if (j < Er) p[e * Er + j] = dw[e][j];
+    for (int j = 0; j < E; ++j) p[e * E + j] = dw[e][j];
 }
 
 __global__ __launch_bounds__(256) void split_sum_kernel(const float* __restrict__ part, int64_t n, int splits,
@@ -246,7 +279,7 @@ __global__ __launch_bounds__(256) void split_sum_kernel(const float* __restrict_
 // least in each (a split writes its part of dw once).
 int64_t router_splits(int64_t T, int64_t NC) {
   const int64_t blocks = (NC + 1023) / 1024;
-  int64_t s = (1024 + blocks - 1) / blocks;
+  int64_t s = 768 / blocks;  // three workgroups a CU are resident: one round
   const int64_t most = (T + 31) / 32;
   if (s > most) s = most;
   return s < 1 ? 1 : s;
@@ -261,26 +294,32 @@ hipError_t balance_go(const float* score, const int32_t* idx, const uint8_t* mas
                       int m, float coef, float* loss, int32_t* count, int32_t* tokens, float* mean_p, void* ws,
                       hipStream_t st) {
   const int64_t nblk = bal_blocks(S), parts = B * nblk;
+  int subs = 1024 / W;  // lane groups of one sequence: all of them, halved while sequences go without
+  while (subs > 1 && (1024 / W) / subs < B) subs /= 2;
+  if (B * S <= BAL_ALONE) {
+    hipLaunchKernelGGL((balance_finish_kernel<W, true>), dim3(1), dim3(1024), 0, st, nullptr, nullptr, nullptr, score,
+                       idx, mask, B, S, nblk, subs, N, k, m, coef, loss, count, tokens, mean_p);
+    return hipGetLastError();
+  }
   char* q = (char*)ws;
   float* psum = (float*)q;
   q += al256(parts * W * 4);
   int32_t* cnt = (int32_t*)q;
   q += al256(parts * W * 4);
   int32_t* tok = (int32_t*)q;
-  if (parts > 0)
-    hipLaunchKernelGGL((balance_part_kernel<W>), dim3((unsigned)parts), dim3(256), 0, st, score, idx, mask, S, nblk,
-                       N - m, k, psum, cnt, tok);
-  hipLaunchKernelGGL((balance_finish_kernel<W>), dim3(1), dim3(256), 0, st, psum, cnt, tok, B, nblk, N, k, m, coef,
-                     loss, count, tokens, mean_p);
+  hipLaunchKernelGGL((balance_part_kernel<W>), dim3((unsigned)parts), dim3(256), 0, st, score, idx, mask, S, nblk,
+                     N - m, k, psum, cnt, tok);
+  hipLaunchKernelGGL((balance_finish_kernel<W, false>), dim3(1), dim3(1024), 0, st, psum, cnt, tok, score, idx, mask,
+                     B, S, nblk, subs, N, k, m, coef, loss, count, tokens, mean_p);
   return hipGetLastError();
 }
 
 template <int E>
-void router_apply(const void* X, int64_t T, int64_t NC, int Er, int64_t splits, const float* w, const float* P,
+void router_apply(const void* X, int64_t T, int64_t NC, int64_t splits, const float* w, const float* P,
                   const void* dX_in, void* dX_out, float* part, hipStream_t st) {
   const int64_t per = (T + splits - 1) / splits;
   hipLaunchKernelGGL((router_apply_kernel<E>), dim3((unsigned)((NC + 1023) / 1024), (unsigned)splits), dim3(256), 0, st,
-                     (const bf16_t*)X, T, NC, Er, per, w, P, (const bf16_t*)dX_in, (bf16_t*)dX_out, part);
+                     (const bf16_t*)X, T, NC, per, w, P, (const bf16_t*)dX_in, (bf16_t*)dX_out, part);
 }
 
 }  // namespace
@@ -288,6 +327,7 @@ void router_apply(const void* X, int64_t T, int64_t NC, int Er, int64_t splits, 
 int64_t balance_ws_bytes(int64_t B, int64_t S, int N, int m) {
   const int W = N <= 16 ? 16 : 64;
   const int64_t parts = B * bal_blocks(S);
+  if (B * S <= BAL_ALONE) return 0;
   return 2 * al256(parts * W * 4) + al256(parts * 4);
 }
 
@@ -332,10 +372,15 @@ hipError_t launch_router_backward(const void* X, int64_t T, int N, int64_t C, in
   }
   hipLaunchKernelGGL(router_factors_kernel, dim3((unsigned)T), dim3(256), 0, st, (const bf16_t*)X, NC, E, score,
                      dscore, P);
-  if (E <= 4) router_apply<4>(X, T, NC, E, splits, w, P, dX_in, dX_out, part, st);
-  else if (E <= 8) router_apply<8>(X, T, NC, E, splits, w, P, dX_in, dX_out, part, st);
-  else if (E <= 12) router_apply<12>(X, T, NC, E, splits, w, P, dX_in, dX_out, part, st);
-  else router_apply<15>(X, T, NC, E, splits, w, P, dX_in, dX_out, part, st);
+  switch (E) {
+#define HC_ROUTER_CASE(e) \
+  case e: router_apply<e>(X, T, NC, splits, w, P, dX_in, dX_out, part, st); break;
+    HC_ROUTER_CASE(1) HC_ROUTER_CASE(2) HC_ROUTER_CASE(3) HC_ROUTER_CASE(4) HC_ROUTER_CASE(5)
+    HC_ROUTER_CASE(6) HC_ROUTER_CASE(7) HC_ROUTER_CASE(8) HC_ROUTER_CASE(9) HC_ROUTER_CASE(10)
+    HC_ROUTER_CASE(11) HC_ROUTER_CASE(12) HC_ROUTER_CASE(13) HC_ROUTER_CASE(14) HC_ROUTER_CASE(15)
+#undef HC_ROUTER_CASE
+    default: break;
+  }
   hipLaunchKernelGGL(split_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, n, (int)splits, dw);
   return hipGetLastError();
 }
