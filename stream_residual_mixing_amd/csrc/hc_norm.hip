@@ -13,14 +13,20 @@ namespace {
 
 constexpr int OUT_STREAM = 0, OUT_E4M3 = 2, OUT_I8 = 3;  // the dtype codes of hc.h for the 8-bit forms
 
-// One row's threads: NT threads with ITEMS pieces of 8 channels each, piece
-// (it * NT + tid). 64 threads (a wave, four rows per workgroup, no barrier) up to
-// 2,048 channels, a workgroup of 256 up to 8,192, of 1,024 up to 16,384.
-template <int NT>
+// A row's channels lie in pieces of 8, piece (it * NT + tid) of item it with its NT
+// threads: a wave, four rows to a workgroup and no barrier (WAVE, up to 2,048 channels),
+// else a workgroup of as many waves as the row fills.
+constexpr int WAVE_ROWS = 4;
+
+template <bool WAVE>
 struct RowThreads {
-  static constexpr int RPB = NT < 256 ? 256 / NT : 1;  // rows in flight per workgroup
-  static constexpr int BLOCK = NT * RPB;
-  static constexpr int NW = NT / 64;
+  int nt, tid, sub;  // threads of a row, this one's number, its row in the workgroup
+  __device__ __forceinline__ RowThreads() {
+    nt = WAVE ? 64 : blockDim.x;
+    tid = WAVE ? threadIdx.x & 63 : threadIdx.x;
+    sub = WAVE ? threadIdx.x >> 6 : 0;
+  }
+  static __device__ __forceinline__ int rows() { return WAVE ? WAVE_ROWS : 1; }
 };
 
 // VEC: rows of whole pieces at 16-byte aligned addresses. Otherwise whole pieces are
@@ -58,11 +64,11 @@ __device__ __forceinline__ void row_store(T* row, int64_t c0, int64_t C, const f
 }
 
 // The weight is used by every row: ordinary loads, kept in registers over the rows.
-template <bool VEC, int NT, int ITEMS>
-__device__ __forceinline__ void load_weight(const float* w, int64_t C, int tid, float out[ITEMS][8]) {
+template <bool VEC, int ITEMS>
+__device__ __forceinline__ void load_weight(const float* w, int64_t C, int nt, int tid, float out[ITEMS][8]) {
 #pragma unroll
   for (int it = 0; it < ITEMS; ++it) {
-    const int64_t c0 = ((int64_t)it * NT + tid) * 8;
+    const int64_t c0 = ((int64_t)it * nt + tid) * 8;
     if (w == nullptr) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) out[it][e] = 1.f;
@@ -75,36 +81,48 @@ __device__ __forceinline__ void load_weight(const float* w, int64_t C, int tid, 
   }
 }
 
-// Sums over one row's threads, the same value in each; `red` is this row parity's
-// slice of LDS (the next row uses the other one, so one barrier per sum is enough).
-template <int NT>
-__device__ __forceinline__ float row_sum(float v, float* red) {
-  v = wave_sum(v);
-  if (NT == 64) return v;
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = 0.f;
+// Sums of NV values over one row's threads, the same in each; `red` is this row parity's
+// slice of LDS (the next row uses the other one, so one barrier a row is enough).
+template <bool WAVE, int NV>
+__device__ __forceinline__ void row_sum(float v[NV], float (*red)[16]) {
 #pragma unroll
-  for (int i = 0; i < RowThreads<NT>::NW; ++i) s += red[i];
-  return s;
+  for (int i = 0; i < NV; ++i) v[i] = wave_sum(v[i]);
+  if (WAVE) return;
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) red[i][threadIdx.x >> 6] = v[i];
+  __syncthreads();
+  const int nw = blockDim.x >> 6;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    v[i] = 0.f;
+    for (int w = 0; w < nw; ++w) v[i] += red[i][w];
+  }
 }
 
 // The largest magnitude as float bits: ordering the bits as unsigned numbers puts
 // infinity above every number and NaN above infinity, so a NaN is never lost.
-__device__ __forceinline__ uint32_t umax_xor(uint32_t v, int mask) {
-  return max(v, (uint32_t)__shfl_xor((int)v, mask, 64));
+template <int CTRL>
+__device__ __forceinline__ uint32_t umax_dpp(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true));
 }
+constexpr int DPP_HALF_MIRROR = 0x141;  // lane i of 8 takes lane 7 - i
 
-template <int NT>
+__device__ __forceinline__ uint32_t umax4(uint32_t v) { return umax_dpp<DPP_QXOR2>(umax_dpp<DPP_QXOR1>(v)); }
+__device__ __forceinline__ uint32_t umax8(uint32_t v) { return umax_dpp<DPP_HALF_MIRROR>(umax4(v)); }
+__device__ __forceinline__ uint32_t umax16(uint32_t v) { return umax_dpp<DPP_ROR8>(umax8(v)); }
+
+template <bool WAVE>
 __device__ __forceinline__ uint32_t row_umax(uint32_t v, uint32_t* red) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v = umax_xor(v, o);
-  if (NT == 64) return v;
+  v = umax16(v);
+  v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
+  v = max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
+  if (WAVE) return v;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
   __syncthreads();
+  const int nw = blockDim.x >> 6;
   uint32_t s = 0;
-#pragma unroll
-  for (int i = 0; i < RowThreads<NT>::NW; ++i) s = max(s, red[i]);
+  for (int i = 0; i < nw; ++i) s = max(s, red[i]);
   return s;
 }
 
@@ -146,42 +164,67 @@ __device__ __forceinline__ uint2 pack_i8(const float v[8], float inv) {
 }
 
 // MODE 0: v = x; 1: v = x + residual; 2: v = sum_i h[i] x[i] (n streams).
-template <typename T, int MODE, int NT, int ITEMS, bool VEC>
-__global__ __launch_bounds__(RowThreads<NT>::BLOCK) void rms_norm_kernel(NormArgs a) {
-  using R = RowThreads<NT>;
-  __shared__ float red[2][16];
+template <typename T, int MODE, int ITEMS, bool WAVE, bool VEC>
+__global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(NormArgs a) {
+  __shared__ float red[2][1][16];
   __shared__ uint32_t redm[2][16];
-  const int tid = threadIdx.x % NT, sub = threadIdx.x / NT;
+  const RowThreads<WAVE> r;
+  const int tid = r.tid, NT = r.nt;
   const int64_t C = a.C;
   const float inv_c = 1.0f / (float)C;
   float w[ITEMS][8];
-  load_weight<VEC, NT, ITEMS>(a.w, C, tid, w);
+  load_weight<VEC, ITEMS>(a.w, C, NT, tid, w);
   int parity = 0;
-  for (int64_t t = (int64_t)blockIdx.x * R::RPB + sub; t < a.T; t += (int64_t)gridDim.x * R::RPB, parity ^= 1) {
+  for (int64_t t = (int64_t)blockIdx.x * r.rows() + r.sub; t < a.T; t += (int64_t)gridDim.x * r.rows(), parity ^= 1) {
     float v[ITEMS][8];
     float ss = 0.f;
+    if (MODE == 2) {
 #pragma unroll
-    for (int it = 0; it < ITEMS; ++it) {
-      const int64_t c0 = ((int64_t)it * NT + tid) * 8;
-      if (MODE == 2) {
+      for (int it = 0; it < ITEMS; ++it)
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[it][e] = 0.f;
-        for (int i = 0; i < a.n; ++i) {
+      const T* x = (const T*)a.x + t * a.n * C;
+      const float* h = a.h + t * a.n;
+      int i = 0;
+      for (; i + 4 <= a.n; i += 4) {  // four streams in flight
+        float xi[4][ITEMS][8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int it = 0; it < ITEMS; ++it)
+            row_load<VEC>(x + (i + q) * C, ((int64_t)it * NT + tid) * 8, C, xi[q][it]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float hi = h[i + q];
+#pragma unroll
+          for (int it = 0; it < ITEMS; ++it)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[it][e] += hi * xi[q][it][e];
+        }
+      }
+      for (; i < a.n; ++i) {
+        const float hi = h[i];
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it) {
           float xi[8];
-          row_load<VEC>((const T*)a.x + (t * a.n + i) * C, c0, C, xi);
-          const float hi = a.h[t * a.n + i];
+          row_load<VEC>(x + i * C, ((int64_t)it * NT + tid) * 8, C, xi);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[it][e] += hi * xi[e];
         }
-      } else {
-        row_load<VEC>((const T*)a.x + t * C, c0, C, v[it]);
-        if (MODE == 1) {
-          float r[8];
-          row_load<VEC>((const T*)a.res + t * C, c0, C, r);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[it][e] += r[e];
-        }
       }
+    } else {
+      float res[ITEMS][8];
+#pragma unroll
+      for (int it = 0; it < ITEMS; ++it) {
+        const int64_t c0 = ((int64_t)it * NT + tid) * 8;
+        row_load<VEC>((const T*)a.x + t * C, c0, C, v[it]);
+        if (MODE == 1) row_load<VEC>((const T*)a.res + t * C, c0, C, res[it]);
+      }
+      if (MODE == 1)
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[it][e] += res[it][e];
     }
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
@@ -191,7 +234,8 @@ __global__ __launch_bounds__(RowThreads<NT>::BLOCK) void rms_norm_kernel(NormArg
       for (int e = 0; e < 8; ++e)
         if (MODE != 2 || (VEC ? c0 : c0 + e) < C) ss += v[it][e] * v[it][e];  // 0 * an infinite h is no channel's
     }
-    const float rstd = rms_factor(row_sum<NT>(ss, red[parity]), inv_c, a.eps);
+    row_sum<WAVE, 1>(&ss, red[parity]);
+    const float rstd = rms_factor(ss, inv_c, a.eps);
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it)
 #pragma unroll
@@ -217,16 +261,13 @@ __global__ __launch_bounds__(RowThreads<NT>::BLOCK) void rms_norm_kernel(NormArg
       uint32_t all = 0;
 #pragma unroll
       for (int it = 0; it < ITEMS; ++it) all = max(all, m[it]);
-      all = row_umax<NT>(all, redm[parity]);
+      all = row_umax<WAVE>(all, redm[parity]);
 #pragma unroll
       for (int it = 0; it < ITEMS; ++it) m[it] = all;
     } else {  // a group's 4, 8 or 16 threads are neighbours in a wave
 #pragma unroll
-      for (int it = 0; it < ITEMS; ++it) {
-        m[it] = umax_xor(umax_xor(m[it], 1), 2);
-        if (a.group > 32) m[it] = umax_xor(m[it], 4);
-        if (a.group > 64) m[it] = umax_xor(m[it], 8);
-      }
+      for (int it = 0; it < ITEMS; ++it)
+        m[it] = a.group == 32 ? umax4(m[it]) : a.group == 64 ? umax8(m[it]) : umax16(m[it]);
     }
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
@@ -258,23 +299,23 @@ __global__ __launch_bounds__(RowThreads<NT>::BLOCK) void rms_norm_kernel(NormArg
 // dx = rstd w dy - v rstd^3 mean(w dy v) + ds, and this workgroup's part of
 // dw = sum_t dy v rstd, kept in registers over its rows and written once to
 // part[workgroup row][C] (the parts are added in a fixed order afterwards).
-template <typename T, int NT, int ITEMS, bool VEC>
-__global__ __launch_bounds__(RowThreads<NT>::BLOCK) void rms_norm_backward_kernel(NormBwdArgs a) {
-  using R = RowThreads<NT>;
+template <typename T, int ITEMS, bool WAVE, bool VEC>
+__global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_backward_kernel(NormBwdArgs a) {
   __shared__ float red[2][2][16];
-  const int tid = threadIdx.x % NT, sub = threadIdx.x / NT;
+  const RowThreads<WAVE> r;
+  const int tid = r.tid, NT = r.nt;
   const int64_t C = a.C;
   const float inv_c = 1.0f / (float)C;
   float w[ITEMS][8], dw[ITEMS][8];
-  load_weight<VEC, NT, ITEMS>(a.w, C, tid, w);
+  load_weight<VEC, ITEMS>(a.w, C, NT, tid, w);
 #pragma unroll
   for (int it = 0; it < ITEMS; ++it)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[it][e] = 0.f;
   int parity = 0;
-  for (int64_t t = (int64_t)blockIdx.x * R::RPB + sub; t < a.T; t += (int64_t)gridDim.x * R::RPB, parity ^= 1) {
+  for (int64_t t = (int64_t)blockIdx.x * r.rows() + r.sub; t < a.T; t += (int64_t)gridDim.x * r.rows(), parity ^= 1) {
     float v[ITEMS][8], dy[ITEMS][8], ds[ITEMS][8];
-    float ss = 0.f, dot = 0.f;
+    float sums[2] = {0.f, 0.f};
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
       const int64_t c0 = ((int64_t)it * NT + tid) * 8;
@@ -286,29 +327,12 @@ __global__ __launch_bounds__(RowThreads<NT>::BLOCK) void rms_norm_backward_kerne
     for (int it = 0; it < ITEMS; ++it)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        ss += v[it][e] * v[it][e];
-        dot += v[it][e] * (w[it][e] * dy[it][e]);
+        sums[0] += v[it][e] * v[it][e];
+        sums[1] += v[it][e] * (w[it][e] * dy[it][e]);
       }
-    if (NT == 64) {
-      ss = wave_sum(ss);
-      dot = wave_sum(dot);
-    } else {
-      ss = wave_sum(ss);
-      dot = wave_sum(dot);
-      if ((threadIdx.x & 63) == 0) {
-        red[parity][0][threadIdx.x >> 6] = ss;
-        red[parity][1][threadIdx.x >> 6] = dot;
-      }
-      __syncthreads();
-      ss = dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < R::NW; ++i) {
-        ss += red[parity][0][i];
-        dot += red[parity][1][i];
-      }
-    }
-    const float rstd = rms_factor(ss, inv_c, a.eps);
-    const float k = (dot * rstd) * inv_c * rstd;
+    row_sum<WAVE, 2>(sums, red[parity]);
+    const float rstd = rms_factor(sums[0], inv_c, a.eps);
+    const float k = (sums[1] * rstd) * inv_c * rstd;
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
       float o[8];
@@ -321,7 +345,7 @@ __global__ __launch_bounds__(RowThreads<NT>::BLOCK) void rms_norm_backward_kerne
     }
   }
   if (a.part == nullptr) return;
-  float* p = a.part + ((int64_t)blockIdx.x * R::RPB + sub) * C;
+  float* p = a.part + ((int64_t)blockIdx.x * r.rows() + r.sub) * C;
 #pragma unroll
   for (int it = 0; it < ITEMS; ++it) {
     const int64_t c0 = ((int64_t)it * NT + tid) * 8;
@@ -335,74 +359,86 @@ __global__ __launch_bounds__(RowThreads<NT>::BLOCK) void rms_norm_backward_kerne
   }
 }
 
-// out[c] = sum_p part[p][c]: 32 columns by 8 interleaved walks per workgroup, the
+// out[c] = sum_p part[p][c]: 32 columns by 32 interleaved walks per workgroup, the
 // walks added in order.
-__global__ __launch_bounds__(256) void column_sum_kernel(const float* __restrict__ part, int64_t P, int64_t C,
-                                                         float* __restrict__ out) {
-  __shared__ float s[8][32];
+__global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restrict__ part, int64_t P, int64_t C,
+                                                          float* __restrict__ out) {
+  __shared__ float s[32][33];
   const int cl = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + cl;
   float v = 0.f;
-  if (c < C)
-    for (int64_t p = g; p < P; p += 8) v += part[p * C + c];
+  if (c < C) {
+#pragma unroll 4
+    for (int64_t p = g; p < P; p += 32) v += part[p * C + c];
+  }
   s[g][cl] = v;
   __syncthreads();
   if (g == 0 && c < C) {
     float r = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r += s[i][cl];
+    for (int i = 0; i < 32; ++i) r += s[i][cl];
     out[c] = r;
   }
 }
 
-// The workgroups of a pass over T rows: enough to fill the device, few enough that
-// each keeps the weight in registers over several rows.
-template <int NT>
-int64_t row_blocks(int64_t T, int64_t most) {
-  const int64_t need = (T + RowThreads<NT>::RPB - 1) / RowThreads<NT>::RPB;
-  return need < most ? need : most;
+// Launch shape of a pass over T rows of C channels: pieces per thread, threads, and
+// the workgroups, bounded so that each keeps the weight in registers over several rows.
+struct RowShape {
+  int items;
+  bool wave;
+  unsigned block, grid;
+};
+
+RowShape row_shape(int64_t T, int64_t C, int64_t most_waves) {
+  RowShape s;
+  const int64_t pieces = (C + 7) / 8;
+  s.wave = C <= 2048;
+  s.items = s.wave ? (C <= 512 ? 1 : C <= 1024 ? 2 : 4) : (C <= 8192 ? 1 : 2);
+  s.block = s.wave ? 64 * WAVE_ROWS : (unsigned)((pieces + 64 * s.items - 1) / (64 * s.items) * 64);
+  const int64_t need = s.wave ? (T + WAVE_ROWS - 1) / WAVE_ROWS : T, most = most_waves * 64 / s.block;
+  s.grid = (unsigned)(need < most ? need : most);
+  return s;
 }
 
-constexpr int64_t FWD_BLOCKS = 2048, BWD_BLOCKS = 512;
+constexpr int64_t FWD_WAVES = 8192, BWD_WAVES = 4096;
 
-template <typename T, int MODE, int NT, int ITEMS>
-void norm_go(bool vec, const NormArgs& a, hipStream_t st) {
-  const dim3 g((unsigned)row_blocks<NT>(a.T, FWD_BLOCKS)), b(RowThreads<NT>::BLOCK);
-  if (vec) hipLaunchKernelGGL((rms_norm_kernel<T, MODE, NT, ITEMS, true>), g, b, 0, st, a);
-  else hipLaunchKernelGGL((rms_norm_kernel<T, MODE, NT, ITEMS, false>), g, b, 0, st, a);
+template <typename T, int MODE, int ITEMS, bool WAVE>
+void norm_go(bool vec, const RowShape& s, const NormArgs& a, hipStream_t st) {
+  if (vec) hipLaunchKernelGGL((rms_norm_kernel<T, MODE, ITEMS, WAVE, true>), dim3(s.grid), dim3(s.block), 0, st, a);
+  else hipLaunchKernelGGL((rms_norm_kernel<T, MODE, ITEMS, WAVE, false>), dim3(s.grid), dim3(s.block), 0, st, a);
 }
 
 template <typename T, int MODE>
 void norm_by_width(bool vec, const NormArgs& a, hipStream_t st) {
-  if (a.C <= 512) norm_go<T, MODE, 64, 1>(vec, a, st);
-  else if (a.C <= 1024) norm_go<T, MODE, 64, 2>(vec, a, st);
-  else if (a.C <= 2048) norm_go<T, MODE, 64, 4>(vec, a, st);
-  else if (a.C <= 4096) norm_go<T, MODE, 256, 2>(vec, a, st);
-  else if (a.C <= 8192) norm_go<T, MODE, 256, 4>(vec, a, st);
-  else norm_go<T, MODE, 1024, 2>(vec, a, st);
+  const RowShape s = row_shape(a.T, a.C, FWD_WAVES);
+  if (s.wave && s.items == 1) norm_go<T, MODE, 1, true>(vec, s, a, st);
+  else if (s.wave && s.items == 2) norm_go<T, MODE, 2, true>(vec, s, a, st);
+  else if (s.wave) norm_go<T, MODE, 4, true>(vec, s, a, st);
+  else if (s.items == 1) norm_go<T, MODE, 1, false>(vec, s, a, st);
+  else norm_go<T, MODE, 2, false>(vec, s, a, st);
 }
 
-template <typename T, int NT, int ITEMS>
-void norm_bwd_go(bool vec, const NormBwdArgs& a, hipStream_t st) {
-  const dim3 g((unsigned)row_blocks<NT>(a.T, BWD_BLOCKS)), b(RowThreads<NT>::BLOCK);
-  if (vec) hipLaunchKernelGGL((rms_norm_backward_kernel<T, NT, ITEMS, true>), g, b, 0, st, a);
-  else hipLaunchKernelGGL((rms_norm_backward_kernel<T, NT, ITEMS, false>), g, b, 0, st, a);
+template <typename T, int ITEMS, bool WAVE>
+void norm_bwd_go(bool vec, const RowShape& s, const NormBwdArgs& a, hipStream_t st) {
+  if (vec) hipLaunchKernelGGL((rms_norm_backward_kernel<T, ITEMS, WAVE, true>), dim3(s.grid), dim3(s.block), 0, st, a);
+  else hipLaunchKernelGGL((rms_norm_backward_kernel<T, ITEMS, WAVE, false>), dim3(s.grid), dim3(s.block), 0, st, a);
 }
 
 template <typename T>
 void norm_bwd_by_width(bool vec, const NormBwdArgs& a, hipStream_t st) {
-  if (a.C <= 512) norm_bwd_go<T, 64, 1>(vec, a, st);
-  else if (a.C <= 1024) norm_bwd_go<T, 64, 2>(vec, a, st);
-  else if (a.C <= 2048) norm_bwd_go<T, 64, 4>(vec, a, st);
-  else if (a.C <= 4096) norm_bwd_go<T, 256, 2>(vec, a, st);
-  else if (a.C <= 8192) norm_bwd_go<T, 256, 4>(vec, a, st);
-  else norm_bwd_go<T, 1024, 2>(vec, a, st);
+  const RowShape s = row_shape(a.T, a.C, BWD_WAVES);
+  if (s.wave && s.items == 1) norm_bwd_go<T, 1, true>(vec, s, a, st);
+  else if (s.wave && s.items == 2) norm_bwd_go<T, 2, true>(vec, s, a, st);
+  else if (s.wave) norm_bwd_go<T, 4, true>(vec, s, a, st);
+  else if (s.items == 1) norm_bwd_go<T, 1, false>(vec, s, a, st);
+  else norm_bwd_go<T, 2, false>(vec, s, a, st);
 }
 
 }  // namespace
 
 int64_t norm_backward_parts(int64_t T, int64_t C) {
-  return C <= 2048 ? row_blocks<64>(T, BWD_BLOCKS) * RowThreads<64>::RPB : row_blocks<256>(T, BWD_BLOCKS);
+  const RowShape s = row_shape(T, C, BWD_WAVES);
+  return (int64_t)s.grid * (s.wave ? WAVE_ROWS : 1);
 }
 
 hipError_t launch_rms_norm(int dtype, int mode, bool vec, const NormArgs& a, hipStream_t st) {
@@ -423,7 +459,7 @@ hipError_t launch_rms_norm_backward(int dtype, bool vec, const NormBwdArgs& a, f
   else if (a.T > 0) norm_bwd_by_width<bf16_t>(vec, a, st);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || dw == nullptr) return e;
-  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((a.C + 31) / 32)), dim3(256), 0, st, a.part,
+  hipLaunchKernelGGL(column_sum_kernel, dim3((unsigned)((a.C + 31) / 32)), dim3(1024), 0, st, a.part,
                      norm_backward_parts(a.T, a.C), a.C, dw);
   return hipGetLastError();
 }

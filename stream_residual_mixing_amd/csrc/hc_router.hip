@@ -271,16 +271,20 @@ __global__ __launch_bounds__(256) void split_sum_kernel(const float* __restrict_
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n) return;
   float s = 0.f;
+#pragma unroll 8
   for (int k = 0; k < splits; ++k) s += part[k * n + i];
   out[i] = s;
 }
 
-// Token splits of the apply pass: enough workgroups for the device, 32 tokens at
-// least in each (a split writes its part of dw once).
-int64_t router_splits(int64_t T, int64_t NC) {
+// Token splits of the apply pass: one round of the workgroups that are resident at once
+// (four a CU, three where 15 columns take more registers; 865 us for one round of 1,024
+// against 921 for 768 at N = 16, C = 4096, T = 8192), and 16 tokens at least in each (a
+// split writes its part of dw once: 24 us at N = 8, C = 512, T = 1021 against 29 with 32
+// and 28 with 8).
+int64_t router_splits(int64_t T, int64_t NC, int E) {
   const int64_t blocks = (NC + 1023) / 1024;
-  int64_t s = 768 / blocks;  // three workgroups a CU are resident: one round
-  const int64_t most = (T + 31) / 32;
+  int64_t s = (E < 15 ? 1024 : 768) / blocks;
+  const int64_t most = (T + 15) / 16;
   if (s > most) s = most;
   return s < 1 ? 1 : s;
 }
@@ -355,14 +359,14 @@ hipError_t launch_balance_backward(const float* score, const int32_t* count, con
 int64_t router_backward_ws_bytes(int64_t T, int N, int64_t C, int m) {
   if (T == 0) return 0;
   const int64_t NC = (int64_t)N * C;
-  return al256(T * PW * 4) + al256(router_splits(T, NC) * NC * (N - m) * 4);
+  return al256(T * PW * 4) + al256(router_splits(T, NC, N - m) * NC * (N - m) * 4);
 }
 
 hipError_t launch_router_backward(const void* X, int64_t T, int N, int64_t C, int m, const float* w,
                                   const float* score, const float* dscore, const void* dX_in, void* dX_out, float* dw,
                                   void* ws, hipStream_t st) {
-  const int64_t NC = (int64_t)N * C, splits = router_splits(T, NC);
   const int E = N - m;
+  const int64_t NC = (int64_t)N * C, splits = router_splits(T, NC, E);
   float* P = (float*)ws;
   float* part = (float*)((char*)ws + al256(T * PW * 4));
   const int64_t n = NC * E;
