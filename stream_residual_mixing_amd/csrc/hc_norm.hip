@@ -36,18 +36,44 @@ __device__ __forceinline__ int piece_count(int64_t c0, int64_t C) {
   return (int)max((int64_t)0, min((int64_t)8, C - c0));
 }
 
-template <bool VEC, typename T>
-__device__ __forceinline__ void row_load(const T* row, int64_t c0, int64_t C, float v[8]) {
-  const int cnt = piece_count(c0, C);
-  if (VEC) {
-    if (cnt > 0) load8_nt(row + c0, v);
-    else
+// A piece as stored, so that the next row's can be on their way in few registers.
+template <typename T> struct Piece;
+template <> struct Piece<float> {
+  float q[8];
+  __device__ __forceinline__ void open(float v[8]) const {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.f;
-  } else if (cnt == 8) {
-    load8_any(row + c0, v);
+    for (int e = 0; e < 8; ++e) v[e] = q[e];
+  }
+};
+template <> struct Piece<bf16_t> {
+  uint32_t q[4];
+  __device__ __forceinline__ void open(float v[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(q[i] << 16);
+      v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
+    }
+  }
+};
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void row_load(const T* row, int64_t c0, int64_t C, Piece<T>& v) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  constexpr int N = sizeof(v) / 16;
+  const int cnt = piece_count(c0, C);
+  if (VEC && cnt > 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const u4 q = __builtin_nontemporal_load(reinterpret_cast<const u4*>(row + c0) + i);
+      __builtin_memcpy((char*)v.q + 16 * i, &q, 16);
+    }
+  } else if (!VEC && cnt == 8) {
+    __builtin_memcpy(v.q, row + c0, sizeof(v));
   } else {
-    load8_tail(row + c0, cnt, v);
+    T e8[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) e8[e] = !VEC && e < cnt ? row[c0 + e] : T(0);
+    __builtin_memcpy(v.q, e8, sizeof(v));
   }
 }
 
@@ -81,6 +107,13 @@ __device__ __forceinline__ void load_weight(const float* w, int64_t C, int nt, i
   }
 }
 
+// A barrier that orders LDS alone: the next row's loads stay on their way.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // Sums of NV values over one row's threads, the same in each; `red` is this row parity's
 // slice of LDS (the next row uses the other one, so one barrier a row is enough).
 template <bool WAVE, int NV>
@@ -91,7 +124,7 @@ __device__ __forceinline__ void row_sum(float v[NV], float (*red)[16]) {
   if ((threadIdx.x & 63) == 0)
 #pragma unroll
     for (int i = 0; i < NV; ++i) red[i][threadIdx.x >> 6] = v[i];
-  __syncthreads();
+  lds_barrier();
   const int nw = blockDim.x >> 6;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -119,7 +152,7 @@ __device__ __forceinline__ uint32_t row_umax(uint32_t v, uint32_t* red) {
   v = max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
   if (WAVE) return v;
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
+  lds_barrier();
   const int nw = blockDim.x >> 6;
   uint32_t s = 0;
   for (int i = 0; i < nw; ++i) s = max(s, red[i]);
@@ -163,19 +196,34 @@ __device__ __forceinline__ uint2 pack_i8(const float v[8], float inv) {
   return r;
 }
 
-// MODE 0: v = x; 1: v = x + residual; 2: v = sum_i h[i] x[i] (n streams).
+// MODE 0: v = x; 1: v = x + residual; 2: v = sum_i h[i] x[i] (n streams); 4: the same
+// with n = 4. But for MODE 2 the next row is on its way while this one is finished
+// (NS arrays or streams of it).
 template <typename T, int MODE, int ITEMS, bool WAVE, bool VEC>
 __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(NormArgs a) {
+  constexpr int NS = MODE == 0 ? 1 : MODE == 4 ? 4 : 2;
+  constexpr bool STREAMS = MODE == 2 || MODE == 4;
   __shared__ float red[2][1][16];
   __shared__ uint32_t redm[2][16];
   const RowThreads<WAVE> r;
   const int tid = r.tid, NT = r.nt;
-  const int64_t C = a.C;
+  const int64_t C = a.C, step = (int64_t)gridDim.x * r.rows();
   const float inv_c = 1.0f / (float)C;
   float w[ITEMS][8];
   load_weight<VEC, ITEMS>(a.w, C, NT, tid, w);
-  int parity = 0;
-  for (int64_t t = (int64_t)blockIdx.x * r.rows() + r.sub; t < a.T; t += (int64_t)gridDim.x * r.rows(), parity ^= 1) {
+  int64_t t = (int64_t)blockIdx.x * r.rows() + r.sub;
+  Piece<T> raw[NS][ITEMS];
+  const auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+#pragma unroll
+      for (int it = 0; it < ITEMS; ++it) {
+        const T* p = MODE == 4 ? (const T*)a.x + (row * 4 + i) * C : (const T*)(i == 0 ? a.x : a.res) + row * C;
+        row_load<VEC>(p, ((int64_t)it * NT + tid) * 8, C, raw[i][it]);
+      }
+  };
+  if (MODE != 2 && t < a.T) fetch(t);
+  for (int parity = 0; t < a.T; t += step, parity ^= 1) {
     float v[ITEMS][8];
     float ss = 0.f;
     if (MODE == 2) {
@@ -183,48 +231,33 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(
       for (int it = 0; it < ITEMS; ++it)
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[it][e] = 0.f;
-      const T* x = (const T*)a.x + t * a.n * C;
-      const float* h = a.h + t * a.n;
-      int i = 0;
-      for (; i + 4 <= a.n; i += 4) {  // four streams in flight
-        float xi[4][ITEMS][8];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int it = 0; it < ITEMS; ++it)
-            row_load<VEC>(x + (i + q) * C, ((int64_t)it * NT + tid) * 8, C, xi[q][it]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float hi = h[i + q];
-#pragma unroll
-          for (int it = 0; it < ITEMS; ++it)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[it][e] += hi * xi[q][it][e];
-        }
-      }
-      for (; i < a.n; ++i) {
-        const float hi = h[i];
+#pragma unroll 4
+      for (int i = 0; i < a.n; ++i) {
+        const float hi = a.h[t * a.n + i];
 #pragma unroll
         for (int it = 0; it < ITEMS; ++it) {
+          Piece<T> q;
           float xi[8];
-          row_load<VEC>(x + i * C, ((int64_t)it * NT + tid) * 8, C, xi);
+          row_load<VEC>((const T*)a.x + (t * a.n + i) * C, ((int64_t)it * NT + tid) * 8, C, q);
+          q.open(xi);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[it][e] += hi * xi[e];
         }
       }
     } else {
-      float res[ITEMS][8];
 #pragma unroll
-      for (int it = 0; it < ITEMS; ++it) {
-        const int64_t c0 = ((int64_t)it * NT + tid) * 8;
-        row_load<VEC>((const T*)a.x + t * C, c0, C, v[it]);
-        if (MODE == 1) row_load<VEC>((const T*)a.res + t * C, c0, C, res[it]);
+      for (int i = 0; i < NS; ++i) {
+        const float hi = MODE == 4 ? a.h[t * 4 + i] : 1.f;
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it) {
+          float xi[8];
+          raw[i][it].open(xi);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[it][e] = MODE == 4 ? (i == 0 ? hi * xi[e] : v[it][e] + hi * xi[e])
+                                                           : (i == 0 ? xi[e] : v[it][e] + xi[e]);
+        }
       }
-      if (MODE == 1)
-#pragma unroll
-        for (int it = 0; it < ITEMS; ++it)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[it][e] += res[it][e];
+      if (t + step < a.T) fetch(t + step);
     }
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
@@ -232,7 +265,7 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(
       if (MODE != 0 && a.s) row_store<VEC>((T*)a.s + t * C, c0, C, v[it]);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (MODE != 2 || (VEC ? c0 : c0 + e) < C) ss += v[it][e] * v[it][e];  // 0 * an infinite h is no channel's
+        if (!STREAMS || (VEC ? c0 : c0 + e) < C) ss += v[it][e] * v[it][e];  // 0 * an infinite h is no channel's
     }
     row_sum<WAVE, 1>(&ss, red[parity]);
     const float rstd = rms_factor(ss, inv_c, a.eps);
@@ -312,17 +345,29 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_backwar
   for (int it = 0; it < ITEMS; ++it)
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[it][e] = 0.f;
-  int parity = 0;
-  for (int64_t t = (int64_t)blockIdx.x * r.rows() + r.sub; t < a.T; t += (int64_t)gridDim.x * r.rows(), parity ^= 1) {
+  const int64_t step = (int64_t)gridDim.x * r.rows();
+  int64_t t = (int64_t)blockIdx.x * r.rows() + r.sub;
+  Piece<T> rv[ITEMS], ry[ITEMS], rs[ITEMS];
+  const auto fetch = [&](int64_t row) {
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const int64_t c0 = ((int64_t)it * NT + tid) * 8;
+      row_load<VEC>((const T*)a.s + row * C, c0, C, rv[it]);
+      row_load<VEC>((const T*)a.dy + row * C, c0, C, ry[it]);
+      if (a.ds) row_load<VEC>((const T*)a.ds + row * C, c0, C, rs[it]);
+    }
+  };
+  if (t < a.T) fetch(t);
+  for (int parity = 0; t < a.T; t += step, parity ^= 1) {
     float v[ITEMS][8], dy[ITEMS][8], ds[ITEMS][8];
     float sums[2] = {0.f, 0.f};
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
-      const int64_t c0 = ((int64_t)it * NT + tid) * 8;
-      row_load<VEC>((const T*)a.s + t * C, c0, C, v[it]);
-      row_load<VEC>((const T*)a.dy + t * C, c0, C, dy[it]);
-      if (a.ds) row_load<VEC>((const T*)a.ds + t * C, c0, C, ds[it]);
+      rv[it].open(v[it]);
+      ry[it].open(dy[it]);
+      rs[it].open(ds[it]);
     }
+    if (t + step < a.T) fetch(t + step);
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it)
 #pragma unroll
@@ -382,25 +427,29 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restric
 }
 
 // Launch shape of a pass over T rows of C channels: pieces per thread, threads, and
-// the workgroups, bounded so that each keeps the weight in registers over several rows.
+// the workgroups, bounded so that each keeps the weight in registers over several rows
+// and reads ahead. Measured at 8,192 x 4,096 with residual and e4m3 groups / 16,384 x 4 x
+// 7,168 / backward of 8,191 x 4,096: forward with two pieces a thread and 16,384 waves
+// 42.8 / 254 us (8,192 waves 43.9 / 261; one piece, 6,144 waves 41.6 / 264, 16,384 waves
+// 43.5 / 260); backward with one piece and 4,096 waves, 16 a CU, 50.4 us (2,048 waves
+// 50.1, 6,144 waves 59.6, each writing a part of dw; two pieces, which spill, 93).
 struct RowShape {
   int items;
   bool wave;
   unsigned block, grid;
 };
 
-RowShape row_shape(int64_t T, int64_t C, int64_t most_waves) {
+RowShape row_shape(int64_t T, int64_t C, bool bwd) {
+  const int64_t most_waves = bwd ? 4096 : 16384;
   RowShape s;
   const int64_t pieces = (C + 7) / 8;
   s.wave = C <= 2048;
-  s.items = s.wave ? (C <= 512 ? 1 : C <= 1024 ? 2 : 4) : (C <= 8192 ? 1 : 2);
+  s.items = s.wave ? (C <= 512 ? 1 : C <= 1024 ? 2 : 4) : (bwd && C <= 8192 ? 1 : 2);
   s.block = s.wave ? 64 * WAVE_ROWS : (unsigned)((pieces + 64 * s.items - 1) / (64 * s.items) * 64);
   const int64_t need = s.wave ? (T + WAVE_ROWS - 1) / WAVE_ROWS : T, most = most_waves * 64 / s.block;
   s.grid = (unsigned)(need < most ? need : most);
   return s;
 }
-
-constexpr int64_t FWD_WAVES = 8192, BWD_WAVES = 4096;
 
 template <typename T, int MODE, int ITEMS, bool WAVE>
 void norm_go(bool vec, const RowShape& s, const NormArgs& a, hipStream_t st) {
@@ -410,11 +459,10 @@ void norm_go(bool vec, const RowShape& s, const NormArgs& a, hipStream_t st) {
 
 template <typename T, int MODE>
 void norm_by_width(bool vec, const NormArgs& a, hipStream_t st) {
-  const RowShape s = row_shape(a.T, a.C, FWD_WAVES);
+  const RowShape s = row_shape(a.T, a.C, false);
   if (s.wave && s.items == 1) norm_go<T, MODE, 1, true>(vec, s, a, st);
   else if (s.wave && s.items == 2) norm_go<T, MODE, 2, true>(vec, s, a, st);
   else if (s.wave) norm_go<T, MODE, 4, true>(vec, s, a, st);
-  else if (s.items == 1) norm_go<T, MODE, 1, false>(vec, s, a, st);
   else norm_go<T, MODE, 2, false>(vec, s, a, st);
 }
 
@@ -426,7 +474,7 @@ void norm_bwd_go(bool vec, const RowShape& s, const NormBwdArgs& a, hipStream_t 
 
 template <typename T>
 void norm_bwd_by_width(bool vec, const NormBwdArgs& a, hipStream_t st) {
-  const RowShape s = row_shape(a.T, a.C, BWD_WAVES);
+  const RowShape s = row_shape(a.T, a.C, true);
   if (s.wave && s.items == 1) norm_bwd_go<T, 1, true>(vec, s, a, st);
   else if (s.wave && s.items == 2) norm_bwd_go<T, 2, true>(vec, s, a, st);
   else if (s.wave) norm_bwd_go<T, 4, true>(vec, s, a, st);
@@ -437,7 +485,7 @@ void norm_bwd_by_width(bool vec, const NormBwdArgs& a, hipStream_t st) {
 }  // namespace
 
 int64_t norm_backward_parts(int64_t T, int64_t C) {
-  const RowShape s = row_shape(T, C, BWD_WAVES);
+  const RowShape s = row_shape(T, C, true);
   return (int64_t)s.grid * (s.wave ? WAVE_ROWS : 1);
 }
 
@@ -445,10 +493,12 @@ hipError_t launch_rms_norm(int dtype, int mode, bool vec, const NormArgs& a, hip
   if (dtype == 0) {
     if (mode == 0) norm_by_width<float, 0>(vec, a, st);
     else if (mode == 1) norm_by_width<float, 1>(vec, a, st);
+    else if (a.n == 4) norm_by_width<float, 4>(vec, a, st);
     else norm_by_width<float, 2>(vec, a, st);
   } else {
     if (mode == 0) norm_by_width<bf16_t, 0>(vec, a, st);
     else if (mode == 1) norm_by_width<bf16_t, 1>(vec, a, st);
+    else if (a.n == 4) norm_by_width<bf16_t, 4>(vec, a, st);
     else norm_by_width<bf16_t, 2>(vec, a, st);
   }
   return hipGetLastError();
