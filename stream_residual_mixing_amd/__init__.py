@@ -144,7 +144,7 @@ def _check(fn: str, status: int) -> None:
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 # The current stream's handle without building a Stream object (2 us of every call).
@@ -153,10 +153,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream(device, stream):
     if stream is not None:
-        return ctypes.c_void_p(int(stream))
+        return int(stream)
     if _raw_stream is not None and device.index is not None:
-        return ctypes.c_void_p(_raw_stream(device.index))
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _dev_tensor(t, name, dtypes=None, shape=None, device=None):

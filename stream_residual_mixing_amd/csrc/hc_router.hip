@@ -221,7 +221,7 @@ __global__ __launch_bounds__(256) void router_factors_kernel(const bf16_t* __res
 // token's 16 factors are the same for the whole wave (scalar registers).
 template <int E>
 __global__ __launch_bounds__(256) void router_apply_kernel(const bf16_t* __restrict__ X, int64_t T, int64_t NC,
-                                                           int64_t per, const float* __restrict__ w,
+                                                           const float* __restrict__ w,
                                                            const float* __restrict__ P, const bf16_t* dX_in,
                                                            bf16_t* dX_out, float* __restrict__ part) {
   typedef uint32_t u2 __attribute__((ext_vector_type(2)));
@@ -235,9 +235,10 @@ __global__ __launch_bounds__(256) void router_apply_kernel(const bf16_t* __restr
       wv[e][j] = w[(c0 + e) * E + j];
       dw[e][j] = 0.f;
     }
-  const int64_t t0 = (int64_t)blockIdx.y * per, t1 = t0 + per < T ? t0 + per : T;
+  // the splits take turns: what runs at once reads neighbouring rows (845 us against 865
+  // with a range of tokens each)
 #pragma unroll 4
-  for (int64_t t = t0; t < t1; ++t) {
+  for (int64_t t = blockIdx.y; t < T; t += gridDim.y) {
     u2 xq = __builtin_nontemporal_load(reinterpret_cast<const u2*>(X + t * NC + c0));
     const u2 dq = __builtin_nontemporal_load(reinterpret_cast<const u2*>(dX_in + t * NC + c0));
     const float* f = P + t * PW;
@@ -321,9 +322,8 @@ hipError_t balance_go(const float* score, const int32_t* idx, const uint8_t* mas
 template <int E>
 void router_apply(const void* X, int64_t T, int64_t NC, int64_t splits, const float* w, const float* P,
                   const void* dX_in, void* dX_out, float* part, hipStream_t st) {
-  const int64_t per = (T + splits - 1) / splits;
   hipLaunchKernelGGL((router_apply_kernel<E>), dim3((unsigned)((NC + 1023) / 1024), (unsigned)splits), dim3(256), 0, st,
-                     (const bf16_t*)X, T, NC, per, w, P, (const bf16_t*)dX_in, (bf16_t*)dX_out, part);
+                     (const bf16_t*)X, T, NC, w, P, (const bf16_t*)dX_in, (bf16_t*)dX_out, part);
 }
 
 }  // namespace
