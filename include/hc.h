@@ -714,7 +714,7 @@ int hc_gated_scan_backward(const void* x, const void* gate, const void* y, const
  *   part; dX_out may be dX (in place). A token whose dscore is all zero takes no
  *   part (its X and score may hold anything); the all-zero state passes nothing.
  *   Covered: dtype HC_BF16 (HC_F32 -> HC_ERR_DTYPE), 1 <= m < N <=
- *   HC_MAX_ROUTER_STREAMS, C a multiple of 32, T < 2^24 (else HC_ERR_SHAPE). X, dX,
+ *   HC_MAX_ROUTER_STREAMS, C a multiple of 32, N*C <= 2^25, T < 2^24 (else HC_ERR_SHAPE). X, dX,
  *   dX_out 16-byte aligned, float arrays 4; workspace 256 bytes,
  *   xhc_router_backward_workspace_bytes (-1 for what is not covered). Deterministic.
  */

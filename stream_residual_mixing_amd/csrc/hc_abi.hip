@@ -1620,7 +1620,7 @@ int xhc_balance_loss_backward(const float* score, const int32_t* count, const in
 static int check_router_shape(int dtype, int64_t T, int N, int64_t C, int m) {
   if (dtype != HC_BF16) return HC_ERR_DTYPE;
   if (T < 0 || T >= (1ll << 24) || m < 1 || N <= m || N > HC_MAX_ROUTER_STREAMS || C < 32 || C % 32 != 0 ||
-      C > (1ll << 26))
+      C > (1ll << 26) || N * C > (1ll << 25))  // 32 rows are reached with 32-bit offsets
     return HC_ERR_SHAPE;
   return HC_OK;
 }

@@ -172,99 +172,192 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(const float* __re
 
 // ---------------------------------------------------- the router's projection
 
-// Floats per token: dz_j / r for j < E <= 15, and the factor c of x in slot 15, -0 for a
-// token that takes no part (one that does has +0).
-constexpr int PW = 16;
-constexpr uint32_t NO_PART = 0x80000000u;
+// The apply pass multiplies on the matrix cores (v_mfma_f32_16x16x32_bf16), 32 tokens
+// and 64 channels of a wave at a time, so that the 2 E products per value of X hide
+// behind its memory traffic (on the vector units they took half as long as the traffic:
+// 845 against 7xx us at N = 16, C = 4096, T = 8192). X is bfloat16 as it is; the float32
+// factors P = dz / r and the weights are split into bfloat16 parts: P into three (24 bits,
+// all of it) for dw, and P and w into two each (16 bits) for dX, which is rounded to 8.
+// Lane 16 q + m of a wave holds channels 4 m .. 4 m + 3 of tokens 4 q + i and 16 + 4 q +
+// i, i < 4: what it loads is its part of both operands and of both results,
+//   dX:  D[token][channel] += [P_hi | P_lo] [w_part | w_part]^T, k = 16 part + j,
+//   dw:  D[channel][j] += x^T P_part, k = 8 q + kk the lane's kk-th token.
+// Factors of one group of 32 tokens, written by the pass before in the operands' layout.
+struct Group {
+  uint16_t a[2][64][8];   // dX's operand of each 16 tokens: lane, k
+  uint16_t b[3][64][8];   // dw's operand of each part of P: lane (16 q + j), kk
+  float c[32];            // the factor of x; NO_PART for a token that takes no part
+};
+constexpr uint32_t NO_PART = 0x80000000u;  // -0; a token that does take part has +0
+constexpr int GT = 32;
 
-// One workgroup per token: r from the whole row, then the token's factors. A token
-// whose dscore is all zero takes part in nothing: its row is not read.
-__global__ __launch_bounds__(256) void router_factors_kernel(const bf16_t* __restrict__ X, int64_t NC, int E,
-                                                             const float* __restrict__ score,
-                                                             const float* __restrict__ dscore, float* __restrict__ P) {
+__device__ __forceinline__ uint16_t bf_part(float& v) {  // the leading bfloat16 of v, taken off
+  const uint32_t h = f2bf(v);
+  v -= bf2f(h);
+  return (uint16_t)h;
+}
+
+// One workgroup per token (and for the places behind the last one, which are cleared):
+// r from the whole row, then the token's factors. A token whose dscore is all zero takes
+// part in nothing: its row is not read.
+__global__ __launch_bounds__(256) void router_factors_kernel(const bf16_t* __restrict__ X, int64_t T, int64_t NC,
+                                                             int E, const float* __restrict__ score,
+                                                             const float* __restrict__ dscore,
+                                                             Group* __restrict__ G) {
   __shared__ float red[4];
   const int64_t t = blockIdx.x;
   const int j = threadIdx.x;
   bool any = false;
-  for (int i = 0; i < E; ++i) any |= dscore[t * E + i] != 0.f;
-  float* out = P + t * PW;
-  if (!any) {
-    if (j < PW) out[j] = j == PW - 1 ? __uint_as_float(NO_PART) : 0.f;
-    return;
-  }
-  const bf16_t* x = X + t * NC;
+  if (t < T)
+    for (int i = 0; i < E; ++i) any |= dscore[t * E + i] != 0.f;
   float ss = 0.f;
-  for (int64_t c = (int64_t)threadIdx.x * 8; c < NC; c += 2048) {
-    float v[8];
-    load8(x + c, v);
+  if (any) {
+    const bf16_t* x = X + t * NC;
+    for (int64_t c = (int64_t)threadIdx.x * 8; c < NC; c += 2048) {
+      float v[8];
+      load8(x + c, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
-  }
-  ss = block_sum(ss, red);
-  if (j < 64) {
-    float dz = 0.f, along = 0.f;
-    if (j < E) {
-      const float s = score[t * E + j];
-      dz = dscore[t * E + j] * (s * (1.f - s));
-      along = dz == 0.f ? 0.f : dz * (logf(s) - logf(1.f - s));  // z from its sigmoid
+      for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
     }
-    along = row16_sum(along);  // E <= 15: one row of 16 lanes
-    const float ms = ss / (float)NC;
-    const float inv_r = ms == 0.f ? 0.f : 1.f / sqrtf(ms);
-    if (j < PW - 1) out[j] = dz * inv_r;
-    else if (j == PW - 1) out[j] = along * inv_r * inv_r / (float)NC + 0.f;  // -0 + 0 = +0
+    ss = block_sum(ss, red);
   }
+  if (j >= 16) return;
+  float dz = 0.f, along = 0.f;
+  if (any && j < E) {
+    const float s = score[t * E + j];
+    dz = dscore[t * E + j] * (s * (1.f - s));
+    along = dz == 0.f ? 0.f : dz * (logf(s) - logf(1.f - s));  // z from its sigmoid
+  }
+  along = row16_sum(along);
+  const float ms = ss / (float)NC;
+  const float inv_r = ms == 0.f ? 0.f : 1.f / sqrtf(ms);
+  float p = dz * inv_r;
+  Group& g = G[t / GT];
+  const int tau = (int)(t % GT), tile = tau / 16, m = tau % 16, q = m / 4, kk = 4 * tile + m % 4;
+  uint16_t part[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    part[i] = bf_part(p);
+    g.b[i][16 * q + j][kk] = part[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) g.a[tile][16 * (2 * i + j / 8) + m][j % 8] = part[i];
+  if (j == 0) g.c[tau] = any ? along * inv_r * inv_r / (float)NC + 0.f : __uint_as_float(NO_PART);  // -0 + 0 = +0
 }
 
-// dX_out = dX_in + P w - c x and this split's part of dw = sum_t x P. Each thread
-// owns 4 of the N*C channels and keeps their rows of w and dw in registers; the
-// token's 16 factors are the same for the whole wave (scalar registers).
+typedef __bf16 bfv8 __attribute__((ext_vector_type(8)));
+typedef float fv4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ bfv8 as_bf8(uint4 v) { return __builtin_bit_cast(bfv8, v); }
+
+// 8 weights of one channel, column j0 on, their bfloat16 parts packed.
 template <int E>
-__global__ __launch_bounds__(256) void router_apply_kernel(const bf16_t* __restrict__ X, int64_t T, int64_t NC,
-                                                           const float* __restrict__ w,
-                                                           const float* __restrict__ P, const bf16_t* dX_in,
-                                                           bf16_t* dX_out, float* __restrict__ part) {
-  typedef uint32_t u2 __attribute__((ext_vector_type(2)));
-  const int64_t c0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+__device__ __forceinline__ void weight_parts(const float* __restrict__ w, int64_t ch, int j0, uint4& hi, uint4& lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a = j0 + 2 * i < E ? w[ch * E + j0 + 2 * i] : 0.f, b = j0 + 2 * i + 1 < E ? w[ch * E + j0 + 2 * i + 1] : 0.f;
+    const uint32_t ha = bf_part(a), hb = bf_part(b);
+    h[i] = ha | hb << 16;
+    l[i] = (uint32_t)bf_part(a) | (uint32_t)bf_part(b) << 16;
+  }
+  hi = make_uint4(h[0], h[1], h[2], h[3]);
+  lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
+template <int E>
+__global__ __launch_bounds__(256, 3) void router_apply_kernel(const bf16_t* __restrict__ X, int64_t T, int64_t NC,
+                                                              const float* __restrict__ w,
+                                                              const Group* __restrict__ G, const bf16_t* dX_in,
+                                                              bf16_t* dX_out, float* __restrict__ part) {
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = lane & 15, q = lane >> 4;
+  const int64_t c0 = (int64_t)blockIdx.x * 256 + wv * 64;  // this wave's channels
   if (c0 >= NC) return;
-  float wv[4][E], dw[4][E];
+  const bool in = c0 + 4 * m < NC;  // NC is a multiple of 32; lanes past it read channel c0 on and store nothing
+  const uint32_t ch = in ? 4 * m : 0;
+  uint4 wh[4], wl[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
+  for (int e = 0; e < 4; ++e) weight_parts<E>(w, c0 + ch + e, 8 * (q & 1), wh[e], wl[e]);
+  fv4 dw[4];
 #pragma unroll
-    for (int j = 0; j < E; ++j) {
-      wv[e][j] = w[(c0 + e) * E + j];
-      dw[e][j] = 0.f;
+  for (int e = 0; e < 4; ++e) dw[e] = fv4{0.f, 0.f, 0.f, 0.f};
+  const uint32_t row = (uint32_t)NC;
+
+  for (int64_t g = blockIdx.y; g * GT < T; g += gridDim.y) {
+    const int64_t t0 = g * GT;
+    const int live = (int)min((int64_t)GT, T - t0);
+    const bf16_t* xb = X + t0 * NC + c0;
+    const bf16_t* db = dX_in + t0 * NC + c0;
+    u2 x[8], d[8];
+    uint32_t off[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int tau = 16 * (i >> 2) + 4 * q + (i & 3);
+      off[i] = (uint32_t)min(tau, live - 1) * row + ch;  // past the end: the last token's row again
+      x[i] = __builtin_nontemporal_load(reinterpret_cast<const u2*>(xb + off[i]));
     }
-  // the splits take turns: what runs at once reads neighbouring rows (845 us against 865
-  // with a range of tokens each)
-#pragma unroll 4
-  for (int64_t t = blockIdx.y; t < T; t += gridDim.y) {
-    u2 xq = __builtin_nontemporal_load(reinterpret_cast<const u2*>(X + t * NC + c0));
-    const u2 dq = __builtin_nontemporal_load(reinterpret_cast<const u2*>(dX_in + t * NC + c0));
-    const float* f = P + t * PW;
-    if (__float_as_uint(f[PW - 1]) == NO_PART) xq = u2{0u, 0u};  // such a token may hold anything
-    const float x[4] = {__uint_as_float(xq.x << 16), __uint_as_float(xq.x & 0xffff0000u),
-                        __uint_as_float(xq.y << 16), __uint_as_float(xq.y & 0xffff0000u)};
-    float o[4] = {__uint_as_float(dq.x << 16), __uint_as_float(dq.x & 0xffff0000u), __uint_as_float(dq.y << 16),
-                  __uint_as_float(dq.y & 0xffff0000u)};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) d[i] = __builtin_nontemporal_load(reinterpret_cast<const u2*>(db + off[i]));
+    const Group& f = G[g];
+    uint4 pa[2], pb[3];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) pa[i] = reinterpret_cast<const uint4*>(f.a[i])[lane];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) pb[i] = reinterpret_cast<const uint4*>(f.b[i])[lane];
+    float c[8];
+    {
+      const float4 u = reinterpret_cast<const float4*>(f.c)[q], v = reinterpret_cast<const float4*>(f.c)[4 + q];
+      c[0] = u.x; c[1] = u.y; c[2] = u.z; c[3] = u.w;
+      c[4] = v.x; c[5] = v.y; c[6] = v.z; c[7] = v.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (__float_as_uint(c[i]) == NO_PART) x[i] = u2{0u, 0u};  // such a token may hold anything
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float s = -f[PW - 1] * x[e];
+      uint32_t k[4];
 #pragma unroll
-      for (int j = 0; j < E; ++j) {
-        s += f[j] * wv[e][j];
-        dw[e][j] += f[j] * x[e];
+      for (int i = 0; i < 4; ++i) {  // channel e of tokens 2 i, 2 i + 1
+        const uint32_t u = e < 2 ? x[2 * i].x : x[2 * i].y, v = e < 2 ? x[2 * i + 1].x : x[2 * i + 1].y;
+        k[i] = (e & 1) ? __builtin_amdgcn_perm(v, u, 0x07060302) : __builtin_amdgcn_perm(v, u, 0x05040100);
       }
-      o[e] += s;
+      const bfv8 xa = as_bf8(make_uint4(k[0], k[1], k[2], k[3]));
+#pragma unroll
+      for (int i = 0; i < 3; ++i) dw[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xa, as_bf8(pb[i]), dw[e], 0, 0, 0);
     }
-    __builtin_nontemporal_store(u2{pack_bf2_hw(o[0], o[1]), pack_bf2_hw(o[2], o[3])},
-                                reinterpret_cast<u2*>(dX_out + t * NC + c0));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // 16 tokens each
+      fv4 s[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf8(pa[h]), as_bf8(wl[e]), fv4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+        s[e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf8(pa[h]), as_bf8(wh[e]), s[e], 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const u2 xq = x[4 * h + i], dq = d[4 * h + i];
+        const float cf = c[4 * h + i];
+        const float o0 = __uint_as_float(dq.x << 16) + (s[0][i] - cf * __uint_as_float(xq.x << 16));
+        const float o1 = __uint_as_float(dq.x & 0xffff0000u) + (s[1][i] - cf * __uint_as_float(xq.x & 0xffff0000u));
+        const float o2 = __uint_as_float(dq.y << 16) + (s[2][i] - cf * __uint_as_float(xq.y << 16));
+        const float o3 = __uint_as_float(dq.y & 0xffff0000u) + (s[3][i] - cf * __uint_as_float(xq.y & 0xffff0000u));
+        if (in && 16 * h + 4 * q + i < live)
+          __builtin_nontemporal_store(u2{pack_bf2_hw(o0, o1), pack_bf2_hw(o2, o3)},
+                                      reinterpret_cast<u2*>(dX_out + t0 * NC + c0 + off[4 * h + i]));
+      }
+    }
   }
+  // D row 4 q + i, column m: channel 4 (4 q + i) + e, j = m
   float* p = part + ((int64_t)blockIdx.y * NC + c0) * E;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
 #pragma unroll
-    for (int j = 0; j < E; ++j) p[e * E + j] = dw[e][j];
+    for (int i = 0; i < 4; ++i) {
+      const int cc = 4 * (4 * q + i) + e;
+      if (m < E && c0 + cc < NC) p[(int64_t)cc * E + m] = dw[e][i];
+    }
 }
 
 __global__ __launch_bounds__(256) void split_sum_kernel(const float* __restrict__ part, int64_t n, int splits,
@@ -277,18 +370,17 @@ __global__ __launch_bounds__(256) void split_sum_kernel(const float* __restrict_
   out[i] = s;
 }
 
-// Token splits of the apply pass: one round of the workgroups that are resident at once
-// (four a CU, three where 15 columns take more registers; 865 us for one round of 1,024
-// against 921 for 768 at N = 16, C = 4096, T = 8192), and 16 tokens at least in each (a
-// split writes its part of dw once: 24 us at N = 8, C = 512, T = 1021 against 29 with 32
-// and 28 with 8).
-int64_t router_splits(int64_t T, int64_t NC, int E) {
-  const int64_t blocks = (NC + 1023) / 1024;
-  int64_t s = (E < 15 ? 1024 : 768) / blocks;
-  const int64_t most = (T + 15) / 16;
+// Token splits of the apply pass: one round of the workgroups that are resident at
+// once, three a CU.
+int64_t router_splits(int64_t T, int64_t NC) {
+  const int64_t blocks = (NC + 255) / 256;
+  int64_t s = 768 / blocks;
+  const int64_t most = (T + GT - 1) / GT;
   if (s > most) s = most;
   return s < 1 ? 1 : s;
 }
+
+inline int64_t router_groups(int64_t T) { return (T + GT - 1) / GT; }
 
 inline int64_t al256(int64_t b) { return (b + 255) & ~(int64_t)255; }
 
@@ -320,10 +412,10 @@ hipError_t balance_go(const float* score, const int32_t* idx, const uint8_t* mas
 }
 
 template <int E>
-void router_apply(const void* X, int64_t T, int64_t NC, int64_t splits, const float* w, const float* P,
+void router_apply(const void* X, int64_t T, int64_t NC, int64_t splits, const float* w, const Group* G,
                   const void* dX_in, void* dX_out, float* part, hipStream_t st) {
-  hipLaunchKernelGGL((router_apply_kernel<E>), dim3((unsigned)((NC + 1023) / 1024), (unsigned)splits), dim3(256), 0, st,
-                     (const bf16_t*)X, T, NC, w, P, (const bf16_t*)dX_in, (bf16_t*)dX_out, part);
+  hipLaunchKernelGGL((router_apply_kernel<E>), dim3((unsigned)((NC + 255) / 256), (unsigned)splits), dim3(256), 0, st,
+                     (const bf16_t*)X, T, NC, w, G, (const bf16_t*)dX_in, (bf16_t*)dX_out, part);
 }
 
 }  // namespace
@@ -359,26 +451,26 @@ hipError_t launch_balance_backward(const float* score, const int32_t* count, con
 int64_t router_backward_ws_bytes(int64_t T, int N, int64_t C, int m) {
   if (T == 0) return 0;
   const int64_t NC = (int64_t)N * C;
-  return al256(T * PW * 4) + al256(router_splits(T, NC, N - m) * NC * (N - m) * 4);
+  return al256(router_groups(T) * sizeof(Group)) + al256(router_splits(T, NC) * NC * (N - m) * 4);
 }
 
 hipError_t launch_router_backward(const void* X, int64_t T, int N, int64_t C, int m, const float* w,
                                   const float* score, const float* dscore, const void* dX_in, void* dX_out, float* dw,
                                   void* ws, hipStream_t st) {
   const int E = N - m;
-  const int64_t NC = (int64_t)N * C, splits = router_splits(T, NC, E);
-  float* P = (float*)ws;
-  float* part = (float*)((char*)ws + al256(T * PW * 4));
+  const int64_t NC = (int64_t)N * C, splits = router_splits(T, NC);
+  Group* G = (Group*)ws;
+  float* part = (float*)((char*)ws + al256(router_groups(T) * sizeof(Group)));
   const int64_t n = NC * E;
   if (T == 0) {
     hipLaunchKernelGGL(split_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, n, 0, dw);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL(router_factors_kernel, dim3((unsigned)T), dim3(256), 0, st, (const bf16_t*)X, NC, E, score,
-                     dscore, P);
+  hipLaunchKernelGGL(router_factors_kernel, dim3((unsigned)(router_groups(T) * GT)), dim3(256), 0, st,
+                     (const bf16_t*)X, T, NC, E, score, dscore, G);
   switch (E) {
 #define HC_ROUTER_CASE(e) \
-  case e: router_apply<e>(X, T, NC, splits, w, P, dX_in, dX_out, part, st); break;
+  case e: router_apply<e>(X, T, NC, splits, w, G, dX_in, dX_out, part, st); break;
     HC_ROUTER_CASE(1) HC_ROUTER_CASE(2) HC_ROUTER_CASE(3) HC_ROUTER_CASE(4) HC_ROUTER_CASE(5)
     HC_ROUTER_CASE(6) HC_ROUTER_CASE(7) HC_ROUTER_CASE(8) HC_ROUTER_CASE(9) HC_ROUTER_CASE(10)
     HC_ROUTER_CASE(11) HC_ROUTER_CASE(12) HC_ROUTER_CASE(13) HC_ROUTER_CASE(14) HC_ROUTER_CASE(15)

@@ -434,7 +434,10 @@ def test_router_backward(T, N, m, C):
     mag = np.zeros((T, N * C))
     mag[live] = (dz / rl) @ np.abs(w64).T * (kr + E + 4) + np.abs(xl) / (rl * rl * N * C) * (
         (dz * (z + 1)).sum(1, keepdims=True) * (2 * kr + 16))
-    tol = U * (mag.reshape(T, N, C) + 4 * np.abs(dX64))
+    # dX's product takes P and w in two bfloat16 parts each: what is left of either is at most 2^-8 of 2^-8 of it
+    split = np.zeros((T, N * C))
+    split[live] = 2 * 2.0 ** -16 * ((dz / rl) @ np.abs(w64).T)
+    tol = U * (mag.reshape(T, N, C) + 4 * np.abs(dX64)) + split.reshape(T, N, C)
     within("dX", down(out), ref, tol + P["bf16"] * (np.abs(ref) + tol))
     wmag = np.abs(xl).T @ (dz / rl)
     within("dw", down(dw), rdw, (kr + 4 + T) * U * wmag + 1e-37)
