@@ -10,9 +10,9 @@
 //
 // Two forms. Up to SHORT tokens one thread walks the whole sequence of its channels.
 // Longer ones run in one pass over the data: a workgroup holds a tile of tokens in
-// registers, publishes the tile's composed map, composes the maps of the tiles
-// before it while they are published (or takes a finished state, published as a
-// constant map, where one is there), and walks its tokens again from registers.
+// registers, publishes the tile's composed map, joins the maps of the few tiles before
+// it to the state that an earlier group of tiles left, and walks its tokens again from
+// registers.
 // Tiles are taken from a counter in walk order, so that every tile waited for
 // belongs to a workgroup that already runs and waits for earlier tiles only.
 #include "hc_device.h"
@@ -192,16 +192,14 @@ __global__ __launch_bounds__(256) void scan_short_kernel(ScanArgs a) {
 
 // A published map is one 64-bit word per channel, so no word is ever seen half
 // written: A in the low half, H in the high half. All ones: not there yet (a value
-// of that pattern, a NaN, is published as another NaN). A = -0: a constant map, the
-// finished state behind the tile (a is never negative, so no composed map has it).
-constexpr uint32_t DONE = 0x80000000u;
+// of that pattern, a NaN, is published as another NaN).
 constexpr uint64_t ABSENT = ~0ull;
 
-__device__ __forceinline__ uint64_t word_of(uint32_t A, float H) {
+__device__ __forceinline__ uint64_t word_of(float A, float H) {
+  const uint32_t a = __float_as_uint(A);
   uint32_t h = __float_as_uint(H);
   if (h == 0xffffffffu) h = 0x7fc00000u;
-  if (A == 0xffffffffu) A = 0x7fc00000u;
-  return (uint64_t)h << 32 | A;
+  return (uint64_t)h << 32 | a;
 }
 
 __device__ __forceinline__ void publish(uint64_t* p, uint64_t w) {
@@ -337,59 +335,59 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
 
   uint64_t* words = (uint64_t*)((char*)a.ws + 256) + (b * nct + ct) * TILE_C + lane * V;  // one per lane channel, inside the row or not
   const int64_t wstep = a.B * nct * TILE_C;  // from one tile of the walk to the next
-  if (!ONE && wv == WAVES - 1 && j > 0 && j + 1 < ntile)
+  // The state before the tile. Tiles are joined in groups of WAVES, always in the same
+  // order (what is ready first makes no difference to a sum's rounding): from the state
+  // that the group before left, through the maps of the group's earlier tiles. Each wave
+  // fetches one of these words; the group's last tile publishes the state, the others
+  // their maps.
+  const uint32_t gj = j % WAVES, g0 = j - gj;  // place in the group, its first tile
+  const bool leaves = !ONE && wv == WAVES - 1 && j + 1 < ntile;
+  if (leaves && gj < WAVES - 1)
 #pragma unroll
-    for (int e = 0; e < V; ++e) publish(words + (int64_t)j * wstep + e, word_of(__float_as_uint(tA[e]), tH[e]));
-
-  // the state before the tile: compose backwards until a constant map is met
-  float init[V] = {0.f, 0.f};
+    for (int e = 0; e < V; ++e) publish(words + (int64_t)j * wstep + e, word_of(tA[e], tH[e]));
+  float s[V] = {0.f, 0.f};
   const float* first = BWD ? a.dlast : a.state0;
-  if (first) ld2f<VEC>(first + st0 + lo, cnt, init);
-  float s[V];
   if (ONE || j == 0) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) s[e] = init[e];
+    if (first) ld2f<VEC>(first + st0 + lo, cnt, s);
   } else {
-    float bA[V] = {1.f, 1.f}, bH[V] = {0.f, 0.f};
-    bool done[V] = {false, false};
-    for (int64_t p0 = (int64_t)j - 1;; p0 -= WAVES) {
-      const int64_t p = p0 - wv;  // each wave fetches one of the next WAVES tiles
+    // wave w: the map of the group's w-th tile; the last wave: the state before the group
+    const bool state = wv == WAVES - 1;
+    float wa[V] = {1.f, 1.f}, wh[V] = {0.f, 0.f};
+    if (state && g0 == 0) {
+      if (first) ld2f<VEC>(first + st0 + lo, cnt, wh);
+    } else if (state || (uint32_t)wv < gj) {
+      const uint64_t* p = words + (int64_t)(state ? g0 - 1 : g0 + wv) * wstep;
+      uint64_t w[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) w[e] = peek(p + e);
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        uint32_t wa = DONE;
-        float wh = init[e];
-        if (p >= 0) {
-          const uint64_t w = await(words + p * wstep + e);
-          wa = (uint32_t)w;
-          wh = __uint_as_float((uint32_t)(w >> 32));
-        }
-        lA[wv][lane * V + e] = __uint_as_float(wa);
-        lH[wv][lane * V + e] = wh;
+        if (w[e] == ABSENT) w[e] = await(p + e);
+        wa[e] = __uint_as_float((uint32_t)w[e]);
+        wh[e] = __uint_as_float((uint32_t)(w[e] >> 32));
       }
-      lds_barrier();
-      bool more = false;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-#pragma unroll BWD ? 2 : WAVES
-        for (int w = 0; w < WAVES; ++w) {
-          const float wa = lA[w][lane * V + e], wh = lH[w][lane * V + e];
-          if (!done[e]) {
-            bH[e] += bA[e] * wh;
-            bA[e] *= wa;
-            done[e] = __float_as_uint(wa) == DONE;
-          }
-        }
-        more |= !done[e];
-      }
-      if (!__any(more)) break;  // the same in every wave: all compose the same maps
-      lds_barrier();            // lA, lH are read
     }
 #pragma unroll
-    for (int e = 0; e < V; ++e) s[e] = bH[e];
-  }
-  if (!ONE && wv == WAVES - 1 && j + 1 < ntile)
+    for (int e = 0; e < V; ++e) {
+      lA[wv][lane * V + e] = wa[e];
+      lH[wv][lane * V + e] = wh[e];
+    }
+    lds_barrier();
 #pragma unroll
-    for (int e = 0; e < V; ++e) publish(words + (int64_t)j * wstep + e, word_of(DONE, tA[e] * s[e] + tH[e]));
+    for (int e = 0; e < V; ++e) s[e] = lH[WAVES - 1][lane * V + e];
+#pragma unroll BWD ? 2 : WAVES - 1
+    for (int w = 0; w < WAVES - 1; ++w)
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if ((uint32_t)w < gj) s[e] = lA[w][lane * V + e] * s[e] + lH[w][lane * V + e];
+  }
+  if (leaves && gj == WAVES - 1)
+#pragma unroll
+    for (int e = 0; e < V; ++e) publish(words + (int64_t)j * wstep + e, word_of(0.f, tA[e] * s[e] + tH[e]));
+
+  // what the waves before this one make of it
+#pragma unroll
+  for (int e = 0; e < V; ++e) s[e] = pA[e] * s[e] + pH[e];
 
   // The backward's walk opens q and the rows again: without this the compiler keeps what
   // it made of them, four registers for one.
@@ -403,8 +401,6 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
     }
 
   // the walk itself
-#pragma unroll
-  for (int e = 0; e < V; ++e) s[e] = pA[e] * s[e] + pH[e];
 #pragma unroll
   for (int k = 0; k < LW; ++k) {
     const int64_t t = HC_TOKEN(k);
