@@ -8,6 +8,7 @@
 #include "hc.h"
 #include "hc_launch.h"
 #include "hc_fast.h"
+#include "hc_sublayer.h"
 
 namespace {
 

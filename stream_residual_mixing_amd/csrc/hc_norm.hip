@@ -4,8 +4,8 @@
 //   codes with a scale per row or per group of 32, 64 or 128 channels.
 // Each row is read once and stays in float32 registers between the sum of squares
 // and the outputs, so the passes are bound by HBM traffic.
-#include "hc_device.h"
-#include "hc_launch.h"
+#include "hc_sublayer.h"
+#include "hc_sublayer_device.h"
 
 namespace hc {
 
@@ -105,13 +105,6 @@ __device__ __forceinline__ void load_weight(const float* w, int64_t C, int nt, i
       load8_tail(w + c0, piece_count(c0, C), out[it]);
     }
   }
-}
-
-// A barrier that orders LDS alone: the next row's loads stay on their way.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // Sums of NV values over one row's threads, the same in each; `red` is this row parity's

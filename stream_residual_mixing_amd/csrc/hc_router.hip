@@ -4,8 +4,8 @@
 //   set holds stream i, p_tj = s_tj / sum_j s_tj, P_j = mean_t p_tj,
 //   f_j = E / ((k - m) n_b) count_{m+j};  loss = coef / B sum_b sum_j f_j P_j.
 //   router: z_t = (vec X_t @ W) / r_t, s = sigmoid(z), r = ||vec X|| / sqrt(NC).
-#include "hc_device.h"
-#include "hc_launch.h"
+#include "hc_sublayer.h"
+#include "hc_sublayer_device.h"
 
 namespace hc {
 

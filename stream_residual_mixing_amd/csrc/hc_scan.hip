@@ -15,8 +15,8 @@
 // registers.
 // Tiles are taken from a counter in walk order, so that every tile waited for
 // belongs to a workgroup that already runs and waits for earlier tiles only.
-#include "hc_device.h"
-#include "hc_launch.h"
+#include "hc_sublayer.h"
+#include "hc_sublayer_device.h"
 
 namespace hc {
 
@@ -229,13 +229,6 @@ __global__ __launch_bounds__(256) void scan_clear_kernel(uint4* ws, int64_t n16)
   if (i >= n16) return;
   const uint32_t v = i < 16 ? 0u : 0xffffffffu;  // 256 bytes of counter, then the words
   ws[i] = make_uint4(v, v, v, v);
-}
-
-// A barrier that orders LDS alone: the rows that are on their way stay on their way.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 __device__ __forceinline__ void forget(float& v) { asm volatile("" : "+v"(v)); }

@@ -298,3 +298,62 @@ def test_routed_step_with_balance_loss_trains_its_router():
         l2 = 0.5 * (f * (s2 / s2.sum(1, keepdim=True)).view(B, S, E).mean(1)).sum() / B
     slope = float((Wr.grad * dw.cpu().double()).sum()) * step
     assert abs(float(loss - l2) - slope) < 0.05 * slope
+
+
+def _raises(exc, fn, *a, **k):
+    with pytest.raises(exc):
+        fn(*a, **k)
+
+
+def test_binding_refuses_wrong_arguments():
+    note("binding validation: norm, scan and router calls")
+    i = _inputs(14, S=5, C=64)
+    x, w, X = i["x"], i["w"], i["X"]
+    e4 = torch.float8_e4m3fn
+    _raises(ValueError, hc.hc_rms_norm, x.view(2, 5, 64), w)
+    _raises(ValueError, hc.hc_rms_norm, x, w[:-1])
+    _raises(TypeError, hc.hc_rms_norm, x, w.bfloat16())
+    _raises(TypeError, hc.hc_rms_norm, x.half(), w)
+    _raises(ValueError, hc.hc_rms_norm, x.t(), None)
+    _raises(ValueError, hc.hc_rms_norm, x, w, residual=i["r"][:4])
+    _raises(TypeError, hc.hc_rms_norm, x, w, residual=i["r"].float())
+    _raises(ValueError, hc.hc_rms_norm, x, w, s_out=torch.empty_like(x))  # no residual
+    _raises(ValueError, hc.hc_rms_norm, x, w, group=32)  # no 8-bit output
+    _raises(ValueError, hc.hc_rms_norm, x, w, quant=e4, group=48)
+    _raises(TypeError, hc.hc_rms_norm, x, w, quant=torch.float8_e5m2)
+    _raises(ValueError, hc.hc_rms_norm, x, w, quant=e4, out=(None, torch.empty(10, 2, device="cuda")))
+    _raises(TypeError, hc.hc_rms_norm, x, w, quant=e4, out=(torch.empty_like(x), None))
+    _raises(hc.HCError, hc.hc_rms_norm, x, w, -1.0)
+    _raises(hc.HCError, hc.hc_rms_norm, x, w, out=(x, None))  # y over x
+    _raises(hc.HCError, hc.hc_rms_norm, torch.zeros(1, 16392, device="cuda"))
+    _raises(ValueError, hc.hc_pre_norm, X, i["h"][:, :4].contiguous(), w)
+    _raises(ValueError, hc.hc_pre_norm, X, i["h"], w, F_in_out=torch.empty(5, 64, dtype=x.dtype, device="cuda"))
+    _raises(ValueError, hc.hc_rms_norm_backward, x, w, x[:3])
+    _raises(ValueError, hc.hc_rms_norm_backward, x, w, x, ds=x[:, :32].contiguous())
+    _raises(hc.HCError, hc.hc_rms_norm_backward, x, w, x, out=(x, None))
+    xs = x.view(2, 5, 64)
+    _raises(ValueError, hc.hc_gated_scan, x, i["gate"])
+    _raises(ValueError, hc.hc_gated_scan, xs, i["gate"][:, :4].contiguous())
+    _raises(TypeError, hc.hc_gated_scan, xs, i["gate"].float())
+    _raises(ValueError, hc.hc_gated_scan, xs, i["gate"], i["h0"][:1])
+    _raises(TypeError, hc.hc_gated_scan, xs, i["gate"], lengths=i["L"].long())
+    _raises(ValueError, hc.hc_gated_scan, xs, i["gate"], lengths=i["L"][:1])
+    _raises(hc.HCError, hc.hc_gated_scan, xs, i["gate"], out=(xs, None))
+    _raises(ValueError, hc.hc_gated_scan_backward, xs, i["gate"], xs, i["dy"][:1])
+    _raises(hc.HCError, hc.hc_gated_scan_backward, xs, i["gate"], xs, i["dy"], out=(i["dy"], None, None))
+    sc, idx = i["score"], i["idx"]
+    _raises(ValueError, hc.xhc_balance_loss, sc, idx, 2, 6)
+    _raises(ValueError, hc.xhc_balance_loss, sc, idx[:4], 2, 5)
+    _raises(TypeError, hc.xhc_balance_loss, sc, idx.long(), 2, 5)
+    _raises(ValueError, hc.xhc_balance_loss, sc, idx, 2, 5, mask=torch.ones(3, dtype=torch.bool, device="cuda"))
+    _raises(hc.HCError, hc.xhc_balance_loss, sc, idx[:, :2].contiguous(), 2, 5)  # k = m: nothing is chosen
+    b = hc.xhc_balance_loss(sc, idx, 2, 5)
+    _raises(ValueError, hc.xhc_balance_loss_backward, sc, b["count"][:1], b["tokens"], 4, 2, 5)
+    _raises(ValueError, hc.xhc_balance_loss_backward, sc, b["count"], b["tokens"], 4, 2, 5,
+            dloss=torch.ones(2, device="cuda"))
+    ds = torch.zeros_like(sc)
+    _raises(ValueError, hc.xhc_router_backward, X, i["wr"][:-1], sc, ds, i["dX"])
+    _raises(ValueError, hc.xhc_router_backward, X, i["wr"], sc, ds[:3], i["dX"])
+    _raises(TypeError, hc.xhc_router_backward, X.float(), i["wr"], sc, ds, i["dX"].float())
+    _raises(hc.HCError, hc.xhc_router_backward, X, i["wr"], sc, ds, X)  # in place on the state itself
+    assert torch.isfinite(hc.xhc_balance_loss(sc, idx, 2, 5)["loss"])  # a valid call after the refusals
