@@ -1080,7 +1080,8 @@ def xhc_balance_loss(score, idx, B, S, *, m=2, coef=1.0, mask=None, out=None, wo
     """Balance loss of the router over B sequences of S tokens: score [B*S, N-m] and idx [B*S, k] as
     xhc_pre wrote them; mask [B*S] (bool): the tokens that take part. Returns dict(loss [], count
     [B, N] int32, tokens [B] int32, mean_p [B, N-m]); out = these four, in this order."""
-    T = int(B) * int(S)
+    B, S, m = int(B), int(S), int(m)
+    T = B * S
     score, E, N = _scores(score, T, m)
     dev = score.device
     idx = _i32(idx, "idx", device=dev)
@@ -1107,7 +1108,8 @@ def xhc_balance_loss_backward(score, count, tokens, k, B, S, *, coef=1.0, dloss=
                               stream=None):
     """dscore [B*S, N-m] of xhc_balance_loss (count, tokens: its outputs; k: streams per token); dloss: the
     loss's gradient, one float32 on the device (None: 1)."""
-    T = int(B) * int(S)
+    B, S = int(B), int(S)
+    T = B * S
     score, E, _ = _scores(score, T, 0)
     dev = score.device
     count = _i32(count, "count", device=dev)

@@ -305,6 +305,19 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
       if (!BWD) kb[BWD ? 0 : k][e] = bb;
     }
   }
+  // The caller's state is read here and nowhere else, by the walk's first wave, which
+  // makes its map constant: whoever writes the last state (it may be the same array) has
+  // waited for that map or for one composed from it.
+  float init[V] = {0.f, 0.f};
+  const float* first = BWD ? a.dlast : a.state0;
+  if (i0 == 0 && first) {
+    ld2f<VEC>(first + st0 + lo, cnt, init);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      H[e] = A[e] * init[e] + H[e];
+      A[e] = 0.f;
+    }
+  }
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     sA[wv][lane * V + e] = A[e];
@@ -326,29 +339,25 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
       tA[e] *= wa;
     }
 
-  uint64_t* words = (uint64_t*)((char*)a.ws + 256) + (b * nct + ct) * TILE_C + lane * V;  // one per lane channel, inside the row or not
+  // one word per lane's channel, inside the row or not
+  uint64_t* words = (uint64_t*)((char*)a.ws + 256) + (b * nct + ct) * TILE_C + lane * V;
   const int64_t wstep = a.B * nct * TILE_C;  // from one tile of the walk to the next
   // The state before the tile. Tiles are joined in groups of WAVES, always in the same
   // order (what is ready first makes no difference to a sum's rounding): from the state
-  // that the group before left, through the maps of the group's earlier tiles. Each wave
-  // fetches one of these words; the group's last tile publishes the state, the others
-  // their maps.
+  // that the group before left, through the maps of the group's earlier tiles (in the
+  // first group, the first tile's map is constant). Each wave fetches one of these words;
+  // the group's last tile publishes the state, the others their maps.
   const uint32_t gj = j % WAVES, g0 = j - gj;  // place in the group, its first tile
   const bool leaves = !ONE && wv == WAVES - 1 && j + 1 < ntile;
   if (leaves && gj < WAVES - 1)
 #pragma unroll
     for (int e = 0; e < V; ++e) publish(words + (int64_t)j * wstep + e, word_of(tA[e], tH[e]));
   float s[V] = {0.f, 0.f};
-  const float* first = BWD ? a.dlast : a.state0;
-  if (ONE || j == 0) {
-    if (first) ld2f<VEC>(first + st0 + lo, cnt, s);
-  } else {
+  if (!ONE && j > 0) {
     // wave w: the map of the group's w-th tile; the last wave: the state before the group
     const bool state = wv == WAVES - 1;
     float wa[V] = {1.f, 1.f}, wh[V] = {0.f, 0.f};
-    if (state && g0 == 0) {
-      if (first) ld2f<VEC>(first + st0 + lo, cnt, wh);
-    } else if (state || (uint32_t)wv < gj) {
+    if (state ? g0 > 0 : (uint32_t)wv < gj) {
       const uint64_t* p = words + (int64_t)(state ? g0 - 1 : g0 + wv) * wstep;
       uint64_t w[V];
 #pragma unroll
@@ -380,7 +389,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
 
   // what the waves before this one make of it
 #pragma unroll
-  for (int e = 0; e < V; ++e) s[e] = pA[e] * s[e] + pH[e];
+  for (int e = 0; e < V; ++e) s[e] = i0 == 0 ? init[e] : pA[e] * s[e] + pH[e];
 
   // The backward's walk opens q and the rows again: without this the compiler keeps what
   // it made of them, four registers for one.

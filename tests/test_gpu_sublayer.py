@@ -160,6 +160,16 @@ def test_norm_in_place_residual_and_given_outputs():
     assert torch.equal(sc, want["scale"])
 
 
+def test_norm_without_rows():
+    note("hc_rms_norm, hc_pre_norm and the backward with T = 0")
+    e = torch.empty(0, 64, device="cuda")
+    r = hc.hc_rms_norm(e, torch.ones(64, device="cuda"), residual=e, quant=_dt("e4m3"), group=32)
+    assert r["y"].shape == (0, 64) and r["s"].shape == (0, 64) and r["scale"].shape == (0, 2)
+    assert hc.hc_pre_norm(torch.empty(0, 4, 64, device="cuda"), torch.empty(0, 4, device="cuda"))["y"].shape == (0, 64)
+    dx, dw = hc.hc_rms_norm_backward(e, None, e)
+    assert dx.shape == (0, 64) and dw.shape == (64,) and not dw.any()
+
+
 def test_norm_unaligned_arrays():
     note("hc_rms_norm on arrays one element off a 16-byte address")
     for dt in ("bf16", "f32"):

@@ -139,6 +139,20 @@ def test_explicit_stream_keeps_its_workspace():
     _same(want, _step(i, stream=0), "default stream")
 
 
+@pytest.mark.parametrize("S", [1, 100, 129, 700, 1024, 1500, 9000])
+def test_scan_state_in_place(S):
+    note(f"scan with h_last written over h0, S={S}")
+    g = torch.Generator(device="cuda").manual_seed(S)
+    B, C = 3, 2050
+    x, gate = torch.randn(B, S, C, device="cuda", generator=g), 4 + torch.randn(B, S, C, device="cuda", generator=g)
+    h0 = 100 * torch.randn(B, C, device="cuda", generator=g)
+    y, last = hc.hc_gated_scan(x, gate, h0)
+    for _ in range(5):
+        state = h0.clone()
+        y2, l2 = hc.hc_gated_scan(x, gate, state, out=(None, state))
+        assert l2 is state and torch.equal(y2, y) and torch.equal(state, last)
+
+
 def test_batches_do_not_touch_each_other():
     note("scan: a sequence alone gives what it gives in a batch")
     g = torch.Generator(device="cuda").manual_seed(9)
