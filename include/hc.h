@@ -3,7 +3,9 @@
  *
  * The library computes one forward hyper-connection sublayer per token:
  * mHC's Sinkhorn-constrained n-stream residual mixing and xHC's routed,
- * augmented extension. Sources of the definitions:
+ * augmented extension, with their gradients; and beside the mixing the norm in
+ * front of the sublayer function, the gated linear recurrence of a state space
+ * block, and the training of xHC's router. Sources of the definitions:
  *   [mHC]   "mHC: Manifold-Constrained Hyper-Connections" (paper notes),
  *           Eq. 3, Eq. 6, section 4.2 (Eq. 7-9), section 4.3.1 (Eq. 10-19 and
  *           the F_pre / F_post,res kernels).
@@ -378,7 +380,8 @@ int xhc_route_pre(void* X, int dtype, int64_t T, int N, int64_t C, int k, int m,
  * the route is the mHC post/res write with maps formed from the active state
  * alone, so its backward follows the mHC one ([mHC] 4.3.1: the Sinkhorn backward
  * recomputes the iterates on chip; the maps are recomputed from X). The active
- * set is a discrete choice: it and the router weights receive no gradient.
+ * set is a discrete choice: it passes no gradient on (a loss on the router's
+ * scores trains its weights through xhc_router_backward).
  *   X [T, N, C]: the state both forward calls read, i.e. before xhc_route's
  *   in-place update (keep it, or its active rows, for the backward).
  *   xhc_route_backward (first; it does not need dF_in): dX [T, N, C] holds the

@@ -175,7 +175,7 @@ __global__ __launch_bounds__(256) void balance_backward_kernel(const float* __re
 // The apply pass multiplies on the matrix cores (v_mfma_f32_16x16x32_bf16), 32 tokens
 // and 64 channels of a wave at a time, so that the 2 E products per value of X hide
 // behind its memory traffic (on the vector units they took half as long as the traffic:
-// 845 against 7xx us at N = 16, C = 4096, T = 8192). X is bfloat16 as it is; the float32
+// 845 against 768 us at N = 16, C = 4096, T = 8192). X is bfloat16 as it is; the float32
 // factors P = dz / r and the weights are split into bfloat16 parts: P into three (24 bits,
 // all of it) for dw, and P and w into two each (16 bits) for dX, which is rounded to 8.
 // Lane 16 q + m of a wave holds channels 4 m .. 4 m + 3 of tokens 4 q + i and 16 + 4 q +
