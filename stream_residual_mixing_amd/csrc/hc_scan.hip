@@ -53,6 +53,8 @@ template <> struct Pair<float> {
     __builtin_nontemporal_store(f2{q.x, q.y}, reinterpret_cast<f2*>(p));
   }
   static __device__ __forceinline__ raw one(float e) { return make_float2(e, 0.f); }
+  static __device__ __forceinline__ raw zero() { return make_float2(0.f, 0.f); }
+  static __device__ __forceinline__ raw inf() { return make_float2(INFINITY, INFINITY); }
 };
 template <> struct Pair<bf16_t> {
   typedef uint32_t raw;
@@ -68,6 +70,8 @@ template <> struct Pair<bf16_t> {
     __builtin_nontemporal_store(q, reinterpret_cast<uint32_t*>(p));
   }
   static __device__ __forceinline__ raw one(bf16_t e) { return e; }
+  static __device__ __forceinline__ raw zero() { return 0u; }
+  static __device__ __forceinline__ raw inf() { return 0x7f807f80u; }
 };
 
 // OLD: the backward's arrays were written long before and are not kept in the caches
@@ -281,13 +285,23 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
     }
   }
 
+  // steps past the end and behind a sequence's length leave the state as it is: a = 1, b = 0
+  if (BWD ? i0 + LW > a.S || a.S - i0 > len : i0 + LW > len)
+#pragma unroll
+    for (int k = 0; k < LW; ++k) {
+      const int64_t t = HC_TOKEN(k);
+      if (t < 0 || t >= len) {
+        rg[k] = Pair<T>::inf();
+        if (BWD) rd[BWD ? k : 0] = Pair<T>::zero();
+        else rx[k] = Pair<T>::zero();
+      }
+    }
+
   // this wave's composed map; the forward keeps a and b, the backward the signed q
   float ka[LW][V], kb[BWD ? 1 : LW][V];
   float A[V] = {1.f, 1.f}, H[V] = {0.f, 0.f};
 #pragma unroll
   for (int k = 0; k < LW; ++k) {
-    const int64_t t = HC_TOKEN(k);
-    const bool live = t >= 0 && t < len;
     float g[V], x[V];
     Pair<T>::open(rg[k], g);
     Pair<T>::open(BWD ? rd[BWD ? k : 0] : rx[k], x);
@@ -296,9 +310,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
       const float q = gate_q(g[e]);
       float d, u;
       gate_au(q, d, u);
-      float bb = BWD ? d * x[e] : (tied ? u * x[e] : x[e]);
-      d = live ? d : 1.f;
-      bb = live ? bb : 0.f;
+      const float bb = BWD ? d * x[e] : (tied ? u * x[e] : x[e]);
       H[e] = d * H[e] + bb;
       A[e] *= d;
       ka[k][e] = BWD ? q : d;
