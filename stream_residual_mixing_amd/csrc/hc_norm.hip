@@ -3,7 +3,10 @@
 //   y = v * w / sqrt(mean_c v^2 + eps), stored in the stream dtype or as 8-bit
 //   codes with a scale per row or per group of 32, 64 or 128 channels.
 // Each row is read once and stays in float32 registers between the sum of squares
-// and the outputs, so the passes are bound by HBM traffic.
+// and the outputs, so the passes are bound by HBM traffic: 5.5 TB/s for 8,192 x 4,096
+// bfloat16 with residual and e4m3 output (43 us) and for the pre-read form of 16,384 x
+// 4 x 7,168 (249 us), 5.4 for the backward of 8,191 x 4,096 (50 us). Small calls are
+// bound by the launch (16 x 4,096: 5 us).
 #include "hc_sublayer.h"
 #include "hc_sublayer_device.h"
 
@@ -11,11 +14,13 @@ namespace hc {
 
 namespace {
 
-constexpr int OUT_STREAM = 0, OUT_E4M3 = 2, OUT_I8 = 3;  // the dtype codes of hc.h for the 8-bit forms
+constexpr int OUT_STREAM = 0, OUT_E4M3 = 2;  // else int8 codes (the 8-bit forms by their dtype codes in hc.h)
 
 // A row's channels lie in pieces of 8, piece (it * NT + tid) of item it with its NT
-// threads: a wave, four rows to a workgroup and no barrier (WAVE, up to 2,048 channels),
-// else a workgroup of as many waves as the row fills.
+// threads: a wave, four rows to a workgroup and no barrier (WAVE, up to 512 channels),
+// else a workgroup of as many waves as the row fills (a wave with more pieces a thread
+// takes 45 against 35 us backward at 16,384 x 1,024 and 73 against 55 at 2,048 channels;
+// forward the two are within 4 %).
 constexpr int WAVE_ROWS = 4;
 
 template <bool WAVE>
@@ -189,13 +194,12 @@ __device__ __forceinline__ uint2 pack_i8(const float v[8], float inv) {
   return r;
 }
 
-// MODE 0: v = x; 1: v = x + residual; 2: v = sum_i h[i] x[i] (n streams); 4: the same
-// with n = 4. But for MODE 2 the next row is on its way while this one is finished
-// (NS arrays or streams of it).
+// MODE 0: v = x; 1: v = x + residual; 2: v = sum_i h[i] x[i] (n streams, four of them on
+// their way at once). In modes 0 and 1 the next row is on its way while this one is
+// finished (the same for four streams gained nothing: 254 against 248 us).
 template <typename T, int MODE, int ITEMS, bool WAVE, bool VEC>
 __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(NormArgs a) {
-  constexpr int NS = MODE == 0 ? 1 : MODE == 4 ? 4 : 2;
-  constexpr bool STREAMS = MODE == 2 || MODE == 4;
+  constexpr int NS = MODE == 1 ? 2 : 1;  // arrays of a row
   __shared__ float red[2][1][16];
   __shared__ uint32_t redm[2][16];
   const RowThreads<WAVE> r;
@@ -211,8 +215,7 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(
     for (int i = 0; i < NS; ++i)
 #pragma unroll
       for (int it = 0; it < ITEMS; ++it) {
-        const T* p = MODE == 4 ? (const T*)a.x + (row * 4 + i) * C : (const T*)(i == 0 ? a.x : a.res) + row * C;
-        row_load<VEC>(p, ((int64_t)it * NT + tid) * 8, C, raw[i][it]);
+        row_load<VEC>((const T*)(i == 0 ? a.x : a.res) + row * C, ((int64_t)it * NT + tid) * 8, C, raw[i][it]);
       }
   };
   if (MODE != 2 && t < a.T) fetch(t);
@@ -240,14 +243,12 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(
     } else {
 #pragma unroll
       for (int i = 0; i < NS; ++i) {
-        const float hi = MODE == 4 ? a.h[t * 4 + i] : 1.f;
 #pragma unroll
         for (int it = 0; it < ITEMS; ++it) {
           float xi[8];
           raw[i][it].open(xi);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[it][e] = MODE == 4 ? (i == 0 ? hi * xi[e] : v[it][e] + hi * xi[e])
-                                                           : (i == 0 ? xi[e] : v[it][e] + xi[e]);
+          for (int e = 0; e < 8; ++e) v[it][e] = i == 0 ? xi[e] : v[it][e] + xi[e];
         }
       }
       if (t + step < a.T) fetch(t + step);
@@ -258,7 +259,7 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(
       if (MODE != 0 && a.s) row_store<VEC>((T*)a.s + t * C, c0, C, v[it]);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (!STREAMS || (VEC ? c0 : c0 + e) < C) ss += v[it][e] * v[it][e];  // 0 * an infinite h is no channel's
+        if (MODE != 2 || (VEC ? c0 : c0 + e) < C) ss += v[it][e] * v[it][e];  // 0 * an infinite h is no channel's
     }
     row_sum<WAVE, 1>(&ss, red[parity]);
     const float rstd = rms_factor(ss, inv_c, a.eps);
@@ -423,7 +424,7 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restric
 // the workgroups, bounded so that each keeps the weight in registers over several rows
 // and reads ahead. Measured at 8,192 x 4,096 with residual and e4m3 groups / 16,384 x 4 x
 // 7,168 / backward of 8,191 x 4,096: forward with two pieces a thread and 16,384 waves
-// 42.8 / 254 us (8,192 waves 43.9 / 261; one piece, 6,144 waves 41.6 / 264, 16,384 waves
+// 42.8 / 248 us (8,192 waves 43.9 / 261; one piece, 6,144 waves 41.6 / 264, 16,384 waves
 // 43.5 / 260); backward with one piece and 4,096 waves, 16 a CU, 50.4 us (2,048 waves
 // 50.1, 6,144 waves 59.6, each writing a part of dw; two pieces, which spill, 93).
 struct RowShape {
@@ -436,8 +437,8 @@ RowShape row_shape(int64_t T, int64_t C, bool bwd) {
   const int64_t most_waves = bwd ? 4096 : 16384;
   RowShape s;
   const int64_t pieces = (C + 7) / 8;
-  s.wave = C <= 2048;
-  s.items = s.wave ? (C <= 512 ? 1 : C <= 1024 ? 2 : 4) : (bwd && C <= 8192 ? 1 : 2);
+  s.wave = C <= 512;
+  s.items = C <= 2048 || (bwd && C <= 8192) ? 1 : 2;
   s.block = s.wave ? 64 * WAVE_ROWS : (unsigned)((pieces + 64 * s.items - 1) / (64 * s.items) * 64);
   const int64_t need = s.wave ? (T + WAVE_ROWS - 1) / WAVE_ROWS : T, most = most_waves * 64 / s.block;
   s.grid = (unsigned)(need < most ? need : most);
@@ -453,9 +454,8 @@ void norm_go(bool vec, const RowShape& s, const NormArgs& a, hipStream_t st) {
 template <typename T, int MODE>
 void norm_by_width(bool vec, const NormArgs& a, hipStream_t st) {
   const RowShape s = row_shape(a.T, a.C, false);
-  if (s.wave && s.items == 1) norm_go<T, MODE, 1, true>(vec, s, a, st);
-  else if (s.wave && s.items == 2) norm_go<T, MODE, 2, true>(vec, s, a, st);
-  else if (s.wave) norm_go<T, MODE, 4, true>(vec, s, a, st);
+  if (s.wave) norm_go<T, MODE, 1, true>(vec, s, a, st);
+  else if (s.items == 1) norm_go<T, MODE, 1, false>(vec, s, a, st);
   else norm_go<T, MODE, 2, false>(vec, s, a, st);
 }
 
@@ -468,9 +468,7 @@ void norm_bwd_go(bool vec, const RowShape& s, const NormBwdArgs& a, hipStream_t 
 template <typename T>
 void norm_bwd_by_width(bool vec, const NormBwdArgs& a, hipStream_t st) {
   const RowShape s = row_shape(a.T, a.C, true);
-  if (s.wave && s.items == 1) norm_bwd_go<T, 1, true>(vec, s, a, st);
-  else if (s.wave && s.items == 2) norm_bwd_go<T, 2, true>(vec, s, a, st);
-  else if (s.wave) norm_bwd_go<T, 4, true>(vec, s, a, st);
+  if (s.wave) norm_bwd_go<T, 1, true>(vec, s, a, st);
   else if (s.items == 1) norm_bwd_go<T, 1, false>(vec, s, a, st);
   else norm_bwd_go<T, 2, false>(vec, s, a, st);
 }
@@ -486,12 +484,10 @@ hipError_t launch_rms_norm(int dtype, int mode, bool vec, const NormArgs& a, hip
   if (dtype == 0) {
     if (mode == 0) norm_by_width<float, 0>(vec, a, st);
     else if (mode == 1) norm_by_width<float, 1>(vec, a, st);
-    else if (a.n == 4) norm_by_width<float, 4>(vec, a, st);
     else norm_by_width<float, 2>(vec, a, st);
   } else {
     if (mode == 0) norm_by_width<bf16_t, 0>(vec, a, st);
     else if (mode == 1) norm_by_width<bf16_t, 1>(vec, a, st);
-    else if (a.n == 4) norm_by_width<bf16_t, 4>(vec, a, st);
     else norm_by_width<bf16_t, 2>(vec, a, st);
   }
   return hipGetLastError();

@@ -19,8 +19,11 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 
 // Tokens of one workgroup's part, and the most that one workgroup takes alone: above,
-// the loads of more workgroups pay for a second launch.
-constexpr int BAL_TOKENS = 128, BAL_ALONE = 1024;
+// the loads of more workgroups pay for a second launch. With 16 lanes a token, loss and
+// gradient take 24.9 us alone and 27.5 in parts at 4,096 tokens, 42 and 27 at 8,192; with
+// 64 lanes 58 and 27 at 2,048.
+constexpr int BAL_TOKENS = 128;
+inline int64_t balance_alone(int W) { return W == 16 ? 4096 : 512; }
 
 __device__ __forceinline__ float share(float s, float total) { return total == 0.f ? 0.f : s / total; }
 
@@ -393,7 +396,7 @@ hipError_t balance_go(const float* score, const int32_t* idx, const uint8_t* mas
   const int64_t nblk = bal_blocks(S), parts = B * nblk;
   int subs = 1024 / W;  // lane groups of one sequence: all of them, halved while sequences go without
   while (subs > 1 && (1024 / W) / subs < B) subs /= 2;
-  if (B * S <= BAL_ALONE) {
+  if (B * S <= balance_alone(W)) {
     hipLaunchKernelGGL((balance_finish_kernel<W, true>), dim3(1), dim3(1024), 0, st, nullptr, nullptr, nullptr, score,
                        idx, mask, B, S, nblk, subs, N, k, m, coef, loss, count, tokens, mean_p);
     return hipGetLastError();
@@ -423,7 +426,7 @@ void router_apply(const void* X, int64_t T, int64_t NC, int64_t splits, const fl
 int64_t balance_ws_bytes(int64_t B, int64_t S, int N, int m) {
   const int W = N <= 16 ? 16 : 64;
   const int64_t parts = B * bal_blocks(S);
-  if (B * S <= BAL_ALONE) return 0;
+  if (B * S <= balance_alone(W)) return 0;
   return 2 * al256(parts * W * 4) + al256(parts * 4);
 }
 

@@ -9,16 +9,6 @@ namespace hc {
 // memory needs no more alignment than that, and the compiler keeps the copy one access.
 __device__ __forceinline__ void load8_any(const float* p, float v[8]) { __builtin_memcpy(v, p, 32); }
 
-__device__ __forceinline__ void load8_any(const bf16_t* p, float v[8]) {
-  uint32_t q[4];
-  __builtin_memcpy(q, p, 16);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf2f(q[i] & 0xffffu);
-    v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
-  }
-}
-
 __device__ __forceinline__ void store8_any(float* p, const float v[8]) { __builtin_memcpy(p, v, 32); }
 
 __device__ __forceinline__ void store8_any(bf16_t* p, const float v[8]) {

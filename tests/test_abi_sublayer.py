@@ -89,12 +89,12 @@ def test_scan_refusals(L):
 
 
 def test_router_refusals(L):
-    need = L.xhc_balance_loss_workspace_bytes(2, 3000, 16, 2)
+    need = L.xhc_balance_loss_workspace_bytes(2, 9000, 16, 2)
     assert need > 0 and L.xhc_balance_loss_workspace_bytes(1, 509, 8, 1) == 0  # one workgroup takes those alone
     assert L.xhc_balance_loss_workspace_bytes(2, 300, 65, 2) == -1
     assert L.xhc_balance_loss_workspace_bytes(1 << 20, 1 << 20, 16, 2) == -1
 
-    def loss(s=at(0), i=at(1), mk=at(2), B=2, S=3000, N=16, k=4, m=2, lo=at(3), c=at(4), t=at(5), p=at(6), ws=at(7),
+    def loss(s=at(0), i=at(1), mk=at(2), B=2, S=9000, N=16, k=4, m=2, lo=at(3), c=at(4), t=at(5), p=at(6), ws=at(7),
              wsb=need):
         return L.xhc_balance_loss(s, i, mk, B, S, N, k, m, 0.01, lo, c, t, p, ws, wsb, None)
 
