@@ -260,16 +260,19 @@ __device__ __forceinline__ void weight_parts(const float* __restrict__ w, int64_
   uint32_t h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float a = j0 + 2 * i < E ? w[ch * E + j0 + 2 * i] : 0.f, b = j0 + 2 * i + 1 < E ? w[ch * E + j0 + 2 * i + 1] : 0.f;
-    const uint32_t ha = bf_part(a), hb = bf_part(b);
-    h[i] = ha | hb << 16;
-    l[i] = (uint32_t)bf_part(a) | (uint32_t)bf_part(b) << 16;
+    const float a = j0 + 2 * i < E ? w[ch * E + j0 + 2 * i] : 0.f;
+    const float b = j0 + 2 * i + 1 < E ? w[ch * E + j0 + 2 * i + 1] : 0.f;
+    h[i] = pack_bf2_hw(a, b);
+    l[i] = pack_bf2_hw(a - __uint_as_float(h[i] << 16), b - __uint_as_float(h[i] & 0xffff0000u));
   }
   hi = make_uint4(h[0], h[1], h[2], h[3]);
   lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 
-template <int E>
+// The groups are taken from the last one back, the splits in turns: the pass before has
+// just read the last rows. KEPT: all of X may still be in the last-level cache (256 MB)
+// and is read through it (T = 240 of 16 x 4,096: 43 against 49 us; 1 GB: 776 against 770).
+template <int E, bool KEPT>
 __global__ __launch_bounds__(256, 3) void router_apply_kernel(const bf16_t* __restrict__ X, int64_t T, int64_t NC,
                                                               const float* __restrict__ w,
                                                               const Group* __restrict__ G, const bf16_t* dX_in,
@@ -288,7 +291,7 @@ __global__ __launch_bounds__(256, 3) void router_apply_kernel(const bf16_t* __re
   for (int e = 0; e < 4; ++e) dw[e] = fv4{0.f, 0.f, 0.f, 0.f};
   const uint32_t row = (uint32_t)NC;
 
-  for (int64_t g = blockIdx.y; g * GT < T; g += gridDim.y) {
+  for (int64_t g = (T + GT - 1) / GT - 1 - blockIdx.y; g >= 0; g -= gridDim.y) {
     const int64_t t0 = g * GT;
     const int live = (int)min((int64_t)GT, T - t0);
     const bf16_t* xb = X + t0 * NC + c0;
@@ -299,7 +302,8 @@ __global__ __launch_bounds__(256, 3) void router_apply_kernel(const bf16_t* __re
     for (int i = 0; i < 8; ++i) {
       const int tau = 16 * (i >> 2) + 4 * q + (i & 3);
       off[i] = (uint32_t)min(tau, live - 1) * row + ch;  // past the end: the last token's row again
-      x[i] = __builtin_nontemporal_load(reinterpret_cast<const u2*>(xb + off[i]));
+      const u2* xp = reinterpret_cast<const u2*>(xb + off[i]);
+      x[i] = KEPT ? *xp : __builtin_nontemporal_load(xp);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) d[i] = __builtin_nontemporal_load(reinterpret_cast<const u2*>(db + off[i]));
@@ -417,8 +421,13 @@ hipError_t balance_go(const float* score, const int32_t* idx, const uint8_t* mas
 template <int E>
 void router_apply(const void* X, int64_t T, int64_t NC, int64_t splits, const float* w, const Group* G,
                   const void* dX_in, void* dX_out, float* part, hipStream_t st) {
-  hipLaunchKernelGGL((router_apply_kernel<E>), dim3((unsigned)((NC + 255) / 256), (unsigned)splits), dim3(256), 0, st,
-                     (const bf16_t*)X, T, NC, w, G, (const bf16_t*)dX_in, (bf16_t*)dX_out, part);
+  const dim3 g((unsigned)((NC + 255) / 256), (unsigned)splits), b(256);
+  if (T * NC * 2 <= (256ll << 20))
+    hipLaunchKernelGGL((router_apply_kernel<E, true>), g, b, 0, st, (const bf16_t*)X, T, NC, w, G,
+                       (const bf16_t*)dX_in, (bf16_t*)dX_out, part);
+  else
+    hipLaunchKernelGGL((router_apply_kernel<E, false>), g, b, 0, st, (const bf16_t*)X, T, NC, w, G,
+                       (const bf16_t*)dX_in, (bf16_t*)dX_out, part);
 }
 
 }  // namespace
@@ -463,7 +472,8 @@ hipError_t launch_router_backward(const void* X, int64_t T, int N, int64_t C, in
   const int E = N - m;
   const int64_t NC = (int64_t)N * C, splits = router_splits(T, NC);
   Group* G = (Group*)ws;
-  float* part = (float*)((char*)ws + al256(router_groups(T) * sizeof(Group)));
+  // one split's part is dw itself
+  float* part = splits == 1 ? dw : (float*)((char*)ws + al256(router_groups(T) * sizeof(Group)));
   const int64_t n = NC * E;
   if (T == 0) {
     hipLaunchKernelGGL(split_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, n, 0, dw);
@@ -480,6 +490,7 @@ hipError_t launch_router_backward(const void* X, int64_t T, int N, int64_t C, in
 #undef HC_ROUTER_CASE
     default: break;
   }
+  if (splits == 1) return hipGetLastError();
   hipLaunchKernelGGL(split_sum_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, part, n, (int)splits, dw);
   return hipGetLastError();
 }
