@@ -326,6 +326,24 @@ def test_scan_padding_may_hold_anything():
     assert torch.equal(hc.hc_gated_scan(x, g, lengths=L2, out=(torch.zeros(B, S, C, device="cuda"), None))[0], y)
 
 
+@pytest.mark.parametrize("where", ["x", "gate", "h0"])
+def test_scan_nan_goes_on_in_its_channel(where):
+    note(f"hc_gated_scan with a NaN of all ones in {where}")
+    S, C = 2000, 300
+    x, g = torch.randn(2, S, C, device="cuda"), torch.randn(2, S, C, device="cuda")
+    h0 = torch.randn(2, C, device="cuda")
+    y0, l0 = hc.hc_gated_scan(x, g, h0)
+    ones = torch.full((1,), -1, dtype=torch.int32, device="cuda").view(torch.float32)
+    t = 0 if where == "h0" else 150
+    {"x": x, "gate": g, "h0": h0[:, None]}[where][1, t, 37] = ones[0]
+    y, last = hc.hc_gated_scan(x, g, h0)
+    torch.cuda.synchronize()
+    assert y[1, t:, 37].isnan().all() and last[1, 37].isnan()
+    y[1, t:, 37] = y0[1, t:, 37]
+    last[1, 37] = l0[1, 37]
+    assert torch.equal(y, y0) and torch.equal(last, l0)
+
+
 def test_scan_gates_at_the_ends_of_their_range():
     note("hc_gated_scan with gates of -inf, +inf and the type's extremes")
     for dt in ("f32", "bf16"):
