@@ -657,7 +657,8 @@ int hc_rms_norm_backward(const void* s, int dtype, int64_t T, int64_t C, const f
  *   lengths (NULL: S each) [B] int32 device array: sequence b has lengths[b] tokens
  *   (taken as 0 below 0 and as S above S); behind them x and gate are not used, y is
  *   left as it was, and h_last is the state after the last token (h0 for length 0).
- *   The state is float32 throughout; y is rounded once.
+ *   The state is float32 throughout; y is rounded once. The pieces of a long sequence
+ *   are joined in a fixed order: the same call gives the same bits.
  *
  * hc_gated_scan_backward - gradients for the upstream gradients dy [B, S, C] of y
  *   and dh_last [B, C] float32 (NULL: zeros) of h_last. With y the forward's output
