@@ -13,11 +13,12 @@
 // registers, publishes the tile's composed map, joins the maps of the few tiles before
 // it to the state that an earlier group of tiles left, and walks its tokens again from
 // registers.
-// Tiles are taken from a counter in walk order, so that every tile waited for
-// belongs to a workgroup that already runs and waits for earlier tiles only.
-// Bound by HBM: 8,192 x 4,096 bfloat16 forward in 50 us (46 of them here, 4.7 TB/s with
-// the words, 5 the clearing), the backward of 2 x 4,096 x 4,096 in 87 (4.75 TB/s).
-// Reading the data twice (chunk maps, a walk over them, the outputs) took 135 and 176.
+// A column's tiles (128 channels of a sequence) are taken from its counter in walk
+// order, so that every tile waited for belongs to a workgroup that already runs and
+// waits for earlier tiles only.
+// Bound by HBM: 8,192 x 4,096 bfloat16 forward in 48 us (5 of them the clearing, 5 the
+// joining), the backward of 2 x 4,096 x 4,096 in 81. One counter for all columns took 51
+// and 87; reading the data twice (chunk maps, a walk over them, the outputs) 135 and 176.
 #include "hc_sublayer.h"
 #include "hc_sublayer_device.h"
 
@@ -28,6 +29,7 @@ namespace {
 constexpr int V = 2;          // channels of one thread: 128 of a wave, one full access a row
 constexpr int WAVES = 8;      // waves of a tile, one after another in time
 constexpr int TILE_C = 64 * V;
+constexpr int COUNTER = 32;   // words of a counter: a cache line of its own
 // Sequences that one thread walks alone: 16 us against 24 in tiles for 64 x 32 x 4,096
 // forward; backward 14.0 against 13.9 for 16 x 16 x 4,096 and 24 against 14 for 32 tokens.
 constexpr int SHORT_FWD = 32, SHORT_BWD = 16;
@@ -232,11 +234,11 @@ __device__ __forceinline__ uint64_t await(const uint64_t* p) {
   return w;
 }
 
-// The words of all tiles absent, the counter zero.
-__global__ __launch_bounds__(256) void scan_clear_kernel(uint4* ws, int64_t n16) {
+// The words of all tiles absent, the counters zero.
+__global__ __launch_bounds__(256) void scan_clear_kernel(uint4* ws, int64_t counters16, int64_t n16) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= n16) return;
-  const uint32_t v = i < 16 ? 0u : 0xffffffffu;  // 256 bytes of counter, then the words
+  const uint32_t v = i < counters16 ? 0u : 0xffffffffu;
   ws[i] = make_uint4(v, v, v, v);
 }
 
@@ -258,13 +260,16 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
   // what the whole wave shares is kept in scalar registers: every row is then one scalar
   // base and a 32-bit lane offset
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // A column is one channel tile of one sequence; its tiles in walk order, by its counter.
+  // The columns move on by one from one row of workgroups to the next, or with a multiple
+  // of 8 of them each would stay on one of the 8 dies (53 against 49 us at 8,192 x 4,096).
+  const uint32_t ncol = (uint32_t)nct * (uint32_t)a.B, col = (blockIdx.x + blockIdx.x / ncol) % ncol;
   if (!ONE) {
-    if (threadIdx.x == 0) ticket = atomicAdd((unsigned*)a.ws, 1u);
+    if (threadIdx.x == 0) ticket = atomicAdd((unsigned*)a.ws + (int64_t)col * COUNTER, 1u);
     lds_barrier();
   }
-  // walk order: every sequence's and channel tile's j-th tile before any (j+1)-th
-  const uint32_t tk = ONE ? blockIdx.x : __builtin_amdgcn_readfirstlane(ticket);
-  const uint32_t ct = tk % (uint32_t)nct, r = tk / (uint32_t)nct, b = r % (uint32_t)a.B, j = r / (uint32_t)a.B;
+  const uint32_t j = ONE ? 0u : __builtin_amdgcn_readfirstlane(ticket);
+  const uint32_t ct = col % (uint32_t)nct, b = col / (uint32_t)nct;
   const int64_t c0 = (int64_t)ct * TILE_C;
   const bool in = lane * V < a.C - c0;
   const uint32_t lo = in ? lane * V : 0;  // lanes past the row read its tile's first channels and store nothing
@@ -357,8 +362,8 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
     }
 
   // one word per lane's channel, inside the row or not
-  uint64_t* words = (uint64_t*)((char*)a.ws + 256) + (b * nct + ct) * TILE_C + lane * V;
-  const int64_t wstep = a.B * nct * TILE_C;  // from one tile of the walk to the next
+  uint64_t* words = (uint64_t*)((unsigned*)a.ws + (int64_t)ncol * COUNTER) + (int64_t)col * TILE_C + lane * V;
+  const int64_t wstep = (int64_t)ncol * TILE_C;  // from one tile of the walk to the next
   // The state before the tile. Tiles are joined in groups of WAVES, always in the same
   // order (what is ready first makes no difference to a sum's rounding): from the state
   // that the group before left, through the maps of the group's earlier tiles (in the
@@ -371,34 +376,26 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
     for (int e = 0; e < V; ++e) publish(words + (int64_t)j * wstep + e, word_of(tA[e], tH[e]));
   float s[V] = {0.f, 0.f};
   if (!ONE && j > 0) {
-    // wave w: the map of the group's w-th tile; the last wave: the state before the group
+    // wave i: the map of the group's i-th tile; the last wave: the state before the group
     const bool state = wv == WAVES - 1;
-    float wa[V] = {1.f, 1.f}, wh[V] = {0.f, 0.f};
-    if (state ? g0 > 0 : (uint32_t)wv < gj) {
-      const uint64_t* p = words + (int64_t)(state ? g0 - 1 : g0 + wv) * wstep;
-      uint64_t w[V];
+    const bool want = state ? g0 > 0 : (uint32_t)wv < gj;
+    const uint64_t* p = words + (int64_t)(state ? g0 - 1 : g0 + wv) * wstep;
+    uint64_t w[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) w[e] = peek(p + e);
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if (w[e] == ABSENT) w[e] = await(p + e);
-        wa[e] = __uint_as_float((uint32_t)w[e]);
-        wh[e] = __uint_as_float((uint32_t)(w[e] >> 32));
-      }
-    }
+    for (int e = 0; e < V; ++e) w[e] = want ? peek(p + e) : word_of(1.f, 0.f);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      lA[wv][lane * V + e] = wa[e];
-      lH[wv][lane * V + e] = wh[e];
+      if (w[e] == ABSENT) w[e] = await(p + e);
+      lA[wv][lane * V + e] = __uint_as_float((uint32_t)w[e]);
+      lH[wv][lane * V + e] = __uint_as_float((uint32_t)(w[e] >> 32));
     }
     lds_barrier();
 #pragma unroll
     for (int e = 0; e < V; ++e) s[e] = lH[WAVES - 1][lane * V + e];
-#pragma unroll BWD ? 2 : WAVES - 1
-    for (int w = 0; w < WAVES - 1; ++w)
+#pragma unroll 4
+    for (uint32_t i = 0; i < gj; ++i)
 #pragma unroll
-      for (int e = 0; e < V; ++e)
-        if ((uint32_t)w < gj) s[e] = lA[w][lane * V + e] * s[e] + lH[w][lane * V + e];
+      for (int e = 0; e < V; ++e) s[e] = lA[i][lane * V + e] * s[e] + lH[i][lane * V + e];
   }
   if (leaves && gj == WAVES - 1)
 #pragma unroll
@@ -471,8 +468,9 @@ hipError_t scan_go(const ScanArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((scan_tile_kernel<T, VEC, BWD, true>), g, b, 0, st, a, ntile, nct);
     return hipGetLastError();
   }
-  const int64_t n16 = 16 + ntile * a.B * nct * TILE_C / 2;
-  hipLaunchKernelGGL(scan_clear_kernel, dim3((unsigned)((n16 + 255) / 256)), dim3(256), 0, st, (uint4*)a.ws, n16);
+  const int64_t counters16 = a.B * nct * COUNTER / 4, n16 = counters16 + ntile * a.B * nct * TILE_C / 2;
+  hipLaunchKernelGGL(scan_clear_kernel, dim3((unsigned)((n16 + 255) / 256)), dim3(256), 0, st, (uint4*)a.ws, counters16,
+                     n16);
   hipLaunchKernelGGL((scan_tile_kernel<T, VEC, BWD, false>), g, b, 0, st, a, ntile, nct);
   return hipGetLastError();
 }
@@ -490,7 +488,7 @@ int64_t scan_ws_bytes(int64_t B, int64_t S, int64_t C) {
   constexpr int TOKENS = Tile<float, true>::TOKENS;
   if (S <= TOKENS) return 0;
   const int64_t ntile = (S + TOKENS - 1) / TOKENS, nct = (C + TILE_C - 1) / TILE_C;
-  return 256 + ntile * B * nct * TILE_C * 8;
+  return B * nct * (COUNTER * 4 + ntile * TILE_C * 8);
 }
 
 hipError_t launch_scan(int dtype, bool bwd, bool vec, const ScanArgs& a, hipStream_t st) {
