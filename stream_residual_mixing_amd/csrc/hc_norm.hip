@@ -34,12 +34,16 @@ struct RowThreads {
   static __device__ __forceinline__ int rows() { return WAVE ? WAVE_ROWS : 1; }
 };
 
-// VEC: rows of whole pieces at 16-byte aligned addresses. Otherwise whole pieces are
-// still one access each (global memory takes any element-aligned address), and only
-// a row's ragged last piece goes element by element.
-__device__ __forceinline__ int piece_count(int64_t c0, int64_t C) {
-  return (int)max((int64_t)0, min((int64_t)8, C - c0));
-}
+// VEC: rows of whole pieces at 16-byte aligned addresses. Otherwise every load is still
+// one access (global memory takes any element-aligned address): a row's ragged last
+// piece is read as the row's last 8 channels and moved into place when it is opened, so
+// that nothing waits for it early.
+__device__ __forceinline__ int piece_count(uint32_t c0, uint32_t C) { return c0 < C ? (int)min(8u, C - c0) : 0; }
+
+// 16 bytes at any address of a 2-byte element. bfloat16 rows are streamed, as the aligned
+// ones are (ordinary loads are moved down to their first use: 97 against 59 us at 8,192 x
+// 4,098); float32 rows, whose lanes skip every other 16 bytes, are not (113 against 120).
+typedef uint32_t u4_any __attribute__((ext_vector_type(4), aligned(2)));
 
 // A piece as stored, so that the next row's can be on their way in few registers.
 template <typename T> struct Piece;
@@ -48,6 +52,10 @@ template <> struct Piece<float> {
   __device__ __forceinline__ void open(float v[8]) const {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = q[e];
+  }
+  __device__ __forceinline__ void close(const float v[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = v[e];
   }
 };
 template <> struct Piece<bf16_t> {
@@ -59,21 +67,30 @@ template <> struct Piece<bf16_t> {
       v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
     }
   }
+  __device__ __forceinline__ void close(const float v[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = pack_bf2_hw(v[2 * i], v[2 * i + 1]);
+  }
 };
 
 template <bool VEC, typename T>
-__device__ __forceinline__ void row_load(const T* row, int64_t c0, int64_t C, Piece<T>& v) {
+__device__ __forceinline__ void row_load(const T* row, uint32_t c0, uint32_t C, Piece<T>& v) {
   typedef uint32_t u4 __attribute__((ext_vector_type(4)));
-  constexpr int N = sizeof(v) / 16;
   const int cnt = piece_count(c0, C);
   if (VEC && cnt > 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < (int)sizeof(v) / 16; ++i) {
       const u4 q = __builtin_nontemporal_load(reinterpret_cast<const u4*>(row + c0) + i);
       __builtin_memcpy((char*)v.q + 16 * i, &q, 16);
     }
-  } else if (!VEC && cnt == 8) {
-    __builtin_memcpy(v.q, row + c0, sizeof(v));
+  } else if (!VEC && C >= 8) {
+    const T* p = row + (cnt == 8 ? c0 : C - 8);
+    if (sizeof(T) == 2) {
+      const u4_any q = __builtin_nontemporal_load(reinterpret_cast<const u4_any*>(p));
+      __builtin_memcpy(v.q, &q, 16);
+    } else {
+      __builtin_memcpy(v.q, p, sizeof(v));
+    }
   } else {
     T e8[8];
 #pragma unroll
@@ -82,24 +99,66 @@ __device__ __forceinline__ void row_load(const T* row, int64_t c0, int64_t C, Pi
   }
 }
 
+// The piece as 8 channels, those past the row 0.
 template <bool VEC, typename T>
-__device__ __forceinline__ void row_store(T* row, int64_t c0, int64_t C, const float v[8]) {
+__device__ __forceinline__ void row_open(const Piece<T>& raw, uint32_t c0, uint32_t C, float v[8]) {
   const int cnt = piece_count(c0, C);
+  if (VEC || C < 8 || cnt == 8) {
+    raw.open(v);
+    return;
+  }
+  const int by = 8 - cnt;  // the piece's first channel is element `by` of what was read
+  raw.open(v);
+#pragma unroll
+  for (int st = 4; st >= 1; st >>= 1)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float up = e + st < 8 ? v[e + st] : 0.f;
+      v[e] = (by & st) ? up : v[e];
+    }
+  if (by == 8) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.f;
+  }
+}
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void row_store(T* row, uint32_t c0, uint32_t C, const float v[8]) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  const int cnt = piece_count(c0, C);
+  Piece<T> p;
+  p.close(v);
   if (VEC) {
-    if (cnt > 0) store8_nt(row + c0, v);
+    if (cnt > 0)
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(p) / 16; ++i) {
+        u4 q;
+        __builtin_memcpy(&q, (const char*)p.q + 16 * i, 16);
+        __builtin_nontemporal_store(q, reinterpret_cast<u4*>(row + c0) + i);
+      }
   } else if (cnt == 8) {
-    store8_any(row + c0, v);
+    if (sizeof(T) == 2) {
+      u4_any q;
+      __builtin_memcpy(&q, p.q, 16);
+      __builtin_nontemporal_store(q, reinterpret_cast<u4_any*>(row + c0));
+    } else {
+      __builtin_memcpy(row + c0, p.q, sizeof(p));
+    }
   } else {
-    store8_tail(row + c0, cnt, v);
+    T e8[8];
+    __builtin_memcpy(e8, p.q, sizeof(p));
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (e < cnt) row[c0 + e] = e8[e];
   }
 }
 
 // The weight is used by every row: ordinary loads, kept in registers over the rows.
 template <bool VEC, int ITEMS>
-__device__ __forceinline__ void load_weight(const float* w, int64_t C, int nt, int tid, float out[ITEMS][8]) {
+__device__ __forceinline__ void load_weight(const float* w, uint32_t C, uint32_t nt, uint32_t tid, float out[ITEMS][8]) {
 #pragma unroll
   for (int it = 0; it < ITEMS; ++it) {
-    const int64_t c0 = ((int64_t)it * nt + tid) * 8;
+    const uint32_t c0 = (it * nt + tid) * 8;
     if (w == nullptr) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) out[it][e] = 1.f;
@@ -203,8 +262,8 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(
   __shared__ float red[2][1][16];
   __shared__ uint32_t redm[2][16];
   const RowThreads<WAVE> r;
-  const int tid = r.tid, NT = r.nt;
-  const int64_t C = a.C, step = (int64_t)gridDim.x * r.rows();
+  const uint32_t tid = r.tid, NT = r.nt, C = (uint32_t)a.C;
+  const int64_t step = (int64_t)gridDim.x * r.rows();
   const float inv_c = 1.0f / (float)C;
   float w[ITEMS][8];
   load_weight<VEC, ITEMS>(a.w, C, NT, tid, w);
@@ -215,7 +274,7 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(
     for (int i = 0; i < NS; ++i)
 #pragma unroll
       for (int it = 0; it < ITEMS; ++it) {
-        row_load<VEC>((const T*)(i == 0 ? a.x : a.res) + row * C, ((int64_t)it * NT + tid) * 8, C, raw[i][it]);
+        row_load<VEC>((const T*)(i == 0 ? a.x : a.res) + row * C, (it * NT + tid) * 8, C, raw[i][it]);
       }
   };
   if (MODE != 2 && t < a.T) fetch(t);
@@ -234,8 +293,8 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(
         for (int it = 0; it < ITEMS; ++it) {
           Piece<T> q;
           float xi[8];
-          row_load<VEC>((const T*)a.x + (t * a.n + i) * C, ((int64_t)it * NT + tid) * 8, C, q);
-          q.open(xi);
+          row_load<VEC>((const T*)a.x + (t * a.n + i) * C, (it * NT + tid) * 8, C, q);
+          row_open<VEC>(q, (it * NT + tid) * 8, C, xi);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[it][e] += hi * xi[e];
         }
@@ -246,7 +305,7 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(
 #pragma unroll
         for (int it = 0; it < ITEMS; ++it) {
           float xi[8];
-          raw[i][it].open(xi);
+          row_open<VEC>(raw[i][it], (it * NT + tid) * 8, C, xi);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[it][e] = i == 0 ? xi[e] : v[it][e] + xi[e];
         }
@@ -255,7 +314,7 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(
     }
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
-      const int64_t c0 = ((int64_t)it * NT + tid) * 8;
+      const uint32_t c0 = (it * NT + tid) * 8;
       if (MODE != 0 && a.s) row_store<VEC>((T*)a.s + t * C, c0, C, v[it]);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
@@ -270,7 +329,7 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(
     if (a.out == OUT_STREAM) {
 #pragma unroll
       for (int it = 0; it < ITEMS; ++it)
-        row_store<VEC>((T*)a.y + t * C, ((int64_t)it * NT + tid) * 8, C, v[it]);
+        row_store<VEC>((T*)a.y + t * C, (it * NT + tid) * 8, C, v[it]);
       continue;
     }
     uint32_t m[ITEMS];
@@ -279,7 +338,7 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(
       m[it] = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const bool in = VEC ? ((int64_t)it * NT + tid) * 8 < C : ((int64_t)it * NT + tid) * 8 + e < C;
+        const bool in = VEC ? (it * NT + tid) * 8 < C : (it * NT + tid) * 8 + e < C;
         if (in) m[it] = max(m[it], __float_as_uint(v[it][e]) & 0x7fffffffu);
       }
     }
@@ -298,7 +357,7 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(
     }
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
-      const int64_t c0 = ((int64_t)it * NT + tid) * 8;
+      const uint32_t c0 = (it * NT + tid) * 8;
       float scale = __uint_as_float(m[it]) / qmax;
       if (scale < 0x1p-126f) scale = 1.f;
       const float inv = 1.f / scale;
@@ -330,8 +389,7 @@ template <typename T, int ITEMS, bool WAVE, bool VEC>
 __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_backward_kernel(NormBwdArgs a) {
   __shared__ float red[2][2][16];
   const RowThreads<WAVE> r;
-  const int tid = r.tid, NT = r.nt;
-  const int64_t C = a.C;
+  const uint32_t tid = r.tid, NT = r.nt, C = (uint32_t)a.C;
   const float inv_c = 1.0f / (float)C;
   float w[ITEMS][8], dw[ITEMS][8];
   load_weight<VEC, ITEMS>(a.w, C, NT, tid, w);
@@ -345,7 +403,7 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_backwar
   const auto fetch = [&](int64_t row) {
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
-      const int64_t c0 = ((int64_t)it * NT + tid) * 8;
+      const uint32_t c0 = (it * NT + tid) * 8;
       row_load<VEC>((const T*)a.s + row * C, c0, C, rv[it]);
       row_load<VEC>((const T*)a.dy + row * C, c0, C, ry[it]);
       if (a.ds) row_load<VEC>((const T*)a.ds + row * C, c0, C, rs[it]);
@@ -353,13 +411,14 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_backwar
   };
   if (t < a.T) fetch(t);
   for (int parity = 0; t < a.T; t += step, parity ^= 1) {
-    float v[ITEMS][8], dy[ITEMS][8], ds[ITEMS][8];
+    float v[ITEMS][8], dy[ITEMS][8];
     float sums[2] = {0.f, 0.f};
+    Piece<T> cs[ITEMS];
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
-      rv[it].open(v[it]);
-      ry[it].open(dy[it]);
-      rs[it].open(ds[it]);
+      row_open<VEC>(rv[it], (it * NT + tid) * 8, C, v[it]);
+      row_open<VEC>(ry[it], (it * NT + tid) * 8, C, dy[it]);
+      cs[it] = rs[it];
     }
     if (t + step < a.T) fetch(t + step);
 #pragma unroll
@@ -374,20 +433,21 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_backwar
     const float k = (sums[1] * rstd) * inv_c * rstd;
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
-      float o[8];
+      float o[8], ds[8];
+      row_open<VEC>(cs[it], (it * NT + tid) * 8, C, ds);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         dw[it][e] += dy[it][e] * (v[it][e] * rstd);
-        o[e] = rstd * (w[it][e] * dy[it][e] - v[it][e] * k) + (a.ds ? ds[it][e] : 0.f);
+        o[e] = rstd * (w[it][e] * dy[it][e] - v[it][e] * k) + (a.ds ? ds[e] : 0.f);
       }
-      row_store<VEC>((T*)a.dx + t * C, ((int64_t)it * NT + tid) * 8, C, o);
+      row_store<VEC>((T*)a.dx + t * C, (it * NT + tid) * 8, C, o);
     }
   }
   if (a.part == nullptr) return;
   float* p = a.part + ((int64_t)blockIdx.x * r.rows() + r.sub) * C;
 #pragma unroll
   for (int it = 0; it < ITEMS; ++it) {
-    const int64_t c0 = ((int64_t)it * NT + tid) * 8;
+    const uint32_t c0 = (it * NT + tid) * 8;
     if (VEC) {
       if (c0 < C) store8(p + c0, dw[it]);
     } else if (piece_count(c0, C) == 8) {
@@ -423,10 +483,11 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restric
 // Launch shape of a pass over T rows of C channels: pieces per thread, threads, and
 // the workgroups, bounded so that each keeps the weight in registers over several rows
 // and reads ahead. Measured at 8,192 x 4,096 with residual and e4m3 groups / 16,384 x 4 x
-// 7,168 / backward of 8,191 x 4,096: forward with two pieces a thread and 16,384 waves
-// 42.8 / 248 us (8,192 waves 43.9 / 261; one piece, 6,144 waves 41.6 / 264, 16,384 waves
-// 43.5 / 260); backward with one piece and 4,096 waves, 16 a CU, 50.4 us (2,048 waves
-// 50.1, 6,144 waves 59.6, each writing a part of dw; two pieces, which spill, 93).
+// 7,168: forward with two pieces a thread and 16,384 waves 42.8 / 248 us (8,192 waves 43.9
+// / 261; one piece, 6,144 waves 41.6 / 264, 16,384 waves 43.5 / 260). The backward keeps 256
+// CUs equally busy, with up to 16 waves each (bfloat16, 8,192 rows of 2,560 / 4,096 / 7,168
+// channels: 36 / 50 / 97 us; 4,096 waves in all, however they fall, 50 / 51 / 156; one
+// workgroup each 49 / 49 / 98) and one piece a thread (two spill).
 struct RowShape {
   int items;
   bool wave;
@@ -434,13 +495,13 @@ struct RowShape {
 };
 
 RowShape row_shape(int64_t T, int64_t C, bool bwd) {
-  const int64_t most_waves = bwd ? 4096 : 16384;
   RowShape s;
   const int64_t pieces = (C + 7) / 8;
   s.wave = C <= 512;
   s.items = C <= 2048 || (bwd && C <= 8192) ? 1 : 2;
   s.block = s.wave ? 64 * WAVE_ROWS : (unsigned)((pieces + 64 * s.items - 1) / (64 * s.items) * 64);
-  const int64_t need = s.wave ? (T + WAVE_ROWS - 1) / WAVE_ROWS : T, most = most_waves * 64 / s.block;
+  const int64_t need = s.wave ? (T + WAVE_ROWS - 1) / WAVE_ROWS : T;
+  const int64_t waves = s.block / 64, most = bwd ? 256 * (waves < 16 ? 16 / waves : 1) : 16384 / waves;
   s.grid = (unsigned)(need < most ? need : most);
   return s;
 }
