@@ -384,7 +384,7 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(
 
 // dx = rstd w dy - v rstd^3 mean(w dy v) + ds, and this workgroup's part of
 // dw = sum_t dy v rstd, kept in registers over its rows and written once to
-// part[workgroup row][C] (the parts are added in a fixed order afterwards).
+// part[workgroup][C] (the parts are added in a fixed order afterwards).
 template <typename T, int ITEMS, bool WAVE, bool VEC>
 __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_backward_kernel(NormBwdArgs a) {
   __shared__ float red[2][2][16];
@@ -444,7 +444,19 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_backwar
     }
   }
   if (a.part == nullptr) return;
-  float* p = a.part + ((int64_t)blockIdx.x * r.rows() + r.sub) * C;
+  float* p = a.part + (int64_t)blockIdx.x * C;
+  if constexpr (WAVE) {  // the waves' sums are added here: a fourth of the parts
+    __shared__ __attribute__((aligned(16))) float add[WAVE_ROWS][512];
+    store8(add[r.sub] + tid * 8, dw[0]);
+    __syncthreads();
+    for (uint32_t c = threadIdx.x; c < C; c += 64 * WAVE_ROWS) {
+      float sum = add[0][c];
+#pragma unroll
+      for (int i = 1; i < WAVE_ROWS; ++i) sum += add[i][c];
+      p[c] = sum;
+    }
+    return;
+  }
 #pragma unroll
   for (int it = 0; it < ITEMS; ++it) {
     const uint32_t c0 = (it * NT + tid) * 8;
@@ -537,8 +549,7 @@ void norm_bwd_by_width(bool vec, const NormBwdArgs& a, hipStream_t st) {
 }  // namespace
 
 int64_t norm_backward_parts(int64_t T, int64_t C) {
-  const RowShape s = row_shape(T, C, true);
-  return (int64_t)s.grid * (s.wave ? WAVE_ROWS : 1);
+  return row_shape(T, C, true).grid;
 }
 
 hipError_t launch_rms_norm(int dtype, int mode, bool vec, const NormArgs& a, hipStream_t st) {
