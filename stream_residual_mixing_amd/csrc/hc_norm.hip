@@ -382,6 +382,40 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(
   }
 }
 
+// A thread's eight values of each of its pieces, kept over the rows: in registers with
+// one piece, in its own places of LDS (128 KB, one workgroup per CU as its registers leave it)
+// with two, where the weight and its gradient beside two rows of operands would spill: 4,096
+// rows of 16,384 channels 99 us in bfloat16 and 238 in float32, 152 and 464 from registers.
+template <int ITEMS>
+struct PieceSums {
+  float r[8];
+  __device__ __forceinline__ void put(int, const float (&v)[8], int) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r[e] = v[e];
+  }
+  __device__ __forceinline__ void get(int, float (&v)[8], int) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = r[e];
+  }
+};
+template <>
+struct PieceSums<2> {
+  static __device__ __forceinline__ float4* at(int it, int array) {
+    __shared__ float4 kept[2][4][1024];
+    return &kept[array][2 * it][threadIdx.x];
+  }
+  __device__ __forceinline__ void put(int it, const float (&v)[8], int array) {
+    float4* p = at(it, array);
+    p[0] = make_float4(v[0], v[1], v[2], v[3]);
+    p[1024] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  __device__ __forceinline__ void get(int it, float (&v)[8], int array) const {
+    const float4 *p = at(it, array), a = p[0], b = p[1024];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+
 // dx = rstd w dy - v rstd^3 mean(w dy v) + ds, and this workgroup's part of
 // dw = sum_t dy v rstd, kept in registers over its rows and written once to
 // part[workgroup][C] (the parts are added in a fixed order afterwards).
@@ -391,14 +425,20 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_backwar
   const RowThreads<WAVE> r;
   const uint32_t tid = r.tid, NT = r.nt, C = (uint32_t)a.C;
   const float inv_c = 1.0f / (float)C;
-  float w[ITEMS][8], dw[ITEMS][8];
-  load_weight<VEC, ITEMS>(a.w, C, NT, tid, w);
+  PieceSums<ITEMS> w, dw;
+  {
+    float w0[ITEMS][8];
+    const float zero[8] = {};
+    load_weight<VEC, ITEMS>(a.w, C, NT, tid, w0);
 #pragma unroll
-  for (int it = 0; it < ITEMS; ++it)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) dw[it][e] = 0.f;
+    for (int it = 0; it < ITEMS; ++it) {
+      w.put(it, w0[it], 0);
+      dw.put(it, zero, 1);
+    }
+  }
   const int64_t step = (int64_t)gridDim.x * r.rows();
   int64_t t = (int64_t)blockIdx.x * r.rows() + r.sub;
+  constexpr bool DS_AHEAD = ITEMS == 1 || sizeof(T) == 2;  // two pieces of float32 would spill
   Piece<T> rv[ITEMS], ry[ITEMS], rs[ITEMS];
   const auto fetch = [&](int64_t row) {
 #pragma unroll
@@ -406,7 +446,7 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_backwar
       const uint32_t c0 = (it * NT + tid) * 8;
       row_load<VEC>((const T*)a.s + row * C, c0, C, rv[it]);
       row_load<VEC>((const T*)a.dy + row * C, c0, C, ry[it]);
-      if (a.ds) row_load<VEC>((const T*)a.ds + row * C, c0, C, rs[it]);
+      if (DS_AHEAD && a.ds) row_load<VEC>((const T*)a.ds + row * C, c0, C, rs[it]);
     }
   };
   if (t < a.T) fetch(t);
@@ -418,42 +458,53 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_backwar
     for (int it = 0; it < ITEMS; ++it) {
       row_open<VEC>(rv[it], (it * NT + tid) * 8, C, v[it]);
       row_open<VEC>(ry[it], (it * NT + tid) * 8, C, dy[it]);
-      cs[it] = rs[it];
+      if (DS_AHEAD) cs[it] = rs[it];
+      else if (a.ds) row_load<VEC>((const T*)a.ds + t * C, (it * NT + tid) * 8, C, cs[it]);
     }
     if (t + step < a.T) fetch(t + step);
 #pragma unroll
-    for (int it = 0; it < ITEMS; ++it)
+    for (int it = 0; it < ITEMS; ++it) {
+      float wi[8];
+      w.get(it, wi, 0);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         sums[0] += v[it][e] * v[it][e];
-        sums[1] += v[it][e] * (w[it][e] * dy[it][e]);
+        sums[1] += v[it][e] * (wi[e] * dy[it][e]);
       }
+    }
     row_sum<WAVE, 2>(sums, red[parity]);
     const float rstd = rms_factor(sums[0], inv_c, a.eps);
     const float k = (sums[1] * rstd) * inv_c * rstd;
+    if (ITEMS == 2) asm volatile("" ::: "memory");  // the weight is read again, not kept
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
-      float o[8], ds[8];
+      float o[8], ds[8], wi[8], dwi[8];
       row_open<VEC>(cs[it], (it * NT + tid) * 8, C, ds);
+      w.get(it, wi, 0);
+      dw.get(it, dwi, 1);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        dw[it][e] += dy[it][e] * (v[it][e] * rstd);
-        o[e] = rstd * (w[it][e] * dy[it][e] - v[it][e] * k) + (a.ds ? ds[e] : 0.f);
+        dwi[e] += dy[it][e] * (v[it][e] * rstd);
+        o[e] = rstd * (wi[e] * dy[it][e] - v[it][e] * k) + (a.ds ? ds[e] : 0.f);
       }
+      dw.put(it, dwi, 1);
       row_store<VEC>((T*)a.dx + t * C, (it * NT + tid) * 8, C, o);
     }
   }
   if (a.part == nullptr) return;
   float* p = a.part + (int64_t)blockIdx.x * C;
+  float sum[ITEMS][8];
+#pragma unroll
+  for (int it = 0; it < ITEMS; ++it) dw.get(it, sum[it], 1);
   if constexpr (WAVE) {  // the waves' sums are added here: a fourth of the parts
     __shared__ __attribute__((aligned(16))) float add[WAVE_ROWS][512];
-    store8(add[r.sub] + tid * 8, dw[0]);
+    store8(add[r.sub] + tid * 8, sum[0]);
     __syncthreads();
     for (uint32_t c = threadIdx.x; c < C; c += 64 * WAVE_ROWS) {
-      float sum = add[0][c];
+      float all = add[0][c];
 #pragma unroll
-      for (int i = 1; i < WAVE_ROWS; ++i) sum += add[i][c];
-      p[c] = sum;
+      for (int i = 1; i < WAVE_ROWS; ++i) all += add[i][c];
+      p[c] = all;
     }
     return;
   }
@@ -461,11 +512,11 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_backwar
   for (int it = 0; it < ITEMS; ++it) {
     const uint32_t c0 = (it * NT + tid) * 8;
     if (VEC) {
-      if (c0 < C) store8(p + c0, dw[it]);
+      if (c0 < C) store8(p + c0, sum[it]);
     } else if (piece_count(c0, C) == 8) {
-      store8_any(p + c0, dw[it]);
+      store8_any(p + c0, sum[it]);
     } else {
-      store8_tail(p + c0, piece_count(c0, C), dw[it]);
+      store8_tail(p + c0, piece_count(c0, C), sum[it]);
     }
   }
 }
@@ -499,7 +550,7 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restric
 // / 261; one piece, 6,144 waves 41.6 / 264, 16,384 waves 43.5 / 260). The backward keeps 256
 // CUs equally busy, with up to 16 waves each (bfloat16, 8,192 rows of 2,560 / 4,096 / 7,168
 // channels: 36 / 50 / 97 us; 4,096 waves in all, however they fall, 50 / 51 / 156; one
-// workgroup each 49 / 49 / 98) and one piece a thread (two spill).
+// workgroup each 49 / 49 / 98) and one piece a thread up to 8,192 channels.
 struct RowShape {
   int items;
   bool wave;
