@@ -885,11 +885,11 @@ def _norm_outs(out, x, T, C, quant, ngroups):
     """(y, scale or None), of `out` or new."""
     dt = x.dtype if quant is None else quant
     y, scale = (None, None) if out is None else out
-    y = torch.empty(T, C, dtype=dt, device=x.device) if y is None else _dev_tensor(y, "y out", (dt,), (T, C), x.device)
+    y = x.new_empty((T, C), dtype=dt) if y is None else _dev_tensor(y, "y out", (dt,), (T, C), x.device)
     if quant is None:
         return y, None
     if scale is None:
-        return y, torch.empty(T, ngroups, device=x.device)
+        return y, x.new_empty((T, ngroups), dtype=torch.float32)
     return y, _f32(scale, "scale out", (T, ngroups), x.device)
 
 
@@ -913,7 +913,7 @@ def hc_rms_norm(x, weight=None, eps=1e-6, *, residual=None, quant=None, group=0,
         s = None
         if residual is not None:
             residual = _dev_tensor(residual, "residual", (x.dtype,), (T, C), dev)
-            s = _stream_out(s_out, "s out", (T, C), x.dtype, dev)
+            s = torch.empty_like(x) if s_out is None else _dev_tensor(s_out, "s out", (x.dtype,), (T, C), dev)
         elif s_out is not None:
             raise ValueError("s_out needs a residual")
         y, scale = _norm_outs(out, x, T, C, quant, ngroups)
@@ -974,7 +974,7 @@ def hc_rms_norm_backward(s, weight, dy, eps=1e-6, *, ds=None, want_dweight=True,
         if dw is not None:
             dw = _f32(dw, "dweight out", (C,), dev)
         elif want_dweight:
-            dw = torch.empty(C, device=dev)
+            dw = torch.empty(C, dtype=torch.float32, device=dev)
         ws = None
         if dw is not None:
             ws = _workspace(hc_rms_norm_backward_workspace_bytes(T, C), dev, workspace)
@@ -1017,9 +1017,9 @@ def hc_gated_scan(x, gate, h0=None, *, lengths=None, tied=True, want_state=True,
     y, h_last = (None, None) if out is None else out
     h_last = _per_channel(h_last, "h_last out", B, C, dev)
     with _on(dev, stream):
-        y = _stream_out(y, "y out", (B, S, C), x.dtype, dev)
+        y = torch.empty_like(x) if y is None else _dev_tensor(y, "y out", (x.dtype,), (B, S, C), dev)
         if h_last is None and want_state:
-            h_last = torch.empty(B, C, device=dev)
+            h_last = torch.empty(B, C, dtype=torch.float32, device=dev)
         nbytes = hc_gated_scan_workspace_bytes(B, S, C)
         ws = None if nbytes == 0 else _workspace(nbytes, dev, workspace)
         _check("hc_gated_scan", lib().hc_gated_scan(
@@ -1047,7 +1047,7 @@ def hc_gated_scan_backward(x, gate, y, dy, h0=None, dh_last=None, *, lengths=Non
         dx = _stream_out(dx, "dx out", (B, S, C), x.dtype, dev)
         dgate = _stream_out(dgate, "dgate out", (B, S, C), x.dtype, dev)
         if dh0 is None:
-            dh0 = torch.empty(B, C, device=dev)
+            dh0 = torch.empty(B, C, dtype=torch.float32, device=dev)
         nbytes = hc_gated_scan_workspace_bytes(B, S, C)
         ws = None if nbytes == 0 else _workspace(nbytes, dev, workspace)
         _check("hc_gated_scan_backward", lib().hc_gated_scan_backward(
@@ -1091,8 +1091,8 @@ def xhc_balance_loss(score, idx, B, S, *, m=2, coef=1.0, mask=None, out=None, wo
     mask = _token_mask(mask, T, dev)
     with _on(dev, stream):
         if out is None:
-            loss, count = torch.empty((), device=dev), torch.empty(B, N, dtype=torch.int32, device=dev)
-            tokens, mean_p = torch.empty(B, dtype=torch.int32, device=dev), torch.empty(B, E, device=dev)
+            loss, mean_p = score.new_empty(()), score.new_empty((B, E))
+            count, tokens = idx.new_empty((B, N)), idx.new_empty((B,))
         else:
             loss, count = _f32(out[0], "loss out", (), dev), _i32(out[1], "count out", (B, N), dev)
             tokens, mean_p = _i32(out[2], "tokens out", (B,), dev), _f32(out[3], "mean_p out", (B, E), dev)
@@ -1123,7 +1123,7 @@ def xhc_balance_loss_backward(score, count, tokens, k, B, S, *, coef=1.0, dloss=
         if dloss.numel() != 1:
             raise ValueError(f"dloss must hold one value, got shape {tuple(dloss.shape)}")
     with _on(dev, stream):
-        dscore = torch.empty(T, E, device=dev) if out is None else _f32(out, "dscore out", (T, E), dev)
+        dscore = torch.empty_like(score) if out is None else _f32(out, "dscore out", (T, E), dev)
         _check("xhc_balance_loss_backward", lib().xhc_balance_loss_backward(
             _ptr(score), _ptr(count), _ptr(tokens), _ptr(mask), B, S, N, int(k), N - E, float(coef), _ptr(dloss),
             _ptr(dscore), _stream(dev, stream)))
@@ -1149,7 +1149,7 @@ def xhc_router_backward(X, w_router, score, dscore, dX, *, out=None, workspace=N
     dX = _dev_tensor(dX, "dX", (X.dtype,), (T, N, C), dev)
     dX_out = dX if out is None else _dev_tensor(out, "dX out", (X.dtype,), (T, N, C), dev)
     with _on(dev, stream):
-        dw = torch.empty(N * C, E, device=dev)
+        dw = torch.empty(N * C, E, dtype=torch.float32, device=dev)
         ws = _workspace(xhc_router_backward_workspace_bytes(T, N, C, N - E, X.dtype), dev, workspace)
         _check("xhc_router_backward", lib().xhc_router_backward(
             _ptr(X), _DT[X.dtype], T, N, C, N - E, _ptr(w_router), _ptr(score), _ptr(dscore), _ptr(dX), _ptr(dX_out),

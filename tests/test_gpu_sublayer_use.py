@@ -371,3 +371,18 @@ def test_binding_refuses_wrong_arguments():
     _raises(TypeError, hc.xhc_router_backward, X.float(), i["wr"], sc, ds, i["dX"].float())
     _raises(hc.HCError, hc.xhc_router_backward, X, i["wr"], sc, ds, X)  # in place on the state itself
     assert torch.isfinite(hc.xhc_balance_loss(sc, idx, 2, 5)["loss"])  # a valid call after the refusals
+
+
+@pytest.mark.parametrize("default", ["float64", "bfloat16"])
+def test_program_with_another_default_type(default):
+    """What a call allocates is float32 where the library writes float32."""
+    i = _inputs(23)
+    want = _step(i)
+    before = torch.get_default_dtype()
+    try:
+        torch.set_default_dtype(getattr(torch, default))
+        got = _step(i)
+    finally:
+        torch.set_default_dtype(before)
+    assert [t.dtype for t in got] == [t.dtype for t in want]
+    _same(got, want, f"default type {default}")
