@@ -702,8 +702,8 @@ int hc_gated_scan_backward(const void* x, const void* gate, const void* y, const
  *   the counts are a discrete choice), 0 for masked tokens:
  *   dscore_tj = dloss coef / (B n_b) (f_bj - sum_i f_bi p_ti) / sum_i score_ti.
  *   dloss [1] float32 device value (NULL: 1); count, tokens as the forward wrote them.
- *   Both: 1 <= m < k <= N <= 64, k <= 16, T * 64 < 2^32 (HC_ERR_SHAPE); 4-byte aligned
- *   arrays; outputs overlap no input, other output or workspace (HC_ERR_ALIAS).
+ *   Both: 1 <= m < k <= N <= 64, k <= 16, T <= 2^26 - 4, B < 2^24 (HC_ERR_SHAPE); 4-byte
+ *   aligned arrays; outputs overlap no input, other output or workspace (HC_ERR_ALIAS).
  *   Deterministic: every sum runs in a fixed order.
  *
  * xhc_router_backward - gradients of the router's projection score = sigmoid((vec X @
@@ -718,8 +718,8 @@ int hc_gated_scan_backward(const void* x, const void* gate, const void* y, const
  *   part; dX_out may be dX (in place). A token whose dscore is all zero takes no
  *   part (its X and score may hold anything); the all-zero state passes nothing.
  *   Covered: dtype HC_BF16 (HC_F32 -> HC_ERR_DTYPE), 1 <= m < N <=
- *   HC_MAX_ROUTER_STREAMS, C a multiple of 32, N*C <= 2^25, T < 2^24 (else HC_ERR_SHAPE). X, dX,
- *   dX_out 16-byte aligned, float arrays 4; workspace 256 bytes,
+ *   HC_MAX_ROUTER_STREAMS, C a multiple of 32, N*C <= 2^25, T <= 2^24 - 32 (else HC_ERR_SHAPE).
+ *   X, dX, dX_out 16-byte aligned, float arrays 4; workspace 256 bytes,
  *   xhc_router_backward_workspace_bytes (-1 for what is not covered). Deterministic.
  */
 int64_t xhc_balance_loss_workspace_bytes(int64_t B, int64_t S, int N, int m);

@@ -1577,7 +1577,9 @@ int hc_gated_scan_backward(const void* x, const void* gate, const void* y, const
 
 static int check_balance_shape(int64_t B, int64_t S, int N, int k, int m) {
   if (N < 2 || N > HC_MAX_STREAMS || m < 1 || k <= m || k > N || k > HC_MAX_ACTIVE) return HC_ERR_SHAPE;
-  if (B < 0 || S < 0 || B >= (1ll << 26) || S >= (1ll << 26) || B * S >= (1ll << 26)) return HC_ERR_SHAPE;
+  // grids of whole workgroups of 256 threads, fewer than 2^32 in all: 64 threads a token, one
+  // workgroup a sequence
+  if (B < 0 || S < 0 || B >= (1ll << 24) || S >= (1ll << 26) || B * S > (1ll << 26) - 4) return HC_ERR_SHAPE;
   return HC_OK;
 }
 
@@ -1620,7 +1622,8 @@ int xhc_balance_loss_backward(const float* score, const int32_t* count, const in
 
 static int check_router_shape(int dtype, int64_t T, int N, int64_t C, int m) {
   if (dtype != HC_BF16) return HC_ERR_DTYPE;
-  if (T < 0 || T >= (1ll << 24) || m < 1 || N <= m || N > HC_MAX_ROUTER_STREAMS || C < 32 || C % 32 != 0 ||
+  // T: 256 threads for each token of whole groups of 32, fewer than 2^32 in all
+  if (T < 0 || T > (1ll << 24) - 32 || m < 1 || N <= m || N > HC_MAX_ROUTER_STREAMS || C < 32 || C % 32 != 0 ||
       C > (1ll << 26) || N * C > (1ll << 25))  // 32 rows are reached with 32-bit offsets
     return HC_ERR_SHAPE;
   return HC_OK;

@@ -127,3 +127,20 @@ def test_router_refusals(L):
     assert rt(ws=None) == -8 and rt(wsb=need - 1) == -8
     assert rt(o=at(0)) == -5 and rt(dw=at(4)) == -5 and rt(dw=at(1)) == -5
     assert rt(o=ctypes.c_void_p(at(4).value + 16)) == -5 and rt(ws=at(5)) == -5
+
+
+def test_sizes_whose_grids_no_launch_takes(L):
+    """A launch has fewer than 2^32 threads along x: calls that would need more are refused."""
+    ws = L.xhc_router_backward_workspace_bytes
+    assert ws((1 << 24) - 32, 2, 32, 1, 1) > 0
+    for T in ((1 << 24) - 31, (1 << 24) - 1):  # whole groups of 32 tokens, 256 threads each token: 2^32
+        assert ws(T, 2, 32, 1, 1) == -1
+    ws = L.xhc_balance_loss_workspace_bytes
+    assert ws(1, (1 << 26) - 4, 32, 2) > 0 and ws((1 << 24) - 1, 1, 16, 2) > 0
+    assert ws(1, (1 << 26) - 3, 32, 2) == -1  # 64 threads a token, workgroups of 256
+    assert ws(1 << 24, 1, 16, 2) == -1 and ws(1 << 25, 0, 16, 2) == -1  # a workgroup a sequence
+
+    def bwd(B, S):
+        return L.xhc_balance_loss_backward(None, None, None, None, B, S, 32, 4, 2, 0.01, None, None, None)
+
+    assert bwd(1, (1 << 26) - 3) == -2 and bwd(1 << 24, 1) == -2 and bwd(1, (1 << 26) - 4) == -1
