@@ -207,6 +207,29 @@ def test_norm_backward(C, dt):
             assert got is ds and torch.equal(ds, dx)
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("C", [8193, 9001, 12288, 16383])
+def test_norm_backward_of_rows_with_two_pieces_a_thread(C, dt):
+    """Above 8,192 channels the weight and its gradient lie in LDS; the bounds are test_norm_backward's."""
+    test_norm_backward(C, dt)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T, C", [(9001, 8), (9001, 200), (4099, 511), (4500, 1032)])
+def test_norm_backward_of_many_rows(T, C, dt):
+    """Several rows a wave or workgroup: dw adds rows, waves and workgroups, T terms in all, each sum in
+    at most T + 60 roundings of the magnitudes."""
+    rng = np.random.default_rng(T + C)
+    v, v64 = up(2 * rng.normal(size=(T, C)), dt)
+    dy, dy64 = up(rng.normal(size=(T, C)), dt)
+    w, w64 = up(1 + 0.3 * rng.normal(size=C))
+    _, dw = hc.hc_rms_norm_backward(v, w, dy, 1e-6)
+    torch.cuda.synchronize()
+    _, rw = R.rms_norm_backward(v64, w64, 1e-6, dy64, None)
+    rstd = 1 / np.sqrt((v64 * v64).mean(1, keepdims=True) + 1e-6)
+    within("dw", down(dw), rw, (T + 60) * U * (np.abs(dy64 * v64) * rstd).sum(0) + 1e-37)
+
+
 # --------------------------------------------------------------------- scan
 
 
