@@ -1006,7 +1006,8 @@ def hc_gated_scan(x, gate, h0=None, *, lengths=None, tied=True, want_state=True,
                   stream=None):
     """h_t = a_t h_{t-1} + u_t x_t with a = sigmoid(gate) and u = 1 - a (tied) or 1, over x, gate
     [B, S, C]; h0 [B, C] float32, lengths [B] int32. Returns (y [B, S, C], h_last [B, C] or None);
-    out = (y, h_last), h_last may be h0. Rows of y behind a sequence's length are left as they are."""
+    out = (y, h_last), h_last may be h0. Rows behind a sequence's length are zero in a y that the call
+    allocates, and left as they are in a given one."""
     x = _sequences(x, "x")
     B, S, C = x.shape
     dev = x.device
@@ -1017,7 +1018,10 @@ def hc_gated_scan(x, gate, h0=None, *, lengths=None, tied=True, want_state=True,
     y, h_last = (None, None) if out is None else out
     h_last = _per_channel(h_last, "h_last out", B, C, dev)
     with _on(dev, stream):
-        y = torch.empty_like(x) if y is None else _dev_tensor(y, "y out", (x.dtype,), (B, S, C), dev)
+        if y is None:  # padding is not written: what the allocator hands out must not be left in it
+            y = torch.empty_like(x) if lengths is None else torch.zeros_like(x)
+        else:
+            y = _dev_tensor(y, "y out", (x.dtype,), (B, S, C), dev)
         if h_last is None and want_state:
             h_last = torch.empty(B, C, dtype=torch.float32, device=dev)
         nbytes = hc_gated_scan_workspace_bytes(B, S, C)
