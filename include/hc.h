@@ -613,7 +613,9 @@ int hc_static_post(const void* X, int dtype, int64_t T, int n, int64_t C, const 
  *   127; 1 where that is below the smallest normal float32), code = y * (1 / scale)
  *   rounded to nearest even; the value it stands for is code * scale. A NaN in a
  *   group makes its scale NaN.
- *   1 <= C <= HC_MAX_NORM_CHANNELS. No workspace. Statistics are float32.
+ *   1 <= C <= HC_MAX_NORM_CHANNELS. No workspace. Statistics are float32, of a row
+ *   whose squares would leave its range relative to a power of two: a finite v has its
+ *   norm whatever its size, and so has its gradient.
  *
  * hc_pre_norm - hc_pre followed by the norm in one pass over the state: v = F_in =
  *   sum_i h_pre[t, i] X[t, i] ([mHC] 4.3.1), y as above.

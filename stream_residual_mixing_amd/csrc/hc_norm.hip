@@ -202,6 +202,11 @@ __device__ __forceinline__ uint32_t umax4(uint32_t v) { return umax_dpp<DPP_QXOR
 __device__ __forceinline__ uint32_t umax8(uint32_t v) { return umax_dpp<DPP_HALF_MIRROR>(umax4(v)); }
 __device__ __forceinline__ uint32_t umax16(uint32_t v) { return umax_dpp<DPP_ROR8>(umax8(v)); }
 
+// A value that the wave's lanes have in common, in a scalar register.
+__device__ __forceinline__ float uniform(float v) {
+  return __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(v)));
+}
+
 template <bool WAVE>
 __device__ __forceinline__ uint32_t row_umax(uint32_t v, uint32_t* red) {
   v = umax16(v);
@@ -216,9 +221,24 @@ __device__ __forceinline__ uint32_t row_umax(uint32_t v, uint32_t* red) {
   return s;
 }
 
-__device__ __forceinline__ float rms_factor(float sumsq, float inv_c, float eps) {
-  const float ms = sumsq * inv_c + eps;
+__device__ __forceinline__ float rms_factor(float ms) {
   return ms == 0.f ? 0.f : 1.0f / sqrtf(ms);  // the all-zero row without eps normalises to zero
+}
+
+// A row whose mean square + eps is in this range has the sum it should have: no square
+// passes float32's largest number, and what squares lose below its smallest normal one
+// (2^-126 each) is at most 2^-26 of their mean.
+__device__ __forceinline__ bool in_range(float ms) { return ms >= 0x1p-100f && ms <= 3.4028235e38f; }
+
+// The others are taken relative to 2^k, the power of two over the row's largest magnitude
+// (its bits: `largest`) or sqrt(eps), whichever is more: the norm of v 2^-k with eps 2^-2k
+// is that of v with eps, and scaling by a power of two is exact. No such power where the
+// row is all zero, or infinite or NaN somewhere.
+__device__ __forceinline__ bool scale_of(uint32_t largest, float eps, int& k) {
+  if (largest == 0 || largest >= 0x7f800000u) return false;
+  k = __builtin_amdgcn_frexp_expf(__uint_as_float(largest));
+  if (eps > 0.f) k = max(k, (__builtin_amdgcn_frexp_expf(eps) + 1) >> 1);
+  return true;
 }
 
 // 8 codes of 8 bits. Clamped first: rounding up at the largest code would overflow.
@@ -321,7 +341,29 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(
         if (MODE != 2 || (VEC ? c0 : c0 + e) < C) ss += v[it][e] * v[it][e];  // 0 * an infinite h is no channel's
     }
     row_sum<WAVE, 1>(&ss, red[parity]);
-    const float rstd = rms_factor(ss, inv_c, a.eps);
+    float ms = uniform(ss * inv_c + a.eps);
+    if (!in_range(ms)) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int it = 0; it < ITEMS; ++it)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (MODE != 2 || (it * NT + tid) * 8 + (VEC ? 0 : e) < C) top = max(top, __float_as_uint(v[it][e]) & 0x7fffffffu);
+      int k;
+      if (scale_of(row_umax<WAVE>(top, redm[parity]), a.eps, k)) {
+        ss = 0.f;
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[it][e] = __builtin_amdgcn_ldexpf(v[it][e], -k);
+            if (MODE != 2 || (it * NT + tid) * 8 + (VEC ? 0 : e) < C) ss += v[it][e] * v[it][e];
+          }
+        row_sum<WAVE, 1>(&ss, red[parity]);
+        ms = ss * inv_c + __builtin_amdgcn_ldexpf(a.eps, -2 * k);
+      }
+    }
+    const float rstd = rms_factor(ms);
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it)
 #pragma unroll
@@ -422,6 +464,7 @@ struct PieceSums<2> {
 template <typename T, int ITEMS, bool WAVE, bool VEC>
 __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_backward_kernel(NormBwdArgs a) {
   __shared__ float red[2][2][16];
+  __shared__ uint32_t redm[2][16];
   const RowThreads<WAVE> r;
   const uint32_t tid = r.tid, NT = r.nt, C = (uint32_t)a.C;
   const float inv_c = 1.0f / (float)C;
@@ -473,7 +516,35 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_backwar
       }
     }
     row_sum<WAVE, 2>(sums, red[parity]);
-    const float rstd = rms_factor(sums[0], inv_c, a.eps);
+    float ms = uniform(sums[0] * inv_c + a.eps);
+    float back1 = 1.f, back2 = 1.f;  // dx = ... 2^-k, as a product of two that are in range
+    if (!in_range(ms) || !(fabsf(uniform(sums[1])) <= 3.4028235e38f)) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int it = 0; it < ITEMS; ++it)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[it][e]) & 0x7fffffffu);
+      int p;
+      if (scale_of(row_umax<WAVE>(top, redm[parity]), a.eps, p)) {
+        sums[0] = sums[1] = 0.f;
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it) {
+          float wi[8];
+          w.get(it, wi, 0);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[it][e] = __builtin_amdgcn_ldexpf(v[it][e], -p);
+            sums[0] += v[it][e] * v[it][e];
+            sums[1] += v[it][e] * (wi[e] * dy[it][e]);
+          }
+        }
+        row_sum<WAVE, 2>(sums, red[parity]);
+        ms = sums[0] * inv_c + __builtin_amdgcn_ldexpf(a.eps, -2 * p);
+        back1 = __builtin_amdgcn_ldexpf(1.f, -(p / 2));
+        back2 = __builtin_amdgcn_ldexpf(1.f, -(p - p / 2));
+      }
+    }
+    const float rstd = rms_factor(ms), rstd_dx = rstd * back1;
     const float k = (sums[1] * rstd) * inv_c * rstd;
     if (ITEMS == 2) asm volatile("" ::: "memory");  // the weight is read again, not kept
 #pragma unroll
@@ -485,7 +556,7 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_backwar
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         dwi[e] += dy[it][e] * (v[it][e] * rstd);
-        o[e] = rstd * (wi[e] * dy[it][e] - v[it][e] * k) + (a.ds ? ds[e] : 0.f);
+        o[e] = rstd_dx * (wi[e] * dy[it][e] - v[it][e] * k) * back2 + (a.ds ? ds[e] : 0.f);
       }
       dw.put(it, dwi, 1);
       row_store<VEC>((T*)a.dx + t * C, (it * NT + tid) * 8, C, o);

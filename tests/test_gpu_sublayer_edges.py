@@ -1,9 +1,11 @@
 """The norm and the scan at the edges of what their definitions allow: padded batches whose output
-the call allocates."""
+the call allocates, and rows whose squares leave float32's range."""
+import numpy as np
 import pytest
 
 from hc_testutil import have_gpu, note
-from test_gpu_sublayer import _dt
+from oracle import sublayer_ops as R
+from test_gpu_sublayer import P, U, _check_y, _dt, down, up, within
 
 pytestmark = pytest.mark.gpu
 
@@ -59,3 +61,99 @@ def test_scan_padding_of_an_allocated_output_in_a_graph():
         want, wl = hc.hc_gated_scan(x, g, lengths=L, out=(torch.zeros_like(x), None))
         torch.cuda.synchronize()
         assert torch.equal(y, want) and torch.equal(last, wl)
+
+
+# ------------------------------------- rows whose squares leave float32's range
+
+# magnitudes of rows: squares over and under float32's range, its ends, and one in the middle
+SIZES = [2e19, 1e20, 1e30, 3e37, 1.0, 3e-22, 1e-23, 1e-30, 1e-38, 1e-41]
+DENORMAL = 2.0 ** -149
+
+
+def _rows(rng, C, dt):
+    """Rows of the magnitudes above, and mixed ones: one channel far beyond the others."""
+    v = rng.normal(size=(len(SIZES) + 4, C))
+    v[:len(SIZES)] *= np.array(SIZES)[:, None]
+    v[-4, 0] = 1e30
+    v[-3] *= 1e-30
+    v[-3, C - 1] = 1e-20
+    v[-2] *= 1e25
+    v[-2, C // 2] = -3e38
+    v[-1] = 0
+    return up(v, dt)
+
+
+@pytest.mark.parametrize("C", [1, 7, 128, 500, 1000, 2050, 4096, 9001])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_norm_of_rows_beyond_the_squares_range(C, dt):
+    """Scaling a row by a power of two is exact: the bounds are those of rows in range, and one step
+    of the smallest stored numbers (2^-133 bfloat16, 2^-149 float32: half of it for each of two roundings)."""
+    rng = np.random.default_rng(C)
+    x, x64 = _rows(rng, C, dt)
+    w, w64 = up(1 + 0.3 * rng.normal(size=C))
+    for eps in (0.0, 1e-6, 1e-32, 1e-41, 1e30):
+        e64 = float(np.float32(eps))
+        ref = R.rms_norm(x64, w64, e64)
+        note(f"hc_rms_norm of large and small rows C={C} {dt} eps={eps}")
+        y = hc.hc_rms_norm(x, w, eps)["y"]
+        tol = (40 * U + P[dt]) * np.abs(ref) + 2.0 ** (-133 if dt == "bf16" else -149)
+        within(f"y eps={eps}", down(y), ref, tol)
+        for quant, group in (("e4m3", 0), ("i8", 64)):
+            got = hc.hc_rms_norm(x, w, eps, quant=_dt(quant), group=group)
+            keep = np.abs(ref).max(1) > 1e-30  # smaller rows take the scale 1, or one at its border
+            _check_y(f"{quant} eps={eps}", got["y"][torch.from_numpy(keep).cuda()],
+                     got["scale"][torch.from_numpy(keep).cuda()], ref[keep], 0 * ref[keep], dt, quant, group)
+
+
+@pytest.mark.parametrize("C", [36, 520, 4096])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_residual_and_pre_norm_beyond_the_squares_range(C, dt):
+    rng = np.random.default_rng(C + 2)
+    x, x64 = _rows(rng, C, dt)
+    T = x.shape[0]
+    note(f"hc_rms_norm with residual and hc_pre_norm of large and small rows C={C} {dt}")
+    # x + x/2: exact in float64, no cancellation
+    r = x / 2
+    v = x64 + r.double().cpu().numpy()
+    for eps in (0.0, 1e-6):
+        e64 = float(np.float32(eps))
+        big = np.abs(v) > 3.3e38  # sums past float32's range are infinite by definition
+        assert not big[:-4].any()
+        ok = ~big.any(1)
+        got = hc.hc_rms_norm(x, None, eps, residual=r)
+        ref = R.rms_norm(v, None, e64)
+        tol = (44 * U + P[dt]) * np.abs(ref) + 2.0 ** (-133 if dt == "bf16" else -149)
+        within("y", down(got["y"])[ok], ref[ok], tol[ok])
+        within("s", down(got["s"])[ok], v[ok], ((P[dt] + U) * np.abs(v) + 2.0 ** -134)[ok])
+        X = torch.stack([x, r], 1)
+        h = torch.ones(T, 2, device="cuda")
+        pre = hc.hc_pre_norm(X, h, None, eps)
+        within("pre y", down(pre["y"])[ok], ref[ok], tol[ok])
+
+
+@pytest.mark.parametrize("C", [1, 7, 128, 500, 1000, 4096, 8200])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_norm_backward_of_rows_beyond_the_squares_range(C, dt):
+    """test_norm_backward's bounds on the magnitudes, and one step of the smallest stored numbers. dy is
+    small where the row is, so that dx stays in range."""
+    rng = np.random.default_rng(C + 1)
+    v, v64 = _rows(rng, C, dt)
+    T = v.shape[0]
+    g = rng.normal(size=(T, C))
+    g[np.abs(v64).max(1) < 1e-25] *= 1e-12
+    dy, dy64 = up(g, dt)
+    w, w64 = up(1 + 0.3 * rng.normal(size=C))
+    for eps in (0.0, 1e-6, 1e-32):
+        note(f"hc_rms_norm_backward of large and small rows C={C} {dt} eps={eps}")
+        e64 = float(np.float32(eps))
+        dx, dw = hc.hc_rms_norm_backward(v, w, dy, eps)
+        torch.cuda.synchronize()
+        rx, rw = R.rms_norm_backward(v64, w64, e64, dy64)
+        ms = (v64 * v64).mean(1, keepdims=True) + e64
+        rstd = np.where(ms > 0, 1 / np.sqrt(np.where(ms > 0, ms, 1)), 0)
+        wdy = np.abs(w64 * dy64)
+        vh = np.abs(v64) * rstd
+        mag = rstd * (wdy + vh * (wdy * vh).mean(1, keepdims=True))
+        within(f"dx eps={eps}", down(dx), rx,
+               120 * U * mag + (P[dt] + U) * np.abs(rx) + 2.0 ** (-133 if dt == "bf16" else -149))
+        within(f"dw eps={eps}", down(dw), rw, (T + 60) * U * (np.abs(dy64) * vh).sum(0) + 1e-37)
