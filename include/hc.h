@@ -660,7 +660,9 @@ int hc_rms_norm_backward(const void* s, int dtype, int64_t T, int64_t C, const f
  *   (taken as 0 below 0 and as S above S); behind them x and gate are not used, y is
  *   left as it was, and h_last is the state after the last token (h0 for length 0).
  *   The state is float32 throughout; y is rounded once. The pieces of a long sequence
- *   are joined in a fixed order: the same call gives the same bits.
+ *   are joined in a fixed order: the same call gives the same bits. An infinite state
+ *   stays infinite while a > 0 (a is 0, and forgets, for gates below about -87); a joined
+ *   piece's product of a may round by 2^-150, which only states beyond 1e30 show.
  *
  * hc_gated_scan_backward - gradients for the upstream gradients dy [B, S, C] of y
  *   and dh_last [B, C] float32 (NULL: zeros) of h_last. With y the forward's output

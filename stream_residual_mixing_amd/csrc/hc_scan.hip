@@ -212,6 +212,22 @@ __global__ __launch_bounds__(256) void scan_short_kernel(ScanArgs a) {
 
 // ---------------------------------------------- long sequences: joined tiles
 
+// The product A of many a that are all above 0 may fall below float32's smallest number.
+// To a finite state 0 is as good, but an infinite one stays infinite: such a product is
+// kept as -0, apart from the +0 of a gate that closed fully (or of a constant map).
+constexpr uint32_t FADED = 0x80000000u;
+
+// A with its zero's sign by `least`, the smallest of its factors' bits (-0 and NaN are
+// above every number there).
+__device__ __forceinline__ float product_of(float A, uint32_t least) {
+  return A == 0.f ? __uint_as_float(least ? FADED : 0u) : A;
+}
+
+// s -> A s + H of an infinite state as well.
+__device__ __forceinline__ float apply_map(float A, float s, float H) {
+  return (__float_as_uint(A) == FADED && fabsf(s) == INFINITY ? s : A * s) + H;
+}
+
 // A published map is one 64-bit word per channel, so no word is ever seen half
 // written: A in the low half, H in the high half. All ones: not there yet (a value
 // of that pattern, a NaN, is published as another NaN).
@@ -321,6 +337,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
   // this wave's composed map; the forward keeps a and b, the backward the signed q
   float ka[LW][V], kb[BWD ? 1 : LW][V];
   float A[V] = {1.f, 1.f}, H[V] = {0.f, 0.f};
+  uint32_t least[V] = {~0u, ~0u};
 #pragma unroll
   for (int k = 0; k < LW; ++k) {
     float g[V], x[V];
@@ -334,6 +351,7 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
       const float bb = BWD ? d * x[e] : (tied ? u * x[e] : x[e]);
       H[e] = d * H[e] + bb;
       A[e] *= d;
+      least[e] = min(least[e], __float_as_uint(d));
       ka[k][e] = BWD ? q : d;
       if (!BWD) kb[BWD ? 0 : k][e] = bb;
     }
@@ -342,12 +360,14 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
   // makes its map constant: whoever writes the last state (it may be the same array) has
   // waited for that map or for one composed from it.
   float init[V] = {0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < V; ++e) A[e] = product_of(A[e], least[e]);
   const float* first = BWD ? a.dlast : a.state0;
   if (i0 == 0 && first) {
     ld2f<VEC>(first + st0 + lo, cnt, init);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      H[e] = A[e] * init[e] + H[e];
+      H[e] = apply_map(A[e], init[e], H[e]);
       A[e] = 0.f;
     }
   }
@@ -359,17 +379,32 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
   lds_barrier();
   // the waves before this one (pA, pH), and the whole tile's map
   float pA[V] = {1.f, 1.f}, pH[V] = {0.f, 0.f}, tA[V] = {1.f, 1.f}, tH[V] = {0.f, 0.f};
+  uint32_t least_t[V] = {~0u, ~0u};
 #pragma unroll BWD ? 2 : WAVES
   for (int w = 0; w < WAVES; ++w)
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       if (w == wv) {
-        pA[e] = tA[e];
+        pA[e] = product_of(tA[e], least_t[e]);
         pH[e] = tH[e];
       }
       const float wa = sA[w][lane * V + e];
       tH[e] = wa * tH[e] + sH[w][lane * V + e];
       tA[e] *= wa;
+      least_t[e] = min(least_t[e], __float_as_uint(wa));
+    }
+#pragma unroll
+  for (int e = 0; e < V; ++e) tA[e] = product_of(tA[e], least_t[e]);
+  // A NaN may be what 0 made of an infinite state: the sums again, with care.
+  if (__any(tH[0] != tH[0] || tH[1] != tH[1]))
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      tH[e] = 0.f;
+#pragma unroll 1
+      for (int w = 0; w < WAVES; ++w) {
+        if (w == wv) pH[e] = tH[e];
+        tH[e] = apply_map(sA[w][lane * V + e], tH[e], sH[w][lane * V + e]);
+      }
     }
 
   // one word per lane's channel, inside the row or not
@@ -407,14 +442,21 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
     for (uint32_t i = 0; i < gj; ++i)
 #pragma unroll
       for (int e = 0; e < V; ++e) s[e] = lA[i][lane * V + e] * s[e] + lH[i][lane * V + e];
+    if (__any(s[0] != s[0] || s[1] != s[1]))  // as above
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        s[e] = lH[WAVES - 1][lane * V + e];
+#pragma unroll 1
+        for (uint32_t i = 0; i < gj; ++i) s[e] = apply_map(lA[i][lane * V + e], s[e], lH[i][lane * V + e]);
+      }
   }
   if (leaves && gj == WAVES - 1)
 #pragma unroll
-    for (int e = 0; e < V; ++e) publish(words + (int64_t)j * wstep + e, word_of(0.f, tA[e] * s[e] + tH[e]));
+    for (int e = 0; e < V; ++e) publish(words + (int64_t)j * wstep + e, word_of(0.f, apply_map(tA[e], s[e], tH[e])));
 
-  // what the waves before this one make of it
+  // what the waves before this one make of it (one tile's first wave's map is constant, or of 0)
 #pragma unroll
-  for (int e = 0; e < V; ++e) s[e] = i0 == 0 ? init[e] : pA[e] * s[e] + pH[e];
+  for (int e = 0; e < V; ++e) s[e] = i0 == 0 ? init[e] : ONE ? pH[e] : apply_map(pA[e], s[e], pH[e]);
 
   // The backward's walk opens q and the rows again: without this the compiler keeps what
   // it made of them, four registers for one.

@@ -1,5 +1,5 @@
-"""The norm and the scan at the edges of what their definitions allow: padded batches whose output
-the call allocates, and rows whose squares leave float32's range."""
+"""The norm and the scan at the edges of what their definitions allow: padded batches whose
+output the call allocates, rows whose squares leave float32's range, and infinite states."""
 import numpy as np
 import pytest
 
@@ -157,3 +157,63 @@ def test_norm_backward_of_rows_beyond_the_squares_range(C, dt):
         within(f"dx eps={eps}", down(dx), rx,
                120 * U * mag + (P[dt] + U) * np.abs(rx) + 2.0 ** (-133 if dt == "bf16" else -149))
         within(f"dw eps={eps}", down(dw), rw, (T + 60) * U * (np.abs(dy64) * vh).sum(0) + 1e-37)
+
+
+# ------------------------------------------------------------ infinite states
+
+
+@pytest.mark.parametrize("S", [5, 40, 129, 300, 1100, 2500])
+@pytest.mark.parametrize("tied", [True, False])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_scan_keeps_an_infinite_state(S, tied, dt):
+    """Every a is above 0, so an infinite state stays infinite whatever the sequence's length, until
+    an infinity of the other sign meets it; the other channels give what they give without it."""
+    note(f"hc_gated_scan with infinities S={S} tied={tied} {dt}")
+    B, C = 2, 130
+    gen = torch.Generator(device="cuda").manual_seed(S)
+    rn = lambda *s: torch.randn(*s, device="cuda", generator=gen)  # noqa: E731
+    x, g = rn(B, S, C).to(_dt(dt)), (rn(B, S, C) - 2).to(_dt(dt))  # a of about 0.12: products underflow
+    h0, dy, dl = rn(B, C), rn(B, S, C).to(_dt(dt)), rn(B, C)
+    y0, l0 = hc.hc_gated_scan(x, g, h0, tied=tied)
+    x2, h2 = x.clone(), h0.clone()
+    inf = float("inf")
+    h2[0, 3], h2[1, 70], h2[0, 129] = inf, -inf, inf
+    x2[0, 4, 9], x2[1, S // 2, 64], x2[0, S - 1, 65] = -inf, inf, inf
+    x2[0, S // 2, 129] = -inf  # meets the other infinity: NaN from there on
+    y, last = hc.hc_gated_scan(x2, g, h2, tied=tied)
+    torch.cuda.synchronize()
+    with np.errstate(invalid="ignore"):
+        ry, rl = R.gated_scan(down(x2), down(g), down(h2), None, tied)
+    odd = ~np.isfinite(ry)
+    got, gl = down(y), down(last)
+    assert np.array_equal(np.isnan(got), np.isnan(ry)) and np.array_equal(got[np.isinf(ry)], ry[np.isinf(ry)])
+    assert np.array_equal(np.isnan(gl), np.isnan(rl)) and np.array_equal(gl[np.isinf(rl)], rl[np.isinf(rl)])
+    assert np.array_equal(got[~odd], down(y0)[~odd]) and np.array_equal(gl[np.isfinite(rl)], down(l0)[np.isfinite(rl)])
+
+    # backward: infinite gradients pass on to the earlier tokens
+    dx0, dg0, d0 = hc.hc_gated_scan_backward(x, g, y0, dy, h0, dl, tied=tied)
+    dy2, dl2 = dy.clone(), dl.clone()
+    dl2[0, 3], dl2[1, 70], dl2[0, 129] = inf, -inf, inf
+    dy2[0, S - 2, 9], dy2[1, S // 2, 64], dy2[0, 0, 65] = -inf, inf, inf
+    dx, dg, dh = hc.hc_gated_scan_backward(x, g, y0, dy2, h0, dl2, tied=tied)
+    torch.cuda.synchronize()
+    with np.errstate(invalid="ignore"):
+        ref = R.gated_scan_backward(down(x), down(g), down(y0), down(dy2), down(h0), down(dl2), None, tied)
+    for name, t, clean, r in zip(("dx", "dgate", "dh0"), (dx, dg, dh), (dx0, dg0, d0), ref):
+        t, clean = down(t), down(clean)
+        assert np.array_equal(np.isnan(t), np.isnan(r)), name
+        assert np.array_equal(t[np.isinf(r)], r[np.isinf(r)]), name
+        assert np.array_equal(t[np.isfinite(r)], clean[np.isfinite(r)]), name
+
+
+def test_scan_map_of_closed_gates_forgets():
+    """A gate that closes fully (a = 0) resets the state: nothing of what was before is left, in any
+    form of the scan."""
+    note("hc_gated_scan with closed gates after a large state")
+    for S in (20, 300, 1500):
+        x = torch.zeros(1, S, 64, device="cuda")
+        g = torch.zeros(1, S, 64, device="cuda")
+        g[0, S // 3] = float("-inf")
+        h0 = torch.full((1, 64), 3e38, device="cuda")
+        y, last = hc.hc_gated_scan(x, g, h0)
+        assert not y[0, S // 3:].any() and not last.any() and bool((y[0, 0] > 1e38).all())
