@@ -663,6 +663,9 @@ int hc_rms_norm_backward(const void* s, int dtype, int64_t T, int64_t C, const f
  *   are joined in a fixed order: the same call gives the same bits. An infinite state
  *   stays infinite while a > 0 (a is 0, and forgets, for gates below about -87); a joined
  *   piece's product of a may round by 2^-150, which only states beyond 1e30 show.
+ *   The pieces wait for each other through the workspace: calls that share one must be
+ *   ordered, as everywhere here; should another call write it meanwhile, the wait ends
+ *   after some seconds without an error and the outputs are wrong or NaN.
  *
  * hc_gated_scan_backward - gradients for the upstream gradients dy [B, S, C] of y
  *   and dh_last [B, C] float32 (NULL: zeros) of h_last. With y the forward's output

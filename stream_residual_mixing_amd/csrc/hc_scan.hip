@@ -249,7 +249,8 @@ __device__ __forceinline__ uint64_t peek(const uint64_t* p) {
 }
 
 // Waits for a word. The tile waited for is running (see the counter), so the wait
-// ends; the bound turns a broken workspace into NaN outputs instead of a hang.
+// ends; the bound (some seconds) turns a workspace that another call writes meanwhile into
+// NaN outputs instead of a hang.
 constexpr int MOST_POLLS = 1 << 22;
 
 __device__ __forceinline__ uint64_t await(const uint64_t* p) {
@@ -295,7 +296,8 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
     if (threadIdx.x == 0) ticket = atomicAdd((unsigned*)a.ws + (int64_t)col * COUNTER, 1u);
     lds_barrier();
   }
-  const uint32_t j = ONE ? 0u : __builtin_amdgcn_readfirstlane(ticket);
+  // A counter that another call spoils meanwhile must not lead out of the workspace.
+  const uint32_t j = ONE ? 0u : min((uint32_t)__builtin_amdgcn_readfirstlane(ticket), (uint32_t)ntile - 1);
   const uint32_t ct = col % (uint32_t)nct, b = col / (uint32_t)nct;
   const int64_t c0 = (int64_t)ct * TILE_C;
   const bool in = lane * V < a.C - c0;

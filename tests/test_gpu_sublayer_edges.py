@@ -217,3 +217,32 @@ def test_scan_map_of_closed_gates_forgets():
         h0 = torch.full((1, 64), 3e38, device="cuda")
         y, last = hc.hc_gated_scan(x, g, h0)
         assert not y[0, S // 3:].any() and not last.any() and bool((y[0, 0] > 1e38).all())
+
+
+def test_scan_workspace_with_anything_in_it_used_by_one_call_after_another():
+    """One workspace for calls of other sizes, in order on one stream, eager and captured."""
+    note("hc_gated_scan with a shared workspace that holds anything")
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    cases = []
+    for B, S, C in ((1, 3000, 130), (3, 300, 512), (2, 129, 64)):
+        x, g = (torch.randn(B, S, C, device="cuda", generator=gen) for _ in range(2))
+        cases.append((x, g, hc.hc_gated_scan(x, g)))
+    n = max(hc.hc_gated_scan_workspace_bytes(*x.shape) for x, _, _ in cases)
+    graphs = []
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for x, g, _ in cases:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = hc.hc_gated_scan(x, g, workspace=ws)
+        graphs.append((graph, out))
+    for fill in (0, 255, 1, None):
+        if fill is None:
+            ws.random_(generator=gen)
+        else:
+            ws.fill_(fill)
+        for (x, g, want), (graph, out) in zip(cases, graphs):
+            y, last = hc.hc_gated_scan(x, g, workspace=ws)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want[0]) and torch.equal(last, want[1])
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
