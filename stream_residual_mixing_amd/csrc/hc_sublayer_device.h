@@ -11,13 +11,6 @@ __device__ __forceinline__ void load8_any(const float* p, float v[8]) { __builti
 
 __device__ __forceinline__ void store8_any(float* p, const float v[8]) { __builtin_memcpy(p, v, 32); }
 
-__device__ __forceinline__ void store8_any(bf16_t* p, const float v[8]) {
-  uint32_t q[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = pack_bf2(v[2 * i], v[2 * i + 1]);
-  __builtin_memcpy(p, q, 16);
-}
-
 // A barrier that orders LDS alone: global loads that are on their way stay on their way.
 __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
