@@ -225,7 +225,7 @@ __device__ __forceinline__ float product_of(float A, uint32_t least) {
 
 // s -> A s + H of an infinite state as well.
 __device__ __forceinline__ float apply_map(float A, float s, float H) {
-  return (__float_as_uint(A) == FADED && fabsf(s) == INFINITY ? s : A * s) + H;
+  return (__float_as_uint(A) == FADED && fabsf(s) == INFINITY ? 1.f : A) * s + H;
 }
 
 // A published map is one 64-bit word per channel, so no word is ever seen half
@@ -381,22 +381,29 @@ __global__ __launch_bounds__(64 * WAVES, 4) void scan_tile_kernel(ScanArgs a, in
   lds_barrier();
   // the waves before this one (pA, pH), and the whole tile's map
   float pA[V] = {1.f, 1.f}, pH[V] = {0.f, 0.f}, tA[V] = {1.f, 1.f}, tH[V] = {0.f, 0.f};
-  uint32_t least_t[V] = {~0u, ~0u};
 #pragma unroll BWD ? 2 : WAVES
   for (int w = 0; w < WAVES; ++w)
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       if (w == wv) {
-        pA[e] = product_of(tA[e], least_t[e]);
+        pA[e] = tA[e];
         pH[e] = tH[e];
       }
       const float wa = sA[w][lane * V + e];
       tH[e] = wa * tH[e] + sH[w][lane * V + e];
       tA[e] *= wa;
-      least_t[e] = min(least_t[e], __float_as_uint(wa));
     }
+  if (__any(tA[0] == 0.f || tA[1] == 0.f || pA[0] == 0.f || pA[1] == 0.f))
 #pragma unroll
-  for (int e = 0; e < V; ++e) tA[e] = product_of(tA[e], least_t[e]);
+    for (int e = 0; e < V; ++e) {
+      uint32_t least = ~0u;
+#pragma unroll 1
+      for (int w = 0; w < WAVES; ++w) {
+        if (w == wv) pA[e] = product_of(pA[e], least);
+        least = min(least, __float_as_uint(sA[w][lane * V + e]));
+      }
+      tA[e] = product_of(tA[e], least);
+    }
   // A NaN may be what 0 made of an infinite state: the sums again, with care.
   if (__any(tH[0] != tH[0] || tH[1] != tH[1]))
 #pragma unroll
