@@ -556,7 +556,7 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_backwar
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         dwi[e] += dy[it][e] * (v[it][e] * rstd);
-        o[e] = rstd_dx * (wi[e] * dy[it][e] - v[it][e] * k) * back2 + (a.ds ? ds[e] : 0.f);
+        o[e] = rstd_dx * ((wi[e] * dy[it][e] - v[it][e] * k) * back2) + (a.ds ? ds[e] : 0.f);
       }
       dw.put(it, dwi, 1);
       row_store<VEC>((T*)a.dx + t * C, (it * NT + tid) * 8, C, o);
