@@ -695,8 +695,8 @@ int hc_gated_scan_backward(const void* x, const void* gate, const void* y, const
 /*
  * xhc_balance_loss - keeps the xHC router from choosing the same streams for every
  * token: over B sequences of S tokens, for sequence b with n_b unmasked tokens,
- *   count[b, i] = its tokens whose active set idx holds stream i (entries outside
- *     [0, N) count nowhere), p_tj = score[t, j] / sum_j score[t, j] (0 where the sum is 0),
+ *   count[b, i] = its tokens whose active set idx holds stream i (a token's entries
+ *     are distinct, as the forward writes them; entries outside [0, N) count nowhere), p_tj = score[t, j] / sum_j score[t, j] (0 where the sum is 0),
  *   P[b, j] = mean_t p_tj, f_bj = E / ((k - m) n_b) * count[b, m + j], E = N - m,
  *   loss = coef / B * sum_b sum_j f_bj P_bj  (coef when the choice is even).
  *   score [T, E] float32 and idx [T, k] int32 as xhc_pre or xhc_route wrote them
@@ -724,6 +724,10 @@ int hc_gated_scan_backward(const void* x, const void* gate, const void* y, const
  *   xhc_route_backward and xhc_pre_backward formed and the one with the router's
  *   part; dX_out may be dX (in place). A token whose dscore is all zero takes no
  *   part (its X and score may hold anything); the all-zero state passes nothing.
+ *   Sums are float32. dw takes dz / r with all its 24 bits; the product in dX takes dz / r
+ *   and w_router with 16 bits each (two bfloat16 parts, off by at most 2^-16 of either),
+ *   below the 8 bits that dX is rounded to. r, its square and their reciprocals are
+ *   float32 as in xhc_pre: for states with 1e-18 <= r <= 1e15.
  *   Covered: dtype HC_BF16 (HC_F32 -> HC_ERR_DTYPE), 1 <= m < N <=
  *   HC_MAX_ROUTER_STREAMS, C a multiple of 32, N*C <= 2^25, T <= 2^24 - 32 (else HC_ERR_SHAPE).
  *   X, dX, dX_out 16-byte aligned, float arrays 4; workspace 256 bytes,

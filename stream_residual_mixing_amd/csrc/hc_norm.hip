@@ -3,10 +3,10 @@
 //   y = v * w / sqrt(mean_c v^2 + eps), stored in the stream dtype or as 8-bit
 //   codes with a scale per row or per group of 32, 64 or 128 channels.
 // Each row is read once and stays in float32 registers between the sum of squares
-// and the outputs, so the passes are bound by HBM traffic: 5.5 TB/s for 8,192 x 4,096
-// bfloat16 with residual and e4m3 output (43 us) and for the pre-read form of 16,384 x
-// 4 x 7,168 (249 us), 5.4 for the backward of 8,191 x 4,096 (50 us). Small calls are
-// bound by the launch (16 x 4,096: 5 us).
+// and the outputs, so the passes are bound by HBM traffic. Per call: 5.8 TB/s for 8,192 x
+// 4,096 bfloat16 with residual and e4m3 output (40.5 us), 5.7 for the pre-read form of
+// 16,384 x 4 x 7,168 (247 us), 5.5 for the backward of 8,191 x 4,096 (49 us, 4 of them the
+// sum of dw's parts). Small calls are bound by the launch (16 x 4,096: 5 us).
 #include "hc_sublayer.h"
 #include "hc_sublayer_device.h"
 
@@ -616,8 +616,8 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restric
 
 // Launch shape of a pass over T rows of C channels: pieces per thread, threads, and
 // the workgroups, bounded so that each keeps the weight in registers over several rows
-// and reads ahead. Measured at 8,192 x 4,096 with residual and e4m3 groups / 16,384 x 4 x
-// 7,168: forward with two pieces a thread and 16,384 waves 42.8 / 248 us (8,192 waves 43.9
+// and reads ahead. Measured against each other, by events over changing inputs, at 8,192 x
+// 4,096 with residual and e4m3 groups / 16,384 x 4 x 7,168: forward with two pieces a thread and 16,384 waves 42.8 / 248 us (8,192 waves 43.9
 // / 261; one piece, 6,144 waves 41.6 / 264, 16,384 waves 43.5 / 260). The backward keeps 256
 // CUs equally busy, with up to 16 waves each (bfloat16, 8,192 rows of 2,560 / 4,096 / 7,168
 // channels: 36 / 50 / 97 us; 4,096 waves in all, however they fall, 50 / 51 / 156; one

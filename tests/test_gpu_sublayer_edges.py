@@ -1,5 +1,6 @@
-"""The norm and the scan at the edges of what their definitions allow: padded batches whose
-output the call allocates, rows whose squares leave float32's range, and infinite states."""
+"""The norm, the scan and the router's backward at the edges of what their definitions allow:
+padded batches whose output the call allocates, rows whose squares leave float32's range,
+infinite states, workspaces with anything in them, and the smallest and largest states."""
 import numpy as np
 import pytest
 
@@ -246,3 +247,34 @@ def test_scan_workspace_with_anything_in_it_used_by_one_call_after_another():
             torch.cuda.synchronize()
             assert torch.equal(y, want[0]) and torch.equal(last, want[1])
             assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+# ------------------------------------------------ the router's range of states
+
+
+@pytest.mark.parametrize("size", [1e-18, 1e-9, 1e6, 1e15])
+def test_router_backward_over_its_range_of_states(size):
+    """test_router_backward's bounds where r is at the ends of the stated range (dX = 0: the router's part alone)."""
+    note(f"xhc_router_backward with states of size {size}")
+    rng = np.random.default_rng(7)
+    T, N, m, C = 70, 16, 2, 512
+    E = N - m
+    x = rng.normal(size=(T, N, C))
+    x *= size / np.sqrt((x * x).mean((1, 2), keepdims=True))
+    X, X64 = up(x * (1.01 if size < 1 else 0.99), "bf16")  # inside the range after rounding
+    w, w64 = up(rng.normal(size=(N * C, E)) * 2 / np.sqrt(N * C))
+    xf = X64.reshape(T, -1)
+    r = np.sqrt((xf * xf).mean(1, keepdims=True))
+    score, s64 = up(R.sigmoid((xf @ w64) / r))
+    ds, ds64 = up(rng.normal(size=(T, E)))
+    out, dw = hc.xhc_router_backward(X, w, score, ds, torch.zeros_like(X), out=torch.empty_like(X))
+    torch.cuda.synchronize()
+    ref, rdw = R.router_backward(X64, w64, s64, ds64, np.zeros_like(X64))
+    dz = np.abs(ds64 * s64 * (1 - s64))
+    z = np.abs(np.log(s64) - np.log1p(-s64))
+    kr = (N * C / 256 + 10) / 2 + 8
+    prod = (dz / r) @ np.abs(w64).T
+    tol = U * (prod * (kr + E + 4) + np.abs(xf) / (r * r * N * C) * ((dz * (z + 1)).sum(1, keepdims=True) * (2 * kr + 16)))
+    tol = (tol + 2 * 2.0 ** -16 * prod).reshape(T, N, C)
+    within("dX", down(out), ref, tol + P["bf16"] * (np.abs(ref) + tol))
+    within("dw", down(dw), rdw, (kr + 4 + T) * U * (np.abs(xf).T @ (dz / r)) + 1e-37)
