@@ -696,7 +696,8 @@ int hc_gated_scan_backward(const void* x, const void* gate, const void* y, const
  * xhc_balance_loss - keeps the xHC router from choosing the same streams for every
  * token: over B sequences of S tokens, for sequence b with n_b unmasked tokens,
  *   count[b, i] = its tokens whose active set idx holds stream i (a token's entries
- *     are distinct, as the forward writes them; entries outside [0, N) count nowhere), p_tj = score[t, j] / sum_j score[t, j] (0 where the sum is 0),
+ *     are distinct, as the forward writes them; entries outside [0, N) count nowhere),
+ *   p_tj = score[t, j] / sum_j score[t, j] (0 where the sum is 0),
  *   P[b, j] = mean_t p_tj, f_bj = E / ((k - m) n_b) * count[b, m + j], E = N - m,
  *   loss = coef / B * sum_b sum_j f_bj P_bj  (coef when the choice is even).
  *   score [T, E] float32 and idx [T, k] int32 as xhc_pre or xhc_route wrote them

@@ -348,7 +348,8 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void rms_norm_kernel(
       for (int it = 0; it < ITEMS; ++it)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (MODE != 2 || (it * NT + tid) * 8 + (VEC ? 0 : e) < C) top = max(top, __float_as_uint(v[it][e]) & 0x7fffffffu);
+          if (MODE != 2 || (it * NT + tid) * 8 + (VEC ? 0 : e) < C)
+            top = max(top, __float_as_uint(v[it][e]) & 0x7fffffffu);
       int k;
       if (scale_of(row_umax<WAVE>(top, redm[parity]), a.eps, k)) {
         ss = 0.f;
@@ -617,11 +618,12 @@ __global__ __launch_bounds__(1024) void column_sum_kernel(const float* __restric
 // Launch shape of a pass over T rows of C channels: pieces per thread, threads, and
 // the workgroups, bounded so that each keeps the weight in registers over several rows
 // and reads ahead. Measured against each other, by events over changing inputs, at 8,192 x
-// 4,096 with residual and e4m3 groups / 16,384 x 4 x 7,168: forward with two pieces a thread and 16,384 waves 42.8 / 248 us (8,192 waves 43.9
-// / 261; one piece, 6,144 waves 41.6 / 264, 16,384 waves 43.5 / 260). The backward keeps 256
-// CUs equally busy, with up to 16 waves each (bfloat16, 8,192 rows of 2,560 / 4,096 / 7,168
-// channels: 36 / 50 / 97 us; 4,096 waves in all, however they fall, 50 / 51 / 156; one
-// workgroup each 49 / 49 / 98) and one piece a thread up to 8,192 channels.
+// 4,096 with residual and e4m3 groups / 16,384 x 4 x 7,168: forward with two pieces a
+// thread and 16,384 waves 42.8 / 248 us (8,192 waves 43.9 / 261; one piece, 6,144 waves
+// 41.6 / 264, 16,384 waves 43.5 / 260). The backward keeps 256 CUs equally busy, with up to
+// 16 waves each (bfloat16, 8,192 rows of 2,560 / 4,096 / 7,168 channels: 36 / 50 / 97 us;
+// 4,096 waves in all, however they fall, 50 / 51 / 156; one workgroup each 49 / 49 / 98) and
+// one piece a thread up to 8,192 channels.
 struct RowShape {
   int items;
   bool wave;
