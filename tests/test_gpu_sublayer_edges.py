@@ -274,7 +274,7 @@ def test_router_backward_over_its_range_of_states(size):
     z = np.abs(np.log(s64) - np.log1p(-s64))
     kr = (N * C / 256 + 10) / 2 + 8
     prod = (dz / r) @ np.abs(w64).T
-    tol = U * (prod * (kr + E + 4) + np.abs(xf) / (r * r * N * C) * ((dz * (z + 1)).sum(1, keepdims=True) * (2 * kr + 16)))
-    tol = (tol + 2 * 2.0 ** -16 * prod).reshape(T, N, C)
+    along = np.abs(xf) / (r * r * N * C) * ((dz * (z + 1)).sum(1, keepdims=True) * (2 * kr + 16))
+    tol = (U * (prod * (kr + E + 4) + along) + 2 * 2.0 ** -16 * prod).reshape(T, N, C)
     within("dX", down(out), ref, tol + P["bf16"] * (np.abs(ref) + tol))
     within("dw", down(dw), rdw, (kr + 4 + T) * U * (np.abs(xf).T @ (dz / r)) + 1e-37)
