@@ -644,6 +644,38 @@ int hc_rms_norm_backward(const void* s, int dtype, int64_t T, int64_t C, const f
                          const void* dy, const void* ds, void* dx, float* dweight, void* workspace,
                          int64_t workspace_bytes, void* stream);
 
+/*
+ * hc_layer_norm - layer norm of a sublayer's input, otherwise as hc_rms_norm:
+ *   v = x + residual (x alone when residual is NULL), mean = mean_c v,
+ *   y = (v - mean) / sqrt(mean_c (v - mean)^2 + eps) * weight + bias.
+ *   weight, bias [C] float32 (NULL: ones, zeros); a row whose variance + eps is 0 (equal
+ *   values) gives y = bias. s, y, y_dtype, group, scale, limits and types as hc_rms_norm's.
+ *   Statistics are float32: the variance is that of the deviations from the mean, and a
+ *   row far off zero (deviations within 2^-15 of the mean) or out of float32's squares'
+ *   range is normalised as any other.
+ *
+ * hc_pre_layer_norm - hc_pre followed by the layer norm in one pass over the state; X,
+ *   h_pre, n and F_in as hc_pre_norm's.
+ *
+ * hc_layer_norm_backward - gradients of both for the upstream gradient dy [T, C] of y:
+ *   with v = s as stored, n = (v - mean) rstd and u = weight dy,
+ *   dx = rstd (u - mean_c u - n mean_c(u n)) + ds, stored in the stream dtype, rounded once;
+ *   dweight[c] = sum_t dy n, dbias[c] = sum_t dy, float32 (each may be NULL: not formed;
+ *   T = 0 gives zeros). s, dy, ds, dx as hc_rms_norm_backward's; dx may be ds.
+ *   Workspace: hc_layer_norm_backward_workspace_bytes(T, C) (0 for T = 0; may be NULL when
+ *   dweight and dbias are). Deterministic: every sum runs in a fixed order.
+ * All: alignment and overlap as for the calls above.
+ */
+int hc_layer_norm(const void* x, int dtype, int64_t T, int64_t C, const void* residual, const float* weight,
+                  const float* bias, float eps, void* s, int y_dtype, int group, void* y, float* scale, void* stream);
+int hc_pre_layer_norm(const void* X, int dtype, int64_t T, int n, int64_t C, const float* h_pre, const float* weight,
+                      const float* bias, float eps, void* F_in, int y_dtype, int group, void* y, float* scale,
+                      void* stream);
+int64_t hc_layer_norm_backward_workspace_bytes(int64_t T, int64_t C);
+int hc_layer_norm_backward(const void* s, int dtype, int64_t T, int64_t C, const float* weight, float eps,
+                           const void* dy, const void* ds, void* dx, float* dweight, float* dbias, void* workspace,
+                           int64_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------ gated linear recurrence -- */
 
 /*

@@ -1,8 +1,8 @@
 """Plain float64 forms of the operators beside the stream mixing (tests only).
 
-The root-mean-square norm with its 8-bit codes, the gated linear recurrence, the
-router's balance loss and the router's backward, each with its gradient, written
-one token at a time from the definitions in include/hc.h.
+The root-mean-square norm and the layer norm with their 8-bit codes, the gated linear
+recurrence, the router's balance loss and the router's backward, each with its gradient,
+written one token at a time from the definitions in include/hc.h.
 """
 from __future__ import annotations
 
@@ -40,6 +40,31 @@ def rms_norm_backward(v, weight, eps, dy, ds=None):
     if ds is not None:
         dx = dx + np.asarray(ds, np.float64)
     return dx, (dy * vh).sum(0)
+
+
+def layer_norm(v, weight, bias, eps):
+    """y of rows v [T, C]; a row whose variance + eps is 0 gives the bias."""
+    v = np.asarray(v, np.float64)
+    w = np.ones(v.shape[1]) if weight is None else np.asarray(weight, np.float64)
+    b = np.zeros(v.shape[1]) if bias is None else np.asarray(bias, np.float64)
+    d = v - v.mean(1, keepdims=True)
+    var = (d * d).mean(1, keepdims=True) + eps
+    rstd = np.where(var > 0, 1 / np.sqrt(np.where(var > 0, var, 1)), 0.0)
+    return d * rstd * w + b
+
+
+def layer_norm_backward(v, weight, eps, dy, ds=None):
+    """(dx, dweight, dbias)."""
+    v, dy = np.asarray(v, np.float64), np.asarray(dy, np.float64)
+    w = np.ones(v.shape[1]) if weight is None else np.asarray(weight, np.float64)
+    d = v - v.mean(1, keepdims=True)
+    var = (d * d).mean(1, keepdims=True) + eps
+    rstd = np.where(var > 0, 1 / np.sqrt(np.where(var > 0, var, 1)), 0.0)
+    n, u = d * rstd, w * dy
+    dx = rstd * (u - u.mean(1, keepdims=True) - n * (u * n).mean(1, keepdims=True))
+    if ds is not None:
+        dx = dx + np.asarray(ds, np.float64)
+    return dx, (dy * n).sum(0), dy.sum(0)
 
 
 def quant_scales(y, kind, group):

@@ -88,6 +88,13 @@ _SIGS = {
     "hc_rms_norm_backward_workspace_bytes": (_c_i64, [_c_i64, _c_i64]),
     "hc_rms_norm_backward": (_c_int, [_vp, _c_int, _c_i64, _c_i64, _vp, _c_float, _vp, _vp, _vp, _vp, _vp, _c_i64,
                                       _vp]),
+    "hc_layer_norm": (_c_int, [_vp, _c_int, _c_i64, _c_i64, _vp, _vp, _vp, _c_float, _vp, _c_int, _c_int, _vp, _vp,
+                               _vp]),
+    "hc_pre_layer_norm": (_c_int, [_vp, _c_int, _c_i64, _c_int, _c_i64, _vp, _vp, _vp, _c_float, _vp, _c_int, _c_int,
+                                   _vp, _vp, _vp]),
+    "hc_layer_norm_backward_workspace_bytes": (_c_i64, [_c_i64, _c_i64]),
+    "hc_layer_norm_backward": (_c_int, [_vp, _c_int, _c_i64, _c_i64, _vp, _c_float, _vp, _vp, _vp, _vp, _vp, _vp,
+                                        _c_i64, _vp]),
     "hc_gated_scan_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64]),
     "hc_gated_scan": (_c_int, [_vp, _vp, _c_int, _c_i64, _c_i64, _c_i64, _vp, _vp, _c_int, _vp, _vp, _vp, _c_i64,
                                _vp]),
@@ -982,6 +989,99 @@ def hc_rms_norm_backward(s, weight, dy, eps=1e-6, *, ds=None, want_dweight=True,
             _ptr(s), _DT[s.dtype], T, C, _ptr(weight), float(eps), _ptr(dy), _ptr(ds), _ptr(dx), _ptr(dw), _ptr(ws),
             0 if ws is None else _nbytes(ws), _stream(dev, stream)))
     return dx, dw
+
+
+def hc_layer_norm(x, weight=None, bias=None, eps=1e-5, *, residual=None, quant=None, group=0, s_out=None, out=None,
+                  stream=None):
+    """y = (v - mean) / sqrt(var + eps) * weight + bias of v = x [T, C] (+ residual); quant, group, s_out,
+    out and the returned dict(y[, s][, scale]) as hc_rms_norm's."""
+    x = _matrix(x, "x")
+    T, C = x.shape
+    dev = x.device
+    weight, code, ngroups = _norm_args(x, weight, C, quant, group)
+    if bias is not None:
+        bias = _f32(bias, "bias", (C,), dev)
+    with _on(dev, stream):
+        s = None
+        if residual is not None:
+            residual = _dev_tensor(residual, "residual", (x.dtype,), (T, C), dev)
+            s = torch.empty_like(x) if s_out is None else _dev_tensor(s_out, "s out", (x.dtype,), (T, C), dev)
+        elif s_out is not None:
+            raise ValueError("s_out needs a residual")
+        y, scale = _norm_outs(out, x, T, C, quant, ngroups)
+        _check("hc_layer_norm", lib().hc_layer_norm(
+            _ptr(x), _DT[x.dtype], T, C, _ptr(residual), _ptr(weight), _ptr(bias), float(eps), _ptr(s), code,
+            int(group), _ptr(y), _ptr(scale), _stream(dev, stream)))
+    res = dict(y=y)
+    if s is not None:
+        res["s"] = s
+    if scale is not None:
+        res["scale"] = scale
+    return res
+
+
+def hc_pre_layer_norm(X, h_pre, weight=None, bias=None, eps=1e-5, *, quant=None, group=0, want_F_in=True,
+                      F_in_out=None, out=None, stream=None):
+    """hc_pre and the layer norm of its result in one pass; arguments and the returned dict(y[, F_in]
+    [, scale]) as hc_pre_norm's."""
+    X = _state(X)
+    T, n, C = X.shape
+    dev = X.device
+    h_pre = _f32(h_pre, "h_pre", (T, n), dev)
+    weight, code, ngroups = _norm_args(X, weight, C, quant, group)
+    if bias is not None:
+        bias = _f32(bias, "bias", (C,), dev)
+    with _on(dev, stream):
+        F_in = None
+        if want_F_in or F_in_out is not None:
+            F_in = _stream_out(F_in_out, "F_in out", (T, C), X.dtype, dev)
+        y, scale = _norm_outs(out, X, T, C, quant, ngroups)
+        _check("hc_pre_layer_norm", lib().hc_pre_layer_norm(
+            _ptr(X), _DT[X.dtype], T, n, C, _ptr(h_pre), _ptr(weight), _ptr(bias), float(eps), _ptr(F_in), code,
+            int(group), _ptr(y), _ptr(scale), _stream(dev, stream)))
+    res = dict(y=y)
+    if F_in is not None:
+        res["F_in"] = F_in
+    if scale is not None:
+        res["scale"] = scale
+    return res
+
+
+def hc_layer_norm_backward_workspace_bytes(T: int, C: int) -> int:
+    return int(lib().hc_layer_norm_backward_workspace_bytes(T, C))
+
+
+def hc_layer_norm_backward(s, weight, dy, eps=1e-5, *, ds=None, want_dweight=True, out=None, workspace=None,
+                           stream=None):
+    """Backward of hc_layer_norm (s: its s, or x without a residual) and of hc_pre_layer_norm's norm (s:
+    F_in): (dx, dweight, dbias), the last two None without want_dweight, for the gradient dy of y and ds
+    of s (dx may be ds). out = (dx, dweight, dbias)."""
+    s = _matrix(s, "s")
+    T, C = s.shape
+    dev = s.device
+    if weight is not None:
+        weight = _f32(weight, "weight", (C,), dev)
+    dy = _dev_tensor(dy, "dy", (s.dtype,), (T, C), dev)
+    if ds is not None:
+        ds = _dev_tensor(ds, "ds", (s.dtype,), (T, C), dev)
+    dx, dw, db = (None, None, None) if out is None else out
+    with _on(dev, stream):
+        dx = _stream_out(dx, "dx out", (T, C), s.dtype, dev)
+        if dw is not None:
+            dw = _f32(dw, "dweight out", (C,), dev)
+        elif want_dweight:
+            dw = torch.empty(C, dtype=torch.float32, device=dev)
+        if db is not None:
+            db = _f32(db, "dbias out", (C,), dev)
+        elif want_dweight:
+            db = torch.empty(C, dtype=torch.float32, device=dev)
+        ws = None
+        if dw is not None or db is not None:
+            ws = _workspace(hc_layer_norm_backward_workspace_bytes(T, C), dev, workspace)
+        _check("hc_layer_norm_backward", lib().hc_layer_norm_backward(
+            _ptr(s), _DT[s.dtype], T, C, _ptr(weight), float(eps), _ptr(dy), _ptr(ds), _ptr(dx), _ptr(dw), _ptr(db),
+            _ptr(ws), 0 if ws is None else _nbytes(ws), _stream(dev, stream)))
+    return dx, dw, db
 
 
 # ---------------------------------------------------- gated linear recurrence

@@ -1504,6 +1504,77 @@ int hc_rms_norm_backward(const void* s, int dtype, int64_t T, int64_t C, const f
   return launch_status(hc::launch_rms_norm_backward(dtype, vec, a, dweight, (hipStream_t)stream));
 }
 
+int hc_layer_norm(const void* x, int dtype, int64_t T, int64_t C, const void* residual, const float* weight,
+                  const float* bias, float eps, void* s, int y_dtype, int group, void* y, float* scale, void* stream) {
+  int r = check_norm(dtype, T, C, eps, y_dtype, group);
+  if (r != HC_OK || T == 0) return r;
+  if (s && !residual) return HC_ERR_NULL;
+  const int64_t e = (int64_t)esize(dtype), xb = T * C * e;
+  Buf by, bs;
+  int64_t ngroups;
+  norm_outs(dtype, T, C, y_dtype, group, y, scale, by, bs, ngroups);
+  const Buf bx{x, xb, (uintptr_t)e, true}, br{residual, xb, (uintptr_t)e, false}, bw{weight, C * 4, 4, false},
+      bb{bias, C * 4, 4, false}, bo{s, xb, (uintptr_t)e, false};
+  if ((r = check_bufs({bx, br, bw, bb, bo, by, bs})) != HC_OK) return r;
+  if (bufs_overlap({by, bs}, {bx, br, bw, bb, bo}) || bufs_overlap({bo}, {bx, bw, bb}) ||
+      (s != residual && overlaps(s, xb, residual, xb)))
+    return HC_ERR_ALIAS;
+  if ((r = device_status()) != HC_OK) return r;
+  const bool q8 = y_dtype != dtype;
+  const bool vec = vec_ok(C, {x, residual, weight, bias, s}) && aligned_to(y, q8 ? 8 : 16);
+  const hc::NormArgs a{x, residual, nullptr, weight, s, y, scale, T, C, ngroups, 1, q8 ? y_dtype : 0, group, eps};
+  return launch_status(hc::launch_layer_norm(dtype, residual ? 1 : 0, vec, a, bias, (hipStream_t)stream));
+}
+
+int hc_pre_layer_norm(const void* X, int dtype, int64_t T, int n, int64_t C, const float* h_pre, const float* weight,
+                      const float* bias, float eps, void* F_in, int y_dtype, int group, void* y, float* scale,
+                      void* stream) {
+  int r = check_norm(dtype, T, C, eps, y_dtype, group);
+  if (r != HC_OK) return r;
+  if (n < 1 || n > HC_MAX_STREAMS) return HC_ERR_SHAPE;
+  if (T == 0) return HC_OK;
+  const int64_t e = (int64_t)esize(dtype), fb = T * C * e;
+  Buf by, bs;
+  int64_t ngroups;
+  norm_outs(dtype, T, C, y_dtype, group, y, scale, by, bs, ngroups);
+  const Buf bx{X, fb * n, (uintptr_t)e, true}, bh{h_pre, T * n * 4, 4, true}, bw{weight, C * 4, 4, false},
+      bb{bias, C * 4, 4, false}, bo{F_in, fb, (uintptr_t)e, false};
+  if ((r = check_bufs({bx, bh, bw, bb, bo, by, bs})) != HC_OK) return r;
+  if (bufs_overlap({by, bs, bo}, {bx, bh, bw, bb})) return HC_ERR_ALIAS;
+  if ((r = device_status()) != HC_OK) return r;
+  const bool q8 = y_dtype != dtype;
+  const bool vec = vec_ok(C, {X, weight, bias, F_in}) && aligned_to(y, q8 ? 8 : 16);
+  const hc::NormArgs a{X, nullptr, h_pre, weight, F_in, y, scale, T, C, ngroups, n, q8 ? y_dtype : 0, group, eps};
+  return launch_status(hc::launch_layer_norm(dtype, 2, vec, a, bias, (hipStream_t)stream));
+}
+
+int64_t hc_layer_norm_backward_workspace_bytes(int64_t T, int64_t C) {
+  const int64_t one = hc_rms_norm_backward_workspace_bytes(T, C);
+  return one < 0 ? -1 : 2 * one;
+}
+
+int hc_layer_norm_backward(const void* s, int dtype, int64_t T, int64_t C, const float* weight, float eps,
+                           const void* dy, const void* ds, void* dx, float* dweight, float* dbias, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  int r = check_norm(dtype, T, C, eps, dtype, 0);
+  const bool sums = dweight || dbias;
+  if (r != HC_OK || (T == 0 && !sums)) return r;
+  const int64_t e = (int64_t)esize(dtype), xb = T * C * e;
+  const int64_t wsb = sums ? hc_layer_norm_backward_workspace_bytes(T, C) : 0;
+  const Buf bv{s, xb, (uintptr_t)e, T > 0}, bw{weight, C * 4, 4, false}, bd{dy, xb, (uintptr_t)e, T > 0},
+      bs{ds, xb, (uintptr_t)e, false}, bx{dx, xb, (uintptr_t)e, T > 0}, bg{dweight, C * 4, 4, false},
+      bb{dbias, C * 4, 4, false}, bk{wsb ? workspace : nullptr, wsb, 1, false};
+  if ((r = check_bufs({bv, bw, bd, bs, bx, bg, bb})) != HC_OK) return r;
+  if ((r = check_ws(workspace, workspace_bytes, wsb)) != HC_OK) return r;
+  if (bufs_overlap({bx, bg, bb, bk}, {bv, bw, bd}) || bufs_overlap({bg, bb, bk}, {bs}) ||
+      (dx != ds && overlaps(dx, xb, ds, xb)))
+    return HC_ERR_ALIAS;
+  if ((r = device_status()) != HC_OK) return r;
+  const bool vec = vec_ok(C, {s, weight, dy, ds, dx});
+  const hc::NormBwdArgs a{s, weight, dy, ds, dx, sums ? (float*)workspace : nullptr, T, C, eps};
+  return launch_status(hc::launch_layer_norm_backward(dtype, vec, a, dweight, dbias, (hipStream_t)stream));
+}
+
 // ------------------------------------------------- gated linear recurrence
 
 static int check_scan_shape(int dtype, int64_t B, int64_t S, int64_t C) {

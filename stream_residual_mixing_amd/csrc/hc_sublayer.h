@@ -38,6 +38,14 @@ struct NormBwdArgs {
 };
 int64_t norm_backward_parts(int64_t T, int64_t C);
 hipError_t launch_rms_norm_backward(int dtype, bool vec, const NormBwdArgs& a, float* dw, hipStream_t st);
+// out0[c], out1[c] = the sums over P parts of [P, C], the second array's parts behind the
+// first's; either may be NULL
+hipError_t launch_column_sums(const float* parts, int64_t P, int64_t C, float* out0, float* out1, hipStream_t st);
+
+// ---- layer norm (hc_layer_norm.hip): as above, b the bias (may be NULL)
+hipError_t launch_layer_norm(int dtype, int mode, bool vec, const NormArgs& a, const float* b, hipStream_t st);
+// dw, db may be NULL; part (NULL when both are) [2, norm_backward_parts(T, C), C]
+hipError_t launch_layer_norm_backward(int dtype, bool vec, const NormBwdArgs& a, float* dw, float* db, hipStream_t st);
 
 // ---- gated linear recurrence (hc_scan.hip)
 // Forward: y, last from x, gate, h0. Backward (bwd): dx, dgate, dh0 from x, gate, y,
