@@ -77,6 +77,7 @@ extern "C" {
 #define HC_MAX_FLASH_SUBLAYERS 4 /* L, sublayers of an xHC-Flash block */
 #define HC_MAX_NORM_CHANNELS 16384 /* C of the norm calls */
 #define HC_MAX_ROUTER_STREAMS 16   /* N of xhc_router_backward */
+#define HC_MAX_HEAD 256            /* Dk and Dv of the gated delta rule */
 
 /* Human-readable text of a status code (static string, never NULL). */
 const char* hc_status_string(int status);
@@ -721,6 +722,40 @@ int hc_gated_scan_backward(const void* x, const void* gate, const void* y, const
                            int64_t S, int64_t C, const float* h0, const float* dh_last, const int32_t* lengths,
                            int tied, void* dx, void* dgate, float* dh0, void* workspace, int64_t workspace_bytes,
                            void* stream);
+
+/* ------------------------------------------------------- gated delta rule -- */
+
+/*
+ * hc_gated_delta - the gated delta rule, a linear recurrence whose state is a matrix for each head,
+ * as a sublayer function beside hc_gated_scan, over B sequences of S tokens:
+ *   F = exp(g_t) M_{t-1},  z_t = v_t - F^T k_t,  M_t = F + beta_t k_t z_t^T,
+ *   o_t = scale M_t^T q_t, per value head; M_{-1} = state0.
+ *   q, k [B, S, Hk, Dk], v, o [B, S, Hv, Dv] stream dtype; value head h reads key head
+ *   h / (Hv / Hk). g [B, S, Hv] float32: the decay's logarithm, <= 0 (-infinity forgets all that was
+ *   before; taken as -200 below that, which is 0 in float32); beta [B, S, Hv] float32. The state
+ *   stays bounded for keys of unit length (hc_rms_norm over Dk with a weight of 1 / sqrt(Dk)) and
+ *   0 <= beta <= 2.
+ *   state0 (NULL: zeros) and state (NULL: not stored) [B, Hv, Dk, Dv] float32: before the first and
+ *   after the last token, so that a sequence can go on in a later call (S = 1: one new token each).
+ *   state may be state0.
+ *   lengths (NULL: S each) [B] int32 device array, as hc_gated_scan's: behind a sequence's length
+ *   nothing is used, o is left as it was, and state is the one after its last token.
+ *   The state and every sum are float32; o is rounded once. More than a few tokens are taken in
+ *   chunks of 64, whose products hold 16 bits of each factor that is not bfloat16 already: each
+ *   term of the state is off by at most about 2^-16 of itself. Deterministic. A NaN or an infinity
+ *   spoils its head from its chunk's first token on.
+ *   dtype HC_F32 or HC_BF16; Hv a multiple of Hk; 1 <= Dk, Dv <= HC_MAX_HEAD; S = 0 passes the state on
+ *   (B = 0 does nothing); B * Hv * max(8, ceil(S / 64)) < 2^23 (else HC_ERR_SHAPE); arrays aligned to
+ *   their element size; workspace hc_gated_delta_workspace_bytes bytes (-1 for invalid sizes; may be
+ *   NULL when that is 0), 256-byte aligned. Outputs overlap no input (but as stated), other output or
+ *   workspace (HC_ERR_ALIAS).
+ */
+int64_t hc_gated_delta_workspace_bytes(int64_t B, int64_t S, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
+                                       int dtype);
+int hc_gated_delta(const void* q, const void* k, const void* v, int dtype, int64_t B, int64_t S, int64_t Hk,
+                   int64_t Hv, int64_t Dk, int64_t Dv, const float* g, const float* beta, float scale,
+                   const float* state0, const int32_t* lengths, void* o, float* state, void* workspace,
+                   int64_t workspace_bytes, void* stream);
 
 /* --------------------------------------------- training the stream router -- */
 

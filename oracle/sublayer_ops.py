@@ -119,6 +119,68 @@ def gated_scan_backward(x, gate, y, dy, h0=None, dh_last=None, lengths=None, tie
     return dx, dgate, R
 
 
+# --------------------------------------------------------------- delta rule
+
+
+def gated_delta(q, k, v, g, beta, state=None, lengths=None, scale=None, o_init=None):
+    """(o [B, S, Hv, Dv], last state [B, Hv, Dk, Dv]); rows behind a length keep o_init."""
+    q, k, v, g, beta = (np.asarray(x, np.float64) for x in (q, k, v, g, beta))
+    B, S, Hk, Dk = q.shape
+    Hv, Dv = v.shape[2:]
+    scale = Dk ** -0.5 if scale is None else scale
+    o = np.zeros((B, S, Hv, Dv)) if o_init is None else np.array(o_init, np.float64)
+    M = np.zeros((B, Hv, Dk, Dv)) if state is None else np.array(state, np.float64)
+    for b in range(B):
+        n = S if lengths is None else int(np.clip(lengths[b], 0, S))
+        for h in range(Hv):
+            m, kh = M[b, h], h // (Hv // Hk)
+            for t in range(n):
+                kt = k[b, t, kh]
+                F = np.exp(g[b, t, h]) * m
+                m = F + beta[b, t, h] * np.outer(kt, v[b, t, h] - F.T @ kt)
+                o[b, t, h] = scale * (m.T @ q[b, t, kh])
+            M[b, h] = m
+    return o, M
+
+
+def gated_delta_backward(q, k, v, g, beta, do, state=None, dstate=None, lengths=None, scale=None):
+    """(dq, dk, dv, dg, dbeta, dstate0)."""
+    q, k, v, g, beta, do = (np.asarray(x, np.float64) for x in (q, k, v, g, beta, do))
+    B, S, Hk, Dk = q.shape
+    Hv, Dv = v.shape[2:]
+    scale = Dk ** -0.5 if scale is None else scale
+    dq, dk, dv, dg, db = (np.zeros_like(x) for x in (q, k, v, g, beta))
+    R = np.zeros((B, Hv, Dk, Dv)) if dstate is None else np.array(dstate, np.float64)
+    for b in range(B):
+        n = S if lengths is None else int(np.clip(lengths[b], 0, S))
+        for h in range(Hv):
+            kh = h // (Hv // Hk)
+            m = np.zeros((Dk, Dv)) if state is None else np.asarray(state[b, h], np.float64)
+            steps = []
+            for t in range(n):
+                kt = k[b, t, kh]
+                F = np.exp(g[b, t, h]) * m
+                z = v[b, t, h] - F.T @ kt
+                m = F + beta[b, t, h] * np.outer(kt, z)
+                steps.append((F, z, m))
+            r = R[b, h]
+            for t in range(n - 1, -1, -1):
+                F, z, m = steps[t]
+                kt = k[b, t, kh]
+                d = scale * do[b, t, h]
+                r = r + np.outer(q[b, t, kh], d)
+                dz = beta[b, t, h] * (r.T @ kt)
+                dF = r - np.outer(kt, dz)
+                dq[b, t, kh] += m @ d
+                dk[b, t, kh] += beta[b, t, h] * (r @ z) - F @ dz
+                dv[b, t, h] = dz
+                db[b, t, h] = (r.T @ kt) @ z
+                dg[b, t, h] = (dF * F).sum()
+                r = np.exp(g[b, t, h]) * dF
+            R[b, h] = r
+    return dq, dk, dv, dg, db, R
+
+
 # ------------------------------------------------------------------- router
 
 

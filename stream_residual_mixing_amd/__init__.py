@@ -100,6 +100,9 @@ _SIGS = {
                                _vp]),
     "hc_gated_scan_backward": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_i64, _c_i64, _c_i64, _vp, _vp, _vp, _c_int,
                                         _vp, _vp, _vp, _vp, _c_i64, _vp]),
+    "hc_gated_delta_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_int]),
+    "hc_gated_delta": (_c_int, [_vp, _vp, _vp, _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _vp,
+                                _c_float, _vp, _vp, _vp, _vp, _vp, _c_i64, _vp]),
     "xhc_balance_loss_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_int, _c_int]),
     "xhc_balance_loss": (_c_int, [_vp, _vp, _vp, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_float, _vp, _vp, _vp, _vp,
                                   _vp, _c_i64, _vp]),
@@ -1159,6 +1162,64 @@ def hc_gated_scan_backward(x, gate, y, dy, h0=None, dh_last=None, *, lengths=Non
             int(bool(tied)), _ptr(dx), _ptr(dgate), _ptr(dh0), _ptr(ws), 0 if ws is None else _nbytes(ws),
             _stream(dev, stream)))
     return dx, dgate, dh0
+
+
+# ------------------------------------------------------- gated delta rule
+
+
+def hc_gated_delta_workspace_bytes(B: int, S: int, Hk: int, Hv: int, Dk: int, Dv: int, dtype) -> int:
+    return int(lib().hc_gated_delta_workspace_bytes(B, S, Hk, Hv, Dk, Dv, _DT[dtype]))
+
+
+def _delta_args(q, k, v, g, beta, state, lengths):
+    """The checked inputs' sizes (B, S, Hk, Hv, Dk, Dv)."""
+    q = _dev_tensor(q, "q", _DT)
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, S, Hk, Dk], got shape {tuple(q.shape)}")
+    B, S, Hk, Dk = q.shape
+    dev = q.device
+    _dev_tensor(k, "k", (q.dtype,), (B, S, Hk, Dk), dev)
+    _dev_tensor(v, "v", (q.dtype,), device=dev)
+    if v.dim() != 4 or v.shape[0] != B or v.shape[1] != S:
+        raise ValueError(f"v has shape {tuple(v.shape)}, expected ({B}, {S}, Hv, Dv)")
+    Hv, Dv = v.shape[2], v.shape[3]
+    if Hk < 1 or Hv % Hk:
+        raise ValueError(f"{Hv} value heads cannot share {Hk} key heads")
+    _f32(g, "g", (B, S, Hv), dev)
+    _f32(beta, "beta", (B, S, Hv), dev)
+    if state is not None:
+        _f32(state, "state", (B, Hv, Dk, Dv), dev)
+    if lengths is not None:
+        _i32(lengths, "lengths", (B,), dev)
+    return B, S, Hk, Hv, Dk, Dv
+
+
+def hc_gated_delta(q, k, v, g, beta, state=None, *, lengths=None, scale=None, want_state=True, out=None,
+                   workspace=None, stream=None):
+    """M_t = exp(g_t) M_{t-1} + beta_t k_t (v_t - exp(g_t) M_{t-1}^T k_t)^T, o_t = scale M_t^T q_t, over
+    q, k [B, S, Hk, Dk], v [B, S, Hv, Dv], g (<= 0), beta [B, S, Hv] float32; state [B, Hv, Dk, Dv]
+    float32, lengths [B] int32, scale None: 1 / sqrt(Dk). Returns (o [B, S, Hv, Dv], the last state or
+    None); out = (o, state), its state may be the given one. Rows behind a sequence's length are zero in
+    an o that the call allocates, and left as they are in a given one."""
+    B, S, Hk, Hv, Dk, Dv = _delta_args(q, k, v, g, beta, state, lengths)
+    dev = q.device
+    o, last = (None, None) if out is None else out
+    if last is not None:
+        _f32(last, "state out", (B, Hv, Dk, Dv), dev)
+    with _on(dev, stream):
+        if o is None:  # padding is not written: what the allocator hands out must not be left in it
+            o = torch.empty_like(v) if lengths is None else torch.zeros_like(v)
+        else:
+            o = _dev_tensor(o, "o out", (q.dtype,), (B, S, Hv, Dv), dev)
+        if last is None and want_state:
+            last = torch.empty(B, Hv, Dk, Dv, dtype=torch.float32, device=dev)
+        nbytes = hc_gated_delta_workspace_bytes(B, S, Hk, Hv, Dk, Dv, q.dtype)
+        ws = None if nbytes == 0 else _workspace(nbytes, dev, workspace)
+        _check("hc_gated_delta", lib().hc_gated_delta(
+            _ptr(q), _ptr(k), _ptr(v), _DT[q.dtype], B, S, Hk, Hv, Dk, Dv, _ptr(g), _ptr(beta),
+            Dk ** -0.5 if scale is None else float(scale), _ptr(state), _ptr(lengths), _ptr(o), _ptr(last), _ptr(ws),
+            0 if ws is None else _nbytes(ws), _stream(dev, stream)))
+    return o, last
 
 
 # ------------------------------------------------- training the stream router

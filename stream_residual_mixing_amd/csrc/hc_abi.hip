@@ -1644,6 +1644,61 @@ int hc_gated_scan_backward(const void* x, const void* gate, const void* y, const
       dtype, true, scan_vec(C, dtype, {x, gate, y, dy, dx, dgate}, {h0, dh_last, dh0}), a, (hipStream_t)stream));
 }
 
+// ------------------------------------------------------- gated delta rule
+
+static int check_delta_shape(int dtype, int64_t B, int64_t S, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv) {
+  if (!dtype_ok(dtype)) return HC_ERR_DTYPE;
+  if (B < 0 || S < 0 || Hk < 1 || Hv < 1 || Hv % Hk != 0 || Dk < 1 || Dk > HC_MAX_HEAD || Dv < 1 || Dv > HC_MAX_HEAD)
+    return HC_ERR_SHAPE;
+  // the grids: a workgroup of 256 threads for each 64 tokens, and for each 32 columns, of a head
+  const int64_t most = 1ll << 23, per = ((S > 512 ? S + 63 : 512) / 64);
+  if (B >= most || Hv >= most || per >= most || B * Hv >= most || B * Hv * per >= most) return HC_ERR_SHAPE;
+  return HC_OK;
+}
+
+int64_t hc_gated_delta_workspace_bytes(int64_t B, int64_t S, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
+                                       int dtype) {
+  if (check_delta_shape(dtype, B, S, Hk, Hv, Dk, Dv) != HC_OK) return -1;
+  return hc::delta_ws_bytes(B, S, Hv);
+}
+
+// rows in whole pieces of 8 keys, two columns (of a state, four where there are whole fours) at once
+static bool delta_vec(int dtype, int64_t Dk, int64_t Dv, std::initializer_list<const void*> keys,
+                      std::initializer_list<const void*> values, std::initializer_list<const void*> states) {
+  if (Dk % 8 != 0 || Dv % 2 != 0) return false;
+  for (const void* p : keys)
+    if (p && !aligned_to(p, 16)) return false;
+  for (const void* p : values)
+    if (p && !aligned_to(p, 2 * esize(dtype))) return false;
+  for (const void* p : states)
+    if (p && !aligned_to(p, Dv % 4 == 0 ? 16 : 8)) return false;
+  return true;
+}
+
+int hc_gated_delta(const void* q, const void* k, const void* v, int dtype, int64_t B, int64_t S, int64_t Hk,
+                   int64_t Hv, int64_t Dk, int64_t Dv, const float* g, const float* beta, float scale,
+                   const float* state0, const int32_t* lengths, void* o, float* state, void* workspace,
+                   int64_t workspace_bytes, void* stream) {
+  int r = check_delta_shape(dtype, B, S, Hk, Hv, Dk, Dv);
+  if (r != HC_OK || B == 0 || (S == 0 && !state)) return r;
+  const int64_t e = (int64_t)esize(dtype), kb = B * S * Hk * Dk * e, vb = B * S * Hv * Dv * e, gb = B * S * Hv * 4;
+  const int64_t sb = B * Hv * Dk * Dv * 4, wsb = hc::delta_ws_bytes(B, S, Hv);
+  const uintptr_t ea = (uintptr_t)e;
+  const Buf bq{q, kb, ea, S > 0}, bk{k, kb, ea, S > 0}, bv{v, vb, ea, S > 0}, bg{g, gb, 4, S > 0},
+      bb{beta, gb, 4, S > 0}, b0{state0, sb, 4, false}, bl{lengths, B * 4, 4, false}, bo{o, vb, ea, S > 0},
+      b1{state, sb, 4, false}, bw{wsb ? workspace : nullptr, wsb, 1, false};
+  if ((r = check_bufs({bq, bk, bv, bg, bb, b0, bl, bo, b1})) != HC_OK) return r;
+  if ((r = check_ws(workspace, workspace_bytes, wsb)) != HC_OK) return r;
+  if (bufs_overlap({bo, b1, bw}, {bq, bk, bv, bg, bb, bl}) || bufs_overlap({bo, bw}, {b0}) ||
+      (state != state0 && overlaps(state, sb, state0, sb)))
+    return HC_ERR_ALIAS;
+  if ((r = device_status()) != HC_OK) return r;
+  const hc::DeltaArgs a{q,         k,  v,  g,  beta, state0, lengths, o,
+                        state,     workspace, B, S, Hk, Hv, Dk, Dv, (S + 63) / 64, scale,
+                        delta_vec(dtype, Dk, Dv, {q, k}, {v, o}, {state0, state})};
+  return launch_status(hc::launch_delta(dtype, a, (hipStream_t)stream));
+}
+
 // ----------------------------------------------- training the stream router
 
 static int check_balance_shape(int64_t B, int64_t S, int N, int k, int m) {

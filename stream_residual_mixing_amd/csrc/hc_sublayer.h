@@ -69,6 +69,27 @@ struct ScanArgs {
 int64_t scan_ws_bytes(int64_t B, int64_t S, int64_t C);
 hipError_t launch_scan(int dtype, bool bwd, bool vec, const ScanArgs& a, hipStream_t st);
 
+// ---- gated delta rule (hc_delta.hip, hc_delta_backward.hip)
+// rec: the chunks' records in the workspace; NC = ceil(S / 64). vec: Dk % 8 == 0, Dv even, q and k
+// 16-byte aligned, v, o and the states at least to two elements (16 bytes where Dv % 4 == 0).
+struct DeltaArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  const float* beta;
+  const float* state0;     // may be NULL: zeros
+  const int32_t* lengths;  // may be NULL: S tokens each
+  void* o;
+  float* state1;           // may be NULL
+  void* rec;
+  int64_t B, S, Hk, Hv, Dk, Dv, NC;
+  float scale;
+  bool vec;
+};
+int64_t delta_ws_bytes(int64_t B, int64_t S, int64_t Hv);
+hipError_t launch_delta(int dtype, const DeltaArgs& a, hipStream_t st);
+
 // ---- balance loss and the router's backward (hc_router.hip)
 int64_t balance_ws_bytes(int64_t B, int64_t S, int N, int m);
 hipError_t launch_balance(const float* score, const int32_t* idx, const uint8_t* mask, int64_t B, int64_t S, int N,
