@@ -749,6 +749,19 @@ int hc_gated_scan_backward(const void* x, const void* gate, const void* y, const
  *   their element size; workspace hc_gated_delta_workspace_bytes bytes (-1 for invalid sizes; may be
  *   NULL when that is 0), 256-byte aligned. Outputs overlap no input (but as stated), other output or
  *   workspace (HC_ERR_ALIAS).
+ *
+ * hc_gated_delta_backward - gradients for the upstream gradients d_o [B, S, Hv, Dv] of o (stream dtype)
+ *   and dstate [B, Hv, Dk, Dv] float32 (NULL: zeros) of the last state, with respect to all inputs:
+ *   dq, dk [B, S, Hk, Dk] (summed over the value heads that read a key head) and dv [B, S, Hv, Dv]
+ *   stream dtype, rounded once; dg, dbeta [B, S, Hv] float32; dstate0 [B, Hv, Dk, Dv] float32 (NULL:
+ *   not stored). Zero behind a sequence's length. With R_t the gradient of M_t from later tokens,
+ *   N = R_t + scale q_t d_o_t^T, y = N^T k_t:
+ *   dq_t = scale M_t d_o_t,  dbeta_t = y . z_t,  dv_t = beta_t y,  dF = N - k_t dv_t^T,
+ *   dk_t = beta_t N z_t - F dv_t,  dg_t = <dF, F>,  R_{t-1} = exp(g_t) dF.
+ *   The states are formed again from the inputs. Sums are float32 and products hold 16 bits of each
+ *   factor, as the forward's; deterministic. Sizes and alignment as for the forward; workspace
+ *   hc_gated_delta_backward_workspace_bytes bytes, 256-byte aligned (for each 64 tokens of a value
+ *   head two states in 4 bytes an element, Z, W and 38 KB).
  */
 int64_t hc_gated_delta_workspace_bytes(int64_t B, int64_t S, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
                                        int dtype);
@@ -756,6 +769,13 @@ int hc_gated_delta(const void* q, const void* k, const void* v, int dtype, int64
                    int64_t Hv, int64_t Dk, int64_t Dv, const float* g, const float* beta, float scale,
                    const float* state0, const int32_t* lengths, void* o, float* state, void* workspace,
                    int64_t workspace_bytes, void* stream);
+int64_t hc_gated_delta_backward_workspace_bytes(int64_t B, int64_t S, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
+                                                int dtype);
+int hc_gated_delta_backward(const void* q, const void* k, const void* v, const void* d_o, int dtype, int64_t B,
+                            int64_t S, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, const float* g,
+                            const float* beta, float scale, const float* state0, const float* dstate,
+                            const int32_t* lengths, void* dq, void* dk, void* dv, float* dg, float* dbeta,
+                            float* dstate0, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* --------------------------------------------- training the stream router -- */
 

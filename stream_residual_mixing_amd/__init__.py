@@ -103,6 +103,10 @@ _SIGS = {
     "hc_gated_delta_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_int]),
     "hc_gated_delta": (_c_int, [_vp, _vp, _vp, _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _vp,
                                 _c_float, _vp, _vp, _vp, _vp, _vp, _c_i64, _vp]),
+    "hc_gated_delta_backward_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_int]),
+    "hc_gated_delta_backward": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64,
+                                         _vp, _vp, _c_float, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                         _c_i64, _vp]),
     "xhc_balance_loss_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_int, _c_int]),
     "xhc_balance_loss": (_c_int, [_vp, _vp, _vp, _c_i64, _c_i64, _c_int, _c_int, _c_int, _c_float, _vp, _vp, _vp, _vp,
                                   _vp, _c_i64, _vp]),
@@ -1220,6 +1224,34 @@ def hc_gated_delta(q, k, v, g, beta, state=None, *, lengths=None, scale=None, wa
             Dk ** -0.5 if scale is None else float(scale), _ptr(state), _ptr(lengths), _ptr(o), _ptr(last), _ptr(ws),
             0 if ws is None else _nbytes(ws), _stream(dev, stream)))
     return o, last
+
+
+def hc_gated_delta_backward_workspace_bytes(B: int, S: int, Hk: int, Hv: int, Dk: int, Dv: int, dtype) -> int:
+    return int(lib().hc_gated_delta_backward_workspace_bytes(B, S, Hk, Hv, Dk, Dv, _DT[dtype]))
+
+
+def hc_gated_delta_backward(q, k, v, g, beta, do, state=None, dstate=None, *, lengths=None, scale=None, out=None,
+                            workspace=None, stream=None):
+    """Backward of hc_gated_delta: (dq, dk, dv, dg, dbeta, dstate0) for the gradients do of o and dstate
+    of the last state (None: zeros); zero behind a sequence's length. out = these six, any of them None."""
+    B, S, Hk, Hv, Dk, Dv = _delta_args(q, k, v, g, beta, state, lengths)
+    dev = q.device
+    _dev_tensor(do, "do", (q.dtype,), (B, S, Hv, Dv), dev)
+    if dstate is not None:
+        _f32(dstate, "dstate", (B, Hv, Dk, Dv), dev)
+    outs = [None] * 6 if out is None else list(out)
+    like = (("dq", q.dtype, (B, S, Hk, Dk)), ("dk", q.dtype, (B, S, Hk, Dk)), ("dv", q.dtype, (B, S, Hv, Dv)),
+            ("dg", torch.float32, (B, S, Hv)), ("dbeta", torch.float32, (B, S, Hv)),
+            ("dstate0", torch.float32, (B, Hv, Dk, Dv)))
+    with _on(dev, stream):
+        outs = [_stream_out(o, f"{name} out", shape, dt, dev) for o, (name, dt, shape) in zip(outs, like)]
+        nbytes = hc_gated_delta_backward_workspace_bytes(B, S, Hk, Hv, Dk, Dv, q.dtype)
+        ws = None if nbytes == 0 else _workspace(nbytes, dev, workspace)
+        _check("hc_gated_delta_backward", lib().hc_gated_delta_backward(
+            _ptr(q), _ptr(k), _ptr(v), _ptr(do), _DT[q.dtype], B, S, Hk, Hv, Dk, Dv, _ptr(g), _ptr(beta),
+            Dk ** -0.5 if scale is None else float(scale), _ptr(state), _ptr(dstate), _ptr(lengths),
+            *(_ptr(o) for o in outs), _ptr(ws), 0 if ws is None else _nbytes(ws), _stream(dev, stream)))
+    return tuple(outs)
 
 
 # ------------------------------------------------- training the stream router

@@ -1693,10 +1693,47 @@ int hc_gated_delta(const void* q, const void* k, const void* v, int dtype, int64
       (state != state0 && overlaps(state, sb, state0, sb)))
     return HC_ERR_ALIAS;
   if ((r = device_status()) != HC_OK) return r;
-  const hc::DeltaArgs a{q,         k,  v,  g,  beta, state0, lengths, o,
-                        state,     workspace, B, S, Hk, Hv, Dk, Dv, (S + 63) / 64, scale,
+  const hc::DeltaArgs a{q,     k,         v, g, beta, state0, lengths, o,
+                        state, workspace, B, S, Hk,   Hv,     Dk,      Dv, (S + 63) / 64, scale,
                         delta_vec(dtype, Dk, Dv, {q, k}, {v, o}, {state0, state})};
   return launch_status(hc::launch_delta(dtype, a, (hipStream_t)stream));
+}
+
+int64_t hc_gated_delta_backward_workspace_bytes(int64_t B, int64_t S, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
+                                                int dtype) {
+  if (check_delta_shape(dtype, B, S, Hk, Hv, Dk, Dv) != HC_OK) return -1;
+  hc::DeltaArgs a{};
+  a.B = B, a.Hv = Hv, a.Dk = Dk, a.Dv = Dv, a.NC = (S + 63) / 64;
+  return hc::delta_backward_ws(a, nullptr);
+}
+
+int hc_gated_delta_backward(const void* q, const void* k, const void* v, const void* d_o, int dtype, int64_t B,
+                            int64_t S, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, const float* g,
+                            const float* beta, float scale, const float* state0, const float* dstate,
+                            const int32_t* lengths, void* dq, void* dk, void* dv, float* dg, float* dbeta,
+                            float* dstate0, void* workspace, int64_t workspace_bytes, void* stream) {
+  int r = check_delta_shape(dtype, B, S, Hk, Hv, Dk, Dv);
+  if (r != HC_OK || B == 0 || (S == 0 && !dstate0)) return r;
+  const int64_t e = (int64_t)esize(dtype), kb = B * S * Hk * Dk * e, vb = B * S * Hv * Dv * e, gb = B * S * Hv * 4;
+  const int64_t sb = B * Hv * Dk * Dv * 4;
+  const int64_t wsb = hc_gated_delta_backward_workspace_bytes(B, S, Hk, Hv, Dk, Dv, dtype);
+  const uintptr_t ea = (uintptr_t)e;
+  const bool some = S > 0;
+  const Buf iq{q, kb, ea, some}, ik{k, kb, ea, some}, iv{v, vb, ea, some}, id{d_o, vb, ea, some}, ig{g, gb, 4, some},
+      ib{beta, gb, 4, some}, i0{state0, sb, 4, false}, i1{dstate, sb, 4, false}, il{lengths, B * 4, 4, false},
+      oq{dq, kb, ea, some}, ok{dk, kb, ea, some}, ov{dv, vb, ea, some}, og{dg, gb, 4, some}, ob{dbeta, gb, 4, some},
+      o0{dstate0, sb, 4, false}, bw{wsb ? workspace : nullptr, wsb, 1, false};
+  if ((r = check_bufs({iq, ik, iv, id, ig, ib, i0, i1, il, oq, ok, ov, og, ob, o0})) != HC_OK) return r;
+  if ((r = check_ws(workspace, workspace_bytes, wsb)) != HC_OK) return r;
+  if (bufs_overlap({oq, ok, ov, og, ob, o0, bw}, {iq, ik, iv, id, ig, ib, i0, i1, il})) return HC_ERR_ALIAS;
+  if ((r = device_status()) != HC_OK) return r;
+  hc::DeltaArgs a{q,       k,       v, g, beta, state0, lengths, nullptr,
+                  nullptr, nullptr, B, S, Hk,   Hv,     Dk,      Dv, (S + 63) / 64, scale,
+                  delta_vec(dtype, Dk, Dv, {q, k, dq, dk}, {v, d_o, dv}, {state0, dstate, dstate0})};
+  hc::delta_backward_ws(a, workspace);
+  a.d_o = d_o, a.dlast = dstate, a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.dstate0 = dstate0;
+  a.vec8 = a.vec && Dv % 8 == 0 && aligned_to(d_o, 16);
+  return launch_status(hc::launch_delta_backward(dtype, a, (hipStream_t)stream));
 }
 
 // ----------------------------------------------- training the stream router

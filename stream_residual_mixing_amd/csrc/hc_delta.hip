@@ -18,18 +18,6 @@ namespace {
 
 // --------------------------------------------------------------- each chunk by itself
 
-// The decay sums are float64 and their differences float32: a difference between two
-// neighbours must not carry the rounding of a long sum. Below -200 a decay is 0 in float32
-// whatever it is added to, so that -inf (a fresh start) stays a number here.
-__device__ __forceinline__ double clamp_decay(float g) { return g < -200.f ? -200.0 : (double)g; }
-
-template <typename T, int KP, bool VEC>
-__device__ __forceinline__ Op<Stream<T>::NP> token_op(const T* base, int64_t stride, int64_t tokens, int row, int k0,
-                                                      int Dk) {
-  const int cnt = row < tokens ? max(0, min(8, Dk - k0)) : 0;
-  return load_raw8<VEC>(base + row * stride + k0, cnt).op();
-}
-
 template <typename T, int KP, bool VEC, bool BWD>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
   constexpr int NP = Stream<T>::NP, KB = KP / 32, LS = CH + 4;
@@ -53,16 +41,16 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) {
     const int k0 = 32 * kb + 8 * g;
-    const Op<NP> kn = token_op<T, KP, VEC>(k, qs, tokens, 16 * w + n, k0, Dk);
-    const Op<NP> qn = token_op<T, KP, VEC>(q, qs, tokens, 16 * w + n, k0, Dk);
+    const Op<NP> kn = token_op<T, VEC>(k, qs, tokens, 16 * w + n, k0, Dk);
+    const Op<NP> qn = token_op<T, VEC>(q, qs, tokens, 16 * w + n, k0, Dk);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       if ((t >> 1) <= (w >> 1)) {
-        const Op<NP> kr = token_op<T, KP, VEC>(k, qs, tokens, row_of(t, n), k0, Dk);
+        const Op<NP> kr = token_op<T, VEC>(k, qs, tokens, row_of(t, n), k0, Dk);
         kk[t] = mma(kr, kn, kk[t]);
         qk[t] = mma(kr, qn, qk[t]);
       }
-      if (BWD && (t >> 1) >= (w >> 1)) kq[t] = mma(token_op<T, KP, VEC>(q, qs, tokens, row_of(t, n), k0, Dk), kn, kq[t]);
+      if (BWD && (t >> 1) >= (w >> 1)) kq[t] = mma(token_op<T, VEC>(q, qs, tokens, row_of(t, n), k0, Dk), kn, kq[t]);
     }
   }
   // the upper blocks that the inverse's tiles hold stay zero
@@ -73,17 +61,12 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
   const int per = (int)(a.Hv / a.Hk);
   for (int hi = 0; hi < per; ++hi) {
     const int64_t hv = hk * per + hi, rec = (b * a.Hv + hv) * NC + chunk;
-    char* out = (char*)a.rec + rec * REC;
+    char* out = (char*)a.rec + rec * (BWD ? REC_BWD : REC);
     if (threadIdx.x < CH) {  // one wave
       const int i = threadIdx.x;
       const bool on = i < tokens;
       const int64_t at = (b * a.S + t0 + i) * a.Hv + hv;
-      double s = on ? clamp_decay(a.g[at]) : 0.0;
-#pragma unroll
-      for (int o = 1; o < CH; o <<= 1) {
-        const double up = __shfl_up(s, o, 64);
-        if (i >= o) s += up;
-      }
+      const double s = running_sum(on ? clamp_decay(a.g[at]) : 0.0, i);
       const double end = __shfl(s, CH - 1, 64);
       const float be = on ? a.beta[at] : 0.f;
       G[i] = s;
@@ -179,13 +162,12 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
       const int i = row_of(w, n);
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
-        if (!BWD) {
-          if (kb <= (w >> 1)) store_tile(out + REC_T, tri(w, kb), lane, &inv[i][32 * kb + 8 * g]);
-        } else if (kb >= (w >> 1)) {
+        if (kb <= (w >> 1)) store_tile(out + REC_T, tri(w, kb), lane, &inv[i][32 * kb + 8 * g]);
+        if (BWD && kb >= (w >> 1)) {
           float v[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = inv[32 * kb + 8 * g + e][i];
-          store_tile(out + REC_T, tri_t(w, kb), lane, v);
+          store_tile(out + REC_TT, tri_t(w, kb), lane, v);
         }
       }
     }
@@ -195,76 +177,21 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
 
 // --------------------------------------------------------------------- the walk
 
-// Columns of a wave: NT tiles of 16, tile h's column n is NT n + h, so that a lane's are neighbours.
-template <int NT> struct Cols { float v[NT]; };
-
-template <int NT, bool VEC>
-__device__ __forceinline__ Cols<NT> load_cols(const float* p, int cnt) {
-  Cols<NT> r;
-  if (VEC && NT == 2) {
-    r.v[0] = r.v[NT - 1] = 0.f;
-    if (cnt > 0) {
-      const float2 q = *reinterpret_cast<const float2*>(p);
-      r.v[0] = q.x;
-      r.v[NT - 1] = q.y;
-    }
-  } else {
-#pragma unroll
-    for (int h = 0; h < NT; ++h) r.v[h] = h < cnt ? p[h] : 0.f;
-  }
-  return r;
-}
-
-template <int NT, bool VEC>
-__device__ __forceinline__ Cols<NT> load_cols(const bf16_t* p, int cnt) {
-  Cols<NT> r;
-  if (VEC && NT == 2) {
-    const uint32_t q = cnt > 0 ? *reinterpret_cast<const uint32_t*>(p) : 0;
-    r.v[0] = __uint_as_float(q << 16);
-    r.v[NT - 1] = __uint_as_float(q & 0xffff0000u);
-  } else {
-#pragma unroll
-    for (int h = 0; h < NT; ++h) r.v[h] = h < cnt ? bf2f(p[h]) : 0.f;
-  }
-  return r;
-}
-
-template <int NT, bool VEC>
-__device__ __forceinline__ void store_cols(float* p, int cnt, const Cols<NT>& c) {
-  if (VEC && NT == 2) {
-    if (cnt > 0) *reinterpret_cast<float2*>(p) = make_float2(c.v[0], c.v[NT - 1]);
-  } else {
-#pragma unroll
-    for (int h = 0; h < NT; ++h)
-      if (h < cnt) p[h] = c.v[h];
-  }
-}
-
-template <int NT, bool VEC>
-__device__ __forceinline__ void store_cols(bf16_t* p, int cnt, const Cols<NT>& c) {
-  if (VEC && NT == 2) {
-    if (cnt > 0) *reinterpret_cast<uint32_t*>(p) = pack_bf2_hw(c.v[0], c.v[NT - 1]);
-  } else {
-#pragma unroll
-    for (int h = 0; h < NT; ++h)
-      if (h < cnt) p[h] = (bf16_t)(pack_bf2_hw(c.v[h], 0.f) & 0xffffu);
-  }
-}
-
-template <int KP, int NP>
+template <int KP, int NP, bool KEEP>
 struct WalkLds {
-  char k[NP][Tokens<KP>::PART];       // keys: rows in row_of's order, then transposed
-  char q[NP][Tokens<KP>::ROWS];
-  char rec[REC];
+  char k[NP][Tokens<KP>::PART];  // keys: rows in row_of's order, then transposed
+  char q[KEEP ? 1 : NP][KEEP ? 16 : Tokens<KP>::ROWS];
+  char rec[KEEP ? REC_P : REC];
 };
 
-template <typename T, int KP, int NT, bool VEC>
+// KEEP: the backward's, which wants every chunk's first state and Z rather than O.
+template <typename T, int KP, int NT, bool VEC, bool KEEP>
 __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a) {
   constexpr int NP = Stream<T>::NP, KB = KP / 32, KT = KP / 16;
-  static_assert(sizeof(WalkLds<KP, NP>) <= 160 * 1024, "LDS of a CU");
+  static_assert(sizeof(WalkLds<KP, NP, KEEP>) <= 160 * 1024, "LDS of a CU");
   constexpr int PIECES = KP / 8, ITEMS = 32 * PIECES / 256;  // pairs of tokens by pieces of 8, for each thread
   extern __shared__ __attribute__((aligned(16))) char lds_raw[];
-  typedef WalkLds<KP, NP> Lds;
+  typedef WalkLds<KP, NP, KEEP> Lds;
   Lds& lds = *reinterpret_cast<Lds*>(lds_raw);
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n = lane & 15, g = lane >> 4;
   const int64_t groups = (a.Dv + 64 * NT - 1) / (64 * NT);
@@ -277,7 +204,8 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a) {
   const T* kp = (const T*)a.k + b * a.S * qs + hk * a.Dk;
   const T* vp = (const T*)a.v + b * a.S * vs + hv * a.Dv + col;
   T* op = (T*)a.o + b * a.S * vs + hv * a.Dv + col;
-  const char* rec = (const char*)a.rec + bh * a.NC * REC;
+  constexpr int REC_STRIDE = KEEP ? REC_BWD : REC, REC_USED = KEEP ? REC_P : REC;
+  const char* rec = (const char*)a.rec + bh * a.NC * REC_STRIDE;
 
   f4_t S[KT][NT];
   {
@@ -295,7 +223,7 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a) {
 
   // the next chunk's operands on their way
   Raw8<T> kr[ITEMS][2], qr[ITEMS][2];
-  u4_t rr[(REC + 4095) / 4096];
+  u4_t rr[(REC_USED + 4095) / 4096];
   Cols<NT> vr[4][4];
   const auto fetch = [&](int64_t c) {
     const int64_t t0 = c * CH;
@@ -307,12 +235,13 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a) {
         const int64_t t = t0 + 2 * pair + j;
         const int cnt = t < len ? max(0, min(8, Dk - 8 * piece)) : 0;
         kr[i][j] = load_raw8<VEC>(kp + t * qs + 8 * piece, cnt);
-        qr[i][j] = load_raw8<VEC>(qp + t * qs + 8 * piece, cnt);
+        if (!KEEP) qr[i][j] = load_raw8<VEC>(qp + t * qs + 8 * piece, cnt);
       }
     }
 #pragma unroll
-    for (int i = 0; i < (REC + 4095) / 4096; ++i)
-      if (i * 4096 + tid * 16 < REC) rr[i] = *reinterpret_cast<const u4_t*>(rec + c * REC + i * 4096 + tid * 16);
+    for (int i = 0; i < (REC_USED + 4095) / 4096; ++i)
+      if (i * 4096 + tid * 16 < REC_USED)
+        rr[i] = *reinterpret_cast<const u4_t*>(rec + c * REC_STRIDE + i * 4096 + tid * 16);
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -330,17 +259,20 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         ko[i][j] = kr[i][j].op();
-        const Op<NP> qo = qr[i][j].op();
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
+        for (int p = 0; p < NP; ++p)
           *reinterpret_cast<bf8_t*>(lds.k[p] + Tokens<KP>::row_at(place_of(2 * pair + j), 16 * piece)) = ko[i][j].p[p];
-          *reinterpret_cast<bf8_t*>(lds.q[p] + Tokens<KP>::row_at(2 * pair + j, 16 * piece)) = qo.p[p];
+        if (!KEEP) {
+          const Op<NP> qo = qr[i][j].op();
+#pragma unroll
+          for (int p = 0; p < NP; ++p)
+            *reinterpret_cast<bf8_t*>(lds.q[p] + Tokens<KP>::row_at(2 * pair + j, 16 * piece)) = qo.p[p];
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < (REC + 4095) / 4096; ++i)
-      if (i * 4096 + tid * 16 < REC) *reinterpret_cast<u4_t*>(lds.rec + i * 4096 + tid * 16) = rr[i];
+    for (int i = 0; i < (REC_USED + 4095) / 4096; ++i)
+      if (i * 4096 + tid * 16 < REC_USED) *reinterpret_cast<u4_t*>(lds.rec + i * 4096 + tid * 16) = rr[i];
     Cols<NT> v[4][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -348,6 +280,18 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a) {
       for (int r = 0; r < 4; ++r) v[t][r] = vr[t][r];
     __syncthreads();
 
+    if (KEEP && col < a.VP) {
+      bf16_t* keep = (bf16_t*)a.states + (bh * a.NC + c) * 2 * KP * a.VP + col;
+#pragma unroll
+      for (int t = 0; t < KT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          Cols<NT> y;
+#pragma unroll
+          for (int h = 0; h < NT; ++h) y.v[h] = S[t][h][r];
+          store_parts<NT>(keep + row_of(t, 4 * g + r) * a.VP, KP * a.VP, y);
+        }
+    }
     // K M and Q M
     f4_t km[4][NT], o[4][NT];
 #pragma unroll
@@ -366,12 +310,12 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a) {
         for (int p = 0; p < NP; ++p) {
           const int at = Tokens<KP>::row_at(16 * t + n, 64 * kb + 16 * g);
           ka.p[p] = *reinterpret_cast<const bf8_t*>(lds.k[p] + at);
-          qa.p[p] = *reinterpret_cast<const bf8_t*>(lds.q[p] + at);
+          if (!KEEP) qa.p[p] = *reinterpret_cast<const bf8_t*>(lds.q[p] + at);
         }
 #pragma unroll
         for (int h = 0; h < NT; ++h) {
           km[t][h] = mma(ka, sf[h], km[t][h]);
-          o[t][h] = mma(qa, sf[h], o[t][h]);
+          if (!KEEP) o[t][h] = mma(qa, sf[h], o[t][h]);
         }
       }
     }
@@ -381,15 +325,7 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a) {
     for (int i = 0; i < ITEMS; ++i) {
       const int x = i * 256 + tid, piece = x % PIECES, pair = x / PIECES;
 #pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        const u4_t e0 = __builtin_bit_cast(u4_t, ko[i][0].p[p]), e1 = __builtin_bit_cast(u4_t, ko[i][1].p[p]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t lo = e & 1 ? e0[e >> 1] >> 16 : e0[e >> 1] & 0xffffu;
-          const uint32_t hi = e & 1 ? e1[e >> 1] & 0xffff0000u : e1[e >> 1] << 16;
-          *reinterpret_cast<uint32_t*>(lds.k[p] + Tokens<KP>::col_at(place_of(8 * piece + e), 4 * pair)) = lo | hi;
-        }
-      }
+      for (int p = 0; p < NP; ++p) store_transposed<KP>(lds.k[p], pair, piece, ko[i][0].p[p], ko[i][1].p[p]);
     }
     if (c + 1 < chunks) fetch(c + 1);
 
@@ -422,6 +358,18 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a) {
 #pragma unroll
           for (int h = 0; h < NT; ++h) km[t][h] = mma(ta, rf[kb][h], km[t][h]);
         }
+      if (KEEP && col < a.VP) {
+        bf16_t* keep = (bf16_t*)a.z + (bh * a.NC + c) * 2 * CH * a.VP + col;
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            Cols<NT> y;
+#pragma unroll
+            for (int h = 0; h < NT; ++h) y.v[h] = km[t][h][r];
+            store_parts<NT>(keep + row_of(t, 4 * g + r) * a.VP, CH * a.VP, y);
+          }
+      }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const f4_t beta = *reinterpret_cast<const f4_t*>(dec + DEC_BETA + row_of(t, 4 * g));
@@ -433,25 +381,26 @@ __global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a) {
 #pragma unroll
         for (int h = 0; h < NT; ++h) x[kb][h] = split(km[2 * kb][h], km[2 * kb + 1][h]);
     }
-    // O = scale (exp(G) Q M + P X)
+    if (!KEEP) {  // O = scale (exp(G) Q M + P X)
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const f4_t ahead = *reinterpret_cast<const f4_t*>(dec + DEC_AHEAD + 16 * t + 4 * g);
+      for (int t = 0; t < 4; ++t) {
+        const f4_t ahead = *reinterpret_cast<const f4_t*>(dec + DEC_AHEAD + 16 * t + 4 * g);
 #pragma unroll
-      for (int h = 0; h < NT; ++h) o[t][h] *= ahead;
+        for (int h = 0; h < NT; ++h) o[t][h] *= ahead;
 #pragma unroll
-      for (int kb = 0; kb <= (t >> 1); ++kb) {
-        const Split pa = load_tile(lds.rec + REC_P, tri(t, kb), lane);
+        for (int kb = 0; kb <= (t >> 1); ++kb) {
+          const Split pa = load_tile(lds.rec + REC_P, tri(t, kb), lane);
 #pragma unroll
-        for (int h = 0; h < NT; ++h) o[t][h] = mma(pa, x[kb][h], o[t][h]);
-      }
+          for (int h = 0; h < NT; ++h) o[t][h] = mma(pa, x[kb][h], o[t][h]);
+        }
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t tok = c * CH + 16 * t + 4 * g + r;
-        Cols<NT> y;
+        for (int r = 0; r < 4; ++r) {
+          const int64_t tok = c * CH + 16 * t + 4 * g + r;
+          Cols<NT> y;
 #pragma unroll
-        for (int h = 0; h < NT; ++h) y.v[h] = a.scale * o[t][h][r];
-        store_cols<NT, VEC>(op + tok * vs, tok < len ? have : 0, y);
+          for (int h = 0; h < NT; ++h) y.v[h] = a.scale * o[t][h][r];
+          store_cols<NT, VEC>(op + tok * vs, tok < len ? have : 0, y);
+        }
       }
     }
     // M = exp(G_end) M + K^T (exp(G_end - G) X)
@@ -599,9 +548,9 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
 
 constexpr int SHORT = 8;  // tokens up to which they are taken one by one
 
-template <typename T, int KP, int NT>
+template <typename T, int KP, int NT, bool KEEP>
 hipError_t walk_go(const DeltaArgs& a, hipStream_t st) {
-  const size_t lds = sizeof(WalkLds<KP, Stream<T>::NP>);
+  const size_t lds = sizeof(WalkLds<KP, Stream<T>::NP, KEEP>);
   const dim3 prep((unsigned)(a.B * a.Hk * a.NC)), walk((unsigned)(a.B * a.Hv * ((a.Dv + 64 * NT - 1) / (64 * NT))));
   const auto go = [&](auto prep_k, auto walk_k) {
     if (lds > 64 * 1024) {
@@ -612,29 +561,29 @@ hipError_t walk_go(const DeltaArgs& a, hipStream_t st) {
     hipLaunchKernelGGL(walk_k, walk, dim3(256), lds, st, a);
     return hipGetLastError();
   };
-  if (a.vec) return go(delta_prep_kernel<T, KP, true, false>, delta_walk_kernel<T, KP, NT, true>);
-  return go(delta_prep_kernel<T, KP, false, false>, delta_walk_kernel<T, KP, NT, false>);
+  if (a.vec) return go(delta_prep_kernel<T, KP, true, KEEP>, delta_walk_kernel<T, KP, NT, true, KEEP>);
+  return go(delta_prep_kernel<T, KP, false, KEEP>, delta_walk_kernel<T, KP, NT, false, KEEP>);
 }
 
-template <typename T, int KP>
+template <typename T, int KP, bool KEEP>
 hipError_t delta_go(const DeltaArgs& a, hipStream_t st) {
-  if (a.S <= SHORT) {
+  if (!KEEP && a.S <= SHORT) {
     const dim3 grid((unsigned)(a.B * a.Hv * ((a.Dv + 31) / 32)));
     if (a.vec && a.Dv % 4 == 0) hipLaunchKernelGGL((delta_step_kernel<T, KP, true>), grid, dim3(256), 0, st, a);
     else hipLaunchKernelGGL((delta_step_kernel<T, KP, false>), grid, dim3(256), 0, st, a);
     return hipGetLastError();
   }
   if constexpr (KP < 256) {
-    if (a.Dv > 64) return walk_go<T, KP, 2>(a, st);
+    if (a.Dv > 64) return walk_go<T, KP, 2, KEEP>(a, st);
   }
-  return walk_go<T, KP, 1>(a, st);
+  return walk_go<T, KP, 1, KEEP>(a, st);
 }
 
-template <typename T>
+template <typename T, bool KEEP>
 hipError_t delta_by_width(const DeltaArgs& a, hipStream_t st) {
-  if (a.Dk <= 64) return delta_go<T, 64>(a, st);
-  if (a.Dk <= 128) return delta_go<T, 128>(a, st);
-  return delta_go<T, 256>(a, st);
+  if (a.Dk <= 64) return delta_go<T, 64, KEEP>(a, st);
+  if (a.Dk <= 128) return delta_go<T, 128, KEEP>(a, st);
+  return delta_go<T, 256, KEEP>(a, st);
 }
 
 }  // namespace
@@ -644,7 +593,11 @@ int64_t delta_ws_bytes(int64_t B, int64_t S, int64_t Hv) {
 }
 
 hipError_t launch_delta(int dtype, const DeltaArgs& a, hipStream_t st) {
-  return dtype == 0 ? delta_by_width<float>(a, st) : delta_by_width<bf16_t>(a, st);
+  return dtype == 0 ? delta_by_width<float, false>(a, st) : delta_by_width<bf16_t, false>(a, st);
+}
+
+hipError_t launch_delta_keep(int dtype, const DeltaArgs& a, hipStream_t st) {
+  return dtype == 0 ? delta_by_width<float, true>(a, st) : delta_by_width<bf16_t, true>(a, st);
 }
 
 }  // namespace hc

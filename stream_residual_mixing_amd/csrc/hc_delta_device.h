@@ -117,12 +117,23 @@ template <typename T> struct Raw8;
 template <> struct Raw8<bf16_t> {
   u4_t q;
   __device__ __forceinline__ Op<1> op() const { return {as_bf8(q)}; }
+  __device__ __forceinline__ void open(float v[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(q[i] << 16);
+      v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
+    }
+  }
 };
 template <> struct Raw8<float> {
   f4_t a, b;
   __device__ __forceinline__ Op<2> op() const {
     const Split s = split(a, b);
     return {s.hi, s.lo};
+  }
+  __device__ __forceinline__ void open(float v[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
   }
 };
 
@@ -169,13 +180,14 @@ __device__ __forceinline__ int64_t length_of(const int32_t* lengths, int64_t b, 
   return n < 0 ? 0 : n > S ? S : n;
 }
 
-// A chunk's record: 16 x 32 operand tiles of 64 x 16 bytes in the lanes' order, first the six high
-// parts and then the six low ones, of the two lower block-triangular matrices T (rows in row_of's
-// order) and P (rows in their own), tile (t, kb) at tri(t, kb); decays and betas, a float per
-// token. The backward's holds the transposes of both, upper triangular, at tri_t, T^T's rows and
-// P^T's in row_of's order.
+// A chunk's record: decays and betas, a float per token, and 16 x 32 operand tiles of 64 x 16 bytes in
+// the lanes' order, first the six high parts and then the six low ones, of the two lower
+// block-triangular matrices T (rows in row_of's order) and P (rows in their own), tile (t, kb) at
+// tri(t, kb). The backward's holds T and, upper triangular at tri_t, the transposes of both with
+// rows in row_of's order.
 constexpr int TILE = 1024, TRI = 12 * TILE;
 constexpr int REC_T = 0, REC_DEC = TRI, REC_P = TRI + 3 * CH * 4, REC = REC_P + TRI;
+constexpr int REC_TT = REC, REC_BWD = REC + TRI;
 constexpr int DEC_AHEAD = 0, DEC_TO_END = CH, DEC_BETA = 2 * CH;
 
 __device__ __forceinline__ constexpr int tri(int t, int kb) { return t < 2 ? t : 2 * t - 2 + kb; }
@@ -208,6 +220,110 @@ struct Tokens {
     return place * COL + (KP == 256 ? byte ^ ((place & 7) << 4) : byte);
   }
 };
+
+// Columns of a wave: NT tiles of 16, tile h's column n is NT n + h, so that a lane's are neighbours.
+template <int NT> struct Cols { float v[NT]; };
+
+template <int NT, bool VEC>
+__device__ __forceinline__ Cols<NT> load_cols(const float* p, int cnt) {
+  Cols<NT> r;
+  if (VEC && NT == 2) {
+    r.v[0] = r.v[NT - 1] = 0.f;
+    if (cnt > 0) {
+      const float2 q = *reinterpret_cast<const float2*>(p);
+      r.v[0] = q.x;
+      r.v[NT - 1] = q.y;
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < NT; ++h) r.v[h] = h < cnt ? p[h] : 0.f;
+  }
+  return r;
+}
+
+template <int NT, bool VEC>
+__device__ __forceinline__ Cols<NT> load_cols(const bf16_t* p, int cnt) {
+  Cols<NT> r;
+  if (VEC && NT == 2) {
+    const uint32_t q = cnt > 0 ? *reinterpret_cast<const uint32_t*>(p) : 0;
+    r.v[0] = __uint_as_float(q << 16);
+    r.v[NT - 1] = __uint_as_float(q & 0xffff0000u);
+  } else {
+#pragma unroll
+    for (int h = 0; h < NT; ++h) r.v[h] = h < cnt ? bf2f(p[h]) : 0.f;
+  }
+  return r;
+}
+
+template <int NT, bool VEC>
+__device__ __forceinline__ void store_cols(float* p, int cnt, const Cols<NT>& c) {
+  if (VEC && NT == 2) {
+    if (cnt > 0) *reinterpret_cast<float2*>(p) = make_float2(c.v[0], c.v[NT - 1]);
+  } else {
+#pragma unroll
+    for (int h = 0; h < NT; ++h)
+      if (h < cnt) p[h] = c.v[h];
+  }
+}
+
+template <int NT, bool VEC>
+__device__ __forceinline__ void store_cols(bf16_t* p, int cnt, const Cols<NT>& c) {
+  if (VEC && NT == 2) {
+    if (cnt > 0) *reinterpret_cast<uint32_t*>(p) = pack_bf2_hw(c.v[0], c.v[NT - 1]);
+  } else {
+#pragma unroll
+    for (int h = 0; h < NT; ++h)
+      if (h < cnt) p[h] = (bf16_t)(pack_bf2_hw(c.v[h], 0.f) & 0xffffu);
+  }
+}
+
+// The two bfloat16 parts of a lane's columns at p and p + lo.
+template <int NT>
+__device__ __forceinline__ void store_parts(bf16_t* p, int64_t lo, const Cols<NT>& c) {
+  const uint32_t h = pack_bf2_hw(c.v[0], c.v[NT - 1]);
+  const uint32_t l = pack_bf2_hw(c.v[0] - __uint_as_float(h << 16), c.v[NT - 1] - __uint_as_float(h & 0xffff0000u));
+  if (NT == 2) {
+    *reinterpret_cast<uint32_t*>(p) = h;
+    *reinterpret_cast<uint32_t*>(p + lo) = l;
+  } else {
+    p[0] = (bf16_t)h;
+    p[lo] = (bf16_t)l;
+  }
+}
+
+// Two tokens' pieces into the transposed array: eight words of (token, token + 1).
+template <int KP>
+__device__ __forceinline__ void store_transposed(char* dst, int pair, int piece, bf8_t a, bf8_t b) {
+  const u4_t e0 = __builtin_bit_cast(u4_t, a), e1 = __builtin_bit_cast(u4_t, b);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t lo = e & 1 ? e0[e >> 1] >> 16 : e0[e >> 1] & 0xffffu;
+    const uint32_t hi = e & 1 ? e1[e >> 1] & 0xffff0000u : e1[e >> 1] << 16;
+    *reinterpret_cast<uint32_t*>(dst + Tokens<KP>::col_at(place_of(8 * piece + e), 4 * pair)) = lo | hi;
+  }
+}
+
+// The decay sums are float64 and their differences float32: a difference between two
+// neighbours must not carry the rounding of a long sum. Below -200 a decay is 0 in float32
+// whatever it is added to, so that -inf (a fresh start) stays a number here.
+__device__ __forceinline__ double clamp_decay(float g) { return g < -200.f ? -200.0 : (double)g; }
+
+// The running sum over a wave of 64 tokens.
+__device__ __forceinline__ double running_sum(double s, int i) {
+#pragma unroll
+  for (int o = 1; o < CH; o <<= 1) {
+    const double up = __shfl_up(s, o, 64);
+    if (i >= o) s += up;
+  }
+  return s;
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ Op<Stream<T>::NP> token_op(const T* base, int64_t stride, int64_t tokens, int row, int k0,
+                                                      int Dk) {
+  const int cnt = row < tokens ? max(0, min(8, Dk - k0)) : 0;
+  return load_raw8<VEC>(base + row * stride + k0, cnt).op();
+}
 
 }  // namespace
 

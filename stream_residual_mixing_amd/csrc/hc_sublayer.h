@@ -70,8 +70,9 @@ int64_t scan_ws_bytes(int64_t B, int64_t S, int64_t C);
 hipError_t launch_scan(int dtype, bool bwd, bool vec, const ScanArgs& a, hipStream_t st);
 
 // ---- gated delta rule (hc_delta.hip, hc_delta_backward.hip)
-// rec: the chunks' records in the workspace; NC = ceil(S / 64). vec: Dk % 8 == 0, Dv even, q and k
-// 16-byte aligned, v, o and the states at least to two elements (16 bytes where Dv % 4 == 0).
+// rec: the chunks' records in the workspace; NC = ceil(S / 64). vec: Dk % 8 == 0, Dv even, q, k and
+// their gradients 16-byte aligned, v, o and theirs to two elements, the states to 8 bytes (16 where
+// Dv % 4 == 0).
 struct DeltaArgs {
   const void* q;
   const void* k;
@@ -86,9 +87,31 @@ struct DeltaArgs {
   int64_t B, S, Hk, Hv, Dk, Dv, NC;
   float scale;
   bool vec;
+  // the backward's: every chunk's first state [KP, VP] and Z [64, VP], and the state's gradient
+  // behind it and W of the same shapes, each as two bfloat16 parts; KP is Dk as 64, 128 or 256,
+  // VP is Dv in whole 32s
+  void* states;
+  void* z;
+  void* dstates;
+  void* w;
+  int64_t VP;
+  const void* d_o;
+  const float* dlast;      // may be NULL: zeros
+  void* dq;
+  void* dk;
+  void* dv;
+  float* dg;
+  float* dbeta;
+  float* dstate0;          // may be NULL
+  bool vec8;               // vec, and Dv % 8 == 0 with d_o 16-byte aligned
 };
 int64_t delta_ws_bytes(int64_t B, int64_t S, int64_t Hv);
 hipError_t launch_delta(int dtype, const DeltaArgs& a, hipStream_t st);
+// the records, states and z of the backward
+hipError_t launch_delta_keep(int dtype, const DeltaArgs& a, hipStream_t st);
+// sets the workspace's arrays in a and returns their bytes (ws may be NULL)
+int64_t delta_backward_ws(DeltaArgs& a, void* ws);
+hipError_t launch_delta_backward(int dtype, const DeltaArgs& a, hipStream_t st);
 
 // ---- balance loss and the router's backward (hc_router.hip)
 int64_t balance_ws_bytes(int64_t B, int64_t S, int N, int m);

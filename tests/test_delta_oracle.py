@@ -114,3 +114,29 @@ def test_forward_refusals(L):
     assert fwd(s1=at(7)) == -5 and fwd(s1=ctypes.c_void_p(at(5).value + 4)) == -5
     assert fwd(B=0, q=None, k=None, v=None, g=None, be=None, o=None, w=None, wb=0) == 0
     assert fwd(S=0, q=None, k=None, v=None, g=None, be=None, o=None, s1=None, w=None, wb=0) == 0
+
+
+def test_backward_refusals(L):
+    ws = L.hc_gated_delta_backward_workspace_bytes
+    assert ws(1, 8, 2, 3, 8, 8, 1) == -1 and ws(1, 8, 1, 1, 257, 8, 1) == -1 and ws(1, 8, 1, 1, 8, 8, 7) == -1
+    assert ws(0, 8, 1, 1, 8, 8, 1) == 0 and ws(1, 0, 1, 1, 8, 8, 1) == 0
+    need = ws(2, 30, 1, 2, 32, 32, 1)
+    assert need > 0
+
+    def bwd(q=at(0), k=at(1), v=at(2), d=at(3), dt=1, B=2, S=30, Hk=1, Hv=2, Dk=32, Dv=32, g=at(4), be=at(5), s0=at(6),
+            s1=at(7), ln=at(8), dq=at(9), dk=at(10), dv=at(11), dg=at(12), db=at(13), d0=at(14), w=at(20), wb=need):
+        return L.hc_gated_delta_backward(q, k, v, d, dt, B, S, Hk, Hv, Dk, Dv, g, be, 1.0, s0, s1, ln, dq, dk, dv, dg,
+                                         db, d0, w, wb, None)
+
+    assert bwd(dt=3) == -3 and bwd(Hv=3, Hk=2) == -2 and bwd(S=-1) == -2
+    for name in ("q", "k", "v", "d", "g", "be", "dq", "dk", "dv", "dg", "db"):
+        assert bwd(**{name: None}) == -1, name
+    for name in ("k", "d", "s1", "dg", "d0"):
+        assert bwd(**{name: ctypes.c_void_p(FAKE + 1)}) == -4, name
+    assert bwd(w=None) == -8 and bwd(wb=need - 1) == -8
+    for x in range(9):
+        for name in ("dq", "dk", "dv", "dg", "db", "d0", "w"):
+            assert bwd(**{name: at(x)}) == -5, (name, x)
+    assert bwd(dk=at(9)) == -5 and bwd(d0=at(12)) == -5 and bwd(w=at(11)) == -5
+    assert bwd(B=0, q=None, k=None, v=None, d=None, g=None, be=None, dq=None, dk=None, dv=None, dg=None, db=None, w=None,
+               wb=0) == 0
