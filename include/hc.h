@@ -745,8 +745,8 @@ int hc_gated_scan_backward(const void* x, const void* gate, const void* y, const
  *   term of the state is off by at most about 2^-16 of itself. Deterministic. A NaN or an infinity
  *   spoils its head from its chunk's first token on.
  *   dtype HC_F32 or HC_BF16; Hv a multiple of Hk; 1 <= Dk, Dv <= HC_MAX_HEAD; S = 0 passes the state on
- *   (B = 0 does nothing); B * Hv * max(8, ceil(S / 64)) < 2^23 (else HC_ERR_SHAPE); arrays aligned to
- *   their element size; workspace hc_gated_delta_workspace_bytes bytes (-1 for invalid sizes; may be
+ *   (B = 0 does nothing); B * Hv * max(8, ceil(S / 64)), Hk * Dk and Hv * Dv < 2^23 (else HC_ERR_SHAPE);
+ *   arrays aligned to their element size; workspace hc_gated_delta_workspace_bytes bytes (-1 for invalid sizes; may be
  *   NULL when that is 0), 256-byte aligned. Outputs overlap no input (but as stated), other output or
  *   workspace (HC_ERR_ALIAS).
  *

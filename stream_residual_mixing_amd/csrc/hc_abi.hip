@@ -1650,9 +1650,11 @@ static int check_delta_shape(int dtype, int64_t B, int64_t S, int64_t Hk, int64_
   if (!dtype_ok(dtype)) return HC_ERR_DTYPE;
   if (B < 0 || S < 0 || Hk < 1 || Hv < 1 || Hv % Hk != 0 || Dk < 1 || Dk > HC_MAX_HEAD || Dv < 1 || Dv > HC_MAX_HEAD)
     return HC_ERR_SHAPE;
-  // the grids: a workgroup of 256 threads for each 64 tokens, and for each 32 columns, of a head
+  // the grids: a workgroup of up to 512 threads for each 64 tokens, and for each 32 columns, of a
+  // head; a chunk of 64 tokens of all heads is reached with 31-bit offsets
   const int64_t most = 1ll << 23, per = ((S > 512 ? S + 63 : 512) / 64);
   if (B >= most || Hv >= most || per >= most || B * Hv >= most || B * Hv * per >= most) return HC_ERR_SHAPE;
+  if (Hk * Dk >= most || Hv * Dv >= most) return HC_ERR_SHAPE;
   return HC_OK;
 }
 

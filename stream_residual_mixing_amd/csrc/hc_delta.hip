@@ -5,7 +5,7 @@
 //   Z = (I + A)^-1 (V - exp(G) K M),  X = beta Z,
 //   O = scale (exp(G) Q M + P X),  M' = exp(G_end) M + K^T (exp(G_end - G) X).
 // Two kernels: every chunk's triangle, its inverse T and P by themselves, and the walk over the
-// chunks, whose columns of the state (and of V, Z, O) never meet: a wave keeps its 16 or 32
+// chunks, whose columns of the state (and of V, Z, O) never meet: a wave keeps its 16
 // columns' state in registers and hands each product's result to the next as its operand.
 // Products are bfloat16 matrix instructions with float32 sums; values that are not bfloat16
 // already (the state, Z, T, P, float32 streams) enter as two parts, 16 bits, so that the
@@ -19,19 +19,20 @@ namespace {
 // --------------------------------------------------------------- each chunk by itself
 
 template <typename T, int KP, bool VEC, bool BWD>
-__global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
   constexpr int NP = Stream<T>::NP, KB = KP / 32, LS = CH + 4;
   __shared__ __attribute__((aligned(16))) float L[CH][LS], inv[CH][LS];
   __shared__ double G[CH];
   __shared__ __attribute__((aligned(16))) float beta_s[CH];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-  const int64_t NC = a.NC, chunk = blockIdx.x % NC, bh = blockIdx.x / NC, b = bh / a.Hk, hk = bh % a.Hk;
-  const int64_t t0 = chunk * CH, tokens = length_of(a.lengths, b, a.S) - t0;
+  int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+  const int w = wave_number();
+  const uint32_t NC = (uint32_t)a.NC, chunk = blockIdx.x % NC, bh = blockIdx.x / NC, hk = bh % (uint32_t)a.Hk;
+  const int64_t b = bh / (uint32_t)a.Hk;
+  const int64_t t0 = (int64_t)chunk * CH, tokens = length_of(a.lengths, b, a.S) - t0;
   if (tokens <= 0) return;
-  const int Dk = (int)a.Dk;
-  const int64_t qs = a.Hk * a.Dk;
-  const T* q = (const T*)a.q + (b * a.S + t0) * qs + hk * a.Dk;
-  const T* k = (const T*)a.k + (b * a.S + t0) * qs + hk * a.Dk;
+  const int Dk = (int)a.Dk, qs = (int)(a.Hk * a.Dk), left = (int)min((int64_t)CH, tokens);
+  const int64_t at0 = (b * a.S + t0) * qs + hk * Dk;
+  const Range q = head_rows((const T*)a.q + at0, left, qs, Dk), k = head_rows((const T*)a.k + at0, left, qs, Dk);
 
   // keys by queries (and keys by keys): lane n is token 16 w + n as the later one, its rows the
   // earlier ones; in the backward also queries (rows) by keys
@@ -41,25 +42,28 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) {
     const int k0 = 32 * kb + 8 * g;
-    const Op<NP> kn = token_op<T, VEC>(k, qs, tokens, 16 * w + n, k0, Dk);
-    const Op<NP> qn = token_op<T, VEC>(q, qs, tokens, 16 * w + n, k0, Dk);
+    const Op<NP> kn = token_op<T, VEC>(k, qs, 16 * w + n, k0, Dk);
+    const Op<NP> qn = token_op<T, VEC>(q, qs, 16 * w + n, k0, Dk);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       if ((t >> 1) <= (w >> 1)) {
-        const Op<NP> kr = token_op<T, VEC>(k, qs, tokens, row_of(t, n), k0, Dk);
+        const Op<NP> kr = token_op<T, VEC>(k, qs, row_of(t, n), k0, Dk);
         kk[t] = mma(kr, kn, kk[t]);
         qk[t] = mma(kr, qn, qk[t]);
       }
-      if (BWD && (t >> 1) >= (w >> 1)) kq[t] = mma(token_op<T, VEC>(q, qs, tokens, row_of(t, n), k0, Dk), kn, kq[t]);
+      if (BWD && (t >> 1) >= (w >> 1)) kq[t] = mma(token_op<T, VEC>(q, qs, row_of(t, n), k0, Dk), kn, kq[t]);
     }
+    if (kb & 1) keep_order();
   }
   // the upper blocks that the inverse's tiles hold stay zero
   {
     const int bl = threadIdx.x >> 7, i = (threadIdx.x & 127) >> 3, c = 2 * (threadIdx.x & 7);
     inv[32 * bl + i][32 * bl + 16 + c] = inv[32 * bl + i][32 * bl + 16 + c + 1] = 0.f;
   }
-  const int per = (int)(a.Hv / a.Hk);
+  const int per = (int)((uint32_t)a.Hv / (uint32_t)a.Hk);
   for (int hi = 0; hi < per; ++hi) {
+    renew(n, g);
+    lane = 16 * g + n;
     const int64_t hv = hk * per + hi, rec = (b * a.Hv + hv) * NC + chunk;
     char* out = (char*)a.rec + rec * (BWD ? REC_BWD : REC);
     if (threadIdx.x < CH) {  // one wave
@@ -126,6 +130,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
 #pragma unroll
         for (int m = 0; m < i; ++m) s -= L[16 * w + i][16 * w + m] * x[m];
         x[i] = s;
+        if (i & 1) keep_order();
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i)
@@ -177,274 +182,177 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a) {
 
 // --------------------------------------------------------------------- the walk
 
-template <int KP, int NP, bool KEEP>
+constexpr int OUT = 0, KEEP = 1;
+
+template <int KP, int NP, int NW, int MODE>
 struct WalkLds {
-  char k[NP][Tokens<KP>::PART];  // keys: rows in row_of's order, then transposed
-  char q[KEEP ? 1 : NP][KEEP ? 16 : Tokens<KP>::ROWS];
-  char rec[KEEP ? REC_P : REC];
+  static constexpr int PASS = 1024 * NW;  // bytes that the threads bring in at once
+  char k[NP][Tokens<KP>::BYTES];  // rows in row_of's order
+  char q[MODE == OUT ? NP : 1][MODE == OUT ? Tokens<KP>::BYTES : 16];
+  char rec[((MODE == OUT ? REC : REC_P) + PASS - 1) / PASS * PASS];
 };
 
-// KEEP: the backward's, which wants every chunk's first state and Z rather than O.
-template <typename T, int KP, int NT, bool VEC, bool KEEP>
-__global__ __launch_bounds__(256) void delta_walk_kernel(DeltaArgs a) {
-  constexpr int NP = Stream<T>::NP, KB = KP / 32, KT = KP / 16;
-  static_assert(sizeof(WalkLds<KP, NP, KEEP>) <= 160 * 1024, "LDS of a CU");
-  constexpr int PIECES = KP / 8, ITEMS = 32 * PIECES / 256;  // pairs of tokens by pieces of 8, for each thread
+// NW waves of 16 columns. OUT: the forward's. KEEP: the backward's, which wants every chunk's first
+// state and Z rather than O.
+template <typename T, int KP, int NW, bool VEC, int MODE>
+__global__ __launch_bounds__(64 * NW) void delta_walk_kernel(DeltaArgs a) {
+  constexpr int NP = Stream<T>::NP, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
+  constexpr int PIECES = KP / 8, ITEMS = (CH * PIECES + THREADS - 1) / THREADS;
+  constexpr int STRIDE = MODE == KEEP ? REC_BWD : REC, USED = MODE == OUT ? REC : REC_P;
+  constexpr int RR = (USED + 16 * THREADS - 1) / (16 * THREADS);
   extern __shared__ __attribute__((aligned(16))) char lds_raw[];
-  typedef WalkLds<KP, NP, KEEP> Lds;
+  typedef WalkLds<KP, NP, NW, MODE> Lds;
+  typedef Tokens<KP> Tk;
+  static_assert(sizeof(Lds) <= 160 * 1024, "LDS of a CU");
   Lds& lds = *reinterpret_cast<Lds*>(lds_raw);
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n = lane & 15, g = lane >> 4;
-  const int64_t groups = (a.Dv + 64 * NT - 1) / (64 * NT);
-  const int64_t bh = blockIdx.x / groups, b = bh / a.Hv, hv = bh % a.Hv, hk = hv / (a.Hv / a.Hk);
-  const int Dk = (int)a.Dk;
-  const int col = (int)(blockIdx.x % groups) * 64 * NT + 16 * NT * w + NT * n, have = max(0, min(NT, (int)a.Dv - col));
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_number(), n = lane & 15, g = lane >> 4;
+  const int rows_at = Tk::lane_at(n, g), cols_at = Tk::lane_at_t(n, g);
+  const uint32_t groups = ((uint32_t)a.Dv + 16 * NW - 1) / (16 * NW);
+  const int64_t bh = blockIdx.x / groups, b = (uint32_t)bh / (uint32_t)a.Hv;
+  const uint32_t hv = (uint32_t)bh % (uint32_t)a.Hv, hk = hv / ((uint32_t)a.Hv / (uint32_t)a.Hk);
+  const int Dk = (int)a.Dk, Dv = (int)a.Dv, VP = (int)a.VP, qs = (int)a.Hk * Dk, vs = (int)a.Hv * Dv;
+  const int col = (int)(blockIdx.x % groups) * 16 * NW + 16 * w, have = min(16, Dv - col);  // columns; may be none
   const int64_t len = length_of(a.lengths, b, a.S), chunks = (len + CH - 1) / CH;
-  const int64_t qs = a.Hk * a.Dk, vs = a.Hv * a.Dv;
-  const T* qp = (const T*)a.q + b * a.S * qs + hk * a.Dk;
-  const T* kp = (const T*)a.k + b * a.S * qs + hk * a.Dk;
-  const T* vp = (const T*)a.v + b * a.S * vs + hv * a.Dv + col;
-  T* op = (T*)a.o + b * a.S * vs + hv * a.Dv + col;
-  constexpr int REC_STRIDE = KEEP ? REC_BWD : REC, REC_USED = KEEP ? REC_P : REC;
-  const char* rec = (const char*)a.rec + bh * a.NC * REC_STRIDE;
+  const int64_t keys = b * a.S * qs + hk * Dk, values = b * a.S * vs + hv * Dv + col;
+  const char* rec = (const char*)a.rec + bh * a.NC * STRIDE;
+  const uint32_t v_lane = n < have ? (8 * g * vs + n) * (uint32_t)sizeof(T) : NOWHERE;
+  const uint32_t o_lane = n < have ? (4 * g * vs + n) * (uint32_t)sizeof(T) : NOWHERE;
 
-  f4_t S[KT][NT];
-  {
-    const float* s0 = a.state0 ? a.state0 + bh * a.Dk * a.Dv + col : nullptr;
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = row_of(t, 4 * g + r);
-        const Cols<NT> c = load_cols<NT, VEC>(s0 + (int64_t)row * a.Dv, s0 && row < Dk ? have : 0);
-#pragma unroll
-        for (int h = 0; h < NT; ++h) S[t][h][r] = c.v[h];
-      }
-  }
+  State<KP> S;
+  S.load(a.state0 ? a.state0 + bh * Dk * Dv + col : nullptr, Dk, Dv, n, g, have);
 
   // the next chunk's operands on their way
-  Raw8<T> kr[ITEMS][2], qr[ITEMS][2];
-  u4_t rr[(REC_USED + 4095) / 4096];
-  Cols<NT> vr[4][4];
+  Raw8<T> kr[ITEMS], qr[ITEMS];
+  u4_t rr[RR];
+  float vr[4][4];
   const auto fetch = [&](int64_t c) {
-    const int64_t t0 = c * CH;
+    const int left = (int)min((int64_t)CH, len - c * CH);
+    const Range kc = head_rows((const T*)a.k + keys + c * CH * qs, left, qs, Dk);
+    const Range qc = head_rows((const T*)a.q + keys + c * CH * qs, left, qs, Dk);
+    const Range vc = head_rows((const T*)a.v + values + c * CH * vs, have > 0 ? left : 0, vs, have);
+    const Range rc(rec + c * STRIDE, USED);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      const int x = i * 256 + tid, piece = x % PIECES, pair = x / PIECES;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t t = t0 + 2 * pair + j;
-        const int cnt = t < len ? max(0, min(8, Dk - 8 * piece)) : 0;
-        kr[i][j] = load_raw8<VEC>(kp + t * qs + 8 * piece, cnt);
-        if (!KEEP) qr[i][j] = load_raw8<VEC>(qp + t * qs + 8 * piece, cnt);
-      }
+      const int x = i * THREADS + tid, piece = x % PIECES, row = x / PIECES;
+      const uint32_t o = (row * qs + 8 * piece) * (uint32_t)sizeof(T);
+      kr[i].template load<VEC>(kc, o, Dk - 8 * piece);
+      if (MODE == OUT) qr[i].template load<VEC>(qc, o, Dk - 8 * piece);
     }
 #pragma unroll
-    for (int i = 0; i < (REC_USED + 4095) / 4096; ++i)
-      if (i * 4096 + tid * 16 < REC_USED)
-        rr[i] = *reinterpret_cast<const u4_t*>(rec + c * REC_STRIDE + i * 4096 + tid * 16);
+    for (int i = 0; i < RR; ++i) rr[i] = rc.quad((i * THREADS + tid) * 16);
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t tok = t0 + row_of(t, 4 * g + r);
-        vr[t][r] = load_cols<NT, VEC>(vp + tok * vs, tok < len ? have : 0);
-      }
+      for (int r = 0; r < 4; ++r) vr[t][r] = vc.get((const T*)nullptr, v_lane + row_of(t, r) * vs * (uint32_t)sizeof(T));
   };
   if (chunks > 0) fetch(0);
   for (int64_t c = 0; c < chunks; ++c) {
-    Op<NP> ko[ITEMS][2];
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      const int x = i * 256 + tid, piece = x % PIECES, pair = x / PIECES;
+      const int x = i * THREADS + tid, piece = x % PIECES, row = x / PIECES;
+      if (CH * PIECES % THREADS == 0 || row < CH) {
+        const Op<NP> ko = kr[i].op();
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        ko[i][j] = kr[i][j].op();
+        for (int p = 0; p < NP; ++p) *reinterpret_cast<bf8_t*>(lds.k[p] + Tk::at(place_of(row), piece)) = ko.p[p];
+        if (MODE == OUT) {
+          const Op<NP> qo = qr[i].op();
 #pragma unroll
-        for (int p = 0; p < NP; ++p)
-          *reinterpret_cast<bf8_t*>(lds.k[p] + Tokens<KP>::row_at(place_of(2 * pair + j), 16 * piece)) = ko[i][j].p[p];
-        if (!KEEP) {
-          const Op<NP> qo = qr[i][j].op();
-#pragma unroll
-          for (int p = 0; p < NP; ++p)
-            *reinterpret_cast<bf8_t*>(lds.q[p] + Tokens<KP>::row_at(2 * pair + j, 16 * piece)) = qo.p[p];
+          for (int p = 0; p < NP; ++p) *reinterpret_cast<bf8_t*>(lds.q[p] + Tk::at(row, piece)) = qo.p[p];
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < (REC_USED + 4095) / 4096; ++i)
-      if (i * 4096 + tid * 16 < REC_USED) *reinterpret_cast<u4_t*>(lds.rec + i * 4096 + tid * 16) = rr[i];
-    Cols<NT> v[4][4];
+    for (int i = 0; i < RR; ++i) *reinterpret_cast<u4_t*>(lds.rec + (i * THREADS + tid) * 16) = rr[i];
+    f4_t v[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[t][r] = vr[t][r];
+    for (int t = 0; t < 4; ++t) v[t] = f4_t{vr[t][0], vr[t][1], vr[t][2], vr[t][3]};
     __syncthreads();
+    if (c + 1 < chunks) fetch(c + 1);
+    if (MODE == KEEP) S.keep((bf16_t*)a.states + (bh * a.NC + c) * 2 * KP * VP, VP, col, n, g);
 
-    if (KEEP && col < a.VP) {
-      bf16_t* keep = (bf16_t*)a.states + (bh * a.NC + c) * 2 * KP * a.VP + col;
-#pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          Cols<NT> y;
-#pragma unroll
-          for (int h = 0; h < NT; ++h) y.v[h] = S[t][h][r];
-          store_parts<NT>(keep + row_of(t, 4 * g + r) * a.VP, KP * a.VP, y);
-        }
-    }
     // K M and Q M
-    f4_t km[4][NT], o[4][NT];
+    f4_t x[4], o[4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int h = 0; h < NT; ++h) km[t][h] = o[t][h] = f4_t{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < 4; ++t) x[t] = o[t] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
-      Split sf[NT];
-#pragma unroll
-      for (int h = 0; h < NT; ++h) sf[h] = split(S[2 * kb][h], S[2 * kb + 1][h]);
+      const Split sf = split(S.m[2 * kb], S.m[2 * kb + 1]);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         Op<NP> ka, qa;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          const int at = Tokens<KP>::row_at(16 * t + n, 64 * kb + 16 * g);
-          ka.p[p] = *reinterpret_cast<const bf8_t*>(lds.k[p] + at);
-          if (!KEEP) qa.p[p] = *reinterpret_cast<const bf8_t*>(lds.q[p] + at);
+          ka.p[p] = Tk::rows(lds.k[p], rows_at, t, kb);
+          if (MODE == OUT) qa.p[p] = Tk::rows(lds.q[p], rows_at, t, kb);
         }
-#pragma unroll
-        for (int h = 0; h < NT; ++h) {
-          km[t][h] = mma(ka, sf[h], km[t][h]);
-          if (!KEEP) o[t][h] = mma(qa, sf[h], o[t][h]);
-        }
+        x[t] = mma(ka, sf, x[t]);
+        if (MODE == OUT) o[t] = mma(qa, sf, o[t]);
       }
+      keep_order();
     }
-    __syncthreads();
-    // the keys take the rows' place, transposed, two tokens at a time
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int x = i * 256 + tid, piece = x % PIECES, pair = x / PIECES;
-#pragma unroll
-      for (int p = 0; p < NP; ++p) store_transposed<KP>(lds.k[p], pair, piece, ko[i][0].p[p], ko[i][1].p[p]);
-    }
-    if (c + 1 < chunks) fetch(c + 1);
-
     // R = V - exp(G) K M, Z = T R, X = beta Z
     const float* dec = (const float*)(lds.rec + REC_DEC);
-    Split x[2][NT];
-    {
-      Split rf[2][NT];
+    Split f[2];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const f4_t ahead = *reinterpret_cast<const f4_t*>(dec + DEC_AHEAD + row_of(t, 4 * g));
+    for (int t = 0; t < 4; ++t) {
+      x[t] = v[t] - *reinterpret_cast<const f4_t*>(dec + DEC_AHEAD + row_of(t, 4 * g)) * x[t];
+    }
 #pragma unroll
-        for (int h = 0; h < NT; ++h)
+    for (int kb = 0; kb < 2; ++kb) f[kb] = split(x[2 * kb], x[2 * kb + 1]);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) km[t][h][r] = v[t][r].v[h] - ahead[r] * km[t][h][r];
-      }
+    for (int t = 0; t < 4; ++t) x[t] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
-        for (int h = 0; h < NT; ++h) rf[kb][h] = split(km[2 * kb][h], km[2 * kb + 1][h]);
+      for (int t = 2 * kb; t < 4; ++t) x[t] = mma(load_tile(lds.rec + REC_T, tri(t, kb), lane), f[kb], x[t]);
+      keep_order();
+    }
+    if (MODE == KEEP) {
+      const Range z((bf16_t*)a.z + (bh * a.NC + c) * 2 * CH * VP, 4 * CH * VP);
+      const uint32_t z_lane = col < VP ? 2 * (8 * g * VP + col + n) : NOWHERE;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int h = 0; h < NT; ++h) km[t][h] = f4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int t = 2 * kb; t < 4; ++t) {
-          const Split ta = load_tile(lds.rec + REC_T, tri(t, kb), lane);
-#pragma unroll
-          for (int h = 0; h < NT; ++h) km[t][h] = mma(ta, rf[kb][h], km[t][h]);
-        }
-      if (KEEP && col < a.VP) {
-        bf16_t* keep = (bf16_t*)a.z + (bh * a.NC + c) * 2 * CH * a.VP + col;
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            Cols<NT> y;
-#pragma unroll
-            for (int h = 0; h < NT; ++h) y.v[h] = km[t][h][r];
-            store_parts<NT>(keep + row_of(t, 4 * g + r) * a.VP, CH * a.VP, y);
-          }
-      }
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const f4_t beta = *reinterpret_cast<const f4_t*>(dec + DEC_BETA + row_of(t, 4 * g));
-#pragma unroll
-        for (int h = 0; h < NT; ++h) km[t][h] *= beta;
-      }
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int h = 0; h < NT; ++h) x[kb][h] = split(km[2 * kb][h], km[2 * kb + 1][h]);
+        for (int r = 0; r < 4; ++r) z.put_parts(z_lane + 2 * row_of(t, r) * VP, 2 * CH * VP, x[t][r]);
     }
-    if (!KEEP) {  // O = scale (exp(G) Q M + P X)
+#pragma unroll
+    for (int t = 0; t < 4; ++t) x[t] *= *reinterpret_cast<const f4_t*>(dec + DEC_BETA + row_of(t, 4 * g));
+    if (MODE == OUT) {  // O = scale (exp(G) Q M + P X)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) f[kb] = split(x[2 * kb], x[2 * kb + 1]);
+      const Range oc = head_rows((T*)a.o + values + c * CH * vs, have > 0 ? (int)min((int64_t)CH, len - c * CH) : 0, vs, have);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const f4_t ahead = *reinterpret_cast<const f4_t*>(dec + DEC_AHEAD + 16 * t + 4 * g);
+        o[t] *= *reinterpret_cast<const f4_t*>(dec + DEC_AHEAD + 16 * t + 4 * g);
 #pragma unroll
-        for (int h = 0; h < NT; ++h) o[t][h] *= ahead;
+        for (int kb = 0; kb <= (t >> 1); ++kb) o[t] = mma(load_tile(lds.rec + REC_P, tri(t, kb), lane), f[kb], o[t]);
 #pragma unroll
-        for (int kb = 0; kb <= (t >> 1); ++kb) {
-          const Split pa = load_tile(lds.rec + REC_P, tri(t, kb), lane);
-#pragma unroll
-          for (int h = 0; h < NT; ++h) o[t][h] = mma(pa, x[kb][h], o[t][h]);
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int64_t tok = c * CH + 16 * t + 4 * g + r;
-          Cols<NT> y;
-#pragma unroll
-          for (int h = 0; h < NT; ++h) y.v[h] = a.scale * o[t][h][r];
-          store_cols<NT, VEC>(op + tok * vs, tok < len ? have : 0, y);
-        }
+        for (int r = 0; r < 4; ++r)
+          oc.put((T*)nullptr, o_lane + (16 * t + r) * vs * (uint32_t)sizeof(T), a.scale * o[t][r]);
+        keep_order();
       }
     }
     // M = exp(G_end) M + K^T (exp(G_end - G) X)
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const f4_t to_end = *reinterpret_cast<const f4_t*>(dec + DEC_TO_END + row_of(t, 4 * g));
+    for (int t = 0; t < 4; ++t) x[t] *= *reinterpret_cast<const f4_t*>(dec + DEC_TO_END + row_of(t, 4 * g));
 #pragma unroll
-      for (int h = 0; h < NT; ++h) km[t][h] *= to_end;
-    }
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int h = 0; h < NT; ++h) x[kb][h] = split(km[2 * kb][h], km[2 * kb + 1][h]);
+    for (int kb = 0; kb < 2; ++kb) f[kb] = split(x[2 * kb], x[2 * kb + 1]);
     const float whole = dec[DEC_AHEAD + CH - 1];
-    __syncthreads();
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
-#pragma unroll
-      for (int h = 0; h < NT; ++h) S[t][h] *= whole;
+      S.m[t] *= whole;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
         Op<NP> ka;
 #pragma unroll
-        for (int p = 0; p < NP; ++p)
-          ka.p[p] = *reinterpret_cast<const bf8_t*>(lds.k[p] + Tokens<KP>::col_at(16 * t + n, 64 * kb + 16 * g));
-#pragma unroll
-        for (int h = 0; h < NT; ++h) S[t][h] = mma(ka, x[kb][h], S[t][h]);
+        for (int p = 0; p < NP; ++p) ka.p[p] = Tk::cols(lds.k[p], cols_at, t, kb);
+        S.m[t] = mma(ka, f[kb], S.m[t]);
       }
+      if (t & 1) keep_order();
     }
     __syncthreads();
   }
-  if (a.state1) {
-    float* s1 = a.state1 + bh * a.Dk * a.Dv + col;
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = row_of(t, 4 * g + r);
-        Cols<NT> y;
-#pragma unroll
-        for (int h = 0; h < NT; ++h) y.v[h] = S[t][h][r];
-        store_cols<NT, VEC>(s1 + (int64_t)row * a.Dv, row < Dk ? have : 0, y);
-      }
-  }
+  if (a.state1) S.store(a.state1 + bh * Dk * Dv + col, Dk, Dv, n, g, have);
 }
 
 // ---------------------------------------------------------------- token by token
@@ -458,8 +366,9 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
   __shared__ float qk_s[2][KP];
   __shared__ float part[2][4][8][12];
   const int tid = threadIdx.x, w = tid >> 6, cl = tid & 7, rg = tid >> 3;
-  const int64_t groups = (a.Dv + 31) / 32;
-  const int64_t bh = blockIdx.x / groups, b = bh / a.Hv, hv = bh % a.Hv, hk = hv / (a.Hv / a.Hk);
+  const uint32_t groups = ((uint32_t)a.Dv + 31) / 32;
+  const int64_t bh = blockIdx.x / groups, b = (uint32_t)bh / (uint32_t)a.Hv;
+  const int64_t hv = (uint32_t)bh % (uint32_t)a.Hv, hk = (uint32_t)hv / ((uint32_t)a.Hv / (uint32_t)a.Hk);
   const int col = (int)(blockIdx.x % groups) * 32 + 4 * cl, have = max(0, min(4, (int)a.Dv - col));
   const int64_t len = length_of(a.lengths, b, a.S);
   f4_t S[R];
@@ -548,42 +457,42 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
 
 constexpr int SHORT = 8;  // tokens up to which they are taken one by one
 
-template <typename T, int KP, int NT, bool KEEP>
+template <typename T, int KP, int NW, int MODE>
 hipError_t walk_go(const DeltaArgs& a, hipStream_t st) {
-  const size_t lds = sizeof(WalkLds<KP, Stream<T>::NP, KEEP>);
-  const dim3 prep((unsigned)(a.B * a.Hk * a.NC)), walk((unsigned)(a.B * a.Hv * ((a.Dv + 64 * NT - 1) / (64 * NT))));
+  const size_t lds = sizeof(WalkLds<KP, Stream<T>::NP, NW, MODE>);
+  const dim3 prep((unsigned)(a.B * a.Hk * a.NC)), walk((unsigned)(a.B * a.Hv * ((a.Dv + 16 * NW - 1) / (16 * NW))));
   const auto go = [&](auto prep_k, auto walk_k) {
     if (lds > 64 * 1024) {
       hipError_t e = hipFuncSetAttribute((const void*)walk_k, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
       if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL(prep_k, prep, dim3(256), 0, st, a);
-    hipLaunchKernelGGL(walk_k, walk, dim3(256), lds, st, a);
+    hipLaunchKernelGGL(walk_k, walk, dim3(64 * NW), lds, st, a);
     return hipGetLastError();
   };
-  if (a.vec) return go(delta_prep_kernel<T, KP, true, KEEP>, delta_walk_kernel<T, KP, NT, true, KEEP>);
-  return go(delta_prep_kernel<T, KP, false, KEEP>, delta_walk_kernel<T, KP, NT, false, KEEP>);
+  if (a.vec) return go(delta_prep_kernel<T, KP, true, MODE == KEEP>, delta_walk_kernel<T, KP, NW, true, MODE>);
+  return go(delta_prep_kernel<T, KP, false, MODE == KEEP>, delta_walk_kernel<T, KP, NW, false, MODE>);
 }
 
-template <typename T, int KP, bool KEEP>
+template <typename T, int KP, int MODE>
 hipError_t delta_go(const DeltaArgs& a, hipStream_t st) {
-  if (!KEEP && a.S <= SHORT) {
+  if (MODE == OUT && a.S <= SHORT) {
     const dim3 grid((unsigned)(a.B * a.Hv * ((a.Dv + 31) / 32)));
     if (a.vec && a.Dv % 4 == 0) hipLaunchKernelGGL((delta_step_kernel<T, KP, true>), grid, dim3(256), 0, st, a);
     else hipLaunchKernelGGL((delta_step_kernel<T, KP, false>), grid, dim3(256), 0, st, a);
     return hipGetLastError();
   }
-  if constexpr (KP < 256) {
-    if (a.Dv > 64) return walk_go<T, KP, 2, KEEP>(a, st);
+  if constexpr (KP < 256) {  // wider states leave no registers for eight waves
+    if (a.Dv > 64) return walk_go<T, KP, 8, MODE>(a, st);
   }
-  return walk_go<T, KP, 1, KEEP>(a, st);
+  return walk_go<T, KP, 4, MODE>(a, st);
 }
 
-template <typename T, bool KEEP>
+template <typename T, int MODE>
 hipError_t delta_by_width(const DeltaArgs& a, hipStream_t st) {
-  if (a.Dk <= 64) return delta_go<T, 64, KEEP>(a, st);
-  if (a.Dk <= 128) return delta_go<T, 128, KEEP>(a, st);
-  return delta_go<T, 256, KEEP>(a, st);
+  if (a.Dk <= 64) return delta_go<T, 64, MODE>(a, st);
+  if (a.Dk <= 128) return delta_go<T, 128, MODE>(a, st);
+  return delta_go<T, 256, MODE>(a, st);
 }
 
 }  // namespace
@@ -593,11 +502,11 @@ int64_t delta_ws_bytes(int64_t B, int64_t S, int64_t Hv) {
 }
 
 hipError_t launch_delta(int dtype, const DeltaArgs& a, hipStream_t st) {
-  return dtype == 0 ? delta_by_width<float, false>(a, st) : delta_by_width<bf16_t, false>(a, st);
+  return dtype == 0 ? delta_by_width<float, OUT>(a, st) : delta_by_width<bf16_t, OUT>(a, st);
 }
 
 hipError_t launch_delta_keep(int dtype, const DeltaArgs& a, hipStream_t st) {
-  return dtype == 0 ? delta_by_width<float, true>(a, st) : delta_by_width<bf16_t, true>(a, st);
+  return dtype == 0 ? delta_by_width<float, KEEP>(a, st) : delta_by_width<bf16_t, KEEP>(a, st);
 }
 
 }  // namespace hc

@@ -17,169 +17,113 @@ namespace hc {
 
 namespace {
 
-template <int KP, int NP>
+template <int KP, int NP, int NW>
 struct BackLds {
-  char k[NP][Tokens<KP>::PART];         // keys: rows in row_of's order, then transposed
-  char q[NP][KP * Tokens<KP>::COL];     // queries transposed
-  char rec[REC_BWD - REC_DEC];
+  static constexpr int PASS = 1024 * NW;  // bytes that the threads bring in at once
+  char k[NP][Tokens<KP>::BYTES], q[NP][Tokens<KP>::BYTES];  // rows in row_of's order
+  char rec[(REC_BWD - REC_DEC + PASS - 1) / PASS * PASS];
 };
 
-template <typename T, int KP, int NT, bool VEC>
-__global__ __launch_bounds__(256) void delta_back_kernel(DeltaArgs a) {
-  constexpr int NP = Stream<T>::NP, KB = KP / 32, KT = KP / 16;
-  constexpr int PIECES = KP / 8, ITEMS = 32 * PIECES / 256;
-  constexpr int USED = REC_BWD - REC_DEC, RR = (USED + 4095) / 4096;
+template <typename T, int KP, int NW, bool VEC>
+__global__ __launch_bounds__(64 * NW) void delta_back_kernel(DeltaArgs a) {
+  constexpr int NP = Stream<T>::NP, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
+  constexpr int PIECES = KP / 8, ITEMS = (CH * PIECES + THREADS - 1) / THREADS;
+  constexpr int USED = REC_BWD - REC_DEC, RR = (USED + 16 * THREADS - 1) / (16 * THREADS);
   constexpr int PT = REC_P - REC_DEC, TT = REC_TT - REC_DEC;
   extern __shared__ __attribute__((aligned(16))) char lds_raw[];
-  typedef BackLds<KP, NP> Lds;
+  typedef BackLds<KP, NP, NW> Lds;
+  typedef Tokens<KP> Tk;
   static_assert(sizeof(Lds) <= 160 * 1024, "LDS of a CU");
   Lds& lds = *reinterpret_cast<Lds*>(lds_raw);
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n = lane & 15, g = lane >> 4;
-  const int64_t groups = (a.Dv + 64 * NT - 1) / (64 * NT);
-  const int64_t bh = blockIdx.x / groups, b = bh / a.Hv, hv = bh % a.Hv, hk = hv / (a.Hv / a.Hk);
-  const int Dk = (int)a.Dk;
-  const int col = (int)(blockIdx.x % groups) * 64 * NT + 16 * NT * w + NT * n, have = max(0, min(NT, (int)a.Dv - col));
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_number(), n = lane & 15, g = lane >> 4;
+  const int rows_at = Tk::lane_at(n, g), cols_at = Tk::lane_at_t(n, g);
+  const uint32_t groups = ((uint32_t)a.Dv + 16 * NW - 1) / (16 * NW);
+  const int64_t bh = blockIdx.x / groups, b = (uint32_t)bh / (uint32_t)a.Hv;
+  const uint32_t hv = (uint32_t)bh % (uint32_t)a.Hv, hk = hv / ((uint32_t)a.Hv / (uint32_t)a.Hk);
+  const int Dk = (int)a.Dk, Dv = (int)a.Dv, VP = (int)a.VP, qs = (int)a.Hk * Dk, vs = (int)a.Hv * Dv;
+  const int col = (int)(blockIdx.x % groups) * 16 * NW + 16 * w, have = min(16, Dv - col);  // columns; may be none
   const int64_t len = length_of(a.lengths, b, a.S), chunks = (len + CH - 1) / CH;
-  const int64_t qs = a.Hk * a.Dk, vs = a.Hv * a.Dv;
-  const T* qp = (const T*)a.q + b * a.S * qs + hk * a.Dk;
-  const T* kp = (const T*)a.k + b * a.S * qs + hk * a.Dk;
-  const T* dp = (const T*)a.d_o + b * a.S * vs + hv * a.Dv + col;
-  T* dvp = (T*)a.dv + b * a.S * vs + hv * a.Dv + col;
+  const int64_t keys = b * a.S * qs + hk * Dk, values = b * a.S * vs + hv * Dv + col;
   const char* rec = (const char*)a.rec + bh * a.NC * REC_BWD + REC_DEC;
+  const uint32_t v_lane = n < have ? (8 * g * vs + n) * (uint32_t)sizeof(T) : NOWHERE;
 
-  f4_t D[KT][NT];
-  {
-    const float* s1 = a.dlast ? a.dlast + bh * a.Dk * a.Dv + col : nullptr;
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = row_of(t, 4 * g + r);
-        const Cols<NT> c = load_cols<NT, VEC>(s1 + (int64_t)row * a.Dv, s1 && row < Dk ? have : 0);
-#pragma unroll
-        for (int h = 0; h < NT; ++h) D[t][h][r] = c.v[h];
-      }
-  }
-  {  // nothing reaches the tokens behind the sequence's length
-    Cols<NT> zero;
-#pragma unroll
-    for (int h = 0; h < NT; ++h) zero.v[h] = 0.f;
-    for (int64_t t = len + g; t < a.S; t += 4) store_cols<NT, VEC>(dvp + t * vs, have, zero);
-  }
+  State<KP> D;
+  D.load(a.dlast ? a.dlast + bh * Dk * Dv + col : nullptr, Dk, Dv, n, g, have);
+  // nothing reaches the tokens behind the sequence's length
+  if (n < have)
+    for (int64_t t = len + g; t < a.S; t += 4) Elem<T>::st((T*)a.dv + values + t * vs + n, 0.f);
 
-  Raw8<T> kr[ITEMS][2], qr[ITEMS][2];
+  Raw8<T> kr[ITEMS], qr[ITEMS];
   u4_t rr[RR];
-  Cols<NT> dr[4][4];
+  float dr[4][4];
   const auto fetch = [&](int64_t c) {
-    const int64_t t0 = c * CH;
+    const int left = (int)min((int64_t)CH, len - c * CH);
+    const Range kc = head_rows((const T*)a.k + keys + c * CH * qs, left, qs, Dk);
+    const Range qc = head_rows((const T*)a.q + keys + c * CH * qs, left, qs, Dk);
+    const Range dc = head_rows((const T*)a.d_o + values + c * CH * vs, have > 0 ? left : 0, vs, have);
+    const Range rc(rec + c * REC_BWD, USED);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      const int x = i * 256 + tid, piece = x % PIECES, pair = x / PIECES;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t t = t0 + 2 * pair + j;
-        const int cnt = t < len ? max(0, min(8, Dk - 8 * piece)) : 0;
-        kr[i][j] = load_raw8<VEC>(kp + t * qs + 8 * piece, cnt);
-        qr[i][j] = load_raw8<VEC>(qp + t * qs + 8 * piece, cnt);
-      }
+      const int x = i * THREADS + tid, piece = x % PIECES, row = x / PIECES;
+      const uint32_t o = (row * qs + 8 * piece) * (uint32_t)sizeof(T);
+      kr[i].template load<VEC>(kc, o, Dk - 8 * piece);
+      qr[i].template load<VEC>(qc, o, Dk - 8 * piece);
     }
 #pragma unroll
-    for (int i = 0; i < RR; ++i)
-      if (i * 4096 + tid * 16 < USED) rr[i] = *reinterpret_cast<const u4_t*>(rec + c * REC_BWD + i * 4096 + tid * 16);
+    for (int i = 0; i < RR; ++i) rr[i] = rc.quad((i * THREADS + tid) * 16);
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int64_t tok = t0 + row_of(t, 4 * g + r);
-        dr[t][r] = load_cols<NT, VEC>(dp + tok * vs, tok < len ? have : 0);
-      }
+      for (int r = 0; r < 4; ++r) dr[t][r] = dc.get((const T*)nullptr, v_lane + row_of(t, r) * vs * (uint32_t)sizeof(T));
   };
   if (chunks > 0) fetch(chunks - 1);
   for (int64_t c = chunks - 1; c >= 0; --c) {
-    Op<NP> ko[ITEMS][2];
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      const int x = i * 256 + tid, piece = x % PIECES, pair = x / PIECES;
-      Op<NP> qo[2];
+      const int x = i * THREADS + tid, piece = x % PIECES, row = x / PIECES;
+      if (CH * PIECES % THREADS == 0 || row < CH) {
+        const Op<NP> ko = kr[i].op(), qo = qr[i].op();
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        ko[i][j] = kr[i][j].op();
-        qo[j] = qr[i][j].op();
-#pragma unroll
-        for (int p = 0; p < NP; ++p)
-          *reinterpret_cast<bf8_t*>(lds.k[p] + Tokens<KP>::row_at(place_of(2 * pair + j), 16 * piece)) = ko[i][j].p[p];
-      }
-#pragma unroll
-      for (int p = 0; p < NP; ++p) store_transposed<KP>(lds.q[p], pair, piece, qo[0].p[p], qo[1].p[p]);
-    }
-#pragma unroll
-    for (int i = 0; i < RR; ++i)
-      if (i * 4096 + tid * 16 < USED) *reinterpret_cast<u4_t*>(lds.rec + i * 4096 + tid * 16) = rr[i];
-    Cols<NT> d[4][4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) d[t][r] = dr[t][r];
-    if (col < a.VP) {
-      bf16_t* keep = (bf16_t*)a.dstates + (bh * a.NC + c) * 2 * KP * a.VP + col;
-#pragma unroll
-      for (int t = 0; t < KT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          Cols<NT> y;
-#pragma unroll
-          for (int h = 0; h < NT; ++h) y.v[h] = D[t][h][r];
-          store_parts<NT>(keep + row_of(t, 4 * g + r) * a.VP, KP * a.VP, y);
+        for (int p = 0; p < NP; ++p) {
+          const int at = Tk::at(place_of(row), piece);
+          *reinterpret_cast<bf8_t*>(lds.k[p] + at) = ko.p[p];
+          *reinterpret_cast<bf8_t*>(lds.q[p] + at) = qo.p[p];
         }
+      }
     }
+#pragma unroll
+    for (int i = 0; i < RR; ++i) *reinterpret_cast<u4_t*>(lds.rec + (i * THREADS + tid) * 16) = rr[i];
+    f4_t d[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) d[t] = f4_t{dr[t][0], dr[t][1], dr[t][2], dr[t][3]};
     __syncthreads();
+    if (c > 0) fetch(c - 1);
+    D.keep((bf16_t*)a.dstates + (bh * a.NC + c) * 2 * KP * VP, VP, col, n, g);
 
-    f4_t x[4][NT];  // K N
+    f4_t x[4];  // K N
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int h = 0; h < NT; ++h) x[t][h] = f4_t{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < 4; ++t) x[t] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
-      Split sf[NT];
-#pragma unroll
-      for (int h = 0; h < NT; ++h) sf[h] = split(D[2 * kb][h], D[2 * kb + 1][h]);
+      const Split sf = split(D.m[2 * kb], D.m[2 * kb + 1]);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         Op<NP> ka;
 #pragma unroll
-        for (int p = 0; p < NP; ++p)
-          ka.p[p] = *reinterpret_cast<const bf8_t*>(lds.k[p] + Tokens<KP>::row_at(16 * t + n, 64 * kb + 16 * g));
-#pragma unroll
-        for (int h = 0; h < NT; ++h) x[t][h] = mma(ka, sf[h], x[t][h]);
+        for (int p = 0; p < NP; ++p) ka.p[p] = Tk::rows(lds.k[p], rows_at, t, kb);
+        x[t] = mma(ka, sf, x[t]);
       }
+      keep_order();
     }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int it = i * 256 + tid, piece = it % PIECES, pair = it / PIECES;
-#pragma unroll
-      for (int p = 0; p < NP; ++p) store_transposed<KP>(lds.k[p], pair, piece, ko[i][0].p[p], ko[i][1].p[p]);
-    }
-    if (c > 0) fetch(c - 1);
-
     const float* dec = (const float*)lds.rec;
     // beta dX, dX = scale P^T dO + exp(G_end - G) K N
-#pragma unroll
-    for (int h = 0; h < NT; ++h) {
+    {
       Op<NP> df[2];
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = d[2 * kb + (e >> 2)][e & 3].v[h];
-        if (NP == 1) {
-          df[kb].p[0] = as_bf8(pack8(v));  // exact: they are bfloat16
-        } else {
-          const Split s = split(v);
-          df[kb].p[0] = s.hi;
-          df[kb].p[NP - 1] = s.lo;
-        }
+        const Split s = split(d[2 * kb], d[2 * kb + 1]);  // bfloat16 is its own high part
+        df[kb].p[0] = s.hi;
+        if (NP == 2) df[kb].p[NP - 1] = s.lo;
       }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -188,136 +132,99 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaArgs a) {
         for (int kb = t >> 1; kb < 2; ++kb) p = mma(load_tile(lds.rec + PT, tri_t(t, kb), lane), df[kb], p);
         const f4_t to_end = *reinterpret_cast<const f4_t*>(dec + DEC_TO_END + row_of(t, 4 * g));
         const f4_t beta = *reinterpret_cast<const f4_t*>(dec + DEC_BETA + row_of(t, 4 * g));
-        x[t][h] = beta * (a.scale * p + to_end * x[t][h]);
+        x[t] = beta * (a.scale * p + to_end * x[t]);
       }
+      keep_order();
     }
     // W = T^T (beta dX)
-    {
-      Split xf[2][NT];
+    Split f[2], wf[2];
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < 2; ++kb) f[kb] = split(x[2 * kb], x[2 * kb + 1]);
 #pragma unroll
-        for (int h = 0; h < NT; ++h) xf[kb][h] = split(x[2 * kb][h], x[2 * kb + 1][h]);
+    for (int t = 0; t < 4; ++t) {
+      x[t] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int h = 0; h < NT; ++h) x[t][h] = f4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int kb = t >> 1; kb < 2; ++kb) {
-          const Split ta = load_tile(lds.rec + TT, tri_t(t, kb), lane);
-#pragma unroll
-          for (int h = 0; h < NT; ++h) x[t][h] = mma(ta, xf[kb][h], x[t][h]);
-        }
+      for (int kb = t >> 1; kb < 2; ++kb) x[t] = mma(load_tile(lds.rec + TT, tri_t(t, kb), lane), f[kb], x[t]);
     }
+    keep_order();
     {
-      bf16_t* keep = (bf16_t*)a.w + (bh * a.NC + c) * 2 * CH * a.VP + col;
+      const Range vc = head_rows((T*)a.dv + values + c * CH * vs, have > 0 ? (int)min((int64_t)CH, len - c * CH) : 0, vs, have);
+      const Range wc((bf16_t*)a.w + (bh * a.NC + c) * 2 * CH * VP, 4 * CH * VP);
+      const uint32_t w_lane = col < VP ? 2 * (8 * g * VP + col + n) : NOWHERE;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int row = row_of(t, 4 * g + r);
-          Cols<NT> y;
-#pragma unroll
-          for (int h = 0; h < NT; ++h) y.v[h] = x[t][h][r];
-          const int64_t tok = c * CH + row;
-          store_cols<NT, VEC>(dvp + tok * vs, tok < len ? have : 0, y);
-          if (col < a.VP) store_parts<NT>(keep + row * a.VP, CH * a.VP, y);
+          vc.put((T*)nullptr, v_lane + row_of(t, r) * vs * (uint32_t)sizeof(T), x[t][r]);
+          wc.put_parts(w_lane + 2 * row_of(t, r) * VP, 2 * CH * VP, x[t][r]);
         }
     }
     // the gradient of the state before the chunk
-    Split df[2][NT], wf[2][NT];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const f4_t ahead = *reinterpret_cast<const f4_t*>(dec + DEC_AHEAD + row_of(t, 4 * g));
-#pragma unroll
-      for (int h = 0; h < NT; ++h) {
-        x[t][h] *= -ahead;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) d[t][r].v[h] *= a.scale * ahead[r];
-      }
+      x[t] *= -ahead;
+      d[t] *= a.scale * ahead;
     }
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int h = 0; h < NT; ++h) {
-        wf[kb][h] = split(x[2 * kb][h], x[2 * kb + 1][h]);
-        float v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = d[2 * kb + (e >> 2)][e & 3].v[h];
-        df[kb][h] = split(v);
-      }
+    for (int kb = 0; kb < 2; ++kb) {
+      wf[kb] = split(x[2 * kb], x[2 * kb + 1]);
+      f[kb] = split(d[2 * kb], d[2 * kb + 1]);
+    }
     const float whole = dec[DEC_AHEAD + CH - 1];
-    __syncthreads();
+    keep_order();
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
-#pragma unroll
-      for (int h = 0; h < NT; ++h) D[t][h] *= whole;
+      D.m[t] *= whole;
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
         Op<NP> ka, qa;
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
-          const int at = Tokens<KP>::col_at(16 * t + n, 64 * kb + 16 * g);
-          ka.p[p] = *reinterpret_cast<const bf8_t*>(lds.k[p] + at);
-          qa.p[p] = *reinterpret_cast<const bf8_t*>(lds.q[p] + at);
+          ka.p[p] = Tk::cols(lds.k[p], cols_at, t, kb);
+          qa.p[p] = Tk::cols(lds.q[p], cols_at, t, kb);
         }
-#pragma unroll
-        for (int h = 0; h < NT; ++h) {
-          D[t][h] = mma(qa, df[kb][h], D[t][h]);
-          D[t][h] = mma(ka, wf[kb][h], D[t][h]);
-        }
+        D.m[t] = mma(qa, f[kb], D.m[t]);
+        D.m[t] = mma(ka, wf[kb], D.m[t]);
       }
+      keep_order();
     }
     __syncthreads();
   }
-  if (a.dstate0) {
-    float* s0 = a.dstate0 + bh * a.Dk * a.Dv + col;
-#pragma unroll
-    for (int t = 0; t < KT; ++t)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = row_of(t, 4 * g + r);
-        Cols<NT> y;
-#pragma unroll
-        for (int h = 0; h < NT; ++h) y.v[h] = D[t][h][r];
-        store_cols<NT, VEC>(s0 + (int64_t)row * a.Dv, row < Dk ? have : 0, y);
-      }
-  }
+  if (a.dstate0) D.store(a.dstate0 + bh * Dk * Dv + col, Dk, Dv, n, g, have);
 }
 
 // ------------------------------------------------------------- each chunk by itself
 
 template <int KP, int NP>
 struct GradLds {
-  char k[NP][KP * Tokens<KP>::COL];  // transposed
-  char q[NP][KP * Tokens<KP>::COL];
+  char k[NP][Tokens<KP>::BYTES], q[NP][Tokens<KP>::BYTES];  // rows in row_of's order
   double G[CH];
   float beta[CH], dG[CH], end[4];
 };
 
+// Eight elements at byte offset o, the first `cnt` of them (VEC: all or none).
 template <bool VEC>
-__device__ __forceinline__ void store8_some(bf16_t* p, int cnt, const float v[8]) {
+__device__ __forceinline__ void put_row8(bf16_t* p, const Range& m, uint32_t o, int cnt, const float v[8]) {
   if (VEC) {
-    if (cnt > 0) *reinterpret_cast<u4_t*>(p) = pack8(v);
+    m.put_quad(cnt > 0 ? o : NOWHERE, pack8(v));
   } else {
-    store8_tail(p, cnt, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m.put(p, e < cnt ? o + 2 * e : NOWHERE, v[e]);
   }
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store8_some(float* p, int cnt, const float v[8]) {
-  if (VEC) {
-    if (cnt > 0) store8(p, v);
-  } else {
-    store8_tail(p, cnt, v);
+__device__ __forceinline__ void put_row8(float* p, const Range& m, uint32_t o, int cnt, const float v[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (VEC) {
+      m.put_quad(cnt > 0 ? o + 16 * h : NOWHERE, __builtin_bit_cast(u4_t, f4_t{v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]}));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m.put(p, 4 * h + e < cnt ? o + 16 * h + 4 * e : NOWHERE, v[4 * h + e]);
+    }
   }
-}
-
-// A row's 32 values from k0 + 8 g of a kept array in two parts.
-__device__ __forceinline__ Split kept_op(const bf16_t* p, int64_t lo) {
-  return {*reinterpret_cast<const bf8_t*>(p), *reinterpret_cast<const bf8_t*>(p + lo)};
 }
 
 __device__ __forceinline__ float sum_groups(float v) {  // over the four lanes of a token
@@ -329,62 +236,74 @@ __device__ __forceinline__ float sum_groups(float v) {  // over the four lanes o
 template <typename T, int KP, bool VEC, bool SHARED>
 __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
   constexpr int NP = Stream<T>::NP, KB = KP / 32, KT = KP / 16;
-  constexpr int PIECES = KP / 8, ITEMS = 32 * PIECES / 256;
+  constexpr int PIECES = KP / 8, ITEMS = CH * PIECES / 256;
   extern __shared__ __attribute__((aligned(16))) char lds_raw[];
   typedef GradLds<KP, NP> Lds;
+  typedef Tokens<KP> Tk;
   static_assert(sizeof(Lds) <= 160 * 1024, "LDS of a CU");
   Lds& lds = *reinterpret_cast<Lds*>(lds_raw);
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, n = lane & 15, g = lane >> 4;
-  const int64_t NC = a.NC, chunk = blockIdx.x % NC, bh = blockIdx.x / NC, b = bh / a.Hk, hk = bh % a.Hk;
-  const int64_t t0 = chunk * CH, tokens = length_of(a.lengths, b, a.S) - t0, rows = a.S - t0;
-  const int Dk = (int)a.Dk, Dv = (int)a.Dv, VP = (int)a.VP;
-  const int64_t qs = a.Hk * a.Dk, vs = a.Hv * a.Dv;
-  const int64_t q0 = (b * a.S + t0) * qs + hk * a.Dk;
-  const T* q = (const T*)a.q + q0;
-  const T* k = (const T*)a.k + q0;
-  const int tok = 16 * w + n, per = (int)(a.Hv / a.Hk);
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_number();
+  int n = lane & 15, g = lane >> 4;
+  const uint32_t NC = (uint32_t)a.NC, chunk = blockIdx.x % NC, bh = blockIdx.x / NC, hk = bh % (uint32_t)a.Hk;
+  const int64_t b = bh / (uint32_t)a.Hk, t0 = (int64_t)chunk * CH, tokens = length_of(a.lengths, b, a.S) - t0;
+  const int rows = (int)min((int64_t)CH, a.S - t0), left = (int)max((int64_t)0, min((int64_t)CH, tokens));
+  const int Dk = (int)a.Dk, Dv = (int)a.Dv, VP = (int)a.VP, qs = (int)a.Hk * Dk, vs = (int)a.Hv * Dv;
+  const int per = (int)((uint32_t)a.Hv / (uint32_t)a.Hk);
+  const int64_t keys = (b * a.S + t0) * qs + hk * Dk;
+  const Range q = head_rows((const T*)a.q + keys, left, qs, Dk), k = head_rows((const T*)a.k + keys, left, qs, Dk);
+  const int cols_at = Tk::lane_at_t(n, g);
 
   f4_t dqt[KT], dkt[KT];
 #pragma unroll
   for (int t = 0; t < KT; ++t) dqt[t] = dkt[t] = f4_t{0.f, 0.f, 0.f, 0.f};
   f4_t kk[4], qk[4];  // rows: the other token in row_of's order, by k_n
-  if (tokens > 0) {
+  if (left > 0) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      const int x = i * 256 + tid, piece = x % PIECES, pair = x / PIECES;
-      const Op<NP> k0 = token_op<T, VEC>(k, qs, tokens, 2 * pair, 8 * piece, Dk);
-      const Op<NP> k1 = token_op<T, VEC>(k, qs, tokens, 2 * pair + 1, 8 * piece, Dk);
-      const Op<NP> q0 = token_op<T, VEC>(q, qs, tokens, 2 * pair, 8 * piece, Dk);
-      const Op<NP> q1 = token_op<T, VEC>(q, qs, tokens, 2 * pair + 1, 8 * piece, Dk);
+      const int x = i * 256 + tid, piece = x % PIECES, row = x / PIECES;
+      const Op<NP> ko = token_op<T, VEC>(k, qs, row, 8 * piece, Dk), qo = token_op<T, VEC>(q, qs, row, 8 * piece, Dk);
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
-        store_transposed<KP>(lds.k[p], pair, piece, k0.p[p], k1.p[p]);
-        store_transposed<KP>(lds.q[p], pair, piece, q0.p[p], q1.p[p]);
+        const int at = Tk::at(place_of(row), piece);
+        *reinterpret_cast<bf8_t*>(lds.k[p] + at) = ko.p[p];
+        *reinterpret_cast<bf8_t*>(lds.q[p] + at) = qo.p[p];
       }
     }
+    __syncthreads();
+    const int rows_at = Tk::lane_at(n, g), own_at = Tk::at(place_of(16 * w + n), g);
 #pragma unroll
     for (int t = 0; t < 4; ++t) kk[t] = qk[t] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
-      const int k0 = 32 * kb + 8 * g;
-      const Op<NP> kn = token_op<T, VEC>(k, qs, tokens, tok, k0, Dk);
+      Op<NP> kn;
+#pragma unroll
+      for (int p = 0; p < NP; ++p) kn.p[p] = *reinterpret_cast<const bf8_t*>(lds.k[p] + (own_at ^ (kb << 6)));
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         if ((t >> 1) < (w >> 1)) continue;
-        kk[t] = mma(token_op<T, VEC>(k, qs, tokens, row_of(t, n), k0, Dk), kn, kk[t]);
-        qk[t] = mma(token_op<T, VEC>(q, qs, tokens, row_of(t, n), k0, Dk), kn, qk[t]);
+        Op<NP> ka, qa;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          ka.p[p] = Tk::rows(lds.k[p], rows_at, t, kb);
+          qa.p[p] = Tk::rows(lds.q[p], rows_at, t, kb);
+        }
+        kk[t] = mma(ka, kn, kk[t]);
+        qk[t] = mma(qa, kn, qk[t]);
       }
+      keep_order();
     }
   }
   for (int hi = 0; hi < per; ++hi) {
+    renew(n, g);
+    const int tok = 16 * w + n;
     const int64_t hv = hk * per + hi, at = (b * a.Hv + hv) * NC + chunk;
     const int64_t gat = (b * a.S + t0) * a.Hv + hv;
-    if (tokens <= 0) {
-      if (tid < CH && tid < rows) a.dg[gat + tid * a.Hv] = a.dbeta[gat + tid * a.Hv] = 0.f;
+    if (left == 0) {
+      if (tid < rows) a.dg[gat + tid * a.Hv] = a.dbeta[gat + tid * a.Hv] = 0.f;
       continue;
     }
     if (tid < CH) {
-      const bool on = tid < tokens;
+      const bool on = tid < left;
       lds.G[tid] = running_sum(on ? clamp_decay(a.g[gat + tid * a.Hv]) : 0.0, tid);
       lds.beta[tid] = on ? a.beta[gat + tid * a.Hv] : 0.f;
     }
@@ -392,12 +311,11 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
     const double Gn = lds.G[tok], Gend = lds.G[CH - 1];
     const float beta_n = lds.beta[tok], ahead = expf((float)Gn), to_end = expf((float)(Gend - Gn));
 
-    const T* dop = (const T*)a.d_o + (b * a.S + t0) * vs + hv * a.Dv;
-    const bf16_t* zp = (const bf16_t*)a.z + at * 2 * CH * VP;
-    const bf16_t* wp = (const bf16_t*)a.w + at * 2 * CH * VP;
-    const bf16_t* mp = (const bf16_t*)a.states + at * 2 * KP * VP;
-    const bf16_t* np = (const bf16_t*)a.dstates + at * 2 * KP * VP;
-    const int vlo = CH * VP, slo = KP * VP;
+    const Range dop = head_rows((const T*)a.d_o + (b * a.S + t0) * vs + hv * Dv, left, vs, Dv);
+    const Range zp((const bf16_t*)a.z + at * 2 * CH * VP, 4 * CH * VP), wp((const bf16_t*)a.w + at * 2 * CH * VP, 4 * CH * VP);
+    const Range mp((const bf16_t*)a.states + at * 2 * KP * VP, 4 * KP * VP);
+    const Range np((const bf16_t*)a.dstates + at * 2 * KP * VP, 4 * KP * VP);
+    const uint32_t vlo = 2 * CH * VP, slo = 2 * KP * VP;
     // rows j, lane i: Z_j . dO_i and Z_j . W_i; rows i, lane j: dO_i . Z_j and W_i . Z_j
     f4_t zd[4], zw[4], dz[4], wz[4];
     f4_t dq[KT], read[KT], early[KT];
@@ -407,31 +325,33 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
 #pragma unroll
     for (int t = 0; t < KT; ++t) dq[t] = read[t] = early[t] = f4_t{0.f, 0.f, 0.f, 0.f};
     for (int v0 = 8 * g; v0 < VP; v0 += 32) {
-      const Op<NP> dn = token_op<T, VEC>(dop, vs, tokens, tok, v0, Dv);
-      const Split zn = kept_op(zp + tok * VP + v0, vlo), wn = kept_op(wp + tok * VP + v0, vlo);
+      const Op<NP> dn = token_op<T, VEC>(dop, vs, tok, v0, Dv);
+      const Split zn = zp.parts(2 * (tok * VP + v0), vlo), wn = wp.parts(2 * (tok * VP + v0), vlo);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         const int row = row_of(t, n);
         if ((t >> 1) <= (w >> 1)) {
-          const Split zr = kept_op(zp + row * VP + v0, vlo);
+          const Split zr = zp.parts(2 * (row * VP + v0), vlo);
           zd[t] = mma(zr, dn, zd[t]);
           zw[t] = mma(zr, wn, zw[t]);
         }
         if ((t >> 1) >= (w >> 1)) {
-          dz[t] = mma(token_op<T, VEC>(dop, vs, tokens, row, v0, Dv), zn, dz[t]);
-          wz[t] = mma(kept_op(wp + row * VP + v0, vlo), zn, wz[t]);
+          dz[t] = mma(token_op<T, VEC>(dop, vs, row, v0, Dv), zn, dz[t]);
+          wz[t] = mma(wp.parts(2 * (row * VP + v0), vlo), zn, wz[t]);
         }
       }
+      keep_order();
 #pragma unroll
       for (int t = 0; t < KT; ++t) {
         const int row = row_of(t, n);
-        const Split m = kept_op(mp + row * VP + v0, slo), nn = kept_op(np + row * VP + v0, slo);
+        const Split m = mp.parts(2 * (row * VP + v0), slo), nn = np.parts(2 * (row * VP + v0), slo);
         dq[t] = mma(m, dn, dq[t]);
         read[t] = mma(m, wn, read[t]);
         early[t] = mma(nn, zn, early[t]);
         if ((t & 3) == w)
 #pragma unroll
           for (int e = 0; e < 8; ++e) mn += ((float)m.hi[e] + (float)m.lo[e]) * ((float)nn.hi[e] + (float)nn.lo[e]);
+        if (t & 1) keep_order();
       }
     }
     // what each pair of tokens passes on
@@ -472,9 +392,10 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
     for (int kb = 0; kb < KB; ++kb) {
       float kf[8], qf[8];
       {
-        const int cnt = tok < tokens ? max(0, min(8, Dk - 32 * kb - 8 * g)) : 0;
-        const int64_t o = tok * qs + 32 * kb + 8 * g;
-        const Raw8<T> kraw = load_raw8<VEC>(k + o, cnt), qraw = load_raw8<VEC>(q + o, cnt);
+        const int k0 = 32 * kb + 8 * g;
+        Raw8<T> kraw, qraw;
+        kraw.template load<VEC>(k, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0);
+        qraw.template load<VEC>(q, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0);
         kraw.open(kf);
         qraw.open(qf);
       }
@@ -494,9 +415,8 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
           Op<NP> ka, qa;
 #pragma unroll
           for (int p = 0; p < NP; ++p) {
-            const int o = Tokens<KP>::col_at(16 * t + n, 64 * b2 + 16 * g);
-            ka.p[p] = *reinterpret_cast<const bf8_t*>(lds.k[p] + o);
-            qa.p[p] = *reinterpret_cast<const bf8_t*>(lds.q[p] + o);
+            ka.p[p] = Tk::cols(lds.k[p], cols_at, t, b2);
+            qa.p[p] = Tk::cols(lds.q[p], cols_at, t, b2);
           }
           if (b2 <= (w >> 1)) {
             dq[t] = mma(ka, bq[b2], dq[t]);
@@ -512,6 +432,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
           dot += qf[4 * half + r] * dq[t][r] + kf[4 * half + r] * (read[t][r] - early[t][r]);
         dqt[t] = SHARED ? dqt[t] + dq[t] : dq[t];
         dkt[t] = SHARED ? dkt[t] + (read[t] + early[t]) : read[t] + early[t];
+        keep_order();
       }
     }
     dot = sum_groups(dot);
@@ -520,7 +441,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
     const float ends = wave_sum(at_end + expf((float)Gend) * mn);
     if (g == 0) {
       lds.dG[tok] = dot;
-      if (tok < rows) a.dbeta[gat + tok * a.Hv] = tok < tokens ? db : 0.f;
+      if (tok < rows) a.dbeta[gat + tok * a.Hv] = tok < left ? db : 0.f;
     }
     if (lane == 0) lds.end[w] = ends;
     __syncthreads();
@@ -532,41 +453,42 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
         if (tid + o < CH) s += down;
       }
       s += (lds.end[0] + lds.end[1]) + (lds.end[2] + lds.end[3]);
-      if (tid < rows) a.dg[gat + tid * a.Hv] = tid < tokens ? s : 0.f;
+      if (tid < rows) a.dg[gat + tid * a.Hv] = tid < left ? s : 0.f;
     }
     __syncthreads();
   }
+  const int tok = 16 * w + n;
+  const Range dqp = head_rows((T*)a.dq + keys, rows, qs, Dk), dkp = head_rows((T*)a.dk + keys, rows, qs, Dk);
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) {
-    const int cnt = tok < rows ? max(0, min(8, Dk - 32 * kb - 8 * g)) : 0;
-    const int64_t o = q0 + tok * qs + 32 * kb + 8 * g;
+    const int k0 = 32 * kb + 8 * g;
     float vq[8], vk[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      vq[e] = tok < tokens ? dqt[2 * kb + (e >> 2)][e & 3] : 0.f;
-      vk[e] = tok < tokens ? dkt[2 * kb + (e >> 2)][e & 3] : 0.f;
+      vq[e] = tok < left ? dqt[2 * kb + (e >> 2)][e & 3] : 0.f;
+      vk[e] = tok < left ? dkt[2 * kb + (e >> 2)][e & 3] : 0.f;
     }
-    store8_some<VEC>((T*)a.dq + o, cnt, vq);
-    store8_some<VEC>((T*)a.dk + o, cnt, vk);
+    put_row8<VEC>((T*)nullptr, dqp, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0, vq);
+    put_row8<VEC>((T*)nullptr, dkp, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0, vk);
   }
 }
 
 template <typename K>
-hipError_t with_lds(K kernel, size_t lds, unsigned grid, const DeltaArgs& a, hipStream_t st) {
+hipError_t with_lds(K kernel, size_t lds, unsigned grid, unsigned block, const DeltaArgs& a, hipStream_t st) {
   if (lds > 64 * 1024) {
     hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), lds, st, a);
+  hipLaunchKernelGGL(kernel, dim3(grid), dim3(block), lds, st, a);
   return hipGetLastError();
 }
 
-template <typename T, int KP, int NT>
+template <typename T, int KP, int NW>
 hipError_t back_go(const DeltaArgs& a, hipStream_t st) {
-  const unsigned grid = (unsigned)(a.B * a.Hv * ((a.Dv + 64 * NT - 1) / (64 * NT)));
-  const size_t lds = sizeof(BackLds<KP, Stream<T>::NP>);
-  return a.vec ? with_lds(delta_back_kernel<T, KP, NT, true>, lds, grid, a, st)
-               : with_lds(delta_back_kernel<T, KP, NT, false>, lds, grid, a, st);
+  const unsigned grid = (unsigned)(a.B * a.Hv * ((a.Dv + 16 * NW - 1) / (16 * NW)));
+  const size_t lds = sizeof(BackLds<KP, Stream<T>::NP, NW>);
+  return a.vec ? with_lds(delta_back_kernel<T, KP, NW, true>, lds, grid, 64 * NW, a, st)
+               : with_lds(delta_back_kernel<T, KP, NW, false>, lds, grid, 64 * NW, a, st);
 }
 
 template <typename T, int KP>
@@ -574,17 +496,17 @@ hipError_t grad_go(const DeltaArgs& a, hipStream_t st) {
   const unsigned grid = (unsigned)(a.B * a.Hk * a.NC);
   const size_t lds = sizeof(GradLds<KP, Stream<T>::NP>);
   if (a.Hv == a.Hk)
-    return a.vec8 ? with_lds(delta_grad_kernel<T, KP, true, false>, lds, grid, a, st)
-                  : with_lds(delta_grad_kernel<T, KP, false, false>, lds, grid, a, st);
-  return a.vec8 ? with_lds(delta_grad_kernel<T, KP, true, true>, lds, grid, a, st)
-                : with_lds(delta_grad_kernel<T, KP, false, true>, lds, grid, a, st);
+    return a.vec8 ? with_lds(delta_grad_kernel<T, KP, true, false>, lds, grid, 256, a, st)
+                  : with_lds(delta_grad_kernel<T, KP, false, false>, lds, grid, 256, a, st);
+  return a.vec8 ? with_lds(delta_grad_kernel<T, KP, true, true>, lds, grid, 256, a, st)
+                : with_lds(delta_grad_kernel<T, KP, false, true>, lds, grid, 256, a, st);
 }
 
 template <typename T, int KP>
 hipError_t backward_go(const DeltaArgs& a, hipStream_t st) {
   hipError_t e;
-  if constexpr (KP < 256) e = a.Dv > 64 ? back_go<T, KP, 2>(a, st) : back_go<T, KP, 1>(a, st);
-  else e = back_go<T, KP, 1>(a, st);
+  if constexpr (KP < 256) e = a.Dv > 64 ? back_go<T, KP, 8>(a, st) : back_go<T, KP, 4>(a, st);
+  else e = back_go<T, KP, 4>(a, st);
   return e != hipSuccess || a.NC == 0 ? e : grad_go<T, KP>(a, st);
 }
 

@@ -112,10 +112,68 @@ __device__ __forceinline__ f4_t mma(const Op<NP>& a, const Op<NP>& b, f4_t c) {
   return mma(a.p[0], b.p[0], c);
 }
 
-// Eight consecutive stream elements as stored; `cnt` of them exist (VEC: 8 or none).
+// Memory from an address that the wave's lanes have in common, read and written at 32-bit offsets:
+// what lies at or behind its end reads as 0 and is not written, so that neither the last chunk's
+// missing tokens nor a head's missing keys and columns need a branch. NOWHERE is behind every end
+// and stays so with a row's offset added (both below 2^31).
+constexpr uint32_t NOWHERE = 0x80000000u;
+
+struct Range {
+  __amdgpu_buffer_rsrc_t r;
+  __device__ __forceinline__ Range(const void* p, int64_t bytes)
+      : r(__builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00027000)) {}
+  __device__ __forceinline__ u4_t quad(uint32_t o) const {
+    return __builtin_bit_cast(u4_t, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, 0));
+  }
+  __device__ __forceinline__ float get(const float*, uint32_t o) const {
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, o, 0, 0));
+  }
+  __device__ __forceinline__ float get(const bf16_t*, uint32_t o) const {
+    return bf2f(__builtin_amdgcn_raw_buffer_load_b16(r, o, 0, 0));
+  }
+  __device__ __forceinline__ void put(float* , uint32_t o, float v) const {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, o, 0, 0);
+  }
+  __device__ __forceinline__ void put(bf16_t*, uint32_t o, float v) const {
+    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf2_hw(v, 0.f), r, o, 0, 0);
+  }
+  __device__ __forceinline__ void put_quad(uint32_t o, u4_t v) const {
+    __builtin_amdgcn_raw_buffer_store_b128(v, r, o, 0, 0);
+  }
+  // the two bfloat16 parts of v, the low one `lo` bytes behind the high one
+  __device__ __forceinline__ void put_parts(uint32_t o, uint32_t lo, float v) const {
+    const uint32_t h = pack_bf2_hw(v, 0.f);
+    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)h, r, o, 0, 0);
+    put((bf16_t*)nullptr, o + lo, v - __uint_as_float(h << 16));
+  }
+  __device__ __forceinline__ Split parts(uint32_t o, uint32_t lo) const {
+    return {__builtin_bit_cast(bf8_t, quad(o)), __builtin_bit_cast(bf8_t, quad(o + lo))};
+  }
+};
+
+// Rows of a head's keys, queries or values in a chunk: `left` of them, `stride` elements apart,
+// `width` elements each.
+template <typename T>
+__device__ __forceinline__ Range head_rows(const T* p, int left, int64_t stride, int width) {
+  return Range(p, left > 0 ? ((left - 1) * stride + width) * (int64_t)sizeof(T) : 0);
+}
+
+// Eight consecutive stream elements as stored, at byte offset o; the first `cnt` exist (VEC: all or
+// none).
 template <typename T> struct Raw8;
 template <> struct Raw8<bf16_t> {
   u4_t q;
+  template <bool VEC>
+  __device__ __forceinline__ void load(const Range& m, uint32_t o, int cnt) {
+    if (VEC) {
+      q = m.quad(cnt > 0 ? o : NOWHERE);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        q[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(m.r, 2 * i < cnt ? o + 4 * i : NOWHERE, 0, 0) |
+               (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(m.r, 2 * i + 1 < cnt ? o + 4 * i + 2 : NOWHERE, 0, 0) << 16;
+    }
+  }
   __device__ __forceinline__ Op<1> op() const { return {as_bf8(q)}; }
   __device__ __forceinline__ void open(float v[8]) const {
 #pragma unroll
@@ -127,6 +185,19 @@ template <> struct Raw8<bf16_t> {
 };
 template <> struct Raw8<float> {
   f4_t a, b;
+  template <bool VEC>
+  __device__ __forceinline__ void load(const Range& m, uint32_t o, int cnt) {
+    if (VEC) {
+      a = __builtin_bit_cast(f4_t, m.quad(cnt > 0 ? o : NOWHERE));
+      b = __builtin_bit_cast(f4_t, m.quad(cnt > 0 ? o + 16 : NOWHERE));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        a[e] = m.get((const float*)nullptr, e < cnt ? o + 4 * e : NOWHERE);
+        b[e] = m.get((const float*)nullptr, 4 + e < cnt ? o + 16 + 4 * e : NOWHERE);
+      }
+    }
+  }
   __device__ __forceinline__ Op<2> op() const {
     const Split s = split(a, b);
     return {s.hi, s.lo};
@@ -137,40 +208,12 @@ template <> struct Raw8<float> {
   }
 };
 
-template <bool VEC>
-__device__ __forceinline__ Raw8<bf16_t> load_raw8(const bf16_t* p, int cnt) {
-  Raw8<bf16_t> r;
-  r.q = u4_t{0, 0, 0, 0};
-  if (VEC) {
-    if (cnt > 0) r.q = *reinterpret_cast<const u4_t*>(p);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t x = e < cnt ? p[e] : 0;
-      r.q[e >> 1] |= x << (16 * (e & 1));
-    }
-  }
-  return r;
-}
-
-template <bool VEC>
-__device__ __forceinline__ Raw8<float> load_raw8(const float* p, int cnt) {
-  Raw8<float> r;
-  r.a = r.b = f4_t{0.f, 0.f, 0.f, 0.f};
-  if (VEC) {
-    if (cnt > 0) {
-      r.a = *reinterpret_cast<const f4_t*>(p);
-      r.b = *reinterpret_cast<const f4_t*>(p + 4);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = e < cnt ? p[e] : 0.f;
-      if (e < 4) r.a[e] = x;
-      else r.b[e - 4] = x;
-    }
-  }
-  return r;
+// Eight keys of a row from k0 on, as an operand.
+template <typename T, bool VEC>
+__device__ __forceinline__ Op<Stream<T>::NP> token_op(const Range& m, uint32_t stride, int row, int k0, int width) {
+  Raw8<T> x;
+  x.template load<VEC>(m, (row * stride + k0) * (uint32_t)sizeof(T), width - k0);
+  return x.op();
 }
 
 // Tokens of sequence b.
@@ -205,103 +248,78 @@ __device__ __forceinline__ void store_tile(char* m, int idx, int lane, const flo
   *reinterpret_cast<u4_t*>(m + (6 + idx) * TILE + lane * 16) = lo;
 }
 
-// A chunk's keys or queries in LDS: rows of tokens [CH][KP], or transposed [KP][CH] with rows in
-// row_of's order. Token rows hold an odd number of 16-byte pieces, so that 16 lanes reading a piece
-// of 16 rows reach all 64 banks once. So do transposed rows, but of 256, where LDS has no room left
-// for it (float32 streams): their pieces are exchanged within the row instead.
+// A chunk's keys or queries in LDS, [CH][KP] with the rows where the caller puts them. The 16-byte
+// pieces of a row are exchanged so that both readings reach all banks: a piece of 16 rows (an
+// operand whose rows are tokens), and four tokens by 16 keys (its transpose's).
 template <int KP>
 struct Tokens {
-  static constexpr int ROW = 2 * KP + 16;                      // bytes of a token's row
-  static constexpr int COL = 2 * CH + (KP == 256 ? 0 : 16);    // bytes of a transposed row
-  static constexpr int ROWS = CH * ROW;                        // bytes in all
-  static constexpr int PART = KP * COL > ROWS ? KP * COL : ROWS;
-  static __device__ __forceinline__ int row_at(int place, int byte) { return place * ROW + byte; }
-  static __device__ __forceinline__ int col_at(int place, int byte) {
-    return place * COL + (KP == 256 ? byte ^ ((place & 7) << 4) : byte);
+  static constexpr int ROW = 2 * KP, BYTES = CH * ROW;
+  static __device__ __forceinline__ int key(int place) {
+    return KP == 64 ? ((place << 1) & 4) | ((place >> 2) & 3) : ((place & 3) << 2) | ((place >> 2) & 3);
+  }
+  static __device__ __forceinline__ int at(int place, int piece) { return place * ROW + ((piece ^ key(place)) << 4); }
+  // operand tile t by k block kb, rows 16 t + n: `lane_at` is the lane's own part
+  static __device__ __forceinline__ int lane_at(int n, int g) { return at(n, g); }
+  static __device__ __forceinline__ bf8_t rows(const char* m, int lane_at, int t, int kb) {
+    return *reinterpret_cast<const bf8_t*>(m + 16 * t * ROW + (lane_at ^ (kb << 6)));
+  }
+  // the transpose's: rows are keys in row_of's order, k are tokens whose places are place_of theirs
+  static __device__ __forceinline__ int lane_at_t(int n, int g) { return at(4 * g + (n >> 2), n & 3); }
+  static __device__ __forceinline__ bf8_t cols(const char* m, int lane_at, int t, int kb) {
+    typedef short s4_t __attribute__((ext_vector_type(4)));
+    typedef short s8_t __attribute__((ext_vector_type(8)));
+    typedef __attribute__((address_space(3))) s4_t lds_s4;
+    const char* p = m + 32 * kb * ROW + (lane_at ^ ((t >> 1) << 6)) + 8 * (t & 1);
+    const s4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)p);
+    const s4_t b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(p + 16 * ROW));
+    return __builtin_bit_cast(bf8_t, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
   }
 };
 
-// Columns of a wave: NT tiles of 16, tile h's column n is NT n + h, so that a lane's are neighbours.
-template <int NT> struct Cols { float v[NT]; };
+// The wave's number in its workgroup, as a value that its lanes have in common.
+__device__ __forceinline__ int wave_number() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
 
-template <int NT, bool VEC>
-__device__ __forceinline__ Cols<NT> load_cols(const float* p, int cnt) {
-  Cols<NT> r;
-  if (VEC && NT == 2) {
-    r.v[0] = r.v[NT - 1] = 0.f;
-    if (cnt > 0) {
-      const float2 q = *reinterpret_cast<const float2*>(p);
-      r.v[0] = q.x;
-      r.v[NT - 1] = q.y;
-    }
-  } else {
-#pragma unroll
-    for (int h = 0; h < NT; ++h) r.v[h] = h < cnt ? p[h] : 0.f;
-  }
-  return r;
+// No instruction is moved across: the next step's operands are not all read ahead, for
+// which there are no registers.
+__device__ __forceinline__ void keep_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int NT, bool VEC>
-__device__ __forceinline__ Cols<NT> load_cols(const bf16_t* p, int cnt) {
-  Cols<NT> r;
-  if (VEC && NT == 2) {
-    const uint32_t q = cnt > 0 ? *reinterpret_cast<const uint32_t*>(p) : 0;
-    r.v[0] = __uint_as_float(q << 16);
-    r.v[NT - 1] = __uint_as_float(q & 0xffff0000u);
-  } else {
-#pragma unroll
-    for (int h = 0; h < NT; ++h) r.v[h] = h < cnt ? bf2f(p[h]) : 0.f;
-  }
-  return r;
-}
+// The lane's numbers anew, so that what a loop forms of them is not kept in registers over it.
+__device__ __forceinline__ void renew(int& a, int& b) { asm volatile("" : "+v"(a), "+v"(b)); }
 
-template <int NT, bool VEC>
-__device__ __forceinline__ void store_cols(float* p, int cnt, const Cols<NT>& c) {
-  if (VEC && NT == 2) {
-    if (cnt > 0) *reinterpret_cast<float2*>(p) = make_float2(c.v[0], c.v[NT - 1]);
-  } else {
-#pragma unroll
-    for (int h = 0; h < NT; ++h)
-      if (h < cnt) p[h] = c.v[h];
-  }
-}
-
-template <int NT, bool VEC>
-__device__ __forceinline__ void store_cols(bf16_t* p, int cnt, const Cols<NT>& c) {
-  if (VEC && NT == 2) {
-    if (cnt > 0) *reinterpret_cast<uint32_t*>(p) = pack_bf2_hw(c.v[0], c.v[NT - 1]);
-  } else {
-#pragma unroll
-    for (int h = 0; h < NT; ++h)
-      if (h < cnt) p[h] = (bf16_t)(pack_bf2_hw(c.v[h], 0.f) & 0xffffu);
-  }
-}
-
-// The two bfloat16 parts of a lane's columns at p and p + lo.
-template <int NT>
-__device__ __forceinline__ void store_parts(bf16_t* p, int64_t lo, const Cols<NT>& c) {
-  const uint32_t h = pack_bf2_hw(c.v[0], c.v[NT - 1]);
-  const uint32_t l = pack_bf2_hw(c.v[0] - __uint_as_float(h << 16), c.v[NT - 1] - __uint_as_float(h & 0xffff0000u));
-  if (NT == 2) {
-    *reinterpret_cast<uint32_t*>(p) = h;
-    *reinterpret_cast<uint32_t*>(p + lo) = l;
-  } else {
-    p[0] = (bf16_t)h;
-    p[lo] = (bf16_t)l;
-  }
-}
-
-// Two tokens' pieces into the transposed array: eight words of (token, token + 1).
+// A wave's 16 columns of the state: a lane has column n and, of each tile of 16 rows, four of them.
 template <int KP>
-__device__ __forceinline__ void store_transposed(char* dst, int pair, int piece, bf8_t a, bf8_t b) {
-  const u4_t e0 = __builtin_bit_cast(u4_t, a), e1 = __builtin_bit_cast(u4_t, b);
+struct State {
+  f4_t m[KP / 16];
+  // [Dk, Dv] at p, the wave's first column; NULL: zeros
+  __device__ __forceinline__ void load(const float* p, int Dk, int Dv, int n, int g, int columns) {
+    const Range m(p, p && columns > 0 ? ((int64_t)(Dk - 1) * Dv + columns) * 4 : 0);
+    const uint32_t lane = n < columns ? 4 * (8 * g * Dv + n) : NOWHERE;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t lo = e & 1 ? e0[e >> 1] >> 16 : e0[e >> 1] & 0xffffu;
-    const uint32_t hi = e & 1 ? e1[e >> 1] & 0xffff0000u : e1[e >> 1] << 16;
-    *reinterpret_cast<uint32_t*>(dst + Tokens<KP>::col_at(place_of(8 * piece + e), 4 * pair)) = lo | hi;
+    for (int t = 0; t < KP / 16; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) this->m[t][r] = m.get(p, lane + 4 * row_of(t, r) * Dv);
   }
-}
+  __device__ __forceinline__ void store(float* p, int Dk, int Dv, int n, int g, int columns) const {
+    const Range m(p, columns > 0 ? ((int64_t)(Dk - 1) * Dv + columns) * 4 : 0);
+    const uint32_t lane = n < columns ? 4 * (8 * g * Dv + n) : NOWHERE;
+#pragma unroll
+    for (int t = 0; t < KP / 16; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) m.put(p, lane + 4 * row_of(t, r) * Dv, this->m[t][r]);
+  }
+  // [KP, stride] in two parts at p, column `col` of lane 0
+  __device__ __forceinline__ void keep(bf16_t* p, int stride, int col, int n, int g) const {
+    const Range m(p, (int64_t)4 * KP * stride);
+    const uint32_t lane = col < stride ? 2 * (8 * g * stride + col + n) : NOWHERE;
+#pragma unroll
+    for (int t = 0; t < KP / 16; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) m.put_parts(lane + 2 * row_of(t, r) * stride, 2 * KP * stride, this->m[t][r]);
+  }
+};
 
 // The decay sums are float64 and their differences float32: a difference between two
 // neighbours must not carry the rounding of a long sum. Below -200 a decay is 0 in float32
@@ -316,13 +334,6 @@ __device__ __forceinline__ double running_sum(double s, int i) {
     if (i >= o) s += up;
   }
   return s;
-}
-
-template <typename T, bool VEC>
-__device__ __forceinline__ Op<Stream<T>::NP> token_op(const T* base, int64_t stride, int64_t tokens, int row, int k0,
-                                                      int Dk) {
-  const int cnt = row < tokens ? max(0, min(8, Dk - k0)) : 0;
-  return load_raw8<VEC>(base + row * stride + k0, cnt).op();
 }
 
 }  // namespace
