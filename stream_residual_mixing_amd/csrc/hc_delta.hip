@@ -19,7 +19,7 @@ namespace {
 // --------------------------------------------------------------- each chunk by itself
 
 template <typename T, int KP, bool VEC, bool BWD>
-__global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(256, 3) void delta_prep_kernel(DeltaArgs a) {
   constexpr int NP = Stream<T>::NP, KB = KP / 32, LS = CH + 4;
   __shared__ __attribute__((aligned(16))) float L[CH][LS], inv[CH][LS];
   __shared__ double G[CH];
@@ -80,7 +80,7 @@ __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
       dec[DEC_TO_END + i] = expf((float)(end - s));
       dec[DEC_BETA + i] = be;
     }
-    __syncthreads();
+    lds_barrier();
     {
       const int i = 16 * w + n;
       const double Gi = G[i];
@@ -120,7 +120,7 @@ __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
       if (w < 2) store_tile(out + REC_P, tri_t(t, 0), to, p[0]);
       store_tile(out + REC_P, tri_t(t, 1), to, p[1]);
     }
-    __syncthreads();
+    lds_barrier();
     // (I + A)^-1: wave w inverts its 16 x 16 block on the diagonal, a lane a column, ...
     {
       float x[16];
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
       for (int i = 0; i < 16; ++i)
         if ((i >> 2) == g) inv[16 * w + i][16 * w + n] = x[i];
     }
-    __syncthreads();
+    lds_barrier();
     // ... then forms the blocks below it: T_iw = -T_ii sum_m A_im T_mw, in float32 products
     {
       f4_t col[4];
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
         for (int r = 0; r < 4; ++r) inv[i0 + 4 * g + r][16 * w + n] = o[r];
       }
     }
-    __syncthreads();
+    lds_barrier();
     {
       const int i = row_of(w, n);
 #pragma unroll
@@ -176,7 +176,7 @@ __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
         }
       }
     }
-    __syncthreads();
+    lds_barrier();
   }
 }
 
@@ -231,6 +231,7 @@ __global__ __launch_bounds__(64 * NW) void delta_walk_kernel(DeltaArgs a) {
     const Range qc = head_rows((const T*)a.q + keys + c * CH * qs, left, qs, Dk);
     const Range vc = head_rows((const T*)a.v + values + c * CH * vs, have > 0 ? left : 0, vs, have);
     const Range rc(rec + c * STRIDE, USED);
+    const uint32_t vl = anew(v_lane);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int x = i * THREADS + tid, piece = x % PIECES, row = x / PIECES;
@@ -243,7 +244,7 @@ __global__ __launch_bounds__(64 * NW) void delta_walk_kernel(DeltaArgs a) {
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) vr[t][r] = vc.get((const T*)nullptr, v_lane + row_of(t, r) * vs * (uint32_t)sizeof(T));
+      for (int r = 0; r < 4; ++r) vr[t][r] = vc.get((const T*)nullptr, vl + row_of(t, r) * vs * (uint32_t)sizeof(T));
   };
   if (chunks > 0) fetch(0);
   for (int64_t c = 0; c < chunks; ++c) {
@@ -266,7 +267,7 @@ __global__ __launch_bounds__(64 * NW) void delta_walk_kernel(DeltaArgs a) {
     f4_t v[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) v[t] = f4_t{vr[t][0], vr[t][1], vr[t][2], vr[t][3]};
-    __syncthreads();
+    lds_barrier();
     if (c + 1 < chunks) fetch(c + 1);
     if (MODE == KEEP) S.keep((bf16_t*)a.states + (bh * a.NC + c) * 2 * KP * VP, VP, col, n, g);
 
@@ -307,20 +308,14 @@ __global__ __launch_bounds__(64 * NW) void delta_walk_kernel(DeltaArgs a) {
       for (int t = 2 * kb; t < 4; ++t) x[t] = mma(load_tile(lds.rec + REC_T, tri(t, kb), lane), f[kb], x[t]);
       keep_order();
     }
-    if (MODE == KEEP) {
-      const Range z((bf16_t*)a.z + (bh * a.NC + c) * 2 * CH * VP, 4 * CH * VP);
-      const uint32_t z_lane = col < VP ? 2 * (8 * g * VP + col + n) : NOWHERE;
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) z.put_parts(z_lane + 2 * row_of(t, r) * VP, 2 * CH * VP, x[t][r]);
-    }
+    if (MODE == KEEP) keep_rows((bf16_t*)a.z + (bh * a.NC + c) * 2 * CH * VP, VP, col, n, g, x);
 #pragma unroll
     for (int t = 0; t < 4; ++t) x[t] *= *reinterpret_cast<const f4_t*>(dec + DEC_BETA + row_of(t, 4 * g));
     if (MODE == OUT) {  // O = scale (exp(G) Q M + P X)
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) f[kb] = split(x[2 * kb], x[2 * kb + 1]);
       const Range oc = head_rows((T*)a.o + values + c * CH * vs, have > 0 ? (int)min((int64_t)CH, len - c * CH) : 0, vs, have);
+      const uint32_t ol = anew(o_lane);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         o[t] *= *reinterpret_cast<const f4_t*>(dec + DEC_AHEAD + 16 * t + 4 * g);
@@ -328,7 +323,7 @@ __global__ __launch_bounds__(64 * NW) void delta_walk_kernel(DeltaArgs a) {
         for (int kb = 0; kb <= (t >> 1); ++kb) o[t] = mma(load_tile(lds.rec + REC_P, tri(t, kb), lane), f[kb], o[t]);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          oc.put((T*)nullptr, o_lane + (16 * t + r) * vs * (uint32_t)sizeof(T), a.scale * o[t][r]);
+          oc.put((T*)nullptr, ol + (16 * t + r) * vs * (uint32_t)sizeof(T), a.scale * o[t][r]);
         keep_order();
       }
     }
@@ -350,7 +345,7 @@ __global__ __launch_bounds__(64 * NW) void delta_walk_kernel(DeltaArgs a) {
       }
       if (t & 1) keep_order();
     }
-    __syncthreads();
+    lds_barrier();
   }
   if (a.state1) S.store(a.state1 + bh * Dk * Dv + col, Dk, Dv, n, g, have);
 }
@@ -398,7 +393,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
     float v[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = e < have ? Elem<T>::ld((const T*)a.v + vo * a.Dv + col + e) : 0.f;
-    __syncthreads();
+    lds_barrier();
     float s[9] = {};
     float k[R];
 #pragma unroll
@@ -421,7 +416,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
     if ((tid & 63) < 8)
 #pragma unroll
       for (int x = 0; x < 9; ++x) part[t & 1][w][cl][x] = s[x];
-    __syncthreads();
+    lds_barrier();
 #pragma unroll
     for (int x = 0; x < 9; ++x)
       s[x] = (part[t & 1][0][cl][x] + part[t & 1][1][cl][x]) + (part[t & 1][2][cl][x] + part[t & 1][3][cl][x]);

@@ -62,6 +62,7 @@ __global__ __launch_bounds__(64 * NW) void delta_back_kernel(DeltaArgs a) {
     const Range qc = head_rows((const T*)a.q + keys + c * CH * qs, left, qs, Dk);
     const Range dc = head_rows((const T*)a.d_o + values + c * CH * vs, have > 0 ? left : 0, vs, have);
     const Range rc(rec + c * REC_BWD, USED);
+    const uint32_t vl = anew(v_lane);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int x = i * THREADS + tid, piece = x % PIECES, row = x / PIECES;
@@ -74,7 +75,7 @@ __global__ __launch_bounds__(64 * NW) void delta_back_kernel(DeltaArgs a) {
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) dr[t][r] = dc.get((const T*)nullptr, v_lane + row_of(t, r) * vs * (uint32_t)sizeof(T));
+      for (int r = 0; r < 4; ++r) dr[t][r] = dc.get((const T*)nullptr, vl + row_of(t, r) * vs * (uint32_t)sizeof(T));
   };
   if (chunks > 0) fetch(chunks - 1);
   for (int64_t c = chunks - 1; c >= 0; --c) {
@@ -96,7 +97,7 @@ __global__ __launch_bounds__(64 * NW) void delta_back_kernel(DeltaArgs a) {
     f4_t d[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) d[t] = f4_t{dr[t][0], dr[t][1], dr[t][2], dr[t][3]};
-    __syncthreads();
+    lds_barrier();
     if (c > 0) fetch(c - 1);
     D.keep((bf16_t*)a.dstates + (bh * a.NC + c) * 2 * KP * VP, VP, col, n, g);
 
@@ -149,15 +150,12 @@ __global__ __launch_bounds__(64 * NW) void delta_back_kernel(DeltaArgs a) {
     keep_order();
     {
       const Range vc = head_rows((T*)a.dv + values + c * CH * vs, have > 0 ? (int)min((int64_t)CH, len - c * CH) : 0, vs, have);
-      const Range wc((bf16_t*)a.w + (bh * a.NC + c) * 2 * CH * VP, 4 * CH * VP);
-      const uint32_t w_lane = col < VP ? 2 * (8 * g * VP + col + n) : NOWHERE;
+      const uint32_t vl = anew(v_lane);
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          vc.put((T*)nullptr, v_lane + row_of(t, r) * vs * (uint32_t)sizeof(T), x[t][r]);
-          wc.put_parts(w_lane + 2 * row_of(t, r) * VP, 2 * CH * VP, x[t][r]);
-        }
+        for (int r = 0; r < 4; ++r) vc.put((T*)nullptr, vl + row_of(t, r) * vs * (uint32_t)sizeof(T), x[t][r]);
+      keep_rows((bf16_t*)a.w + (bh * a.NC + c) * 2 * CH * VP, VP, col, n, g, x);
     }
     // the gradient of the state before the chunk
 #pragma unroll
@@ -189,7 +187,7 @@ __global__ __launch_bounds__(64 * NW) void delta_back_kernel(DeltaArgs a) {
       }
       keep_order();
     }
-    __syncthreads();
+    lds_barrier();
   }
   if (a.dstate0) D.store(a.dstate0 + bh * Dk * Dv + col, Dk, Dv, n, g, have);
 }
@@ -232,10 +230,11 @@ __device__ __forceinline__ float sum_groups(float v) {  // over the four lanes o
   return v + __shfl_xor(v, 32, 64);
 }
 
-// SHARED: several value heads read a key head.
+// SHARED: several value heads read a key head. Up to 128 keys at a time, for which there are
+// registers: wider heads take two passes, the second of which adds to the first's dg and dbeta.
 template <typename T, int KP, bool VEC, bool SHARED>
-__global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
-  constexpr int NP = Stream<T>::NP, KB = KP / 32, KT = KP / 16;
+__global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaArgs a) {
+  constexpr int NP = Stream<T>::NP, KB = KP / 32, KT = KP < 128 ? KP / 16 : 8, PASSES = KP / 16 / KT;
   constexpr int PIECES = KP / 8, ITEMS = CH * PIECES / 256;
   extern __shared__ __attribute__((aligned(16))) char lds_raw[];
   typedef GradLds<KP, NP> Lds;
@@ -251,225 +250,243 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
   const int per = (int)((uint32_t)a.Hv / (uint32_t)a.Hk);
   const int64_t keys = (b * a.S + t0) * qs + hk * Dk;
   const Range q = head_rows((const T*)a.q + keys, left, qs, Dk), k = head_rows((const T*)a.k + keys, left, qs, Dk);
-  const int cols_at = Tk::lane_at_t(n, g);
-
-  f4_t dqt[KT], dkt[KT];
 #pragma unroll
-  for (int t = 0; t < KT; ++t) dqt[t] = dkt[t] = f4_t{0.f, 0.f, 0.f, 0.f};
-  f4_t kk[4], qk[4];  // rows: the other token in row_of's order, by k_n
-  if (left > 0) {
+  for (int i = 0; i < ITEMS; ++i) {
+    const int x = i * 256 + tid, piece = x % PIECES, row = x / PIECES;
+    const Op<NP> ko = token_op<T, VEC>(k, qs, row, 8 * piece, Dk), qo = token_op<T, VEC>(q, qs, row, 8 * piece, Dk);
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int x = i * 256 + tid, piece = x % PIECES, row = x / PIECES;
-      const Op<NP> ko = token_op<T, VEC>(k, qs, row, 8 * piece, Dk), qo = token_op<T, VEC>(q, qs, row, 8 * piece, Dk);
-#pragma unroll
-      for (int p = 0; p < NP; ++p) {
-        const int at = Tk::at(place_of(row), piece);
-        *reinterpret_cast<bf8_t*>(lds.k[p] + at) = ko.p[p];
-        *reinterpret_cast<bf8_t*>(lds.q[p] + at) = qo.p[p];
-      }
-    }
-    __syncthreads();
-    const int rows_at = Tk::lane_at(n, g), own_at = Tk::at(place_of(16 * w + n), g);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) kk[t] = qk[t] = f4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      Op<NP> kn;
-#pragma unroll
-      for (int p = 0; p < NP; ++p) kn.p[p] = *reinterpret_cast<const bf8_t*>(lds.k[p] + (own_at ^ (kb << 6)));
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if ((t >> 1) < (w >> 1)) continue;
-        Op<NP> ka, qa;
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          ka.p[p] = Tk::rows(lds.k[p], rows_at, t, kb);
-          qa.p[p] = Tk::rows(lds.q[p], rows_at, t, kb);
-        }
-        kk[t] = mma(ka, kn, kk[t]);
-        qk[t] = mma(qa, kn, qk[t]);
-      }
-      keep_order();
+    for (int p = 0; p < NP; ++p) {
+      const int at = Tk::at(place_of(row), piece);
+      *reinterpret_cast<bf8_t*>(lds.k[p] + at) = ko.p[p];
+      *reinterpret_cast<bf8_t*>(lds.q[p] + at) = qo.p[p];
     }
   }
-  for (int hi = 0; hi < per; ++hi) {
-    renew(n, g);
-    const int tok = 16 * w + n;
-    const int64_t hv = hk * per + hi, at = (b * a.Hv + hv) * NC + chunk;
-    const int64_t gat = (b * a.S + t0) * a.Hv + hv;
-    if (left == 0) {
-      if (tid < rows) a.dg[gat + tid * a.Hv] = a.dbeta[gat + tid * a.Hv] = 0.f;
-      continue;
-    }
-    if (tid < CH) {
-      const bool on = tid < left;
-      lds.G[tid] = running_sum(on ? clamp_decay(a.g[gat + tid * a.Hv]) : 0.0, tid);
-      lds.beta[tid] = on ? a.beta[gat + tid * a.Hv] : 0.f;
-    }
-    __syncthreads();
-    const double Gn = lds.G[tok], Gend = lds.G[CH - 1];
-    const float beta_n = lds.beta[tok], ahead = expf((float)Gn), to_end = expf((float)(Gend - Gn));
+#pragma unroll 1
+  for (int pass = 0; pass < PASSES; ++pass) {
+    f4_t dqt[KT], dkt[KT];
+#pragma unroll
+    for (int t = 0; t < KT; ++t) dqt[t] = dkt[t] = f4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int hi = 0; hi < per; ++hi) {
+      renew(n, g);
+      const int tok = 16 * w + n;
+      const int64_t hv = hk * per + hi, at = (b * a.Hv + hv) * NC + chunk;
+      const int64_t gat = (b * a.S + t0) * a.Hv + hv;
+      if (left == 0) {
+        if (tid < rows) a.dg[gat + tid * a.Hv] = a.dbeta[gat + tid * a.Hv] = 0.f;
+        continue;
+      }
+      if (tid < CH) {
+        const bool on = tid < left;
+        lds.G[tid] = running_sum(on ? clamp_decay(a.g[gat + tid * a.Hv]) : 0.0, tid);
+        lds.beta[tid] = on ? a.beta[gat + tid * a.Hv] : 0.f;
+      }
+      lds_barrier();
+      const double Gn = lds.G[tok];
+      const float beta_n = lds.beta[tok];
 
-    const Range dop = head_rows((const T*)a.d_o + (b * a.S + t0) * vs + hv * Dv, left, vs, Dv);
-    const Range zp((const bf16_t*)a.z + at * 2 * CH * VP, 4 * CH * VP), wp((const bf16_t*)a.w + at * 2 * CH * VP, 4 * CH * VP);
-    const Range mp((const bf16_t*)a.states + at * 2 * KP * VP, 4 * KP * VP);
-    const Range np((const bf16_t*)a.dstates + at * 2 * KP * VP, 4 * KP * VP);
-    const uint32_t vlo = 2 * CH * VP, slo = 2 * KP * VP;
-    // rows j, lane i: Z_j . dO_i and Z_j . W_i; rows i, lane j: dO_i . Z_j and W_i . Z_j
-    f4_t zd[4], zw[4], dz[4], wz[4];
-    f4_t dq[KT], read[KT], early[KT];
-    float mn = 0.f;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) zd[t] = zw[t] = dz[t] = wz[t] = f4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int t = 0; t < KT; ++t) dq[t] = read[t] = early[t] = f4_t{0.f, 0.f, 0.f, 0.f};
-    for (int v0 = 8 * g; v0 < VP; v0 += 32) {
-      const Op<NP> dn = token_op<T, VEC>(dop, vs, tok, v0, Dv);
-      const Split zn = zp.parts(2 * (tok * VP + v0), vlo), wn = wp.parts(2 * (tok * VP + v0), vlo);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int row = row_of(t, n);
-        if ((t >> 1) <= (w >> 1)) {
-          const Split zr = zp.parts(2 * (row * VP + v0), vlo);
-          zd[t] = mma(zr, dn, zd[t]);
-          zw[t] = mma(zr, wn, zw[t]);
-        }
-        if ((t >> 1) >= (w >> 1)) {
-          dz[t] = mma(token_op<T, VEC>(dop, vs, row, v0, Dv), zn, dz[t]);
-          wz[t] = mma(wp.parts(2 * (row * VP + v0), vlo), zn, wz[t]);
-        }
-      }
-      keep_order();
-#pragma unroll
-      for (int t = 0; t < KT; ++t) {
-        const int row = row_of(t, n);
-        const Split m = mp.parts(2 * (row * VP + v0), slo), nn = np.parts(2 * (row * VP + v0), slo);
-        dq[t] = mma(m, dn, dq[t]);
-        read[t] = mma(m, wn, read[t]);
-        early[t] = mma(nn, zn, early[t]);
-        if ((t & 3) == w)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) mn += ((float)m.hi[e] + (float)m.lo[e]) * ((float)nn.hi[e] + (float)nn.lo[e]);
-        if (t & 1) keep_order();
-      }
-    }
-    // what each pair of tokens passes on
-    float db = 0.f;
-    Split bq[2], ar[2], bk[2], aw[2];  // operands: B^T and A^T (lane i), B and A (lane j)
-    {
-      float vb[2][8], va[2][8];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const f4_t beta = *reinterpret_cast<const f4_t*>(lds.beta + row_of(t, 4 * g));
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int j = row_of(t, 4 * g + r);
-          const float d = j <= tok ? beta[r] * expf((float)(Gn - lds.G[j])) : 0.f;
-          vb[t >> 1][4 * (t & 1) + r] = j <= tok ? a.scale * d * zd[t][r] : 0.f;
-          va[t >> 1][4 * (t & 1) + r] = j < tok ? -d * zw[t][r] : 0.f;
-        }
-      }
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) bq[kb] = split(vb[kb]), ar[kb] = split(va[kb]);
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = row_of(t, 4 * g + r);
-          const float d = i >= tok ? expf((float)(lds.G[i] - Gn)) : 0.f;
-          const float bz = i >= tok ? a.scale * d * dz[t][r] : 0.f, az = i > tok ? -d * wz[t][r] : 0.f;
-          db += (i >= tok ? bz * qk[t][r] : 0.f) + (i > tok ? az * kk[t][r] : 0.f);
-          vb[t >> 1][4 * (t & 1) + r] = beta_n * bz;
-          va[t >> 1][4 * (t & 1) + r] = beta_n * az;
-        }
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb) bk[kb] = split(vb[kb]), aw[kb] = split(va[kb]);
-    }
-    float dot = 0.f, at_end = 0.f;  // q . dq + k . (dk as read - as written); k . early
-    const float eb = to_end * beta_n;
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      float kf[8], qf[8];
+      const Range dop = head_rows((const T*)a.d_o + (b * a.S + t0) * vs + hv * Dv, left, vs, Dv);
+      const Range zp((const bf16_t*)a.z + at * 2 * CH * VP, 4 * CH * VP);
+      const Range wp((const bf16_t*)a.w + at * 2 * CH * VP, 4 * CH * VP);
+      const uint32_t two = 2 * VP, vlo = CH * two, slo = KP * two;
+      const int row0 = 8 * (n >> 2) + (n & 3);  // row_of(t, n) without the tile's own part
+
+      // what each pair of tokens passes on: B^T and A^T (lane i, rows j), B and A (lane j, rows i)
+      float db = 0.f;
+      Split bq[2], ar[2], bk[2], aw[2];
       {
-        const int k0 = 32 * kb + 8 * g;
-        Raw8<T> kraw, qraw;
-        kraw.template load<VEC>(k, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0);
-        qraw.template load<VEC>(q, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0);
-        kraw.open(kf);
-        qraw.open(qf);
-      }
+        // rows j, lane i: Z_j . dO_i and Z_j . W_i; rows i, lane j: dO_i . Z_j and W_i . Z_j
+        f4_t zd[4], zw[4], dz[4], wz[4];
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int t = 2 * kb + half;
-        float ke = 0.f;
+        for (int t = 0; t < 4; ++t) zd[t] = zw[t] = dz[t] = wz[t] = f4_t{0.f, 0.f, 0.f, 0.f};
+        for (int vb = 0; vb < VP; vb += 32) {
+          const int v0 = vb + 8 * g;
+          const uint32_t own = 2 * (n * VP + v0), other = 2 * (row0 * VP + v0);
+          const Op<NP> dn = token_op<T, VEC>(dop, vs, tok, v0, Dv);
+          const Split zn = zp.parts(own, 16 * w * two, vlo), wn = wp.parts(own, 16 * w * two, vlo);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) ke += kf[4 * half + r] * early[t][r];
-        db += to_end * ke;
-        at_end += eb * ke;
-        dq[t] *= a.scale * ahead;
-        read[t] *= -ahead;
-        early[t] *= eb;
-#pragma unroll
-        for (int b2 = 0; b2 < 2; ++b2) {
-          Op<NP> ka, qa;
-#pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            ka.p[p] = Tk::cols(lds.k[p], cols_at, t, b2);
-            qa.p[p] = Tk::cols(lds.q[p], cols_at, t, b2);
+          for (int t = 0; t < 4; ++t) {
+            if ((t >> 1) <= (w >> 1)) {
+              const Split zr = zp.parts(other, row_of(t, 0) * two, vlo);
+              zd[t] = mma(zr, dn, zd[t]);
+              zw[t] = mma(zr, wn, zw[t]);
+            }
+            if ((t >> 1) >= (w >> 1)) {
+              dz[t] = mma(token_op<T, VEC>(dop, vs, row0 + row_of(t, 0), v0, Dv), zn, dz[t]);
+              wz[t] = mma(wp.parts(other, row_of(t, 0) * two, vlo), zn, wz[t]);
+            }
           }
-          if (b2 <= (w >> 1)) {
-            dq[t] = mma(ka, bq[b2], dq[t]);
-            read[t] = mma(ka, ar[b2], read[t]);
-          }
-          if (b2 >= (w >> 1)) {
-            early[t] = mma(qa, bk[b2], early[t]);
-            early[t] = mma(ka, aw[b2], early[t]);
+          keep_order();
+        }
+        float vb[2][8], va[2][8];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const f4_t beta = *reinterpret_cast<const f4_t*>(lds.beta + row_of(t, 4 * g));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int j = row_of(t, 4 * g + r);
+            const float d = j <= tok ? beta[r] * expf((float)(Gn - lds.G[j])) : 0.f;
+            vb[t >> 1][4 * (t & 1) + r] = j <= tok ? a.scale * d * zd[t][r] : 0.f;
+            va[t >> 1][4 * (t & 1) + r] = j < tok ? -d * zw[t][r] : 0.f;
           }
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          dot += qf[4 * half + r] * dq[t][r] + kf[4 * half + r] * (read[t][r] - early[t][r]);
-        dqt[t] = SHARED ? dqt[t] + dq[t] : dq[t];
-        dkt[t] = SHARED ? dkt[t] + (read[t] + early[t]) : read[t] + early[t];
+        for (int kb = 0; kb < 2; ++kb) bq[kb] = split(vb[kb]), ar[kb] = split(va[kb]);
+        keep_order();
+        f4_t kk[4], qk[4];  // rows i: k_i . k_j and q_i . k_j
+#pragma unroll
+        for (int t = 0; t < 4; ++t) kk[t] = qk[t] = f4_t{0.f, 0.f, 0.f, 0.f};
+        if (pass == 0) {
+          const int rows_at = Tk::lane_at(n, g), own_at = Tk::at(place_of(tok), g);
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb) {
+            Op<NP> kn;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) kn.p[p] = *reinterpret_cast<const bf8_t*>(lds.k[p] + (own_at ^ (kb << 6)));
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              if ((t >> 1) < (w >> 1)) continue;
+              Op<NP> ka, qa;
+#pragma unroll
+              for (int p = 0; p < NP; ++p) {
+                ka.p[p] = Tk::rows(lds.k[p], rows_at, t, kb);
+                qa.p[p] = Tk::rows(lds.q[p], rows_at, t, kb);
+              }
+              kk[t] = mma(ka, kn, kk[t]);
+              qk[t] = mma(qa, kn, qk[t]);
+            }
+            keep_order();
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int i = row_of(t, 4 * g + r);
+            const float d = i >= tok ? expf((float)(lds.G[i] - Gn)) : 0.f;
+            const float bz = i >= tok ? a.scale * d * dz[t][r] : 0.f, az = i > tok ? -d * wz[t][r] : 0.f;
+            db += (i >= tok ? bz * qk[t][r] : 0.f) + (i > tok ? az * kk[t][r] : 0.f);
+            vb[t >> 1][4 * (t & 1) + r] = beta_n * bz;
+            va[t >> 1][4 * (t & 1) + r] = beta_n * az;
+          }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) bk[kb] = split(vb[kb]), aw[kb] = split(va[kb]);
         keep_order();
       }
-    }
-    dot = sum_groups(dot);
-    db = sum_groups(db);
-    // <M, N> and the ends' sum over the chunk
-    const float ends = wave_sum(at_end + expf((float)Gend) * mn);
-    if (g == 0) {
-      lds.dG[tok] = dot;
-      if (tok < rows) a.dbeta[gat + tok * a.Hv] = tok < left ? db : 0.f;
-    }
-    if (lane == 0) lds.end[w] = ends;
-    __syncthreads();
-    if (tid < CH) {
-      float s = lds.dG[tid];
+      // what the states pass on
+      f4_t dq[KT], read[KT], early[KT];
+      float mn = 0.f;
+      const Range mp((const bf16_t*)a.states + at * 2 * KP * VP, 4 * KP * VP);
+      const Range np((const bf16_t*)a.dstates + at * 2 * KP * VP, 4 * KP * VP);
 #pragma unroll
-      for (int o = 1; o < CH; o <<= 1) {
-        const float down = __shfl_down(s, o, 64);
-        if (tid + o < CH) s += down;
+      for (int t = 0; t < KT; ++t) dq[t] = read[t] = early[t] = f4_t{0.f, 0.f, 0.f, 0.f};
+      for (int vb = 0; vb < VP; vb += 32) {
+        const int v0 = vb + 8 * g;
+        const uint32_t own = 2 * (n * VP + v0), other = 2 * (row0 * VP + v0);
+        const Op<NP> dn = token_op<T, VEC>(dop, vs, tok, v0, Dv);
+        const Split zn = zp.parts(own, 16 * w * two, vlo), wn = wp.parts(own, 16 * w * two, vlo);
+#pragma unroll
+        for (int t = 0; t < KT; ++t) {
+          const uint32_t tile = (row_of(t, 0) + 16 * KT * pass) * two;
+          const Split m = mp.parts(other, tile, slo), nn = np.parts(other, tile, slo);
+          dq[t] = mma(m, dn, dq[t]);
+          read[t] = mma(m, wn, read[t]);
+          early[t] = mma(nn, zn, early[t]);
+          if ((t & 3) == w)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mn += ((float)m.hi[e] + (float)m.lo[e]) * ((float)nn.hi[e] + (float)nn.lo[e]);
+          if ((t & 1) == 1) keep_order();
+        }
       }
-      s += (lds.end[0] + lds.end[1]) + (lds.end[2] + lds.end[3]);
-      if (tid < rows) a.dg[gat + tid * a.Hv] = tid < left ? s : 0.f;
-    }
-    __syncthreads();
-  }
-  const int tok = 16 * w + n;
-  const Range dqp = head_rows((T*)a.dq + keys, rows, qs, Dk), dkp = head_rows((T*)a.dk + keys, rows, qs, Dk);
+      const double Gend = lds.G[CH - 1];
+      const float ahead = expf((float)Gn), to_end = expf((float)(Gend - Gn)), eb = to_end * beta_n;
+      const int cols_at = Tk::lane_at_t(n, g) ^ (pass << 8);
+      float dot = 0.f, at_end = 0.f;  // q . dq + k . (dk as read - as written); k . early
 #pragma unroll
-  for (int kb = 0; kb < KB; ++kb) {
-    const int k0 = 32 * kb + 8 * g;
-    float vq[8], vk[8];
+      for (int t2 = 0; t2 < KT / 2; ++t2) {
+        float kf[8], qf[8];
+        {
+          const int k0 = 32 * t2 + 16 * KT * pass + 8 * g;
+          Raw8<T> kraw, qraw;
+          kraw.template load<VEC>(k, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0);
+          qraw.template load<VEC>(q, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0);
+          kraw.open(kf);
+          qraw.open(qf);
+        }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      vq[e] = tok < left ? dqt[2 * kb + (e >> 2)][e & 3] : 0.f;
-      vk[e] = tok < left ? dkt[2 * kb + (e >> 2)][e & 3] : 0.f;
+        for (int half = 0; half < 2; ++half) {
+          const int t = 2 * t2 + half;
+          float ke = 0.f;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) ke += kf[4 * half + r] * early[t][r];
+          db += to_end * ke;
+          at_end += eb * ke;
+          dq[t] *= a.scale * ahead;
+          read[t] *= -ahead;
+          early[t] *= eb;
+#pragma unroll
+          for (int b2 = 0; b2 < 2; ++b2) {
+            Op<NP> ka, qa;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+              ka.p[p] = Tk::cols(lds.k[p], cols_at, t, b2);
+              qa.p[p] = Tk::cols(lds.q[p], cols_at, t, b2);
+            }
+            if (b2 <= (w >> 1)) {
+              dq[t] = mma(ka, bq[b2], dq[t]);
+              read[t] = mma(ka, ar[b2], read[t]);
+            }
+            if (b2 >= (w >> 1)) {
+              early[t] = mma(qa, bk[b2], early[t]);
+              early[t] = mma(ka, aw[b2], early[t]);
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            dot += qf[4 * half + r] * dq[t][r] + kf[4 * half + r] * (read[t][r] - early[t][r]);
+          dqt[t] = SHARED ? dqt[t] + dq[t] : dq[t];
+          dkt[t] = SHARED ? dkt[t] + (read[t] + early[t]) : read[t] + early[t];
+        }
+        keep_order();
+      }
+      dot = sum_groups(dot);
+      db = sum_groups(db);
+      // <M, N> and the ends' sum over the chunk
+      const float ends = wave_sum(at_end + expf((float)Gend) * mn);
+      if (g == 0) {
+        lds.dG[tok] = dot;
+        float* p = a.dbeta + gat + tok * a.Hv;
+        if (tok < rows) *p = tok < left ? (pass ? *p + db : db) : 0.f;
+      }
+      if (lane == 0) lds.end[w] = ends;
+      lds_barrier();
+      if (tid < CH) {
+        float s = lds.dG[tid];
+#pragma unroll
+        for (int o = 1; o < CH; o <<= 1) {
+          const float down = __shfl_down(s, o, 64);
+          if (tid + o < CH) s += down;
+        }
+        s += (lds.end[0] + lds.end[1]) + (lds.end[2] + lds.end[3]);
+        float* p = a.dg + gat + tid * a.Hv;
+        if (tid < rows) *p = tid < left ? (pass ? *p + s : s) : 0.f;
+      }
+      lds_barrier();
     }
-    put_row8<VEC>((T*)nullptr, dqp, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0, vq);
-    put_row8<VEC>((T*)nullptr, dkp, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0, vk);
+    const int tok = 16 * w + n;
+    const Range dqp = head_rows((T*)a.dq + keys, rows, qs, Dk), dkp = head_rows((T*)a.dk + keys, rows, qs, Dk);
+#pragma unroll
+    for (int t2 = 0; t2 < KT / 2; ++t2) {
+      const int k0 = 32 * t2 + 16 * KT * pass + 8 * g;
+      float vq[8], vk[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        vq[e] = tok < left ? dqt[2 * t2 + (e >> 2)][e & 3] : 0.f;
+        vk[e] = tok < left ? dkt[2 * t2 + (e >> 2)][e & 3] : 0.f;
+      }
+      put_row8<VEC>((T*)nullptr, dqp, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0, vq);
+      put_row8<VEC>((T*)nullptr, dkp, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0, vk);
+    }
   }
 }
 

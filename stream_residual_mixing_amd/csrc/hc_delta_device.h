@@ -140,14 +140,16 @@ struct Range {
   __device__ __forceinline__ void put_quad(uint32_t o, u4_t v) const {
     __builtin_amdgcn_raw_buffer_store_b128(v, r, o, 0, 0);
   }
-  // the two bfloat16 parts of v, the low one `lo` bytes behind the high one
-  __device__ __forceinline__ void put_parts(uint32_t o, uint32_t lo, float v) const {
+  // the two bfloat16 parts of v, the low one in its own array
+  __device__ __forceinline__ void put_parts(const Range& low, uint32_t o, float v) const {
     const uint32_t h = pack_bf2_hw(v, 0.f);
     __builtin_amdgcn_raw_buffer_store_b16((uint16_t)h, r, o, 0, 0);
-    put((bf16_t*)nullptr, o + lo, v - __uint_as_float(h << 16));
+    low.put((bf16_t*)nullptr, o, v - __uint_as_float(h << 16));
   }
-  __device__ __forceinline__ Split parts(uint32_t o, uint32_t lo) const {
-    return {__builtin_bit_cast(bf8_t, quad(o)), __builtin_bit_cast(bf8_t, quad(o + lo))};
+  // a kept array's operand, at an offset `s` more that the lanes have in common; inside it
+  __device__ __forceinline__ Split parts(uint32_t o, uint32_t s, uint32_t lo) const {
+    return {__builtin_bit_cast(bf8_t, __builtin_amdgcn_raw_buffer_load_b128(r, o, s, 0)),
+            __builtin_bit_cast(bf8_t, __builtin_amdgcn_raw_buffer_load_b128(r, o, s + lo, 0))};
   }
 };
 
@@ -288,6 +290,10 @@ __device__ __forceinline__ void keep_order() {
 
 // The lane's numbers anew, so that what a loop forms of them is not kept in registers over it.
 __device__ __forceinline__ void renew(int& a, int& b) { asm volatile("" : "+v"(a), "+v"(b)); }
+__device__ __forceinline__ uint32_t anew(uint32_t a) {
+  asm volatile("" : "+v"(a));
+  return a;
+}
 
 // A wave's 16 columns of the state: a lane has column n and, of each tile of 16 rows, four of them.
 template <int KP>
@@ -312,14 +318,25 @@ struct State {
   }
   // [KP, stride] in two parts at p, column `col` of lane 0
   __device__ __forceinline__ void keep(bf16_t* p, int stride, int col, int n, int g) const {
-    const Range m(p, (int64_t)4 * KP * stride);
-    const uint32_t lane = col < stride ? 2 * (8 * g * stride + col + n) : NOWHERE;
+    const Range hi(p, 2 * KP * stride), lo(p + KP * stride, 2 * KP * stride);
+    const uint32_t lane = anew(col < stride ? 2 * (8 * g * stride + col + n) : NOWHERE);
 #pragma unroll
-    for (int t = 0; t < KP / 16; ++t)
+    for (int t = 0; t < KP / 16; ++t) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) m.put_parts(lane + 2 * row_of(t, r) * stride, 2 * KP * stride, this->m[t][r]);
+      for (int r = 0; r < 4; ++r) hi.put_parts(lo, lane + 2 * row_of(t, r) * stride, m[t][r]);
+    }
   }
 };
+
+// Four tiles of a chunk's 64 rows, as [CH, stride] in two parts.
+__device__ __forceinline__ void keep_rows(bf16_t* p, int stride, int col, int n, int g, const f4_t (&x)[4]) {
+  const Range hi(p, 2 * CH * stride), lo(p + CH * stride, 2 * CH * stride);
+  const uint32_t lane = anew(col < stride ? 2 * (8 * g * stride + col + n) : NOWHERE);
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) hi.put_parts(lo, lane + 2 * row_of(t, r) * stride, x[t][r]);
+}
 
 // The decay sums are float64 and their differences float32: a difference between two
 // neighbours must not carry the rounding of a long sum. Below -200 a decay is 0 in float32
