@@ -1658,23 +1658,16 @@ static int check_delta_shape(int dtype, int64_t B, int64_t S, int64_t Hk, int64_
   return HC_OK;
 }
 
+static int64_t delta_ws(int64_t B, int64_t S, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv, bool backward) {
+  hc::DeltaArgs a{};
+  a.B = B, a.S = S, a.Hk = Hk, a.Hv = Hv, a.Dk = Dk, a.Dv = Dv;
+  return hc::delta_plan(a, backward, nullptr);
+}
+
 int64_t hc_gated_delta_workspace_bytes(int64_t B, int64_t S, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
                                        int dtype) {
   if (check_delta_shape(dtype, B, S, Hk, Hv, Dk, Dv) != HC_OK) return -1;
-  return hc::delta_ws_bytes(B, S, Hv);
-}
-
-// rows in whole pieces of 8 keys, two columns (of a state, four where there are whole fours) at once
-static bool delta_vec(int dtype, int64_t Dk, int64_t Dv, std::initializer_list<const void*> keys,
-                      std::initializer_list<const void*> values, std::initializer_list<const void*> states) {
-  if (Dk % 8 != 0 || Dv % 2 != 0) return false;
-  for (const void* p : keys)
-    if (p && !aligned_to(p, 16)) return false;
-  for (const void* p : values)
-    if (p && !aligned_to(p, 2 * esize(dtype))) return false;
-  for (const void* p : states)
-    if (p && !aligned_to(p, Dv % 4 == 0 ? 16 : 8)) return false;
-  return true;
+  return delta_ws(B, S, Hk, Hv, Dk, Dv, false);
 }
 
 int hc_gated_delta(const void* q, const void* k, const void* v, int dtype, int64_t B, int64_t S, int64_t Hk,
@@ -1684,7 +1677,7 @@ int hc_gated_delta(const void* q, const void* k, const void* v, int dtype, int64
   int r = check_delta_shape(dtype, B, S, Hk, Hv, Dk, Dv);
   if (r != HC_OK || B == 0 || (S == 0 && !state)) return r;
   const int64_t e = (int64_t)esize(dtype), kb = B * S * Hk * Dk * e, vb = B * S * Hv * Dv * e, gb = B * S * Hv * 4;
-  const int64_t sb = B * Hv * Dk * Dv * 4, wsb = hc::delta_ws_bytes(B, S, Hv);
+  const int64_t sb = B * Hv * Dk * Dv * 4, wsb = delta_ws(B, S, Hk, Hv, Dk, Dv, false);
   const uintptr_t ea = (uintptr_t)e;
   const Buf bq{q, kb, ea, S > 0}, bk{k, kb, ea, S > 0}, bv{v, vb, ea, S > 0}, bg{g, gb, 4, S > 0},
       bb{beta, gb, 4, S > 0}, b0{state0, sb, 4, false}, bl{lengths, B * 4, 4, false}, bo{o, vb, ea, S > 0},
@@ -1695,18 +1688,17 @@ int hc_gated_delta(const void* q, const void* k, const void* v, int dtype, int64
       (state != state0 && overlaps(state, sb, state0, sb)))
     return HC_ERR_ALIAS;
   if ((r = device_status()) != HC_OK) return r;
-  const hc::DeltaArgs a{q,     k,         v, g, beta, state0, lengths, o,
-                        state, workspace, B, S, Hk,   Hv,     Dk,      Dv, (S + 63) / 64, scale,
-                        delta_vec(dtype, Dk, Dv, {q, k}, {v, o}, {state0, state})};
+  hc::DeltaArgs a{q, k, v, g, beta, state0, lengths, o, state, B, S, Hk, Hv, Dk, Dv, scale};
+  a.vec = Dk % 8 == 0 && aligned_to(q, 16) && aligned_to(k, 16);
+  a.vec4 = Dv % 4 == 0 && aligned_to(state0, 16) && aligned_to(state, 16);
+  hc::delta_plan(a, false, workspace);
   return launch_status(hc::launch_delta(dtype, a, (hipStream_t)stream));
 }
 
 int64_t hc_gated_delta_backward_workspace_bytes(int64_t B, int64_t S, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
                                                 int dtype) {
   if (check_delta_shape(dtype, B, S, Hk, Hv, Dk, Dv) != HC_OK) return -1;
-  hc::DeltaArgs a{};
-  a.B = B, a.Hv = Hv, a.Dk = Dk, a.Dv = Dv, a.NC = (S + 63) / 64;
-  return hc::delta_backward_ws(a, nullptr);
+  return delta_ws(B, S, Hk, Hv, Dk, Dv, true);
 }
 
 int hc_gated_delta_backward(const void* q, const void* k, const void* v, const void* d_o, int dtype, int64_t B,
@@ -1729,12 +1721,11 @@ int hc_gated_delta_backward(const void* q, const void* k, const void* v, const v
   if ((r = check_ws(workspace, workspace_bytes, wsb)) != HC_OK) return r;
   if (bufs_overlap({oq, ok, ov, og, ob, o0, bw}, {iq, ik, iv, id, ig, ib, i0, i1, il})) return HC_ERR_ALIAS;
   if ((r = device_status()) != HC_OK) return r;
-  hc::DeltaArgs a{q,       k,       v, g, beta, state0, lengths, nullptr,
-                  nullptr, nullptr, B, S, Hk,   Hv,     Dk,      Dv, (S + 63) / 64, scale,
-                  delta_vec(dtype, Dk, Dv, {q, k, dq, dk}, {v, d_o, dv}, {state0, dstate, dstate0})};
-  hc::delta_backward_ws(a, workspace);
-  a.d_o = d_o, a.dlast = dstate, a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.dstate0 = dstate0;
+  hc::DeltaArgs a{q, k, v, g, beta, state0, lengths, nullptr, nullptr, B, S, Hk, Hv, Dk, Dv, scale};
+  a.vec = Dk % 8 == 0 && aligned_to(q, 16) && aligned_to(k, 16) && aligned_to(dq, 16) && aligned_to(dk, 16);
   a.vec8 = a.vec && Dv % 8 == 0 && aligned_to(d_o, 16);
+  a.d_o = d_o, a.dlast = dstate, a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.dstate0 = dstate0;
+  hc::delta_plan(a, true, workspace);
   return launch_status(hc::launch_delta_backward(dtype, a, (hipStream_t)stream));
 }
 

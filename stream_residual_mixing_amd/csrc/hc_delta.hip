@@ -182,7 +182,7 @@ __global__ __launch_bounds__(256, 3) void delta_prep_kernel(DeltaArgs a) {
 
 // --------------------------------------------------------------------- the walk
 
-constexpr int OUT = 0, KEEP = 1;
+constexpr int OUT = 0, KEEP = 1, SUM = 2, SUM_BWD = 3;
 
 template <int KP, int NP, int NW, int MODE>
 struct WalkLds {
@@ -192,13 +192,15 @@ struct WalkLds {
   char rec[((MODE == OUT ? REC : REC_P) + PASS - 1) / PASS * PASS];
 };
 
-// NW waves of 16 columns. OUT: the forward's. KEEP: the backward's, which wants every chunk's first
-// state and Z rather than O.
+// NW waves of 16 columns over a segment's chunks. OUT: the forward's. KEEP: the backward's, which wants
+// every chunk's first state and Z rather than O. SUM: a segment's last state from zeros (the first
+// segment's from its own) and, as further columns that start as the unit matrix without values, its
+// map of the state; SUM_BWD: the map's transpose too.
 template <typename T, int KP, int NW, bool VEC, int MODE>
-__global__ __launch_bounds__(64 * NW) void delta_walk_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(64 * NW, 2) void delta_walk_kernel(DeltaArgs a) {
   constexpr int NP = Stream<T>::NP, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
   constexpr int PIECES = KP / 8, ITEMS = (CH * PIECES + THREADS - 1) / THREADS;
-  constexpr int STRIDE = MODE == KEEP ? REC_BWD : REC, USED = MODE == OUT ? REC : REC_P;
+  constexpr int STRIDE = MODE == KEEP || MODE == SUM_BWD ? REC_BWD : REC, USED = MODE == OUT ? REC : REC_P;
   constexpr int RR = (USED + 16 * THREADS - 1) / (16 * THREADS);
   extern __shared__ __attribute__((aligned(16))) char lds_raw[];
   typedef WalkLds<KP, NP, NW, MODE> Lds;
@@ -207,19 +209,30 @@ __global__ __launch_bounds__(64 * NW) void delta_walk_kernel(DeltaArgs a) {
   Lds& lds = *reinterpret_cast<Lds*>(lds_raw);
   const int tid = threadIdx.x, lane = tid & 63, w = wave_number(), n = lane & 15, g = lane >> 4;
   const int rows_at = Tk::lane_at(n, g), cols_at = Tk::lane_at_t(n, g);
-  const uint32_t groups = ((uint32_t)a.Dv + 16 * NW - 1) / (16 * NW);
-  const int64_t bh = blockIdx.x / groups, b = (uint32_t)bh / (uint32_t)a.Hv;
-  const uint32_t hv = (uint32_t)bh % (uint32_t)a.Hv, hk = hv / ((uint32_t)a.Hv / (uint32_t)a.Hk);
   const int Dk = (int)a.Dk, Dv = (int)a.Dv, VP = (int)a.VP, qs = (int)a.Hk * Dk, vs = (int)a.Hv * Dv;
-  const int col = (int)(blockIdx.x % groups) * 16 * NW + 16 * w, have = min(16, Dv - col);  // columns; may be none
-  const int64_t len = length_of(a.lengths, b, a.S), chunks = (len + CH - 1) / CH;
-  const int64_t keys = b * a.S * qs + hk * Dk, values = b * a.S * vs + hv * Dv + col;
+  const uint32_t v_groups = (Dv + 16 * NW - 1) / (16 * NW);
+  const Part part(a, v_groups + (MODE >= SUM ? KP / (16 * NW) : 0));
+  const bool unit = MODE >= SUM && part.group >= (int)v_groups;
+  if (part.empty() || (MODE >= SUM && (part.ends() || (unit && part.seg == 0)))) return;
+  const int64_t bh = part.bh, len = part.len;
+  const int col = (part.group - (unit ? (int)v_groups : 0)) * 16 * NW + 16 * w;
+  const int have = unit ? 0 : min(16, Dv - col);  // columns of values; may be none
+  const int64_t keys = part.b * a.S * qs + part.hk * Dk, values = part.b * a.S * vs + part.hv * Dv + col;
   const char* rec = (const char*)a.rec + bh * a.NC * STRIDE;
   const uint32_t v_lane = n < have ? (8 * g * vs + n) * (uint32_t)sizeof(T) : NOWHERE;
   const uint32_t o_lane = n < have ? (4 * g * vs + n) * (uint32_t)sizeof(T) : NOWHERE;
 
   State<KP> S;
-  S.load(a.state0 ? a.state0 + bh * Dk * Dv + col : nullptr, Dk, Dv, n, g, have);
+  if (unit) {
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) S.m[t][r] = row_of(t, 4 * g + r) == col + n ? 1.f : 0.f;
+  } else {
+    const float* from = part.seg == 0 ? a.state0 + (a.state0 ? bh * Dk * Dv : 0)
+                        : MODE >= SUM ? nullptr : a.slots + (part.slot - 1) * Dk * Dv;
+    S.load(from ? from + col : nullptr, Dk, Dv, n, g, have);
+  }
 
   // the next chunk's operands on their way
   Raw8<T> kr[ITEMS], qr[ITEMS];
@@ -246,8 +259,8 @@ __global__ __launch_bounds__(64 * NW) void delta_walk_kernel(DeltaArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) vr[t][r] = vc.get((const T*)nullptr, vl + row_of(t, r) * vs * (uint32_t)sizeof(T));
   };
-  if (chunks > 0) fetch(0);
-  for (int64_t c = 0; c < chunks; ++c) {
+  if (part.first < part.last) fetch(part.first);
+  for (int64_t c = part.first; c < part.last; ++c) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int x = i * THREADS + tid, piece = x % PIECES, row = x / PIECES;
@@ -268,7 +281,7 @@ __global__ __launch_bounds__(64 * NW) void delta_walk_kernel(DeltaArgs a) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) v[t] = f4_t{vr[t][0], vr[t][1], vr[t][2], vr[t][3]};
     lds_barrier();
-    if (c + 1 < chunks) fetch(c + 1);
+    if (c + 1 < part.last) fetch(c + 1);
     if (MODE == KEEP) S.keep((bf16_t*)a.states + (bh * a.NC + c) * 2 * KP * VP, VP, col, n, g);
 
     // K M and Q M
@@ -347,7 +360,24 @@ __global__ __launch_bounds__(64 * NW) void delta_walk_kernel(DeltaArgs a) {
     }
     lds_barrier();
   }
-  if (a.state1) S.store(a.state1 + bh * Dk * Dv + col, Dk, Dv, n, g, have);
+  if (MODE == OUT && a.state1 && part.ends()) S.store(a.state1 + bh * Dk * Dv + col, Dk, Dv, n, g, have);
+  if (MODE >= SUM) {
+    if (!unit) {
+      S.store(a.slots + part.slot * Dk * Dv + col, Dk, Dv, n, g, have);
+      return;
+    }
+    S.keep((bf16_t*)a.phi + part.slot * 2 * KP * KP, KP, col, n, g);
+    if (MODE == SUM_BWD) {
+      const Range m((bf16_t*)a.phi_t + part.slot * 2 * KP * KP, 4 * KP * KP);
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        const Split s = split(S.m[2 * kb], S.m[2 * kb + 1]);
+        const uint32_t o = 2 * ((col + n) * KP + 32 * kb + 8 * g);
+        m.put_quad(o, __builtin_bit_cast(u4_t, s.hi));
+        m.put_quad(o + 2 * KP * KP, __builtin_bit_cast(u4_t, s.lo));
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------- token by token
@@ -450,37 +480,78 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
   }
 }
 
+// ----------------------------------------------------------------- the segments
+
+// M_{s+1} = Phi_s M_s + N_s over a head's segments, 16 columns of the state by a wave; the slots' N
+// become the states. BACK: the gradients, from the last segment on, with Phi's transpose.
+template <int KP, bool BACK>
+__global__ __launch_bounds__(64) void delta_join_kernel(DeltaArgs a) {
+  constexpr int KB = KP / 32, KT = KP / 16;
+  const int lane = threadIdx.x, n = lane & 15, g = lane >> 4;
+  const int Dk = (int)a.Dk, Dv = (int)a.Dv;
+  const uint32_t groups = ((uint32_t)Dv + 15) / 16;
+  const int64_t bh = blockIdx.x / groups, b = (uint32_t)bh / (uint32_t)a.Hv;
+  const int col = (int)(blockIdx.x % groups) * 16, have = min(16, Dv - col);
+  const int64_t chunks = (length_of(a.lengths, b, a.S) + CH - 1) / CH;
+  const int segs = (int)((chunks + a.SL - 1) / a.SL);  // that hold tokens
+  float* slots = a.slots + bh * a.NS * Dk * Dv + col;
+  const bf16_t* maps = (const bf16_t*)(BACK ? a.phi_t : a.phi) + bh * a.NS * 2 * KP * KP;
+  if (segs < 3) return;  // the second segment's state is the first's last one
+  State<KP> S;
+  S.load(slots + (BACK ? segs - 1 : 0) * (int64_t)Dk * Dv, Dk, Dv, n, g, have);
+  for (int i = 1; i < segs - 1; ++i) {
+    const int s = BACK ? segs - 1 - i : i;
+    const Range m(maps + s * (int64_t)2 * KP * KP, 4 * KP * KP);
+    const uint32_t at = 2 * ((8 * (n >> 2) + (n & 3)) * KP + 8 * g);
+    Split f[KB];
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) f[kb] = split(S.m[2 * kb], S.m[2 * kb + 1]);
+    S.load(slots + s * (int64_t)Dk * Dv, Dk, Dv, n, g, have);
+#pragma unroll
+    for (int t = 0; t < KT; ++t)
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+        S.m[t] = mma(m.parts(at, 2 * (row_of(t, 0) * KP + 32 * kb), 2 * KP * KP), f[kb], S.m[t]);
+    S.store(slots + s * (int64_t)Dk * Dv, Dk, Dv, n, g, have);
+  }
+}
+
 constexpr int SHORT = 8;  // tokens up to which they are taken one by one
 
-template <typename T, int KP, int NW, int MODE>
+template <typename T, int KP, int MODE>
 hipError_t walk_go(const DeltaArgs& a, hipStream_t st) {
+  constexpr int NW = 4;
   const size_t lds = sizeof(WalkLds<KP, Stream<T>::NP, NW, MODE>);
-  const dim3 prep((unsigned)(a.B * a.Hk * a.NC)), walk((unsigned)(a.B * a.Hv * ((a.Dv + 16 * NW - 1) / (16 * NW))));
-  const auto go = [&](auto prep_k, auto walk_k) {
+  const unsigned groups = (unsigned)((a.Dv + 16 * NW - 1) / (16 * NW)) + (MODE >= SUM ? KP / (16 * NW) : 0);
+  const dim3 grid((unsigned)(a.B * a.Hv * a.NS) * groups);
+  const auto go = [&](auto kernel) {
     if (lds > 64 * 1024) {
-      hipError_t e = hipFuncSetAttribute((const void*)walk_k, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+      hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
       if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(prep_k, prep, dim3(256), 0, st, a);
-    hipLaunchKernelGGL(walk_k, walk, dim3(64 * NW), lds, st, a);
+    hipLaunchKernelGGL(kernel, grid, dim3(64 * NW), lds, st, a);
     return hipGetLastError();
   };
-  if (a.vec) return go(delta_prep_kernel<T, KP, true, MODE == KEEP>, delta_walk_kernel<T, KP, NW, true, MODE>);
-  return go(delta_prep_kernel<T, KP, false, MODE == KEEP>, delta_walk_kernel<T, KP, NW, false, MODE>);
+  return a.vec ? go(delta_walk_kernel<T, KP, NW, true, MODE>) : go(delta_walk_kernel<T, KP, NW, false, MODE>);
 }
 
 template <typename T, int KP, int MODE>
 hipError_t delta_go(const DeltaArgs& a, hipStream_t st) {
   if (MODE == OUT && a.S <= SHORT) {
     const dim3 grid((unsigned)(a.B * a.Hv * ((a.Dv + 31) / 32)));
-    if (a.vec && a.Dv % 4 == 0) hipLaunchKernelGGL((delta_step_kernel<T, KP, true>), grid, dim3(256), 0, st, a);
+    if (a.vec4) hipLaunchKernelGGL((delta_step_kernel<T, KP, true>), grid, dim3(256), 0, st, a);
     else hipLaunchKernelGGL((delta_step_kernel<T, KP, false>), grid, dim3(256), 0, st, a);
     return hipGetLastError();
   }
-  if constexpr (KP < 256) {  // wider states leave no registers for eight waves
-    if (a.Dv > 64) return walk_go<T, KP, 8, MODE>(a, st);
+  const dim3 prep((unsigned)(a.B * a.Hk * a.NC));
+  if (a.vec) hipLaunchKernelGGL((delta_prep_kernel<T, KP, true, MODE == KEEP>), prep, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((delta_prep_kernel<T, KP, false, MODE == KEEP>), prep, dim3(256), 0, st, a);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && a.NS > 1) {
+    e = walk_go<T, KP, MODE == KEEP ? SUM_BWD : SUM>(a, st);
+    if (e == hipSuccess) e = launch_delta_join(false, a, st);
   }
-  return walk_go<T, KP, 4, MODE>(a, st);
+  return e == hipSuccess ? walk_go<T, KP, MODE>(a, st) : e;
 }
 
 template <typename T, int MODE>
@@ -490,10 +561,49 @@ hipError_t delta_by_width(const DeltaArgs& a, hipStream_t st) {
   return delta_go<T, 256, MODE>(a, st);
 }
 
+template <bool BACK>
+void join_go(const DeltaArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)(a.B * a.Hv * ((a.Dv + 15) / 16)));
+  if (a.Dk <= 64) hipLaunchKernelGGL((delta_join_kernel<64, BACK>), grid, dim3(64), 0, st, a);
+  else if (a.Dk <= 128) hipLaunchKernelGGL((delta_join_kernel<128, BACK>), grid, dim3(64), 0, st, a);
+  else hipLaunchKernelGGL((delta_join_kernel<256, BACK>), grid, dim3(64), 0, st, a);
+}
+
 }  // namespace
 
-int64_t delta_ws_bytes(int64_t B, int64_t S, int64_t Hv) {
-  return S <= SHORT ? 0 : B * Hv * ((S + CH - 1) / CH) * (int64_t)REC;
+int64_t delta_plan(DeltaArgs& a, bool backward, void* ws) {
+  const int64_t KP = a.Dk <= 64 ? 64 : a.Dk <= 128 ? 128 : 256, heads = a.B * a.Hv;
+  a.NC = (a.S + CH - 1) / CH;
+  a.VP = (a.Dv + 31) / 32 * 32;
+  a.NS = 1;
+  a.SL = a.NC;
+  const int64_t wide = heads * ((a.Dv + 63) / 64);  // workgroups that walk whole sequences
+  if (wide > 0 && 512 / wide >= 4 && a.NC >= 16) {
+    const int64_t most = 512 / wide < a.NC / 4 ? 512 / wide : a.NC / 4;
+    a.SL = (a.NC + most - 1) / most;
+    a.NS = (a.NC + a.SL - 1) / a.SL;
+  }
+  if (!backward && a.S <= SHORT) return 0;
+  int64_t at = 0;
+  const auto take = [&](int64_t bytes) {
+    char* p = (char*)ws + at;
+    at += (bytes + 255) / 256 * 256;
+    return (void*)p;
+  };
+  a.rec = take(heads * a.NC * (backward ? REC_BWD : REC));
+  if (a.NS > 1) {
+    a.slots = (float*)take(heads * a.NS * a.Dk * a.Dv * 4);
+    a.phi = take(heads * a.NS * 4 * KP * KP);
+    if (backward) a.phi_t = take(heads * a.NS * 4 * KP * KP);
+  }
+  if (backward) {
+    const int64_t n = heads * a.NC;
+    a.states = take(n * 4 * KP * a.VP);
+    a.dstates = take(n * 4 * KP * a.VP);
+    a.z = take(n * 4 * CH * a.VP);
+    a.w = take(n * 4 * CH * a.VP);
+  }
+  return at;
 }
 
 hipError_t launch_delta(int dtype, const DeltaArgs& a, hipStream_t st) {
@@ -502,6 +612,12 @@ hipError_t launch_delta(int dtype, const DeltaArgs& a, hipStream_t st) {
 
 hipError_t launch_delta_keep(int dtype, const DeltaArgs& a, hipStream_t st) {
   return dtype == 0 ? delta_by_width<float, KEEP>(a, st) : delta_by_width<bf16_t, KEEP>(a, st);
+}
+
+hipError_t launch_delta_join(bool back, const DeltaArgs& a, hipStream_t st) {
+  if (back) join_go<true>(a, st);
+  else join_go<false>(a, st);
+  return hipGetLastError();
 }
 
 }  // namespace hc

@@ -24,8 +24,10 @@ struct BackLds {
   char rec[(REC_BWD - REC_DEC + PASS - 1) / PASS * PASS];
 };
 
-template <typename T, int KP, int NW, bool VEC>
-__global__ __launch_bounds__(64 * NW) void delta_back_kernel(DeltaArgs a) {
+// FULL: as above, over a segment's chunks. Otherwise a segment's first gradient from zeros (the last
+// segment's from its own), nothing else.
+template <typename T, int KP, int NW, bool VEC, bool FULL>
+__global__ __launch_bounds__(64 * NW, 2) void delta_back_kernel(DeltaArgs a) {
   constexpr int NP = Stream<T>::NP, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
   constexpr int PIECES = KP / 8, ITEMS = (CH * PIECES + THREADS - 1) / THREADS;
   constexpr int USED = REC_BWD - REC_DEC, RR = (USED + 16 * THREADS - 1) / (16 * THREADS);
@@ -37,21 +39,24 @@ __global__ __launch_bounds__(64 * NW) void delta_back_kernel(DeltaArgs a) {
   Lds& lds = *reinterpret_cast<Lds*>(lds_raw);
   const int tid = threadIdx.x, lane = tid & 63, w = wave_number(), n = lane & 15, g = lane >> 4;
   const int rows_at = Tk::lane_at(n, g), cols_at = Tk::lane_at_t(n, g);
-  const uint32_t groups = ((uint32_t)a.Dv + 16 * NW - 1) / (16 * NW);
-  const int64_t bh = blockIdx.x / groups, b = (uint32_t)bh / (uint32_t)a.Hv;
-  const uint32_t hv = (uint32_t)bh % (uint32_t)a.Hv, hk = hv / ((uint32_t)a.Hv / (uint32_t)a.Hk);
   const int Dk = (int)a.Dk, Dv = (int)a.Dv, VP = (int)a.VP, qs = (int)a.Hk * Dk, vs = (int)a.Hv * Dv;
-  const int col = (int)(blockIdx.x % groups) * 16 * NW + 16 * w, have = min(16, Dv - col);  // columns; may be none
-  const int64_t len = length_of(a.lengths, b, a.S), chunks = (len + CH - 1) / CH;
-  const int64_t keys = b * a.S * qs + hk * Dk, values = b * a.S * vs + hv * Dv + col;
+  const Part part(a, ((uint32_t)Dv + 16 * NW - 1) / (16 * NW));
+  const int64_t bh = part.bh, len = part.len;
+  const int col = part.group * 16 * NW + 16 * w, have = min(16, Dv - col);  // columns; may be none
+  const int64_t keys = part.b * a.S * qs + part.hk * Dk, values = part.b * a.S * vs + part.hv * Dv + col;
+  if (FULL && part.ends() && n < have) {  // nothing reaches the tokens behind the sequence's length
+    const int64_t from = max(len, part.first * CH), to = min(a.S, (part.first + a.SL) * CH);
+    for (int64_t t = from + g; t < to; t += 4) Elem<T>::st((T*)a.dv + values + t * vs + n, 0.f);
+  }
+  if (part.empty() || (!FULL && part.seg == 0)) return;
   const char* rec = (const char*)a.rec + bh * a.NC * REC_BWD + REC_DEC;
   const uint32_t v_lane = n < have ? (8 * g * vs + n) * (uint32_t)sizeof(T) : NOWHERE;
 
   State<KP> D;
-  D.load(a.dlast ? a.dlast + bh * Dk * Dv + col : nullptr, Dk, Dv, n, g, have);
-  // nothing reaches the tokens behind the sequence's length
-  if (n < have)
-    for (int64_t t = len + g; t < a.S; t += 4) Elem<T>::st((T*)a.dv + values + t * vs + n, 0.f);
+  {
+    const float* from = part.ends() ? a.dlast + (a.dlast ? bh * Dk * Dv : 0) : FULL ? a.slots + (part.slot + 1) * Dk * Dv : nullptr;
+    D.load(from ? from + col : nullptr, Dk, Dv, n, g, have);
+  }
 
   Raw8<T> kr[ITEMS], qr[ITEMS];
   u4_t rr[RR];
@@ -77,8 +82,8 @@ __global__ __launch_bounds__(64 * NW) void delta_back_kernel(DeltaArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) dr[t][r] = dc.get((const T*)nullptr, vl + row_of(t, r) * vs * (uint32_t)sizeof(T));
   };
-  if (chunks > 0) fetch(chunks - 1);
-  for (int64_t c = chunks - 1; c >= 0; --c) {
+  if (part.first < part.last) fetch(part.last - 1);
+  for (int64_t c = part.last - 1; c >= part.first; --c) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int x = i * THREADS + tid, piece = x % PIECES, row = x / PIECES;
@@ -98,8 +103,8 @@ __global__ __launch_bounds__(64 * NW) void delta_back_kernel(DeltaArgs a) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) d[t] = f4_t{dr[t][0], dr[t][1], dr[t][2], dr[t][3]};
     lds_barrier();
-    if (c > 0) fetch(c - 1);
-    D.keep((bf16_t*)a.dstates + (bh * a.NC + c) * 2 * KP * VP, VP, col, n, g);
+    if (c > part.first) fetch(c - 1);
+    if (FULL) D.keep((bf16_t*)a.dstates + (bh * a.NC + c) * 2 * KP * VP, VP, col, n, g);
 
     f4_t x[4];  // K N
 #pragma unroll
@@ -148,7 +153,7 @@ __global__ __launch_bounds__(64 * NW) void delta_back_kernel(DeltaArgs a) {
       for (int kb = t >> 1; kb < 2; ++kb) x[t] = mma(load_tile(lds.rec + TT, tri_t(t, kb), lane), f[kb], x[t]);
     }
     keep_order();
-    {
+    if (FULL) {
       const Range vc = head_rows((T*)a.dv + values + c * CH * vs, have > 0 ? (int)min((int64_t)CH, len - c * CH) : 0, vs, have);
       const uint32_t vl = anew(v_lane);
 #pragma unroll
@@ -189,7 +194,8 @@ __global__ __launch_bounds__(64 * NW) void delta_back_kernel(DeltaArgs a) {
     }
     lds_barrier();
   }
-  if (a.dstate0) D.store(a.dstate0 + bh * Dk * Dv + col, Dk, Dv, n, g, have);
+  float* to = !FULL ? a.slots + part.slot * Dk * Dv : part.seg == 0 && a.dstate0 ? a.dstate0 + bh * Dk * Dv : nullptr;
+  if (to) D.store(to + col, Dk, Dv, n, g, have);
 }
 
 // ------------------------------------------------------------- each chunk by itself
@@ -500,12 +506,13 @@ hipError_t with_lds(K kernel, size_t lds, unsigned grid, unsigned block, const D
   return hipGetLastError();
 }
 
-template <typename T, int KP, int NW>
+template <typename T, int KP, bool FULL>
 hipError_t back_go(const DeltaArgs& a, hipStream_t st) {
-  const unsigned grid = (unsigned)(a.B * a.Hv * ((a.Dv + 16 * NW - 1) / (16 * NW)));
+  constexpr int NW = 4;
+  const unsigned grid = (unsigned)(a.B * a.Hv * a.NS * ((a.Dv + 16 * NW - 1) / (16 * NW)));
   const size_t lds = sizeof(BackLds<KP, Stream<T>::NP, NW>);
-  return a.vec ? with_lds(delta_back_kernel<T, KP, NW, true>, lds, grid, 64 * NW, a, st)
-               : with_lds(delta_back_kernel<T, KP, NW, false>, lds, grid, 64 * NW, a, st);
+  return a.vec ? with_lds(delta_back_kernel<T, KP, NW, true, FULL>, lds, grid, 64 * NW, a, st)
+               : with_lds(delta_back_kernel<T, KP, NW, false, FULL>, lds, grid, 64 * NW, a, st);
 }
 
 template <typename T, int KP>
@@ -521,9 +528,12 @@ hipError_t grad_go(const DeltaArgs& a, hipStream_t st) {
 
 template <typename T, int KP>
 hipError_t backward_go(const DeltaArgs& a, hipStream_t st) {
-  hipError_t e;
-  if constexpr (KP < 256) e = a.Dv > 64 ? back_go<T, KP, 8>(a, st) : back_go<T, KP, 4>(a, st);
-  else e = back_go<T, KP, 4>(a, st);
+  hipError_t e = hipSuccess;
+  if (a.NS > 1) {
+    e = back_go<T, KP, false>(a, st);
+    if (e == hipSuccess) e = launch_delta_join(true, a, st);
+  }
+  if (e == hipSuccess) e = back_go<T, KP, true>(a, st);
   return e != hipSuccess || a.NC == 0 ? e : grad_go<T, KP>(a, st);
 }
 
@@ -535,23 +545,6 @@ hipError_t backward_by_width(const DeltaArgs& a, hipStream_t st) {
 }
 
 }  // namespace
-
-int64_t delta_backward_ws(DeltaArgs& a, void* ws) {
-  const int64_t n = a.B * a.Hv * a.NC, KP = a.Dk <= 64 ? 64 : a.Dk <= 128 ? 128 : 256;
-  a.VP = (a.Dv + 31) / 32 * 32;
-  int64_t at = 0;
-  const auto take = [&](int64_t bytes) {
-    char* p = (char*)ws + at;
-    at += n * bytes;  // every part is whole kilobytes
-    return (void*)p;
-  };
-  a.states = take(4 * KP * a.VP);
-  a.dstates = take(4 * KP * a.VP);
-  a.z = take(4 * CH * a.VP);
-  a.w = take(4 * CH * a.VP);
-  a.rec = take(REC_BWD);
-  return at;
-}
 
 hipError_t launch_delta_backward(int dtype, const DeltaArgs& a, hipStream_t st) {
   if (a.NC > 0) {

@@ -328,6 +328,31 @@ struct State {
   }
 };
 
+// A workgroup of the walks: a segment of a head's chunks by a group of its columns.
+struct Part {
+  int64_t bh, b, slot;
+  uint32_t hv, hk;
+  int seg, group;
+  int64_t len, chunks, first, last;  // [first, last) of them are this segment's
+  __device__ __forceinline__ Part(const DeltaArgs& a, uint32_t groups) {
+    group = (int)(blockIdx.x % groups);
+    const uint32_t x = blockIdx.x / groups, NS = (uint32_t)a.NS, Hv = (uint32_t)a.Hv;
+    seg = (int)(x % NS);
+    bh = x / NS;
+    b = (uint32_t)bh / Hv;
+    hv = (uint32_t)bh % Hv;
+    hk = hv / (Hv / (uint32_t)a.Hk);
+    slot = bh * NS + seg;
+    len = length_of(a.lengths, b, a.S);
+    chunks = (len + CH - 1) / CH;
+    first = seg * a.SL;
+    last = min(chunks, first + a.SL);
+  }
+  // the sequence ends before this segment; the first one passes an empty sequence's state on
+  __device__ __forceinline__ bool empty() const { return seg > 0 && first >= chunks; }
+  __device__ __forceinline__ bool ends() const { return last >= chunks; }  // none comes behind it
+};
+
 // Four tiles of a chunk's 64 rows, as [CH, stride] in two parts.
 __device__ __forceinline__ void keep_rows(bf16_t* p, int stride, int col, int n, int g, const f4_t (&x)[4]) {
   const Range hi(p, 2 * CH * stride), lo(p + CH * stride, 2 * CH * stride);

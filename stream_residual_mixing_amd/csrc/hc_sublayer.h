@@ -70,9 +70,8 @@ int64_t scan_ws_bytes(int64_t B, int64_t S, int64_t C);
 hipError_t launch_scan(int dtype, bool bwd, bool vec, const ScanArgs& a, hipStream_t st);
 
 // ---- gated delta rule (hc_delta.hip, hc_delta_backward.hip)
-// rec: the chunks' records in the workspace; NC = ceil(S / 64). vec: Dk % 8 == 0, Dv even, q, k and
-// their gradients 16-byte aligned, v, o and theirs to two elements, the states to 8 bytes (16 where
-// Dv % 4 == 0).
+// vec: Dk % 8 == 0 with q, k and their gradients 16-byte aligned; vec8: also Dv % 8 == 0 with d_o
+// 16-byte aligned; vec4: Dv % 4 == 0 with the states 16-byte aligned.
 struct DeltaArgs {
   const void* q;
   const void* k;
@@ -83,18 +82,10 @@ struct DeltaArgs {
   const int32_t* lengths;  // may be NULL: S tokens each
   void* o;
   float* state1;           // may be NULL
-  void* rec;
-  int64_t B, S, Hk, Hv, Dk, Dv, NC;
+  int64_t B, S, Hk, Hv, Dk, Dv;
   float scale;
-  bool vec;
-  // the backward's: every chunk's first state [KP, VP] and Z [64, VP], and the state's gradient
-  // behind it and W of the same shapes, each as two bfloat16 parts; KP is Dk as 64, 128 or 256,
-  // VP is Dv in whole 32s
-  void* states;
-  void* z;
-  void* dstates;
-  void* w;
-  int64_t VP;
+  bool vec, vec8, vec4;
+  // backward
   const void* d_o;
   const float* dlast;      // may be NULL: zeros
   void* dq;
@@ -103,15 +94,26 @@ struct DeltaArgs {
   float* dg;
   float* dbeta;
   float* dstate0;          // may be NULL
-  bool vec8;               // vec, and Dv % 8 == 0 with d_o 16-byte aligned
+  // set by delta_plan: NC = ceil(S / 64) chunks in segments of SL, NS segments at most; VP is Dv in
+  // whole 32s; the arrays in the workspace
+  int64_t NC, SL, NS, VP;
+  void* rec;               // the chunks' records
+  float* slots;            // [B, Hv, NS, Dk, Dv] a segment's last state (backward: the gradient of its first)
+  void* phi;               // [B, Hv, NS, 2, KP, KP] its map of the state, in two bfloat16 parts
+  void* phi_t;             // the same transposed; KP is Dk as 64, 128 or 256
+  void* states;            // backward: every chunk's first state [KP, VP] and Z [64, VP], and the gradient
+  void* z;                 // of the state behind it and W of the same shapes, in two bfloat16 parts
+  void* dstates;
+  void* w;
 };
-int64_t delta_ws_bytes(int64_t B, int64_t S, int64_t Hv);
+// lays the call out and returns the bytes of its workspace; ws may be NULL
+int64_t delta_plan(DeltaArgs& a, bool backward, void* ws);
 hipError_t launch_delta(int dtype, const DeltaArgs& a, hipStream_t st);
-// the records, states and z of the backward
+// the backward's first part: records, segments' maps, states and z
 hipError_t launch_delta_keep(int dtype, const DeltaArgs& a, hipStream_t st);
-// sets the workspace's arrays in a and returns their bytes (ws may be NULL)
-int64_t delta_backward_ws(DeltaArgs& a, void* ws);
 hipError_t launch_delta_backward(int dtype, const DeltaArgs& a, hipStream_t st);
+// joins the segments' states (back: their gradients, from the last one)
+hipError_t launch_delta_join(bool back, const DeltaArgs& a, hipStream_t st);
 
 // ---- balance loss and the router's backward (hc_router.hip)
 int64_t balance_ws_bytes(int64_t B, int64_t S, int N, int m);

@@ -73,7 +73,7 @@ def _bounds(q, k, v, g, beta, M, scale, n):
     return np.sqrt(eo2), em
 
 
-def check_forward(got_o, got_M, ins, lengths, dt, scale=None, o_init=None):
+def check_forward(got_o, got_M, ins, lengths, dt, scale=None, o_init=None, slack=1):
     q, k, v, g, beta, M = (down(x) for x in ins)
     B, S, Hk, Dk = q.shape
     Hv = v.shape[2]
@@ -85,6 +85,7 @@ def check_forward(got_o, got_M, ins, lengths, dt, scale=None, o_init=None):
         for h in range(Hv):
             kh = h // (Hv // Hk)
             eo, em = _bounds(q[b, :, kh], k[b, :, kh], v[b, :, h], g[b, :, h], beta[b, :, h], M[b, h], scale, n)
+            eo, em = slack * eo, slack * em
             err = np.abs(o[b, :n, h] - ro[b, :n, h])
             # what is not the rounding of the element itself
             more = np.maximum(err - P[dt] * (np.abs(ro[b, :n, h]) + err), 0)
@@ -115,6 +116,25 @@ def test_forward(size, dt):
         o, M = hc.hc_gated_delta(*ins, lengths=lengths, out=(o0.clone(), None))
         torch.cuda.synchronize()
         check_forward(o, M, ins, L, dt, o_init=down(o0))
+
+
+@pytest.mark.parametrize("size", [(3, 1500, 1, 1, 64, 24), (2, 1024, 1, 2, 40, 80), (1, 1100, 1, 1, 130, 66)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_segments(size, dt):
+    """Few heads and long sequences are walked in segments that are joined afterwards: lengths that end in
+    the first, at a border, in the middle and in the last of them. The segments' maps are products of the
+    same kind, off by the same c of terms whose norms are at most 1: twice the chunks' bounds."""
+    B, S, Hk, Hv, Dk, Dv = size
+    ins = inputs(*size, dt, seed=S)
+    rng = np.random.default_rng(S)
+    ends = [S, 256, 0, 257, 700, 1, 512, S - 1]
+    for turn in range(0, len(ends), B):
+        L = np.array((ends[turn:] + ends)[:B])
+        note(f"hc_gated_delta {size} {dt} lengths={L}")
+        o0 = up(rng.normal(size=(B, S, Hv, Dv)), dt)
+        o, M = hc.hc_gated_delta(*ins, lengths=torch.from_numpy(L.astype(np.int32)).cuda(), out=(o0.clone(), None))
+        torch.cuda.synchronize()
+        check_forward(o, M, ins, L, dt, o_init=down(o0), slack=2)
 
 
 @pytest.mark.parametrize("S", [4, 150])

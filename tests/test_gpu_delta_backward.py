@@ -71,7 +71,7 @@ def _bounds(q, k, v, g, beta, do, M, N, scale, n):
     return np.append(np.sqrt(out[:5]), en)
 
 
-def check_backward(got, ins, do, dstate, lengths, dt, scale=None):
+def check_backward(got, ins, do, dstate, lengths, dt, scale=None, slack=1):
     q, k, v, g, beta, M, do, dM = (down(x) for x in (*ins, do, dstate))
     B, S, Hk, Dk = q.shape
     Hv = v.shape[2]
@@ -83,7 +83,7 @@ def check_backward(got, ins, do, dstate, lengths, dt, scale=None):
         for h in range(Hv):
             kh = h // (Hv // Hk)
             e = _bounds(q[b, :, kh], k[b, :, kh], v[b, :, h], g[b, :, h], beta[b, :, h], do[b, :, h], M[b, h], dM[b, h],
-                        scale, n)
+                        scale, n) * slack
             shared[kh] += e[:2]
             for i, rnd in ((2, P[dt]), (3, 2.0 ** -22), (4, 2.0 ** -22), (5, 2.0 ** -22)):
                 x, y = (down(got[i])[b, h], ref[i][b, h]) if i == 5 else (down(got[i])[b, :, h], ref[i][b, :, h])
@@ -121,6 +121,23 @@ def test_backward(size, dt):
         got = hc.hc_gated_delta_backward(*ins[:5], do, ins[5], dM, lengths=lengths)
         torch.cuda.synchronize()
         check_backward(got, ins, do, dM, L, dt)
+
+
+@pytest.mark.parametrize("size", [(3, 1100, 1, 1, 64, 24), (2, 1024, 1, 2, 40, 80), (1, 1030, 1, 1, 130, 66)])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_segments(size, dt):
+    """Few heads and long sequences are walked in segments: as in the forward's test, with twice the bounds."""
+    B, S, Hk, Hv, Dk, Dv = size
+    ins = inputs(*size, dt, seed=S)
+    rng = np.random.default_rng(S)
+    do, dM = up(rng.normal(size=(B, S, Hv, Dv)), dt), up(rng.normal(size=(B, Hv, Dk, Dv)))
+    ends = [S, 256, 0, 257, 700, 1]
+    for turn in range(0, len(ends), B):
+        L = np.array((ends[turn:] + ends)[:B])
+        note(f"hc_gated_delta_backward {size} {dt} lengths={L}")
+        got = hc.hc_gated_delta_backward(*ins[:5], do, ins[5], dM, lengths=torch.from_numpy(L.astype(np.int32)).cuda())
+        torch.cuda.synchronize()
+        check_backward(got, ins, do, dM, L, dt, slack=2)
 
 
 def test_against_differences_of_the_forward():
