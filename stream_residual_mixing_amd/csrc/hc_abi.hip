@@ -1723,7 +1723,7 @@ int hc_gated_delta_backward(const void* q, const void* k, const void* v, const v
   if ((r = device_status()) != HC_OK) return r;
   hc::DeltaArgs a{q, k, v, g, beta, state0, lengths, nullptr, nullptr, B, S, Hk, Hv, Dk, Dv, scale};
   a.vec = Dk % 8 == 0 && aligned_to(q, 16) && aligned_to(k, 16) && aligned_to(dq, 16) && aligned_to(dk, 16);
-  a.vec8 = a.vec && Dv % 8 == 0 && aligned_to(d_o, 16);
+  a.vec8 = a.vec && Dv % 8 == 0 && aligned_to(d_o, 16) && aligned_to(v, 16);
   a.d_o = d_o, a.dlast = dstate, a.dq = dq, a.dk = dk, a.dv = dv, a.dg = dg, a.dbeta = dbeta, a.dstate0 = dstate0;
   hc::delta_plan(a, true, workspace);
   return launch_status(hc::launch_delta_backward(dtype, a, (hipStream_t)stream));

@@ -19,15 +19,15 @@ namespace {
 // --------------------------------------------------------------- each chunk by itself
 
 template <typename T, int KP, bool VEC, bool BWD>
-__global__ __launch_bounds__(256, 3) void delta_prep_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
   constexpr int NP = Stream<T>::NP, KB = KP / 32, LS = CH + 4;
   __shared__ __attribute__((aligned(16))) float L[CH][LS], inv[CH][LS];
   __shared__ double G[CH];
   __shared__ __attribute__((aligned(16))) float beta_s[CH];
-  int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
-  const int w = wave_number();
-  const uint32_t NC = (uint32_t)a.NC, chunk = blockIdx.x % NC, bh = blockIdx.x / NC, hk = bh % (uint32_t)a.Hk;
-  const int64_t b = bh / (uint32_t)a.Hk;
+  const int lane = threadIdx.x & 63, w = wave_number(), n = lane & 15, g = lane >> 4;
+  const uint32_t NC = (uint32_t)a.NC, chunk = blockIdx.x % NC, bh = blockIdx.x / NC, hv = bh % (uint32_t)a.Hv;
+  const uint32_t hk = hv / ((uint32_t)a.Hv / (uint32_t)a.Hk);
+  const int64_t b = bh / (uint32_t)a.Hv;
   const int64_t t0 = (int64_t)chunk * CH, tokens = length_of(a.lengths, b, a.S) - t0;
   if (tokens <= 0) return;
   const int Dk = (int)a.Dk, qs = (int)(a.Hk * a.Dk), left = (int)min((int64_t)CH, tokens);
@@ -53,130 +53,123 @@ __global__ __launch_bounds__(256, 3) void delta_prep_kernel(DeltaArgs a) {
       }
       if (BWD && (t >> 1) >= (w >> 1)) kq[t] = mma(token_op<T, VEC>(q, qs, row_of(t, n), k0, Dk), kn, kq[t]);
     }
-    if (kb & 1) keep_order();
+    keep_order();
   }
   // the upper blocks that the inverse's tiles hold stay zero
   {
     const int bl = threadIdx.x >> 7, i = (threadIdx.x & 127) >> 3, c = 2 * (threadIdx.x & 7);
     inv[32 * bl + i][32 * bl + 16 + c] = inv[32 * bl + i][32 * bl + 16 + c + 1] = 0.f;
   }
-  const int per = (int)((uint32_t)a.Hv / (uint32_t)a.Hk);
-  for (int hi = 0; hi < per; ++hi) {
-    renew(n, g);
-    lane = 16 * g + n;
-    const int64_t hv = hk * per + hi, rec = (b * a.Hv + hv) * NC + chunk;
-    char* out = (char*)a.rec + rec * (BWD ? REC_BWD : REC);
-    if (threadIdx.x < CH) {  // one wave
-      const int i = threadIdx.x;
-      const bool on = i < tokens;
-      const int64_t at = (b * a.S + t0 + i) * a.Hv + hv;
-      const double s = running_sum(on ? clamp_decay(a.g[at]) : 0.0, i);
-      const double end = __shfl(s, CH - 1, 64);
-      const float be = on ? a.beta[at] : 0.f;
-      G[i] = s;
-      beta_s[i] = be;
-      float* dec = (float*)(out + REC_DEC);
-      dec[DEC_AHEAD + i] = expf((float)s);
-      dec[DEC_TO_END + i] = expf((float)(end - s));
-      dec[DEC_BETA + i] = be;
-    }
-    lds_barrier();
-    {
-      const int i = 16 * w + n;
-      const double Gi = G[i];
-      float p[2][8];
+  char* out = (char*)a.rec + (int64_t)blockIdx.x * (BWD ? REC_BWD : REC);
+  if (threadIdx.x < CH) {  // one wave
+    const int i = threadIdx.x;
+    const bool on = i < tokens;
+    const int64_t at = (b * a.S + t0 + i) * a.Hv + hv;
+    const double s = running_sum(on ? clamp_decay(a.g[at]) : 0.0, i);
+    const double end = __shfl(s, CH - 1, 64);
+    const float be = on ? a.beta[at] : 0.f;
+    G[i] = s;
+    beta_s[i] = be;
+    float* dec = (float*)(out + REC_DEC);
+    dec[DEC_AHEAD + i] = expf((float)s);
+    dec[DEC_TO_END + i] = expf((float)(end - s));
+    dec[DEC_BETA + i] = be;
+  }
+  lds_barrier();
+  {
+    const int i = 16 * w + n;
+    const double Gi = G[i];
+    float p[2][8];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if ((t >> 1) > (w >> 1)) continue;
-        const int j0 = 32 * (t >> 1) + 8 * g + 4 * (t & 1);
-        f4_t l;
+    for (int t = 0; t < 4; ++t) {
+      if ((t >> 1) > (w >> 1)) continue;
+      const int j0 = 32 * (t >> 1) + 8 * g + 4 * (t & 1);
+      f4_t l;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float d = j0 + r <= i ? expf((float)(Gi - G[j0 + r])) : 0.f;
-          p[t >> 1][4 * (t & 1) + r] = j0 + r <= i ? d * qk[t][r] : 0.f;
-          l[r] = j0 + r < i ? d * kk[t][r] * beta_s[j0 + r] : 0.f;
-        }
-        *reinterpret_cast<f4_t*>(&L[i][j0]) = l;
+      for (int r = 0; r < 4; ++r) {
+        const float d = j0 + r <= i ? expf((float)(Gi - G[j0 + r])) : 0.f;
+        p[t >> 1][4 * (t & 1) + r] = j0 + r <= i ? d * qk[t][r] : 0.f;
+        l[r] = j0 + r < i ? d * kk[t][r] * beta_s[j0 + r] : 0.f;
       }
-      if (!BWD) {
-        store_tile(out + REC_P, tri(w, 0), lane, p[0]);
-        if (w >= 2) store_tile(out + REC_P, tri(w, 1), lane, p[1]);
-      }
+      *reinterpret_cast<f4_t*>(&L[i][j0]) = l;
     }
-    if (BWD) {
-      const int j = 16 * w + n;
-      const double Gj = G[j];
-      float p[2][8];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if ((t >> 1) < (w >> 1)) continue;
-        const int i0 = 32 * (t >> 1) + 8 * g + 4 * (t & 1);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          p[t >> 1][4 * (t & 1) + r] = j <= i0 + r ? expf((float)(G[i0 + r] - Gj)) * kq[t][r] : 0.f;
-      }
-      // lane n holds P^T's row j = 16 w + n: its place in row_of's order
-      const int pl = place_of(j), t = pl >> 4, to = (pl & 15) + 16 * g;
-      if (w < 2) store_tile(out + REC_P, tri_t(t, 0), to, p[0]);
-      store_tile(out + REC_P, tri_t(t, 1), to, p[1]);
+    if (!BWD) {
+      store_tile(out + REC_P, tri(w, 0), lane, p[0]);
+      if (w >= 2) store_tile(out + REC_P, tri(w, 1), lane, p[1]);
     }
-    lds_barrier();
-    // (I + A)^-1: wave w inverts its 16 x 16 block on the diagonal, a lane a column, ...
-    {
-      float x[16];
+  }
+  if (BWD) {
+    const int j = 16 * w + n;
+    const double Gj = G[j];
+    float p[2][8];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float s = i == n ? 1.f : 0.f;
+    for (int t = 0; t < 4; ++t) {
+      if ((t >> 1) < (w >> 1)) continue;
+      const int i0 = 32 * (t >> 1) + 8 * g + 4 * (t & 1);
 #pragma unroll
-        for (int m = 0; m < i; ++m) s -= L[16 * w + i][16 * w + m] * x[m];
-        x[i] = s;
-        if (i & 1) keep_order();
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if ((i >> 2) == g) inv[16 * w + i][16 * w + n] = x[i];
+      for (int r = 0; r < 4; ++r)
+        p[t >> 1][4 * (t & 1) + r] = j <= i0 + r ? expf((float)(G[i0 + r] - Gj)) * kq[t][r] : 0.f;
     }
-    lds_barrier();
-    // ... then forms the blocks below it: T_iw = -T_ii sum_m A_im T_mw, in float32 products
-    {
-      f4_t col[4];
+    // lane n holds P^T's row j = 16 w + n: its place in row_of's order
+    const int pl = place_of(j), t = pl >> 4, to = (pl & 15) + 16 * g;
+    if (w < 2) store_tile(out + REC_P, tri_t(t, 0), to, p[0]);
+    store_tile(out + REC_P, tri_t(t, 1), to, p[1]);
+  }
+  lds_barrier();
+  // (I + A)^-1: wave w inverts its 16 x 16 block on the diagonal, a lane a column, ...
+  {
+    float x[16];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) col[0][r] = inv[16 * w + 4 * g + r][16 * w + n];
+    for (int i = 0; i < 16; ++i) {
+      float s = i == n ? 1.f : 0.f;
 #pragma unroll
-      for (int d = 1; d < 4; ++d) {  // block row w + d
-        if (w + d >= 4) break;
-        const int i0 = 16 * (w + d);
-        f4_t s = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int m = 0; m < d; ++m) {
-          const f4_t l = *reinterpret_cast<const f4_t*>(&L[i0 + n][16 * (w + m) + 4 * g]);
-#pragma unroll
-          for (int r = 0; r < 4; ++r) s = __builtin_amdgcn_mfma_f32_16x16x4f32(l[r], col[m][r], s, 0, 0, 0);
-        }
-        const f4_t ti = *reinterpret_cast<const f4_t*>(&inv[i0 + n][i0 + 4 * g]);
-        f4_t o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o = __builtin_amdgcn_mfma_f32_16x16x4f32(ti[r], -s[r], o, 0, 0, 0);
-        col[d] = o;
-#pragma unroll
-        for (int r = 0; r < 4; ++r) inv[i0 + 4 * g + r][16 * w + n] = o[r];
-      }
+      for (int m = 0; m < i; ++m) s -= L[16 * w + i][16 * w + m] * x[m];
+      x[i] = s;
+      if (i & 1) keep_order();
     }
-    lds_barrier();
-    {
-      const int i = row_of(w, n);
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        if (kb <= (w >> 1)) store_tile(out + REC_T, tri(w, kb), lane, &inv[i][32 * kb + 8 * g]);
-        if (BWD && kb >= (w >> 1)) {
-          float v[8];
+    for (int i = 0; i < 16; ++i)
+      if ((i >> 2) == g) inv[16 * w + i][16 * w + n] = x[i];
+  }
+  lds_barrier();
+  // ... then forms the blocks below it: T_iw = -T_ii sum_m A_im T_mw, in float32 products
+  {
+    f4_t col[4];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = inv[32 * kb + 8 * g + e][i];
-          store_tile(out + REC_TT, tri_t(w, kb), lane, v);
-        }
+    for (int r = 0; r < 4; ++r) col[0][r] = inv[16 * w + 4 * g + r][16 * w + n];
+#pragma unroll
+    for (int d = 1; d < 4; ++d) {  // block row w + d
+      if (w + d >= 4) break;
+      const int i0 = 16 * (w + d);
+      f4_t s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int m = 0; m < d; ++m) {
+        const f4_t l = *reinterpret_cast<const f4_t*>(&L[i0 + n][16 * (w + m) + 4 * g]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s = __builtin_amdgcn_mfma_f32_16x16x4f32(l[r], col[m][r], s, 0, 0, 0);
+      }
+      const f4_t ti = *reinterpret_cast<const f4_t*>(&inv[i0 + n][i0 + 4 * g]);
+      f4_t o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int r = 0; r < 4; ++r) o = __builtin_amdgcn_mfma_f32_16x16x4f32(ti[r], -s[r], o, 0, 0, 0);
+      col[d] = o;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) inv[i0 + 4 * g + r][16 * w + n] = o[r];
+    }
+  }
+  lds_barrier();
+  {
+    const int i = row_of(w, n);
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      if (kb <= (w >> 1)) store_tile(out + REC_T, tri(w, kb), lane, &inv[i][32 * kb + 8 * g]);
+      if (BWD && kb >= (w >> 1)) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = inv[32 * kb + 8 * g + e][i];
+        store_tile(out + REC_TT, tri_t(w, kb), lane, v);
       }
     }
-    lds_barrier();
   }
 }
 
@@ -482,37 +475,68 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
 
 // ----------------------------------------------------------------- the segments
 
-// M_{s+1} = Phi_s M_s + N_s over a head's segments, 16 columns of the state by a wave; the slots' N
-// become the states. BACK: the gradients, from the last segment on, with Phi's transpose.
+// M_{s+1} = Phi_s M_s + N_s over a head's segments, 16 columns of the state by a workgroup; the slots'
+// N become the states. A wave has 32 rows of the state, the operand block that the next step's
+// products take from all of them through LDS; its rows of the next step's Phi and N are on their
+// way meanwhile (one wave that does it all, 7.4 us a step instead of 1.3). BACK: the gradients, from
+// the last segment on, with Phi's transpose.
 template <int KP, bool BACK>
-__global__ __launch_bounds__(64) void delta_join_kernel(DeltaArgs a) {
-  constexpr int KB = KP / 32, KT = KP / 16;
-  const int lane = threadIdx.x, n = lane & 15, g = lane >> 4;
+__global__ __launch_bounds__(2 * KP) void delta_join_kernel(DeltaArgs a) {
+  constexpr int KB = KP / 32;
+  __shared__ __attribute__((aligned(16))) char lds[2][KB][2][TILE];
+  const int lane = threadIdx.x & 63, w = wave_number(), n = lane & 15, g = lane >> 4;
   const int Dk = (int)a.Dk, Dv = (int)a.Dv;
   const uint32_t groups = ((uint32_t)Dv + 15) / 16;
   const int64_t bh = blockIdx.x / groups, b = (uint32_t)bh / (uint32_t)a.Hv;
   const int col = (int)(blockIdx.x % groups) * 16, have = min(16, Dv - col);
-  const int64_t chunks = (length_of(a.lengths, b, a.S) + CH - 1) / CH;
+  const int64_t chunks = (length_of(a.lengths, b, a.S) + CH - 1) / CH, state = (int64_t)Dk * Dv;
   const int segs = (int)((chunks + a.SL - 1) / a.SL);  // that hold tokens
-  float* slots = a.slots + bh * a.NS * Dk * Dv + col;
+  float* slots = a.slots + bh * a.NS * state + col;
   const bf16_t* maps = (const bf16_t*)(BACK ? a.phi_t : a.phi) + bh * a.NS * 2 * KP * KP;
   if (segs < 3) return;  // the second segment's state is the first's last one
-  State<KP> S;
-  S.load(slots + (BACK ? segs - 1 : 0) * (int64_t)Dk * Dv, Dk, Dv, n, g, have);
+  const auto seg = [&](int i) { return BACK ? segs - 1 - i : i; };
+  const uint32_t s_lane = n < have ? 4 * ((32 * w + 8 * g) * Dv + n) : NOWHERE;
+  const uint32_t m_lane = 2 * ((8 * (n >> 2) + (n & 3)) * KP + 8 * g);
+  Split m[2][KB];
+  float add[8];
+  const auto load_slot = [&](int i, float (&v)[8]) {
+    const Range r(slots + seg(i) * state, ((int64_t)(Dk - 1) * Dv + have) * 4);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = r.get((const float*)nullptr, s_lane + 4 * e * Dv);
+  };
+  const auto fetch = [&](int i) {
+    const Range r(maps + seg(i) * (int64_t)2 * KP * KP, 4 * KP * KP);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) m[t][kb] = r.parts(m_lane, 2 * ((32 * w + 4 * t) * KP + 32 * kb), 2 * KP * KP);
+    load_slot(i, add);
+  };
+  float S[8];  // rows 32 w + 8 g + 0 .. 7
+  load_slot(0, S);
+  fetch(1);
   for (int i = 1; i < segs - 1; ++i) {
-    const int s = BACK ? segs - 1 - i : i;
-    const Range m(maps + s * (int64_t)2 * KP * KP, 4 * KP * KP);
-    const uint32_t at = 2 * ((8 * (n >> 2) + (n & 3)) * KP + 8 * g);
-    Split f[KB];
+    u4_t hi, lo;
+    split8(S, hi, lo);
+    char* mine = lds[i & 1][w][0] + lane * 16;
+    *reinterpret_cast<u4_t*>(mine) = hi;
+    *reinterpret_cast<u4_t*>(mine + TILE) = lo;
+    lds_barrier();
+    f4_t o[2] = {{add[0], add[1], add[2], add[3]}, {add[4], add[5], add[6], add[7]}};
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) f[kb] = split(S.m[2 * kb], S.m[2 * kb + 1]);
-    S.load(slots + s * (int64_t)Dk * Dv, Dk, Dv, n, g, have);
+    for (int kb = 0; kb < KB; ++kb) {
+      const char* p = lds[i & 1][kb][0] + lane * 16;
+      const Split f = {*reinterpret_cast<const bf8_t*>(p), *reinterpret_cast<const bf8_t*>(p + TILE)};
 #pragma unroll
-    for (int t = 0; t < KT; ++t)
+      for (int t = 0; t < 2; ++t) o[t] = mma(m[t][kb], f, o[t]);
+    }
+    if (i + 1 < segs - 1) fetch(i + 1);
+    const Range r(slots + seg(i) * state, ((int64_t)(Dk - 1) * Dv + have) * 4);
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
-        S.m[t] = mma(m.parts(at, 2 * (row_of(t, 0) * KP + 32 * kb), 2 * KP * KP), f[kb], S.m[t]);
-    S.store(slots + s * (int64_t)Dk * Dv, Dk, Dv, n, g, have);
+    for (int e = 0; e < 8; ++e) {
+      S[e] = o[e >> 2][e & 3];
+      r.put((float*)nullptr, s_lane + 4 * e * Dv, S[e]);
+    }
   }
 }
 
@@ -543,7 +567,7 @@ hipError_t delta_go(const DeltaArgs& a, hipStream_t st) {
     else hipLaunchKernelGGL((delta_step_kernel<T, KP, false>), grid, dim3(256), 0, st, a);
     return hipGetLastError();
   }
-  const dim3 prep((unsigned)(a.B * a.Hk * a.NC));
+  const dim3 prep((unsigned)(a.B * a.Hv * a.NC));
   if (a.vec) hipLaunchKernelGGL((delta_prep_kernel<T, KP, true, MODE == KEEP>), prep, dim3(256), 0, st, a);
   else hipLaunchKernelGGL((delta_prep_kernel<T, KP, false, MODE == KEEP>), prep, dim3(256), 0, st, a);
   hipError_t e = hipGetLastError();
@@ -564,9 +588,9 @@ hipError_t delta_by_width(const DeltaArgs& a, hipStream_t st) {
 template <bool BACK>
 void join_go(const DeltaArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)(a.B * a.Hv * ((a.Dv + 15) / 16)));
-  if (a.Dk <= 64) hipLaunchKernelGGL((delta_join_kernel<64, BACK>), grid, dim3(64), 0, st, a);
-  else if (a.Dk <= 128) hipLaunchKernelGGL((delta_join_kernel<128, BACK>), grid, dim3(64), 0, st, a);
-  else hipLaunchKernelGGL((delta_join_kernel<256, BACK>), grid, dim3(64), 0, st, a);
+  if (a.Dk <= 64) hipLaunchKernelGGL((delta_join_kernel<64, BACK>), grid, dim3(128), 0, st, a);
+  else if (a.Dk <= 128) hipLaunchKernelGGL((delta_join_kernel<128, BACK>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((delta_join_kernel<256, BACK>), grid, dim3(512), 0, st, a);
 }
 
 }  // namespace

@@ -6,8 +6,8 @@
 //   dQ = exp(G) d M^T + B K,
 //   dK = [-exp(G) W M^T + A K] + [exp(G_end - G) X N^T + B^T Q + A^T K]   (as read, as written),
 //   dbeta_j = Z_j . dX_j - sum_i exp(G_i - G_j) (k_i . k_j) (W_i . Z_j),
-//   dG = q . dq + k . dk_read - k . dk_written, and at the chunk's end
-//        sum_j k_j . (X N^T exp(G_end - G))_j + exp(G_end) <M, N>;  dg_t = sum_{i >= t} dG_i.
+//   dG = q . dq + k . dk_read - k . dk_written = q . dq + W . (Z - V) - beta dbeta, and at the
+//        chunk's end sum_j k_j . (X N^T exp(G_end - G))_j + exp(G_end) <M, N>;  dg_t = sum_{i >= t} dG_i.
 // The forward's walk is run again and keeps every chunk's M and Z; a second walk from the end back
 // keeps N and W and writes dV; then every chunk forms the rest by itself, all value heads of a key
 // head in one workgroup, so that dQ and dK are summed in registers and in a fixed order.
@@ -292,66 +292,68 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaArgs a) {
       const float beta_n = lds.beta[tok];
 
       const Range dop = head_rows((const T*)a.d_o + (b * a.S + t0) * vs + hv * Dv, left, vs, Dv);
+      const Range vp = head_rows((const T*)a.v + (b * a.S + t0) * vs + hv * Dv, left, vs, Dv);
       const Range zp((const bf16_t*)a.z + at * 2 * CH * VP, 4 * CH * VP);
       const Range wp((const bf16_t*)a.w + at * 2 * CH * VP, 4 * CH * VP);
       const uint32_t two = 2 * VP, vlo = CH * two, slo = KP * two;
       const int row0 = 8 * (n >> 2) + (n & 3);  // row_of(t, n) without the tile's own part
 
-      // what each pair of tokens passes on: B^T and A^T (lane i, rows j), B and A (lane j, rows i)
-      float db = 0.f;
-      Split bq[2], ar[2], bk[2], aw[2];
+      // What each pair of tokens passes on. The wave's tokens lie in half h of the chunk; with those of the
+      // same half a token is the earlier or the later one, with the other half's only one of them.
+      // Lane j = tok. Rows i >= j: B_ij and A_ij (it is the earlier one); rows j' <= tok: B and A of
+      // (tok, j'), the later one. As operands: bq by K for dQ, bk by Q and aa by K for dK; x is the
+      // other half's bk (h = 0) or bq (h = 1).
+      const int h = w >> 1;
+      float db = 0.f, own_wz = 0.f, wv = 0.f;
+      Split bq, bk, aa, x, ax;
       {
-        // rows j, lane i: Z_j . dO_i and Z_j . W_i; rows i, lane j: dO_i . Z_j and W_i . Z_j
-        f4_t zd[4], zw[4], dz[4], wz[4];
+        f4_t zd[2], zw[2], dz[2], wz[2];  // Z_row . dO, Z_row . W, dO_row . Z, W_row . Z with the wave's tokens
+        f4_t xd[2], xw[2];                // the other half's: the last two (h = 0) or the first two
 #pragma unroll
-        for (int t = 0; t < 4; ++t) zd[t] = zw[t] = dz[t] = wz[t] = f4_t{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < 2; ++t) zd[t] = zw[t] = dz[t] = wz[t] = xd[t] = xw[t] = f4_t{0.f, 0.f, 0.f, 0.f};
         for (int vb = 0; vb < VP; vb += 32) {
           const int v0 = vb + 8 * g;
           const uint32_t own = 2 * (n * VP + v0), other = 2 * (row0 * VP + v0);
           const Op<NP> dn = token_op<T, VEC>(dop, vs, tok, v0, Dv);
           const Split zn = zp.parts(own, 16 * w * two, vlo), wn = wp.parts(own, 16 * w * two, vlo);
+          Raw8<T> vraw;
+          vraw.template load<VEC>(vp, (tok * vs + v0) * (uint32_t)sizeof(T), Dv - v0);
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            if ((t >> 1) <= (w >> 1)) {
-              const Split zr = zp.parts(other, row_of(t, 0) * two, vlo);
-              zd[t] = mma(zr, dn, zd[t]);
-              zw[t] = mma(zr, wn, zw[t]);
-            }
-            if ((t >> 1) >= (w >> 1)) {
-              dz[t] = mma(token_op<T, VEC>(dop, vs, row0 + row_of(t, 0), v0, Dv), zn, dz[t]);
-              wz[t] = mma(wp.parts(other, row_of(t, 0) * two, vlo), zn, wz[t]);
+          for (int t = 0; t < 2; ++t) {
+            const int r = 32 * h + 4 * t, o = 32 - 32 * h + 4 * t;
+            const Split zr = zp.parts(other, r * two, vlo), wr = wp.parts(other, r * two, vlo);
+            const Op<NP> dr = token_op<T, VEC>(dop, vs, row0 + r, v0, Dv);
+            zd[t] = mma(zr, dn, zd[t]);
+            zw[t] = mma(zr, wn, zw[t]);
+            dz[t] = mma(dr, zn, dz[t]);
+            wz[t] = mma(wr, zn, wz[t]);
+            if (h == 0) {
+              xd[t] = mma(token_op<T, VEC>(dop, vs, row0 + o, v0, Dv), zn, xd[t]);
+              xw[t] = mma(wp.parts(other, o * two, vlo), zn, xw[t]);
+            } else {
+              const Split zo = zp.parts(other, o * two, vlo);
+              xd[t] = mma(zo, dn, xd[t]);
+              xw[t] = mma(zo, wn, xw[t]);
             }
           }
+          float vf[8];
+          vraw.open(vf);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) wv += vf[e] * ((float)wn.hi[e] + (float)wn.lo[e]);
           keep_order();
         }
-        float vb[2][8], va[2][8];
+        f4_t kk[2], qk[2], xk[2], xq[2];  // rows i: k_i . k_j and q_i . k_j
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const f4_t beta = *reinterpret_cast<const f4_t*>(lds.beta + row_of(t, 4 * g));
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int j = row_of(t, 4 * g + r);
-            const float d = j <= tok ? beta[r] * expf((float)(Gn - lds.G[j])) : 0.f;
-            vb[t >> 1][4 * (t & 1) + r] = j <= tok ? a.scale * d * zd[t][r] : 0.f;
-            va[t >> 1][4 * (t & 1) + r] = j < tok ? -d * zw[t][r] : 0.f;
-          }
-        }
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) bq[kb] = split(vb[kb]), ar[kb] = split(va[kb]);
-        keep_order();
-        f4_t kk[4], qk[4];  // rows i: k_i . k_j and q_i . k_j
-#pragma unroll
-        for (int t = 0; t < 4; ++t) kk[t] = qk[t] = f4_t{0.f, 0.f, 0.f, 0.f};
+        for (int t = 0; t < 2; ++t) kk[t] = qk[t] = xk[t] = xq[t] = f4_t{0.f, 0.f, 0.f, 0.f};
         if (pass == 0) {
-          const int rows_at = Tk::lane_at(n, g), own_at = Tk::at(place_of(tok), g);
+          const int rows_at = Tk::lane_at(n, g) + 32 * h * Tk::ROW, own_at = Tk::at(place_of(tok), g);
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb) {
             Op<NP> kn;
 #pragma unroll
             for (int p = 0; p < NP; ++p) kn.p[p] = *reinterpret_cast<const bf8_t*>(lds.k[p] + (own_at ^ (kb << 6)));
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              if ((t >> 1) < (w >> 1)) continue;
+            for (int t = 0; t < 2; ++t) {
               Op<NP> ka, qa;
 #pragma unroll
               for (int p = 0; p < NP; ++p) {
@@ -361,102 +363,142 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaArgs a) {
               kk[t] = mma(ka, kn, kk[t]);
               qk[t] = mma(qa, kn, qk[t]);
             }
+            if (h == 0) {
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+                Op<NP> ka, qa;
+#pragma unroll
+                for (int p = 0; p < NP; ++p) {
+                  ka.p[p] = Tk::rows(lds.k[p], rows_at, 2 + t, kb);
+                  qa.p[p] = Tk::rows(lds.q[p], rows_at, 2 + t, kb);
+                }
+                xk[t] = mma(ka, kn, xk[t]);
+                xq[t] = mma(qa, kn, xq[t]);
+              }
+            }
             keep_order();
           }
         }
+        float vq[8], vk[8], va[8];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 2; ++t) {
+          const int r0 = 32 * h + 8 * g + 4 * t;
+          const f4_t beta = *reinterpret_cast<const f4_t*>(lds.beta + r0);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const int i = row_of(t, 4 * g + r);
-            const float d = i >= tok ? expf((float)(lds.G[i] - Gn)) : 0.f;
-            const float bz = i >= tok ? a.scale * d * dz[t][r] : 0.f, az = i > tok ? -d * wz[t][r] : 0.f;
-            db += (i >= tok ? bz * qk[t][r] : 0.f) + (i > tok ? az * kk[t][r] : 0.f);
-            vb[t >> 1][4 * (t & 1) + r] = beta_n * bz;
-            va[t >> 1][4 * (t & 1) + r] = beta_n * az;
+            const int row = r0 + r;
+            const double G = lds.G[row];
+            const float d = expf((float)(row >= tok ? G - Gn : Gn - G));
+            const float bz = row >= tok ? a.scale * d * dz[t][r] : 0.f, az = row > tok ? -d * wz[t][r] : 0.f;
+            vq[4 * t + r] = row <= tok ? a.scale * beta[r] * d * zd[t][r] : 0.f;
+            vk[4 * t + r] = beta_n * bz;
+            va[4 * t + r] = row < tok ? -beta[r] * d * zw[t][r] : beta_n * az;
+            db += bz * qk[t][r] + az * kk[t][r];
+            own_wz = row == tok ? wz[t][r] : own_wz;
           }
+        }
+        bq = split(vq);
+        bk = split(vk);
+        aa = split(va);
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) bk[kb] = split(vb[kb]), aw[kb] = split(va[kb]);
+        for (int t = 0; t < 2; ++t) {
+          const int r0 = 32 - 32 * h + 8 * g + 4 * t;
+          const f4_t beta = *reinterpret_cast<const f4_t*>(lds.beta + r0);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const double G = lds.G[r0 + r];
+            const float d = expf((float)(h == 0 ? G - Gn : Gn - G));
+            const float bx = a.scale * d * xd[t][r], axx = -d * xw[t][r], be = h == 0 ? beta_n : beta[r];
+            if (h == 0) db += bx * xq[t][r] + axx * xk[t][r];
+            vq[4 * t + r] = be * bx;
+            va[4 * t + r] = be * axx;
+          }
+        }
+        x = split(vq);
+        ax = split(va);
         keep_order();
       }
-      // what the states pass on
-      f4_t dq[KT], read[KT], early[KT];
-      float mn = 0.f;
+      // what the states pass on, four tiles of keys at a time
+      float mn = 0.f, qdq = 0.f, at_end = 0.f;  // <M, N>; q . dq; k . (N Z) to the chunk's end
       const Range mp((const bf16_t*)a.states + at * 2 * KP * VP, 4 * KP * VP);
       const Range np((const bf16_t*)a.dstates + at * 2 * KP * VP, 4 * KP * VP);
-#pragma unroll
-      for (int t = 0; t < KT; ++t) dq[t] = read[t] = early[t] = f4_t{0.f, 0.f, 0.f, 0.f};
-      for (int vb = 0; vb < VP; vb += 32) {
-        const int v0 = vb + 8 * g;
-        const uint32_t own = 2 * (n * VP + v0), other = 2 * (row0 * VP + v0);
-        const Op<NP> dn = token_op<T, VEC>(dop, vs, tok, v0, Dv);
-        const Split zn = zp.parts(own, 16 * w * two, vlo), wn = wp.parts(own, 16 * w * two, vlo);
-#pragma unroll
-        for (int t = 0; t < KT; ++t) {
-          const uint32_t tile = (row_of(t, 0) + 16 * KT * pass) * two;
-          const Split m = mp.parts(other, tile, slo), nn = np.parts(other, tile, slo);
-          dq[t] = mma(m, dn, dq[t]);
-          read[t] = mma(m, wn, read[t]);
-          early[t] = mma(nn, zn, early[t]);
-          if ((t & 3) == w)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) mn += ((float)m.hi[e] + (float)m.lo[e]) * ((float)nn.hi[e] + (float)nn.lo[e]);
-          if ((t & 1) == 1) keep_order();
-        }
-      }
       const double Gend = lds.G[CH - 1];
       const float ahead = expf((float)Gn), to_end = expf((float)(Gend - Gn)), eb = to_end * beta_n;
       const int cols_at = Tk::lane_at_t(n, g) ^ (pass << 8);
-      float dot = 0.f, at_end = 0.f;  // q . dq + k . (dk as read - as written); k . early
 #pragma unroll
-      for (int t2 = 0; t2 < KT / 2; ++t2) {
-        float kf[8], qf[8];
-        {
-          const int k0 = 32 * t2 + 16 * KT * pass + 8 * g;
-          Raw8<T> kraw, qraw;
-          kraw.template load<VEC>(k, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0);
-          qraw.template load<VEC>(q, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0);
-          kraw.open(kf);
-          qraw.open(qf);
+      for (int t4 = 0; t4 < KT; t4 += 4) {
+        f4_t dq[4], read[4], early[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) dq[t] = read[t] = early[t] = f4_t{0.f, 0.f, 0.f, 0.f};
+        for (int vb = 0; vb < VP; vb += 32) {
+          const int v0 = vb + 8 * g;
+          const uint32_t own = 2 * (n * VP + v0), other = 2 * (row0 * VP + v0);
+          const Op<NP> dn = token_op<T, VEC>(dop, vs, tok, v0, Dv);
+          const Split zn = zp.parts(own, 16 * w * two, vlo), wn = wp.parts(own, 16 * w * two, vlo);
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t tile = (row_of(t4 + t, 0) + 16 * KT * pass) * two;
+            const Split m = mp.parts(other, tile, slo), nn = np.parts(other, tile, slo);
+            dq[t] = mma(m, dn, dq[t]);
+            read[t] = mma(m, wn, read[t]);
+            early[t] = mma(nn, zn, early[t]);
+          }
+          {  // a quarter of <M, N>, of what another wave has read too
+            const uint32_t tile = (16 * (t4 + KT * pass) + 16 * w) * two;
+            const Split m = mp.parts(own, tile, slo), nn = np.parts(own, tile, slo);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mn += ((float)m.hi[e] + (float)m.lo[e]) * ((float)nn.hi[e] + (float)nn.lo[e]);
+          }
+          keep_order();
         }
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int t = 2 * t2 + half;
-          float ke = 0.f;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) ke += kf[4 * half + r] * early[t][r];
-          db += to_end * ke;
-          at_end += eb * ke;
-          dq[t] *= a.scale * ahead;
-          read[t] *= -ahead;
-          early[t] *= eb;
-#pragma unroll
-          for (int b2 = 0; b2 < 2; ++b2) {
-            Op<NP> ka, qa;
-#pragma unroll
-            for (int p = 0; p < NP; ++p) {
-              ka.p[p] = Tk::cols(lds.k[p], cols_at, t, b2);
-              qa.p[p] = Tk::cols(lds.q[p], cols_at, t, b2);
-            }
-            if (b2 <= (w >> 1)) {
-              dq[t] = mma(ka, bq[b2], dq[t]);
-              read[t] = mma(ka, ar[b2], read[t]);
-            }
-            if (b2 >= (w >> 1)) {
-              early[t] = mma(qa, bk[b2], early[t]);
-              early[t] = mma(ka, aw[b2], early[t]);
-            }
+        for (int t2 = 0; t2 < 2; ++t2) {
+          float kf[8], qf[8];
+          {
+            const int k0 = 32 * t2 + 16 * (t4 + KT * pass) + 8 * g;
+            Raw8<T> kraw, qraw;
+            kraw.template load<VEC>(k, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0);
+            qraw.template load<VEC>(q, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0);
+            kraw.open(kf);
+            qraw.open(qf);
           }
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            dot += qf[4 * half + r] * dq[t][r] + kf[4 * half + r] * (read[t][r] - early[t][r]);
-          dqt[t] = SHARED ? dqt[t] + dq[t] : dq[t];
-          dkt[t] = SHARED ? dkt[t] + (read[t] + early[t]) : read[t] + early[t];
+          for (int half = 0; half < 2; ++half) {
+            const int t = 2 * t2 + half;
+            float ke = 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) ke += kf[4 * half + r] * early[t][r];
+            db += to_end * ke;
+            at_end += eb * ke;
+            dq[t] *= a.scale * ahead;
+            f4_t dk = eb * early[t] - ahead * read[t];
+            Op<NP> ko, qo, kx, qx;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+              ko.p[p] = Tk::cols(lds.k[p], cols_at, t4 + t, h);
+              qo.p[p] = Tk::cols(lds.q[p], cols_at, t4 + t, h);
+              kx.p[p] = Tk::cols(lds.k[p], cols_at, t4 + t, 1 - h);
+              if (h == 0) qx.p[p] = Tk::cols(lds.q[p], cols_at, t4 + t, 1);
+            }
+            dq[t] = mma(ko, bq, dq[t]);
+            dk = mma(qo, bk, dk);
+            dk = mma(ko, aa, dk);
+            dk = mma(kx, ax, dk);
+            if (h == 0) dk = mma(qx, x, dk);
+            else dq[t] = mma(kx, x, dq[t]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) qdq += qf[4 * half + r] * dq[t][r];
+            dqt[t4 + t] = SHARED ? dqt[t4 + t] + dq[t] : dq[t];
+            dkt[t4 + t] = SHARED ? dkt[t4 + t] + dk : dk;
+          }
+          keep_order();
         }
-        keep_order();
       }
-      dot = sum_groups(dot);
+      // A token's part of the decays' sums: dO . o = q . dq for what it reads with q,
+      // k . dk as it reads = W . (Z - v), and k . dk as it is written = beta dbeta, which is linear in k as
+      // in beta.
       db = sum_groups(db);
+      const float dot = sum_groups(qdq) + (pass == 0 ? sum_groups(own_wz - wv) : 0.f) - beta_n * db;
       // <M, N> and the ends' sum over the chunk
       const float ends = wave_sum(at_end + expf((float)Gend) * mn);
       if (g == 0) {

@@ -70,8 +70,8 @@ int64_t scan_ws_bytes(int64_t B, int64_t S, int64_t C);
 hipError_t launch_scan(int dtype, bool bwd, bool vec, const ScanArgs& a, hipStream_t st);
 
 // ---- gated delta rule (hc_delta.hip, hc_delta_backward.hip)
-// vec: Dk % 8 == 0 with q, k and their gradients 16-byte aligned; vec8: also Dv % 8 == 0 with d_o
-// 16-byte aligned; vec4: Dv % 4 == 0 with the states 16-byte aligned.
+// vec: Dk % 8 == 0 with q, k and their gradients 16-byte aligned; vec8: also Dv % 8 == 0 with v and
+// d_o 16-byte aligned; vec4: Dv % 4 == 0 with the states 16-byte aligned.
 struct DeltaArgs {
   const void* q;
   const void* k;
