@@ -200,11 +200,21 @@ __global__ __launch_bounds__(64 * NW, 2) void delta_back_kernel(DeltaArgs a) {
 
 // ------------------------------------------------------------- each chunk by itself
 
+// Four waves' 64 tokens by 64 keys, or twice as many waves by 128 keys at a time: wider heads take two
+// passes, the second of which adds to the first's dg and dbeta.
 template <int KP, int NP>
 struct GradLds {
+  static constexpr int HALVES = KP == 64 ? 1 : 2, WAVES = 4 * HALVES, ROWS = 64 * HALVES;
+  // Blocks of ROWS keys by 32 columns of a state in two parts, two where there is room: the state's and
+  // its gradient's in turn
+  static constexpr int BLOCKS = KP == 256 && NP == 2 ? 1 : 2, PART = ROWS * 64;
   char k[NP][Tokens<KP>::BYTES], q[NP][Tokens<KP>::BYTES];  // rows in row_of's order
+  char block[BLOCKS][2][PART];
   double G[CH];
-  float beta[CH], dG[CH], end[4];
+  float beta[CH], own[CH], qdq[HALVES][CH], db[HALVES][CH], end[WAVES];
+  // a block's row in row_of's order, its four 16-byte pieces exchanged so that 16 lanes reading a piece of
+  // 16 rows reach all banks once
+  static __device__ __forceinline__ int at(int place, int piece) { return place * 64 + ((piece ^ ((place >> 2) & 3)) << 4); }
 };
 
 // Eight elements at byte offset o, the first `cnt` of them (VEC: all or none).
@@ -236,18 +246,18 @@ __device__ __forceinline__ float sum_groups(float v) {  // over the four lanes o
   return v + __shfl_xor(v, 32, 64);
 }
 
-// SHARED: several value heads read a key head. Up to 128 keys at a time, for which there are
-// registers: wider heads take two passes, the second of which adds to the first's dg and dbeta.
+// SHARED: several value heads read a key head.
 template <typename T, int KP, bool VEC, bool SHARED>
-__global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaArgs a) {
-  constexpr int NP = Stream<T>::NP, KB = KP / 32, KT = KP < 128 ? KP / 16 : 8, PASSES = KP / 16 / KT;
-  constexpr int PIECES = KP / 8, ITEMS = CH * PIECES / 256;
-  extern __shared__ __attribute__((aligned(16))) char lds_raw[];
+__global__ __launch_bounds__((GradLds<KP, Stream<T>::NP>::WAVES * 64)) void delta_grad_kernel(DeltaArgs a) {
+  constexpr int NP = Stream<T>::NP, KB = KP / 32;
   typedef GradLds<KP, NP> Lds;
   typedef Tokens<KP> Tk;
+  constexpr int THREADS = 64 * Lds::WAVES, ROWS = Lds::ROWS, PASSES = KP / ROWS;
+  constexpr int PIECES = KP / 8, ITEMS = CH * PIECES / THREADS;
+  extern __shared__ __attribute__((aligned(16))) char lds_raw[];
   static_assert(sizeof(Lds) <= 160 * 1024, "LDS of a CU");
   Lds& lds = *reinterpret_cast<Lds*>(lds_raw);
-  const int tid = threadIdx.x, lane = tid & 63, w = wave_number();
+  const int tid = threadIdx.x, lane = tid & 63, wave = wave_number(), w = wave & 3, half = wave >> 2;
   int n = lane & 15, g = lane >> 4;
   const uint32_t NC = (uint32_t)a.NC, chunk = blockIdx.x % NC, bh = blockIdx.x / NC, hk = bh % (uint32_t)a.Hk;
   const int64_t b = bh / (uint32_t)a.Hk, t0 = (int64_t)chunk * CH, tokens = length_of(a.lengths, b, a.S) - t0;
@@ -258,7 +268,7 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaArgs a) {
   const Range q = head_rows((const T*)a.q + keys, left, qs, Dk), k = head_rows((const T*)a.k + keys, left, qs, Dk);
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
-    const int x = i * 256 + tid, piece = x % PIECES, row = x / PIECES;
+    const int x = i * THREADS + tid, piece = x % PIECES, row = x / PIECES;
     const Op<NP> ko = token_op<T, VEC>(k, qs, row, 8 * piece, Dk), qo = token_op<T, VEC>(q, qs, row, 8 * piece, Dk);
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
@@ -269,9 +279,10 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaArgs a) {
   }
 #pragma unroll 1
   for (int pass = 0; pass < PASSES; ++pass) {
-    f4_t dqt[KT], dkt[KT];
+    const int key0 = ROWS * pass + 64 * half;  // the wave's 64 keys
+    f4_t dqt[4], dkt[4];
 #pragma unroll
-    for (int t = 0; t < KT; ++t) dqt[t] = dkt[t] = f4_t{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < 4; ++t) dqt[t] = dkt[t] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int hi = 0; hi < per; ++hi) {
       renew(n, g);
@@ -287,6 +298,18 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaArgs a) {
         lds.G[tid] = running_sum(on ? clamp_decay(a.g[gat + tid * a.Hv]) : 0.0, tid);
         lds.beta[tid] = on ? a.beta[gat + tid * a.Hv] : 0.f;
       }
+      // the states' first blocks on their way: a thread has eight columns of a row of each
+      const Range mp((const bf16_t*)a.states + at * 2 * KP * VP, 4 * KP * VP);
+      const Range np((const bf16_t*)a.dstates + at * 2 * KP * VP, 4 * KP * VP);
+      const uint32_t two = 2 * VP, vlo = CH * two, slo = KP * two;
+      const int b_row = tid >> 2, b_piece = tid & 3, b_at = Lds::at(place_of(b_row), b_piece);
+      const uint32_t b_lane = 2 * ((ROWS * pass + b_row) * VP + 8 * b_piece);
+      Split mr, nr;
+      const auto fetch = [&](int vb) {
+        mr = mp.parts(b_lane, 2 * vb, slo);
+        nr = np.parts(b_lane, 2 * vb, slo);
+      };
+      fetch(0);
       lds_barrier();
       const double Gn = lds.G[tok];
       const float beta_n = lds.beta[tok];
@@ -295,7 +318,6 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaArgs a) {
       const Range vp = head_rows((const T*)a.v + (b * a.S + t0) * vs + hv * Dv, left, vs, Dv);
       const Range zp((const bf16_t*)a.z + at * 2 * CH * VP, 4 * CH * VP);
       const Range wp((const bf16_t*)a.w + at * 2 * CH * VP, 4 * CH * VP);
-      const uint32_t two = 2 * VP, vlo = CH * two, slo = KP * two;
       const int row0 = 8 * (n >> 2) + (n & 3);  // row_of(t, n) without the tile's own part
 
       // What each pair of tokens passes on. The wave's tokens lie in half h of the chunk; with those of the
@@ -345,7 +367,7 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaArgs a) {
         f4_t kk[2], qk[2], xk[2], xq[2];  // rows i: k_i . k_j and q_i . k_j
 #pragma unroll
         for (int t = 0; t < 2; ++t) kk[t] = qk[t] = xk[t] = xq[t] = f4_t{0.f, 0.f, 0.f, 0.f};
-        if (pass == 0) {
+        if (pass == 0 && half == 0) {
           const int rows_at = Tk::lane_at(n, g) + 32 * h * Tk::ROW, own_at = Tk::at(place_of(tok), g);
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb) {
@@ -418,114 +440,135 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaArgs a) {
         ax = split(va);
         keep_order();
       }
-      // what the states pass on, four tiles of keys at a time
-      float mn = 0.f, qdq = 0.f, at_end = 0.f;  // <M, N>; q . dq; k . (N Z) to the chunk's end
-      const Range mp((const bf16_t*)a.states + at * 2 * KP * VP, 4 * KP * VP);
-      const Range np((const bf16_t*)a.dstates + at * 2 * KP * VP, 4 * KP * VP);
+      // what the states pass on, the wave's 64 keys by 32 columns at a time
+      f4_t dq[4], read[4], early[4];
+      float mn = 0.f;  // <M, N>
+#pragma unroll
+      for (int t = 0; t < 4; ++t) dq[t] = read[t] = early[t] = f4_t{0.f, 0.f, 0.f, 0.f};
+      const int a_lane = Lds::at(n, g) + 64 * half * 64;
+      for (int vb = 0; vb < VP; vb += 32) {
+        const int v0 = vb + 8 * g;
+        const uint32_t own = 2 * (n * VP + v0);
+        char *mb = lds.block[0][0], *nb = lds.block[Lds::BLOCKS - 1][0];
+        *reinterpret_cast<bf8_t*>(mb + b_at) = mr.hi;
+        *reinterpret_cast<bf8_t*>(mb + Lds::PART + b_at) = mr.lo;
+        if (Lds::BLOCKS == 2) {
+          *reinterpret_cast<bf8_t*>(nb + b_at) = nr.hi;
+          *reinterpret_cast<bf8_t*>(nb + Lds::PART + b_at) = nr.lo;
+        }
+        const Op<NP> dn = token_op<T, VEC>(dop, vs, tok, v0, Dv);
+        const Split zn = zp.parts(own, 16 * w * two, vlo), wn = wp.parts(own, 16 * w * two, vlo);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          mn += ((float)mr.hi[e] + (float)mr.lo[e]) * ((float)nr.hi[e] + (float)nr.lo[e]);
+        const Split last = nr;
+        if (vb + 32 < VP) fetch(vb + 32);
+        lds_barrier();
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const char* p = mb + a_lane + 1024 * t;
+          const Split m = {*reinterpret_cast<const bf8_t*>(p), *reinterpret_cast<const bf8_t*>(p + Lds::PART)};
+          dq[t] = mma(m, dn, dq[t]);
+          read[t] = mma(m, wn, read[t]);
+        }
+        if (Lds::BLOCKS == 1) {
+          lds_barrier();
+          *reinterpret_cast<bf8_t*>(nb + b_at) = last.hi;
+          *reinterpret_cast<bf8_t*>(nb + Lds::PART + b_at) = last.lo;
+          lds_barrier();
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const char* p = nb + a_lane + 1024 * t;
+          const Split m = {*reinterpret_cast<const bf8_t*>(p), *reinterpret_cast<const bf8_t*>(p + Lds::PART)};
+          early[t] = mma(m, zn, early[t]);
+        }
+        lds_barrier();
+      }
       const double Gend = lds.G[CH - 1];
       const float ahead = expf((float)Gn), to_end = expf((float)(Gend - Gn)), eb = to_end * beta_n;
-      const int cols_at = Tk::lane_at_t(n, g) ^ (pass << 8);
+      const int cols_at = Tk::lane_at_t(n, g) ^ (2 * key0);
+      float qdq = 0.f, at_end = 0.f;  // q . dq; k . (N Z) to the chunk's end
 #pragma unroll
-      for (int t4 = 0; t4 < KT; t4 += 4) {
-        f4_t dq[4], read[4], early[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) dq[t] = read[t] = early[t] = f4_t{0.f, 0.f, 0.f, 0.f};
-        for (int vb = 0; vb < VP; vb += 32) {
-          const int v0 = vb + 8 * g;
-          const uint32_t own = 2 * (n * VP + v0), other = 2 * (row0 * VP + v0);
-          const Op<NP> dn = token_op<T, VEC>(dop, vs, tok, v0, Dv);
-          const Split zn = zp.parts(own, 16 * w * two, vlo), wn = wp.parts(own, 16 * w * two, vlo);
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const uint32_t tile = (row_of(t4 + t, 0) + 16 * KT * pass) * two;
-            const Split m = mp.parts(other, tile, slo), nn = np.parts(other, tile, slo);
-            dq[t] = mma(m, dn, dq[t]);
-            read[t] = mma(m, wn, read[t]);
-            early[t] = mma(nn, zn, early[t]);
-          }
-          {  // a quarter of <M, N>, of what another wave has read too
-            const uint32_t tile = (16 * (t4 + KT * pass) + 16 * w) * two;
-            const Split m = mp.parts(own, tile, slo), nn = np.parts(own, tile, slo);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) mn += ((float)m.hi[e] + (float)m.lo[e]) * ((float)nn.hi[e] + (float)nn.lo[e]);
-          }
-          keep_order();
+      for (int t2 = 0; t2 < 2; ++t2) {
+        float kf[8], qf[8];
+        {
+          const int k0 = key0 + 32 * t2 + 8 * g;
+          Raw8<T> kraw, qraw;
+          kraw.template load<VEC>(k, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0);
+          qraw.template load<VEC>(q, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0);
+          kraw.open(kf);
+          qraw.open(qf);
         }
 #pragma unroll
-        for (int t2 = 0; t2 < 2; ++t2) {
-          float kf[8], qf[8];
-          {
-            const int k0 = 32 * t2 + 16 * (t4 + KT * pass) + 8 * g;
-            Raw8<T> kraw, qraw;
-            kraw.template load<VEC>(k, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0);
-            qraw.template load<VEC>(q, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0);
-            kraw.open(kf);
-            qraw.open(qf);
+        for (int u = 0; u < 2; ++u) {
+          const int t = 2 * t2 + u;
+          float ke = 0.f;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) ke += kf[4 * u + r] * early[t][r];
+          db += to_end * ke;
+          at_end += eb * ke;
+          dq[t] *= a.scale * ahead;
+          f4_t dk = eb * early[t] - ahead * read[t];
+          Op<NP> ko, qo, kx, qx;
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            ko.p[p] = Tk::cols(lds.k[p], cols_at, t, h);
+            qo.p[p] = Tk::cols(lds.q[p], cols_at, t, h);
+            kx.p[p] = Tk::cols(lds.k[p], cols_at, t, 1 - h);
+            if (h == 0) qx.p[p] = Tk::cols(lds.q[p], cols_at, t, 1);
           }
+          dq[t] = mma(ko, bq, dq[t]);
+          dk = mma(qo, bk, dk);
+          dk = mma(ko, aa, dk);
+          dk = mma(kx, ax, dk);
+          if (h == 0) dk = mma(qx, x, dk);
+          else dq[t] = mma(kx, x, dq[t]);
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int t = 2 * t2 + half;
-            float ke = 0.f;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) ke += kf[4 * half + r] * early[t][r];
-            db += to_end * ke;
-            at_end += eb * ke;
-            dq[t] *= a.scale * ahead;
-            f4_t dk = eb * early[t] - ahead * read[t];
-            Op<NP> ko, qo, kx, qx;
-#pragma unroll
-            for (int p = 0; p < NP; ++p) {
-              ko.p[p] = Tk::cols(lds.k[p], cols_at, t4 + t, h);
-              qo.p[p] = Tk::cols(lds.q[p], cols_at, t4 + t, h);
-              kx.p[p] = Tk::cols(lds.k[p], cols_at, t4 + t, 1 - h);
-              if (h == 0) qx.p[p] = Tk::cols(lds.q[p], cols_at, t4 + t, 1);
-            }
-            dq[t] = mma(ko, bq, dq[t]);
-            dk = mma(qo, bk, dk);
-            dk = mma(ko, aa, dk);
-            dk = mma(kx, ax, dk);
-            if (h == 0) dk = mma(qx, x, dk);
-            else dq[t] = mma(kx, x, dq[t]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) qdq += qf[4 * half + r] * dq[t][r];
-            dqt[t4 + t] = SHARED ? dqt[t4 + t] + dq[t] : dq[t];
-            dkt[t4 + t] = SHARED ? dkt[t4 + t] + dk : dk;
-          }
-          keep_order();
+          for (int r = 0; r < 4; ++r) qdq += qf[4 * u + r] * dq[t][r];
+          dqt[t] = SHARED ? dqt[t] + dq[t] : dq[t];
+          dkt[t] = SHARED ? dkt[t] + dk : dk;
         }
+        keep_order();
       }
       // A token's part of the decays' sums: dO . o = q . dq for what it reads with q,
       // k . dk as it reads = W . (Z - v), and k . dk as it is written = beta dbeta, which is linear in k as
-      // in beta.
+      // in beta. <M, N> and the ends' sum are the chunk's.
+      qdq = sum_groups(qdq);
       db = sum_groups(db);
-      const float dot = sum_groups(qdq) + (pass == 0 ? sum_groups(own_wz - wv) : 0.f) - beta_n * db;
-      // <M, N> and the ends' sum over the chunk
+      const float own = pass == 0 ? sum_groups(own_wz - wv) : 0.f;
       const float ends = wave_sum(at_end + expf((float)Gend) * mn);
       if (g == 0) {
-        lds.dG[tok] = dot;
-        float* p = a.dbeta + gat + tok * a.Hv;
-        if (tok < rows) *p = tok < left ? (pass ? *p + db : db) : 0.f;
+        lds.qdq[half][tok] = qdq;
+        lds.db[half][tok] = db;
+        if (half == 0) lds.own[tok] = own;
       }
-      if (lane == 0) lds.end[w] = ends;
+      if (lane == 0) lds.end[wave] = ends;
       lds_barrier();
       if (tid < CH) {
-        float s = lds.dG[tid];
+        float dbeta = lds.db[0][tid], s = lds.qdq[0][tid] + lds.own[tid];
+        if (Lds::HALVES == 2) dbeta += lds.db[Lds::HALVES - 1][tid], s += lds.qdq[Lds::HALVES - 1][tid];
+        s -= lds.beta[tid] * dbeta;
 #pragma unroll
         for (int o = 1; o < CH; o <<= 1) {
           const float down = __shfl_down(s, o, 64);
           if (tid + o < CH) s += down;
         }
-        s += (lds.end[0] + lds.end[1]) + (lds.end[2] + lds.end[3]);
-        float* p = a.dg + gat + tid * a.Hv;
-        if (tid < rows) *p = tid < left ? (pass ? *p + s : s) : 0.f;
+#pragma unroll
+        for (int i = 0; i < Lds::WAVES; ++i) s += lds.end[i];
+        float *pb = a.dbeta + gat + tid * a.Hv, *pg = a.dg + gat + tid * a.Hv;
+        if (tid < rows) {
+          *pb = tid < left ? (pass ? *pb + dbeta : dbeta) : 0.f;
+          *pg = tid < left ? (pass ? *pg + s : s) : 0.f;
+        }
       }
       lds_barrier();
     }
     const int tok = 16 * w + n;
     const Range dqp = head_rows((T*)a.dq + keys, rows, qs, Dk), dkp = head_rows((T*)a.dk + keys, rows, qs, Dk);
 #pragma unroll
-    for (int t2 = 0; t2 < KT / 2; ++t2) {
-      const int k0 = 32 * t2 + 16 * KT * pass + 8 * g;
+    for (int t2 = 0; t2 < 2; ++t2) {
+      const int k0 = key0 + 32 * t2 + 8 * g;
       float vq[8], vk[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -559,13 +602,13 @@ hipError_t back_go(const DeltaArgs& a, hipStream_t st) {
 
 template <typename T, int KP>
 hipError_t grad_go(const DeltaArgs& a, hipStream_t st) {
-  const unsigned grid = (unsigned)(a.B * a.Hk * a.NC);
-  const size_t lds = sizeof(GradLds<KP, Stream<T>::NP>);
+  typedef GradLds<KP, Stream<T>::NP> Lds;
+  const unsigned grid = (unsigned)(a.B * a.Hk * a.NC), block = 64 * Lds::WAVES;
   if (a.Hv == a.Hk)
-    return a.vec8 ? with_lds(delta_grad_kernel<T, KP, true, false>, lds, grid, 256, a, st)
-                  : with_lds(delta_grad_kernel<T, KP, false, false>, lds, grid, 256, a, st);
-  return a.vec8 ? with_lds(delta_grad_kernel<T, KP, true, true>, lds, grid, 256, a, st)
-                : with_lds(delta_grad_kernel<T, KP, false, true>, lds, grid, 256, a, st);
+    return a.vec8 ? with_lds(delta_grad_kernel<T, KP, true, false>, sizeof(Lds), grid, block, a, st)
+                  : with_lds(delta_grad_kernel<T, KP, false, false>, sizeof(Lds), grid, block, a, st);
+  return a.vec8 ? with_lds(delta_grad_kernel<T, KP, true, true>, sizeof(Lds), grid, block, a, st)
+                : with_lds(delta_grad_kernel<T, KP, false, true>, sizeof(Lds), grid, block, a, st);
 }
 
 template <typename T, int KP>
