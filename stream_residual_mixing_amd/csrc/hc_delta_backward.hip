@@ -206,15 +206,25 @@ template <int KP, int NP>
 struct GradLds {
   static constexpr int HALVES = KP == 64 ? 1 : 2, WAVES = 4 * HALVES, ROWS = 64 * HALVES;
   // Blocks of ROWS keys by 32 columns of a state in two parts, two where there is room: the state's and
-  // its gradient's in turn
+  // its gradient's in turn. In their place before that the chunk's Z and W in two parts and dO, 64
+  // tokens by SC columns at a time.
   static constexpr int BLOCKS = KP == 256 && NP == 2 ? 1 : 2, PART = ROWS * 64;
+  static constexpr int SC = KP == 256 && NP == 2 ? 32 : 64, STAGE = CH * SC * 2;
+  static constexpr int SHARED_BYTES = BLOCKS * 2 * PART > (4 + NP) * STAGE ? BLOCKS * 2 * PART : (4 + NP) * STAGE;
   char k[NP][Tokens<KP>::BYTES], q[NP][Tokens<KP>::BYTES];  // rows in row_of's order
-  char block[BLOCKS][2][PART];
+  char block[SHARED_BYTES];
   double G[CH];
-  float beta[CH], own[CH], qdq[HALVES][CH], db[HALVES][CH], end[WAVES];
+  float beta[CH], own[CH], wv[CH], qdq[HALVES][CH], db[HALVES][CH], end[WAVES];
   // a block's row in row_of's order, its four 16-byte pieces exchanged so that 16 lanes reading a piece of
   // 16 rows reach all banks once
   static __device__ __forceinline__ int at(int place, int piece) { return place * 64 + ((piece ^ ((place >> 2) & 3)) << 4); }
+  // the same of a stage
+  static __device__ __forceinline__ int stage_at(int place, int piece) {
+    return SC == 64 ? Tokens<64>::at(place, piece) : at(place, piece);
+  }
+  static __device__ __forceinline__ bf8_t stage(const char* m, int at, int tile, int kb) {
+    return *reinterpret_cast<const bf8_t*>(m + 16 * tile * 2 * SC + (at ^ (kb << 6)));
+  }
 };
 
 // Eight elements at byte offset o, the first `cnt` of them (VEC: all or none).
@@ -309,16 +319,33 @@ __global__ __launch_bounds__((GradLds<KP, Stream<T>::NP>::WAVES * 64)) void delt
         mr = mp.parts(b_lane, 2 * vb, slo);
         nr = np.parts(b_lane, 2 * vb, slo);
       };
-      fetch(0);
-      lds_barrier();
-      const double Gn = lds.G[tok];
-      const float beta_n = lds.beta[tok];
-
       const Range dop = head_rows((const T*)a.d_o + (b * a.S + t0) * vs + hv * Dv, left, vs, Dv);
       const Range vp = head_rows((const T*)a.v + (b * a.S + t0) * vs + hv * Dv, left, vs, Dv);
       const Range zp((const bf16_t*)a.z + at * 2 * CH * VP, 4 * CH * VP);
       const Range wp((const bf16_t*)a.w + at * 2 * CH * VP, 4 * CH * VP);
-      const int row0 = 8 * (n >> 2) + (n & 3);  // row_of(t, n) without the tile's own part
+      // and the first columns of Z, W, dO and V
+      constexpr int SC = Lds::SC, S_PIECES = SC / 8, S_ITEMS = (CH * S_PIECES + THREADS - 1) / THREADS;
+      Split zs[S_ITEMS], ws[S_ITEMS];
+      Raw8<T> ds[S_ITEMS], vr[S_ITEMS];
+      float wv[S_ITEMS];
+      const auto fetch_stage = [&](int vb) {
+#pragma unroll
+        for (int i = 0; i < S_ITEMS; ++i) {
+          const int x = i * THREADS + tid, row = x / S_PIECES, c = vb + 8 * (x % S_PIECES);
+          const uint32_t o = c < VP ? 2 * (row * VP + c) : NOWHERE;
+          zs[i] = zp.parts(o, 0, vlo);
+          ws[i] = wp.parts(o, 0, vlo);
+          ds[i].template load<VEC>(dop, (row * vs + c) * (uint32_t)sizeof(T), Dv - c);
+          vr[i].template load<VEC>(vp, (row * vs + c) * (uint32_t)sizeof(T), Dv - c);
+        }
+      };
+      fetch_stage(0);
+      fetch(0);
+#pragma unroll
+      for (int i = 0; i < S_ITEMS; ++i) wv[i] = 0.f;
+      lds_barrier();
+      const double Gn = lds.G[tok];
+      const float beta_n = lds.beta[tok];
 
       // What each pair of tokens passes on. The wave's tokens lie in half h of the chunk; with those of the
       // same half a token is the earlier or the later one, with the other half's only one of them.
@@ -326,43 +353,78 @@ __global__ __launch_bounds__((GradLds<KP, Stream<T>::NP>::WAVES * 64)) void delt
       // (tok, j'), the later one. As operands: bq by K for dQ, bk by Q and aa by K for dK; x is the
       // other half's bk (h = 0) or bq (h = 1).
       const int h = w >> 1;
-      float db = 0.f, own_wz = 0.f, wv = 0.f;
+      float db = 0.f, own_wz = 0.f;
       Split bq, bk, aa, x, ax;
       {
         f4_t zd[2], zw[2], dz[2], wz[2];  // Z_row . dO, Z_row . W, dO_row . Z, W_row . Z with the wave's tokens
         f4_t xd[2], xw[2];                // the other half's: the last two (h = 0) or the first two
 #pragma unroll
         for (int t = 0; t < 2; ++t) zd[t] = zw[t] = dz[t] = wz[t] = xd[t] = xw[t] = f4_t{0.f, 0.f, 0.f, 0.f};
-        for (int vb = 0; vb < VP; vb += 32) {
-          const int v0 = vb + 8 * g;
-          const uint32_t own = 2 * (n * VP + v0), other = 2 * (row0 * VP + v0);
-          const Op<NP> dn = token_op<T, VEC>(dop, vs, tok, v0, Dv);
-          const Split zn = zp.parts(own, 16 * w * two, vlo), wn = wp.parts(own, 16 * w * two, vlo);
-          Raw8<T> vraw;
-          vraw.template load<VEC>(vp, (tok * vs + v0) * (uint32_t)sizeof(T), Dv - v0);
+        const int own_s = Lds::stage_at(place_of(tok), g), rows_s = Lds::stage_at(n, g);
+        for (int vb = 0; vb < VP; vb += SC) {
+          char* st = lds.block;
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int r = 32 * h + 4 * t, o = 32 - 32 * h + 4 * t;
-            const Split zr = zp.parts(other, r * two, vlo), wr = wp.parts(other, r * two, vlo);
-            const Op<NP> dr = token_op<T, VEC>(dop, vs, row0 + r, v0, Dv);
-            zd[t] = mma(zr, dn, zd[t]);
-            zw[t] = mma(zr, wn, zw[t]);
-            dz[t] = mma(dr, zn, dz[t]);
-            wz[t] = mma(wr, zn, wz[t]);
-            if (h == 0) {
-              xd[t] = mma(token_op<T, VEC>(dop, vs, row0 + o, v0, Dv), zn, xd[t]);
-              xw[t] = mma(wp.parts(other, o * two, vlo), zn, xw[t]);
-            } else {
-              const Split zo = zp.parts(other, o * two, vlo);
-              xd[t] = mma(zo, dn, xd[t]);
-              xw[t] = mma(zo, wn, xw[t]);
+          for (int i = 0; i < S_ITEMS; ++i) {
+            const int x = i * THREADS + tid, row = x / S_PIECES, o = Lds::stage_at(place_of(row), x % S_PIECES);
+            if (CH * S_PIECES % THREADS == 0 || row < CH) {
+              const Op<NP> d = ds[i].op();
+              *reinterpret_cast<bf8_t*>(st + o) = zs[i].hi;
+              *reinterpret_cast<bf8_t*>(st + Lds::STAGE + o) = zs[i].lo;
+              *reinterpret_cast<bf8_t*>(st + 2 * Lds::STAGE + o) = ws[i].hi;
+              *reinterpret_cast<bf8_t*>(st + 3 * Lds::STAGE + o) = ws[i].lo;
+#pragma unroll
+              for (int p = 0; p < NP; ++p) *reinterpret_cast<bf8_t*>(st + (4 + p) * Lds::STAGE + o) = d.p[p];
             }
-          }
-          float vf[8];
-          vraw.open(vf);
+            float vf[8];
+            vr[i].open(vf);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) wv += vf[e] * ((float)wn.hi[e] + (float)wn.lo[e]);
-          keep_order();
+            for (int e = 0; e < 8; ++e) wv[i] += vf[e] * ((float)ws[i].hi[e] + (float)ws[i].lo[e]);
+          }
+          if (vb + SC < VP) fetch_stage(vb + SC);
+          lds_barrier();
+          const auto z_at = [&](int o, int tile, int kb) -> Split {
+            return {Lds::stage(st, o, tile, kb), Lds::stage(st + Lds::STAGE, o, tile, kb)};
+          };
+          const auto w_at = [&](int o, int tile, int kb) -> Split {
+            return {Lds::stage(st + 2 * Lds::STAGE, o, tile, kb), Lds::stage(st + 3 * Lds::STAGE, o, tile, kb)};
+          };
+          const auto d_at = [&](int o, int tile, int kb) {
+            Op<NP> d;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) d.p[p] = Lds::stage(st + (4 + p) * Lds::STAGE, o, tile, kb);
+            return d;
+          };
+#pragma unroll
+          for (int kb = 0; kb < SC / 32; ++kb) {
+            const Op<NP> dn = d_at(own_s, 0, kb);
+            const Split zn = z_at(own_s, 0, kb), wn = w_at(own_s, 0, kb);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int r = 2 * h + t, o = 2 - 2 * h + t;
+              const Split zr = z_at(rows_s, r, kb);
+              zd[t] = mma(zr, dn, zd[t]);
+              zw[t] = mma(zr, wn, zw[t]);
+              dz[t] = mma(d_at(rows_s, r, kb), zn, dz[t]);
+              wz[t] = mma(w_at(rows_s, r, kb), zn, wz[t]);
+              if (h == 0) {
+                xd[t] = mma(d_at(rows_s, o, kb), zn, xd[t]);
+                xw[t] = mma(w_at(rows_s, o, kb), zn, xw[t]);
+              } else {
+                const Split zo = z_at(rows_s, o, kb);
+                xd[t] = mma(zo, dn, xd[t]);
+                xw[t] = mma(zo, wn, xw[t]);
+              }
+            }
+            keep_order();
+          }
+          lds_barrier();
+        }
+#pragma unroll
+        for (int i = 0; i < S_ITEMS; ++i) {
+          const int x = i * THREADS + tid, row = x / S_PIECES;
+#pragma unroll
+          for (int o = 1; o < S_PIECES; o <<= 1) wv[i] += __shfl_xor(wv[i], o, 64);
+          if (x % S_PIECES == 0 && row < CH) lds.wv[row] = wv[i];
         }
         f4_t kk[2], qk[2], xk[2], xq[2];  // rows i: k_i . k_j and q_i . k_j
 #pragma unroll
@@ -446,23 +508,33 @@ __global__ __launch_bounds__((GradLds<KP, Stream<T>::NP>::WAVES * 64)) void delt
 #pragma unroll
       for (int t = 0; t < 4; ++t) dq[t] = read[t] = early[t] = f4_t{0.f, 0.f, 0.f, 0.f};
       const int a_lane = Lds::at(n, g) + 64 * half * 64;
+      Op<NP> dn_next;
+      Split zn_next, wn_next;
+      const auto fetch_own = [&](int vb) {
+        const uint32_t own = 2 * (n * VP + vb + 8 * g);
+        dn_next = token_op<T, VEC>(dop, vs, tok, vb + 8 * g, Dv);
+        zn_next = zp.parts(own, 16 * w * two, vlo);
+        wn_next = wp.parts(own, 16 * w * two, vlo);
+      };
+      fetch_own(0);
       for (int vb = 0; vb < VP; vb += 32) {
-        const int v0 = vb + 8 * g;
-        const uint32_t own = 2 * (n * VP + v0);
-        char *mb = lds.block[0][0], *nb = lds.block[Lds::BLOCKS - 1][0];
+        char *mb = lds.block, *nb = lds.block + (Lds::BLOCKS - 1) * 2 * Lds::PART;
         *reinterpret_cast<bf8_t*>(mb + b_at) = mr.hi;
         *reinterpret_cast<bf8_t*>(mb + Lds::PART + b_at) = mr.lo;
         if (Lds::BLOCKS == 2) {
           *reinterpret_cast<bf8_t*>(nb + b_at) = nr.hi;
           *reinterpret_cast<bf8_t*>(nb + Lds::PART + b_at) = nr.lo;
         }
-        const Op<NP> dn = token_op<T, VEC>(dop, vs, tok, v0, Dv);
-        const Split zn = zp.parts(own, 16 * w * two, vlo), wn = wp.parts(own, 16 * w * two, vlo);
+        const Op<NP> dn = dn_next;
+        const Split zn = zn_next, wn = wn_next;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           mn += ((float)mr.hi[e] + (float)mr.lo[e]) * ((float)nr.hi[e] + (float)nr.lo[e]);
         const Split last = nr;
-        if (vb + 32 < VP) fetch(vb + 32);
+        if (vb + 32 < VP) {
+          fetch(vb + 32);
+          fetch_own(vb + 32);
+        }
         lds_barrier();
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -493,12 +565,14 @@ __global__ __launch_bounds__((GradLds<KP, Stream<T>::NP>::WAVES * 64)) void delt
       for (int t2 = 0; t2 < 2; ++t2) {
         float kf[8], qf[8];
         {
-          const int k0 = key0 + 32 * t2 + 8 * g;
-          Raw8<T> kraw, qraw;
-          kraw.template load<VEC>(k, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0);
-          qraw.template load<VEC>(q, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0);
-          kraw.open(kf);
-          qraw.open(qf);
+          const int o = Tk::at(place_of(tok), (key0 >> 3) + 4 * t2 + g);
+          const bf8_t k8 = *reinterpret_cast<const bf8_t*>(lds.k[0] + o), q8 = *reinterpret_cast<const bf8_t*>(lds.q[0] + o);
+          const bf8_t kl = *reinterpret_cast<const bf8_t*>(lds.k[NP - 1] + o), ql = *reinterpret_cast<const bf8_t*>(lds.q[NP - 1] + o);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            kf[e] = (float)k8[e] + (NP == 2 ? (float)kl[e] : 0.f);
+            qf[e] = (float)q8[e] + (NP == 2 ? (float)ql[e] : 0.f);
+          }
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -536,7 +610,7 @@ __global__ __launch_bounds__((GradLds<KP, Stream<T>::NP>::WAVES * 64)) void delt
       // in beta. <M, N> and the ends' sum are the chunk's.
       qdq = sum_groups(qdq);
       db = sum_groups(db);
-      const float own = pass == 0 ? sum_groups(own_wz - wv) : 0.f;
+      const float own = pass == 0 ? sum_groups(own_wz) : 0.f;
       const float ends = wave_sum(at_end + expf((float)Gend) * mn);
       if (g == 0) {
         lds.qdq[half][tok] = qdq;
@@ -546,7 +620,7 @@ __global__ __launch_bounds__((GradLds<KP, Stream<T>::NP>::WAVES * 64)) void delt
       if (lane == 0) lds.end[wave] = ends;
       lds_barrier();
       if (tid < CH) {
-        float dbeta = lds.db[0][tid], s = lds.qdq[0][tid] + lds.own[tid];
+        float dbeta = lds.db[0][tid], s = lds.qdq[0][tid] + (pass == 0 ? lds.own[tid] - lds.wv[tid] : 0.f);
         if (Lds::HALVES == 2) dbeta += lds.db[Lds::HALVES - 1][tid], s += lds.qdq[Lds::HALVES - 1][tid];
         s -= lds.beta[tid] * dbeta;
 #pragma unroll
