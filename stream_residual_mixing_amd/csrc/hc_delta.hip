@@ -71,8 +71,8 @@ __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
     G[i] = s;
     beta_s[i] = be;
     float* dec = (float*)(out + REC_DEC);
-    dec[DEC_AHEAD + i] = expf((float)s);
-    dec[DEC_TO_END + i] = expf((float)(end - s));
+    dec[DEC_AHEAD + i] = decay(s);
+    dec[DEC_TO_END + i] = decay(end - s);
     dec[DEC_BETA + i] = be;
   }
   lds_barrier();
@@ -87,7 +87,7 @@ __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
       f4_t l;
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const float d = j0 + r <= i ? expf((float)(Gi - G[j0 + r])) : 0.f;
+        const float d = j0 + r <= i ? decay(Gi - G[j0 + r]) : 0.f;
         p[t >> 1][4 * (t & 1) + r] = j0 + r <= i ? d * qk[t][r] : 0.f;
         l[r] = j0 + r < i ? d * kk[t][r] * beta_s[j0 + r] : 0.f;
       }
@@ -108,7 +108,7 @@ __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
       const int i0 = 32 * (t >> 1) + 8 * g + 4 * (t & 1);
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        p[t >> 1][4 * (t & 1) + r] = j <= i0 + r ? expf((float)(G[i0 + r] - Gj)) * kq[t][r] : 0.f;
+        p[t >> 1][4 * (t & 1) + r] = j <= i0 + r ? decay(G[i0 + r] - Gj) * kq[t][r] : 0.f;
     }
     // lane n holds P^T's row j = 16 w + n: its place in row_of's order
     const int pl = place_of(j), t = pl >> 4, to = (pl & 15) + 16 * g;

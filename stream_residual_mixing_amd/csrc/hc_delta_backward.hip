@@ -200,30 +200,30 @@ __global__ __launch_bounds__(64 * NW, 2) void delta_back_kernel(DeltaArgs a) {
 
 // ------------------------------------------------------------- each chunk by itself
 
-// Four waves' 64 tokens by 64 keys, or twice as many waves by 128 keys at a time: wider heads take two
-// passes, the second of which adds to the first's dg and dbeta.
+// What each chunk's workgroup of four waves, 16 tokens each, brings through LDS, in turn in NBUF
+// buffers: Z, W (two parts each) and dO, 64 tokens by 32 columns, and then the state and its gradient
+// (two parts each), 64 keys by 32 columns.
 template <int KP, int NP>
 struct GradLds {
-  static constexpr int HALVES = KP == 64 ? 1 : 2, WAVES = 4 * HALVES, ROWS = 64 * HALVES;
-  // Blocks of ROWS keys by 32 columns of a state in two parts, two where there is room: the state's and
-  // its gradient's in turn. In their place before that the chunk's Z and W in two parts and dO, 64
-  // tokens by SC columns at a time.
-  static constexpr int BLOCKS = KP == 256 && NP == 2 ? 1 : 2, PART = ROWS * 64;
-  static constexpr int SC = KP == 256 && NP == 2 ? 32 : 64, STAGE = CH * SC * 2;
-  static constexpr int SHARED_BYTES = BLOCKS * 2 * PART > (4 + NP) * STAGE ? BLOCKS * 2 * PART : (4 + NP) * STAGE;
+  static constexpr int PART = CH * 64, NBUF = KP == 256 && NP == 2 ? 1 : 2;  // there is no room for two
   char k[NP][Tokens<KP>::BYTES], q[NP][Tokens<KP>::BYTES];  // rows in row_of's order
-  char block[SHARED_BYTES];
+  char buf[NBUF][(4 + NP) * PART];
   double G[CH];
-  float beta[CH], own[CH], wv[CH], qdq[HALVES][CH], db[HALVES][CH], end[WAVES];
-  // a block's row in row_of's order, its four 16-byte pieces exchanged so that 16 lanes reading a piece of
+  float beta[CH], dG[CH], wv[CH], end[4];
+  // a row's place in row_of's order, its four 16-byte pieces exchanged so that 16 lanes reading a piece of
   // 16 rows reach all banks once
   static __device__ __forceinline__ int at(int place, int piece) { return place * 64 + ((piece ^ ((place >> 2) & 3)) << 4); }
-  // the same of a stage
-  static __device__ __forceinline__ int stage_at(int place, int piece) {
-    return SC == 64 ? Tokens<64>::at(place, piece) : at(place, piece);
+  static __device__ __forceinline__ bf8_t one(const char* m, int part, int at, int tile) {
+    return *reinterpret_cast<const bf8_t*>(m + part * PART + 1024 * tile + at);
   }
-  static __device__ __forceinline__ bf8_t stage(const char* m, int at, int tile, int kb) {
-    return *reinterpret_cast<const bf8_t*>(m + 16 * tile * 2 * SC + (at ^ (kb << 6)));
+  static __device__ __forceinline__ Split two(const char* m, int part, int at, int tile) {
+    return {one(m, part, at, tile), one(m, part + 1, at, tile)};
+  }
+  static __device__ __forceinline__ Op<NP> stream(const char* m, int part, int at, int tile) {
+    Op<NP> d;
+#pragma unroll
+    for (int p = 0; p < NP; ++p) d.p[p] = one(m, part + p, at, tile);
+    return d;
   }
 };
 
@@ -256,18 +256,18 @@ __device__ __forceinline__ float sum_groups(float v) {  // over the four lanes o
   return v + __shfl_xor(v, 32, 64);
 }
 
-// SHARED: several value heads read a key head.
+// SHARED: several value heads read a key head. Up to 128 keys at a time, for which there are registers:
+// wider heads take two passes, the second of which adds to the first's dg and dbeta.
 template <typename T, int KP, bool VEC, bool SHARED>
-__global__ __launch_bounds__((GradLds<KP, Stream<T>::NP>::WAVES * 64)) void delta_grad_kernel(DeltaArgs a) {
-  constexpr int NP = Stream<T>::NP, KB = KP / 32;
+__global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaArgs a) {
+  constexpr int NP = Stream<T>::NP, KB = KP / 32, QUADS = KP == 64 ? 1 : 2, PASSES = KP / 64 / QUADS;
+  constexpr int PIECES = KP / 8, ITEMS = CH * PIECES / 256;
   typedef GradLds<KP, NP> Lds;
   typedef Tokens<KP> Tk;
-  constexpr int THREADS = 64 * Lds::WAVES, ROWS = Lds::ROWS, PASSES = KP / ROWS;
-  constexpr int PIECES = KP / 8, ITEMS = CH * PIECES / THREADS;
   extern __shared__ __attribute__((aligned(16))) char lds_raw[];
   static_assert(sizeof(Lds) <= 160 * 1024, "LDS of a CU");
   Lds& lds = *reinterpret_cast<Lds*>(lds_raw);
-  const int tid = threadIdx.x, lane = tid & 63, wave = wave_number(), w = wave & 3, half = wave >> 2;
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_number(), h = w >> 1;
   int n = lane & 15, g = lane >> 4;
   const uint32_t NC = (uint32_t)a.NC, chunk = blockIdx.x % NC, bh = blockIdx.x / NC, hk = bh % (uint32_t)a.Hk;
   const int64_t b = bh / (uint32_t)a.Hk, t0 = (int64_t)chunk * CH, tokens = length_of(a.lengths, b, a.S) - t0;
@@ -275,24 +275,40 @@ __global__ __launch_bounds__((GradLds<KP, Stream<T>::NP>::WAVES * 64)) void delt
   const int Dk = (int)a.Dk, Dv = (int)a.Dv, VP = (int)a.VP, qs = (int)a.Hk * Dk, vs = (int)a.Hv * Dv;
   const int per = (int)((uint32_t)a.Hv / (uint32_t)a.Hk);
   const int64_t keys = (b * a.S + t0) * qs + hk * Dk;
-  const Range q = head_rows((const T*)a.q + keys, left, qs, Dk), k = head_rows((const T*)a.k + keys, left, qs, Dk);
+  {
+    const Range q = head_rows((const T*)a.q + keys, left, qs, Dk), k = head_rows((const T*)a.k + keys, left, qs, Dk);
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-    const int x = i * THREADS + tid, piece = x % PIECES, row = x / PIECES;
-    const Op<NP> ko = token_op<T, VEC>(k, qs, row, 8 * piece, Dk), qo = token_op<T, VEC>(q, qs, row, 8 * piece, Dk);
+    for (int i = 0; i < ITEMS; ++i) {
+      const int x = i * 256 + tid, piece = x % PIECES, row = x / PIECES;
+      const Op<NP> ko = token_op<T, VEC>(k, qs, row, 8 * piece, Dk), qo = token_op<T, VEC>(q, qs, row, 8 * piece, Dk);
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      const int at = Tk::at(place_of(row), piece);
-      *reinterpret_cast<bf8_t*>(lds.k[p] + at) = ko.p[p];
-      *reinterpret_cast<bf8_t*>(lds.q[p] + at) = qo.p[p];
+      for (int p = 0; p < NP; ++p) {
+        const int at = Tk::at(place_of(row), piece);
+        *reinterpret_cast<bf8_t*>(lds.k[p] + at) = ko.p[p];
+        *reinterpret_cast<bf8_t*>(lds.q[p] + at) = qo.p[p];
+      }
     }
   }
+  const Range dqp = head_rows((T*)a.dq + keys, rows, qs, Dk), dkp = head_rows((T*)a.dk + keys, rows, qs, Dk);
+  const auto put = [&](int tok, int key0, const f4_t* dq, const f4_t* dk) {  // 64 keys of the wave's tokens
+#pragma unroll
+    for (int t2 = 0; t2 < 2; ++t2) {
+      const int k0 = key0 + 32 * t2 + 8 * g;
+      float vq[8], vk[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        vq[e] = tok < left ? dq[2 * t2 + (e >> 2)][e & 3] : 0.f;
+        vk[e] = tok < left ? dk[2 * t2 + (e >> 2)][e & 3] : 0.f;
+      }
+      put_row8<VEC>((T*)nullptr, dqp, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0, vq);
+      put_row8<VEC>((T*)nullptr, dkp, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0, vk);
+    }
+  };
 #pragma unroll 1
   for (int pass = 0; pass < PASSES; ++pass) {
-    const int key0 = ROWS * pass + 64 * half;  // the wave's 64 keys
-    f4_t dqt[4], dkt[4];
+    f4_t dqt[4 * QUADS], dkt[4 * QUADS];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) dqt[t] = dkt[t] = f4_t{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < 4 * QUADS; ++t) dqt[t] = dkt[t] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
     for (int hi = 0; hi < per; ++hi) {
       renew(n, g);
@@ -308,141 +324,97 @@ __global__ __launch_bounds__((GradLds<KP, Stream<T>::NP>::WAVES * 64)) void delt
         lds.G[tid] = running_sum(on ? clamp_decay(a.g[gat + tid * a.Hv]) : 0.0, tid);
         lds.beta[tid] = on ? a.beta[gat + tid * a.Hv] : 0.f;
       }
-      // the states' first blocks on their way: a thread has eight columns of a row of each
-      const Range mp((const bf16_t*)a.states + at * 2 * KP * VP, 4 * KP * VP);
-      const Range np((const bf16_t*)a.dstates + at * 2 * KP * VP, 4 * KP * VP);
       const uint32_t two = 2 * VP, vlo = CH * two, slo = KP * two;
-      const int b_row = tid >> 2, b_piece = tid & 3, b_at = Lds::at(place_of(b_row), b_piece);
-      const uint32_t b_lane = 2 * ((ROWS * pass + b_row) * VP + 8 * b_piece);
-      Split mr, nr;
-      const auto fetch = [&](int vb) {
-        mr = mp.parts(b_lane, 2 * vb, slo);
-        nr = np.parts(b_lane, 2 * vb, slo);
-      };
       const Range dop = head_rows((const T*)a.d_o + (b * a.S + t0) * vs + hv * Dv, left, vs, Dv);
       const Range vp = head_rows((const T*)a.v + (b * a.S + t0) * vs + hv * Dv, left, vs, Dv);
       const Range zp((const bf16_t*)a.z + at * 2 * CH * VP, 4 * CH * VP);
       const Range wp((const bf16_t*)a.w + at * 2 * CH * VP, 4 * CH * VP);
-      // and the first columns of Z, W, dO and V
-      constexpr int SC = Lds::SC, S_PIECES = SC / 8, S_ITEMS = (CH * S_PIECES + THREADS - 1) / THREADS;
-      Split zs[S_ITEMS], ws[S_ITEMS];
-      Raw8<T> ds[S_ITEMS], vr[S_ITEMS];
-      float wv[S_ITEMS];
-      const auto fetch_stage = [&](int vb) {
-#pragma unroll
-        for (int i = 0; i < S_ITEMS; ++i) {
-          const int x = i * THREADS + tid, row = x / S_PIECES, c = vb + 8 * (x % S_PIECES);
-          const uint32_t o = c < VP ? 2 * (row * VP + c) : NOWHERE;
-          zs[i] = zp.parts(o, 0, vlo);
-          ws[i] = wp.parts(o, 0, vlo);
-          ds[i].template load<VEC>(dop, (row * vs + c) * (uint32_t)sizeof(T), Dv - c);
-          vr[i].template load<VEC>(vp, (row * vs + c) * (uint32_t)sizeof(T), Dv - c);
-        }
-      };
-      fetch_stage(0);
-      fetch(0);
-#pragma unroll
-      for (int i = 0; i < S_ITEMS; ++i) wv[i] = 0.f;
-      lds_barrier();
-      const double Gn = lds.G[tok];
-      const float beta_n = lds.beta[tok];
+      // a thread brings eight columns of a row of each array
+      const int m_row = tid >> 2, m_col = 8 * (tid & 3), m_at = Lds::at(place_of(m_row), tid & 3);
+      const int own_at = Lds::at(place_of(tok), g), rows_at = Lds::at(n, g);
 
       // What each pair of tokens passes on. The wave's tokens lie in half h of the chunk; with those of the
       // same half a token is the earlier or the later one, with the other half's only one of them.
       // Lane j = tok. Rows i >= j: B_ij and A_ij (it is the earlier one); rows j' <= tok: B and A of
       // (tok, j'), the later one. As operands: bq by K for dQ, bk by Q and aa by K for dK; x is the
-      // other half's bk (h = 0) or bq (h = 1).
-      const int h = w >> 1;
+      // other half's bk (h = 0) or bq (h = 1), ax its aa.
       float db = 0.f, own_wz = 0.f;
       Split bq, bk, aa, x, ax;
       {
+        Split zs, ws;
+        Raw8<T> ds, vr;
+        const auto fetch = [&](int vb) {
+          const uint32_t o = 2 * (m_row * VP + vb + m_col);
+          zs = zp.parts(o, 0, vlo);
+          ws = wp.parts(o, 0, vlo);
+          ds.template load<VEC>(dop, (m_row * vs + vb + m_col) * (uint32_t)sizeof(T), Dv - vb - m_col);
+          vr.template load<VEC>(vp, (m_row * vs + vb + m_col) * (uint32_t)sizeof(T), Dv - vb - m_col);
+        };
         f4_t zd[2], zw[2], dz[2], wz[2];  // Z_row . dO, Z_row . W, dO_row . Z, W_row . Z with the wave's tokens
         f4_t xd[2], xw[2];                // the other half's: the last two (h = 0) or the first two
 #pragma unroll
         for (int t = 0; t < 2; ++t) zd[t] = zw[t] = dz[t] = wz[t] = xd[t] = xw[t] = f4_t{0.f, 0.f, 0.f, 0.f};
-        const int own_s = Lds::stage_at(place_of(tok), g), rows_s = Lds::stage_at(n, g);
-        for (int vb = 0; vb < VP; vb += SC) {
-          char* st = lds.block;
+        float wv = 0.f;  // W . v
+        fetch(0);
+        for (int vb = 0, i = 0; vb < VP; vb += 32, i ^= 1) {
+          char* m = lds.buf[Lds::NBUF == 2 ? i : 0];
+          {
+            const Op<NP> d = ds.op();
+            *reinterpret_cast<bf8_t*>(m + m_at) = zs.hi;
+            *reinterpret_cast<bf8_t*>(m + Lds::PART + m_at) = zs.lo;
+            *reinterpret_cast<bf8_t*>(m + 2 * Lds::PART + m_at) = ws.hi;
+            *reinterpret_cast<bf8_t*>(m + 3 * Lds::PART + m_at) = ws.lo;
 #pragma unroll
-          for (int i = 0; i < S_ITEMS; ++i) {
-            const int x = i * THREADS + tid, row = x / S_PIECES, o = Lds::stage_at(place_of(row), x % S_PIECES);
-            if (CH * S_PIECES % THREADS == 0 || row < CH) {
-              const Op<NP> d = ds[i].op();
-              *reinterpret_cast<bf8_t*>(st + o) = zs[i].hi;
-              *reinterpret_cast<bf8_t*>(st + Lds::STAGE + o) = zs[i].lo;
-              *reinterpret_cast<bf8_t*>(st + 2 * Lds::STAGE + o) = ws[i].hi;
-              *reinterpret_cast<bf8_t*>(st + 3 * Lds::STAGE + o) = ws[i].lo;
-#pragma unroll
-              for (int p = 0; p < NP; ++p) *reinterpret_cast<bf8_t*>(st + (4 + p) * Lds::STAGE + o) = d.p[p];
-            }
+            for (int p = 0; p < NP; ++p) *reinterpret_cast<bf8_t*>(m + (4 + p) * Lds::PART + m_at) = d.p[p];
             float vf[8];
-            vr[i].open(vf);
+            vr.open(vf);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) wv[i] += vf[e] * ((float)ws[i].hi[e] + (float)ws[i].lo[e]);
+            for (int e = 0; e < 8; ++e) wv += vf[e] * ((float)ws.hi[e] + (float)ws.lo[e]);
           }
-          if (vb + SC < VP) fetch_stage(vb + SC);
+          if (vb + 32 < VP) fetch(vb + 32);
           lds_barrier();
-          const auto z_at = [&](int o, int tile, int kb) -> Split {
-            return {Lds::stage(st, o, tile, kb), Lds::stage(st + Lds::STAGE, o, tile, kb)};
-          };
-          const auto w_at = [&](int o, int tile, int kb) -> Split {
-            return {Lds::stage(st + 2 * Lds::STAGE, o, tile, kb), Lds::stage(st + 3 * Lds::STAGE, o, tile, kb)};
-          };
-          const auto d_at = [&](int o, int tile, int kb) {
-            Op<NP> d;
+          const Op<NP> dn = Lds::stream(m, 4, own_at, 0);
+          const Split zn = Lds::two(m, 0, own_at, 0), wn = Lds::two(m, 2, own_at, 0);
 #pragma unroll
-            for (int p = 0; p < NP; ++p) d.p[p] = Lds::stage(st + (4 + p) * Lds::STAGE, o, tile, kb);
-            return d;
-          };
-#pragma unroll
-          for (int kb = 0; kb < SC / 32; ++kb) {
-            const Op<NP> dn = d_at(own_s, 0, kb);
-            const Split zn = z_at(own_s, 0, kb), wn = w_at(own_s, 0, kb);
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const int r = 2 * h + t, o = 2 - 2 * h + t;
-              const Split zr = z_at(rows_s, r, kb);
-              zd[t] = mma(zr, dn, zd[t]);
-              zw[t] = mma(zr, wn, zw[t]);
-              dz[t] = mma(d_at(rows_s, r, kb), zn, dz[t]);
-              wz[t] = mma(w_at(rows_s, r, kb), zn, wz[t]);
-              if (h == 0) {
-                xd[t] = mma(d_at(rows_s, o, kb), zn, xd[t]);
-                xw[t] = mma(w_at(rows_s, o, kb), zn, xw[t]);
-              } else {
-                const Split zo = z_at(rows_s, o, kb);
-                xd[t] = mma(zo, dn, xd[t]);
-                xw[t] = mma(zo, wn, xw[t]);
-              }
+          for (int t = 0; t < 2; ++t) {
+            const int r = 2 * h + t, o = 2 - 2 * h + t;
+            const Split zr = Lds::two(m, 0, rows_at, r);
+            zd[t] = mma(zr, dn, zd[t]);
+            zw[t] = mma(zr, wn, zw[t]);
+            dz[t] = mma(Lds::stream(m, 4, rows_at, r), zn, dz[t]);
+            wz[t] = mma(Lds::two(m, 2, rows_at, r), zn, wz[t]);
+            if (h == 0) {
+              xd[t] = mma(Lds::stream(m, 4, rows_at, o), zn, xd[t]);
+              xw[t] = mma(Lds::two(m, 2, rows_at, o), zn, xw[t]);
+            } else {
+              const Split zo = Lds::two(m, 0, rows_at, o);
+              xd[t] = mma(zo, dn, xd[t]);
+              xw[t] = mma(zo, wn, xw[t]);
             }
-            keep_order();
           }
-          lds_barrier();
+          if (Lds::NBUF == 1) lds_barrier();
         }
-#pragma unroll
-        for (int i = 0; i < S_ITEMS; ++i) {
-          const int x = i * THREADS + tid, row = x / S_PIECES;
-#pragma unroll
-          for (int o = 1; o < S_PIECES; o <<= 1) wv[i] += __shfl_xor(wv[i], o, 64);
-          if (x % S_PIECES == 0 && row < CH) lds.wv[row] = wv[i];
-        }
+        wv += __shfl_xor(wv, 1, 64);
+        wv += __shfl_xor(wv, 2, 64);
+        if ((tid & 3) == 0) lds.wv[m_row] = wv;
+        keep_order();
         f4_t kk[2], qk[2], xk[2], xq[2];  // rows i: k_i . k_j and q_i . k_j
 #pragma unroll
         for (int t = 0; t < 2; ++t) kk[t] = qk[t] = xk[t] = xq[t] = f4_t{0.f, 0.f, 0.f, 0.f};
-        if (pass == 0 && half == 0) {
-          const int rows_at = Tk::lane_at(n, g) + 32 * h * Tk::ROW, own_at = Tk::at(place_of(tok), g);
+        if (pass == 0) {
+          const int k_rows = Tk::lane_at(n, g) + 32 * h * Tk::ROW, k_own = Tk::at(place_of(tok), g);
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb) {
             Op<NP> kn;
 #pragma unroll
-            for (int p = 0; p < NP; ++p) kn.p[p] = *reinterpret_cast<const bf8_t*>(lds.k[p] + (own_at ^ (kb << 6)));
+            for (int p = 0; p < NP; ++p) kn.p[p] = *reinterpret_cast<const bf8_t*>(lds.k[p] + (k_own ^ (kb << 6)));
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               Op<NP> ka, qa;
 #pragma unroll
               for (int p = 0; p < NP; ++p) {
-                ka.p[p] = Tk::rows(lds.k[p], rows_at, t, kb);
-                qa.p[p] = Tk::rows(lds.q[p], rows_at, t, kb);
+                ka.p[p] = Tk::rows(lds.k[p], k_rows, t, kb);
+                qa.p[p] = Tk::rows(lds.q[p], k_rows, t, kb);
               }
               kk[t] = mma(ka, kn, kk[t]);
               qk[t] = mma(qa, kn, qk[t]);
@@ -453,8 +425,8 @@ __global__ __launch_bounds__((GradLds<KP, Stream<T>::NP>::WAVES * 64)) void delt
                 Op<NP> ka, qa;
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
-                  ka.p[p] = Tk::rows(lds.k[p], rows_at, 2 + t, kb);
-                  qa.p[p] = Tk::rows(lds.q[p], rows_at, 2 + t, kb);
+                  ka.p[p] = Tk::rows(lds.k[p], k_rows, 2 + t, kb);
+                  qa.p[p] = Tk::rows(lds.q[p], k_rows, 2 + t, kb);
                 }
                 xk[t] = mma(ka, kn, xk[t]);
                 xq[t] = mma(qa, kn, xq[t]);
@@ -463,6 +435,8 @@ __global__ __launch_bounds__((GradLds<KP, Stream<T>::NP>::WAVES * 64)) void delt
             keep_order();
           }
         }
+        const double Gn = lds.G[tok];
+        const float beta_n = lds.beta[tok];
         float vq[8], vk[8], va[8];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -472,7 +446,7 @@ __global__ __launch_bounds__((GradLds<KP, Stream<T>::NP>::WAVES * 64)) void delt
           for (int r = 0; r < 4; ++r) {
             const int row = r0 + r;
             const double G = lds.G[row];
-            const float d = expf((float)(row >= tok ? G - Gn : Gn - G));
+            const float d = decay(row >= tok ? G - Gn : Gn - G);
             const float bz = row >= tok ? a.scale * d * dz[t][r] : 0.f, az = row > tok ? -d * wz[t][r] : 0.f;
             vq[4 * t + r] = row <= tok ? a.scale * beta[r] * d * zd[t][r] : 0.f;
             vk[4 * t + r] = beta_n * bz;
@@ -484,6 +458,9 @@ __global__ __launch_bounds__((GradLds<KP, Stream<T>::NP>::WAVES * 64)) void delt
         bq = split(vq);
         bk = split(vk);
         aa = split(va);
+        pin(bq);
+        pin(bk);
+        pin(aa);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int r0 = 32 - 32 * h + 8 * g + 4 * t;
@@ -491,7 +468,7 @@ __global__ __launch_bounds__((GradLds<KP, Stream<T>::NP>::WAVES * 64)) void delt
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const double G = lds.G[r0 + r];
-            const float d = expf((float)(h == 0 ? G - Gn : Gn - G));
+            const float d = decay(h == 0 ? G - Gn : Gn - G);
             const float bx = a.scale * d * xd[t][r], axx = -d * xw[t][r], be = h == 0 ? beta_n : beta[r];
             if (h == 0) db += bx * xq[t][r] + axx * xk[t][r];
             vq[4 * t + r] = be * bx;
@@ -500,158 +477,137 @@ __global__ __launch_bounds__((GradLds<KP, Stream<T>::NP>::WAVES * 64)) void delt
         }
         x = split(vq);
         ax = split(va);
+        pin(x);
+        pin(ax);
         keep_order();
       }
-      // what the states pass on, the wave's 64 keys by 32 columns at a time
-      f4_t dq[4], read[4], early[4];
-      float mn = 0.f;  // <M, N>
-#pragma unroll
-      for (int t = 0; t < 4; ++t) dq[t] = read[t] = early[t] = f4_t{0.f, 0.f, 0.f, 0.f};
-      const int a_lane = Lds::at(n, g) + 64 * half * 64;
+      // What the states pass on, 64 keys at a time.
+      const Range mp((const bf16_t*)a.states + at * 2 * KP * VP, 4 * KP * VP);
+      const Range np((const bf16_t*)a.dstates + at * 2 * KP * VP, 4 * KP * VP);
+      Split mr, nr, zn_next, wn_next;
       Op<NP> dn_next;
-      Split zn_next, wn_next;
-      const auto fetch_own = [&](int vb) {
-        const uint32_t own = 2 * (n * VP + vb + 8 * g);
+      const auto fetch = [&](int key0, int vb) {
+        const uint32_t o = 2 * (m_row * VP + m_col), s = 2 * (key0 * VP + vb), own = 2 * (n * VP + vb + 8 * g);
+        mr = mp.parts(o, s, slo);
+        nr = np.parts(o, s, slo);
         dn_next = token_op<T, VEC>(dop, vs, tok, vb + 8 * g, Dv);
         zn_next = zp.parts(own, 16 * w * two, vlo);
         wn_next = wp.parts(own, 16 * w * two, vlo);
       };
-      fetch_own(0);
-      for (int vb = 0; vb < VP; vb += 32) {
-        char *mb = lds.block, *nb = lds.block + (Lds::BLOCKS - 1) * 2 * Lds::PART;
-        *reinterpret_cast<bf8_t*>(mb + b_at) = mr.hi;
-        *reinterpret_cast<bf8_t*>(mb + Lds::PART + b_at) = mr.lo;
-        if (Lds::BLOCKS == 2) {
-          *reinterpret_cast<bf8_t*>(nb + b_at) = nr.hi;
-          *reinterpret_cast<bf8_t*>(nb + Lds::PART + b_at) = nr.lo;
-        }
-        const Op<NP> dn = dn_next;
-        const Split zn = zn_next, wn = wn_next;
+      fetch(64 * QUADS * pass, 0);
+      const double Gend = lds.G[CH - 1], Gown = lds.G[tok];
+      const float ahead = decay(Gown), to_end = decay(Gend - Gown), eb = to_end * lds.beta[tok];
+      float mn = 0.f, qdq = 0.f, at_end = 0.f;  // <M, N>; q . dq; k . (N Z) to the chunk's end
+      lds_barrier();  // the buffers held Z, W and dO until here
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          mn += ((float)mr.hi[e] + (float)mr.lo[e]) * ((float)nr.hi[e] + (float)nr.lo[e]);
-        const Split last = nr;
-        if (vb + 32 < VP) {
-          fetch(vb + 32);
-          fetch_own(vb + 32);
-        }
-        lds_barrier();
+      for (int quad = 0; quad < QUADS; ++quad) {
+        const int key0 = 64 * (QUADS * pass + quad);
+        f4_t dq[4], read[4], early[4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const char* p = mb + a_lane + 1024 * t;
-          const Split m = {*reinterpret_cast<const bf8_t*>(p), *reinterpret_cast<const bf8_t*>(p + Lds::PART)};
-          dq[t] = mma(m, dn, dq[t]);
-          read[t] = mma(m, wn, read[t]);
-        }
-        if (Lds::BLOCKS == 1) {
+        for (int t = 0; t < 4; ++t) dq[t] = read[t] = early[t] = f4_t{0.f, 0.f, 0.f, 0.f};
+        for (int vb = 0, i = 0; vb < VP; vb += 32, i ^= 1) {
+          char* m = lds.buf[Lds::NBUF == 2 ? i : 0];
+          *reinterpret_cast<bf8_t*>(m + m_at) = mr.hi;
+          *reinterpret_cast<bf8_t*>(m + Lds::PART + m_at) = mr.lo;
+          *reinterpret_cast<bf8_t*>(m + 2 * Lds::PART + m_at) = nr.hi;
+          *reinterpret_cast<bf8_t*>(m + 3 * Lds::PART + m_at) = nr.lo;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            mn += ((float)mr.hi[e] + (float)mr.lo[e]) * ((float)nr.hi[e] + (float)nr.lo[e]);
+          const Op<NP> dn = dn_next;
+          const Split zn = zn_next, wn = wn_next;
+          if (vb + 32 < VP) fetch(key0, vb + 32);
+          else if (quad + 1 < QUADS) fetch(key0 + 64, 0);
           lds_barrier();
-          *reinterpret_cast<bf8_t*>(nb + b_at) = last.hi;
-          *reinterpret_cast<bf8_t*>(nb + Lds::PART + b_at) = last.lo;
-          lds_barrier();
-        }
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const char* p = nb + a_lane + 1024 * t;
-          const Split m = {*reinterpret_cast<const bf8_t*>(p), *reinterpret_cast<const bf8_t*>(p + Lds::PART)};
-          early[t] = mma(m, zn, early[t]);
-        }
-        lds_barrier();
-      }
-      const double Gend = lds.G[CH - 1];
-      const float ahead = expf((float)Gn), to_end = expf((float)(Gend - Gn)), eb = to_end * beta_n;
-      const int cols_at = Tk::lane_at_t(n, g) ^ (2 * key0);
-      float qdq = 0.f, at_end = 0.f;  // q . dq; k . (N Z) to the chunk's end
-#pragma unroll
-      for (int t2 = 0; t2 < 2; ++t2) {
-        float kf[8], qf[8];
-        {
-          const int o = Tk::at(place_of(tok), (key0 >> 3) + 4 * t2 + g);
-          const bf8_t k8 = *reinterpret_cast<const bf8_t*>(lds.k[0] + o), q8 = *reinterpret_cast<const bf8_t*>(lds.q[0] + o);
-          const bf8_t kl = *reinterpret_cast<const bf8_t*>(lds.k[NP - 1] + o), ql = *reinterpret_cast<const bf8_t*>(lds.q[NP - 1] + o);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            kf[e] = (float)k8[e] + (NP == 2 ? (float)kl[e] : 0.f);
-            qf[e] = (float)q8[e] + (NP == 2 ? (float)ql[e] : 0.f);
+          for (int t = 0; t < 4; ++t) {
+            const Split ms = Lds::two(m, 0, rows_at, t), ns = Lds::two(m, 2, rows_at, t);
+            dq[t] = mma(ms, dn, dq[t]);
+            read[t] = mma(ms, wn, read[t]);
+            early[t] = mma(ns, zn, early[t]);
           }
+          if (Lds::NBUF == 1) lds_barrier();
         }
+        if (Lds::NBUF == 2 && (VP & 32)) lds_barrier();  // an odd number of steps: the next one takes the same buffer
+        const int cols_at = Tk::lane_at_t(n, g) ^ (2 * key0);
+        f4_t dk[4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int t = 2 * t2 + u;
-          float ke = 0.f;
+        for (int t2 = 0; t2 < 2; ++t2) {
+          float kf[8], qf[8];
+          {
+            const int o = Tk::at(place_of(tok), (key0 >> 3) + 4 * t2 + g);
+            const bf8_t k0 = *reinterpret_cast<const bf8_t*>(lds.k[0] + o), q0 = *reinterpret_cast<const bf8_t*>(lds.q[0] + o);
+            const bf8_t k1 = *reinterpret_cast<const bf8_t*>(lds.k[NP - 1] + o), q1 = *reinterpret_cast<const bf8_t*>(lds.q[NP - 1] + o);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) ke += kf[4 * u + r] * early[t][r];
-          db += to_end * ke;
-          at_end += eb * ke;
-          dq[t] *= a.scale * ahead;
-          f4_t dk = eb * early[t] - ahead * read[t];
-          Op<NP> ko, qo, kx, qx;
-#pragma unroll
-          for (int p = 0; p < NP; ++p) {
-            ko.p[p] = Tk::cols(lds.k[p], cols_at, t, h);
-            qo.p[p] = Tk::cols(lds.q[p], cols_at, t, h);
-            kx.p[p] = Tk::cols(lds.k[p], cols_at, t, 1 - h);
-            if (h == 0) qx.p[p] = Tk::cols(lds.q[p], cols_at, t, 1);
+            for (int e = 0; e < 8; ++e) {
+              kf[e] = (float)k0[e] + (NP == 2 ? (float)k1[e] : 0.f);
+              qf[e] = (float)q0[e] + (NP == 2 ? (float)q1[e] : 0.f);
+            }
           }
-          dq[t] = mma(ko, bq, dq[t]);
-          dk = mma(qo, bk, dk);
-          dk = mma(ko, aa, dk);
-          dk = mma(kx, ax, dk);
-          if (h == 0) dk = mma(qx, x, dk);
-          else dq[t] = mma(kx, x, dq[t]);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) qdq += qf[4 * u + r] * dq[t][r];
-          dqt[t] = SHARED ? dqt[t] + dq[t] : dq[t];
-          dkt[t] = SHARED ? dkt[t] + dk : dk;
+          for (int u = 0; u < 2; ++u) {
+            const int t = 2 * t2 + u;
+            float ke = 0.f;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) ke += kf[4 * u + r] * early[t][r];
+            db += to_end * ke;
+            at_end += eb * ke;
+            dq[t] *= a.scale * ahead;
+            dk[t] = eb * early[t] - ahead * read[t];
+            Op<NP> ko, qo, kx, qx;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) {
+              ko.p[p] = Tk::cols(lds.k[p], cols_at, t, h);
+              qo.p[p] = Tk::cols(lds.q[p], cols_at, t, h);
+              kx.p[p] = Tk::cols(lds.k[p], cols_at, t, 1 - h);
+              if (h == 0) qx.p[p] = Tk::cols(lds.q[p], cols_at, t, 1);
+            }
+            dq[t] = mma(ko, bq, dq[t]);
+            dk[t] = mma(qo, bk, dk[t]);
+            dk[t] = mma(ko, aa, dk[t]);
+            dk[t] = mma(kx, ax, dk[t]);
+            if (h == 0) dk[t] = mma(qx, x, dk[t]);
+            else dq[t] = mma(kx, x, dq[t]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) qdq += qf[4 * u + r] * dq[t][r];
+            if (SHARED) {
+              dqt[4 * quad + t] += dq[t];
+              dkt[4 * quad + t] += dk[t];
+            }
+          }
+          keep_order();
         }
-        keep_order();
+        if (!SHARED) put(tok, key0, dq, dk);
       }
       // A token's part of the decays' sums: dO . o = q . dq for what it reads with q,
       // k . dk as it reads = W . (Z - v), and k . dk as it is written = beta dbeta, which is linear in k as
       // in beta. <M, N> and the ends' sum are the chunk's.
-      qdq = sum_groups(qdq);
       db = sum_groups(db);
-      const float own = pass == 0 ? sum_groups(own_wz) : 0.f;
-      const float ends = wave_sum(at_end + expf((float)Gend) * mn);
+      const float dot = sum_groups(pass == 0 ? qdq + own_wz : qdq) - lds.beta[tok] * db - (pass == 0 ? lds.wv[tok] : 0.f);
+      const float ends = wave_sum(at_end + decay(Gend) * mn);
       if (g == 0) {
-        lds.qdq[half][tok] = qdq;
-        lds.db[half][tok] = db;
-        if (half == 0) lds.own[tok] = own;
+        lds.dG[tok] = dot;
+        float* p = a.dbeta + gat + tok * a.Hv;
+        if (tok < rows) *p = tok < left ? (pass ? *p + db : db) : 0.f;
       }
-      if (lane == 0) lds.end[wave] = ends;
+      if (lane == 0) lds.end[w] = ends;
       lds_barrier();
       if (tid < CH) {
-        float dbeta = lds.db[0][tid], s = lds.qdq[0][tid] + (pass == 0 ? lds.own[tid] - lds.wv[tid] : 0.f);
-        if (Lds::HALVES == 2) dbeta += lds.db[Lds::HALVES - 1][tid], s += lds.qdq[Lds::HALVES - 1][tid];
-        s -= lds.beta[tid] * dbeta;
+        float s = lds.dG[tid];
 #pragma unroll
         for (int o = 1; o < CH; o <<= 1) {
           const float down = __shfl_down(s, o, 64);
           if (tid + o < CH) s += down;
         }
-#pragma unroll
-        for (int i = 0; i < Lds::WAVES; ++i) s += lds.end[i];
-        float *pb = a.dbeta + gat + tid * a.Hv, *pg = a.dg + gat + tid * a.Hv;
-        if (tid < rows) {
-          *pb = tid < left ? (pass ? *pb + dbeta : dbeta) : 0.f;
-          *pg = tid < left ? (pass ? *pg + s : s) : 0.f;
-        }
+        s += (lds.end[0] + lds.end[1]) + (lds.end[2] + lds.end[3]);
+        float* p = a.dg + gat + tid * a.Hv;
+        if (tid < rows) *p = tid < left ? (pass ? *p + s : s) : 0.f;
       }
       lds_barrier();
     }
-    const int tok = 16 * w + n;
-    const Range dqp = head_rows((T*)a.dq + keys, rows, qs, Dk), dkp = head_rows((T*)a.dk + keys, rows, qs, Dk);
+    if (SHARED || left == 0)
 #pragma unroll
-    for (int t2 = 0; t2 < 2; ++t2) {
-      const int k0 = key0 + 32 * t2 + 8 * g;
-      float vq[8], vk[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        vq[e] = tok < left ? dqt[2 * t2 + (e >> 2)][e & 3] : 0.f;
-        vk[e] = tok < left ? dkt[2 * t2 + (e >> 2)][e & 3] : 0.f;
-      }
-      put_row8<VEC>((T*)nullptr, dqp, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0, vq);
-      put_row8<VEC>((T*)nullptr, dkp, (tok * qs + k0) * (uint32_t)sizeof(T), Dk - k0, vk);
-    }
+      for (int quad = 0; quad < QUADS; ++quad) put(16 * w + n, 64 * (QUADS * pass + quad), dqt + 4 * quad, dkt + 4 * quad);
   }
 }
 
@@ -677,7 +633,7 @@ hipError_t back_go(const DeltaArgs& a, hipStream_t st) {
 template <typename T, int KP>
 hipError_t grad_go(const DeltaArgs& a, hipStream_t st) {
   typedef GradLds<KP, Stream<T>::NP> Lds;
-  const unsigned grid = (unsigned)(a.B * a.Hk * a.NC), block = 64 * Lds::WAVES;
+  const unsigned grid = (unsigned)(a.B * a.Hk * a.NC), block = 256;
   if (a.Hv == a.Hk)
     return a.vec8 ? with_lds(delta_grad_kernel<T, KP, true, false>, sizeof(Lds), grid, block, a, st)
                   : with_lds(delta_grad_kernel<T, KP, false, false>, sizeof(Lds), grid, block, a, st);

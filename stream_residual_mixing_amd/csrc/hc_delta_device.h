@@ -290,6 +290,12 @@ __device__ __forceinline__ void keep_order() {
 
 // The lane's numbers anew, so that what a loop forms of them is not kept in registers over it.
 __device__ __forceinline__ void renew(int& a, int& b) { asm volatile("" : "+v"(a), "+v"(b)); }
+// The operand is formed here, not where it is used.
+__device__ __forceinline__ void pin(Split& s) {
+  u4_t h = __builtin_bit_cast(u4_t, s.hi), l = __builtin_bit_cast(u4_t, s.lo);
+  asm volatile("" : "+v"(h), "+v"(l));
+  s = {as_bf8(h), as_bf8(l)};
+}
 __device__ __forceinline__ uint32_t anew(uint32_t a) {
   asm volatile("" : "+v"(a));
   return a;
@@ -367,6 +373,10 @@ __device__ __forceinline__ void keep_rows(bf16_t* p, int stride, int col, int n,
 // neighbours must not carry the rounding of a long sum. Below -200 a decay is 0 in float32
 // whatever it is added to, so that -inf (a fresh start) stays a number here.
 __device__ __forceinline__ double clamp_decay(float g) { return g < -200.f ? -200.0 : (double)g; }
+
+// exp(x) of a difference of the sums, off by |x| 2^-23 of itself at most: below what the products that
+// it enters leave of it until exp(x) is 1e-27.
+__device__ __forceinline__ float decay(double x) { return __builtin_amdgcn_exp2f((float)x * 1.44269504f); }
 
 // The running sum over a wave of 64 tokens.
 __device__ __forceinline__ double running_sum(double s, int i) {
