@@ -201,28 +201,33 @@ __global__ __launch_bounds__(64 * NW, 2) void delta_back_kernel(DeltaArgs a) {
 // ------------------------------------------------------------- each chunk by itself
 
 // What each chunk's workgroup of four waves, 16 tokens each, brings through LDS, in turn in NBUF
-// buffers: Z, W (two parts each) and dO, 64 tokens by 32 columns, and then the state and its gradient
-// (two parts each), 64 keys by 32 columns.
+// buffers: Z, W (two parts each) and dO, 64 tokens by COLS columns, and then the state and its gradient
+// (two parts each), 64 keys by COLS columns. Each step waits for memory once: steps of 32 columns took
+// 27 us a head of 128 x 128.
 template <int KP, int NP>
 struct GradLds {
-  static constexpr int PART = CH * 64, NBUF = KP == 256 && NP == 2 ? 1 : 2;  // there is no room for two
+  static constexpr int COLS = KP == 256 && NP == 2 ? 32 : 64, PIECES = COLS / 8, PART = CH * COLS * 2;
+  static constexpr int NBUF = (KP == 64 ? 1 : KP / 64) * NP <= 4 && !(KP == 128 && NP == 2) ? 2 : 1;  // as there is room
   char k[NP][Tokens<KP>::BYTES], q[NP][Tokens<KP>::BYTES];  // rows in row_of's order
   char buf[NBUF][(4 + NP) * PART];
   double G[CH];
   float beta[CH], dG[CH], wv[CH], end[4];
-  // a row's place in row_of's order, its four 16-byte pieces exchanged so that 16 lanes reading a piece of
-  // 16 rows reach all banks once
-  static __device__ __forceinline__ int at(int place, int piece) { return place * 64 + ((piece ^ ((place >> 2) & 3)) << 4); }
-  static __device__ __forceinline__ bf8_t one(const char* m, int part, int at, int tile) {
-    return *reinterpret_cast<const bf8_t*>(m + part * PART + 1024 * tile + at);
+  // a row's place in row_of's order, its 16-byte pieces exchanged so that 16 lanes reading a piece of 16 rows
+  // reach all banks
+  static __device__ __forceinline__ int at(int place, int piece) {
+    return COLS == 64 ? Tokens<64>::at(place, piece) : place * 64 + ((piece ^ ((place >> 2) & 3)) << 4);
   }
-  static __device__ __forceinline__ Split two(const char* m, int part, int at, int tile) {
-    return {one(m, part, at, tile), one(m, part + 1, at, tile)};
+  // an operand of tile `tile` (64-byte k block kb), the lane's own part at `at`
+  static __device__ __forceinline__ bf8_t one(const char* m, int part, int at, int tile, int kb) {
+    return *reinterpret_cast<const bf8_t*>(m + part * PART + 32 * COLS * tile + (at ^ (kb << 6)));
   }
-  static __device__ __forceinline__ Op<NP> stream(const char* m, int part, int at, int tile) {
+  static __device__ __forceinline__ Split two(const char* m, int part, int at, int tile, int kb) {
+    return {one(m, part, at, tile, kb), one(m, part + 1, at, tile, kb)};
+  }
+  static __device__ __forceinline__ Op<NP> stream(const char* m, int part, int at, int tile, int kb) {
     Op<NP> d;
 #pragma unroll
-    for (int p = 0; p < NP; ++p) d.p[p] = one(m, part + p, at, tile);
+    for (int p = 0; p < NP; ++p) d.p[p] = one(m, part + p, at, tile, kb);
     return d;
   }
 };
@@ -259,7 +264,7 @@ __device__ __forceinline__ float sum_groups(float v) {  // over the four lanes o
 // SHARED: several value heads read a key head. Up to 128 keys at a time, for which there are registers:
 // wider heads take two passes, the second of which adds to the first's dg and dbeta.
 template <typename T, int KP, bool VEC, bool SHARED>
-__global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
   constexpr int NP = Stream<T>::NP, KB = KP / 32, QUADS = KP == 64 ? 1 : 2, PASSES = KP / 64 / QUADS;
   constexpr int PIECES = KP / 8, ITEMS = CH * PIECES / 256;
   typedef GradLds<KP, NP> Lds;
@@ -329,8 +334,9 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaArgs a) {
       const Range vp = head_rows((const T*)a.v + (b * a.S + t0) * vs + hv * Dv, left, vs, Dv);
       const Range zp((const bf16_t*)a.z + at * 2 * CH * VP, 4 * CH * VP);
       const Range wp((const bf16_t*)a.w + at * 2 * CH * VP, 4 * CH * VP);
-      // a thread brings eight columns of a row of each array
-      const int m_row = tid >> 2, m_col = 8 * (tid & 3), m_at = Lds::at(place_of(m_row), tid & 3);
+      // a thread brings eight columns of a row, or of two, of each array
+      constexpr int COLS = Lds::COLS, N = COLS / 32, M_ROWS = 256 / Lds::PIECES;
+      const int m_row = tid / Lds::PIECES, m_piece = tid % Lds::PIECES, m_col = 8 * m_piece;
       const int own_at = Lds::at(place_of(tok), g), rows_at = Lds::at(n, g);
 
       // What each pair of tokens passes on. The wave's tokens lie in half h of the chunk; with those of the
@@ -341,62 +347,77 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaArgs a) {
       float db = 0.f, own_wz = 0.f;
       Split bq, bk, aa, x, ax;
       {
-        Split zs, ws;
-        Raw8<T> ds, vr;
+        Split zs[N], ws[N];
+        Raw8<T> ds[N], vr[N];
         const auto fetch = [&](int vb) {
-          const uint32_t o = 2 * (m_row * VP + vb + m_col);
-          zs = zp.parts(o, 0, vlo);
-          ws = wp.parts(o, 0, vlo);
-          ds.template load<VEC>(dop, (m_row * vs + vb + m_col) * (uint32_t)sizeof(T), Dv - vb - m_col);
-          vr.template load<VEC>(vp, (m_row * vs + vb + m_col) * (uint32_t)sizeof(T), Dv - vb - m_col);
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int row = M_ROWS * i + m_row, c = vb + m_col;
+            const uint32_t o = c < VP ? 2 * (row * VP + c) : NOWHERE;
+            zs[i] = zp.parts(o, 0, vlo);
+            ws[i] = wp.parts(o, 0, vlo);
+            ds[i].template load<VEC>(dop, (row * vs + c) * (uint32_t)sizeof(T), Dv - c);
+            vr[i].template load<VEC>(vp, (row * vs + c) * (uint32_t)sizeof(T), Dv - c);
+          }
         };
         f4_t zd[2], zw[2], dz[2], wz[2];  // Z_row . dO, Z_row . W, dO_row . Z, W_row . Z with the wave's tokens
         f4_t xd[2], xw[2];                // the other half's: the last two (h = 0) or the first two
 #pragma unroll
         for (int t = 0; t < 2; ++t) zd[t] = zw[t] = dz[t] = wz[t] = xd[t] = xw[t] = f4_t{0.f, 0.f, 0.f, 0.f};
-        float wv = 0.f;  // W . v
+        float wv[N];  // W . v
+#pragma unroll
+        for (int i = 0; i < N; ++i) wv[i] = 0.f;
         fetch(0);
-        for (int vb = 0, i = 0; vb < VP; vb += 32, i ^= 1) {
-          char* m = lds.buf[Lds::NBUF == 2 ? i : 0];
-          {
-            const Op<NP> d = ds.op();
-            *reinterpret_cast<bf8_t*>(m + m_at) = zs.hi;
-            *reinterpret_cast<bf8_t*>(m + Lds::PART + m_at) = zs.lo;
-            *reinterpret_cast<bf8_t*>(m + 2 * Lds::PART + m_at) = ws.hi;
-            *reinterpret_cast<bf8_t*>(m + 3 * Lds::PART + m_at) = ws.lo;
+        for (int vb = 0, turn = 0; vb < VP; vb += COLS, turn ^= 1) {
+          char* m = lds.buf[Lds::NBUF == 2 ? turn : 0];
 #pragma unroll
-            for (int p = 0; p < NP; ++p) *reinterpret_cast<bf8_t*>(m + (4 + p) * Lds::PART + m_at) = d.p[p];
+          for (int i = 0; i < N; ++i) {
+            const int o = Lds::at(place_of(M_ROWS * i + m_row), m_piece);
+            const Op<NP> d = ds[i].op();
+            *reinterpret_cast<bf8_t*>(m + o) = zs[i].hi;
+            *reinterpret_cast<bf8_t*>(m + Lds::PART + o) = zs[i].lo;
+            *reinterpret_cast<bf8_t*>(m + 2 * Lds::PART + o) = ws[i].hi;
+            *reinterpret_cast<bf8_t*>(m + 3 * Lds::PART + o) = ws[i].lo;
+#pragma unroll
+            for (int p = 0; p < NP; ++p) *reinterpret_cast<bf8_t*>(m + (4 + p) * Lds::PART + o) = d.p[p];
             float vf[8];
-            vr.open(vf);
+            vr[i].open(vf);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) wv += vf[e] * ((float)ws.hi[e] + (float)ws.lo[e]);
+            for (int e = 0; e < 8; ++e) wv[i] += vf[e] * ((float)ws[i].hi[e] + (float)ws[i].lo[e]);
           }
-          if (vb + 32 < VP) fetch(vb + 32);
+          if (vb + COLS < VP) fetch(vb + COLS);
           lds_barrier();
-          const Op<NP> dn = Lds::stream(m, 4, own_at, 0);
-          const Split zn = Lds::two(m, 0, own_at, 0), wn = Lds::two(m, 2, own_at, 0);
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int r = 2 * h + t, o = 2 - 2 * h + t;
-            const Split zr = Lds::two(m, 0, rows_at, r);
-            zd[t] = mma(zr, dn, zd[t]);
-            zw[t] = mma(zr, wn, zw[t]);
-            dz[t] = mma(Lds::stream(m, 4, rows_at, r), zn, dz[t]);
-            wz[t] = mma(Lds::two(m, 2, rows_at, r), zn, wz[t]);
-            if (h == 0) {
-              xd[t] = mma(Lds::stream(m, 4, rows_at, o), zn, xd[t]);
-              xw[t] = mma(Lds::two(m, 2, rows_at, o), zn, xw[t]);
-            } else {
-              const Split zo = Lds::two(m, 0, rows_at, o);
-              xd[t] = mma(zo, dn, xd[t]);
-              xw[t] = mma(zo, wn, xw[t]);
+          for (int kb = 0; kb < N; ++kb) {
+            const Op<NP> dn = Lds::stream(m, 4, own_at, 0, kb);
+            const Split zn = Lds::two(m, 0, own_at, 0, kb), wn = Lds::two(m, 2, own_at, 0, kb);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int r = 2 * h + t, o = 2 - 2 * h + t;
+              const Split zr = Lds::two(m, 0, rows_at, r, kb);
+              zd[t] = mma(zr, dn, zd[t]);
+              zw[t] = mma(zr, wn, zw[t]);
+              dz[t] = mma(Lds::stream(m, 4, rows_at, r, kb), zn, dz[t]);
+              wz[t] = mma(Lds::two(m, 2, rows_at, r, kb), zn, wz[t]);
+              if (h == 0) {
+                xd[t] = mma(Lds::stream(m, 4, rows_at, o, kb), zn, xd[t]);
+                xw[t] = mma(Lds::two(m, 2, rows_at, o, kb), zn, xw[t]);
+              } else {
+                const Split zo = Lds::two(m, 0, rows_at, o, kb);
+                xd[t] = mma(zo, dn, xd[t]);
+                xw[t] = mma(zo, wn, xw[t]);
+              }
+              keep_order();
             }
           }
           if (Lds::NBUF == 1) lds_barrier();
         }
-        wv += __shfl_xor(wv, 1, 64);
-        wv += __shfl_xor(wv, 2, 64);
-        if ((tid & 3) == 0) lds.wv[m_row] = wv;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+          for (int o = 1; o < Lds::PIECES; o <<= 1) wv[i] += __shfl_xor(wv[i], o, 64);
+          if (m_piece == 0) lds.wv[M_ROWS * i + m_row] = wv[i];
+        }
         keep_order();
         f4_t kk[2], qk[2], xk[2], xq[2];  // rows i: k_i . k_j and q_i . k_j
 #pragma unroll
@@ -484,15 +505,20 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaArgs a) {
       // What the states pass on, 64 keys at a time.
       const Range mp((const bf16_t*)a.states + at * 2 * KP * VP, 4 * KP * VP);
       const Range np((const bf16_t*)a.dstates + at * 2 * KP * VP, 4 * KP * VP);
-      Split mr, nr, zn_next, wn_next;
-      Op<NP> dn_next;
+      Split mr[N], nr[N], zn_next[N], wn_next[N];
+      Op<NP> dn_next[N];
       const auto fetch = [&](int key0, int vb) {
-        const uint32_t o = 2 * (m_row * VP + m_col), s = 2 * (key0 * VP + vb), own = 2 * (n * VP + vb + 8 * g);
-        mr = mp.parts(o, s, slo);
-        nr = np.parts(o, s, slo);
-        dn_next = token_op<T, VEC>(dop, vs, tok, vb + 8 * g, Dv);
-        zn_next = zp.parts(own, 16 * w * two, vlo);
-        wn_next = wp.parts(own, 16 * w * two, vlo);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const uint32_t o = vb + m_col < VP ? 2 * ((M_ROWS * i + m_row) * VP + m_col) : NOWHERE;
+          mr[i] = mp.parts(o, 2 * (key0 * VP + vb), slo);
+          nr[i] = np.parts(o, 2 * (key0 * VP + vb), slo);
+          const int c = vb + 32 * i + 8 * g;
+          const uint32_t own = c < VP ? 2 * (tok * VP + c) : NOWHERE;
+          dn_next[i] = token_op<T, VEC>(dop, vs, tok, c, Dv);
+          zn_next[i] = zp.parts(own, 0, vlo);
+          wn_next[i] = wp.parts(own, 0, vlo);
+        }
       };
       fetch(64 * QUADS * pass, 0);
       const double Gend = lds.G[CH - 1], Gown = lds.G[tok];
@@ -505,30 +531,42 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaArgs a) {
         f4_t dq[4], read[4], early[4];
 #pragma unroll
         for (int t = 0; t < 4; ++t) dq[t] = read[t] = early[t] = f4_t{0.f, 0.f, 0.f, 0.f};
-        for (int vb = 0, i = 0; vb < VP; vb += 32, i ^= 1) {
-          char* m = lds.buf[Lds::NBUF == 2 ? i : 0];
-          *reinterpret_cast<bf8_t*>(m + m_at) = mr.hi;
-          *reinterpret_cast<bf8_t*>(m + Lds::PART + m_at) = mr.lo;
-          *reinterpret_cast<bf8_t*>(m + 2 * Lds::PART + m_at) = nr.hi;
-          *reinterpret_cast<bf8_t*>(m + 3 * Lds::PART + m_at) = nr.lo;
+        for (int vb = 0, turn = 0; vb < VP; vb += COLS, turn ^= 1) {
+          char* m = lds.buf[Lds::NBUF == 2 ? turn : 0];
+          Op<NP> dn[N];
+          Split zn[N], wn[N];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            mn += ((float)mr.hi[e] + (float)mr.lo[e]) * ((float)nr.hi[e] + (float)nr.lo[e]);
-          const Op<NP> dn = dn_next;
-          const Split zn = zn_next, wn = wn_next;
-          if (vb + 32 < VP) fetch(key0, vb + 32);
+          for (int i = 0; i < N; ++i) {
+            const int o = Lds::at(place_of(M_ROWS * i + m_row), m_piece);
+            *reinterpret_cast<bf8_t*>(m + o) = mr[i].hi;
+            *reinterpret_cast<bf8_t*>(m + Lds::PART + o) = mr[i].lo;
+            *reinterpret_cast<bf8_t*>(m + 2 * Lds::PART + o) = nr[i].hi;
+            *reinterpret_cast<bf8_t*>(m + 3 * Lds::PART + o) = nr[i].lo;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              mn += ((float)mr[i].hi[e] + (float)mr[i].lo[e]) * ((float)nr[i].hi[e] + (float)nr[i].lo[e]);
+            dn[i] = dn_next[i];
+            zn[i] = zn_next[i];
+            wn[i] = wn_next[i];
+          }
+          if (vb + COLS < VP) fetch(key0, vb + COLS);
           else if (quad + 1 < QUADS) fetch(key0 + 64, 0);
           lds_barrier();
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const Split ms = Lds::two(m, 0, rows_at, t), ns = Lds::two(m, 2, rows_at, t);
-            dq[t] = mma(ms, dn, dq[t]);
-            read[t] = mma(ms, wn, read[t]);
-            early[t] = mma(ns, zn, early[t]);
+          for (int kb = 0; kb < N; ++kb) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const Split ms = Lds::two(m, 0, rows_at, t, kb), ns = Lds::two(m, 2, rows_at, t, kb);
+              dq[t] = mma(ms, dn[kb], dq[t]);
+              read[t] = mma(ms, wn[kb], read[t]);
+              early[t] = mma(ns, zn[kb], early[t]);
+              if (t & 1) keep_order();
+            }
           }
           if (Lds::NBUF == 1) lds_barrier();
         }
-        if (Lds::NBUF == 2 && (VP & 32)) lds_barrier();  // an odd number of steps: the next one takes the same buffer
+        // after an odd number of steps the next one takes the same buffer
+        if (Lds::NBUF == 2 && ((VP + COLS - 1) / COLS & 1)) lds_barrier();
         const int cols_at = Tk::lane_at_t(n, g) ^ (2 * key0);
         f4_t dk[4];
 #pragma unroll
@@ -574,8 +612,8 @@ __global__ __launch_bounds__(256, 2) void delta_grad_kernel(DeltaArgs a) {
               dqt[4 * quad + t] += dq[t];
               dkt[4 * quad + t] += dk[t];
             }
+            keep_order();
           }
-          keep_order();
         }
         if (!SHARED) put(tok, key0, dq, dk);
       }
