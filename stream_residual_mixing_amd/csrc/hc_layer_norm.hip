@@ -4,12 +4,48 @@
 //   (hc_norm.hip) stores its own.
 // Each row is read once and stays in float32 registers. The variance is that of the
 // deviations from the mean, never a difference of two large sums: one exchange over the
-// row's threads for the mean, one for the deviations' sums.
+// row's threads for the mean, one for the deviations' sums; what rounding leaves in the
+// mean is taken off with the scale, in one multiply-add an element.
+//   Memory bounds the forward: 8,192 rows of 4,096 bfloat16 with residual, stored as e4m3
+// groups, 47 us for 236 MB; the pre-read of 4 streams 67 us for 403 MB. In the backward
+// (60 us for 268 MB) a row's two exchanges, and the threads that wait in them, cost as much.
+// They were the larger part of both: sums by DPP and lane swaps instead of trips through
+// LDS, and one LDS word a lane for the waves' sums instead of a loop over them, took the
+// forward from 55 to 47 us, the backward from 69 to 60, and from 159 to 111 us at 7,168
+// channels, where 14 waves share a row.
 #include "hc_norm_row.h"
 
 namespace hc {
 
 namespace {
+
+// The sum over a wave's lanes, in every lane: within rows of 16 by DPP, the rows by lane swaps, with no
+// trip through LDS (a row takes up to six sums one after the other).
+__device__ __forceinline__ float lanes_sum(float v) {
+  typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+  v = row16_sum(v);
+  u2 p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+
+// Sums of NV values over one row's threads, the same in each; `red` is not used again before the
+// row's threads have met another barrier.
+template <bool WAVE, int NV>
+__device__ __forceinline__ void sum_over_row(float (&v)[NV], float (*red)[16]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] = lanes_sum(v[i]);
+  if (WAVE) return;
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) red[i][threadIdx.x >> 6] = v[i];
+  lds_barrier();
+  const uint32_t w = threadIdx.x & 15;  // at most 16 waves
+  const bool there = w < blockDim.x >> 6;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i] = row16_sum(there ? red[i][w] : 0.f);
+}
 
 // LDS of one row parity: two slots of up to NV sums, and the words of the row's extremes.
 template <int NV>
@@ -18,10 +54,10 @@ struct RowRed {
   uint32_t top[4][16];
 };
 
-// Turns a row's values v into their deviations from the mean and gives ms, the deviations'
-// mean square + eps; of the values u that `up` gives (the backward's w dy) s[0] = sum u and
-// s[1] = sum u v.
-//   What rounding leaves in the mean is the deviations' own mean, which is taken off again.
+// Turns a row's values v into their deviations from the mean, but for `rest`, and gives ms, the
+// deviations' mean square + eps; of the values u that `up` gives (the backward's w dy) s[0] = sum u
+// and s[1] = sum u (v - rest).
+//   What rounding leaves in the mean is the deviations' own mean, `rest`, for the caller to take off.
 //   Where the deviations are within 2^-15 of the mean, that rounding is no longer small
 //   beside them: equal values are found by their bits (their square is 0), others are
 //   centred a second time.
@@ -31,7 +67,7 @@ struct RowRed {
 //   returned, 0 otherwise, and v and ms are those of the scaled row.
 template <int ITEMS, bool WAVE, bool VEC, bool BWD, typename UP>
 __device__ __forceinline__ int row_center(float (&v)[ITEMS][8], const RowThreads<WAVE>& r, uint32_t C, float inv_c,
-                                          float eps, RowRed<BWD ? 4 : 2>& red, UP up, float& ms, float (&s)[2]) {
+                                          float eps, RowRed<BWD ? 4 : 2>& red, UP up, float& ms, float& rest, float (&s)[2]) {
   constexpr int NV = BWD ? 4 : 2;
   const auto inside = [&](int it, int e) { return (uint32_t)((it * r.nt + r.tid) * 8 + (VEC ? 0 : e)) < C; };
   float total[2];
@@ -45,7 +81,7 @@ __device__ __forceinline__ int row_center(float (&v)[ITEMS][8], const RowThreads
           total[0] += v[it][e];
           total[1] += fabsf(v[it][e]);
         }
-    row_sum<WAVE, 2>(total, red.sum[0]);
+    sum_over_row<WAVE, 2>(total, red.sum[0]);
   };
   add_up();
   int k = 0;
@@ -71,8 +107,8 @@ __device__ __forceinline__ int row_center(float (&v)[ITEMS][8], const RowThreads
 #pragma unroll
   for (int it = 0; it < ITEMS; ++it)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[it][e] = inside(it, e) ? v[it][e] - mean : 0.f;
-  float q[NV], rest;
+    for (int e = 0; e < 8; ++e) v[it][e] -= inside(it, e) ? mean : 0.f;  // 0 where there is no channel
+  float q[NV];
   const auto sums = [&](int slot) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) q[i] = 0.f;
@@ -90,7 +126,7 @@ __device__ __forceinline__ int row_center(float (&v)[ITEMS][8], const RowThreads
         }
       }
     }
-    row_sum<WAVE, NV>(q, red.sum[slot]);
+    sum_over_row<WAVE, NV>(q, red.sum[slot]);
     rest = uniform(q[0] * inv_c);
     ms = uniform(q[1] * inv_c - rest * rest);
   };
@@ -115,10 +151,6 @@ __device__ __forceinline__ int row_center(float (&v)[ITEMS][8], const RowThreads
     sums(0);
     ms = fmaxf(ms, 0.f);
   }
-#pragma unroll
-  for (int it = 0; it < ITEMS; ++it)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[it][e] -= rest;
   if (BWD) {
     s[0] = q[NV - 2];
     s[1] = q[NV - 1] - rest * s[0];
@@ -198,15 +230,15 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void layer_norm_kerne
 #pragma unroll
       for (int it = 0; it < ITEMS; ++it) row_store<VEC>((T*)a.s + t * C, (it * NT + tid) * 8, C, v[it]);
     }
-    float unused[2], ms;
-    row_center<ITEMS, WAVE, VEC, false>(v, r, C, inv_c, a.eps, red[parity], [](int, float*) {}, ms, unused);
-    const float rstd = rms_factor(ms);
+    float unused[2], ms, rest;
+    row_center<ITEMS, WAVE, VEC, false>(v, r, C, inv_c, a.eps, red[parity], [](int, float*) {}, ms, rest, unused);
+    const float rstd = rms_factor(ms), off = -rest * rstd;
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
       float wi[8], bi[8];
       weight(it, wi, bi);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[it][e] = v[it][e] * rstd * wi[e] + bi[e];
+      for (int e = 0; e < 8; ++e) v[it][e] = fmaf(fmaf(v[it][e], rstd, off), wi[e], bi[e]);
     }
     row_write<T, ITEMS, WAVE, VEC>(a, t, NT, tid, v, red[parity].top[3]);
   }
@@ -263,11 +295,13 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void layer_norm_backw
 #pragma unroll
       for (int e = 0; e < 8; ++e) u[e] = wi[e] * dy[it][e];
     };
-    const int p = row_center<ITEMS, WAVE, VEC, true>(v, r, C, inv_c, a.eps, red[parity], up, ms, s);
-    // dx = ... 2^-p, as a product of two that are in range
-    const float back1 = __builtin_amdgcn_ldexpf(1.f, -(p / 2)), back2 = __builtin_amdgcn_ldexpf(1.f, -(p - p / 2));
-    const float rstd = rms_factor(ms), rstd_dx = rstd * back1;
+    float rest;
+    const int p = row_center<ITEMS, WAVE, VEC, true>(v, r, C, inv_c, a.eps, red[parity], up, ms, rest, s);
+    const float rstd = rms_factor(ms), off = -rest * rstd;
     const float k = (s[1] * rstd) * inv_c * rstd, mean_u = s[0] * inv_c;
+    // dx = rstd (u - mean_u - (v - rest) k) 2^-p + ds
+    const float by_v = -rstd * k, fixed = -rstd * (mean_u - rest * k);
+    const float back1 = __builtin_amdgcn_ldexpf(1.f, -(p / 2)), back2 = __builtin_amdgcn_ldexpf(1.f, -(p - p / 2));
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
       float o[8], ds[8], u[8], dwi[8], dbi[8];
@@ -277,9 +311,16 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void layer_norm_backw
       db.get(it, dbi, 1);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        dwi[e] += dy[it][e] * (v[it][e] * rstd);
+        dwi[e] = fmaf(dy[it][e], fmaf(v[it][e], rstd, off), dwi[e]);
         dbi[e] += dy[it][e];
-        o[e] = rstd_dx * ((u[e] - mean_u - v[it][e] * k) * back2) + (a.ds ? ds[e] : 0.f);
+        if (!a.ds) ds[e] = 0.f;
+      }
+      if (p == 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = fmaf(u[e], rstd, fmaf(v[it][e], by_v, ds[e] + fixed));
+      } else {  // 2^-p as a product of two that are in range, the second inside
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = (rstd * back1) * ((u[e] - mean_u - (v[it][e] - rest) * k) * back2) + ds[e];
       }
       dw.put(it, dwi, 0);
       db.put(it, dbi, 1);
@@ -330,6 +371,12 @@ __global__ __launch_bounds__(WAVE ? 64 * WAVE_ROWS : 1024) void layer_norm_backw
   }
 }
 
+// Up to this many channels a thread of the forward has one piece and keeps weight and bias in
+// registers: 4,096 channels 47 us against 56 with two pieces that read both again, 7,168
+// channels 91 against 102 with one piece and 14 waves in step (bfloat16; 6,000 channels of
+// float32 84 against 78).
+constexpr int64_t ONE_PIECE = 4096;
+
 template <typename T, int MODE, int ITEMS, bool WAVE>
 void norm_go(bool vec, const RowShape& s, const NormArgs& a, const float* b, hipStream_t st) {
   if (vec) hipLaunchKernelGGL((layer_norm_kernel<T, MODE, ITEMS, WAVE, true>), dim3(s.grid), dim3(s.block), 0, st, a, b);
@@ -338,7 +385,7 @@ void norm_go(bool vec, const RowShape& s, const NormArgs& a, const float* b, hip
 
 template <typename T, int MODE>
 void norm_by_width(bool vec, const NormArgs& a, const float* b, hipStream_t st) {
-  const RowShape s = row_shape(a.T, a.C, false);
+  const RowShape s = row_shape(a.T, a.C, false, ONE_PIECE);
   if (s.wave) norm_go<T, MODE, 1, true>(vec, s, a, b, st);
   else if (s.items == 1) norm_go<T, MODE, 1, false>(vec, s, a, b, st);
   else norm_go<T, MODE, 2, false>(vec, s, a, b, st);

@@ -374,18 +374,18 @@ struct PieceSums<2> {
 // 41.6 / 264, 16,384 waves 43.5 / 260). The backward keeps 256 CUs equally busy, with up to
 // 16 waves each (bfloat16, 8,192 rows of 2,560 / 4,096 / 7,168 channels: 36 / 50 / 97 us;
 // 4,096 waves in all, however they fall, 50 / 51 / 156; one workgroup each 49 / 49 / 98) and
-// one piece a thread up to 8,192 channels.
+// one piece a thread up to 8,192 channels. one_piece is the forward's own limit.
 struct RowShape {
   int items;
   bool wave;
   unsigned block, grid;
 };
 
-RowShape row_shape(int64_t T, int64_t C, bool bwd) {
+RowShape row_shape(int64_t T, int64_t C, bool bwd, int64_t one_piece = 2048) {
   RowShape s;
   const int64_t pieces = (C + 7) / 8;
   s.wave = C <= 512;
-  s.items = C <= 2048 || (bwd && C <= 8192) ? 1 : 2;
+  s.items = C <= one_piece || (bwd && C <= 8192) ? 1 : 2;
   s.block = s.wave ? 64 * WAVE_ROWS : (unsigned)((pieces + 64 * s.items - 1) / (64 * s.items) * 64);
   const int64_t need = s.wave ? (T + WAVE_ROWS - 1) / WAVE_ROWS : T;
   const int64_t waves = s.block / 64, most = bwd ? 256 * (waves < 16 ? 16 / waves : 1) : 16384 / waves;
