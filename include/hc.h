@@ -761,7 +761,8 @@ int hc_gated_scan_backward(const void* x, const void* gate, const void* y, const
  *   The states are formed again from the inputs. Sums are float32 and products hold 16 bits of each
  *   factor, as the forward's; deterministic. Sizes and alignment as for the forward; workspace
  *   hc_gated_delta_backward_workspace_bytes bytes, 256-byte aligned (for each 64 tokens of a value
- *   head two states in 4 bytes an element, Z, W and 38 KB).
+ *   head two states in 4 bytes an element, Z, W and 38 KB; where few heads have long sequences, for each of
+ *   the segments that they are cut into a state and two maps of it in 4 bytes an element).
  */
 int64_t hc_gated_delta_workspace_bytes(int64_t B, int64_t S, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
                                        int dtype);

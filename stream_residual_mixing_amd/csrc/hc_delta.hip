@@ -9,7 +9,17 @@
 // columns' state in registers and hands each product's result to the next as its operand.
 // Products are bfloat16 matrix instructions with float32 sums; values that are not bfloat16
 // already (the state, Z, T, P, float32 streams) enter as two parts, 16 bits, so that the
-// state carries errors of 2^-17 of its terms rather than 2^-9.
+// state carries errors of 2^-17 of its terms rather than 2^-9: 2 to 8 x 10^-6 of the norm of
+// states, gradients and float32 outputs, measured. Sums, states in registers and the
+// states that are given and returned are float32. (Three parts would keep float32's own
+// 24 bits, for twice the products and half as much LDS again, which a CU has not got at
+// 256 x 256; bfloat16 outputs are far above both.)
+//   What bounds it: 2,048 chunks of 128 x 128 in bfloat16 (8 sequences of 1,024 tokens, 16 value
+// heads on 8 key heads) read and write 118 MB and need 15 GFLOP, 20 us of memory; the chunks
+// by themselves take 38 us (latency of the triangle's inverse), the walk 85 us as 16 chunks in
+// a row on 256 workgroups, 5 us a chunk of which the matrix units work for 1: each product waits for the one before it. Hence few heads are
+// walked in segments at once (see delta_plan), and what does not depend on the state is done
+// by every chunk for itself.
 #include "hc_delta_device.h"
 
 namespace hc {
@@ -478,8 +488,9 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
 // M_{s+1} = Phi_s M_s + N_s over a head's segments, 16 columns of the state by a workgroup; the slots'
 // N become the states. A wave has 32 rows of the state, the operand block that the next step's
 // products take from all of them through LDS; its rows of the next step's Phi and N are on their
-// way meanwhile (one wave that does it all, 7.4 us a step instead of 1.3). BACK: the gradients, from
-// the last segment on, with Phi's transpose.
+// way meanwhile. A chain of products on data that other dies' caches hold: 40 us for 16 heads of 16
+// segments (128 x 128); one wave with all rows 103. BACK: the gradients, from the last segment on, with
+// Phi's transpose.
 template <int KP, bool BACK>
 __global__ __launch_bounds__(2 * KP) void delta_join_kernel(DeltaArgs a) {
   constexpr int KB = KP / 32;
@@ -540,8 +551,13 @@ __global__ __launch_bounds__(2 * KP) void delta_join_kernel(DeltaArgs a) {
   }
 }
 
-constexpr int SHORT = 8;  // tokens up to which they are taken one by one
+// Tokens up to which they are taken one by one, rather than as a chunk: 4 tokens of 32 heads of 128 x 128
+// take 11.6 us against 16.4, of 256 heads 16.4 against 24 and of 2,048 heads 83 against 103; 8 tokens 14.3
+// against 16.6, 25.2 against 24.3 and 137 against 106 (whole calls, bfloat16).
+constexpr int SHORT = 6;
 
+// Four waves a workgroup, 64 columns: 572 us for 8,192 tokens of 16 heads in one walk and 129 for 8 x 1,024
+// against 671 and 136 with eight waves, which share keys and queries but wait for each other.
 template <typename T, int KP, int MODE>
 hipError_t walk_go(const DeltaArgs& a, hipStream_t st) {
   constexpr int NW = 4;
@@ -601,7 +617,12 @@ int64_t delta_plan(DeltaArgs& a, bool backward, void* ws) {
   a.VP = (a.Dv + 31) / 32 * 32;
   a.NS = 1;
   a.SL = a.NC;
-  const int64_t wide = heads * ((a.Dv + 63) / 64);  // workgroups that walk whole sequences
+  // Workgroups that walk whole sequences. Where they are few for 256 CUs of two each, every sequence is cut
+  // into segments of 4 chunks and more, as many as fill the CUs, walked at once from zeros, with their maps
+  // of the state, joined, and walked again from their own states: twice the work and the join, so worth it
+  // from four segments and 1,024 tokens on (16 heads of 128 x 128: 8,192 tokens 210 us against 572 in one
+  // walk, whole calls).
+  const int64_t wide = heads * ((a.Dv + 63) / 64);
   if (wide > 0 && 512 / wide >= 4 && a.NC >= 16) {
     const int64_t most = 512 / wide < a.NC / 4 ? 512 / wide : a.NC / 4;
     a.SL = (a.NC + most - 1) / most;
