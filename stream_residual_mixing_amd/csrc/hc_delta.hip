@@ -16,7 +16,7 @@
 // 256 x 256; bfloat16 outputs are far above both.)
 //   What bounds it: 2,048 chunks of 128 x 128 in bfloat16 (8 sequences of 1,024 tokens, 16 value
 // heads on 8 key heads) read and write 118 MB and need 15 GFLOP, 20 us of memory; the chunks
-// by themselves take 38 us (latency of the triangle's inverse), the walk 85 us as 16 chunks in
+// by themselves take 38 us (latency of the triangle's inverse), the walk 79 us as 16 chunks in
 // a row on 256 workgroups, 5 us a chunk of which the matrix units work for 1: each product waits for the one before it. Hence few heads are
 // walked in segments at once (see delta_plan), and what does not depend on the state is done
 // by every chunk for itself.
@@ -487,9 +487,10 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
 
 // M_{s+1} = Phi_s M_s + N_s over a head's segments, 16 columns of the state by a workgroup; the slots'
 // N become the states. A wave has 32 rows of the state, the operand block that the next step's
-// products take from all of them through LDS; its rows of the next step's Phi and N are on their
-// way meanwhile. A chain of products on data that other dies' caches hold: 40 us for 16 heads of 16
-// segments (128 x 128); one wave with all rows 103. BACK: the gradients, from the last segment on, with
+// products take from all of them through LDS; its rows of the next two steps' Phi and N are on their
+// way meanwhile. A chain of products whose maps come from other dies' caches, 64 KB a step: 34 us for 16
+// heads of 16 segments (128 x 128); 40 with a head's columns spread over the dies and one step ahead, 103
+// with one wave for all rows. BACK: the gradients, from the last segment on, with
 // Phi's transpose.
 template <int KP, bool BACK>
 __global__ __launch_bounds__(2 * KP) void delta_join_kernel(DeltaArgs a) {
@@ -497,9 +498,9 @@ __global__ __launch_bounds__(2 * KP) void delta_join_kernel(DeltaArgs a) {
   __shared__ __attribute__((aligned(16))) char lds[2][KB][2][TILE];
   const int lane = threadIdx.x & 63, w = wave_number(), n = lane & 15, g = lane >> 4;
   const int Dk = (int)a.Dk, Dv = (int)a.Dv;
-  const uint32_t groups = ((uint32_t)Dv + 15) / 16;
-  const int64_t bh = blockIdx.x / groups, b = (uint32_t)bh / (uint32_t)a.Hv;
-  const int col = (int)(blockIdx.x % groups) * 16, have = min(16, Dv - col);
+  const Place at((uint32_t)(a.B * a.Hv), ((uint32_t)Dv + 15) / 16);
+  const int64_t bh = at.unit, b = at.unit / (uint32_t)a.Hv;
+  const int col = (int)at.member * 16, have = min(16, Dv - col);
   const int64_t chunks = (length_of(a.lengths, b, a.S) + CH - 1) / CH, state = (int64_t)Dk * Dv;
   const int segs = (int)((chunks + a.SL - 1) / a.SL);  // that hold tokens
   float* slots = a.slots + bh * a.NS * state + col;
@@ -508,46 +509,52 @@ __global__ __launch_bounds__(2 * KP) void delta_join_kernel(DeltaArgs a) {
   const auto seg = [&](int i) { return BACK ? segs - 1 - i : i; };
   const uint32_t s_lane = n < have ? 4 * ((32 * w + 8 * g) * Dv + n) : NOWHERE;
   const uint32_t m_lane = 2 * ((8 * (n >> 2) + (n & 3)) * KP + 8 * g);
-  Split m[2][KB];
-  float add[8];
+  constexpr int AHEAD = KP == 256 ? 1 : 2;  // steps whose maps are on their way, as there are registers
+  Split m[AHEAD][2][KB];
+  float add[AHEAD][8];
   const auto load_slot = [&](int i, float (&v)[8]) {
     const Range r(slots + seg(i) * state, ((int64_t)(Dk - 1) * Dv + have) * 4);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = r.get((const float*)nullptr, s_lane + 4 * e * Dv);
   };
-  const auto fetch = [&](int i) {
+  const auto fetch = [&](int i, int x) {
     const Range r(maps + seg(i) * (int64_t)2 * KP * KP, 4 * KP * KP);
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) m[t][kb] = r.parts(m_lane, 2 * ((32 * w + 4 * t) * KP + 32 * kb), 2 * KP * KP);
-    load_slot(i, add);
+      for (int kb = 0; kb < KB; ++kb) m[x][t][kb] = r.parts(m_lane, 2 * ((32 * w + 4 * t) * KP + 32 * kb), 2 * KP * KP);
+    load_slot(i, add[x]);
   };
   float S[8];  // rows 32 w + 8 g + 0 .. 7
   load_slot(0, S);
-  fetch(1);
-  for (int i = 1; i < segs - 1; ++i) {
+  const auto step = [&](int i, int x) {
     u4_t hi, lo;
     split8(S, hi, lo);
     char* mine = lds[i & 1][w][0] + lane * 16;
     *reinterpret_cast<u4_t*>(mine) = hi;
     *reinterpret_cast<u4_t*>(mine + TILE) = lo;
     lds_barrier();
-    f4_t o[2] = {{add[0], add[1], add[2], add[3]}, {add[4], add[5], add[6], add[7]}};
+    f4_t o[2] = {{add[x][0], add[x][1], add[x][2], add[x][3]}, {add[x][4], add[x][5], add[x][6], add[x][7]}};
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
       const char* p = lds[i & 1][kb][0] + lane * 16;
       const Split f = {*reinterpret_cast<const bf8_t*>(p), *reinterpret_cast<const bf8_t*>(p + TILE)};
 #pragma unroll
-      for (int t = 0; t < 2; ++t) o[t] = mma(m[t][kb], f, o[t]);
+      for (int t = 0; t < 2; ++t) o[t] = mma(m[x][t][kb], f, o[t]);
     }
-    if (i + 1 < segs - 1) fetch(i + 1);
+    if (i + AHEAD < segs - 1) fetch(i + AHEAD, x);
     const Range r(slots + seg(i) * state, ((int64_t)(Dk - 1) * Dv + have) * 4);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       S[e] = o[e >> 2][e & 3];
       r.put((float*)nullptr, s_lane + 4 * e * Dv, S[e]);
     }
+  };
+  fetch(1, 0);
+  if (AHEAD == 2 && segs > 3) fetch(2, 1);
+  for (int i = 1; i < segs - 1; i += AHEAD) {
+    step(i, 0);
+    if (AHEAD == 2 && i + 1 < segs - 1) step(i + 1, 1);
   }
 }
 
@@ -621,7 +628,7 @@ int64_t delta_plan(DeltaArgs& a, bool backward, void* ws) {
   // into segments of 4 chunks and more, as many as fill the CUs, walked at once from zeros, with their maps
   // of the state, joined, and walked again from their own states: twice the work and the join, so worth it
   // from four segments and 1,024 tokens on (16 heads of 128 x 128: 8,192 tokens 210 us against 572 in one
-  // walk, whole calls).
+  // walk, whole calls when this was chosen).
   const int64_t wide = heads * ((a.Dv + 63) / 64);
   if (wide > 0 && 512 / wide >= 4 && a.NC >= 16) {
     const int64_t most = 512 / wide < a.NC / 4 ? 512 / wide : a.NC / 4;

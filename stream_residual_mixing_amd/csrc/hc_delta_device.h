@@ -16,7 +16,8 @@ namespace hc {
 
 namespace {
 
-constexpr int CH = 64;  // tokens of a chunk
+constexpr int CH = 64;        // tokens of a chunk
+constexpr uint32_t DIES = 8;  // with an L2 each
 
 typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
 typedef float f4_t __attribute__((ext_vector_type(4)));
@@ -334,20 +335,36 @@ struct State {
   }
 };
 
-// A workgroup of the walks: a segment of a head's chunks by a group of its columns.
+// The grid's `units` by `members` workgroups, the members of a unit on one die, whose L2 then brings
+// what they all read once: consecutive workgroups go round the dies. The units behind the last
+// multiple of the dies in plain order. Against plain order throughout: walks of 2,048 chunks 85 -> 79 us, in
+// segments 70 + 69 -> 62 + 60; the backward's 637 -> 619 us in all.
+struct Place {
+  uint32_t unit, member;
+  __device__ __forceinline__ Place(uint32_t units, uint32_t members) {
+    const uint32_t x = blockIdx.x, even = units / DIES * DIES, mixed = even * members;
+    const uint32_t j = x < mixed ? x / DIES : x - mixed;
+    unit = x < mixed ? j / members * DIES + x % DIES : even + j / members;
+    member = j % members;
+  }
+};
+
+// A workgroup of the walks: a segment of a head's chunks by a group of its columns. All that walk the same
+// keys are a unit.
 struct Part {
   int64_t bh, b, slot;
   uint32_t hv, hk;
   int seg, group;
   int64_t len, chunks, first, last;  // [first, last) of them are this segment's
   __device__ __forceinline__ Part(const DeltaArgs& a, uint32_t groups) {
-    group = (int)(blockIdx.x % groups);
-    const uint32_t x = blockIdx.x / groups, NS = (uint32_t)a.NS, Hv = (uint32_t)a.Hv;
-    seg = (int)(x % NS);
-    bh = x / NS;
-    b = (uint32_t)bh / Hv;
-    hv = (uint32_t)bh % Hv;
-    hk = hv / (Hv / (uint32_t)a.Hk);
+    const uint32_t NS = (uint32_t)a.NS, Hk = (uint32_t)a.Hk, per = (uint32_t)a.Hv / Hk;
+    const Place at((uint32_t)a.B * Hk * NS, per * groups);
+    group = (int)(at.member % groups);
+    seg = (int)(at.unit % NS);
+    b = at.unit / NS / Hk;
+    hk = at.unit / NS % Hk;
+    hv = hk * per + at.member / groups;
+    bh = b * a.Hv + hv;
     slot = bh * NS + seg;
     len = length_of(a.lengths, b, a.S);
     chunks = (len + CH - 1) / CH;
