@@ -17,9 +17,9 @@
 //   What bounds it: 2,048 chunks of 128 x 128 in bfloat16 (8 sequences of 1,024 tokens, 16 value
 // heads on 8 key heads) read and write 118 MB and need 15 GFLOP, 20 us of memory; the chunks
 // by themselves take 38 us (latency of the triangle's inverse), the walk 79 us as 16 chunks in
-// a row on 256 workgroups, 5 us a chunk of which the matrix units work for 1: each product waits for the one before it. Hence few heads are
-// walked in segments at once (see delta_plan), and what does not depend on the state is done
-// by every chunk for itself.
+// a row on 256 workgroups, 5 us a chunk of which the matrix units work for 1: each product
+// waits for the one before it. Hence few heads are walked in segments at once (see
+// delta_plan), and what does not depend on the state is done by every chunk for itself.
 #include "hc_delta_device.h"
 
 namespace hc {
@@ -232,9 +232,15 @@ __global__ __launch_bounds__(64 * NW, 2) void delta_walk_kernel(DeltaArgs a) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) S.m[t][r] = row_of(t, 4 * g + r) == col + n ? 1.f : 0.f;
   } else {
-    const float* from = part.seg == 0 ? a.state0 + (a.state0 ? bh * Dk * Dv : 0)
-                        : MODE >= SUM ? nullptr : a.slots + (part.slot - 1) * Dk * Dv;
-    S.load(from ? from + col : nullptr, Dk, Dv, n, g, have);
+    // Where the last state is written over the first, the last segment may end before the first one
+    // begins: that one takes the copy that SUM made in the slot of a head's last segment, which has no
+    // other use in the forward.
+    const bool copied = (MODE == OUT || MODE == SUM) && part.seg == 0 && a.state0 && a.state0 == a.state1 && !part.ends();
+    float* copy = a.slots + (copied ? (bh * a.NS + a.NS - 1) * Dk * Dv + col : 0);
+    const float* from = part.seg != 0 ? (MODE >= SUM ? nullptr : a.slots + (part.slot - 1) * Dk * Dv + col)
+                        : copied && MODE == OUT ? copy : a.state0 ? a.state0 + bh * Dk * Dv + col : nullptr;
+    S.load(from, Dk, Dv, n, g, have);
+    if (copied && MODE == SUM) S.store(copy, Dk, Dv, n, g, have);
   }
 
   // the next chunk's operands on their way

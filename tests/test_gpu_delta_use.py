@@ -149,6 +149,23 @@ def test_state_in_place(S):
         assert l2 is state and torch.equal(y2, y) and torch.equal(state, last)
 
 
+def test_state_in_place_beside_other_work():
+    """A long sequence's segments are walked at once, in whatever order the workgroups start: the first must
+    not read the state that the last one has written over it."""
+    note("last state written over the given one, five streams at once")
+    runs = []
+    for s in range(5):
+        i = _inputs(40 + s, B=1, S=4000, Hk=4, Hv=16, Dk=128, Dv=128)
+        d = [i[n] for n in ("q", "k", "v", "g", "be")]
+        runs.append((d, i["M"], hc.hc_gated_delta(*d, i["M"]), [i["M"].clone() for _ in range(4)], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [(hc.hc_gated_delta(*d, state, out=(None, state), stream=st.cuda_stream), want)
+           for k in range(4) for d, _, want, states, st in runs for state in (states[k],)]
+    torch.cuda.synchronize()
+    for g, want in got:
+        _same(want, g)
+
+
 def test_batches_do_not_touch_each_other():
     note("a sequence alone gives what it gives in a batch, forward and backward")
     i = _inputs(9, B=4, S=500)
