@@ -200,7 +200,7 @@ struct WalkLds {
 // segment's from its own) and, as further columns that start as the unit matrix without values, its
 // map of the state; SUM_BWD: the map's transpose too.
 template <typename T, int KP, int NW, bool VEC, int MODE>
-__global__ __launch_bounds__(64 * NW, 2) void delta_walk_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, Stream<T>::NP, NW, MODE>>)) void delta_walk_kernel(DeltaArgs a) {
   constexpr int NP = Stream<T>::NP, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
   constexpr int PIECES = KP / 8, ITEMS = (CH * PIECES + THREADS - 1) / THREADS;
   constexpr int STRIDE = MODE == KEEP || MODE == SUM_BWD ? REC_BWD : REC, USED = MODE == OUT ? REC : REC_P;

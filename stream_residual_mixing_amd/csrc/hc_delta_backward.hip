@@ -31,7 +31,7 @@ struct BackLds {
 // FULL: as above, over a segment's chunks. Otherwise a segment's first gradient from zeros (the last
 // segment's from its own), nothing else.
 template <typename T, int KP, int NW, bool VEC, bool FULL>
-__global__ __launch_bounds__(64 * NW, 2) void delta_back_kernel(DeltaArgs a) {
+__global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, Stream<T>::NP, NW>>)) void delta_back_kernel(DeltaArgs a) {
   constexpr int NP = Stream<T>::NP, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
   constexpr int PIECES = KP / 8, ITEMS = (CH * PIECES + THREADS - 1) / THREADS;
   constexpr int USED = REC_BWD - REC_DEC, RR = (USED + 16 * THREADS - 1) / (16 * THREADS);
