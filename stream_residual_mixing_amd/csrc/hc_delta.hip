@@ -291,7 +291,7 @@ __global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, Stream<T>::NP, NW, MODE
     for (int t = 0; t < 4; ++t) v[t] = f4_t{vr[t][0], vr[t][1], vr[t][2], vr[t][3]};
     lds_barrier();
     if (c + 1 < part.last) fetch(c + 1);
-    if (MODE == KEEP) S.keep((bf16_t*)a.states + (bh * a.NC + c) * 2 * KP * VP, VP, col, n, g);
+    if (MODE == KEEP) S.keep((float*)a.states + (bh * a.NC + c) * KP * VP, VP, col, n, g);
 
     // K M and Q M
     f4_t x[4], o[4];
@@ -299,7 +299,7 @@ __global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, Stream<T>::NP, NW, MODE
     for (int t = 0; t < 4; ++t) x[t] = o[t] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
-      const Split sf = split(S.m[2 * kb], S.m[2 * kb + 1]);
+      const Fine sf = split_fine(S.m[2 * kb], S.m[2 * kb + 1]);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         Op<NP> ka, qa;
@@ -309,19 +309,19 @@ __global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, Stream<T>::NP, NW, MODE
           if (MODE == OUT) qa.p[p] = Tk::rows(lds.q[p], rows_at, t, kb);
         }
         x[t] = mma(ka, sf, x[t]);
-        if (MODE == OUT) o[t] = mma(qa, sf, o[t]);
+        if (MODE == OUT) o[t] = NP == 1 ? mma(qa, Split{sf.p[0], sf.p[1]}, o[t]) : mma(qa, sf, o[t]);
       }
       keep_order();
     }
     // R = V - exp(G) K M, Z = T R, X = beta Z
     const float* dec = (const float*)(lds.rec + REC_DEC);
-    Split f[2];
+    Fine f[2];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       x[t] = v[t] - *reinterpret_cast<const f4_t*>(dec + DEC_AHEAD + row_of(t, 4 * g)) * x[t];
     }
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) f[kb] = split(x[2 * kb], x[2 * kb + 1]);
+    for (int kb = 0; kb < 2; ++kb) f[kb] = split_fine(x[2 * kb], x[2 * kb + 1]);
 #pragma unroll
     for (int t = 0; t < 4; ++t) x[t] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -330,19 +330,22 @@ __global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, Stream<T>::NP, NW, MODE
       for (int t = 2 * kb; t < 4; ++t) x[t] = mma(load_tile(lds.rec + REC_T, tri(t, kb), lane), f[kb], x[t]);
       keep_order();
     }
-    if (MODE == KEEP) keep_rows((bf16_t*)a.z + (bh * a.NC + c) * 2 * CH * VP, VP, col, n, g, x);
+    if (MODE == KEEP) keep_rows((float*)a.z + (bh * a.NC + c) * CH * VP, VP, col, n, g, x);
 #pragma unroll
     for (int t = 0; t < 4; ++t) x[t] *= *reinterpret_cast<const f4_t*>(dec + DEC_BETA + row_of(t, 4 * g));
     if (MODE == OUT) {  // O = scale (exp(G) Q M + P X)
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) f[kb] = split(x[2 * kb], x[2 * kb + 1]);
+      for (int kb = 0; kb < 2; ++kb) f[kb] = split_fine(x[2 * kb], x[2 * kb + 1]);
       const Range oc = head_rows((T*)a.o + values + c * CH * vs, have > 0 ? (int)min((int64_t)CH, len - c * CH) : 0, vs, have);
       const uint32_t ol = anew(o_lane);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         o[t] *= *reinterpret_cast<const f4_t*>(dec + DEC_AHEAD + 16 * t + 4 * g);
 #pragma unroll
-        for (int kb = 0; kb <= (t >> 1); ++kb) o[t] = mma(load_tile(lds.rec + REC_P, tri(t, kb), lane), f[kb], o[t]);
+        for (int kb = 0; kb <= (t >> 1); ++kb) {
+          const Split p = load_tile(lds.rec + REC_P, tri(t, kb), lane);
+          o[t] = NP == 1 ? mma(p, Split{f[kb].p[0], f[kb].p[1]}, o[t]) : mma(p, f[kb], o[t]);
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           oc.put((T*)nullptr, ol + (16 * t + r) * vs * (uint32_t)sizeof(T), a.scale * o[t][r]);
@@ -353,7 +356,7 @@ __global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, Stream<T>::NP, NW, MODE
 #pragma unroll
     for (int t = 0; t < 4; ++t) x[t] *= *reinterpret_cast<const f4_t*>(dec + DEC_TO_END + row_of(t, 4 * g));
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) f[kb] = split(x[2 * kb], x[2 * kb + 1]);
+    for (int kb = 0; kb < 2; ++kb) f[kb] = split_fine(x[2 * kb], x[2 * kb + 1]);
     const float whole = dec[DEC_AHEAD + CH - 1];
 #pragma unroll
     for (int t = 0; t < KT; ++t) {

@@ -6,8 +6,12 @@
 //   dQ = exp(G) d M^T + B K,
 //   dK = [-exp(G) W M^T + A K] + [exp(G_end - G) X N^T + B^T Q + A^T K]   (as read, as written),
 //   dbeta_j = Z_j . dX_j - sum_i exp(G_i - G_j) (k_i . k_j) (W_i . Z_j),
-//   dG = q . dq + k . dk_read - k . dk_written = q . dq + W . (Z - V) - beta dbeta, and at the
-//        chunk's end sum_j k_j . (X N^T exp(G_end - G))_j + exp(G_end) <M, N>;  dg_t = sum_{i >= t} dG_i.
+//   dg_t = sum_{i >= t} exp(G_i) [d_i . (M^T q_i) - W_i . (M^T k_i)] + sum_{j < t} exp(G_end - G_j) X_j . (N^T k_j)
+//        + exp(G_end) <M, N> + sum_{i >= t > j} c_ij,  c_ij = (P_ij d_i - exp(G_i - G_j) (k_i . k_j) W_i) . X_j:
+//        all that passes over token t, each with its own decay, so that what is forgotten leaves no
+//        rounding behind. (q . dq - v . dv summed over the later tokens is the same, and was off by
+//        4 x 10^-5 in heads that forget fast.) The pairs as a running sum of what starts at a token less what
+//        ends there, the same c_ij in both.
 // The forward's walk is run again and keeps every chunk's M and Z; a second walk from the end back
 // keeps N and W and writes dV; then every chunk forms the rest by itself, all value heads of a key
 // head in one workgroup, so that dQ and dK are summed in registers and in a fixed order.
@@ -108,14 +112,14 @@ __global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, Stream<T>::NP, NW>>)) v
     for (int t = 0; t < 4; ++t) d[t] = f4_t{dr[t][0], dr[t][1], dr[t][2], dr[t][3]};
     lds_barrier();
     if (c > part.first) fetch(c - 1);
-    if (FULL) D.keep((bf16_t*)a.dstates + (bh * a.NC + c) * 2 * KP * VP, VP, col, n, g);
+    if (FULL) D.keep((float*)a.dstates + (bh * a.NC + c) * KP * VP, VP, col, n, g);
 
     f4_t x[4];  // K N
 #pragma unroll
     for (int t = 0; t < 4; ++t) x[t] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
-      const Split sf = split(D.m[2 * kb], D.m[2 * kb + 1]);
+      const Fine sf = split_fine(D.m[2 * kb], D.m[2 * kb + 1]);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         Op<NP> ka;
@@ -147,9 +151,9 @@ __global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, Stream<T>::NP, NW>>)) v
       keep_order();
     }
     // W = T^T (beta dX)
-    Split f[2], wf[2];
+    Fine f[2], wf[2];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) f[kb] = split(x[2 * kb], x[2 * kb + 1]);
+    for (int kb = 0; kb < 2; ++kb) f[kb] = split_fine(x[2 * kb], x[2 * kb + 1]);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       x[t] = f4_t{0.f, 0.f, 0.f, 0.f};
@@ -164,7 +168,7 @@ __global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, Stream<T>::NP, NW>>)) v
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int r = 0; r < 4; ++r) vc.put((T*)nullptr, vl + row_of(t, r) * vs * (uint32_t)sizeof(T), x[t][r]);
-      keep_rows((bf16_t*)a.w + (bh * a.NC + c) * 2 * CH * VP, VP, col, n, g, x);
+      keep_rows((float*)a.w + (bh * a.NC + c) * CH * VP, VP, col, n, g, x);
     }
     // the gradient of the state before the chunk
 #pragma unroll
@@ -175,8 +179,8 @@ __global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, Stream<T>::NP, NW>>)) v
     }
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      wf[kb] = split(x[2 * kb], x[2 * kb + 1]);
-      f[kb] = split(d[2 * kb], d[2 * kb + 1]);
+      wf[kb] = split_fine(x[2 * kb], x[2 * kb + 1]);
+      f[kb] = split_fine(d[2 * kb], d[2 * kb + 1]);
     }
     const float whole = dec[DEC_AHEAD + CH - 1];
     keep_order();
@@ -215,7 +219,7 @@ struct GradLds {
   char k[NP][Tokens<KP>::BYTES], q[NP][Tokens<KP>::BYTES];  // rows in row_of's order
   char buf[NBUF][(4 + NP) * PART];
   double G[CH];
-  float beta[CH], dG[CH], wv[CH], end[4];
+  float beta[CH], read[CH], late[CH], row[4][CH], end[4];
   // a row's place in row_of's order, its 16-byte pieces exchanged so that 16 lanes reading a piece of 16 rows
   // reach all banks
   static __device__ __forceinline__ int at(int place, int piece) {
@@ -224,6 +228,11 @@ struct GradLds {
   // an operand of tile `tile` (64-byte k block kb), the lane's own part at `at`
   static __device__ __forceinline__ bf8_t one(const char* m, int part, int at, int tile, int kb) {
     return *reinterpret_cast<const bf8_t*>(m + part * PART + 32 * COLS * tile + (at ^ (kb << 6)));
+  }
+  static __device__ __forceinline__ void put(char* m, int part, int at, const F8& v) {
+    const Split s = split(v.a, v.b);
+    *reinterpret_cast<bf8_t*>(m + part * PART + at) = s.hi;
+    *reinterpret_cast<bf8_t*>(m + (part + 1) * PART + at) = s.lo;
   }
   static __device__ __forceinline__ Split two(const char* m, int part, int at, int tile, int kb) {
     return {one(m, part, at, tile, kb), one(m, part + 1, at, tile, kb)};
@@ -333,11 +342,9 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
         lds.G[tid] = running_sum(on ? clamp_decay(a.g[gat + tid * a.Hv]) : 0.0, tid);
         lds.beta[tid] = on ? a.beta[gat + tid * a.Hv] : 0.f;
       }
-      const uint32_t two = 2 * VP, vlo = CH * two, slo = KP * two;
       const Range dop = head_rows((const T*)a.d_o + (b * a.S + t0) * vs + hv * Dv, left, vs, Dv);
-      const Range vp = head_rows((const T*)a.v + (b * a.S + t0) * vs + hv * Dv, left, vs, Dv);
-      const Range zp((const bf16_t*)a.z + at * 2 * CH * VP, 4 * CH * VP);
-      const Range wp((const bf16_t*)a.w + at * 2 * CH * VP, 4 * CH * VP);
+      const Range zp((const float*)a.z + at * CH * VP, 4 * CH * VP);
+      const Range wp((const float*)a.w + at * CH * VP, 4 * CH * VP);
       // a thread brings eight columns of a row, or of two, of each array
       constexpr int COLS = Lds::COLS, N = COLS / 32, M_ROWS = 256 / Lds::PIECES;
       const int m_row = tid / Lds::PIECES, m_piece = tid % Lds::PIECES, m_col = 8 * m_piece;
@@ -348,29 +355,25 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
       // Lane j = tok. Rows i >= j: B_ij and A_ij (it is the earlier one); rows j' <= tok: B and A of
       // (tok, j'), the later one. As operands: bq by K for dQ, bk by Q and aa by K for dK; x is the
       // other half's bk (h = 0) or bq (h = 1), ax its aa.
-      float db = 0.f, own_wz = 0.f;
+      float db = 0.f, late = 0.f;  // late: of the token as the earlier one of pairs and of the chunk's end
       Split bq, bk, aa, x, ax;
       {
-        Split zs[N], ws[N];
-        Raw8<T> ds[N], vr[N];
+        F8 zs[N], ws[N];
+        Raw8<T> ds[N];
         const auto fetch = [&](int vb) {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             const int row = M_ROWS * i + m_row, c = vb + m_col;
-            const uint32_t o = c < VP ? 2 * (row * VP + c) : NOWHERE;
-            zs[i] = zp.parts(o, 0, vlo);
-            ws[i] = wp.parts(o, 0, vlo);
+            const uint32_t o = c < VP ? 4 * (row * VP + c) : NOWHERE;
+            zs[i] = zp.floats(o, 0);
+            ws[i] = wp.floats(o, 0);
             ds[i].template load<VEC>(dop, (row * vs + c) * (uint32_t)sizeof(T), Dv - c);
-            vr[i].template load<VEC>(vp, (row * vs + c) * (uint32_t)sizeof(T), Dv - c);
           }
         };
         f4_t zd[2], zw[2], dz[2], wz[2];  // Z_row . dO, Z_row . W, dO_row . Z, W_row . Z with the wave's tokens
         f4_t xd[2], xw[2];                // the other half's: the last two (h = 0) or the first two
 #pragma unroll
         for (int t = 0; t < 2; ++t) zd[t] = zw[t] = dz[t] = wz[t] = xd[t] = xw[t] = f4_t{0.f, 0.f, 0.f, 0.f};
-        float wv[N];  // W . v
-#pragma unroll
-        for (int i = 0; i < N; ++i) wv[i] = 0.f;
         fetch(0);
         for (int vb = 0, turn = 0; vb < VP; vb += COLS, turn ^= 1) {
           char* m = lds.buf[Lds::NBUF == 2 ? turn : 0];
@@ -378,16 +381,10 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
           for (int i = 0; i < N; ++i) {
             const int o = Lds::at(place_of(M_ROWS * i + m_row), m_piece);
             const Op<NP> d = ds[i].op();
-            *reinterpret_cast<bf8_t*>(m + o) = zs[i].hi;
-            *reinterpret_cast<bf8_t*>(m + Lds::PART + o) = zs[i].lo;
-            *reinterpret_cast<bf8_t*>(m + 2 * Lds::PART + o) = ws[i].hi;
-            *reinterpret_cast<bf8_t*>(m + 3 * Lds::PART + o) = ws[i].lo;
+            Lds::put(m, 0, o, zs[i]);
+            Lds::put(m, 2, o, ws[i]);
 #pragma unroll
             for (int p = 0; p < NP; ++p) *reinterpret_cast<bf8_t*>(m + (4 + p) * Lds::PART + o) = d.p[p];
-            float vf[8];
-            vr[i].open(vf);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) wv[i] += vf[e] * ((float)ws[i].hi[e] + (float)ws[i].lo[e]);
           }
           if (vb + COLS < VP) fetch(vb + COLS);
           lds_barrier();
@@ -415,12 +412,6 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
             }
           }
           if (Lds::NBUF == 1) lds_barrier();
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-#pragma unroll
-          for (int o = 1; o < Lds::PIECES; o <<= 1) wv[i] += __shfl_xor(wv[i], o, 64);
-          if (m_piece == 0) lds.wv[M_ROWS * i + m_row] = wv[i];
         }
         keep_order();
         f4_t kk[2], qk[2], xk[2], xq[2];  // rows i: k_i . k_j and q_i . k_j
@@ -462,7 +453,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
         }
         const double Gn = lds.G[tok];
         const float beta_n = lds.beta[tok];
-        float vq[8], vk[8], va[8];
+        float vq[8], vk[8], va[8], c[8];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int r0 = 32 * h + 8 * g + 4 * t;
@@ -476,10 +467,20 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
             vq[4 * t + r] = row <= tok ? a.scale * beta[r] * d * zd[t][r] : 0.f;
             vk[4 * t + r] = beta_n * bz;
             va[4 * t + r] = row < tok ? -beta[r] * d * zw[t][r] : beta_n * az;
-            db += bz * qk[t][r] + az * kk[t][r];
-            own_wz = row == tok ? wz[t][r] : own_wz;
+            const float both = bz * qk[t][r] + az * kk[t][r];
+            db += both;
+            c[4 * t + r] = row > tok ? beta_n * both : 0.f;
           }
         }
+        const auto ends_at = [&](int row0) {  // the pairs' parts by the later token, over the wave's earlier ones
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            late += c[e];
+            c[e] = row16_sum(c[e]);
+          }
+          if (n == 0) store8(lds.row[w] + row0, c);
+        };
+        ends_at(32 * h + 8 * g);
         bq = split(vq);
         bk = split(vk);
         aa = split(va);
@@ -495,11 +496,14 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
             const double G = lds.G[r0 + r];
             const float d = decay(h == 0 ? G - Gn : Gn - G);
             const float bx = a.scale * d * xd[t][r], axx = -d * xw[t][r], be = h == 0 ? beta_n : beta[r];
-            if (h == 0) db += bx * xq[t][r] + axx * xk[t][r];
+            const float both = h == 0 ? bx * xq[t][r] + axx * xk[t][r] : 0.f;
+            db += both;
+            c[4 * t + r] = beta_n * both;
             vq[4 * t + r] = be * bx;
             va[4 * t + r] = be * axx;
           }
         }
+        if (h == 0) ends_at(32 + 8 * g);
         x = split(vq);
         ax = split(va);
         pin(x);
@@ -507,27 +511,27 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
         keep_order();
       }
       // What the states pass on, 64 keys at a time.
-      const Range mp((const bf16_t*)a.states + at * 2 * KP * VP, 4 * KP * VP);
-      const Range np((const bf16_t*)a.dstates + at * 2 * KP * VP, 4 * KP * VP);
-      Split mr[N], nr[N], zn_next[N], wn_next[N];
+      const Range mp((const float*)a.states + at * KP * VP, 4 * KP * VP);
+      const Range np((const float*)a.dstates + at * KP * VP, 4 * KP * VP);
+      F8 mr[N], nr[N], zn_next[N], wn_next[N];
       Op<NP> dn_next[N];
       const auto fetch = [&](int key0, int vb) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          const uint32_t o = vb + m_col < VP ? 2 * ((M_ROWS * i + m_row) * VP + m_col) : NOWHERE;
-          mr[i] = mp.parts(o, 2 * (key0 * VP + vb), slo);
-          nr[i] = np.parts(o, 2 * (key0 * VP + vb), slo);
+          const uint32_t o = vb + m_col < VP ? 4 * ((M_ROWS * i + m_row) * VP + m_col) : NOWHERE;
+          mr[i] = mp.floats(o, 4 * (key0 * VP + vb));
+          nr[i] = np.floats(o, 4 * (key0 * VP + vb));
           const int c = vb + 32 * i + 8 * g;
-          const uint32_t own = c < VP ? 2 * (tok * VP + c) : NOWHERE;
+          const uint32_t own = c < VP ? 4 * (tok * VP + c) : NOWHERE;
           dn_next[i] = token_op<T, VEC>(dop, vs, tok, c, Dv);
-          zn_next[i] = zp.parts(own, 0, vlo);
-          wn_next[i] = wp.parts(own, 0, vlo);
+          zn_next[i] = zp.floats(own, 0);
+          wn_next[i] = wp.floats(own, 0);
         }
       };
       fetch(64 * QUADS * pass, 0);
       const double Gend = lds.G[CH - 1], Gown = lds.G[tok];
       const float ahead = decay(Gown), to_end = decay(Gend - Gown), eb = to_end * lds.beta[tok];
-      float mn = 0.f, qdq = 0.f, at_end = 0.f;  // <M, N>; q . dq; k . (N Z) to the chunk's end
+      float mn = 0.f, from_start = 0.f;  // <M, N>; what the token reads of M
       lds_barrier();  // the buffers held Z, W and dO until here
 #pragma unroll
       for (int quad = 0; quad < QUADS; ++quad) {
@@ -542,16 +546,13 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             const int o = Lds::at(place_of(M_ROWS * i + m_row), m_piece);
-            *reinterpret_cast<bf8_t*>(m + o) = mr[i].hi;
-            *reinterpret_cast<bf8_t*>(m + Lds::PART + o) = mr[i].lo;
-            *reinterpret_cast<bf8_t*>(m + 2 * Lds::PART + o) = nr[i].hi;
-            *reinterpret_cast<bf8_t*>(m + 3 * Lds::PART + o) = nr[i].lo;
+            Lds::put(m, 0, o, mr[i]);
+            Lds::put(m, 2, o, nr[i]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              mn += ((float)mr[i].hi[e] + (float)mr[i].lo[e]) * ((float)nr[i].hi[e] + (float)nr[i].lo[e]);
+            for (int e = 0; e < 4; ++e) mn += mr[i].a[e] * nr[i].a[e] + mr[i].b[e] * nr[i].b[e];
             dn[i] = dn_next[i];
-            zn[i] = zn_next[i];
-            wn[i] = wn_next[i];
+            zn[i] = split(zn_next[i].a, zn_next[i].b);
+            wn[i] = split(wn_next[i].a, wn_next[i].b);
           }
           if (vb + COLS < VP) fetch(key0, vb + COLS);
           else if (quad + 1 < QUADS) fetch(key0 + 64, 0);
@@ -593,8 +594,10 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) ke += kf[4 * u + r] * early[t][r];
             db += to_end * ke;
-            at_end += eb * ke;
+            late += eb * ke;
             dq[t] *= a.scale * ahead;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) from_start += qf[4 * u + r] * dq[t][r] - kf[4 * u + r] * (ahead * read[t][r]);
             dk[t] = eb * early[t] - ahead * read[t];
             Op<NP> ko, qo, kx, qx;
 #pragma unroll
@@ -610,8 +613,6 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
             dk[t] = mma(kx, ax, dk[t]);
             if (h == 0) dk[t] = mma(qx, x, dk[t]);
             else dq[t] = mma(kx, x, dq[t]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) qdq += qf[4 * u + r] * dq[t][r];
             if (SHARED) {
               dqt[4 * quad + t] += dq[t];
               dkt[4 * quad + t] += dk[t];
@@ -621,27 +622,29 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
         }
         if (!SHARED) put(tok, key0, dq, dk);
       }
-      // A token's part of the decays' sums: dO . o = q . dq for what it reads with q,
-      // k . dk as it reads = W . (Z - v), and k . dk as it is written = beta dbeta, which is linear in k as
-      // in beta. <M, N> and the ends' sum are the chunk's.
       db = sum_groups(db);
-      const float dot = sum_groups(pass == 0 ? qdq + own_wz : qdq) - lds.beta[tok] * db - (pass == 0 ? lds.wv[tok] : 0.f);
-      const float ends = wave_sum(at_end + decay(Gend) * mn);
+      late = sum_groups(late);
+      from_start = sum_groups(from_start);
+      const float whole = wave_sum(decay(Gend) * mn);
       if (g == 0) {
-        lds.dG[tok] = dot;
+        lds.read[tok] = from_start;
+        lds.late[tok] = late;
         float* p = a.dbeta + gat + tok * a.Hv;
         if (tok < rows) *p = tok < left ? (pass ? *p + db : db) : 0.f;
       }
-      if (lane == 0) lds.end[w] = ends;
+      if (lane == 0) lds.end[w] = whole;
       lds_barrier();
       if (tid < CH) {
-        float s = lds.dG[tid];
+        float s = lds.read[tid], open = lds.late[tid] - (lds.row[0][tid] + lds.row[1][tid]);
+        if (tid >= CH / 2) open -= lds.row[2][tid] + lds.row[3][tid];
 #pragma unroll
         for (int o = 1; o < CH; o <<= 1) {
-          const float down = __shfl_down(s, o, 64);
+          const float down = __shfl_down(s, o, 64), up = __shfl_up(open, o, 64);
           if (tid + o < CH) s += down;
+          if (tid >= o) open += up;
         }
-        s += (lds.end[0] + lds.end[1]) + (lds.end[2] + lds.end[3]);
+        const float before = __shfl_up(open, 1, 64);
+        s += (tid > 0 ? before : 0.f) + ((lds.end[0] + lds.end[1]) + (lds.end[2] + lds.end[3]));
         float* p = a.dg + gat + tid * a.Hv;
         if (tid < rows) *p = tid < left ? (pass ? *p + s : s) : 0.f;
       }

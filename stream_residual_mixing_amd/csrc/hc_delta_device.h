@@ -66,6 +66,28 @@ __device__ __forceinline__ Split split(f4_t a, f4_t b) {
   return split(v);
 }
 
+// In three parts, float32's own 24 bits: what the walks add to the state passes through the chunks that
+// follow, and two parts of it would be off by 4 x 10^-6 of the state's norm where three leave 5 x 10^-7.
+struct Fine {
+  bf8_t p[3];
+};
+
+__device__ __forceinline__ Fine split_fine(f4_t a, f4_t b) {
+  float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  Fine f;
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+    const u4_t q = pack8(v);
+    f.p[p] = as_bf8(q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] -= __uint_as_float(q[i] << 16);
+      v[2 * i + 1] -= __uint_as_float(q[i] & 0xffff0000u);
+    }
+  }
+  return f;
+}
+
 __device__ __forceinline__ f4_t mma(bf8_t a, bf8_t b, f4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
@@ -74,6 +96,14 @@ __device__ __forceinline__ f4_t mma(const Split& a, const Split& b, f4_t c) {
   c = mma(a.lo, b.hi, c);
   c = mma(a.hi, b.lo, c);
   return mma(a.hi, b.hi, c);
+}
+
+__device__ __forceinline__ f4_t mma(const Split& a, const Fine& b, f4_t c) {
+  c = mma(a.lo, b.p[1], c);
+  c = mma(a.hi, b.p[2], c);
+  c = mma(a.lo, b.p[0], c);
+  c = mma(a.hi, b.p[1], c);
+  return mma(a.hi, b.p[0], c);
 }
 
 // Stream operands: bfloat16 is exact in one part, float32 takes two.
@@ -98,6 +128,14 @@ __device__ __forceinline__ f4_t mma(const Op<NP>& a, const Split& b, f4_t c) {
 }
 
 template <int NP>
+__device__ __forceinline__ f4_t mma(const Op<NP>& a, const Fine& b, f4_t c) {
+  if (NP == 2) return mma(Split{a.p[0], a.p[NP - 1]}, b, c);
+  c = mma(a.p[0], b.p[2], c);
+  c = mma(a.p[0], b.p[1], c);
+  return mma(a.p[0], b.p[0], c);
+}
+
+template <int NP>
 __device__ __forceinline__ f4_t mma(const Split& a, const Op<NP>& b, f4_t c) {
   if (NP == 2) c = mma(a.hi, b.p[NP - 1], c);
   c = mma(a.lo, b.p[0], c);
@@ -118,6 +156,10 @@ __device__ __forceinline__ f4_t mma(const Op<NP>& a, const Op<NP>& b, f4_t c) {
 // missing tokens nor a head's missing keys and columns need a branch. NOWHERE is behind every end
 // and stays so with a row's offset added (both below 2^31).
 constexpr uint32_t NOWHERE = 0x80000000u;
+
+struct F8 {
+  f4_t a, b;
+};
 
 struct Range {
   __amdgpu_buffer_rsrc_t r;
@@ -147,7 +189,12 @@ struct Range {
     __builtin_amdgcn_raw_buffer_store_b16((uint16_t)h, r, o, 0, 0);
     low.put((bf16_t*)nullptr, o, v - __uint_as_float(h << 16));
   }
-  // a kept array's operand, at an offset `s` more that the lanes have in common; inside it
+  // eight floats of a kept array, at an offset `s` more that the lanes have in common; inside it
+  __device__ __forceinline__ F8 floats(uint32_t o, uint32_t s) const {
+    return {__builtin_bit_cast(f4_t, __builtin_amdgcn_raw_buffer_load_b128(r, o, s, 0)),
+            __builtin_bit_cast(f4_t, __builtin_amdgcn_raw_buffer_load_b128(r, o, s + 16, 0))};
+  }
+  // an operand kept in two parts, at an offset `s` more that the lanes have in common; inside it
   __device__ __forceinline__ Split parts(uint32_t o, uint32_t s, uint32_t lo) const {
     return {__builtin_bit_cast(bf8_t, __builtin_amdgcn_raw_buffer_load_b128(r, o, s, 0)),
             __builtin_bit_cast(bf8_t, __builtin_amdgcn_raw_buffer_load_b128(r, o, s + lo, 0))};
@@ -323,7 +370,16 @@ struct State {
 #pragma unroll
       for (int r = 0; r < 4; ++r) m.put(p, lane + 4 * row_of(t, r) * Dv, this->m[t][r]);
   }
-  // [KP, stride] in two parts at p, column `col` of lane 0
+  // [KP, stride] at p, column `col` of lane 0
+  __device__ __forceinline__ void keep(float* p, int stride, int col, int n, int g) const {
+    const Range m(p, 4 * KP * stride);
+    const uint32_t lane = anew(col < stride ? 4 * (8 * g * stride + col + n) : NOWHERE);
+#pragma unroll
+    for (int t = 0; t < KP / 16; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) m.put(p, lane + 4 * row_of(t, r) * stride, this->m[t][r]);
+  }
+  // the same in two parts
   __device__ __forceinline__ void keep(bf16_t* p, int stride, int col, int n, int g) const {
     const Range hi(p, 2 * KP * stride), lo(p + KP * stride, 2 * KP * stride);
     const uint32_t lane = anew(col < stride ? 2 * (8 * g * stride + col + n) : NOWHERE);
@@ -382,14 +438,14 @@ struct Part {
   __device__ __forceinline__ bool ends() const { return last >= chunks; }  // none comes behind it
 };
 
-// Four tiles of a chunk's 64 rows, as [CH, stride] in two parts.
-__device__ __forceinline__ void keep_rows(bf16_t* p, int stride, int col, int n, int g, const f4_t (&x)[4]) {
-  const Range hi(p, 2 * CH * stride), lo(p + CH * stride, 2 * CH * stride);
-  const uint32_t lane = anew(col < stride ? 2 * (8 * g * stride + col + n) : NOWHERE);
+// Four tiles of a chunk's 64 rows, as [CH, stride].
+__device__ __forceinline__ void keep_rows(float* p, int stride, int col, int n, int g, const f4_t (&x)[4]) {
+  const Range m(p, 4 * CH * stride);
+  const uint32_t lane = anew(col < stride ? 4 * (8 * g * stride + col + n) : NOWHERE);
 #pragma unroll
   for (int t = 0; t < 4; ++t)
 #pragma unroll
-    for (int r = 0; r < 4; ++r) hi.put_parts(lo, lane + 2 * row_of(t, r) * stride, x[t][r]);
+    for (int r = 0; r < 4; ++r) m.put(p, lane + 4 * row_of(t, r) * stride, x[t][r]);
 }
 
 // The decay sums are float64 and their differences float32: a difference between two
