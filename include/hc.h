@@ -741,7 +741,7 @@ int hc_gated_scan_backward(const void* x, const void* gate, const void* y, const
  *   lengths (NULL: S each) [B] int32 device array, as hc_gated_scan's: behind a sequence's length
  *   nothing is used, o is left as it was, and state is the one after its last token.
  *   The state and every sum are float32; o is rounded once. More than a few tokens are taken in
- *   chunks of 64, whose products hold 16 bits of each factor that is not bfloat16 already: each
+ *   chunks of 64, whose products hold at least 16 bits of each factor that is not bfloat16 already: each
  *   term of the state is off by at most about 2^-16 of itself. Deterministic. A NaN or an infinity
  *   spoils its head from its chunk's first token on.
  *   dtype HC_F32 or HC_BF16; Hv a multiple of Hk; 1 <= Dk, Dv <= HC_MAX_HEAD; S = 0 passes the state on

@@ -8,16 +8,17 @@
 // chunks, whose columns of the state (and of V, Z, O) never meet: a wave keeps its 16
 // columns' state in registers and hands each product's result to the next as its operand.
 // Products are bfloat16 matrix instructions with float32 sums; values that are not bfloat16
-// already (the state, Z, T, P, float32 streams) enter as two parts, 16 bits, so that the
-// state carries errors of 2^-17 of its terms rather than 2^-9: 2 to 8 x 10^-6 of the norm of
-// states, gradients and float32 outputs, measured. Sums, states in registers and the
-// states that are given and returned are float32. (Three parts would keep float32's own
-// 24 bits, for twice the products and half as much LDS again, which a CU has not got at
-// 256 x 256; bfloat16 outputs are far above both.)
+// already enter as two parts, 16 bits of each (T, P, float32 streams), or as three, float32's 24
+// (the state, R = V - exp(G) K M and X, whose products the state takes up and hands on). Of
+// their norm, measured: the state is off by 6 x 10^-7 with bfloat16 streams (two parts throughout
+// 3.5 x 10^-6) and by 2 to 3 x 10^-6 with float32 ones, float32 outputs by 5 x 10^-6. Sums and
+// states are float32 throughout. (Three parts of float32 streams, T and P would leave
+// float32's own roundings, for half as much LDS again, which a CU has not got at 256 x 256;
+// bfloat16 outputs round by far more.)
 //   What bounds it: 2,048 chunks of 128 x 128 in bfloat16 (8 sequences of 1,024 tokens, 16 value
 // heads on 8 key heads) read and write 118 MB and need 15 GFLOP, 20 us of memory; the chunks
-// by themselves take 38 us (latency of the triangle's inverse), the walk 79 us as 16 chunks in
-// a row on 256 workgroups, 5 us a chunk of which the matrix units work for 1: each product
+// by themselves take 38 us (latency of the triangle's inverse), the walk 88 us as 16 chunks in
+// a row on 256 workgroups, 5.5 us a chunk of which the matrix units work for 1: each product
 // waits for the one before it. Hence few heads are walked in segments at once (see
 // delta_plan), and what does not depend on the state is done by every chunk for itself.
 #include "hc_delta_device.h"

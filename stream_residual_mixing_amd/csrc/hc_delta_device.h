@@ -30,7 +30,8 @@ __device__ __forceinline__ int row_of(int t, int m) { return 32 * (t >> 1) + 8 *
 __device__ __forceinline__ int place_of(int x) { return (x & ~31) + 16 * ((x >> 2) & 1) + 4 * ((x >> 3) & 3) + (x & 3); }
 
 // Eight float32 values as the sum of two bfloat16 parts, 16 bits of each value: the part left
-// over is at most 2^-17 of it. Products of two such operands keep hi hi + hi lo + lo hi.
+// over is at most 2^-17 of it. Products of two such operands keep hi hi + hi lo + lo hi, and those of
+// float32 streams lo lo as well.
 struct Split {
   bf8_t hi, lo;
 };
@@ -122,7 +123,7 @@ struct Op {
 
 template <int NP>
 __device__ __forceinline__ f4_t mma(const Op<NP>& a, const Split& b, f4_t c) {
-  if (NP == 2) c = mma(a.p[NP - 1], b.hi, c);
+  if (NP == 2) c = mma(a.p[NP - 1], b.hi, mma(a.p[NP - 1], b.lo, c));
   c = mma(a.p[0], b.lo, c);
   return mma(a.p[0], b.hi, c);
 }
@@ -137,7 +138,7 @@ __device__ __forceinline__ f4_t mma(const Op<NP>& a, const Fine& b, f4_t c) {
 
 template <int NP>
 __device__ __forceinline__ f4_t mma(const Split& a, const Op<NP>& b, f4_t c) {
-  if (NP == 2) c = mma(a.hi, b.p[NP - 1], c);
+  if (NP == 2) c = mma(a.hi, b.p[NP - 1], mma(a.lo, b.p[NP - 1], c));
   c = mma(a.lo, b.p[0], c);
   return mma(a.hi, b.p[0], c);
 }
@@ -145,6 +146,7 @@ __device__ __forceinline__ f4_t mma(const Split& a, const Op<NP>& b, f4_t c) {
 template <int NP>
 __device__ __forceinline__ f4_t mma(const Op<NP>& a, const Op<NP>& b, f4_t c) {
   if (NP == 2) {
+    c = mma(a.p[NP - 1], b.p[NP - 1], c);
     c = mma(a.p[NP - 1], b.p[0], c);
     c = mma(a.p[0], b.p[NP - 1], c);
   }

@@ -102,7 +102,7 @@ struct DeltaArgs {
   void* phi;               // [B, Hv, NS, 2, KP, KP] its map of the state, in two bfloat16 parts
   void* phi_t;             // the same transposed; KP is Dk as 64, 128 or 256
   void* states;            // backward: every chunk's first state [KP, VP] and Z [64, VP], and the gradient
-  void* z;                 // of the state behind it and W of the same shapes, in two bfloat16 parts
+  void* z;                 // of the state behind it and W of the same shapes, float32
   void* dstates;
   void* w;
 };
