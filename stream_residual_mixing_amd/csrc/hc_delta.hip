@@ -8,13 +8,12 @@
 // chunks, whose columns of the state (and of V, Z, O) never meet: a wave keeps its 16
 // columns' state in registers and hands each product's result to the next as its operand.
 // Products are bfloat16 matrix instructions with float32 sums; values that are not bfloat16
-// already enter as two parts, 16 bits of each (T, P, float32 streams), or as three, float32's 24
-// (the state, R = V - exp(G) K M and X, whose products the state takes up and hands on). Of
-// their norm, measured: the state is off by 6 x 10^-7 with bfloat16 streams (two parts throughout
-// 3.5 x 10^-6) and by 2 to 3 x 10^-6 with float32 ones, float32 outputs by 5 x 10^-6. Sums and
-// states are float32 throughout. (Three parts of float32 streams, T and P would leave
-// float32's own roundings, for half as much LDS again, which a CU has not got at 256 x 256;
-// bfloat16 outputs round by far more.)
+// already enter as two parts, 16 bits of each (T, P), or as three, float32's 24 (the state,
+// R = V - exp(G) K M and X, whose products the state takes up and hands on, and float32 keys and
+// queries up to 128; a CU has no LDS for three parts of 256). Of its norm, measured, the state is
+// off by 6 x 10^-7 (with two parts throughout 3.5 x 10^-6, with float32 streams 5 x 10^-6; with those
+// of 256 keys 2 to 3 x 10^-6), and float32 outputs by 2 x 10^-6. Sums and states are float32
+// throughout. For this a walk takes a tenth longer, for float32 streams a quarter.
 //   What bounds it: 2,048 chunks of 128 x 128 in bfloat16 (8 sequences of 1,024 tokens, 16 value
 // heads on 8 key heads) read and write 118 MB and need 15 GFLOP, 20 us of memory; the chunks
 // by themselves take 38 us (latency of the triangle's inverse), the walk 88 us as 16 chunks in
@@ -31,7 +30,7 @@ namespace {
 
 template <typename T, int KP, bool VEC, bool BWD>
 __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
-  constexpr int NP = Stream<T>::NP, KB = KP / 32, LS = CH + 4;
+  constexpr int NP = WALK_PARTS<T, KP>, KB = KP / 32, LS = CH + 4;
   __shared__ __attribute__((aligned(16))) float L[CH][LS], inv[CH][LS];
   __shared__ double G[CH];
   __shared__ __attribute__((aligned(16))) float beta_s[CH];
@@ -53,16 +52,16 @@ __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) {
     const int k0 = 32 * kb + 8 * g;
-    const Op<NP> kn = token_op<T, VEC>(k, qs, 16 * w + n, k0, Dk);
-    const Op<NP> qn = token_op<T, VEC>(q, qs, 16 * w + n, k0, Dk);
+    const Op<NP> kn = token_op<T, VEC, NP>(k, qs, 16 * w + n, k0, Dk);
+    const Op<NP> qn = token_op<T, VEC, NP>(q, qs, 16 * w + n, k0, Dk);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       if ((t >> 1) <= (w >> 1)) {
-        const Op<NP> kr = token_op<T, VEC>(k, qs, row_of(t, n), k0, Dk);
+        const Op<NP> kr = token_op<T, VEC, NP>(k, qs, row_of(t, n), k0, Dk);
         kk[t] = mma(kr, kn, kk[t]);
         qk[t] = mma(kr, qn, qk[t]);
       }
-      if (BWD && (t >> 1) >= (w >> 1)) kq[t] = mma(token_op<T, VEC>(q, qs, row_of(t, n), k0, Dk), kn, kq[t]);
+      if (BWD && (t >> 1) >= (w >> 1)) kq[t] = mma(token_op<T, VEC, NP>(q, qs, row_of(t, n), k0, Dk), kn, kq[t]);
     }
     keep_order();
   }
@@ -201,8 +200,8 @@ struct WalkLds {
 // segment's from its own) and, as further columns that start as the unit matrix without values, its
 // map of the state; SUM_BWD: the map's transpose too.
 template <typename T, int KP, int NW, bool VEC, int MODE>
-__global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, Stream<T>::NP, NW, MODE>>)) void delta_walk_kernel(DeltaArgs a) {
-  constexpr int NP = Stream<T>::NP, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
+__global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, WALK_PARTS<T, KP>, NW, MODE>>)) void delta_walk_kernel(DeltaArgs a) {
+  constexpr int NP = WALK_PARTS<T, KP>, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
   constexpr int PIECES = KP / 8, ITEMS = (CH * PIECES + THREADS - 1) / THREADS;
   constexpr int STRIDE = MODE == KEEP || MODE == SUM_BWD ? REC_BWD : REC, USED = MODE == OUT ? REC : REC_P;
   constexpr int RR = (USED + 16 * THREADS - 1) / (16 * THREADS);
@@ -275,11 +274,11 @@ __global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, Stream<T>::NP, NW, MODE
     for (int i = 0; i < ITEMS; ++i) {
       const int x = i * THREADS + tid, piece = x % PIECES, row = x / PIECES;
       if (CH * PIECES % THREADS == 0 || row < CH) {
-        const Op<NP> ko = kr[i].op();
+        const Op<NP> ko = kr[i].template op<NP>();
 #pragma unroll
         for (int p = 0; p < NP; ++p) *reinterpret_cast<bf8_t*>(lds.k[p] + Tk::at(place_of(row), piece)) = ko.p[p];
         if (MODE == OUT) {
-          const Op<NP> qo = qr[i].op();
+          const Op<NP> qo = qr[i].template op<NP>();
 #pragma unroll
           for (int p = 0; p < NP; ++p) *reinterpret_cast<bf8_t*>(lds.q[p] + Tk::at(row, piece)) = qo.p[p];
         }
@@ -578,7 +577,7 @@ constexpr int SHORT = 6;
 template <typename T, int KP, int MODE>
 hipError_t walk_go(const DeltaArgs& a, hipStream_t st) {
   constexpr int NW = 4;
-  const size_t lds = sizeof(WalkLds<KP, Stream<T>::NP, NW, MODE>);
+  const size_t lds = sizeof(WalkLds<KP, WALK_PARTS<T, KP>, NW, MODE>);
   const unsigned groups = (unsigned)((a.Dv + 16 * NW - 1) / (16 * NW)) + (MODE >= SUM ? KP / (16 * NW) : 0);
   const dim3 grid((unsigned)(a.B * a.Hv * a.NS) * groups);
   const auto go = [&](auto kernel) {

@@ -35,8 +35,8 @@ struct BackLds {
 // FULL: as above, over a segment's chunks. Otherwise a segment's first gradient from zeros (the last
 // segment's from its own), nothing else.
 template <typename T, int KP, int NW, bool VEC, bool FULL>
-__global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, Stream<T>::NP, NW>>)) void delta_back_kernel(DeltaArgs a) {
-  constexpr int NP = Stream<T>::NP, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
+__global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, WALK_PARTS<T, KP>, NW>>)) void delta_back_kernel(DeltaArgs a) {
+  constexpr int NP = WALK_PARTS<T, KP>, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
   constexpr int PIECES = KP / 8, ITEMS = (CH * PIECES + THREADS - 1) / THREADS;
   constexpr int USED = REC_BWD - REC_DEC, RR = (USED + 16 * THREADS - 1) / (16 * THREADS);
   constexpr int PT = REC_P - REC_DEC, TT = REC_TT - REC_DEC;
@@ -96,7 +96,7 @@ __global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, Stream<T>::NP, NW>>)) v
     for (int i = 0; i < ITEMS; ++i) {
       const int x = i * THREADS + tid, piece = x % PIECES, row = x / PIECES;
       if (CH * PIECES % THREADS == 0 || row < CH) {
-        const Op<NP> ko = kr[i].op(), qo = qr[i].op();
+        const Op<NP> ko = kr[i].template op<NP>(), qo = qr[i].template op<NP>();
 #pragma unroll
         for (int p = 0; p < NP; ++p) {
           const int at = Tk::at(place_of(row), piece);
@@ -135,9 +135,9 @@ __global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, Stream<T>::NP, NW>>)) v
       Op<NP> df[2];
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
-        const Split s = split(d[2 * kb], d[2 * kb + 1]);  // bfloat16 is its own high part
-        df[kb].p[0] = s.hi;
-        if (NP == 2) df[kb].p[NP - 1] = s.lo;
+        const Fine s = split_fine(d[2 * kb], d[2 * kb + 1]);  // bfloat16 is its own high part
+#pragma unroll
+        for (int p = 0; p < NP; ++p) df[kb].p[p] = s.p[p];
       }
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -380,7 +380,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             const int o = Lds::at(place_of(M_ROWS * i + m_row), m_piece);
-            const Op<NP> d = ds[i].op();
+            const Op<NP> d = ds[i].template op<NP>();
             Lds::put(m, 0, o, zs[i]);
             Lds::put(m, 2, o, ws[i]);
 #pragma unroll
@@ -670,7 +670,7 @@ template <typename T, int KP, bool FULL>
 hipError_t back_go(const DeltaArgs& a, hipStream_t st) {
   constexpr int NW = 4;
   const unsigned grid = (unsigned)(a.B * a.Hv * a.NS * ((a.Dv + 16 * NW - 1) / (16 * NW)));
-  const size_t lds = sizeof(BackLds<KP, Stream<T>::NP, NW>);
+  const size_t lds = sizeof(BackLds<KP, WALK_PARTS<T, KP>, NW>);
   return a.vec ? with_lds(delta_back_kernel<T, KP, NW, true, FULL>, lds, grid, 64 * NW, a, st)
                : with_lds(delta_back_kernel<T, KP, NW, false, FULL>, lds, grid, 64 * NW, a, st);
 }

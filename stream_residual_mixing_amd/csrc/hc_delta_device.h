@@ -116,6 +116,11 @@ template <> struct Stream<float> {
   static constexpr int NP = 2;
 };
 
+// The walks, whose states pass their errors on, and the triangles: three parts where LDS has room for them (dg of
+// heads that forget fast is off by 10^-5 of its norm with two).
+template <typename T, int KP>
+constexpr int WALK_PARTS = Stream<T>::NP == 2 && KP <= 128 ? 3 : Stream<T>::NP;
+
 template <int NP>
 struct Op {
   bf8_t p[NP];
@@ -128,8 +133,19 @@ __device__ __forceinline__ f4_t mma(const Op<NP>& a, const Split& b, f4_t c) {
   return mma(a.p[0], b.hi, c);
 }
 
+// three parts of each: what 24 bits leave
+__device__ __forceinline__ f4_t mma(const bf8_t (&a)[3], const bf8_t (&b)[3], f4_t c) {
+  c = mma(a[1], b[1], c);
+  c = mma(a[2], b[0], c);
+  c = mma(a[0], b[2], c);
+  c = mma(a[1], b[0], c);
+  c = mma(a[0], b[1], c);
+  return mma(a[0], b[0], c);
+}
+
 template <int NP>
 __device__ __forceinline__ f4_t mma(const Op<NP>& a, const Fine& b, f4_t c) {
+  if constexpr (NP == 3) return mma(a.p, b.p, c);
   if (NP == 2) return mma(Split{a.p[0], a.p[NP - 1]}, b, c);
   c = mma(a.p[0], b.p[2], c);
   c = mma(a.p[0], b.p[1], c);
@@ -138,6 +154,7 @@ __device__ __forceinline__ f4_t mma(const Op<NP>& a, const Fine& b, f4_t c) {
 
 template <int NP>
 __device__ __forceinline__ f4_t mma(const Split& a, const Op<NP>& b, f4_t c) {
+  if constexpr (NP == 3) return mma(a, Fine{b.p[0], b.p[1], b.p[2]}, c);
   if (NP == 2) c = mma(a.hi, b.p[NP - 1], mma(a.lo, b.p[NP - 1], c));
   c = mma(a.lo, b.p[0], c);
   return mma(a.hi, b.p[0], c);
@@ -145,6 +162,7 @@ __device__ __forceinline__ f4_t mma(const Split& a, const Op<NP>& b, f4_t c) {
 
 template <int NP>
 __device__ __forceinline__ f4_t mma(const Op<NP>& a, const Op<NP>& b, f4_t c) {
+  if constexpr (NP == 3) return mma(a.p, b.p, c);
   if (NP == 2) {
     c = mma(a.p[NP - 1], b.p[NP - 1], c);
     c = mma(a.p[NP - 1], b.p[0], c);
@@ -226,7 +244,8 @@ template <> struct Raw8<bf16_t> {
                (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(m.r, 2 * i + 1 < cnt ? o + 4 * i + 2 : NOWHERE, 0, 0) << 16;
     }
   }
-  __device__ __forceinline__ Op<1> op() const { return {as_bf8(q)}; }
+  template <int NP>
+  __device__ __forceinline__ Op<NP> op() const { return {as_bf8(q)}; }
   __device__ __forceinline__ void open(float v[8]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -250,9 +269,15 @@ template <> struct Raw8<float> {
       }
     }
   }
-  __device__ __forceinline__ Op<2> op() const {
-    const Split s = split(a, b);
-    return {s.hi, s.lo};
+  template <int NP>
+  __device__ __forceinline__ Op<NP> op() const {
+    if constexpr (NP == 3) {
+      const Fine f = split_fine(a, b);
+      return {f.p[0], f.p[1], f.p[2]};
+    } else {
+      const Split s = split(a, b);
+      return {s.hi, s.lo};
+    }
   }
   __device__ __forceinline__ void open(float v[8]) const {
 #pragma unroll
@@ -261,11 +286,11 @@ template <> struct Raw8<float> {
 };
 
 // Eight keys of a row from k0 on, as an operand.
-template <typename T, bool VEC>
-__device__ __forceinline__ Op<Stream<T>::NP> token_op(const Range& m, uint32_t stride, int row, int k0, int width) {
+template <typename T, bool VEC, int NP = Stream<T>::NP>
+__device__ __forceinline__ Op<NP> token_op(const Range& m, uint32_t stride, int row, int k0, int width) {
   Raw8<T> x;
   x.template load<VEC>(m, (row * stride + k0) * (uint32_t)sizeof(T), width - k0);
-  return x.op();
+  return x.template op<NP>();
 }
 
 // Tokens of sequence b.
