@@ -30,8 +30,7 @@ __device__ __forceinline__ int row_of(int t, int m) { return 32 * (t >> 1) + 8 *
 __device__ __forceinline__ int place_of(int x) { return (x & ~31) + 16 * ((x >> 2) & 1) + 4 * ((x >> 3) & 3) + (x & 3); }
 
 // Eight float32 values as the sum of two bfloat16 parts, 16 bits of each value: the part left
-// over is at most 2^-17 of it. Products of two such operands keep hi hi + hi lo + lo hi, and those of
-// float32 streams lo lo as well.
+// over is at most 2^-17 of it. Products of two such operands keep all four terms.
 struct Split {
   bf8_t hi, lo;
 };
@@ -94,6 +93,7 @@ __device__ __forceinline__ f4_t mma(bf8_t a, bf8_t b, f4_t c) {
 }
 
 __device__ __forceinline__ f4_t mma(const Split& a, const Split& b, f4_t c) {
+  c = mma(a.lo, b.lo, c);
   c = mma(a.lo, b.hi, c);
   c = mma(a.hi, b.lo, c);
   return mma(a.hi, b.hi, c);
