@@ -17,9 +17,9 @@
 // head in one workgroup, so that dQ and dK are summed in registers and in a fixed order.
 //   2,048 chunks of 128 x 128 (2 x 4,096 tokens, 16 value heads on 8 key heads, bfloat16), with segments: the
 // forward's part 227 us, the walks back 199, the chunks' own part 225. That one reads the states that the
-// walks kept, 64 KB a chunk and direction in float32, and Z and W, these more than once
-// (400 MB, 645 MB of reads at 2.9 TB/s), on one
-// workgroup a CU, whose registers hold dQ and dK; its steps wait for memory and barriers.
+// walks kept, 64 KB a chunk and direction in float32, and Z and W, these more than once (400 MB, 619 MB of
+// reads at 2.8 TB/s), on one workgroup a CU, whose registers hold dQ and dK; its steps wait for memory
+// and barriers.
 #include "hc_delta_device.h"
 
 namespace hc {
@@ -211,8 +211,8 @@ __global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, WALK_PARTS<T, KP>, NW>>
 
 // What each chunk's workgroup of four waves, 16 tokens each, brings through LDS, in turn in NBUF
 // buffers: Z, W (two parts each) and dO, 64 tokens by COLS columns, and then the state and its gradient
-// (two parts each), 64 keys by COLS columns. Each step waits for memory once: steps of 32 columns took
-// 27 us a head of 128 x 128.
+// (two parts each), 64 keys by COLS columns. Each step waits for memory once: steps of 32 columns
+// took 277 us for 2,048 chunks of 128 x 128 where these take 226.
 template <int KP, int NP>
 struct GradLds {
   static constexpr int COLS = KP == 256 && NP == 2 ? 32 : 64, PIECES = COLS / 8, PART = CH * COLS * 2;

@@ -234,6 +234,18 @@ def test_beta_of_zero_one_and_scale():
         check_forward(o, last, [q, k, v, g, be, M], None, "f32", scale)
 
 
+@pytest.mark.parametrize("S", [6, 7, 200])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_beta_up_to_two(S, dt):
+    """Up to beta = 2 a token's map of the state has no norm above 1 (but for bfloat16's rounding of unit keys,
+    2 x 2 x 2^-9 of it a token at most, e^(S 2^-7) over all of them). Six tokens go one by one, seven as a chunk."""
+    note(f"beta in (0, 2), S={S}")
+    ins = inputs(2, S, 1, 2, 64, 40, dt, seed=77)
+    ins[4] = 2 * ins[4]
+    o, M = hc.hc_gated_delta(*ins)
+    check_forward(o, M, ins, None, dt, slack=np.exp(S * 2.0 ** -7) if dt == "bf16" else 1)
+
+
 @pytest.mark.parametrize("S", [2, 90])
 def test_a_nan_stays_in_its_head_and_later_tokens(S):
     note(f"hc_gated_delta S={S}: NaN")
