@@ -246,13 +246,6 @@ template <> struct Raw8<bf16_t> {
   }
   template <int NP>
   __device__ __forceinline__ Op<NP> op() const { return {as_bf8(q)}; }
-  __device__ __forceinline__ void open(float v[8]) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(q[i] << 16);
-      v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
-    }
-  }
 };
 template <> struct Raw8<float> {
   f4_t a, b;
@@ -278,10 +271,6 @@ template <> struct Raw8<float> {
       const Split s = split(a, b);
       return {s.hi, s.lo};
     }
-  }
-  __device__ __forceinline__ void open(float v[8]) const {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
   }
 };
 
