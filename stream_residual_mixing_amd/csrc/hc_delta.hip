@@ -7,13 +7,12 @@
 // Two kernels: every chunk's triangle, its inverse T and P by themselves, and the walk over the
 // chunks, whose columns of the state (and of V, Z, O) never meet: a wave keeps its 16
 // columns' state in registers and hands each product's result to the next as its operand.
-// Products are bfloat16 matrix instructions with float32 sums; values that are not bfloat16
-// already enter as two parts, 16 bits of each (T, P), or as three, float32's 24 (the state,
-// R = V - exp(G) K M and X, whose products the state takes up and hands on, and float32 keys and
-// queries up to 128; a CU has no LDS for three parts of 256). Of its norm, measured, the state is
-// off by 6 x 10^-7 (with two parts throughout 3.5 x 10^-6, with float32 streams 5 x 10^-6; with those
-// of 256 keys 2 to 3 x 10^-6), and float32 outputs by 2 x 10^-6. Sums and states are float32
-// throughout. For this a walk takes a tenth longer, for float32 streams a quarter.
+// Products are bfloat16 matrix instructions with float32 sums; values that are not bfloat16 already enter
+// as three parts, float32's 24 bits, and the six products of parts that matter (with two parts, 16 bits,
+// states were off by 7 x 10^-7 of their norm and float32 outputs by 2 to 4 x 10^-6 where a float32 form is by 2
+// and 3 x 10^-7; as they are now they are within that, and bfloat16 outputs differ from it in a tenth of the
+// roundings. For this a walk takes a tenth longer, of 256 float32 keys a quarter). T and P lie in the record as
+// float32, which is smaller than three parts, and are split where they enter LDS, once for all waves.
 //   What bounds it: 2,048 chunks of 128 x 128 in bfloat16 (8 sequences of 1,024 tokens, 16 value
 // heads on 8 key heads) read and write 118 MB and need 15 GFLOP, 20 us of memory; the chunks
 // by themselves take 38 us (latency of the triangle's inverse), the walk 88 us as 16 chunks in
@@ -30,7 +29,7 @@ namespace {
 
 template <typename T, int KP, bool VEC, bool BWD>
 __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
-  constexpr int NP = WALK_PARTS<T, KP>, KB = KP / 32, LS = CH + 4;
+  constexpr int NP = WALK_PARTS<T>, KB = KP / 32, LS = CH + 4;
   __shared__ __attribute__((aligned(16))) float L[CH][LS], inv[CH][LS];
   __shared__ double G[CH];
   __shared__ __attribute__((aligned(16))) float beta_s[CH];
@@ -189,10 +188,10 @@ constexpr int OUT = 0, KEEP = 1, SUM = 2, SUM_BWD = 3;
 
 template <int KP, int NP, int NW, int MODE>
 struct WalkLds {
-  static constexpr int PASS = 1024 * NW;  // bytes that the threads bring in at once
+  static constexpr bool TURN = MODE == OUT && NP == 3 && KP == 256;  // no room for both: keys after queries, in k
   char k[NP][Tokens<KP>::BYTES];  // rows in row_of's order
-  char q[MODE == OUT ? NP : 1][MODE == OUT ? Tokens<KP>::BYTES : 16];
-  char rec[((MODE == OUT ? REC : REC_P) + PASS - 1) / PASS * PASS];
+  char q[MODE == OUT && !TURN ? NP : 1][MODE == OUT && !TURN ? Tokens<KP>::BYTES : 16];
+  Record<MODE == OUT ? 2 : 1, 64 * NW> rec;
 };
 
 // NW waves of 16 columns over a segment's chunks. OUT: the forward's. KEEP: the backward's, which wants
@@ -200,16 +199,17 @@ struct WalkLds {
 // segment's from its own) and, as further columns that start as the unit matrix without values, its
 // map of the state; SUM_BWD: the map's transpose too.
 template <typename T, int KP, int NW, bool VEC, int MODE>
-__global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, WALK_PARTS<T, KP>, NW, MODE>>)) void delta_walk_kernel(DeltaArgs a) {
-  constexpr int NP = WALK_PARTS<T, KP>, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
+__global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, WALK_PARTS<T>, NW, MODE>>)) void delta_walk_kernel(DeltaArgs a) {
+  constexpr int NP = WALK_PARTS<T>, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
   constexpr int PIECES = KP / 8, ITEMS = (CH * PIECES + THREADS - 1) / THREADS;
   constexpr int STRIDE = MODE == KEEP || MODE == SUM_BWD ? REC_BWD : REC, USED = MODE == OUT ? REC : REC_P;
-  constexpr int RR = (USED + 16 * THREADS - 1) / (16 * THREADS);
   extern __shared__ __attribute__((aligned(16))) char lds_raw[];
   typedef WalkLds<KP, NP, NW, MODE> Lds;
   typedef Tokens<KP> Tk;
+  constexpr bool TURN = Lds::TURN;
   static_assert(sizeof(Lds) <= 160 * 1024, "LDS of a CU");
   Lds& lds = *reinterpret_cast<Lds*>(lds_raw);
+  char(*const lds_q)[Tk::BYTES] = reinterpret_cast<char(*)[Tk::BYTES]>(TURN ? lds.k[0] : lds.q[0]);
   const int tid = threadIdx.x, lane = tid & 63, w = wave_number(), n = lane & 15, g = lane >> 4;
   const int rows_at = Tk::lane_at(n, g), cols_at = Tk::lane_at_t(n, g);
   const int Dk = (int)a.Dk, Dv = (int)a.Dv, VP = (int)a.VP, qs = (int)a.Hk * Dk, vs = (int)a.Hv * Dv;
@@ -245,7 +245,7 @@ __global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, WALK_PARTS<T, KP>, NW, 
 
   // the next chunk's operands on their way
   Raw8<T> kr[ITEMS], qr[ITEMS];
-  u4_t rr[RR];
+  typename decltype(lds.rec)::Raw rr;
   float vr[4][4];
   const auto fetch = [&](int64_t c) {
     const int left = (int)min((int64_t)CH, len - c * CH);
@@ -261,73 +261,80 @@ __global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, WALK_PARTS<T, KP>, NW, 
       kr[i].template load<VEC>(kc, o, Dk - 8 * piece);
       if (MODE == OUT) qr[i].template load<VEC>(qc, o, Dk - 8 * piece);
     }
-#pragma unroll
-    for (int i = 0; i < RR; ++i) rr[i] = rc.quad((i * THREADS + tid) * 16);
+    rr.load(rc, REC_T, tid);
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) vr[t][r] = vc.get((const T*)nullptr, vl + row_of(t, r) * vs * (uint32_t)sizeof(T));
   };
-  if (part.first < part.last) fetch(part.first);
-  for (int64_t c = part.first; c < part.last; ++c) {
+  const auto put = [&](char(*m)[Tk::BYTES], const Raw8<T>(&raw)[ITEMS], bool in_order) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int x = i * THREADS + tid, piece = x % PIECES, row = x / PIECES;
       if (CH * PIECES % THREADS == 0 || row < CH) {
-        const Op<NP> ko = kr[i].template op<NP>();
+        const Op<NP> o = raw[i].template op<NP>();
 #pragma unroll
-        for (int p = 0; p < NP; ++p) *reinterpret_cast<bf8_t*>(lds.k[p] + Tk::at(place_of(row), piece)) = ko.p[p];
-        if (MODE == OUT) {
-          const Op<NP> qo = qr[i].template op<NP>();
-#pragma unroll
-          for (int p = 0; p < NP; ++p) *reinterpret_cast<bf8_t*>(lds.q[p] + Tk::at(row, piece)) = qo.p[p];
-        }
+        for (int p = 0; p < NP; ++p) *reinterpret_cast<bf8_t*>(m[p] + Tk::at(in_order ? row : place_of(row), piece)) = o.p[p];
       }
     }
-#pragma unroll
-    for (int i = 0; i < RR; ++i) *reinterpret_cast<u4_t*>(lds.rec + (i * THREADS + tid) * 16) = rr[i];
+  };
+  if (part.first < part.last) fetch(part.first);
+  for (int64_t c = part.first; c < part.last; ++c) {
+    if (!TURN) put(lds.k, kr, false);
+    if (MODE == OUT) put(lds_q, qr, true);
+    lds.rec.put(rr, tid);
     f4_t v[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) v[t] = f4_t{vr[t][0], vr[t][1], vr[t][2], vr[t][3]};
     lds_barrier();
-    if (c + 1 < part.last) fetch(c + 1);
+    if (!TURN && c + 1 < part.last) fetch(c + 1);
     if (MODE == KEEP) S.keep((float*)a.states + (bh * a.NC + c) * KP * VP, VP, col, n, g);
 
     // K M and Q M
     f4_t x[4], o[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) x[t] = o[t] = f4_t{0.f, 0.f, 0.f, 0.f};
+    const auto by_state = [&](bool by_k, bool by_q) {
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-      const Fine sf = split_fine(S.m[2 * kb], S.m[2 * kb + 1]);
+      for (int kb = 0; kb < KB; ++kb) {
+        const Fine sf = split<3>(S.m[2 * kb], S.m[2 * kb + 1]);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        Op<NP> ka, qa;
+        for (int t = 0; t < 4; ++t) {
+          Op<NP> ka, qa;
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          ka.p[p] = Tk::rows(lds.k[p], rows_at, t, kb);
-          if (MODE == OUT) qa.p[p] = Tk::rows(lds.q[p], rows_at, t, kb);
+          for (int p = 0; p < NP; ++p) {
+            if (by_k) ka.p[p] = Tk::rows(lds.k[p], rows_at, t, kb);
+            if (by_q) qa.p[p] = Tk::rows(lds_q[p], rows_at, t, kb);
+          }
+          if (by_k) x[t] = mma(ka, sf, x[t]);
+          if (by_q) o[t] = mma(qa, sf, o[t]);
         }
-        x[t] = mma(ka, sf, x[t]);
-        if (MODE == OUT) o[t] = NP == 1 ? mma(qa, Split{sf.p[0], sf.p[1]}, o[t]) : mma(qa, sf, o[t]);
+        keep_order();
       }
-      keep_order();
+    };
+    by_state(!TURN, MODE == OUT);
+    if (TURN) {
+      lds_barrier();
+      put(lds.k, kr, false);
+      lds_barrier();
+      if (c + 1 < part.last) fetch(c + 1);
+      by_state(true, false);
     }
     // R = V - exp(G) K M, Z = T R, X = beta Z
-    const float* dec = (const float*)(lds.rec + REC_DEC);
+    const float* dec = lds.rec.dec;
     Fine f[2];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       x[t] = v[t] - *reinterpret_cast<const f4_t*>(dec + DEC_AHEAD + row_of(t, 4 * g)) * x[t];
     }
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) f[kb] = split_fine(x[2 * kb], x[2 * kb + 1]);
+    for (int kb = 0; kb < 2; ++kb) f[kb] = split<3>(x[2 * kb], x[2 * kb + 1]);
 #pragma unroll
     for (int t = 0; t < 4; ++t) x[t] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
-      for (int t = 2 * kb; t < 4; ++t) x[t] = mma(load_tile(lds.rec + REC_T, tri(t, kb), lane), f[kb], x[t]);
+      for (int t = 2 * kb; t < 4; ++t) x[t] = mma(lds.rec.tile(0, tri(t, kb), lane), f[kb], x[t]);
       keep_order();
     }
     if (MODE == KEEP) keep_rows((float*)a.z + (bh * a.NC + c) * CH * VP, VP, col, n, g, x);
@@ -335,17 +342,14 @@ __global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, WALK_PARTS<T, KP>, NW, 
     for (int t = 0; t < 4; ++t) x[t] *= *reinterpret_cast<const f4_t*>(dec + DEC_BETA + row_of(t, 4 * g));
     if (MODE == OUT) {  // O = scale (exp(G) Q M + P X)
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) f[kb] = split_fine(x[2 * kb], x[2 * kb + 1]);
+      for (int kb = 0; kb < 2; ++kb) f[kb] = split<3>(x[2 * kb], x[2 * kb + 1]);
       const Range oc = head_rows((T*)a.o + values + c * CH * vs, have > 0 ? (int)min((int64_t)CH, len - c * CH) : 0, vs, have);
       const uint32_t ol = anew(o_lane);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         o[t] *= *reinterpret_cast<const f4_t*>(dec + DEC_AHEAD + 16 * t + 4 * g);
 #pragma unroll
-        for (int kb = 0; kb <= (t >> 1); ++kb) {
-          const Split p = load_tile(lds.rec + REC_P, tri(t, kb), lane);
-          o[t] = NP == 1 ? mma(p, Split{f[kb].p[0], f[kb].p[1]}, o[t]) : mma(p, f[kb], o[t]);
-        }
+        for (int kb = 0; kb <= (t >> 1); ++kb) o[t] = mma(lds.rec.tile(1, tri(t, kb), lane), f[kb], o[t]);
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           oc.put((T*)nullptr, ol + (16 * t + r) * vs * (uint32_t)sizeof(T), a.scale * o[t][r]);
@@ -356,7 +360,7 @@ __global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, WALK_PARTS<T, KP>, NW, 
 #pragma unroll
     for (int t = 0; t < 4; ++t) x[t] *= *reinterpret_cast<const f4_t*>(dec + DEC_TO_END + row_of(t, 4 * g));
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) f[kb] = split_fine(x[2 * kb], x[2 * kb + 1]);
+    for (int kb = 0; kb < 2; ++kb) f[kb] = split<3>(x[2 * kb], x[2 * kb + 1]);
     const float whole = dec[DEC_AHEAD + CH - 1];
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
@@ -383,10 +387,10 @@ __global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, WALK_PARTS<T, KP>, NW, 
       const Range m((bf16_t*)a.phi_t + part.slot * 2 * KP * KP, 4 * KP * KP);
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
-        const Split s = split(S.m[2 * kb], S.m[2 * kb + 1]);
+        const Split s = split<2>(S.m[2 * kb], S.m[2 * kb + 1]);
         const uint32_t o = 2 * ((col + n) * KP + 32 * kb + 8 * g);
-        m.put_quad(o, __builtin_bit_cast(u4_t, s.hi));
-        m.put_quad(o + 2 * KP * KP, __builtin_bit_cast(u4_t, s.lo));
+#pragma unroll
+        for (int p = 0; p < 2; ++p) m.put_quad(o + p * 2 * KP * KP, __builtin_bit_cast(u4_t, s.p[p]));
       }
     }
   }
@@ -537,11 +541,10 @@ __global__ __launch_bounds__(2 * KP) void delta_join_kernel(DeltaArgs a) {
   float S[8];  // rows 32 w + 8 g + 0 .. 7
   load_slot(0, S);
   const auto step = [&](int i, int x) {
-    u4_t hi, lo;
-    split8(S, hi, lo);
+    const Split own = split<2>(S);
     char* mine = lds[i & 1][w][0] + lane * 16;
-    *reinterpret_cast<u4_t*>(mine) = hi;
-    *reinterpret_cast<u4_t*>(mine + TILE) = lo;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) *reinterpret_cast<bf8_t*>(mine + p * TILE) = own.p[p];
     lds_barrier();
     f4_t o[2] = {{add[x][0], add[x][1], add[x][2], add[x][3]}, {add[x][4], add[x][5], add[x][6], add[x][7]}};
 #pragma unroll
@@ -577,7 +580,7 @@ constexpr int SHORT = 6;
 template <typename T, int KP, int MODE>
 hipError_t walk_go(const DeltaArgs& a, hipStream_t st) {
   constexpr int NW = 4;
-  const size_t lds = sizeof(WalkLds<KP, WALK_PARTS<T, KP>, NW, MODE>);
+  const size_t lds = sizeof(WalkLds<KP, WALK_PARTS<T>, NW, MODE>);
   const unsigned groups = (unsigned)((a.Dv + 16 * NW - 1) / (16 * NW)) + (MODE >= SUM ? KP / (16 * NW) : 0);
   const dim3 grid((unsigned)(a.B * a.Hv * a.NS) * groups);
   const auto go = [&](auto kernel) {

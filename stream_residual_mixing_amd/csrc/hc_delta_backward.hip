@@ -28,24 +28,24 @@ namespace {
 
 template <int KP, int NP, int NW>
 struct BackLds {
-  static constexpr int PASS = 1024 * NW;  // bytes that the threads bring in at once
-  char k[NP][Tokens<KP>::BYTES], q[NP][Tokens<KP>::BYTES];  // rows in row_of's order
-  char rec[(REC_BWD - REC_DEC + PASS - 1) / PASS * PASS];
+  static constexpr bool TURN = NP == 3 && KP == 256;  // no room for both: queries after keys, in k
+  char k[NP][Tokens<KP>::BYTES], q[TURN ? 1 : NP][TURN ? 16 : Tokens<KP>::BYTES];  // rows in row_of's order
+  Record<2, 64 * NW> rec;  // P's transpose and T's
 };
 
 // FULL: as above, over a segment's chunks. Otherwise a segment's first gradient from zeros (the last
 // segment's from its own), nothing else.
 template <typename T, int KP, int NW, bool VEC, bool FULL>
-__global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, WALK_PARTS<T, KP>, NW>>)) void delta_back_kernel(DeltaArgs a) {
-  constexpr int NP = WALK_PARTS<T, KP>, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
+__global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, WALK_PARTS<T>, NW>>)) void delta_back_kernel(DeltaArgs a) {
+  constexpr int NP = WALK_PARTS<T>, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
   constexpr int PIECES = KP / 8, ITEMS = (CH * PIECES + THREADS - 1) / THREADS;
-  constexpr int USED = REC_BWD - REC_DEC, RR = (USED + 16 * THREADS - 1) / (16 * THREADS);
-  constexpr int PT = REC_P - REC_DEC, TT = REC_TT - REC_DEC;
   extern __shared__ __attribute__((aligned(16))) char lds_raw[];
   typedef BackLds<KP, NP, NW> Lds;
   typedef Tokens<KP> Tk;
+  constexpr bool TURN = Lds::TURN;
   static_assert(sizeof(Lds) <= 160 * 1024, "LDS of a CU");
   Lds& lds = *reinterpret_cast<Lds*>(lds_raw);
+  char(*const lds_q)[Tk::BYTES] = reinterpret_cast<char(*)[Tk::BYTES]>(TURN ? lds.k[0] : lds.q[0]);
   const int tid = threadIdx.x, lane = tid & 63, w = wave_number(), n = lane & 15, g = lane >> 4;
   const int rows_at = Tk::lane_at(n, g), cols_at = Tk::lane_at_t(n, g);
   const int Dk = (int)a.Dk, Dv = (int)a.Dv, VP = (int)a.VP, qs = (int)a.Hk * Dk, vs = (int)a.Hv * Dv;
@@ -58,7 +58,7 @@ __global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, WALK_PARTS<T, KP>, NW>>
     for (int64_t t = from + g; t < to; t += 4) Elem<T>::st((T*)a.dv + values + t * vs + n, 0.f);
   }
   if (part.empty() || (!FULL && part.seg == 0)) return;
-  const char* rec = (const char*)a.rec + bh * a.NC * REC_BWD + REC_DEC;
+  const char* rec = (const char*)a.rec + bh * a.NC * REC_BWD;
   const uint32_t v_lane = n < have ? (8 * g * vs + n) * (uint32_t)sizeof(T) : NOWHERE;
 
   State<KP> D;
@@ -68,51 +68,54 @@ __global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, WALK_PARTS<T, KP>, NW>>
   }
 
   Raw8<T> kr[ITEMS], qr[ITEMS];
-  u4_t rr[RR];
+  typename decltype(lds.rec)::Raw rr;
   float dr[4][4];
-  const auto fetch = [&](int64_t c) {
-    const int left = (int)min((int64_t)CH, len - c * CH);
-    const Range kc = head_rows((const T*)a.k + keys + c * CH * qs, left, qs, Dk);
-    const Range qc = head_rows((const T*)a.q + keys + c * CH * qs, left, qs, Dk);
-    const Range dc = head_rows((const T*)a.d_o + values + c * CH * vs, have > 0 ? left : 0, vs, have);
-    const Range rc(rec + c * REC_BWD, USED);
-    const uint32_t vl = anew(v_lane);
+  const auto fetch_tokens = [&](Raw8<T>(&raw)[ITEMS], const void* from, int64_t c) {
+    const Range m = head_rows((const T*)from + keys + c * CH * qs, (int)min((int64_t)CH, len - c * CH), qs, Dk);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int x = i * THREADS + tid, piece = x % PIECES, row = x / PIECES;
-      const uint32_t o = (row * qs + 8 * piece) * (uint32_t)sizeof(T);
-      kr[i].template load<VEC>(kc, o, Dk - 8 * piece);
-      qr[i].template load<VEC>(qc, o, Dk - 8 * piece);
+      raw[i].template load<VEC>(m, (row * qs + 8 * piece) * (uint32_t)sizeof(T), Dk - 8 * piece);
     }
-#pragma unroll
-    for (int i = 0; i < RR; ++i) rr[i] = rc.quad((i * THREADS + tid) * 16);
+  };
+  const auto fetch = [&](int64_t c) {  // all but the queries
+    const int left = (int)min((int64_t)CH, len - c * CH);
+    const Range dc = head_rows((const T*)a.d_o + values + c * CH * vs, have > 0 ? left : 0, vs, have);
+    const uint32_t vl = anew(v_lane);
+    fetch_tokens(kr, a.k, c);
+    rr.load(Range(rec + c * REC_BWD, REC_BWD), REC_P, tid);
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int r = 0; r < 4; ++r) dr[t][r] = dc.get((const T*)nullptr, vl + row_of(t, r) * vs * (uint32_t)sizeof(T));
   };
-  if (part.first < part.last) fetch(part.last - 1);
-  for (int64_t c = part.last - 1; c >= part.first; --c) {
+  const auto put = [&](char(*m)[Tk::BYTES], const Raw8<T>(&raw)[ITEMS]) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int x = i * THREADS + tid, piece = x % PIECES, row = x / PIECES;
       if (CH * PIECES % THREADS == 0 || row < CH) {
-        const Op<NP> ko = kr[i].template op<NP>(), qo = qr[i].template op<NP>();
+        const Op<NP> o = raw[i].template op<NP>();
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          const int at = Tk::at(place_of(row), piece);
-          *reinterpret_cast<bf8_t*>(lds.k[p] + at) = ko.p[p];
-          *reinterpret_cast<bf8_t*>(lds.q[p] + at) = qo.p[p];
-        }
+        for (int p = 0; p < NP; ++p) *reinterpret_cast<bf8_t*>(m[p] + Tk::at(place_of(row), piece)) = o.p[p];
       }
     }
-#pragma unroll
-    for (int i = 0; i < RR; ++i) *reinterpret_cast<u4_t*>(lds.rec + (i * THREADS + tid) * 16) = rr[i];
+  };
+  if (part.first < part.last) {
+    fetch_tokens(qr, a.q, part.last - 1);
+    fetch(part.last - 1);
+  }
+  for (int64_t c = part.last - 1; c >= part.first; --c) {
+    put(lds.k, kr);
+    if (!TURN) put(lds_q, qr);
+    lds.rec.put(rr, tid);
     f4_t d[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) d[t] = f4_t{dr[t][0], dr[t][1], dr[t][2], dr[t][3]};
     lds_barrier();
-    if (c > part.first) fetch(c - 1);
+    if (c > part.first) {
+      if (!TURN) fetch_tokens(qr, a.q, c - 1);
+      fetch(c - 1);
+    }
     if (FULL) D.keep((float*)a.dstates + (bh * a.NC + c) * KP * VP, VP, col, n, g);
 
     f4_t x[4];  // K N
@@ -120,7 +123,7 @@ __global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, WALK_PARTS<T, KP>, NW>>
     for (int t = 0; t < 4; ++t) x[t] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
-      const Fine sf = split_fine(D.m[2 * kb], D.m[2 * kb + 1]);
+      const Fine sf = split<3>(D.m[2 * kb], D.m[2 * kb + 1]);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         Op<NP> ka;
@@ -130,21 +133,17 @@ __global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, WALK_PARTS<T, KP>, NW>>
       }
       keep_order();
     }
-    const float* dec = (const float*)lds.rec;
+    const float* dec = lds.rec.dec;
     // beta dX, dX = scale P^T dO + exp(G_end - G) K N
     {
       Op<NP> df[2];
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        const Fine s = split_fine(d[2 * kb], d[2 * kb + 1]);  // bfloat16 is its own high part
-#pragma unroll
-        for (int p = 0; p < NP; ++p) df[kb].p[p] = s.p[p];
-      }
+      for (int kb = 0; kb < 2; ++kb) df[kb] = split<NP>(d[2 * kb], d[2 * kb + 1]);  // bfloat16 is its own high part
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         f4_t p = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int kb = t >> 1; kb < 2; ++kb) p = mma(load_tile(lds.rec + PT, tri_t(t, kb), lane), df[kb], p);
+        for (int kb = t >> 1; kb < 2; ++kb) p = mma(lds.rec.tile(0, tri_t(t, kb), lane), df[kb], p);
         const f4_t to_end = *reinterpret_cast<const f4_t*>(dec + DEC_TO_END + row_of(t, 4 * g));
         const f4_t beta = *reinterpret_cast<const f4_t*>(dec + DEC_BETA + row_of(t, 4 * g));
         x[t] = beta * (a.scale * p + to_end * x[t]);
@@ -154,12 +153,12 @@ __global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, WALK_PARTS<T, KP>, NW>>
     // W = T^T (beta dX)
     Fine f[2], wf[2];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) f[kb] = split_fine(x[2 * kb], x[2 * kb + 1]);
+    for (int kb = 0; kb < 2; ++kb) f[kb] = split<3>(x[2 * kb], x[2 * kb + 1]);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       x[t] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int kb = t >> 1; kb < 2; ++kb) x[t] = mma(load_tile(lds.rec + TT, tri_t(t, kb), lane), f[kb], x[t]);
+      for (int kb = t >> 1; kb < 2; ++kb) x[t] = mma(lds.rec.tile(1, tri_t(t, kb), lane), f[kb], x[t]);
     }
     keep_order();
     if (FULL) {
@@ -180,26 +179,36 @@ __global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, WALK_PARTS<T, KP>, NW>>
     }
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      wf[kb] = split_fine(x[2 * kb], x[2 * kb + 1]);
-      f[kb] = split_fine(d[2 * kb], d[2 * kb + 1]);
+      wf[kb] = split<3>(x[2 * kb], x[2 * kb + 1]);
+      f[kb] = split<3>(d[2 * kb], d[2 * kb + 1]);
     }
     const float whole = dec[DEC_AHEAD + CH - 1];
     keep_order();
+    const auto add = [&](bool by_q, bool by_k) {  // (exp(G) Q)^T dO, -(exp(G) K)^T W
 #pragma unroll
-    for (int t = 0; t < KT; ++t) {
-      D.m[t] *= whole;
+      for (int t = 0; t < KT; ++t) {
+        if (by_k) D.m[t] *= whole;
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        Op<NP> ka, qa;
+        for (int kb = 0; kb < 2; ++kb) {
+          Op<NP> ka, qa;
 #pragma unroll
-        for (int p = 0; p < NP; ++p) {
-          ka.p[p] = Tk::cols(lds.k[p], cols_at, t, kb);
-          qa.p[p] = Tk::cols(lds.q[p], cols_at, t, kb);
+          for (int p = 0; p < NP; ++p) {
+            if (by_k) ka.p[p] = Tk::cols(lds.k[p], cols_at, t, kb);
+            if (by_q) qa.p[p] = Tk::cols(lds_q[p], cols_at, t, kb);
+          }
+          if (by_q) D.m[t] = mma(qa, f[kb], D.m[t]);
+          if (by_k) D.m[t] = mma(ka, wf[kb], D.m[t]);
         }
-        D.m[t] = mma(qa, f[kb], D.m[t]);
-        D.m[t] = mma(ka, wf[kb], D.m[t]);
+        keep_order();
       }
-      keep_order();
+    };
+    add(!TURN, true);
+    if (TURN) {
+      lds_barrier();
+      put(lds_q, qr);
+      lds_barrier();
+      if (c > part.first) fetch_tokens(qr, a.q, c - 1);
+      add(true, false);
     }
     lds_barrier();
   }
@@ -231,9 +240,9 @@ struct GradLds {
     return *reinterpret_cast<const bf8_t*>(m + part * PART + 32 * COLS * tile + (at ^ (kb << 6)));
   }
   static __device__ __forceinline__ void put(char* m, int part, int at, const F8& v) {
-    const Split s = split(v.a, v.b);
-    *reinterpret_cast<bf8_t*>(m + part * PART + at) = s.hi;
-    *reinterpret_cast<bf8_t*>(m + (part + 1) * PART + at) = s.lo;
+    const Split s = split<2>(v.a, v.b);
+#pragma unroll
+    for (int p = 0; p < 2; ++p) *reinterpret_cast<bf8_t*>(m + (part + p) * PART + at) = s.p[p];
   }
   static __device__ __forceinline__ Split two(const char* m, int part, int at, int tile, int kb) {
     return {one(m, part, at, tile, kb), one(m, part + 1, at, tile, kb)};
@@ -482,9 +491,9 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
           if (n == 0) store8(lds.row[w] + row0, c);
         };
         ends_at(32 * h + 8 * g);
-        bq = split(vq);
-        bk = split(vk);
-        aa = split(va);
+        bq = split<2>(vq);
+        bk = split<2>(vk);
+        aa = split<2>(va);
         pin(bq);
         pin(bk);
         pin(aa);
@@ -505,8 +514,8 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
           }
         }
         if (h == 0) ends_at(32 + 8 * g);
-        x = split(vq);
-        ax = split(va);
+        x = split<2>(vq);
+        ax = split<2>(va);
         pin(x);
         pin(ax);
         keep_order();
@@ -552,8 +561,8 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) mn += mr[i].a[e] * nr[i].a[e] + mr[i].b[e] * nr[i].b[e];
             dn[i] = dn_next[i];
-            zn[i] = split(zn_next[i].a, zn_next[i].b);
-            wn[i] = split(wn_next[i].a, wn_next[i].b);
+            zn[i] = split<2>(zn_next[i].a, zn_next[i].b);
+            wn[i] = split<2>(wn_next[i].a, wn_next[i].b);
           }
           if (vb + COLS < VP) fetch(key0, vb + COLS);
           else if (quad + 1 < QUADS) fetch(key0 + 64, 0);
@@ -671,7 +680,7 @@ template <typename T, int KP, bool FULL>
 hipError_t back_go(const DeltaArgs& a, hipStream_t st) {
   constexpr int NW = 4;
   const unsigned grid = (unsigned)(a.B * a.Hv * a.NS * ((a.Dv + 16 * NW - 1) / (16 * NW)));
-  const size_t lds = sizeof(BackLds<KP, WALK_PARTS<T, KP>, NW>);
+  const size_t lds = sizeof(BackLds<KP, WALK_PARTS<T>, NW>);
   return a.vec ? with_lds(delta_back_kernel<T, KP, NW, true, FULL>, lds, grid, 64 * NW, a, st)
                : with_lds(delta_back_kernel<T, KP, NW, false, FULL>, lds, grid, 64 * NW, a, st);
 }

@@ -29,11 +29,14 @@ __device__ __forceinline__ int row_of(int t, int m) { return 32 * (t >> 1) + 8 *
 // the place of row x in that order
 __device__ __forceinline__ int place_of(int x) { return (x & ~31) + 16 * ((x >> 2) & 1) + 4 * ((x >> 3) & 3) + (x & 3); }
 
-// Eight float32 values as the sum of two bfloat16 parts, 16 bits of each value: the part left
-// over is at most 2^-17 of it. Products of two such operands keep all four terms.
-struct Split {
-  bf8_t hi, lo;
+// Eight values as the sum of NP bfloat16 parts. Three hold float32's own 24 bits, bfloat16 streams are
+// their own single part, and two leave 2^-18 of a value.
+template <int NP>
+struct Op {
+  bf8_t p[NP];
 };
+typedef Op<2> Split;
+typedef Op<3> Fine;
 
 __device__ __forceinline__ bf8_t as_bf8(u4_t q) { return __builtin_bit_cast(bf8_t, q); }
 
@@ -44,70 +47,46 @@ __device__ __forceinline__ u4_t pack8(const float v[8]) {
   return q;
 }
 
-__device__ __forceinline__ void split8(const float v[8], u4_t& hi, u4_t& lo) {
-  hi = pack8(v);
-  float rest[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    rest[2 * i] = v[2 * i] - __uint_as_float(hi[i] << 16);
-    rest[2 * i + 1] = v[2 * i + 1] - __uint_as_float(hi[i] & 0xffff0000u);
-  }
-  lo = pack8(rest);
-}
-
-__device__ __forceinline__ Split split(const float v[8]) {
-  u4_t h, l;
-  split8(v, h, l);
-  return {as_bf8(h), as_bf8(l)};
-}
-
-__device__ __forceinline__ Split split(f4_t a, f4_t b) {
-  const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-  return split(v);
-}
-
-// In three parts, float32's own 24 bits: what the walks add to the state passes through the chunks that
-// follow, and two parts of it would be off by 4 x 10^-6 of the state's norm where three leave 5 x 10^-7.
-struct Fine {
-  bf8_t p[3];
-};
-
-__device__ __forceinline__ Fine split_fine(f4_t a, f4_t b) {
+template <int NP>
+__device__ __forceinline__ Op<NP> split(f4_t a, f4_t b) {
   float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-  Fine f;
+  Op<NP> o;
 #pragma unroll
-  for (int p = 0; p < 3; ++p) {
+  for (int p = 0; p < NP; ++p) {
     const u4_t q = pack8(v);
-    f.p[p] = as_bf8(q);
+    o.p[p] = as_bf8(q);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       v[2 * i] -= __uint_as_float(q[i] << 16);
       v[2 * i + 1] -= __uint_as_float(q[i] & 0xffff0000u);
     }
   }
-  return f;
+  return o;
+}
+
+template <int NP>
+__device__ __forceinline__ Op<NP> split(const float v[8]) {
+  return split<NP>(f4_t{v[0], v[1], v[2], v[3]}, f4_t{v[4], v[5], v[6], v[7]});
 }
 
 __device__ __forceinline__ f4_t mma(bf8_t a, bf8_t b, f4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ f4_t mma(const Split& a, const Split& b, f4_t c) {
-  c = mma(a.lo, b.lo, c);
-  c = mma(a.lo, b.hi, c);
-  c = mma(a.hi, b.lo, c);
-  return mma(a.hi, b.hi, c);
+// Parts i and j of two factors, the smallest products first: all but those with i + j > 2, each at most
+// 2^-27 of the whole.
+template <int NA, int NB>
+__device__ __forceinline__ f4_t mma(const Op<NA>& a, const Op<NB>& b, f4_t c) {
+#pragma unroll
+  for (int s = 2; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB) c = mma(a.p[i], b.p[s - i], c);
+  return c;
 }
 
-__device__ __forceinline__ f4_t mma(const Split& a, const Fine& b, f4_t c) {
-  c = mma(a.lo, b.p[1], c);
-  c = mma(a.hi, b.p[2], c);
-  c = mma(a.lo, b.p[0], c);
-  c = mma(a.hi, b.p[1], c);
-  return mma(a.hi, b.p[0], c);
-}
-
-// Stream operands: bfloat16 is exact in one part, float32 takes two.
+// Stream operands: bfloat16 is exact in one part, float32 takes two in the chunks' gradients and three in the
+// walks, whose states pass their errors on.
 template <typename T> struct Stream;
 template <> struct Stream<bf16_t> {
   static constexpr int NP = 1;
@@ -115,61 +94,8 @@ template <> struct Stream<bf16_t> {
 template <> struct Stream<float> {
   static constexpr int NP = 2;
 };
-
-// The walks, whose states pass their errors on, and the triangles: three parts where LDS has room for them (dg of
-// heads that forget fast is off by 10^-5 of its norm with two).
-template <typename T, int KP>
-constexpr int WALK_PARTS = Stream<T>::NP == 2 && KP <= 128 ? 3 : Stream<T>::NP;
-
-template <int NP>
-struct Op {
-  bf8_t p[NP];
-};
-
-template <int NP>
-__device__ __forceinline__ f4_t mma(const Op<NP>& a, const Split& b, f4_t c) {
-  if (NP == 2) c = mma(a.p[NP - 1], b.hi, mma(a.p[NP - 1], b.lo, c));
-  c = mma(a.p[0], b.lo, c);
-  return mma(a.p[0], b.hi, c);
-}
-
-// three parts of each: what 24 bits leave
-__device__ __forceinline__ f4_t mma(const bf8_t (&a)[3], const bf8_t (&b)[3], f4_t c) {
-  c = mma(a[1], b[1], c);
-  c = mma(a[2], b[0], c);
-  c = mma(a[0], b[2], c);
-  c = mma(a[1], b[0], c);
-  c = mma(a[0], b[1], c);
-  return mma(a[0], b[0], c);
-}
-
-template <int NP>
-__device__ __forceinline__ f4_t mma(const Op<NP>& a, const Fine& b, f4_t c) {
-  if constexpr (NP == 3) return mma(a.p, b.p, c);
-  if (NP == 2) return mma(Split{a.p[0], a.p[NP - 1]}, b, c);
-  c = mma(a.p[0], b.p[2], c);
-  c = mma(a.p[0], b.p[1], c);
-  return mma(a.p[0], b.p[0], c);
-}
-
-template <int NP>
-__device__ __forceinline__ f4_t mma(const Split& a, const Op<NP>& b, f4_t c) {
-  if constexpr (NP == 3) return mma(a, Fine{b.p[0], b.p[1], b.p[2]}, c);
-  if (NP == 2) c = mma(a.hi, b.p[NP - 1], mma(a.lo, b.p[NP - 1], c));
-  c = mma(a.lo, b.p[0], c);
-  return mma(a.hi, b.p[0], c);
-}
-
-template <int NP>
-__device__ __forceinline__ f4_t mma(const Op<NP>& a, const Op<NP>& b, f4_t c) {
-  if constexpr (NP == 3) return mma(a.p, b.p, c);
-  if (NP == 2) {
-    c = mma(a.p[NP - 1], b.p[NP - 1], c);
-    c = mma(a.p[NP - 1], b.p[0], c);
-    c = mma(a.p[0], b.p[NP - 1], c);
-  }
-  return mma(a.p[0], b.p[0], c);
-}
+template <typename T>
+constexpr int WALK_PARTS = sizeof(T) == 4 ? 3 : 1;
 
 // Memory from an address that the wave's lanes have in common, read and written at 32-bit offsets:
 // what lies at or behind its end reads as 0 and is not written, so that neither the last chunk's
@@ -264,13 +190,7 @@ template <> struct Raw8<float> {
   }
   template <int NP>
   __device__ __forceinline__ Op<NP> op() const {
-    if constexpr (NP == 3) {
-      const Fine f = split_fine(a, b);
-      return {f.p[0], f.p[1], f.p[2]};
-    } else {
-      const Split s = split(a, b);
-      return {s.hi, s.lo};
-    }
+    return split<NP>(a, b);
   }
 };
 
@@ -289,30 +209,63 @@ __device__ __forceinline__ int64_t length_of(const int32_t* lengths, int64_t b, 
   return n < 0 ? 0 : n > S ? S : n;
 }
 
-// A chunk's record: decays and betas, a float per token, and 16 x 32 operand tiles of 64 x 16 bytes in
-// the lanes' order, first the six high parts and then the six low ones, of the two lower
-// block-triangular matrices T (rows in row_of's order) and P (rows in their own), tile (t, kb) at
-// tri(t, kb). The backward's holds T and, upper triangular at tri_t, the transposes of both with
-// rows in row_of's order.
-constexpr int TILE = 1024, TRI = 12 * TILE;
-constexpr int REC_T = 0, REC_DEC = TRI, REC_P = TRI + 3 * CH * 4, REC = REC_P + TRI;
+// A chunk's record, float32: decays and betas, a value per token, and 16 x 32 operand tiles of 64 lanes by
+// eight values, first all lanes' four and then their other four, of the two lower block-triangular
+// matrices T (rows in row_of's order) and P (rows in their own), tile (t, kb) at tri(t, kb). The backward's
+// holds T and, upper triangular at tri_t, the transposes of both with rows in row_of's order.
+constexpr int TILES = 6, TILE = 1024, TRI = TILES * 2 * TILE;
+constexpr int REC_DEC = 0, REC_T = 3 * CH * 4, REC_P = REC_T + TRI, REC = REC_P + TRI;
 constexpr int REC_TT = REC, REC_BWD = REC + TRI;
 constexpr int DEC_AHEAD = 0, DEC_TO_END = CH, DEC_BETA = 2 * CH;
 
 __device__ __forceinline__ constexpr int tri(int t, int kb) { return t < 2 ? t : 2 * t - 2 + kb; }
 __device__ __forceinline__ constexpr int tri_t(int t, int kb) { return t < 2 ? 2 * t + kb : t + 2; }
 
-__device__ __forceinline__ Split load_tile(const char* m, int idx, int lane) {
-  return {*reinterpret_cast<const bf8_t*>(m + idx * TILE + lane * 16),
-          *reinterpret_cast<const bf8_t*>(m + (6 + idx) * TILE + lane * 16)};
+__device__ __forceinline__ void store_tile(char* m, int idx, int lane, const float v[8]) {
+  f4_t* p = reinterpret_cast<f4_t*>(m + idx * 2 * TILE) + lane;
+  p[0] = f4_t{v[0], v[1], v[2], v[3]};
+  p[64] = f4_t{v[4], v[5], v[6], v[7]};
 }
 
-__device__ __forceinline__ void store_tile(char* m, int idx, int lane, const float v[8]) {
-  u4_t hi, lo;
-  split8(v, hi, lo);
-  *reinterpret_cast<u4_t*>(m + idx * TILE + lane * 16) = hi;
-  *reinterpret_cast<u4_t*>(m + (6 + idx) * TILE + lane * 16) = lo;
-}
+// N of the record's matrices in LDS, as operands in three parts, with the decays and betas.
+template <int N, int THREADS>
+struct Record {
+  static constexpr int PART = TILES * TILE, ALL = N * TILES * 64, ITEMS = (ALL + THREADS - 1) / THREADS;
+  char m[N][3 * PART];
+  float dec[3 * CH];
+  struct Raw {  // on its way
+    f4_t v[ITEMS][2], d;
+    // `r` ends with the last of the matrices, the first lies at `from`
+    __device__ __forceinline__ void load(const Range& r, int from, int tid) {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        const int x = i * THREADS + tid, o = from + (x >> 6) * 2 * TILE + (x & 63) * 16;
+        v[i][0] = __builtin_bit_cast(f4_t, r.quad(o));
+        v[i][1] = __builtin_bit_cast(f4_t, r.quad(o + TILE));
+      }
+      d = __builtin_bit_cast(f4_t, r.quad(tid < 3 * CH / 4 ? REC_DEC + 16 * tid : NOWHERE));
+    }
+  };
+  __device__ __forceinline__ void put(const Raw& raw, int tid) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int x = i * THREADS + tid, of = x / (TILES * 64), at = x % (TILES * 64) * 16;
+      if (ALL % THREADS == 0 || x < ALL) {
+        const Fine f = split<3>(raw.v[i][0], raw.v[i][1]);
+#pragma unroll
+        for (int p = 0; p < 3; ++p) *reinterpret_cast<bf8_t*>(m[of] + p * PART + at) = f.p[p];
+      }
+    }
+    if (tid < 3 * CH / 4) *reinterpret_cast<f4_t*>(dec + 4 * tid) = raw.d;
+  }
+  __device__ __forceinline__ Fine tile(int of, int idx, int lane) const {
+    const char* at = m[of] + idx * TILE + lane * 16;
+    Fine f;
+#pragma unroll
+    for (int p = 0; p < 3; ++p) f.p[p] = *reinterpret_cast<const bf8_t*>(at + p * PART);
+    return f;
+  }
+};
 
 // A chunk's keys or queries in LDS, [CH][KP] with the rows where the caller puts them. The 16-byte
 // pieces of a row are exchanged so that both readings reach all banks: a piece of 16 rows (an
@@ -355,10 +308,14 @@ __device__ __forceinline__ void keep_order() {
 // The lane's numbers anew, so that what a loop forms of them is not kept in registers over it.
 __device__ __forceinline__ void renew(int& a, int& b) { asm volatile("" : "+v"(a), "+v"(b)); }
 // The operand is formed here, not where it is used.
-__device__ __forceinline__ void pin(Split& s) {
-  u4_t h = __builtin_bit_cast(u4_t, s.hi), l = __builtin_bit_cast(u4_t, s.lo);
-  asm volatile("" : "+v"(h), "+v"(l));
-  s = {as_bf8(h), as_bf8(l)};
+template <int NP>
+__device__ __forceinline__ void pin(Op<NP>& s) {
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+    u4_t q = __builtin_bit_cast(u4_t, s.p[p]);
+    asm volatile("" : "+v"(q));
+    s.p[p] = as_bf8(q);
+  }
 }
 __device__ __forceinline__ uint32_t anew(uint32_t a) {
   asm volatile("" : "+v"(a));

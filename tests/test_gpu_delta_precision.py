@@ -1,0 +1,66 @@
+"""The precision of the gated delta rule's float32 and bfloat16 results on the GPU, head by head (bfloat16
+results all heads together), against the float64 form (oracle/sublayer_ops.py); tolerances and inputs in delta_precision.py."""
+import numpy as np
+import pytest
+
+import delta_precision as D
+from hc_testutil import have_gpu, note
+from oracle import sublayer_ops as R
+
+pytestmark = pytest.mark.gpu
+
+if have_gpu():
+    import torch
+    import stream_residual_mixing_amd as hc
+
+
+def put(a, dt="f32"):
+    return torch.from_numpy(np.ascontiguousarray(a, np.float32)).cuda().to(torch.bfloat16 if dt == "bf16" else torch.float32)
+
+
+def get(t):
+    return t.detach().double().cpu().numpy()
+
+
+def device(ins, dt):
+    """(q, k, v, g, beta, state, do, dstate) on the GPU."""
+    return [put(a, dt if i in (0, 1, 2, 6) else "f32") for i, a in enumerate(ins)]
+
+
+def check(name, where, x, y, dt, tol):
+    """x against y: float32 to `tol`, bfloat16 against the rounded y."""
+    if dt == "bf16":
+        y = D.bf16(y)
+        tol = D.half(y)
+    off = D.rel(x, y)
+    assert off <= tol, (name, where, off, tol)
+
+
+def check_forward(o, M, ins, dt, lengths=None, grow=1.0):
+    B, S, _, Dk = ins[0].shape
+    ro, rM = R.gated_delta(*ins[:6], lengths)
+    o, M = get(o), get(M)
+    if dt == "bf16":
+        check("o", "all", o, ro, dt, None)
+    for b in range(B):
+        n = S if lengths is None else lengths[b]
+        for h in range(ins[2].shape[2]):
+            if n and dt == "f32":
+                check("o", (b, h), o[b, :n, h], ro[b, :n, h], dt, D.OUT * grow)
+            check("state", (b, h), M[b, h], rM[b, h], "f32", D.STATE * grow)
+
+
+# B, S, Hk, Hv, Dk, Dv of every width's variants, in one walk
+SIZES = [(1, 300, 1, 2, 64, 48), (4, 500, 2, 4, 128, 128), (1, 900, 1, 1, 72, 100), (1, 200, 2, 2, 256, 64),
+         (1, 330, 1, 2, 100, 36), (1, 130, 1, 1, 200, 30)]
+
+
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_forward(size, dt):
+    note(f"precision of hc_gated_delta {size} {dt}")
+    ins = D.inputs(*size, dt, sum(size))
+    d = device(ins, dt)
+    o, M = hc.hc_gated_delta(*d[:6])
+    torch.cuda.synchronize()
+    check_forward(o, M, ins, dt)
