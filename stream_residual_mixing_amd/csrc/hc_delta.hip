@@ -29,7 +29,7 @@ namespace {
 
 template <typename T, int KP, bool VEC, bool BWD>
 __global__ __launch_bounds__(256, 4) void delta_prep_kernel(DeltaArgs a) {
-  constexpr int NP = WALK_PARTS<T>, KB = KP / 32, LS = CH + 4;
+  constexpr int NP = PARTS<T>, KB = KP / 32, LS = CH + 4;
   __shared__ __attribute__((aligned(16))) float L[CH][LS], inv[CH][LS];
   __shared__ double G[CH];
   __shared__ __attribute__((aligned(16))) float beta_s[CH];
@@ -199,8 +199,8 @@ struct WalkLds {
 // segment's from its own) and, as further columns that start as the unit matrix without values, its
 // map of the state; SUM_BWD: the map's transpose too.
 template <typename T, int KP, int NW, bool VEC, int MODE>
-__global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, WALK_PARTS<T>, NW, MODE>>)) void delta_walk_kernel(DeltaArgs a) {
-  constexpr int NP = WALK_PARTS<T>, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
+__global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, PARTS<T>, NW, MODE>>)) void delta_walk_kernel(DeltaArgs a) {
+  constexpr int NP = PARTS<T>, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
   constexpr int PIECES = KP / 8, ITEMS = (CH * PIECES + THREADS - 1) / THREADS;
   constexpr int STRIDE = MODE == KEEP || MODE == SUM_BWD ? REC_BWD : REC, USED = MODE == OUT ? REC : REC_P;
   extern __shared__ __attribute__((aligned(16))) char lds_raw[];
@@ -580,7 +580,7 @@ constexpr int SHORT = 6;
 template <typename T, int KP, int MODE>
 hipError_t walk_go(const DeltaArgs& a, hipStream_t st) {
   constexpr int NW = 4;
-  const size_t lds = sizeof(WalkLds<KP, WALK_PARTS<T>, NW, MODE>);
+  const size_t lds = sizeof(WalkLds<KP, PARTS<T>, NW, MODE>);
   const unsigned groups = (unsigned)((a.Dv + 16 * NW - 1) / (16 * NW)) + (MODE >= SUM ? KP / (16 * NW) : 0);
   const dim3 grid((unsigned)(a.B * a.Hv * a.NS) * groups);
   const auto go = [&](auto kernel) {

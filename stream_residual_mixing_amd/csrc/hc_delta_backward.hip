@@ -15,6 +15,8 @@
 // The forward's walk is run again and keeps every chunk's M and Z; a second walk from the end back
 // keeps N and W and writes dV; then every chunk forms the rest by itself, all value heads of a key
 // head in one workgroup, so that dQ and dK are summed in registers and in a fixed order.
+// Every factor keeps float32's 24 bits, in three bfloat16 parts: gradients are as near the definition as a float32
+// form's (2 to 4 x 10^-7 of their norm; with two parts 3 to 6 x 10^-6, the whole call 5 % faster).
 //   2,048 chunks of 128 x 128 (2 x 4,096 tokens, 16 value heads on 8 key heads, bfloat16), with segments: the
 // forward's part 227 us, the walks back 199, the chunks' own part 225. That one reads the states that the
 // walks kept, 64 KB a chunk and direction in float32, and Z and W, these more than once (400 MB, 619 MB of
@@ -36,8 +38,8 @@ struct BackLds {
 // FULL: as above, over a segment's chunks. Otherwise a segment's first gradient from zeros (the last
 // segment's from its own), nothing else.
 template <typename T, int KP, int NW, bool VEC, bool FULL>
-__global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, WALK_PARTS<T>, NW>>)) void delta_back_kernel(DeltaArgs a) {
-  constexpr int NP = WALK_PARTS<T>, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
+__global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, PARTS<T>, NW>>)) void delta_back_kernel(DeltaArgs a) {
+  constexpr int NP = PARTS<T>, KB = KP / 32, KT = KP / 16, THREADS = 64 * NW;
   constexpr int PIECES = KP / 8, ITEMS = (CH * PIECES + THREADS - 1) / THREADS;
   extern __shared__ __attribute__((aligned(16))) char lds_raw[];
   typedef BackLds<KP, NP, NW> Lds;
@@ -219,15 +221,17 @@ __global__ __launch_bounds__(64 * NW, (WALKS<BackLds<KP, WALK_PARTS<T>, NW>>)) v
 // ------------------------------------------------------------- each chunk by itself
 
 // What each chunk's workgroup of four waves, 16 tokens each, brings through LDS, in turn in NBUF
-// buffers: Z, W (two parts each) and dO, 64 tokens by COLS columns, and then the state and its gradient
-// (two parts each), 64 keys by COLS columns. Each step waits for memory once: steps of 32 columns
-// took 277 us for 2,048 chunks of 128 x 128 where these take 226.
+// buffers: Z, W (three parts each) and dO, 64 tokens by COLS columns, and then the state and its gradient
+// (three parts each), 64 keys by COLS columns. Each step waits for memory once: steps of 32 columns
+// took 277 us for 2,048 chunks of 128 x 128 where 64 took 226 (with two parts), so these where there is room.
+// Of 256 float32 keys and queries LDS holds KL = 128 at a time.
 template <int KP, int NP>
 struct GradLds {
-  static constexpr int COLS = KP == 256 && NP == 2 ? 32 : 64, PIECES = COLS / 8, PART = CH * COLS * 2;
-  static constexpr int NBUF = (KP == 64 ? 1 : KP / 64) * NP <= 4 && !(KP == 128 && NP == 2) ? 2 : 1;  // as there is room
-  char k[NP][Tokens<KP>::BYTES], q[NP][Tokens<KP>::BYTES];  // rows in row_of's order
-  char buf[NBUF][(4 + NP) * PART];
+  static constexpr int KL = NP == 3 && KP == 256 ? 128 : KP;
+  static constexpr int COLS = KL == 128 && NP == 3 ? 32 : 64, PIECES = COLS / 8, PART = CH * COLS * 2;
+  static constexpr int NBUF = NP == 1 && KP <= 128 ? 2 : 1;
+  char k[NP][Tokens<KL>::BYTES], q[NP][Tokens<KL>::BYTES];  // rows in row_of's order
+  char buf[NBUF][(6 + NP) * PART];
   double G[CH];
   float beta[CH], read[CH], late[CH], row[4][CH], end[4];
   // a row's place in row_of's order, its 16-byte pieces exchanged so that 16 lanes reading a piece of 16 rows
@@ -240,12 +244,12 @@ struct GradLds {
     return *reinterpret_cast<const bf8_t*>(m + part * PART + 32 * COLS * tile + (at ^ (kb << 6)));
   }
   static __device__ __forceinline__ void put(char* m, int part, int at, const F8& v) {
-    const Split s = split<2>(v.a, v.b);
+    const Fine s = split<3>(v.a, v.b);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) *reinterpret_cast<bf8_t*>(m + (part + p) * PART + at) = s.p[p];
+    for (int p = 0; p < 3; ++p) *reinterpret_cast<bf8_t*>(m + (part + p) * PART + at) = s.p[p];
   }
-  static __device__ __forceinline__ Split two(const char* m, int part, int at, int tile, int kb) {
-    return {one(m, part, at, tile, kb), one(m, part + 1, at, tile, kb)};
+  static __device__ __forceinline__ Fine fine(const char* m, int part, int at, int tile, int kb) {
+    return {one(m, part, at, tile, kb), one(m, part + 1, at, tile, kb), one(m, part + 2, at, tile, kb)};
   }
   static __device__ __forceinline__ Op<NP> stream(const char* m, int part, int at, int tile, int kb) {
     Op<NP> d;
@@ -288,10 +292,12 @@ __device__ __forceinline__ float sum_groups(float v) {  // over the four lanes o
 // wider heads take two passes, the second of which adds to the first's dg and dbeta.
 template <typename T, int KP, bool VEC, bool SHARED>
 __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
-  constexpr int NP = Stream<T>::NP, KB = KP / 32, QUADS = KP == 64 ? 1 : 2, PASSES = KP / 64 / QUADS;
-  constexpr int PIECES = KP / 8, ITEMS = CH * PIECES / 256;
+  constexpr int NP = PARTS<T>, QUADS = KP == 64 ? 1 : 2, PASSES = KP / 64 / QUADS;
   typedef GradLds<KP, NP> Lds;
-  typedef Tokens<KP> Tk;
+  constexpr int KL = Lds::KL, PIECES = KL / 8, ITEMS = CH * PIECES / 256;
+  constexpr int KB = KL / 32;
+  constexpr bool HALVES = KL < KP;
+  typedef Tokens<KL> Tk;
   extern __shared__ __attribute__((aligned(16))) char lds_raw[];
   static_assert(sizeof(Lds) <= 160 * 1024, "LDS of a CU");
   Lds& lds = *reinterpret_cast<Lds*>(lds_raw);
@@ -303,12 +309,12 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
   const int Dk = (int)a.Dk, Dv = (int)a.Dv, VP = (int)a.VP, qs = (int)a.Hk * Dk, vs = (int)a.Hv * Dv;
   const int per = (int)((uint32_t)a.Hv / (uint32_t)a.Hk);
   const int64_t keys = (b * a.S + t0) * qs + hk * Dk;
-  {
+  const auto bring = [&](int key0) {
     const Range q = head_rows((const T*)a.q + keys, left, qs, Dk), k = head_rows((const T*)a.k + keys, left, qs, Dk);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int x = i * 256 + tid, piece = x % PIECES, row = x / PIECES;
-      const Op<NP> ko = token_op<T, VEC>(k, qs, row, 8 * piece, Dk), qo = token_op<T, VEC>(q, qs, row, 8 * piece, Dk);
+      const Op<NP> ko = token_op<T, VEC>(k, qs, row, key0 + 8 * piece, Dk), qo = token_op<T, VEC>(q, qs, row, key0 + 8 * piece, Dk);
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
         const int at = Tk::at(place_of(row), piece);
@@ -316,6 +322,56 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
         *reinterpret_cast<bf8_t*>(lds.q[p] + at) = qo.p[p];
       }
     }
+  };
+  // rows i: k_i . k_j and q_i . k_j of the keys in LDS, j the wave's tokens; x: the other half's rows (h = 0)
+  struct Dots {
+    f4_t kk[2], qk[2], xk[2], xq[2];
+  };
+  const auto dots = [&](Dots& o) {
+    const int k_rows = Tk::lane_at(n, g) + 32 * h * Tk::ROW, k_own = Tk::at(place_of(16 * w + n), g);
+#pragma unroll
+    for (int kb = 0; kb < KB; ++kb) {
+      Op<NP> kn;
+#pragma unroll
+      for (int p = 0; p < NP; ++p) kn.p[p] = *reinterpret_cast<const bf8_t*>(lds.k[p] + (k_own ^ (kb << 6)));
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        Op<NP> ka, qa;
+#pragma unroll
+        for (int p = 0; p < NP; ++p) {
+          ka.p[p] = Tk::rows(lds.k[p], k_rows, t, kb);
+          qa.p[p] = Tk::rows(lds.q[p], k_rows, t, kb);
+        }
+        o.kk[t] = mma(ka, kn, o.kk[t]);
+        o.qk[t] = mma(qa, kn, o.qk[t]);
+      }
+      if (h == 0) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          Op<NP> ka, qa;
+#pragma unroll
+          for (int p = 0; p < NP; ++p) {
+            ka.p[p] = Tk::rows(lds.k[p], k_rows, 2 + t, kb);
+            qa.p[p] = Tk::rows(lds.q[p], k_rows, 2 + t, kb);
+          }
+          o.xk[t] = mma(ka, kn, o.xk[t]);
+          o.xq[t] = mma(qa, kn, o.xq[t]);
+        }
+      }
+      keep_order();
+    }
+  };
+  Dots of_halves = {};
+  if (HALVES) {
+    bring(KL);
+    lds_barrier();
+    dots(of_halves);
+    lds_barrier();
+  }
+  bring(0);
+  if (HALVES) {
+    lds_barrier();
+    dots(of_halves);
   }
   const Range dqp = head_rows((T*)a.dq + keys, rows, qs, Dk), dkp = head_rows((T*)a.dk + keys, rows, qs, Dk);
   const auto put = [&](int tok, int key0, const f4_t* dq, const f4_t* dk) {  // 64 keys of the wave's tokens
@@ -334,6 +390,10 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
   };
 #pragma unroll 1
   for (int pass = 0; pass < PASSES; ++pass) {
+    if (HALVES && pass) {
+      of_halves = {};
+      bring(KL);  // every wave has passed the last head's last barrier
+    }
     f4_t dqt[4 * QUADS], dkt[4 * QUADS];
 #pragma unroll
     for (int t = 0; t < 4 * QUADS; ++t) dqt[t] = dkt[t] = f4_t{0.f, 0.f, 0.f, 0.f};
@@ -366,7 +426,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
       // (tok, j'), the later one. As operands: bq by K for dQ, bk by Q and aa by K for dK; x is the
       // other half's bk (h = 0) or bq (h = 1), ax its aa.
       float db = 0.f, late = 0.f;  // late: of the token as the earlier one of pairs and of the chunk's end
-      Split bq, bk, aa, x, ax;
+      Fine bq, bk, aa, x, ax;
       {
         F8 zs[N], ws[N];
         Raw8<T> ds[N];
@@ -392,29 +452,29 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
             const int o = Lds::at(place_of(M_ROWS * i + m_row), m_piece);
             const Op<NP> d = ds[i].template op<NP>();
             Lds::put(m, 0, o, zs[i]);
-            Lds::put(m, 2, o, ws[i]);
+            Lds::put(m, 3, o, ws[i]);
 #pragma unroll
-            for (int p = 0; p < NP; ++p) *reinterpret_cast<bf8_t*>(m + (4 + p) * Lds::PART + o) = d.p[p];
+            for (int p = 0; p < NP; ++p) *reinterpret_cast<bf8_t*>(m + (6 + p) * Lds::PART + o) = d.p[p];
           }
           if (vb + COLS < VP) fetch(vb + COLS);
           lds_barrier();
 #pragma unroll
           for (int kb = 0; kb < N; ++kb) {
-            const Op<NP> dn = Lds::stream(m, 4, own_at, 0, kb);
-            const Split zn = Lds::two(m, 0, own_at, 0, kb), wn = Lds::two(m, 2, own_at, 0, kb);
+            const Op<NP> dn = Lds::stream(m, 6, own_at, 0, kb);
+            const Fine zn = Lds::fine(m, 0, own_at, 0, kb), wn = Lds::fine(m, 3, own_at, 0, kb);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               const int r = 2 * h + t, o = 2 - 2 * h + t;
-              const Split zr = Lds::two(m, 0, rows_at, r, kb);
+              const Fine zr = Lds::fine(m, 0, rows_at, r, kb);
               zd[t] = mma(zr, dn, zd[t]);
               zw[t] = mma(zr, wn, zw[t]);
-              dz[t] = mma(Lds::stream(m, 4, rows_at, r, kb), zn, dz[t]);
-              wz[t] = mma(Lds::two(m, 2, rows_at, r, kb), zn, wz[t]);
+              dz[t] = mma(Lds::stream(m, 6, rows_at, r, kb), zn, dz[t]);
+              wz[t] = mma(Lds::fine(m, 3, rows_at, r, kb), zn, wz[t]);
               if (h == 0) {
-                xd[t] = mma(Lds::stream(m, 4, rows_at, o, kb), zn, xd[t]);
-                xw[t] = mma(Lds::two(m, 2, rows_at, o, kb), zn, xw[t]);
+                xd[t] = mma(Lds::stream(m, 6, rows_at, o, kb), zn, xd[t]);
+                xw[t] = mma(Lds::fine(m, 3, rows_at, o, kb), zn, xw[t]);
               } else {
-                const Split zo = Lds::two(m, 0, rows_at, o, kb);
+                const Fine zo = Lds::fine(m, 0, rows_at, o, kb);
                 xd[t] = mma(zo, dn, xd[t]);
                 xw[t] = mma(zo, wn, xw[t]);
               }
@@ -424,43 +484,9 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
           if (Lds::NBUF == 1) lds_barrier();
         }
         keep_order();
-        f4_t kk[2], qk[2], xk[2], xq[2];  // rows i: k_i . k_j and q_i . k_j
-#pragma unroll
-        for (int t = 0; t < 2; ++t) kk[t] = qk[t] = xk[t] = xq[t] = f4_t{0.f, 0.f, 0.f, 0.f};
-        if (pass == 0) {
-          const int k_rows = Tk::lane_at(n, g) + 32 * h * Tk::ROW, k_own = Tk::at(place_of(tok), g);
-#pragma unroll
-          for (int kb = 0; kb < KB; ++kb) {
-            Op<NP> kn;
-#pragma unroll
-            for (int p = 0; p < NP; ++p) kn.p[p] = *reinterpret_cast<const bf8_t*>(lds.k[p] + (k_own ^ (kb << 6)));
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              Op<NP> ka, qa;
-#pragma unroll
-              for (int p = 0; p < NP; ++p) {
-                ka.p[p] = Tk::rows(lds.k[p], k_rows, t, kb);
-                qa.p[p] = Tk::rows(lds.q[p], k_rows, t, kb);
-              }
-              kk[t] = mma(ka, kn, kk[t]);
-              qk[t] = mma(qa, kn, qk[t]);
-            }
-            if (h == 0) {
-#pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                Op<NP> ka, qa;
-#pragma unroll
-                for (int p = 0; p < NP; ++p) {
-                  ka.p[p] = Tk::rows(lds.k[p], k_rows, 2 + t, kb);
-                  qa.p[p] = Tk::rows(lds.q[p], k_rows, 2 + t, kb);
-                }
-                xk[t] = mma(ka, kn, xk[t]);
-                xq[t] = mma(qa, kn, xq[t]);
-              }
-            }
-            keep_order();
-          }
-        }
+        Dots both_of = of_halves;
+        if (!HALVES && pass == 0) dots(both_of);
+        const f4_t(&kk)[2] = both_of.kk, (&qk)[2] = both_of.qk, (&xk)[2] = both_of.xk, (&xq)[2] = both_of.xq;
         const double Gn = lds.G[tok];
         const float beta_n = lds.beta[tok];
         float vq[8], vk[8], va[8], c[8];
@@ -491,9 +517,9 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
           if (n == 0) store8(lds.row[w] + row0, c);
         };
         ends_at(32 * h + 8 * g);
-        bq = split<2>(vq);
-        bk = split<2>(vk);
-        aa = split<2>(va);
+        bq = split<3>(vq);
+        bk = split<3>(vk);
+        aa = split<3>(va);
         pin(bq);
         pin(bk);
         pin(aa);
@@ -514,8 +540,8 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
           }
         }
         if (h == 0) ends_at(32 + 8 * g);
-        x = split<2>(vq);
-        ax = split<2>(va);
+        x = split<3>(vq);
+        ax = split<3>(va);
         pin(x);
         pin(ax);
         keep_order();
@@ -552,17 +578,17 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
         for (int vb = 0, turn = 0; vb < VP; vb += COLS, turn ^= 1) {
           char* m = lds.buf[Lds::NBUF == 2 ? turn : 0];
           Op<NP> dn[N];
-          Split zn[N], wn[N];
+          Fine zn[N], wn[N];
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             const int o = Lds::at(place_of(M_ROWS * i + m_row), m_piece);
             Lds::put(m, 0, o, mr[i]);
-            Lds::put(m, 2, o, nr[i]);
+            Lds::put(m, 3, o, nr[i]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) mn += mr[i].a[e] * nr[i].a[e] + mr[i].b[e] * nr[i].b[e];
             dn[i] = dn_next[i];
-            zn[i] = split<2>(zn_next[i].a, zn_next[i].b);
-            wn[i] = split<2>(wn_next[i].a, wn_next[i].b);
+            zn[i] = split<3>(zn_next[i].a, zn_next[i].b);
+            wn[i] = split<3>(wn_next[i].a, wn_next[i].b);
           }
           if (vb + COLS < VP) fetch(key0, vb + COLS);
           else if (quad + 1 < QUADS) fetch(key0 + 64, 0);
@@ -571,7 +597,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
           for (int kb = 0; kb < N; ++kb) {
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-              const Split ms = Lds::two(m, 0, rows_at, t, kb), ns = Lds::two(m, 2, rows_at, t, kb);
+              const Fine ms = Lds::fine(m, 0, rows_at, t, kb), ns = Lds::fine(m, 3, rows_at, t, kb);
               dq[t] = mma(ms, dn[kb], dq[t]);
               read[t] = mma(ms, wn[kb], read[t]);
               early[t] = mma(ns, zn[kb], early[t]);
@@ -582,19 +608,24 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaArgs a) {
         }
         // after an odd number of steps the next one takes the same buffer
         if (Lds::NBUF == 2 && ((VP + COLS - 1) / COLS & 1)) lds_barrier();
-        const int cols_at = Tk::lane_at_t(n, g) ^ (2 * key0);
+        const int held = HALVES ? 64 * quad : key0;  // their place in LDS
+        const int cols_at = Tk::lane_at_t(n, g) ^ (2 * held);
         f4_t dk[4];
 #pragma unroll
         for (int t2 = 0; t2 < 2; ++t2) {
           float kf[8], qf[8];
           {
-            const int o = Tk::at(place_of(tok), (key0 >> 3) + 4 * t2 + g);
-            const bf8_t k0 = *reinterpret_cast<const bf8_t*>(lds.k[0] + o), q0 = *reinterpret_cast<const bf8_t*>(lds.q[0] + o);
-            const bf8_t k1 = *reinterpret_cast<const bf8_t*>(lds.k[NP - 1] + o), q1 = *reinterpret_cast<const bf8_t*>(lds.q[NP - 1] + o);
+            const int o = Tk::at(place_of(tok), (held >> 3) + 4 * t2 + g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              kf[e] = (float)k0[e] + (NP == 2 ? (float)k1[e] : 0.f);
-              qf[e] = (float)q0[e] + (NP == 2 ? (float)q1[e] : 0.f);
+            for (int e = 0; e < 8; ++e) kf[e] = qf[e] = 0.f;
+#pragma unroll
+            for (int p = NP - 1; p >= 0; --p) {
+              const bf8_t kp = *reinterpret_cast<const bf8_t*>(lds.k[p] + o), qp = *reinterpret_cast<const bf8_t*>(lds.q[p] + o);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                kf[e] += (float)kp[e];
+                qf[e] += (float)qp[e];
+              }
             }
           }
 #pragma unroll
@@ -680,14 +711,14 @@ template <typename T, int KP, bool FULL>
 hipError_t back_go(const DeltaArgs& a, hipStream_t st) {
   constexpr int NW = 4;
   const unsigned grid = (unsigned)(a.B * a.Hv * a.NS * ((a.Dv + 16 * NW - 1) / (16 * NW)));
-  const size_t lds = sizeof(BackLds<KP, WALK_PARTS<T>, NW>);
+  const size_t lds = sizeof(BackLds<KP, PARTS<T>, NW>);
   return a.vec ? with_lds(delta_back_kernel<T, KP, NW, true, FULL>, lds, grid, 64 * NW, a, st)
                : with_lds(delta_back_kernel<T, KP, NW, false, FULL>, lds, grid, 64 * NW, a, st);
 }
 
 template <typename T, int KP>
 hipError_t grad_go(const DeltaArgs& a, hipStream_t st) {
-  typedef GradLds<KP, Stream<T>::NP> Lds;
+  typedef GradLds<KP, PARTS<T>> Lds;
   const unsigned grid = (unsigned)(a.B * a.Hk * a.NC), block = 256;
   if (a.Hv == a.Hk)
     return a.vec8 ? with_lds(delta_grad_kernel<T, KP, true, false>, sizeof(Lds), grid, block, a, st)

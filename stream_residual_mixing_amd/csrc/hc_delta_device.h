@@ -85,17 +85,9 @@ __device__ __forceinline__ f4_t mma(const Op<NA>& a, const Op<NB>& b, f4_t c) {
   return c;
 }
 
-// Stream operands: bfloat16 is exact in one part, float32 takes two in the chunks' gradients and three in the
-// walks, whose states pass their errors on.
-template <typename T> struct Stream;
-template <> struct Stream<bf16_t> {
-  static constexpr int NP = 1;
-};
-template <> struct Stream<float> {
-  static constexpr int NP = 2;
-};
+// Stream operands: bfloat16 is exact in one part, float32 takes three.
 template <typename T>
-constexpr int WALK_PARTS = sizeof(T) == 4 ? 3 : 1;
+constexpr int PARTS = sizeof(T) == 4 ? 3 : 1;
 
 // Memory from an address that the wave's lanes have in common, read and written at 32-bit offsets:
 // what lies at or behind its end reads as 0 and is not written, so that neither the last chunk's
@@ -195,7 +187,7 @@ template <> struct Raw8<float> {
 };
 
 // Eight keys of a row from k0 on, as an operand.
-template <typename T, bool VEC, int NP = Stream<T>::NP>
+template <typename T, bool VEC, int NP = PARTS<T>>
 __device__ __forceinline__ Op<NP> token_op(const Range& m, uint32_t stride, int row, int k0, int width) {
   Raw8<T> x;
   x.template load<VEC>(m, (row * stride + k0) * (uint32_t)sizeof(T), width - k0);

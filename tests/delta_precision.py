@@ -5,7 +5,8 @@ Tolerances are on the norm of a head's error, relative to the norm of the result
 product keeps 24 bits, so what remains are the roundings of float32 sums, 2^-24 of what is summed each:
 a sum of n terms of random signs is off by sqrt(n) 2^-24 of its norm.
   State: what a chunk adds is a sum over 64 tokens, sqrt(64) 2^-24 = 2^-21.
-  Outputs and gradients: sums over up to 256 keys or columns, 2^-20.
+  Outputs and gradients: sums over up to 256 keys or columns, 2^-20 (the first state's too: what a chunk adds to it
+  holds W, which is such a sum).
   dg: a sum over a chunk that two running sums of 64 pass through one after the other: 2^-19.
   A bfloat16 result against the float64 one rounded to bfloat16, half(): off by e of its rms before it is
   rounded, an element that is u steps of its type, u from 2^-8 to 2^-7 of it, falls on the other side of a

@@ -64,3 +64,30 @@ def test_forward(size, dt):
     o, M = hc.hc_gated_delta(*d[:6])
     torch.cuda.synchronize()
     check_forward(o, M, ins, dt)
+
+
+def check_backward(got, ins, dt, lengths=None, grow=1.0):
+    B, S, Hk, _ = ins[0].shape
+    ref = R.gated_delta_backward(*ins[:5], ins[6], ins[5], ins[7], lengths)
+    got = [get(t) for t in got]
+    for name, x, y in zip(("dq", "dk", "dv", "dg", "dbeta", "dstate0"), got, ref):
+        if dt == "bf16" and name in ("dq", "dk", "dv"):
+            check(name, "all", x, y, dt, None)
+            continue
+        tol = (D.DG if name == "dg" else D.OUT) * grow
+        for b in range(B):
+            for h in range(y.shape[1 if name == "dstate0" else 2]):
+                u, v = (x[b, h], y[b, h]) if name == "dstate0" else (x[b, :, h], y[b, :, h])
+                if np.any(v):
+                    check(name, (b, h), u, v, "f32", tol)
+
+
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_backward(size, dt):
+    note(f"precision of hc_gated_delta_backward {size} {dt}")
+    ins = D.inputs(*size, dt, sum(size))
+    d = device(ins, dt)
+    got = hc.hc_gated_delta_backward(*d[:5], d[6], d[5], d[7])
+    torch.cuda.synchronize()
+    check_backward(got, ins, dt)
