@@ -382,15 +382,15 @@ __global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, PARTS<T>, NW, MODE>>)) 
       S.store(a.slots + part.slot * Dk * Dv + col, Dk, Dv, n, g, have);
       return;
     }
-    S.keep((bf16_t*)a.phi + part.slot * 2 * KP * KP, KP, col, n, g);
+    S.keep((bf16_t*)a.phi + part.slot * 3 * KP * KP, col, n, g);
     if (MODE == SUM_BWD) {
-      const Range m((bf16_t*)a.phi_t + part.slot * 2 * KP * KP, 4 * KP * KP);
+      const Range m((bf16_t*)a.phi_t + part.slot * 3 * KP * KP, 6 * KP * KP);
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) {
-        const Split s = split<2>(S.m[2 * kb], S.m[2 * kb + 1]);
+        const Fine s = split<3>(S.m[2 * kb], S.m[2 * kb + 1]);
         const uint32_t o = 2 * ((col + n) * KP + 32 * kb + 8 * g);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) m.put_quad(o + p * 2 * KP * KP, __builtin_bit_cast(u4_t, s.p[p]));
+        for (int p = 0; p < 3; ++p) m.put_quad(o + p * 2 * KP * KP, __builtin_bit_cast(u4_t, s.p[p]));
       }
     }
   }
@@ -508,7 +508,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
 template <int KP, bool BACK>
 __global__ __launch_bounds__(2 * KP) void delta_join_kernel(DeltaArgs a) {
   constexpr int KB = KP / 32;
-  __shared__ __attribute__((aligned(16))) char lds[2][KB][2][TILE];
+  __shared__ __attribute__((aligned(16))) char lds[2][KB][3][TILE];
   const int lane = threadIdx.x & 63, w = wave_number(), n = lane & 15, g = lane >> 4;
   const int Dk = (int)a.Dk, Dv = (int)a.Dv;
   const Place at((uint32_t)(a.B * a.Hv), ((uint32_t)Dv + 15) / 16);
@@ -517,13 +517,13 @@ __global__ __launch_bounds__(2 * KP) void delta_join_kernel(DeltaArgs a) {
   const int64_t chunks = (length_of(a.lengths, b, a.S) + CH - 1) / CH, state = (int64_t)Dk * Dv;
   const int segs = (int)((chunks + a.SL - 1) / a.SL);  // that hold tokens
   float* slots = a.slots + bh * a.NS * state + col;
-  const bf16_t* maps = (const bf16_t*)(BACK ? a.phi_t : a.phi) + bh * a.NS * 2 * KP * KP;
+  const bf16_t* maps = (const bf16_t*)(BACK ? a.phi_t : a.phi) + bh * a.NS * 3 * KP * KP;
   if (segs < 3) return;  // the second segment's state is the first's last one
   const auto seg = [&](int i) { return BACK ? segs - 1 - i : i; };
   const uint32_t s_lane = n < have ? 4 * ((32 * w + 8 * g) * Dv + n) : NOWHERE;
   const uint32_t m_lane = 2 * ((8 * (n >> 2) + (n & 3)) * KP + 8 * g);
   constexpr int AHEAD = KP == 256 ? 1 : 2;  // steps whose maps are on their way, as there are registers
-  Split m[AHEAD][2][KB];
+  Fine m[AHEAD][2][KB];
   float add[AHEAD][8];
   const auto load_slot = [&](int i, float (&v)[8]) {
     const Range r(slots + seg(i) * state, ((int64_t)(Dk - 1) * Dv + have) * 4);
@@ -531,7 +531,7 @@ __global__ __launch_bounds__(2 * KP) void delta_join_kernel(DeltaArgs a) {
     for (int e = 0; e < 8; ++e) v[e] = r.get((const float*)nullptr, s_lane + 4 * e * Dv);
   };
   const auto fetch = [&](int i, int x) {
-    const Range r(maps + seg(i) * (int64_t)2 * KP * KP, 4 * KP * KP);
+    const Range r(maps + seg(i) * (int64_t)3 * KP * KP, 6 * KP * KP);
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -541,16 +541,17 @@ __global__ __launch_bounds__(2 * KP) void delta_join_kernel(DeltaArgs a) {
   float S[8];  // rows 32 w + 8 g + 0 .. 7
   load_slot(0, S);
   const auto step = [&](int i, int x) {
-    const Split own = split<2>(S);
+    const Fine own = split<3>(S);
     char* mine = lds[i & 1][w][0] + lane * 16;
 #pragma unroll
-    for (int p = 0; p < 2; ++p) *reinterpret_cast<bf8_t*>(mine + p * TILE) = own.p[p];
+    for (int p = 0; p < 3; ++p) *reinterpret_cast<bf8_t*>(mine + p * TILE) = own.p[p];
     lds_barrier();
     f4_t o[2] = {{add[x][0], add[x][1], add[x][2], add[x][3]}, {add[x][4], add[x][5], add[x][6], add[x][7]}};
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
       const char* p = lds[i & 1][kb][0] + lane * 16;
-      const Split f = {*reinterpret_cast<const bf8_t*>(p), *reinterpret_cast<const bf8_t*>(p + TILE)};
+      const Fine f = {*reinterpret_cast<const bf8_t*>(p), *reinterpret_cast<const bf8_t*>(p + TILE),
+                      *reinterpret_cast<const bf8_t*>(p + 2 * TILE)};
 #pragma unroll
       for (int t = 0; t < 2; ++t) o[t] = mma(m[x][t][kb], f, o[t]);
     }
@@ -657,8 +658,8 @@ int64_t delta_plan(DeltaArgs& a, bool backward, void* ws) {
   a.rec = take(heads * a.NC * (backward ? REC_BWD : REC));
   if (a.NS > 1) {
     a.slots = (float*)take(heads * a.NS * a.Dk * a.Dv * 4);
-    a.phi = take(heads * a.NS * 4 * KP * KP);
-    if (backward) a.phi_t = take(heads * a.NS * 4 * KP * KP);
+    a.phi = take(heads * a.NS * 6 * KP * KP);
+    if (backward) a.phi_t = take(heads * a.NS * 6 * KP * KP);
   }
   if (backward) {
     const int64_t n = heads * a.NC;

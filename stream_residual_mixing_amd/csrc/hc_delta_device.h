@@ -29,13 +29,12 @@ __device__ __forceinline__ int row_of(int t, int m) { return 32 * (t >> 1) + 8 *
 // the place of row x in that order
 __device__ __forceinline__ int place_of(int x) { return (x & ~31) + 16 * ((x >> 2) & 1) + 4 * ((x >> 3) & 3) + (x & 3); }
 
-// Eight values as the sum of NP bfloat16 parts. Three hold float32's own 24 bits, bfloat16 streams are
-// their own single part, and two leave 2^-18 of a value.
+// Eight values as the sum of NP bfloat16 parts. Three hold float32's own 24 bits; bfloat16 streams are
+// their own single part.
 template <int NP>
 struct Op {
   bf8_t p[NP];
 };
-typedef Op<2> Split;
 typedef Op<3> Fine;
 
 __device__ __forceinline__ bf8_t as_bf8(u4_t q) { return __builtin_bit_cast(bf8_t, q); }
@@ -121,21 +120,18 @@ struct Range {
   __device__ __forceinline__ void put_quad(uint32_t o, u4_t v) const {
     __builtin_amdgcn_raw_buffer_store_b128(v, r, o, 0, 0);
   }
-  // the two bfloat16 parts of v, the low one in its own array
-  __device__ __forceinline__ void put_parts(const Range& low, uint32_t o, float v) const {
-    const uint32_t h = pack_bf2_hw(v, 0.f);
-    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)h, r, o, 0, 0);
-    low.put((bf16_t*)nullptr, o, v - __uint_as_float(h << 16));
-  }
   // eight floats of a kept array, at an offset `s` more that the lanes have in common; inside it
   __device__ __forceinline__ F8 floats(uint32_t o, uint32_t s) const {
     return {__builtin_bit_cast(f4_t, __builtin_amdgcn_raw_buffer_load_b128(r, o, s, 0)),
             __builtin_bit_cast(f4_t, __builtin_amdgcn_raw_buffer_load_b128(r, o, s + 16, 0))};
   }
-  // an operand kept in two parts, at an offset `s` more that the lanes have in common; inside it
-  __device__ __forceinline__ Split parts(uint32_t o, uint32_t s, uint32_t lo) const {
-    return {__builtin_bit_cast(bf8_t, __builtin_amdgcn_raw_buffer_load_b128(r, o, s, 0)),
-            __builtin_bit_cast(bf8_t, __builtin_amdgcn_raw_buffer_load_b128(r, o, s + lo, 0))};
+  // an operand kept in three parts, `part` bytes apart, at an offset `s` more that the lanes have in common; inside it
+  __device__ __forceinline__ Fine parts(uint32_t o, uint32_t s, uint32_t part) const {
+    Fine f;
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+      f.p[p] = __builtin_bit_cast(bf8_t, __builtin_amdgcn_raw_buffer_load_b128(r, o, s + p * part, 0));
+    return f;
   }
 };
 
@@ -344,14 +340,22 @@ struct State {
 #pragma unroll
       for (int r = 0; r < 4; ++r) m.put(p, lane + 4 * row_of(t, r) * stride, this->m[t][r]);
   }
-  // the same in two parts
-  __device__ __forceinline__ void keep(bf16_t* p, int stride, int col, int n, int g) const {
-    const Range hi(p, 2 * KP * stride), lo(p + KP * stride, 2 * KP * stride);
-    const uint32_t lane = anew(col < stride ? 2 * (8 * g * stride + col + n) : NOWHERE);
+  // the same [KP, KP], in three parts one after the other
+  __device__ __forceinline__ void keep(bf16_t* p, int col, int n, int g) const {
+    const Range m(p, 6 * KP * KP);
+    const uint32_t lane = anew(2 * (8 * g * KP + col + n));
 #pragma unroll
     for (int t = 0; t < KP / 16; ++t) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r) hi.put_parts(lo, lane + 2 * row_of(t, r) * stride, m[t][r]);
+      for (int r = 0; r < 4; ++r) {
+        float left = this->m[t][r];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const uint32_t h = pack_bf2_hw(left, 0.f);
+          __builtin_amdgcn_raw_buffer_store_b16((uint16_t)h, m.r, lane + 2 * row_of(t, r) * KP, i * 2 * KP * KP, 0);
+          left -= __uint_as_float(h << 16);
+        }
+      }
     }
   }
 };

@@ -99,7 +99,7 @@ struct DeltaArgs {
   int64_t NC, SL, NS, VP;
   void* rec;               // the chunks' records
   float* slots;            // [B, Hv, NS, Dk, Dv] a segment's last state (backward: the gradient of its first)
-  void* phi;               // [B, Hv, NS, 2, KP, KP] its map of the state, in two bfloat16 parts
+  void* phi;               // [B, Hv, NS, 3, KP, KP] its map of the state, in three bfloat16 parts
   void* phi_t;             // the same transposed; KP is Dk as 64, 128 or 256
   void* states;            // backward: every chunk's first state [KP, VP] and Z [64, VP], and the gradient
   void* z;                 // of the state behind it and W of the same shapes, float32

@@ -13,6 +13,8 @@ a sum of n terms of random signs is off by sqrt(n) 2^-24 of its norm.
   rounding for one in e / u and is then u off: sqrt(e u) of the norm, 2^-14 for e = 2^-20. The N 2^-12.5
   elements that do so are counted like dice, three times their spread on top, and where N is small
   one of them may be the largest of all.
+  Sequences in segments, joins(): one of 256 tokens and more hands its state to the next by one more such product,
+  whose errors stay where the state does: as many of them as there are segments, of random signs.
 """
 import numpy as np
 
@@ -23,6 +25,11 @@ def half(y):
     """The tolerance of a bfloat16 result whose rounded float64 form is y."""
     tol = 2.0 ** -14 * np.sqrt(1 + 6 / np.sqrt(y.size * 2.0 ** -12.5))
     return tol if y.size >= 1 << 18 else tol + 2.0 ** -7 * np.abs(y).max() / np.linalg.norm(y)
+
+
+def joins(S):
+    """What the tolerances grow by where S tokens are walked in segments."""
+    return max(1.0, np.sqrt(S / 256))
 
 
 def bf16(a):
@@ -99,3 +106,25 @@ def chunked(q, k, v, g, beta, M, scale, held=None, segment=None, maps=None, map_
             Phi = walk(lo, hi, np.eye(Dk), keys_only=True) if maps != "zero" else np.zeros((Dk, Dk))
             state = walk(lo, hi, zeros) + parts(Phi, map_parts) @ parts(state, map_parts)
     return np.concatenate(out), last
+
+
+def dg_size(ins, n, b, h):
+    """The norm over n tokens of ||F|| ||dF|| / sqrt(Dk Dv) of one head, the size of dg = <dF, F> of unrelated states.
+    Where both hardly change from token to token the sum of one token's products cancels as that of all others
+    does, and dg can be small beside it. An error e of the states' elements, relative to their rms and of random
+    signs, is e ||F|| ||dF|| / sqrt(Dk Dv) in the sum of products, whatever the sum itself comes to."""
+    q, k, v, g, beta, M, do, dM = ins
+    kh = h // (v.shape[2] // k.shape[2])
+    m, r, scale, F = M[b, h], dM[b, h], q.shape[3] ** -0.5, []
+    for t in range(n):
+        F.append(np.exp(g[b, t, h]) * m)
+        kt = k[b, t, kh]
+        m = F[-1] + beta[b, t, h] * np.outer(kt, v[b, t, h] - F[-1].T @ kt)
+    size = 0.0
+    for t in range(n - 1, -1, -1):
+        kt = k[b, t, kh]
+        r = r + np.outer(q[b, t, kh], scale * do[b, t, h])
+        dF = r - np.outer(kt, beta[b, t, h] * (r.T @ kt))
+        size += np.sum(F[t] ** 2) * np.sum(dF ** 2) / m.size
+        r = np.exp(g[b, t, h]) * dF
+    return np.sqrt(size)

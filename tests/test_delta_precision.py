@@ -42,3 +42,28 @@ def test_a_bfloat16_result_tells_an_error_before_its_rounding(n):
     off = lambda e: D.rel(D.bf16(y + e * rng.normal(size=n)), D.bf16(y))  # noqa: E731
     assert off(2.0 ** -20) < D.half(D.bf16(y))
     assert n < 10000 or D.half(D.bf16(y)) < off(2.0 ** (-18.5 if n >= 1 << 18 else -13))
+
+
+@pytest.mark.parametrize("size", [(1100, 128, 24, 320), (2100, 64, 32, 320)])
+def test_segments_need_their_maps(size):
+    """The inputs of the segments' tests carry the first state to the last: without the maps the result is another."""
+    S, Dk, Dv, segment = size
+    head = _head(D.inputs(1, S, 1, 1, Dk, Dv, "f32", S, slow=1e-4))
+    o, M = D.chunked(*head, Dk ** -0.5)
+    os, Ms = D.chunked(*head, Dk ** -0.5, segment=segment)
+    oz, Mz = D.chunked(*head, Dk ** -0.5, segment=segment, maps="zero")
+    grow = D.joins(S)
+    assert D.rel(os, o) < D.OUT * grow / 8 and D.rel(Ms, M) < D.STATE * grow / 8
+    assert D.rel(oz, o) > 0.1 and D.rel(Mz, M) > 0.1
+
+
+def test_maps_in_two_parts_are_told():
+    """Over many segments, what two parts leave of the maps and the joined states adds up."""
+    S, Dk, Dv = 8192, 128, 8
+    head = _head(D.inputs(1, S, 1, 1, Dk, Dv, "f32", 5, slow=1e-5))
+    o, M = D.chunked(*head, Dk ** -0.5)
+    two, M2 = D.chunked(*head, Dk ** -0.5, segment=256, map_parts=2)
+    three, M3 = D.chunked(*head, Dk ** -0.5, segment=256, map_parts=3)
+    grow = D.joins(S)
+    assert D.rel(M3, M) < D.STATE * grow / 8 and D.rel(three, o) < D.OUT * grow / 8
+    assert D.rel(M2, M) > 2 * D.STATE * grow and D.rel(two, o) > D.OUT * grow

@@ -78,7 +78,10 @@ def check_backward(got, ins, dt, lengths=None, grow=1.0):
         for b in range(B):
             for h in range(y.shape[1 if name == "dstate0" else 2]):
                 u, v = (x[b, h], y[b, h]) if name == "dstate0" else (x[b, :, h], y[b, :, h])
-                if np.any(v):
+                if name == "dg" and np.any(v) and D.rel(u, v) > tol:  # of states' products that cancel
+                    n = S if lengths is None else lengths[b]
+                    check(name, (b, h), u, v, "f32", tol * max(1.0, D.dg_size(ins, n, b, h) / np.linalg.norm(v)))
+                elif np.any(v):
                     check(name, (b, h), u, v, "f32", tol)
 
 
@@ -91,3 +94,51 @@ def test_backward(size, dt):
     got = hc.hc_gated_delta_backward(*d[:5], d[6], d[5], d[7])
     torch.cuda.synchronize()
     check_backward(got, ins, dt)
+
+
+# few heads and long sequences, which are walked in segments: an odd and an even number of them, the last one
+# short or whole, every width's variants; `slow` decays carry the first state through all of them
+SEGMENTS = [(1, 1100, 1, 2, 128, 128), (1, 2100, 1, 1, 64, 32), (1, 1300, 1, 1, 256, 48), (1, 2048, 1, 2, 100, 40),
+            (1, 8192, 1, 1, 128, 16)]
+
+
+@pytest.mark.parametrize("size", SEGMENTS)
+@pytest.mark.parametrize("slow", [None, 1e-4, 1e-5, 0.0])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_segments_forward(size, slow, dt):
+    note(f"precision of hc_gated_delta {size} {dt} slow={slow}")
+    ins = D.inputs(*size, dt, sum(size), slow)
+    d = device(ins, dt)
+    o, M = hc.hc_gated_delta(*d[:6])
+    state = d[5].clone()
+    o2, M2 = hc.hc_gated_delta(*d[:5], state, out=(None, state))
+    torch.cuda.synchronize()
+    check_forward(o, M, ins, dt, grow=D.joins(size[1]))
+    assert torch.equal(o, o2) and torch.equal(M, M2)
+
+
+@pytest.mark.parametrize("size", SEGMENTS)
+@pytest.mark.parametrize("slow", [None, 1e-4, 0.0])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_segments_backward(size, slow, dt):
+    note(f"precision of hc_gated_delta_backward {size} {dt} slow={slow}")
+    ins = D.inputs(*size, dt, sum(size), slow)
+    d = device(ins, dt)
+    got = hc.hc_gated_delta_backward(*d[:5], d[6], d[5], d[7])
+    torch.cuda.synchronize()
+    check_backward(got, ins, dt, grow=D.joins(size[1]))
+
+
+@pytest.mark.parametrize("Dk", [64, 128, 256])
+def test_lengths_end_in_segments(Dk):
+    """Padded sequences of slow decays that end at the segments' borders, inside and before the last of them."""
+    S, L = 1600, [1600, 0, 300, 641, 1279, 1280]
+    note(f"precision of padded segments Dk={Dk}")
+    ins = D.inputs(len(L), S, 1, 1, Dk, 24, "f32", Dk, 1e-4)
+    d = device(ins, "f32")
+    lengths = torch.tensor(L, dtype=torch.int32, device="cuda")
+    o, M = hc.hc_gated_delta(*d[:6], lengths=lengths)
+    got = hc.hc_gated_delta_backward(*d[:5], d[6], d[5], d[7], lengths=lengths)
+    torch.cuda.synchronize()
+    check_forward(o, M, ins, "f32", L, grow=D.joins(S))
+    check_backward(got, ins, "f32", L, grow=D.joins(S))
