@@ -422,8 +422,8 @@ __device__ __forceinline__ void keep_rows(float* p, int stride, int col, int n, 
 // whatever it is added to, so that -inf (a fresh start) stays a number here.
 __device__ __forceinline__ double clamp_decay(float g) { return g < -200.f ? -200.0 : (double)g; }
 
-// exp(x) of a difference of the sums, off by |x| 2^-23 of itself at most: below what the products that
-// it enters leave of it until exp(x) is 1e-27.
+// exp(x) of a difference of the sums, off by |x| 2^-23 of itself at most: |x| exp(x) 2^-23 <= 4 x 10^-8 of what
+// it decays, however long that has been forgotten.
 __device__ __forceinline__ float decay(double x) { return __builtin_amdgcn_exp2f((float)x * 1.44269504f); }
 
 // The running sum over a wave of 64 tokens.
