@@ -571,9 +571,9 @@ __global__ __launch_bounds__(2 * KP) void delta_join_kernel(DeltaArgs a) {
   }
 }
 
-// Tokens up to which they are taken one by one, rather than as a chunk: 4 tokens of 32 heads of 128 x 128
-// take 11.6 us against 16.4, of 256 heads 16.4 against 24 and of 2,048 heads 83 against 103; 8 tokens 14.3
-// against 16.6, 25.2 against 24.3 and 137 against 106 (whole calls, bfloat16).
+// Tokens up to which they are taken one by one, rather than as a chunk: 6 tokens of 32 heads of 128 x 128
+// take 20 us against 24, of 256 heads 21 against 24 and of 2,048 heads 114 against 111; 8 tokens 19
+// against 24, 26 against 24 and 144 against 111 (whole calls, bfloat16).
 constexpr int SHORT = 6;
 
 // Four waves a workgroup, 64 columns: 572 us for 8,192 tokens of 16 heads in one walk and 129 for 8 x 1,024
@@ -639,12 +639,18 @@ int64_t delta_plan(DeltaArgs& a, bool backward, void* ws) {
   a.SL = a.NC;
   // Workgroups that walk whole sequences. Where they are few for 256 CUs of two each, every sequence is cut
   // into segments of 4 chunks and more, as many as fill the CUs, walked at once from zeros, with their maps
-  // of the state, joined, and walked again from their own states: twice the work and the join, so worth it
-  // from four segments and 1,024 tokens on (16 heads of 128 x 128: 8,192 tokens 210 us against 572 in one
-  // walk, whole calls when this was chosen).
-  const int64_t wide = heads * ((a.Dv + 63) / 64);
-  if (wide > 0 && 512 / wide >= 4 && a.NC >= 16) {
-    const int64_t most = 512 / wide < a.NC / 4 ? 512 / wide : a.NC / 4;
+  // of the state, joined, and walked again from their own states: twice the work and the join. One walk
+  // against segments, us, forward and backward (bfloat16, whole calls):
+  //   eight segments and more fill the CUs: 1,024 tokens of 16 heads of 128 x 128 97 : 68 and 205 : 161, of 32
+  //   heads 101 : 80 and 236 : 207, 16 heads of 256 x 256 142 : 119 and 388 : 355; at 512 tokens 55 : 55 and
+  //   128 : 137;
+  //   four to seven: 1,024 tokens of 64 heads 108 : 119 and 328 : 368, 2,048 208 : 203 and 668 : 663, 4,096
+  //   450 : 395 and 1,332 : 1,220; maps of 256 keys cost more: 24 heads, 2,048 tokens 277 : 312 and 1,004 : 1,068,
+  //   4,096 557 : 506 and 2,009 : 1,893; 32 heads (four) 588 : 644 and 2,254 : 2,353;
+  //   two or three: 128 heads of 128 x 128, 2,048 tokens 275 : 370 and 1,011 : 1,197.
+  const int64_t wide = heads * ((a.Dv + 63) / 64), fill = wide > 0 ? 512 / wide : 0;
+  if (fill >= (KP == 256 ? 5 : 4) && a.NC >= (fill >= 8 ? 16 : KP == 256 ? 64 : 32)) {
+    const int64_t most = fill < a.NC / 4 ? fill : a.NC / 4;
     a.SL = (a.NC + most - 1) / most;
     a.NS = (a.NC + a.SL - 1) / a.SL;
   }
