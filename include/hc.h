@@ -741,8 +741,8 @@ int hc_gated_scan_backward(const void* x, const void* gate, const void* y, const
  *   lengths (NULL: S each) [B] int32 device array, as hc_gated_scan's: behind a sequence's length
  *   nothing is used, o is left as it was, and state is the one after its last token.
  *   The state and every sum are float32; o is rounded once. More than a few tokens are taken in
- *   chunks of 64, whose products hold at least 16 bits of each factor that is not bfloat16 already: each
- *   term of the state is off by at most about 2^-16 of itself. Deterministic. A NaN or an infinity
+ *   chunks of 64 (joined in segments where few heads have long sequences), whose products hold float32's 24 bits
+ *   of each factor: results are as far off as those of float32 sums in another order. Deterministic. A NaN or an infinity
  *   spoils its head from its chunk's first token on.
  *   dtype HC_F32 or HC_BF16; Hv a multiple of Hk; 1 <= Dk, Dv <= HC_MAX_HEAD; S = 0 passes the state on
  *   (B = 0 does nothing); B * Hv * max(8, ceil(S / 64)), Hk * Dk and Hv * Dv < 2^23 (else HC_ERR_SHAPE);
@@ -758,11 +758,11 @@ int hc_gated_scan_backward(const void* x, const void* gate, const void* y, const
  *   N = R_t + scale q_t d_o_t^T, y = N^T k_t:
  *   dq_t = scale M_t d_o_t,  dbeta_t = y . z_t,  dv_t = beta_t y,  dF = N - k_t dv_t^T,
  *   dk_t = beta_t N z_t - F dv_t,  dg_t = <dF, F>,  R_{t-1} = exp(g_t) dF.
- *   The states are formed again from the inputs. Sums are float32 and products hold 16 bits of each
+ *   The states are formed again from the inputs. Sums are float32 and products hold 24 bits of each
  *   factor, as the forward's; deterministic. Sizes and alignment as for the forward; workspace
  *   hc_gated_delta_backward_workspace_bytes bytes, 256-byte aligned (for each 64 tokens of a value
  *   head two states in 4 bytes an element, Z, W and 38 KB; where few heads have long sequences, for each of
- *   the segments that they are cut into a state and two maps of it in 4 bytes an element).
+ *   the segments that they are cut into a state in 4 bytes an element and two maps of it in 6).
  */
 int64_t hc_gated_delta_workspace_bytes(int64_t B, int64_t S, int64_t Hk, int64_t Hv, int64_t Dk, int64_t Dv,
                                        int dtype);

@@ -14,11 +14,15 @@
 // roundings. For this a walk takes a tenth longer, of 256 float32 keys a quarter). T and P lie in the record as
 // float32, which is smaller than three parts, and are split where they enter LDS, once for all waves.
 //   What bounds it: 2,048 chunks of 128 x 128 in bfloat16 (8 sequences of 1,024 tokens, 16 value
-// heads on 8 key heads) read and write 118 MB and need 15 GFLOP, 20 us of memory; the chunks
-// by themselves take 38 us (latency of the triangle's inverse), the walk 88 us as 16 chunks in
-// a row on 256 workgroups, 5.5 us a chunk of which the matrix units work for 1: each product
-// waits for the one before it. Hence few heads are walked in segments at once (see
-// delta_plan), and what does not depend on the state is done by every chunk for itself.
+// heads on 8 key heads) read and write 118 MB and need 15 GFLOP, 20 us of memory. The chunks
+// by themselves take 37 us: each wave reads its tiles of keys and queries from memory between the
+// products, four waves the same rows, and nearly every load is waited for by itself; then come the
+// triangle's steps. The walk takes 102 us as 16 chunks in a row on 256 workgroups, 6.4 us a chunk of which the
+// matrix units work for 1.5. A chunk first waits for the next one's loads, as bfloat16 values are
+// widened where they are fetched and loads are waited for in order; then each product waits for the
+// one before it and for its operands, which come from LDS just ahead of it. Walks that keep states
+// wait for a chunk's stores too. Few heads are walked in segments at once (see delta_plan), and
+// what does not depend on the state is done by every chunk for itself.
 #include "hc_delta_device.h"
 
 namespace hc {
@@ -243,7 +247,7 @@ __global__ __launch_bounds__(64 * NW, (WALKS<WalkLds<KP, PARTS<T>, NW, MODE>>)) 
     if (copied && MODE == SUM) S.store(copy, Dk, Dv, n, g, have);
   }
 
-  // the next chunk's operands on their way
+  // the next chunk's operands, which a bfloat16 chunk waits for before it begins (see above)
   Raw8<T> kr[ITEMS], qr[ITEMS];
   typename decltype(lds.rec)::Raw rr;
   float vr[4][4];
@@ -501,9 +505,9 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs a) {
 // M_{s+1} = Phi_s M_s + N_s over a head's segments, 16 columns of the state by a workgroup; the slots'
 // N become the states. A wave has 32 rows of the state, the operand block that the next step's
 // products take from all of them through LDS; its rows of the next two steps' Phi and N are on their
-// way meanwhile. A chain of products whose maps come from other dies' caches, 64 KB a step: 34 us for 16
-// heads of 16 segments (128 x 128); 40 with a head's columns spread over the dies and one step ahead, 103
-// with one wave for all rows. BACK: the gradients, from the last segment on, with
+// way meanwhile. A chain of products whose maps come from other dies' caches, 96 KB a step in three parts: 51 us
+// for 16 heads of 16 segments (128 x 128); of two parts 34, and then 40 with a head's columns spread over the
+// dies and one step ahead, 103 with one wave for all rows. BACK: the gradients, from the last segment on, with
 // Phi's transpose.
 template <int KP, bool BACK>
 __global__ __launch_bounds__(2 * KP) void delta_join_kernel(DeltaArgs a) {
@@ -576,7 +580,7 @@ __global__ __launch_bounds__(2 * KP) void delta_join_kernel(DeltaArgs a) {
 // against 24, 26 against 24 and 144 against 111 (whole calls, bfloat16).
 constexpr int SHORT = 6;
 
-// Four waves a workgroup, 64 columns: 572 us for 8,192 tokens of 16 heads in one walk and 129 for 8 x 1,024
+// Four waves a workgroup, 64 columns, measured with two parts: 572 us for 8,192 tokens of 16 heads in one walk and 129 for 8 x 1,024
 // against 671 and 136 with eight waves, which share keys and queries but wait for each other.
 template <typename T, int KP, int MODE>
 hipError_t walk_go(const DeltaArgs& a, hipStream_t st) {

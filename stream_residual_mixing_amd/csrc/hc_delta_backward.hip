@@ -18,10 +18,11 @@
 // Every factor keeps float32's 24 bits, in three bfloat16 parts: gradients are as near the definition as a float32
 // form's (2 to 4 x 10^-7 of their norm; with two parts 3 to 6 x 10^-6, the whole call 5 % faster).
 //   2,048 chunks of 128 x 128 (2 x 4,096 tokens, 16 value heads on 8 key heads, bfloat16), with segments: the
-// forward's part 227 us, the walks back 199, the chunks' own part 225. That one reads the states that the
-// walks kept, 64 KB a chunk and direction in float32, and Z and W, these more than once (400 MB, 619 MB of
-// reads at 2.8 TB/s), on one workgroup a CU, whose registers hold dQ and dK; its steps wait for memory
-// and barriers.
+// forward's part 255 us (the chunks 52, segments from zeros 96, joins 26, the walk that keeps states 80), the walks
+// back 218 (80, 28, 110), the chunks' own part 262. That one reads the states that the
+// walks kept, 64 KB a chunk and direction in float32, and Z and W three times, for the pairs and for each 64 keys (400 MB
+// kept, 600 MB of reads at 2.4 TB/s), on one workgroup a CU, whose registers hold dQ and dK; its
+// steps wait for memory and barriers.
 #include "hc_delta_device.h"
 
 namespace hc {

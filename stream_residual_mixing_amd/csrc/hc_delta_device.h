@@ -361,14 +361,14 @@ struct State {
 };
 
 // Workgroups of four waves on a CU that LDS has room for, up to the two that the walks have registers for;
-// with one each wave may take 512 (8 x 1,024 tokens, 16 heads: 256 x 256 in float32 460 us, with 256
-// registers and spills 1,173; in bfloat16 273 and 356; 128 x 128 in float32 162 and 171).
+// with one each wave may take 512 (8 x 1,024 tokens, 16 heads, measured with two parts: 256 x 256 in float32 460 us,
+// with 256 registers and spills 1,173; in bfloat16 273 and 356; 128 x 128 in float32 162 and 171).
 template <typename Lds>
 constexpr int WALKS = sizeof(Lds) <= 80 * 1024 ? 2 : 1;
 
 // The grid's `units` by `members` workgroups, the members of a unit on one die, whose L2 then brings
 // what they all read once: consecutive workgroups go round the dies. The units behind the last
-// multiple of the dies in plain order. Against plain order throughout: walks of 2,048 chunks 85 -> 79 us, in
+// multiple of the dies in plain order. Against plain order throughout, with two parts: walks of 2,048 chunks 85 -> 79 us, in
 // segments 70 + 69 -> 62 + 60; the backward's 637 -> 619 us in all.
 struct Place {
   uint32_t unit, member;

@@ -7,12 +7,16 @@
 // row's threads for the mean, one for the deviations' sums; what rounding leaves in the
 // mean is taken off with the scale, in one multiply-add an element.
 //   Memory bounds the forward: 8,192 rows of 4,096 bfloat16 with residual, stored as e4m3
-// groups, 47 us for 236 MB; the pre-read of 4 streams 67 us for 403 MB. In the backward
-// (60 us for 268 MB) a row's two exchanges, and the threads that wait in them, cost as much.
+// groups, 44 us for 236 MB; the pre-read of 4 streams 67 us for 403 MB. In the backward
+// (57 us for 268 MB) a row's two exchanges, and the threads that wait in them, cost as much.
 // They were the larger part of both: sums by DPP and lane swaps instead of trips through
 // LDS, and one LDS word a lane for the waves' sums instead of a loop over them, took the
-// forward from 55 to 47 us, the backward from 69 to 60, and from 159 to 111 us at 7,168
+// forward from 55 to 45 us, the backward from 69 to 57, and from 159 to 111 us at 7,168
 // channels, where 14 waves share a row.
+//   Wide rows, 4,096 of them: forward 5.0 TB/s up to 16,384 channels (bfloat16 99 us, float32 216), 3 to 4 at
+// odd widths (9,001: 94 and 147 us); backward, whose 16 waves spill above 8,192 channels (8 registers in
+// bfloat16, 24 in float32, 131 at odd widths), 4.1 and 4.7 TB/s at 8,192 (66 and 113 us), 3.6 and 3.0 at
+// 16,384 (150 and 354), 2.5 and 2.1 at 9,001 (120 and 276).
 #include "hc_norm_row.h"
 
 namespace hc {
